@@ -63,7 +63,8 @@ enum mla_status {
 enum mla_device_flag {
   MLA_DEV_BAD_LENGTH = 1,   /* some T[b] outside [S, T_cap]: that sequence was skipped      */
   MLA_DEV_BAD_INDEX = 2,    /* a selected index < 0 or > pos, or nsel outside [1, topk]     */
-  MLA_DEV_TIMEOUT = 4       /* a bounded wait inside a kernel ran out; the kernel returned  */
+  MLA_DEV_TIMEOUT = 4,      /* a bounded wait inside a kernel ran out; the kernel returned  */
+  MLA_DEV_BAD_VALUE = 8     /* a distribution with no finite positive mass (mla_tree_verify) */
 };
 
 /* Message of the last failing call on this thread ("" if none). */
@@ -419,6 +420,107 @@ int mla_cache_append_paged(const mla_dims* d, int dtype, int B, int S, const voi
 int dsa_index_key_append(int B, int S, int index_hd, int rope_dim, const float* k_idx, const float* ln_w,
                          const float* ln_b, float ln_eps, float rope_base, int T_cap, const int32_t* T,
                          float* Ic, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Drafted token trees
+ *
+ * The S new tokens of a call (1 <= S <= 64) may form a tree instead of a
+ * chain: several drafts of the same next tokens, verified in one pass.
+ *   parent [B, S] int32: -1 a child of the last committed token, 0 .. s-1 a
+ *          child of that node, -2 an absent node (pads smaller trees of a batch)
+ * Node s of sequence b has the cache row T[b] - S + s, as the new tokens of
+ * the other calls do, and the rotary position T[b] - S + depth(s), depth being
+ * its number of ancestors.  A chain (parent[s] = s - 1) gives the positions and
+ * masks of the calls above.  A parent at or above its child, below -2, or
+ * absent makes a node and its descendants bad: they raise MLA_DEV_BAD_INDEX.
+ *
+ * One step of a serving loop: mla_cache_append_tree writes the tree's rows,
+ * mla_decode_tree attends in every layer, mla_tree_verify accepts a path and
+ * draws one more token, and mla_tree_commit moves the accepted rows together.
+ * ------------------------------------------------------------------------- */
+
+/* Tree attention: mla_decode_absorbed with the query of node s attending to
+ * the cached prefix t < T[b] - S and, among the tree's rows, to its own and
+ * its ancestors'.  Rows of other branches, of absent nodes and past T[b] never
+ * reach a result, whatever they hold.
+ *   out [B, S, H, v_head] float (out_dtype MLA_F32) or bf16 (MLA_BF16),
+ *       16-byte aligned
+ * An absent node's output is zero, a bad node's NaN.  q, Lc, Rc, T, kv_b and
+ * the choice of kernels are mla_decode_absorbed's (mla_decode_paged's for the
+ * pools); FP8 caches are not served.  The arithmetic is theirs as well; bf16
+ * output is rounded once from the float result.
+ *   workspace: mla_decode_tree_workspace_size() bytes, 256-byte aligned (the
+ *              paged call takes T_cap = max_pages * page_size); 0 for the
+ *              CUDA-core path
+ * Errors: as mla_decode_absorbed; S > 64 returns MLA_ERR_UNSUPPORTED. */
+size_t mla_decode_tree_workspace_size(const mla_dims* d, int dtype, int B, int S, int T_cap);
+int mla_decode_tree(const mla_dims* d, int dtype, int B, int S, const void* q, const void* Lc, const void* Rc,
+                    int T_cap, const int32_t* T, const int32_t* parent, const void* kv_b, int out_dtype, void* out,
+                    void* workspace, size_t workspace_bytes, void* stream);
+int mla_decode_tree_paged(const mla_dims* d, int dtype, int B, int S, const void* q, const void* Lc_pages,
+                          const void* Rc_pages, int num_pages, int page_size, const int32_t* block_table,
+                          int max_pages, const int32_t* T, const int32_t* parent, const void* kv_b, int out_dtype,
+                          void* out, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Cache append of a tree: mla_cache_append with the rotary key of node s at
+ * position T[b] - S + depth(s).  Rows of absent and bad nodes are left as
+ * they were. */
+int mla_cache_append_tree(const mla_dims* d, int dtype, int B, int S, const void* comp, const void* kv_a_ln,
+                          float rms_eps, int T_cap, const int32_t* T, const int32_t* parent, void* Lc, void* Rc,
+                          void* stream);
+int mla_cache_append_tree_paged(const mla_dims* d, int dtype, int B, int S, const void* comp, const void* kv_a_ln,
+                                float rms_eps, void* Lc_pages, void* Rc_pages, int num_pages, int page_size,
+                                const int32_t* block_table, int max_pages, const int32_t* T, const int32_t* parent,
+                                void* stream);
+
+/* Verification of the drafted tokens (speculative sampling on a tree).
+ *
+ * Context 0 is the last committed token, context s + 1 is node s.
+ *   p      row r of sequence b at p + b * p_batch + r * p_row, r = 0 .. S, V
+ *          values: the target's probabilities after context r
+ *   q      likewise: the distribution that the children of context r were
+ *          drawn from, independently of one another; rows of contexts without
+ *          children need not hold one.  NULL: drafts without probabilities
+ *   tokens [B, S] int32 in [0, V)
+ *   u      [B, S + 1] float in [0, 1): u[b, s] decides node s, u[b, S] the draw
+ *   path   [B, S] int32: the accepted nodes from the root down, then -1
+ *   n_acc  [B] int32: their number
+ *   token  [B] int32: the token drawn after the last accepted node
+ * At a context the children are tried in index order, with W = max(p - c q, 0)
+ * and a = 1, c = 0 at first: child x is accepted when u q(x) a < W(x), and the
+ * walk goes on at it; a rejection adds a to c and makes a the sum of the new
+ * W.  When no child is left, token is the least x whose cumulative W exceeds
+ * u[b, S] times the sum of W (the last x with W(x) > 0 if rounding leaves
+ * none).  Without q a child is accepted when u a < W(x) (W = p at first), and a
+ * rejection subtracts W(x) from a and sets W(x) to 0.  If nothing is left of W
+ * the draw is from p.  The emitted tokens are then distributed as the target's
+ * own samples.  Sums over the vocabulary are held to about 2^-48.
+ *
+ * p (and q) are taken as distributions: values >= 0 whose sum is 1 up to
+ * rounding; p_row and q_row >= V.  A context whose p has no finite positive
+ * mass raises MLA_DEV_BAD_VALUE and gives token -1.  A bad node or a token
+ * outside [0, V) raises MLA_DEV_BAD_INDEX and is never accepted.  No workspace. */
+int mla_tree_verify(int B, int S, int V, const float* p, long long p_row, long long p_batch, const float* q,
+                    long long q_row, long long q_batch, const int32_t* tokens, const int32_t* parent, const float* u,
+                    int32_t* path, int32_t* n_acc, int32_t* token, void* stream);
+
+/* Commit of an accepted path: in each of n caches,
+ *   row T[b] - S + i  <-  row T[b] - S + path[b, i],   i < n_acc[b]
+ * and T_out[b] = T[b] - S + n_acc[b] (may be NULL; must not be T itself).
+ * path must increase within [0, S), as mla_tree_verify writes it.
+ *   cache     HOST array of n device pointers, each [B, T_cap, row] (or a pool
+ *             [num_pages, page_size, row]) with rows of row_bytes[i] bytes:
+ *             every layer's Lc, Rc, Ic, FP8 codes, in any mix; all share T_cap
+ *             (the pool's pages and table).  The array is read during the call only.
+ *   row_bytes HOST array of n row sizes, >= 1 (multiples of 16 move fastest)
+ * One launch serves 128 caches.  A bad length leaves the sequence and its
+ * T_out = T as they were (MLA_DEV_BAD_LENGTH); a bad count, path or page
+ * leaves its rows, with T_out = T - S (MLA_DEV_BAD_INDEX). */
+int mla_tree_commit(int n, void* const* cache, const int* row_bytes, int B, int S, int T_cap, const int32_t* T,
+                    const int32_t* path, const int32_t* n_acc, int32_t* T_out, void* stream);
+int mla_tree_commit_paged(int n, void* const* cache, const int* row_bytes, int B, int S, int num_pages,
+                          int page_size, const int32_t* block_table, int max_pages, const int32_t* T,
+                          const int32_t* path, const int32_t* n_acc, int32_t* T_out, void* stream);
 
 #ifdef __cplusplus
 }

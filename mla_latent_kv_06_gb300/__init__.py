@@ -17,7 +17,7 @@ LIB_PATH = os.path.join(PKG, "libmla.so")
 
 MLA_F32, MLA_BF16 = 0, 1
 MLA_OK, MLA_ERR_INVALID, MLA_ERR_UNSUPPORTED, MLA_ERR_CUDA, MLA_ERR_DEVICE = 0, -1, -2, -3, -4
-MLA_DEV_BAD_LENGTH, MLA_DEV_BAD_INDEX, MLA_DEV_TIMEOUT = 1, 2, 4
+MLA_DEV_BAD_LENGTH, MLA_DEV_BAD_INDEX, MLA_DEV_TIMEOUT, MLA_DEV_BAD_VALUE = 1, 2, 4, 8
 
 # Every symbol declared in include/mla.h.
 EXPORTS = (
@@ -34,6 +34,8 @@ EXPORTS = (
     "mla_o_proj_workspace_size", "mla_o_proj", "mla_decode_oproj_workspace_size", "mla_decode_oproj",
     "mla_decode_fp8_workspace_size", "mla_decode_fp8", "mla_decode_fp8_paged", "mla_cache_append_fp8",
     "mla_cache_append_fp8_paged",
+    "mla_decode_tree_workspace_size", "mla_decode_tree", "mla_decode_tree_paged", "mla_cache_append_tree",
+    "mla_cache_append_tree_paged", "mla_tree_verify", "mla_tree_commit", "mla_tree_commit_paged",
 )
 
 
@@ -56,6 +58,8 @@ _I = ctypes.c_int
 _SZ = ctypes.c_size_t
 _DP = ctypes.POINTER(MlaDims)
 _PP = ctypes.POINTER(ctypes.c_void_p)  # host array of device pointers
+_LL = ctypes.c_longlong
+_IP = ctypes.POINTER(ctypes.c_int)
 
 
 def _declare(lib: ctypes.CDLL) -> None:
@@ -102,6 +106,15 @@ def _declare(lib: ctypes.CDLL) -> None:
         "mla_cache_append_fp8": (_I, [_DP, _I, _I, _P, _P, ctypes.c_float, ctypes.c_float, _I, _P, _P, _P, _P]),
         "mla_cache_append_fp8_paged": (_I, [_DP, _I, _I, _P, _P, ctypes.c_float, ctypes.c_float, _P, _P, _I, _I,
                                             _P, _I, _P, _P]),
+        "mla_decode_tree_workspace_size": (_SZ, [_DP, _I, _I, _I, _I]),
+        "mla_decode_tree": (_I, [_DP, _I, _I, _I, _P, _P, _P, _I, _P, _P, _P, _I, _P, _P, _SZ, _P]),
+        "mla_decode_tree_paged": (_I, [_DP, _I, _I, _I, _P, _P, _P, _I, _I, _P, _I, _P, _P, _P, _I, _P, _P, _SZ, _P]),
+        "mla_cache_append_tree": (_I, [_DP, _I, _I, _I, _P, _P, ctypes.c_float, _I, _P, _P, _P, _P, _P]),
+        "mla_cache_append_tree_paged": (_I, [_DP, _I, _I, _I, _P, _P, ctypes.c_float, _P, _P, _I, _I, _P, _I, _P, _P,
+                                             _P]),
+        "mla_tree_verify": (_I, [_I, _I, _I, _P, _LL, _LL, _P, _LL, _LL, _P, _P, _P, _P, _P, _P, _P]),
+        "mla_tree_commit": (_I, [_I, _PP, _IP, _I, _I, _I, _P, _P, _P, _P, _P]),
+        "mla_tree_commit_paged": (_I, [_I, _PP, _IP, _I, _I, _I, _I, _P, _I, _P, _P, _P, _P, _P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -556,3 +569,235 @@ def cache_append_fp8_paged(comp, kv_a_ln, block_table, T, Lc8_pages, Rc_pages, d
                                             float(lat_scale), _ptr(Lc8_pages), _ptr(Rc_pages), num_pages, page_size,
                                             _ptr(block_table), block_table.shape[1], _ptr(T), _stream(stream)))
     return Lc8_pages, Rc_pages
+
+
+# ------------------------------------------------------------- drafted token trees
+def _on_device(device, stream, *named):
+    """The stream handle for a call on `device` (its current stream when none is
+    given) after checking that every (name, tensor, dtype) is a contiguous
+    tensor of that dtype there."""
+    torch = _torch()
+    for name, t, dtype in named:
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, not on {device}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    if device.type != "cuda":
+        raise ValueError("tensors must live on the GPU")
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors on {device}: make it the current device")
+    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+
+
+def _want(name, t, *shape):
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+
+
+def decode_tree_workspace_size(dims, dtype, B: int, S: int, T_cap: int) -> int:
+    """Workspace bytes of decode_tree (dtype: torch.float32 or torch.bfloat16); the
+    paged call takes T_cap = max_pages * page_size."""
+    torch = _torch()
+    code = MLA_BF16 if dtype in (torch.bfloat16, MLA_BF16) else MLA_F32
+    d = make_dims(dims)
+    return lib().mla_decode_tree_workspace_size(ctypes.byref(d), code, B, S, T_cap)
+
+
+def _tree_args(q, caches, T, parent, kv_b, dims, out, out_dtype, stream, extra=()):
+    """Checks shared by the two tree attentions -> (dims struct, dtype code, out, stream handle)."""
+    torch = _torch()
+    B, S, H, qk = q.shape
+    if H != dims.H or qk != dims.qk_nope + dims.qk_rope:
+        raise ValueError(f"q has shape {tuple(q.shape)}, expected [B, S, {dims.H}, {dims.qk_nope + dims.qk_rope}]")
+    code = _dtype_code(q)
+    if out is None:
+        out = torch.empty(B, S, H, dims.v_head, dtype=out_dtype or torch.float32, device=q.device)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise TypeError("out does not have out_dtype")
+    if caches[0].shape[2] != dims.kv_lora or caches[1].shape != caches[0].shape[:2] + (dims.qk_rope,):
+        raise ValueError("cache shapes do not match dims")
+    _want("T", T, B)
+    _want("parent", parent, B, S)
+    _want("kv_b", kv_b, H, dims.qk_nope + dims.v_head, dims.kv_lora)
+    _want("out", out, B, S, H, dims.v_head)
+    _dtype_code(out)
+    st = _on_device(q.device, stream, ("q", q, q.dtype), ("Lc", caches[0], q.dtype), ("Rc", caches[1], q.dtype),
+                    ("kv_b", kv_b, q.dtype), ("T", T, torch.int32), ("parent", parent, torch.int32),
+                    ("out", out, out.dtype), *extra)
+    return make_dims(dims), code, out, st
+
+
+def decode_tree(q, Lc, Rc, T, parent, kv_b, dims, out=None, out_dtype=None, workspace=None, stream=None):
+    """Absorbed decode of a drafted tree: q [B,S,H,qk] (node s at row T[b]-S+s), parent [B,S]
+    int32 (-1 a child of the last committed token, -2 absent).  out [B,S,H,v_head] in
+    out_dtype (float32 unless given; bfloat16 is rounded once)."""
+    B, S = q.shape[0], q.shape[1]
+    T_cap = Lc.shape[1]
+    d, code, out, st = _tree_args(q, (Lc, Rc), T, parent, kv_b, dims, out, out_dtype, stream)
+    if Lc.shape[0] != B:
+        raise ValueError(f"cache of {Lc.shape[0]} sequences for {B} queries")
+    need = lib().mla_decode_tree_workspace_size(ctypes.byref(d), code, B, S, T_cap)
+    workspace, wsb = _workspace(need, q.device, workspace)
+    _check(lib().mla_decode_tree(ctypes.byref(d), code, B, S, q.data_ptr(), Lc.data_ptr(), Rc.data_ptr(), T_cap,
+                                 T.data_ptr(), parent.data_ptr(), kv_b.data_ptr(), _dtype_code(out), out.data_ptr(),
+                                 _ptr(workspace), wsb, st))
+    return out
+
+
+def decode_tree_paged(q, Lc_pages, Rc_pages, block_table, T, parent, kv_b, dims, out=None, out_dtype=None,
+                      workspace=None, stream=None):
+    """decode_tree over page pools (layouts as for decode_paged)."""
+    torch = _torch()
+    B, S = q.shape[0], q.shape[1]
+    num_pages, page_size = Lc_pages.shape[0], Lc_pages.shape[1]
+    max_pages = block_table.shape[1]
+    _want("block_table", block_table, B, max_pages)
+    d, code, out, st = _tree_args(q, (Lc_pages, Rc_pages), T, parent, kv_b, dims, out, out_dtype, stream,
+                                  (("block_table", block_table, torch.int32),))
+    need = lib().mla_decode_tree_workspace_size(ctypes.byref(d), code, B, S, max_pages * page_size)
+    workspace, wsb = _workspace(need, q.device, workspace)
+    _check(lib().mla_decode_tree_paged(ctypes.byref(d), code, B, S, q.data_ptr(), Lc_pages.data_ptr(),
+                                       Rc_pages.data_ptr(), num_pages, page_size, block_table.data_ptr(), max_pages,
+                                       T.data_ptr(), parent.data_ptr(), kv_b.data_ptr(), _dtype_code(out),
+                                       out.data_ptr(), _ptr(workspace), wsb, st))
+    return out
+
+
+def _append_tree_args(comp, kv_a_ln, T, parent, Lc, Rc, dims, stream, extra=()):
+    torch = _torch()
+    B, S = comp.shape[0], comp.shape[1]
+    _want("comp", comp, B, S, dims.kv_lora + dims.qk_rope)
+    _want("kv_a_ln", kv_a_ln, dims.kv_lora)
+    _want("T", T, B)
+    _want("parent", parent, B, S)
+    if Lc.shape[2] != dims.kv_lora or Rc.shape != Lc.shape[:2] + (dims.qk_rope,):
+        raise ValueError("cache shapes do not match dims")
+    code = _dtype_code(comp)
+    st = _on_device(comp.device, stream, ("comp", comp, comp.dtype), ("kv_a_ln", kv_a_ln, comp.dtype),
+                    ("Lc", Lc, comp.dtype), ("Rc", Rc, comp.dtype), ("T", T, torch.int32),
+                    ("parent", parent, torch.int32), *extra)
+    return B, S, make_dims(dims), code, st
+
+
+def cache_append_tree(comp, kv_a_ln, T, parent, Lc, Rc, dims, rms_eps: float, stream=None):
+    """cache_append of a drafted tree: node s goes to row T[b]-S+s with the rotary
+    position of its depth; rows of absent nodes (parent -2) are left as they were."""
+    B, S, d, code, st = _append_tree_args(comp, kv_a_ln, T, parent, Lc, Rc, dims, stream)
+    if Lc.shape[0] != B:
+        raise ValueError(f"cache of {Lc.shape[0]} sequences for {B} rows")
+    _check(lib().mla_cache_append_tree(ctypes.byref(d), code, B, S, comp.data_ptr(), kv_a_ln.data_ptr(), rms_eps,
+                                       Lc.shape[1], T.data_ptr(), parent.data_ptr(), Lc.data_ptr(), Rc.data_ptr(), st))
+    return Lc, Rc
+
+
+def cache_append_tree_paged(comp, kv_a_ln, block_table, T, parent, Lc_pages, Rc_pages, dims, rms_eps: float,
+                            stream=None):
+    """cache_append_tree into the page pools (in place)."""
+    torch = _torch()
+    _want("block_table", block_table, comp.shape[0], block_table.shape[1])
+    B, S, d, code, st = _append_tree_args(comp, kv_a_ln, T, parent, Lc_pages, Rc_pages, dims, stream,
+                                          (("block_table", block_table, torch.int32),))
+    _check(lib().mla_cache_append_tree_paged(ctypes.byref(d), code, B, S, comp.data_ptr(), kv_a_ln.data_ptr(), rms_eps,
+                                             Lc_pages.data_ptr(), Rc_pages.data_ptr(), Lc_pages.shape[0],
+                                             Lc_pages.shape[1], block_table.data_ptr(), block_table.shape[1],
+                                             T.data_ptr(), parent.data_ptr(), st))
+    return Lc_pages, Rc_pages
+
+
+def tree_verify(p, q, tokens, parent, u, path=None, n_acc=None, token=None, stream=None):
+    """Accepts a path of each drafted tree and draws the token after it.
+
+    p [B,S+1,V] float32: the target's probabilities after the last committed token (row 0)
+    and after node s (row s+1); q likewise for the draft, or None for drafts without
+    probabilities (rows may be strided, values within a row contiguous); tokens, parent
+    [B,S] int32; u [B,S+1] float32 in [0,1).  Returns (path [B,S] accepted nodes then -1,
+    n_acc [B], token [B]), all int32."""
+    torch = _torch()
+    B, S = tokens.shape
+    V = p.shape[2]
+    for name, x in (("p", p), ("q", q)):
+        if x is None:
+            continue
+        _want(name, x, B, S + 1, V)
+        if x.dtype != torch.float32:
+            raise TypeError(f"{name} must be torch.float32, got {x.dtype}")
+        if x.stride(2) != 1 and V > 1:
+            raise ValueError(f"the values of a row of {name} must be contiguous")
+        if x.device != p.device:
+            raise ValueError(f"{name} is on {x.device}, not on {p.device}")
+    _want("parent", parent, B, S)
+    _want("u", u, B, S + 1)
+    if path is None:
+        path = torch.empty(B, S, dtype=torch.int32, device=p.device)
+    if n_acc is None:
+        n_acc = torch.empty(B, dtype=torch.int32, device=p.device)
+    if token is None:
+        token = torch.empty(B, dtype=torch.int32, device=p.device)
+    _want("path", path, B, S)
+    _want("n_acc", n_acc, B)
+    _want("token", token, B)
+    i32 = torch.int32
+    st = _on_device(p.device, stream, ("tokens", tokens, i32), ("parent", parent, i32), ("u", u, torch.float32),
+                    ("path", path, i32), ("n_acc", n_acc, i32), ("token", token, i32))
+    _check(lib().mla_tree_verify(B, S, V, p.data_ptr(), p.stride(1), p.stride(0),
+                                 None if q is None else q.data_ptr(), 0 if q is None else q.stride(1),
+                                 0 if q is None else q.stride(0), tokens.data_ptr(), parent.data_ptr(), u.data_ptr(),
+                                 path.data_ptr(), n_acc.data_ptr(), token.data_ptr(), st))
+    return path, n_acc, token
+
+
+class CacheRows:
+    """The caches that tree_commit moves rows in: every layer's tensors [B, T_cap, row]
+    (any dtypes and row widths), or pools [num_pages, page_size, row] with their
+    block_table [B, max_pages].  Holds the tensors, so it can be kept with them."""
+
+    def __init__(self, caches, block_table=None):
+        torch = _torch()
+        self.caches = list(caches)
+        if not self.caches:
+            raise ValueError("no caches")
+        first = self.caches[0]
+        for c in self.caches:
+            if c.dim() != 3 or c.shape[:2] != first.shape[:2] or c.shape[2] < 1:
+                raise ValueError("caches need one shape [B, T_cap, row] up to the row width")
+        for c in self.caches:
+            if not c.is_cuda or c.device != first.device or not c.is_contiguous():
+                raise ValueError("caches must be contiguous tensors on one GPU")
+        self.device = first.device
+        self.block_table = block_table
+        if block_table is not None:
+            if block_table.dtype != torch.int32 or block_table.device != self.device or not block_table.is_contiguous():
+                raise ValueError("block_table must be a contiguous int32 tensor on the caches' GPU")
+        self.B = first.shape[0] if block_table is None else block_table.shape[0]
+        n = len(self.caches)
+        self.n = n
+        self.pointers = (ctypes.c_void_p * n)(*[c.data_ptr() for c in self.caches])
+        self.row_bytes = (ctypes.c_int * n)(*[c.shape[2] * c.element_size() for c in self.caches])
+
+
+def tree_commit(rows: CacheRows, T, path, n_acc, T_out=None, stream=None):
+    """Moves the rows of the accepted nodes (path, n_acc of tree_verify) to the front of the
+    tree's rows in every cache of `rows`; returns T_out [B] int32 = T - S + n_acc."""
+    torch = _torch()
+    B, S = path.shape
+    if B != rows.B:
+        raise ValueError(f"caches of {rows.B} sequences, path of {B}")
+    if T_out is None:
+        T_out = torch.empty(B, dtype=torch.int32, device=path.device)
+    _want("T", T, B)
+    _want("n_acc", n_acc, B)
+    _want("T_out", T_out, B)
+    i32 = torch.int32
+    st = _on_device(rows.device, stream, ("T", T, i32), ("path", path, i32), ("n_acc", n_acc, i32), ("T_out", T_out, i32))
+    first = rows.caches[0]
+    if rows.block_table is None:
+        rc = lib().mla_tree_commit(rows.n, rows.pointers, rows.row_bytes, B, S, first.shape[1], T.data_ptr(),
+                                   path.data_ptr(), n_acc.data_ptr(), T_out.data_ptr(), st)
+    else:
+        rc = lib().mla_tree_commit_paged(rows.n, rows.pointers, rows.row_bytes, B, S, first.shape[0], first.shape[1],
+                                         rows.block_table.data_ptr(), rows.block_table.shape[1], T.data_ptr(),
+                                         path.data_ptr(), n_acc.data_ptr(), T_out.data_ptr(), st)
+    _check(rc)
+    return T_out

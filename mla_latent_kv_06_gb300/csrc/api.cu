@@ -745,7 +745,7 @@ MLA_EXPORT int mla_sparse_decode_layers(const mla_dims* d, int dtype, int L, int
 namespace {
 int run_cache_append(const mla_dims* d, int dtype, int B, int S, const void* comp, const void* kv_a_ln,
                      float rms_eps, int T_cap, const int32_t* T, void* Lc, void* Rc, const mla::PageTable& pages,
-                     void* stream, const char* what, float lat_scale = 0.f) {
+                     void* stream, const char* what, float lat_scale = 0.f, const int32_t* parent = nullptr) {
   mla::Geometry g;
   int rc = check_common(d, dtype, B, S, &g);
   if (rc != MLA_OK) return rc;
@@ -758,6 +758,7 @@ int run_cache_append(const mla_dims* d, int dtype, int B, int S, const void* com
   if (!pages.table && (long long)B * T_cap >= (1ll << 31))
     return fail(MLA_ERR_UNSUPPORTED, "B*T_cap of 2^31 rows or more");
   mla::AppendArgs a{B, S, T_cap, g.Dl, g.Dr, comp, kv_a_ln, rms_eps, T, Lc, Rc, flags_ptr(), pages, {}};
+  a.parent = parent;
   if (lat_scale != 0.f) {  // the FP8 cache
     a.lat_fp8 = 1;
     a.lat_inv_scale = 1.f / lat_scale;
@@ -838,4 +839,169 @@ MLA_EXPORT int dsa_index_key_append(int B, int S, int index_hd, int rope_dim, co
   mla::call_end(st);
   if (e != cudaSuccess) return cuda_fail(e, "dsa_index_key_append launch");
   return MLA_OK;
+}
+
+// ---------------------------------------------------------------- drafted token trees
+namespace {
+int check_tree(int B, int S, const int32_t* parent) {
+  if (B < 1 || S < 1) return fail(MLA_ERR_INVALID, "B=%d and S=%d must be >= 1", B, S);
+  if (S > mla::kMaxTree) return fail(MLA_ERR_UNSUPPORTED, "S=%d: trees have at most %d nodes", S, mla::kMaxTree);
+  if (!parent) return fail(MLA_ERR_INVALID, "null parent array");
+  return MLA_OK;
+}
+
+int run_decode_tree(const mla_dims* d, int dtype, int B, int S, const void* q, const void* Lc, const void* Rc,
+                    int T_cap, const mla::PageTable& pages, const int32_t* T, const int32_t* parent, const void* kv_b,
+                    int out_dtype, void* out, void* workspace, size_t workspace_bytes, void* stream, const char* what) {
+  mla::DecodeArgs a{};
+  int rc = check_common(d, dtype, B, S, &a.g);
+  if (rc) return rc;
+  rc = check_tree(B, S, parent);
+  if (rc) return rc;
+  if (out_dtype != MLA_F32 && out_dtype != MLA_BF16) return fail(MLA_ERR_INVALID, "unknown out_dtype %d", out_dtype);
+  if (T_cap < S) return fail(MLA_ERR_INVALID, "T_cap=%d < S=%d", T_cap, S);
+  if (!q || !Lc || !Rc || !T || !kv_b || !out) return fail(MLA_ERR_INVALID, "null tensor pointer");
+  // the many-row path stores out 16 bytes at a time
+  if (!aligned16(out)) return fail(MLA_ERR_INVALID, "out must be 16-byte aligned");
+  a.B = B;
+  a.S = S;
+  a.T_cap = T_cap;
+  a.q = q;
+  a.Lc = Lc;
+  a.Rc = Rc;
+  a.T = T;
+  a.kv_b = kv_b;
+  a.out = out;
+  a.out_bf16 = out_dtype == MLA_BF16;
+  a.parent = parent;
+  a.pages = pages;
+  return run_decode(a, dtype, false, workspace, workspace_bytes, stream, what);
+}
+
+int run_commit(mla::CommitArgs& a, int n, void* const* cache, const int* row_bytes, int32_t* T_out, void* stream,
+               const char* what) {
+  if (n < 1) return fail(MLA_ERR_INVALID, "n=%d caches", n);
+  if (a.B < 1 || a.B > 65535 || a.S < 1 || a.T_cap < a.S)
+    return fail(MLA_ERR_INVALID, "bad sizes B=%d S=%d T_cap=%d (B at most 65535)", a.B, a.S, a.T_cap);
+  if (a.S > mla::kMaxTree) return fail(MLA_ERR_UNSUPPORTED, "S=%d: trees have at most %d nodes", a.S, mla::kMaxTree);
+  if (!cache || !row_bytes || !a.T || !a.path || !a.n_acc) return fail(MLA_ERR_INVALID, "null pointer");
+  if (T_out == a.T) return fail(MLA_ERR_INVALID, "T_out must not be T");
+  for (int i = 0; i < n; ++i)
+    if (!cache[i] || row_bytes[i] < 1) return fail(MLA_ERR_INVALID, "cache %d: null pointer or row_bytes < 1", i);
+  a.flags = flags_ptr();
+  if (!a.flags) return fail(MLA_ERR_CUDA, "cannot resolve the device status word");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  mla::call_begin();
+  cudaError_t e = cudaSuccess;
+  for (int i0 = 0; i0 < n && e == cudaSuccess; i0 += mla::kCommitCaches) {
+    a.n = n - i0 < mla::kCommitCaches ? n - i0 : mla::kCommitCaches;
+    a.T_out = i0 == 0 ? T_out : nullptr;
+    for (int i = 0; i < a.n; ++i) {
+      a.cache[i] = cache[i0 + i];
+      a.row_bytes[i] = row_bytes[i0 + i];
+    }
+    mla::kernel_mark(st, "tree_commit");
+    e = mla::launch_tree_commit(a, st);
+  }
+  mla::call_end(st);
+  if (e != cudaSuccess) return cuda_fail(e, what);
+  return MLA_OK;
+}
+}  // namespace
+
+MLA_EXPORT size_t mla_decode_tree_workspace_size(const mla_dims* d, int dtype, int B, int S, int T_cap) {
+  mla::Geometry g;
+  if (!resolve(d, &g) || B < 1 || S < 1 || S > mla::kMaxTree || T_cap < S) return 0;
+  if (dtype == MLA_BF16 && mla::tc_decode_geometry_ok(g))
+    return round256(mla::tc_decode_workspace_bytes(g, B, S, T_cap, /*sparse_topk=*/0));
+  return 0;
+}
+
+MLA_EXPORT int mla_decode_tree(const mla_dims* d, int dtype, int B, int S, const void* q, const void* Lc,
+                               const void* Rc, int T_cap, const int32_t* T, const int32_t* parent, const void* kv_b,
+                               int out_dtype, void* out, void* workspace, size_t workspace_bytes, void* stream) {
+  return run_decode_tree(d, dtype, B, S, q, Lc, Rc, T_cap, mla::PageTable{}, T, parent, kv_b, out_dtype, out, workspace,
+                         workspace_bytes, stream, "mla_decode_tree launch");
+}
+
+MLA_EXPORT int mla_decode_tree_paged(const mla_dims* d, int dtype, int B, int S, const void* q, const void* Lc_pages,
+                                     const void* Rc_pages, int num_pages, int page_size, const int32_t* block_table,
+                                     int max_pages, const int32_t* T, const int32_t* parent, const void* kv_b,
+                                     int out_dtype, void* out, void* workspace, size_t workspace_bytes, void* stream) {
+  mla::PageTable pt{};
+  int rc = check_pages(S, num_pages, page_size, block_table, max_pages, &pt);
+  if (rc) return rc;
+  return run_decode_tree(d, dtype, B, S, q, Lc_pages, Rc_pages, max_pages * page_size, pt, T, parent, kv_b, out_dtype,
+                         out, workspace, workspace_bytes, stream, "mla_decode_tree_paged launch");
+}
+
+MLA_EXPORT int mla_cache_append_tree(const mla_dims* d, int dtype, int B, int S, const void* comp, const void* kv_a_ln,
+                                     float rms_eps, int T_cap, const int32_t* T, const int32_t* parent, void* Lc,
+                                     void* Rc, void* stream) {
+  int rc = check_tree(B, S, parent);
+  if (rc) return rc;
+  return run_cache_append(d, dtype, B, S, comp, kv_a_ln, rms_eps, T_cap, T, Lc, Rc, mla::PageTable{}, stream,
+                          "mla_cache_append_tree launch", 0.f, parent);
+}
+
+MLA_EXPORT int mla_cache_append_tree_paged(const mla_dims* d, int dtype, int B, int S, const void* comp,
+                                           const void* kv_a_ln, float rms_eps, void* Lc_pages, void* Rc_pages,
+                                           int num_pages, int page_size, const int32_t* block_table, int max_pages,
+                                           const int32_t* T, const int32_t* parent, void* stream) {
+  int rc = check_tree(B, S, parent);
+  if (rc) return rc;
+  mla::PageTable pt{};
+  rc = check_pages(S, num_pages, page_size, block_table, max_pages, &pt);
+  if (rc) return rc;
+  return run_cache_append(d, dtype, B, S, comp, kv_a_ln, rms_eps, max_pages * page_size, T, Lc_pages, Rc_pages, pt,
+                          stream, "mla_cache_append_tree_paged launch", 0.f, parent);
+}
+
+MLA_EXPORT int mla_tree_verify(int B, int S, int V, const float* p, long long p_row, long long p_batch, const float* q,
+                               long long q_row, long long q_batch, const int32_t* tokens, const int32_t* parent,
+                               const float* u, int32_t* path, int32_t* n_acc, int32_t* token, void* stream) {
+  int rc = check_tree(B, S, parent);
+  if (rc) return rc;
+  if (V < 1 || V > (1 << 30) || B > (1 << 24))
+    return fail(MLA_ERR_INVALID, "bad sizes B=%d V=%d (B at most 2^24, V at most 2^30)", B, V);
+  if (!p || !tokens || !u || !path || !n_acc || !token) return fail(MLA_ERR_INVALID, "null tensor pointer");
+  if (p_row < V || p_batch < 0 || (q && (q_row < V || q_batch < 0)))
+    return fail(MLA_ERR_INVALID, "rows of %d values need p_row and q_row >= V and batch strides >= 0", V);
+  mla::VerifyArgs a{B, S, V, p, q, p_row, p_batch, q_row, q_batch, tokens, parent, u, path, n_acc, token, flags_ptr()};
+  if (!a.flags) return fail(MLA_ERR_CUDA, "cannot resolve the device status word");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  mla::call_begin();
+  mla::kernel_mark(st, "tree_verify");
+  cudaError_t e = mla::launch_tree_verify(a, st);
+  mla::call_end(st);
+  if (e != cudaSuccess) return cuda_fail(e, "mla_tree_verify launch");
+  return MLA_OK;
+}
+
+MLA_EXPORT int mla_tree_commit(int n, void* const* cache, const int* row_bytes, int B, int S, int T_cap,
+                               const int32_t* T, const int32_t* path, const int32_t* n_acc, int32_t* T_out,
+                               void* stream) {
+  mla::CommitArgs a{};
+  a.B = B;
+  a.S = S;
+  a.T_cap = T_cap;
+  a.T = T;
+  a.path = path;
+  a.n_acc = n_acc;
+  return run_commit(a, n, cache, row_bytes, T_out, stream, "mla_tree_commit launch");
+}
+
+MLA_EXPORT int mla_tree_commit_paged(int n, void* const* cache, const int* row_bytes, int B, int S, int num_pages,
+                                     int page_size, const int32_t* block_table, int max_pages, const int32_t* T,
+                                     const int32_t* path, const int32_t* n_acc, int32_t* T_out, void* stream) {
+  mla::CommitArgs a{};
+  int rc = check_pages(S, num_pages, page_size, block_table, max_pages, &a.pages);
+  if (rc) return rc;
+  a.B = B;
+  a.S = S;
+  a.T_cap = max_pages * page_size;
+  a.T = T;
+  a.path = path;
+  a.n_acc = n_acc;
+  return run_commit(a, n, cache, row_bytes, T_out, stream, "mla_tree_commit_paged launch");
 }

@@ -23,6 +23,7 @@
 #include "common.cuh"
 #include "internal.h"
 #include "sm100.cuh"
+#include "tree.cuh"
 
 namespace mla {
 namespace {
@@ -83,6 +84,7 @@ struct AttnParams {
   unsigned int* flags;
   long long wait_ns;
   PageTable pages;  // dense path: key tiles come from pages (page_size a multiple of kTile)
+  const int32_t* parent;  // tree attention: [B, S] parent indices
 };
 
 // One arrival per warp on a barrier initialised with the number of arriving
@@ -259,6 +261,7 @@ struct AttnCtx {
   int NR;
   long long N;        // ts[NR]
   int g, s;           // chunk, query position
+  int sr;             // position that bounds the keys: s, or S - 1 where a tree mask decides (all of T)
   int part, mb0, mb1; // latent part (value-product blocks [mb0, mb1))
   int row0;           // first tile-list row of chunk g
   unsigned char* sQ;  // query block (9 atoms of 64 rows x 64 bf16)
@@ -321,7 +324,7 @@ __device__ __forceinline__ void attn_producer(const AttnParams& p, AttnShared& s
   const int S = p.S;
   const uint64_t pol_once = l2_policy_evict_first();
   TileCursor<kSparse> c;
-  c.start(p, cx.ts, cx.NR, cx.N, cx.g, cx.s, cx.row0);
+  c.start(p, cx.ts, cx.NR, cx.N, cx.g, cx.sr, cx.row0);
   int it = 0, pc = -1, last_it[kSlots], last_q = -1;
   for (int a = 0; a < kSlots; ++a) last_it[a] = -1;
   bool ok = true, q_waited = false;
@@ -365,7 +368,7 @@ __device__ __forceinline__ void attn_producer(const AttnParams& p, AttnShared& s
       }
     }
     ++it;
-    c.next(p, cx.ts, cx.NR, cx.N, cx.g, cx.s);
+    c.next(p, cx.ts, cx.NR, cx.N, cx.g, cx.sr);
   }
   // Never leave with copies in flight: wait for the last load of each slot.
   volatile int no_abort = 0;
@@ -397,7 +400,7 @@ __device__ __forceinline__ void attn_mma(const AttnParams& p, AttnShared& sh, co
   const uint64_t dO0 = smem_desc_sw128(kv0, kSlotBytes, 1024);             // value A: latent atoms, MN-major
   const uint64_t dP0 = smem_desc_sw128(kv0 + 8 * kSlotBytes, kSlotBytes, 1024);  // value B: P^T, MN-major
   TileCursor<kSparse> c;
-  c.start(p, cx.ts, cx.NR, cx.N, cx.g, cx.s, cx.row0);
+  c.start(p, cx.ts, cx.NR, cx.N, cx.g, cx.sr, cx.row0);
   int it = 0, pc = -1;
   bool ok = true, issued = false;
   auto wait = [&](uint64_t* bar, uint32_t par) -> bool {
@@ -407,7 +410,7 @@ __device__ __forceinline__ void attn_mma(const AttnParams& p, AttnShared& sh, co
   while (ok && c.live) {
     const bool first = c.first();
     // keys of this tile, read now so that the load overlaps the waits below
-    const int ksteps = (tile_keys<kSparse>(p, c.row, cx.s, c.k) + 15) >> 4;
+    const int ksteps = (tile_keys<kSparse>(p, c.row, cx.sr, c.k) + 15) >> 4;
     if (first) {
       ++pc;
       ok = wait(&sh.q_full, pc & 1);
@@ -489,7 +492,7 @@ __device__ __forceinline__ void attn_mma(const AttnParams& p, AttnShared& sh, co
     }
     __syncwarp();
     ++it;
-    c.next(p, cx.ts, cx.NR, cx.N, cx.g, cx.s);
+    c.next(p, cx.ts, cx.NR, cx.N, cx.g, cx.sr);
   }
   if (issued) {  // all MMAs retired before TMEM is released
     if (lane == 0) mma_commit(&sh.mma_done);
@@ -501,7 +504,11 @@ __device__ __forceinline__ void attn_mma(const AttnParams& p, AttnShared& sh, co
 }
 
 // ------------------------------------------------------------ softmax warps 2..9
-template <bool kSparse>
+// kTree: the query is node s of a drafted tree: it sees the prefix t < T - S
+// and, among the S tree rows, those of its mask.  A tile may then hold no
+// visible key at all, so the running max starts at a finite floor: such a tile
+// (and an absent node) contributes probabilities of exactly zero.
+template <bool kSparse, bool kTree = false>
 __device__ __forceinline__ void attn_softmax(const AttnParams& p, AttnShared& sh, const AttnCtx& cx) {
   volatile int* abort = &sh.abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -517,9 +524,11 @@ __device__ __forceinline__ void attn_softmax(const AttnParams& p, AttnShared& sh
   const uint32_t t_lane = (uint32_t)(32 * qd) << 16;
   const float c = p.c;
   TileCursor<kSparse> cur;
-  cur.start(p, cx.ts, cx.NR, cx.N, g, s, cx.row0);
+  cur.start(p, cx.ts, cx.NR, cx.N, g, cx.sr, cx.row0);
   int it = 0, slot = 0, pos = 0, nkeys = 0;
   const int32_t* srow = nullptr;
+  unsigned long long tmask = 0;
+  int base = 0;  // tree: keys before the tree rows that the node sees (0 for an absent node)
   bool ok = true, bad_idx = false;
   float lp[32];
 #pragma unroll
@@ -568,6 +577,13 @@ __device__ __forceinline__ void attn_softmax(const AttnParams& p, AttnShared& sh
       const int qs = kSparse ? cur.row % S : s;
       pos = p.T[b] - S + qs;
       nkeys = kSparse ? p.nsel[cur.row] : pos + 1;
+      if (kTree) {
+        const TreeNode node = tree_node(p.parent + (size_t)cur.row * S, s);
+        tmask = node.mask;
+        nkeys = p.T[cur.row];
+        base = nkeys - S;
+        if (node.state == kNodeBad && tsm == 0) raise_flag(p.flags, MLA_DEV_BAD_INDEX);
+      }
       srow = kSparse ? p.sel + (size_t)cur.row * p.topk : nullptr;
       slot = kSparse ? g + cur.row : (g + cur.row) * S + s;
       bad_idx = false;
@@ -589,6 +605,7 @@ __device__ __forceinline__ void attn_softmax(const AttnParams& p, AttnShared& sh
     mbar_arrive_warp(&sh.s_free);
     const int j = cur.k * kTile + trow;
     bool valid = j < nkeys;
+    if (kTree) valid = valid && tmask != 0 && (j < base || ((tmask >> (j - base)) & 1ull));
     if (kSparse && valid) {
       const int idx = srow[j];
       if (idx < 0 || idx > pos) {
@@ -628,7 +645,7 @@ __device__ __forceinline__ void attn_softmax(const AttnParams& p, AttnShared& sh
         const float tmax =
             fmaxf(fmaxf(sh.red_max[0][tsm], sh.red_max[1][tsm]), fmaxf(sh.red_max[2][tsm], sh.red_max[3][tsm]));
         const float cand = tmax * c;
-        const float mo = first ? -INFINITY : sh.m_sh[tsm];
+        const float mo = first ? (kTree ? -1e30f : -INFINITY) : sh.m_sh[tsm];
         float mn = mo, al = 1.f;
         if (cand > mo + kTau) {
           mn = cand;
@@ -711,7 +728,7 @@ __device__ __forceinline__ void attn_softmax(const AttnParams& p, AttnShared& sh
     tc_fence_before();
     mbar_arrive_warp(&sh.p_full);
     ++it;
-    cur.next(p, cx.ts, cx.NR, cx.N, g, s);
+    cur.next(p, cx.ts, cx.NR, cx.N, g, cx.sr);
   }
   if (ok && it > 0) epilogue();
 }

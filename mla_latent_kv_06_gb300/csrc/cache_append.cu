@@ -18,6 +18,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "tree.cuh"
 
 namespace mla {
 namespace {
@@ -86,10 +87,16 @@ __global__ void __launch_bounds__(kAppThreads) cache_append_kernel(AppendArgs a)
 #pragma unroll
   for (int k = 0; k < kPer; ++k) ss = fmaf(xv[k], xv[k], ss);
   const float inv = rsqrtf(block_sum(ss, red) / (float)a.kv_lora + a.eps);
-  const int pos = new_row(Tb, s, a.S, a.T_cap, a.flags);
+  int pos = new_row(Tb, s, a.S, a.T_cap, a.flags);
   if (pos < 0) return;
   bool bad_page = false;
   const long long row = cache_row(a.pages, b, a.T_cap, pos, &bad_page);
+  if (a.parent) {  // a tree node: its row stays, its rotary position is the prefix plus its depth
+    const TreeNode node = tree_node(a.parent + (size_t)b * a.S, s);
+    if (node.state == kNodeBad && tid == 0) raise_flag(a.flags, MLA_DEV_BAD_INDEX);
+    if (node.state != kNodePresent) return;
+    pos = Tb - a.S + node.depth;
+  }
   if (bad_page) {
     if (tid == 0) raise_flag(a.flags, MLA_DEV_BAD_INDEX);
     return;

@@ -10,6 +10,7 @@
 // or bf16 inputs.  The GLM-shaped bf16 case runs on the tensor-core kernels.
 #include "common.cuh"
 #include "internal.h"
+#include "tree.cuh"
 
 namespace mla {
 namespace {
@@ -18,14 +19,21 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kChunk = 64;
 
-template <typename Tin, bool kSparse>
+__device__ __forceinline__ void put(void* out, bool bf16, size_t i, float v) {
+  if (bf16) static_cast<__nv_bfloat16*>(out)[i] = __float2bfloat16_rn(v);
+  else static_cast<float*>(out)[i] = v;
+}
+
+// kTree: query s is a node of a drafted tree (see tree.cuh).
+template <typename Tin, bool kSparse, bool kTree>
 __global__ void __launch_bounds__(kThreads) decode_simt_kernel(DecodeArgs a) {
   const Geometry g = a.g;
   const int h = blockIdx.x, s = blockIdx.y, b = blockIdx.z;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int Dq = g.Dn + g.Dr;
   const int Dkv = g.Dn + g.Dv;
-  float* out = a.out + (((size_t)b * a.S + s) * g.H + h) * g.Dv;
+  const size_t orow = (((size_t)b * a.S + s) * g.H + h) * g.Dv;
+  const bool ob = a.out_bf16 != 0;
 
   extern __shared__ float smem[];
   float* qn = smem;               // [Dn]
@@ -37,16 +45,23 @@ __global__ void __launch_bounds__(kThreads) decode_simt_kernel(DecodeArgs a) {
 
   const int Tb = a.T[b];
   const bool bad_len = (Tb < a.S || Tb > a.T_cap);
-  const int pos = Tb - a.S + s;
-  int n = pos + 1;
-  bool bad_sel = false;
+  TreeNode node{};
+  if (kTree) node = tree_node(a.parent + (size_t)b * a.S, s);
+  const int base = Tb - a.S;
+  const int pos = base + (kTree ? node.depth : s);
+  int n = kTree ? Tb : pos + 1;
+  bool bad_sel = kTree && node.state == kNodeBad;
   if (!bad_len && kSparse) {
     n = a.nsel[(size_t)b * a.S + s];
     bad_sel = (n < 1 || n > a.topk);
   }
   if (bad_len || bad_sel) {
     if (tid == 0) raise_flag(a.flags, bad_len ? MLA_DEV_BAD_LENGTH : MLA_DEV_BAD_INDEX);
-    for (int j = tid; j < g.Dv; j += kThreads) out[j] = qnan();
+    for (int j = tid; j < g.Dv; j += kThreads) put(a.out, ob, orow + j, qnan());
+    return;
+  }
+  if (kTree && node.state == kNodeAbsent) {
+    for (int j = tid; j < g.Dv; j += kThreads) put(a.out, ob, orow + j, 0.f);
     return;
   }
   const int32_t* sel = kSparse ? a.sel + ((size_t)b * a.S + s) * a.topk : nullptr;
@@ -82,7 +97,8 @@ __global__ void __launch_bounds__(kThreads) decode_simt_kernel(DecodeArgs a) {
     const int cn = min(kChunk, n - c0);
     for (int j = warp; j < cn; j += kWarps) {
       int t = kSparse ? sel[c0 + j] : c0 + j;
-      bool ok = (t >= 0 && t <= pos);
+      const bool seen = kTree ? t < base || ((node.mask >> (t - base)) & 1ull) : true;
+      bool ok = kTree ? seen : (t >= 0 && t <= pos);
       long long row = 0;
       if (ok) {
         bool bad_page = false;
@@ -99,7 +115,8 @@ __global__ void __launch_bounds__(kThreads) decode_simt_kernel(DecodeArgs a) {
       }
       if (lane == 0) {
         sc[j] = ok ? dot * g.scale : -INFINITY;
-        tok[j] = ok ? (int)row : -1;  // pool row (< 2^31, checked on the host)
+        // pool row (< 2^31, checked on the host); -1: a bad index or page, -2: outside the tree mask
+        tok[j] = ok ? (int)row : seen ? -1 : -2;
       }
     }
     __syncthreads();
@@ -113,7 +130,7 @@ __global__ void __launch_bounds__(kThreads) decode_simt_kernel(DecodeArgs a) {
     float psum = 0.f;
     for (int j = 0; j < cn; ++j) {
       psum += sc[j];
-      bad_index |= (tok[j] < 0);
+      bad_index |= (tok[j] == -1);
     }
     lsum = lsum * alpha + psum;
     for (int l = tid; l < g.Dl; l += kThreads) {
@@ -127,7 +144,7 @@ __global__ void __launch_bounds__(kThreads) decode_simt_kernel(DecodeArgs a) {
   }
   if (bad_index) {
     if (tid == 0) raise_flag(a.flags, MLA_DEV_BAD_INDEX);
-    for (int j = tid; j < g.Dv; j += kThreads) out[j] = qnan();
+    for (int j = tid; j < g.Dv; j += kThreads) put(a.out, ob, orow + j, qnan());
     return;
   }
   const float inv = 1.f / lsum;
@@ -139,15 +156,15 @@ __global__ void __launch_bounds__(kThreads) decode_simt_kernel(DecodeArgs a) {
     float acc = 0.f;
     for (int l = lane; l < g.Dl; l += 32) acc = fmaf(to_f32(wrow[l]), clat[l], acc);
     acc = warp_sum(acc);
-    if (lane == 0) out[j] = acc;
+    if (lane == 0) put(a.out, ob, orow + j, acc);
   }
 }
 
-template <typename Tin, bool kSparse>
+template <typename Tin, bool kSparse, bool kTree = false>
 cudaError_t launch(const DecodeArgs& a, cudaStream_t st) {
   const Geometry& g = a.g;
   size_t smem = sizeof(float) * (g.Dn + g.Dr + 2 * g.Dl + kChunk) + sizeof(int) * kChunk;
-  auto kern = decode_simt_kernel<Tin, kSparse>;
+  auto kern = decode_simt_kernel<Tin, kSparse, kTree>;
   if (smem > 48 * 1024) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
@@ -160,6 +177,8 @@ cudaError_t launch(const DecodeArgs& a, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_decode_simt(const DecodeArgs& a, int dtype, bool sparse, cudaStream_t st) {
+  if (a.parent)
+    return dtype == MLA_F32 ? launch<float, false, true>(a, st) : launch<__nv_bfloat16, false, true>(a, st);
   if (dtype == MLA_F32) return sparse ? launch<float, true>(a, st) : launch<float, false>(a, st);
   return sparse ? launch<__nv_bfloat16, true>(a, st) : launch<__nv_bfloat16, false>(a, st);
 }

@@ -55,7 +55,7 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
 // programmatic dependent launch behind the absorb kernel (only the query-block
 // loads wait for it; the key tiles stream in meanwhile).
 // ===========================================================================
-template <bool kSparse, bool kPaged = false, bool kStream = false>
+template <bool kSparse, bool kPaged = false, bool kStream = false, bool kTree = false>
 __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_constant__ AttnParams p) {
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -105,6 +105,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
   cx.N = cx.ts[cx.NR];
   cx.g = kSparse ? brow : brow / S;
   cx.s = kSparse ? 0 : brow % S;
+  cx.sr = kTree ? S - 1 : cx.s;
   cx.part = part;
   cx.mb0 = part * (4 / p.qsplit);
   cx.mb1 = cx.mb0 + 4 / p.qsplit;
@@ -123,7 +124,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
   } else if (warp == 1) {
     attn_mma<kSparse, kStream>(p, sh, cx);
   } else {
-    attn_softmax<kSparse>(p, sh, cx);
+    attn_softmax<kSparse, kTree>(p, sh, cx);
   }
   tc_fence_before();
   __syncthreads();
@@ -821,14 +822,21 @@ struct AbsorbParams {
   uint64_t turn[kDr / 2];  // rope_turns(rope_base^(-2j/qk_rope)), from the host
   unsigned int* flags;
   PageTable pages;
+  const int32_t* parent;  // tree attention: [B, S] parent indices, else null
 };
+
+// Rotary position of query row s of sequence b (length Tb): its row, or the
+// prefix length plus its depth in a drafted tree.  Bad lengths give 0.
+__device__ __forceinline__ int query_pos(const AbsorbParams& p, int b, int s, int Tb) {
+  if (Tb < p.S || Tb > p.T_cap) return 0;
+  return Tb - p.S + (p.parent ? tree_node(p.parent + (size_t)b * p.S, s).depth : s);
+}
 
 // Rotary part of query row r of head h, rotated to the row's own position.
 __device__ __forceinline__ void rope_row(const AbsorbParams& p, int r, int h, int j) {
   const int Dq = p.Dn + kDr;
   const int b = r / p.S, s = r % p.S;
-  const int Tb = p.T[b];
-  const int pos = (Tb < p.S || Tb > p.T_cap) ? 0 : Tb - p.S + s;
+  const int pos = query_pos(p, b, s, p.T[b]);
   float sn, cs;
   rope_cs_turns(pos, p.turn[j], &cs, &sn);
   const __nv_bfloat16* qr = p.q + ((size_t)r * kH + h) * Dq + p.Dn;
@@ -846,6 +854,16 @@ __device__ __forceinline__ void rope_rows(const AbsorbParams& p, int h, int tid,
   for (int e0 = tid; e0 < n; e0 += 8 * nthr) {
     uint32_t raw[8];
     int Tb[8];
+    // the 32 pairs of a row sit in one warp, so lane u walks up the tree for
+    // the warp's u-th row
+    int depth = 0;
+    if (p.parent) {
+      const int lane = threadIdx.x & 31, e = e0 - lane + lane * nthr;
+      if (lane < 8 && e < n) {
+        const int r = e / (kDr / 2);
+        depth = tree_node(p.parent + (size_t)(r / p.S) * p.S, r % p.S).depth;
+      }
+    }
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
       const int e = e0 + u * nthr;
@@ -858,8 +876,9 @@ __device__ __forceinline__ void rope_rows(const AbsorbParams& p, int h, int tid,
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
       const int e = e0 + u * nthr;
+      const int up = p.parent ? __shfl_sync(0xffffffffu, depth, u) : 0;
       if (e < n) {
-        const int r = e / (kDr / 2), j = e % (kDr / 2), s = r % p.S;
+        const int r = e / (kDr / 2), j = e % (kDr / 2), s = p.parent ? up : r % p.S;
         const int pos = (Tb[u] < p.S || Tb[u] > p.T_cap) ? 0 : Tb[u] - p.S + s;
         float sn, cs;
         rope_cs_turns(pos, p.turn[j], &cs, &sn);
@@ -1051,9 +1070,11 @@ struct CombineParams {
   const float* ml_part;
   const int32_t* T;
   const int32_t* nsel;
-  float* out;  // [R, 64, Dv], R <= kCmbRows
+  void* out;  // [R, 64, Dv] float or bf16, R <= kCmbRows
   int B, S, G, Dn, Dv, sparse, T_cap, topk;
   unsigned int* flags;
+  int out_bf16;
+  const int32_t* parent;  // tree attention: [B, S] parent indices, else null
 };
 
 
@@ -1111,6 +1132,8 @@ __global__ void __launch_bounds__(kCmbThreads) combine_kernel(const CombineParam
   if (warp < nr) {
     const int r = warp, b = r / p.S, s = r % p.S;
     const int row = p.sparse ? r : b;
+    const int sr = p.parent ? p.S - 1 : s;
+    const int state = p.parent ? tree_node(p.parent + (size_t)b * p.S, s).state : kNodePresent;
     int cnt = 0;
     if (!cbad[row] && N > 0) {
       const long long a = cts[row], e = cts[row + 1];
@@ -1120,7 +1143,7 @@ __global__ void __launch_bounds__(kCmbThreads) combine_kernel(const CombineParam
         int lo = 0, hi = 0;
         if (gg <= ghi) {
           if (p.sparse) piece_range<true>(cts, p.T, p.S, s, row, gg, p.G, N, &lo, &hi);
-          else piece_range<false>(cts, p.T, p.S, s, row, gg, p.G, N, &lo, &hi);
+          else piece_range<false>(cts, p.T, p.S, sr, row, gg, p.G, N, &lo, &hi);
         }
         const bool has = lo < hi;
         const unsigned m = __ballot_sync(0xffffffffu, has);
@@ -1130,7 +1153,7 @@ __global__ void __launch_bounds__(kCmbThreads) combine_kernel(const CombineParam
     }
     if (lane == 0) {
       pcnt[warp] = cnt;
-      inv_l[warp] = (cbad[row] || N <= 0) ? __int_as_float(0x7fc00000) : 1.f;
+      inv_l[warp] = (cbad[row] || N <= 0 || state == kNodeBad) ? __int_as_float(0x7fc00000) : 1.f;
     }
   }
   __syncthreads();  // every warp reads the lists below
@@ -1176,7 +1199,9 @@ __global__ void __launch_bounds__(kCmbThreads) combine_kernel(const CombineParam
         L = fmaf(wg, pw[warp * kMaxPieces + i], L);
       }
       L = warp_sum(L);
-      for (int i = lane; i < cnt; i += 32) pm[warp * kMaxPieces + i] /= L;
+      // an absent tree node has no visible key: L is 0 and its output zero
+      const bool none = p.parent && L == 0.f;
+      for (int i = lane; i < cnt; i += 32) pm[warp * kMaxPieces + i] = none ? 0.f : pm[warp * kMaxPieces + i] / L;
     }
     __syncthreads();
     // (b) clat[w][l] = sum_i weight_i * O_i[h][l] for every row at once:
@@ -1295,7 +1320,9 @@ __global__ void __launch_bounds__(kCmbThreads) combine_kernel(const CombineParam
         d[0] += __shfl_xor_sync(0xffffffffu, d[0], 1);
         if ((lane & 3) == 0) {
           const int jj = 4 * ((lane >> 4) & 1) + 2 * ((lane >> 3) & 1) + ((lane >> 2) & 1);
-          p.out[((size_t)(r0 + w) * kH + h) * p.Dv + j0 + jw + jj] = d[0] * inv_l[w];
+          const size_t at = ((size_t)(r0 + w) * kH + h) * p.Dv + j0 + jw + jj;
+          if (p.out_bf16) static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(d[0] * inv_l[w]);
+          else static_cast<float*>(p.out)[at] = d[0] * inv_l[w];
         }
       }
     }
@@ -1321,6 +1348,7 @@ struct MergeParams {
   __nv_bfloat16* clat;  // [R, 64, 512]
   float* inv_l;         // [R, 64]
   int B, S, G, sparse;
+  const int32_t* parent;  // tree attention: [B, S] parent indices, else null
 };
 
 constexpr int kMergeBatch = 2;  // splits whose partials are loaded together
@@ -1337,10 +1365,12 @@ __global__ void __launch_bounds__(256, 3) merge_kernel(const MergeParams p) {
   const int NR = p.sparse ? R : p.B;
   const long long N = p.tile_start[NR];
   __nv_bfloat16* dst = p.clat + ((size_t)r * kH + h) * kDl + 16 * lane;
-  if (p.bad[row] || N <= 0) {
+  const int state = p.parent ? tree_node(p.parent + (size_t)b * p.S, s).state : kNodePresent;
+  if (p.bad[row] || N <= 0 || state != kNodePresent) {
     *reinterpret_cast<uint4*>(dst) = make_uint4(0, 0, 0, 0);
     *reinterpret_cast<uint4*>(dst + 8) = make_uint4(0, 0, 0, 0);
-    if (lane == 0) p.inv_l[(size_t)r * kH + h] = qnan();
+    // an absent node's output is zero
+    if (lane == 0) p.inv_l[(size_t)r * kH + h] = (p.bad[row] || N <= 0 || state == kNodeBad) ? qnan() : 1.f;
     return;
   }
   const long long a = p.tile_start[row], e = p.tile_start[row + 1];
@@ -1352,7 +1382,7 @@ __global__ void __launch_bounds__(256, 3) merge_kernel(const MergeParams p) {
   auto slot_of = [&](int gg) -> int {  // the split of chunk gg, or -1 when the chunk has no tile of this row
     int lo, hi;
     if (p.sparse) piece_range<true>(p.tile_start, p.T, p.S, s, row, gg, p.G, N, &lo, &hi);
-    else piece_range<false>(p.tile_start, p.T, p.S, s, row, gg, p.G, N, &lo, &hi);
+    else piece_range<false>(p.tile_start, p.T, p.S, p.parent ? p.S - 1 : s, row, gg, p.G, N, &lo, &hi);
     if (lo >= hi) return -1;
     return p.sparse ? gg + row : (gg + row) * p.S + s;
   };
@@ -1549,7 +1579,7 @@ cudaError_t set_smem_once(Kern kern, int bytes, std::atomic<unsigned long long>*
   return e;
 }
 
-std::atomic<unsigned long long> g_abs_attr[9] = {}, g_attn_attr[10] = {}, g_cmb_attr{0};
+std::atomic<unsigned long long> g_abs_attr[9] = {}, g_attn_attr[14] = {}, g_cmb_attr{0};
 
 Plan make_plan(int B, int S, int T_cap, int sparse_topk) {
   Plan pl{};
@@ -1672,6 +1702,7 @@ cudaError_t run(const DecodeArgs& a, void* ws, bool sparse, cudaStream_t st) {
   ap.pages = sparse ? PageTable{} : a.pages;
   for (int j = 0; j < kDr / 2; ++j) ap.turn[j] = rope_turns(std::pow(g.rope_base, -2.0 * j / kDr));
   ap.flags = a.flags;
+  ap.parent = a.parent;
   const size_t abs_smem = (size_t)kAbsRows * g.Dn * 4 + (size_t)kAbsGroups * kAbsRows * kAbsCols * 4;
   // one instantiation per case, so that each carries only its own code
   using AbsKern = void (*)(const AbsorbParams);
@@ -1775,17 +1806,22 @@ cudaError_t run(const DecodeArgs& a, void* ws, bool sparse, cudaStream_t st) {
   tp.flags = a.flags;
   tp.wait_ns = a.wait_limit_ns;
   tp.pages = sparse ? PageTable{} : a.pages;
+  tp.parent = a.parent;
   // Streaming launches (one CTA per piece, at least two tiles a CTA by the
   // T_cap bound) take the instantiation with the single-lane score loop.
   const long long tiles_cap = (long long)B * ((a.T_cap + kTile - 1) / kTile);
   const bool stream = !sparse && tp.qsplit == 1 && tiles_cap >= 2LL * pl.G;
   auto kern = sparse     ? attn_kernel<true>
+              : a.parent ? (paged ? (stream ? attn_kernel<false, true, true, true> : attn_kernel<false, true, false, true>)
+                                  : (stream ? attn_kernel<false, false, true, true>
+                                            : attn_kernel<false, false, false, true>))
               : a.lat_fp8 ? (big ? (stream ? attn8_kernel<false, true> : attn8_kernel<false>)
                                  : (stream ? attn8_kernel<true, true> : attn8_kernel<true>))
               : paged     ? (stream ? attn_kernel<false, true, true> : attn_kernel<false, true>)
                           : (stream ? attn_kernel<false, false, true> : attn_kernel<false>);
   const uint32_t attn_smem = a.lat_fp8 ? kAttn8DynSmem : kAttnDynSmem;
-  const int attr_slot = (sparse ? 1 : a.lat_fp8 ? (big ? 2 : 4) : paged ? 3 : 0) + (stream ? 5 : 0);
+  const int attr_slot = a.parent ? 10 + (paged ? 1 : 0) + (stream ? 2 : 0)
+                                 : (sparse ? 1 : a.lat_fp8 ? (big ? 2 : 4) : paged ? 3 : 0) + (stream ? 5 : 0);
   e = set_smem_once(kern, (int)attn_smem, &g_attn_attr[attr_slot]);
   if (e != cudaSuccess) return e;
   const int nblk = pieces * tp.qsplit;
@@ -1807,6 +1843,7 @@ cudaError_t run(const DecodeArgs& a, void* ws, bool sparse, cudaStream_t st) {
     mp.S = S;
     mp.G = pl.G;
     mp.sparse = sparse ? 1 : 0;
+    mp.parent = a.parent;
     kernel_mark(st, "merge");
     e = launch_pdl(merge_kernel, dim3((pl.R * kH + 7) / 8), dim3(256), 0, st, mp);
     if (e != cudaSuccess) return e;
@@ -1825,7 +1862,7 @@ cudaError_t run(const DecodeArgs& a, void* ws, bool sparse, cudaStream_t st) {
     gu.c_base = a.out;
     gu.c_ld_m = (long long)kH * g.Dv;
     gu.c_ld_z = g.Dv;
-    gu.out_kind = kGemmOutF32Scaled;
+    gu.out_kind = a.out_bf16 ? kGemmOutBf16Scaled : kGemmOutF32Scaled;
     gu.scale = mp.inv_l;
     gu.M = pl.R;
     gu.N = g.Dv;
@@ -1851,6 +1888,8 @@ cudaError_t run(const DecodeArgs& a, void* ws, bool sparse, cudaStream_t st) {
   cp.Dn = g.Dn;
   cp.Dv = g.Dv;
   cp.sparse = sparse ? 1 : 0;
+  cp.parent = a.parent;
+  cp.out_bf16 = a.out_bf16;
   cp.flags = a.flags;
   const size_t cmb_smem = (size_t)kCmbWBytes + (size_t)kCmbRows * kCPitch * 4 + kCmbRows * 8 +
                           (size_t)kCmbRows * kMaxPieces * 12 + (size_t)(kCmbThreads / 32) * 128 * 16;

@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(kGThreads, 1) gemm_kernel(const __grid_constan
       if (bar_red_or(1, 128, fail)) break;
       tc_fence_after();
       float scale = 1.f;
-      if (p.out_kind == kGemmOutF32Scaled && m < p.M) scale = p.scale[(size_t)m * p.Z + z];
+      if ((p.out_kind == kGemmOutF32Scaled || p.out_kind == kGemmOutBf16Scaled) && m < p.M) scale = p.scale[(size_t)m * p.Z + z];
 #pragma unroll 1
       for (int c0 = 0; c0 < BN; c0 += 64) {
         float v[64];
@@ -214,15 +214,15 @@ __global__ void __launch_bounds__(kGThreads, 1) gemm_kernel(const __grid_constan
         tmem_wait_ld();
         const int n = n0 + c0;
         if (m < p.M && n < p.N) {
-          if (p.out_kind == kGemmOutBf16) {
+          if (p.out_kind == kGemmOutBf16 || p.out_kind == kGemmOutBf16Scaled) {
             __nv_bfloat16* c = static_cast<__nv_bfloat16*>(p.c_base) + (size_t)m * p.c_ld_m + (size_t)z * p.c_ld_z + n;
 #pragma unroll
             for (int j = 0; j < 64; j += 8) {
               uint4 q;
-              q.x = pack2(v[j], v[j + 1]);
-              q.y = pack2(v[j + 2], v[j + 3]);
-              q.z = pack2(v[j + 4], v[j + 5]);
-              q.w = pack2(v[j + 6], v[j + 7]);
+              q.x = pack2(v[j] * scale, v[j + 1] * scale);
+              q.y = pack2(v[j + 2] * scale, v[j + 3] * scale);
+              q.z = pack2(v[j + 4] * scale, v[j + 5] * scale);
+              q.w = pack2(v[j + 6] * scale, v[j + 7] * scale);
               *reinterpret_cast<uint4*>(c + j) = q;
             }
           } else {

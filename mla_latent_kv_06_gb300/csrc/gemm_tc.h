@@ -16,7 +16,8 @@ namespace mla {
 enum GemmOut {
   kGemmOutBf16 = 0,        // C (bf16)  = acc
   kGemmOutF32Scaled = 1,   // C (fp32)  = acc * scale[m * Z + z]
-  kGemmOutF32 = 2          // C (fp32)  = acc
+  kGemmOutF32 = 2,         // C (fp32)  = acc
+  kGemmOutBf16Scaled = 3   // C (bf16)  = acc * scale[m * Z + z]
 };
 
 struct GemmArgs {
@@ -33,7 +34,7 @@ struct GemmArgs {
   void* c_base;
   long long c_ld_m, c_ld_z;
   int out_kind;        // GemmOut
-  const float* scale;  // kGemmOutF32Scaled: [M * Z]
+  const float* scale;  // kGemmOutF32Scaled, kGemmOutBf16Scaled: [M * Z]
   int M, N, K, Z;      // K % 64 == 0, N % 64 == 0
   unsigned int* flags;
   long long wait_ns;

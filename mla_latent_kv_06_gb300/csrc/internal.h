@@ -43,7 +43,7 @@ struct DecodeArgs {
   const void* Rc;
   const int32_t* T;
   const void* kv_b;
-  float* out;
+  void* out;            // float, or bf16 where out_bf16
   const int32_t* sel;   // sparse only: [B,S,topk]
   const int32_t* nsel;  // sparse only: [B,S]
   int topk;
@@ -57,6 +57,9 @@ struct DecodeArgs {
   // previous kernel (true only when that buffer was last read two layers back)
   int stage_parity;
   int gather_pdl;
+  // Tree attention (dense only): parents of the S drafted nodes [B, S], else null
+  const int32_t* parent;
+  int out_bf16;
 };
 
 cudaError_t launch_decode_simt(const DecodeArgs& a, int dtype, bool sparse, cudaStream_t st);
@@ -138,6 +141,7 @@ struct AppendArgs {
   void* Rc;  // [B, T_cap, qk_rope] or the page pool
   unsigned int* flags;
   PageTable pages;
+  const int32_t* parent;  // [B, S] parents of a drafted tree, else null
   uint64_t turn[kMaxRopePairs];  // rope_turns(rope_base^(-2j/qk_rope))
   int lat_fp8;          // Lc receives E4M3 codes of the normalised row * lat_inv_scale
   float lat_inv_scale;
@@ -156,6 +160,40 @@ struct KeyAppendArgs {
   uint64_t turn[kMaxRopePairs];  // rope_turns(rope_base^(-2j/rope_dim))
 };
 cudaError_t launch_index_key_append(const KeyAppendArgs& a, cudaStream_t st);
+
+// Largest drafted tree: its ancestor masks are 64-bit words.
+constexpr int kMaxTree = 64;
+
+struct VerifyArgs {
+  int B, S, V;
+  const float* p;  // row r of sequence b at p + b * p_batch + r * p_row, r = 0 .. S
+  const float* q;  // likewise, or null: point drafts
+  long long p_row, p_batch, q_row, q_batch;
+  const int32_t* tokens;  // [B, S]
+  const int32_t* parent;  // [B, S]
+  const float* u;         // [B, S + 1]
+  int32_t* path;          // [B, S]
+  int32_t* n_acc;         // [B]
+  int32_t* token;         // [B]
+  unsigned int* flags;
+};
+cudaError_t launch_tree_verify(const VerifyArgs& a, cudaStream_t st);
+
+// Caches of one commit launch: pointers travel in the launch parameters.
+constexpr int kCommitCaches = 128;
+
+struct CommitArgs {
+  int n, B, S, T_cap;
+  const int32_t* T;
+  const int32_t* path;   // [B, S]
+  const int32_t* n_acc;  // [B]
+  int32_t* T_out;        // [B], or null: a later launch of the same call
+  unsigned int* flags;
+  PageTable pages;
+  void* cache[kCommitCaches];
+  int row_bytes[kCommitCaches];
+};
+cudaError_t launch_tree_commit(const CommitArgs& a, cudaStream_t st);
 
 // Sets the thread-local message returned by mla_last_error().
 void set_last_error(const char* msg);
