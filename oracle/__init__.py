@@ -47,6 +47,10 @@ Parity status of each function (what pins it, see tests/test_oracle_pins.py):
                           ties-to-even and saturation by hand; encode(decode(c)) = c.
 * dequant_latent,       - composed of the pinned e4m3 functions and cache_append;
   cache_append_fp8        codes within half a quantum of the normalised row.
+
+Drafted trees (tree.py, see tests/test_tree_oracle.py): a chain equals the
+causal decode and append; hand-worked trees, acceptances and moves; the emitted
+token's distribution, integrated exactly over u, is the target's.
 """
 from .mla import (  # noqa: F401
     e4m3_decode,
@@ -73,4 +77,11 @@ from .mla import (  # noqa: F401
     topk_select,
     sparse_decode,
     query_positions,
+)
+from .tree import (  # noqa: F401
+    ancestors,
+    cache_append_tree,
+    decode_tree,
+    tree_commit,
+    tree_verify,
 )
