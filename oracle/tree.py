@@ -11,7 +11,7 @@ from fractions import Fraction
 
 import numpy as np
 
-from .mla import attend_dense, rms_norm, rope_interleave
+from .mla import attend_absorbed, rms_norm, rope_interleave
 
 
 def ancestors(parent, s: int):
@@ -41,7 +41,8 @@ def decode_tree(q, Lc, Rc, T, parent, kv_b, qk_nope, scale, rope_base=10000.0, r
             if up is None or (rows is not None and (b, s) not in rows):
                 continue
             at = list(range(base)) + [base + j for j in sorted(up)]
-            out[b, s] = attend_dense(q[b, s], Lc[b, at], Rc[b, at], kv_b, qk_nope, base + len(up) - 1, scale, rope_base)
+            out[b, s] = attend_absorbed(q[b, s], Lc[b, at], Rc[b, at], kv_b, qk_nope, base + len(up) - 1, scale,
+                                        rope_base)
     return out
 
 
