@@ -83,7 +83,7 @@ struct Shared {
 // Row segment of one warp: elements [lo, hi) of the vocabulary.
 struct Segment {
   const float* p;
-  const float* q;  // null: point drafts
+  const float* q;  // null: point drafts, or no rejection yet
   int lo, hi;
   float ch, cl;
   const int* removed;
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(kThreads) tree_verify_kernel(const VerifyArgs 
   // The warps' and CTAs' totals stay in sh for the draw.
   auto total = [&](int at, double c, int nremoved) -> double {
     seg.p = p0 + (long long)at * a.p_row;
-    seg.q = q0 ? q0 + (long long)at * a.q_row : nullptr;
+    seg.q = q0 && c != 0.0 ? q0 + (long long)at * a.q_row : nullptr;  // W = p before any rejection
     seg.ch = (float)c;
     seg.cl = (float)(c - (double)seg.ch);
     seg.removed = sh.removed;
