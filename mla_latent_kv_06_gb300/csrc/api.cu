@@ -175,7 +175,8 @@ int run_decode(mla::DecodeArgs& a, int dtype, bool sparse, void* workspace, size
   cudaError_t e;
   if (own_call) mla::call_begin();
   if (pages_ok && tc_decode_ok(a.g, dtype, a.q, a.Lc, a.Rc, a.kv_b)) {
-    size_t need = mla::tc_decode_workspace_bytes(a.g, a.B, a.S, sparse ? a.topk : a.T_cap, sparse ? a.topk : 0);
+    size_t need = mla::tc_decode_workspace_bytes(a.g, a.B, a.S, sparse ? a.topk : a.T_cap, sparse ? a.topk : 0,
+                                                 a.parent != nullptr);
     if (need && (!workspace || workspace_bytes < need))
       return fail(MLA_ERR_INVALID, "workspace of %zu bytes < %zu required", workspace_bytes, need);
     if (reinterpret_cast<uintptr_t>(workspace) & 255u)
@@ -913,7 +914,7 @@ MLA_EXPORT size_t mla_decode_tree_workspace_size(const mla_dims* d, int dtype, i
   mla::Geometry g;
   if (!resolve(d, &g) || B < 1 || S < 1 || S > mla::kMaxTree || T_cap < S) return 0;
   if (dtype == MLA_BF16 && mla::tc_decode_geometry_ok(g))
-    return round256(mla::tc_decode_workspace_bytes(g, B, S, T_cap, /*sparse_topk=*/0));
+    return round256(mla::tc_decode_workspace_bytes(g, B, S, T_cap, /*sparse_topk=*/0, /*tree=*/true));
   return 0;
 }
 

@@ -1,0 +1,573 @@
+// attn_tree.cu -- tree attention for many query rows on CTA pairs.
+//
+// Scores qabs . Lc + q_rot . Rc, softmax and latent context sum p Lc of the
+// page "MLA 注意力与 KV 缓存", §2.3, for the nodes of a drafted tree.
+//
+// A key row is 1152 bytes and one node's 64 heads do 64 * 1088 multiply-adds
+// with it, so with several nodes the tensor pipe is the bound, and the work
+// per SM is limited by TMEM: the fp32 latent context of 64 query rows takes
+// 256 of its 512 columns.  One node per SM at M = 64 would run the pipe at half
+// rate and a transposed product (keys as M, heads as N = 64) reads shared
+// memory for every 64 columns.  So two SMs form a pair and run M = 128
+// products of cta_group::2: CTA r holds the query rows, probabilities, scores
+// and context of its own node (tree node 2i + r), and each supplies half of
+// the B operand, which the pair's tensor cores share:
+//   S[64 rows x 256 keys] = Q [K-major] . K^T    (K = 576; CTA r loads keys 128r ..)
+//   O[64 rows x 512]     += P [K-major] . V      (two N = 256 blocks; CTA r loads
+//                                                 latents 256n + 128r .. of all keys)
+// All products have N = 256: measured 64.6 cycles each, the full rate, against
+// 52.8 for N = 128 (62%).  Softmax, running maximum and rescale are local to a
+// CTA: only barriers cross the pair.
+//
+// Operands stream through one ring of 16 KB stages in the order of use, K(0),
+// K(1), V(0), K(2), V(1), ...: the score product of tile j + 1 runs while the
+// softmax works on tile j.  TMEM: two S buffers of 128 columns, O of 256.  A
+// row of S sits in two lanes (l: keys 0-127, 64 + l: keys 128-255), a row of O
+// likewise (halves of each 256-column block).
+//
+// Masks cost the main loop nothing.  Prefix keys come from the cache in whole
+// 16-key steps and are visible to every node.  The up to 15 prefix rows past
+// the last step and the tree's rows form one tail tile, copied beforehand into
+// a staging buffer (stage_tail): a row with a value that is not finite is staged as zero
+// latents with a NaN rotary part, so that it turns the nodes that see it into
+// NaN through their scores and the others, whose probability is zero, stay
+// untouched although the pair shares the value operand.
+#include "attn_tree.h"
+
+#include <atomic>
+
+#include "common.cuh"
+#include "sm100.cuh"
+#include "tree.cuh"
+
+namespace mla {
+namespace {
+
+using namespace sm100;
+
+constexpr int kThreads = 320;  // warp 0: TMA, warp 1: MMA (leader CTA), warps 2-9: softmax
+constexpr int kSoft = 256, kSoftWarps = 8;
+constexpr int kRows = 64, kDl = 512, kDc = 576;
+constexpr int kStages = 7;
+constexpr uint32_t kStageBytes = 16384, kQAtom = 8192;
+constexpr uint32_t kQBytes = 9 * kQAtom, kPBytes = 4 * 8192;
+constexpr uint32_t kRingOff = kQBytes + kPBytes;
+constexpr uint32_t kSmem = kRingOff + kStages * kStageBytes + 1024;
+constexpr uint32_t kColS = 0, kColO = 256, kCols = 512;
+constexpr float kTau = 8.f;  // lazy rescale threshold (log2 units)
+constexpr long long kDrainNs = 1000000000LL;
+
+struct Shared {
+  uint64_t full[kStages], empty[kStages];  // full: the leader's, for both CTAs' bytes
+  uint64_t q_full, q_empty, s_full[2], p_full, pv_done, mma_done;
+  uint32_t tmem;
+  int abort;
+  int issued[2], q_issued[2];  // stages and query blocks each CTA has issued (leader's copy, at the end)
+  float red[4][kRows];
+  float m[kRows], alpha[kRows];
+};
+
+__device__ __forceinline__ uint32_t cta_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Shared-cluster address of `p`'s counterpart in CTA `rank`.
+__device__ __forceinline__ uint32_t in_cta(const void* p, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  return a;
+}
+
+// One arrival per warp on the leader's barrier.
+__device__ __forceinline__ void arrive_leader(uint32_t bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0)
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// Tile load into this CTA's shared memory, completing on a barrier of either CTA of the pair.
+__device__ __forceinline__ void load_2d(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
+      "[%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Arrive on both CTAs' `bar` once the MMAs issued so far have retired.
+__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+
+// The pieces (sequence, tile range) of one chunk of the tile list.
+struct Pieces {
+  const int32_t* ts;
+  int B, b, lo, hi;
+  long long c0, c1;
+  __device__ __forceinline__ void start(const PairParams& p, int g) {
+    ts = p.tile_start;
+    B = p.B;
+    const long long N = ts[B];
+    c0 = N * g / p.G;
+    c1 = N * (g + 1) / p.G;
+    int l = 0, h = B;  // first sequence whose tiles reach past c0
+    while (l < h) {
+      const int mid = (l + h) >> 1;
+      if (ts[mid + 1] > c0) h = mid;
+      else l = mid + 1;
+    }
+    b = l - 1;
+  }
+  __device__ __forceinline__ bool next() {
+    for (++b; b < B; ++b) {
+      const long long a = ts[b], e = ts[b + 1];
+      if (a >= c1) return false;
+      lo = (int)((a > c0 ? a : c0) - a);
+      hi = (int)((e < c1 ? e : c1) - a);
+      if (lo < hi) return true;
+    }
+    return false;
+  }
+};
+
+struct Tile {
+  bool tail;
+  int row0, keys;  // prefix: first key and number of keys (a multiple of 16); tail: staged rows
+};
+
+__device__ __forceinline__ Tile tile_at(int Tb, int S, int k) {
+  const int b16 = pair_base16(Tb, S);
+  Tile t;
+  t.row0 = k * kPairTile;
+  t.tail = t.row0 >= b16;
+  t.keys = t.tail ? Tb - b16 : min(kPairTile, b16 - t.row0);
+  return t;
+}
+
+// ------------------------------------------------------------ TMA producer (one thread of each CTA)
+__device__ __forceinline__ void produce(const PairParams& p, Shared& sh, unsigned char* smem, uint32_t rank, int g, int pair,
+                                        int* issued, int* q_issued) {
+  volatile int* abort = &sh.abort;
+  int n = 0;
+  bool ok = true;
+  // next ring stage: its address, or null when the wait for it gave up
+  auto stage = [&](uint32_t* bar) -> unsigned char* {
+    const int s = n % kStages, u = n / kStages;
+    if (!mbar_wait(&sh.empty[s], (u & 1) ^ 1, abort, p.flags, p.wait_ns)) {
+      ok = false;
+      return nullptr;
+    }
+    if (rank == 0) mbar_arrive_expect_tx(&sh.full[s], 2 * kStageBytes);
+    *bar = in_cta(&sh.full[s], 0);
+    ++n;
+    return smem + kRingOff + s * kStageBytes;
+  };
+  auto row_of = [&](int b, int t) -> int {
+    bool bad = false;
+    const int row = (int)cache_row(p.pages, b, p.T_cap, t, &bad);
+    if (bad) raise_flag(p.flags, MLA_DEV_BAD_INDEX);
+    return row;
+  };
+  auto load_k = [&](int b, int Tb, int k) {
+    const Tile t = tile_at(Tb, p.S, k);
+    int y = b * kPairStage;
+    if (!t.tail) {
+      int t0 = t.row0 + 128 * (int)rank;
+      if (t0 >= Tb) t0 = t.row0;  // no key of this half: any rows do
+      y = row_of(b, t0);
+    }
+    for (int d = 0; d < 9 && ok; ++d) {
+      uint32_t bar;
+      unsigned char* dst = stage(&bar);
+      if (!dst) break;
+      if (t.tail) load_2d(dst, &p.mT, 64 * d, y, bar);
+      else if (d < 8) load_2d(dst, &p.mK, 64 * d, y, bar);
+      else load_2d(dst, &p.mKr, 0, y, bar);
+    }
+  };
+  auto load_v = [&](int b, int Tb, int k) {
+    const Tile t = tile_at(Tb, p.S, k);
+    for (int kc = 0; kc < (t.keys + 63) / 64 && ok; ++kc) {
+      const int y = t.tail ? b * kPairStage + 64 * kc : row_of(b, t.row0 + 64 * kc);
+      const CUtensorMap* map = t.tail ? &p.mTv : &p.mV;
+      for (int nb = 0; nb < 2 && ok; ++nb) {
+        uint32_t bar;
+        unsigned char* dst = stage(&bar);
+        if (!dst) break;
+        const int x = 256 * nb + 128 * (int)rank;
+        load_2d(dst, map, x, y, bar);
+        load_2d(dst + 8192, map, x + 64, y, bar);
+      }
+    }
+  };
+  Pieces pc;
+  int np = 0;
+  for (pc.start(p, g); ok && pc.next(); ++np) {
+    const int Tb = p.T[pc.b];
+    ok = mbar_wait(&sh.q_empty, (np & 1) ^ 1, abort, p.flags, p.wait_ns);
+    if (!ok) break;
+    if (rank == 0) mbar_arrive_expect_tx(&sh.q_full, 2 * kQBytes);
+    const uint32_t qbar = in_cta(&sh.q_full, 0);
+    const int qrow = (pc.b * p.S + 2 * pair + (int)rank) * kRows;  // past the last node: another row or zeros
+    for (int d = 0; d < 9; ++d) load_2d(smem + d * kQAtom, &p.mQ, 64 * d, qrow, qbar);
+    ++*q_issued;
+    load_k(pc.b, Tb, pc.lo);
+    for (int k = pc.lo; k < pc.hi && ok; ++k) {
+      if (k + 1 < pc.hi) load_k(pc.b, Tb, k + 1);
+      if (ok) load_v(pc.b, Tb, k);
+    }
+  }
+  *issued = n;
+}
+
+// ------------------------------------------------------------ MMA issuer (one thread of the leader CTA)
+__device__ __forceinline__ void issue(const PairParams& p, Shared& sh, unsigned char* smem, uint32_t tmem, int g) {
+  volatile int* abort = &sh.abort;
+  const uint32_t idS = idesc_bf16_f32(128, 256, 0, 0), idO = idesc_bf16_f32(128, 256, 0, 1);
+  const uint64_t dQ = smem_desc_sw128(smem_u32(smem), 16, 1024);
+  const uint64_t dP = smem_desc_sw128(smem_u32(smem + kQBytes), 16, 1024);
+  const uint64_t dK = smem_desc_sw128(smem_u32(smem + kRingOff), 16, 1024);
+  const uint64_t dV = smem_desc_sw128(smem_u32(smem + kRingOff), 8192, 1024);
+  int n = 0, it = 0;
+  bool ok = true;
+  auto scores = [&](int j) {  // S of tile number j
+    const uint32_t d = tmem + kColS + 128 * (j & 1);
+    for (int a = 0; a < 9; ++a, ++n) {
+      const int s = n % kStages;
+      if (!mbar_wait(&sh.full[s], (n / kStages) & 1, abort, p.flags, p.wait_ns)) {
+        ok = false;
+        return;
+      }
+      tc_fence_after();
+      const uint64_t db = dK + (uint64_t)(s * (kStageBytes >> 4)), da = dQ + (uint64_t)(a * (kQAtom >> 4));
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) mma_pair(d, da + 2 * kk, db + 2 * kk, idS, (a | kk) != 0 ? 1u : 0u);
+      commit_pair(&sh.empty[s]);
+    }
+    commit_pair(&sh.s_full[j & 1]);
+  };
+  Pieces pc;
+  int np = 0;
+  for (pc.start(p, g); ok && pc.next(); ++np) {
+    const int Tb = p.T[pc.b];
+    ok = mbar_wait(&sh.q_full, np & 1, abort, p.flags, p.wait_ns);
+    if (!ok) break;
+    tc_fence_after();
+    scores(it);
+    if (ok && pc.lo + 1 == pc.hi) commit_pair(&sh.q_empty);
+    for (int k = pc.lo; k < pc.hi && ok; ++k, ++it) {
+      if (k + 1 < pc.hi) {
+        scores(it + 1);
+        if (ok && k + 2 == pc.hi) commit_pair(&sh.q_empty);  // the piece's last score product
+      }
+      ok = ok && mbar_wait(&sh.p_full, it & 1, abort, p.flags, p.wait_ns);
+      if (!ok) break;
+      tc_fence_after();
+      const Tile t = tile_at(Tb, p.S, k);
+      for (int kc = 0; kc < (t.keys + 63) / 64 && ok; ++kc) {
+        const int steps = min(4, (t.keys - 64 * kc + 15) / 16);
+        for (int nb = 0; nb < 2; ++nb, ++n) {
+          const int s = n % kStages;
+          if (!mbar_wait(&sh.full[s], (n / kStages) & 1, abort, p.flags, p.wait_ns)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t db = dV + (uint64_t)(s * (kStageBytes >> 4)), da = dP + (uint64_t)(kc * (8192 >> 4));
+          const uint32_t d = tmem + kColO + 128 * nb;
+          const uint32_t keep = (k > pc.lo || kc > 0) ? 1u : 0u;
+          if (steps == 4) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) mma_pair(d, da + 2 * kk, db + 128 * kk, idO, kk > 0 ? 1u : keep);
+          } else {
+            for (int kk = 0; kk < steps; ++kk) mma_pair(d, da + 2 * kk, db + 128 * kk, idO, kk > 0 ? 1u : keep);
+          }
+          commit_pair(&sh.empty[s]);
+        }
+      }
+      if (ok) commit_pair(&sh.pv_done);
+    }
+  }
+  commit_pair(&sh.mma_done);
+}
+
+// ------------------------------------------------------------ softmax warps
+__device__ __forceinline__ void soften(const PairParams& p, Shared& sh, unsigned char* smem, uint32_t tmem, uint32_t rank,
+                                       int g, int pair) {
+  volatile int* abort = &sh.abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tsm = threadIdx.x - 64;
+  const int q = warp & 3, ch = (warp - 2) >> 2;      // TMEM lane quadrant, half of its columns
+  const int row = 32 * (q & 1) + lane;               // head
+  const int key0 = 128 * (q >> 1) + 64 * ch;         // first key of the thread's 64 within the tile
+  const uint32_t t_lane = tmem + ((uint32_t)(32 * q) << 16);
+  const uint32_t p_bar = in_cta(&sh.p_full, 0);
+  unsigned char* prow = smem + kQBytes + (key0 >> 6) * 8192 + row * 128;
+  const int s = 2 * pair + (int)rank;
+  const float c = p.c;
+  int it = 0;
+  Pieces pc;
+  for (pc.start(p, g); pc.next();) {
+    const int b = pc.b, Tb = p.T[b], b16 = pair_base16(Tb, p.S);
+    unsigned long long mask = 0;
+    if (s < p.S) {
+      const TreeNode node = tree_node(p.parent + (size_t)b * p.S, s);
+      mask = node.mask;
+      if (node.state == kNodeBad && tsm == 0) raise_flag(p.flags, MLA_DEV_BAD_INDEX);
+    }
+    float lsum = 0.f;
+    for (int k = pc.lo; k < pc.hi; ++k, ++it) {
+      const bool first = k == pc.lo;
+      const Tile t = tile_at(Tb, p.S, k);
+      bool fail = !mbar_wait(&sh.s_full[it & 1], (it >> 1) & 1, abort, p.flags, p.wait_ns);
+      if (bar_red_or(1, kSoft, fail)) return;
+      tc_fence_after();
+      float v[64];
+      tmem_ld64(t_lane + kColS + 128 * (it & 1) + 64 * ch, v);
+      tmem_wait_ld();
+      if (t.tail) {  // prefix remainder, then the tree's rows through the node's mask
+        const int rem = Tb - p.S - b16;
+#pragma unroll
+        for (int i = 0; i < 64; ++i) {
+          const int j = key0 + i;
+          const bool see = mask != 0 && j < t.keys && (j < rem || ((mask >> (j - rem)) & 1ull));
+          if (!see) v[i] = -INFINITY;
+          else if (fabsf(v[i]) == INFINITY) v[i] = __int_as_float(0x7fc00000);
+        }
+      } else if (t.keys < kPairTile || mask == 0) {
+#pragma unroll
+        for (int i = 0; i < 64; ++i)
+          if (key0 + i >= t.keys || mask == 0) v[i] = -INFINITY;
+      }
+      // running maximum, moved only when a score exceeds it by more than kTau
+      bool slow = first;
+      float mrow = 0.f;
+      if (!first) {
+        mrow = sh.m[row];
+        float mx = v[0];
+#pragma unroll
+        for (int i = 1; i < 64; ++i) mx = fmaxf(mx, v[i]);
+        slow = bar_red_or(2, kSoft, mx * c > mrow + kTau);
+      }
+      bool rescale = false;
+      if (slow) {
+        float mx = v[0];
+#pragma unroll
+        for (int i = 1; i < 64; ++i) mx = fmaxf(mx, v[i]);
+        sh.red[2 * (q >> 1) + ch][row] = mx;
+        named_barrier(1, kSoft);
+        bool need = false;
+        if (tsm < kRows) {
+          const float tmax = fmaxf(fmaxf(sh.red[0][tsm], sh.red[1][tsm]), fmaxf(sh.red[2][tsm], sh.red[3][tsm])) * c;
+          const float mo = first ? -1e30f : sh.m[tsm];
+          float mn = mo, al = 1.f;
+          if (tmax > mo + kTau) {
+            mn = tmax;
+            al = exp2f(mo - mn);
+          }
+          sh.m[tsm] = mn;
+          sh.alpha[tsm] = al;
+          need = !first && al != 1.f;
+        }
+        rescale = bar_red_or(2, kSoft, need);
+        mrow = sh.m[row];
+      }
+      // probabilities: bf16 is the value product's operand; the row sum adds the rounded values
+      uint32_t pk[32];
+      float add0 = 0.f, add1 = 0.f;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        pk[i] = pack2(exp2f(fmaf(v[2 * i], c, -mrow)), exp2f(fmaf(v[2 * i + 1], c, -mrow)));
+        const float2 f = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&pk[i]));
+        add0 += f.x;
+        add1 += f.y;
+      }
+      if (rescale) lsum *= sh.alpha[row];
+      lsum += add0 + add1;
+      if (it > 0) {  // the previous value product has read P and written O
+        fail = !mbar_wait(&sh.pv_done, (it - 1) & 1, abort, p.flags, p.wait_ns);
+        if (bar_red_or(1, kSoft, fail)) return;
+        tc_fence_after();
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        *reinterpret_cast<uint4*>(prow + ((i ^ (row & 7)) << 4)) = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+      if (rescale) {
+        const float al = sh.alpha[row];
+#pragma unroll 1
+        for (int c0 = 0; c0 < 128; c0 += 32) {
+          float w[32];
+          tmem_ld32(t_lane + kColO + 128 * ch + c0, w);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) w[i] *= al;
+          tmem_st32(t_lane + kColO + 128 * ch + c0, w);
+        }
+        tmem_wait_st();
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      arrive_leader(p_bar);
+    }
+    // the piece's partial: O, running maximum and row sum
+    const bool fail = !mbar_wait(&sh.pv_done, (it - 1) & 1, abort, p.flags, p.wait_ns);
+    if (bar_red_or(1, kSoft, fail)) return;
+    tc_fence_after();
+    sh.red[2 * (q >> 1) + ch][row] = lsum;
+    named_barrier(1, kSoft);
+    const size_t slot = (size_t)(g + b) * p.S + s;
+    if (s < p.S) {
+      if (tsm < kRows) {
+        float* ml = p.ml_part + (slot * kRows + tsm) * 2;
+        ml[0] = sh.m[tsm];
+        ml[1] = sh.red[0][tsm] + sh.red[1][tsm] + sh.red[2][tsm] + sh.red[3][tsm];
+      }
+      float* op = p.o_part + (slot * kRows + row) * kDl + 256 * ch + 128 * (q >> 1);
+#pragma unroll 1
+      for (int c0 = 0; c0 < 128; c0 += 32) {
+        float w[32];
+        tmem_ld32(t_lane + kColO + 128 * ch + c0, w);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) *reinterpret_cast<float4*>(op + c0 + i) = make_float4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+      }
+    }
+    tc_fence_before();
+    named_barrier(1, kSoft);  // sh.red and sh.m are reused
+  }
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_pair_kernel(const __grid_constant__ PairParams p) {
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                         ~static_cast<uintptr_t>(1023));
+  __shared__ Shared sh;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cta_rank();
+  const int cluster = blockIdx.x >> 1, pair = cluster % p.NP, g = cluster / p.NP;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.empty[i], 1);
+    }
+    mbar_init(&sh.q_full, 1);
+    mbar_init(&sh.q_empty, 1);
+    mbar_init(&sh.s_full[0], 1);
+    mbar_init(&sh.s_full[1], 1);
+    mbar_init(&sh.p_full, 2 * kSoftWarps);
+    mbar_init(&sh.pv_done, 1);
+    mbar_init(&sh.mma_done, 1);
+    sh.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sh.tmem)), "r"(kCols)
+                 : "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  grid_dep_wait();  // queries, tile list and staged rows come from the previous kernels
+  grid_dep_launch();
+
+  int issued = 0, q_issued = 0;
+  if (warp == 0) {
+    if (lane == 0) produce(p, sh, smem, rank, g, pair, &issued, &q_issued);
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      if (rank == 0) issue(p, sh, smem, tmem, g);
+      // both CTAs: every MMA and every arrival of its commits has happened
+      volatile int no_abort = 0;
+      mbar_wait(&sh.mma_done, 0, &no_abort, p.flags, p.wait_ns > kDrainNs ? p.wait_ns : kDrainNs);
+    }
+    __syncwarp();
+  } else {
+    soften(p, sh, smem, tmem, rank, g, pair);
+    __syncwarp();
+  }
+  // Never leave with copies in flight.  A stage's barrier expects the leader's
+  // arrival and both CTAs' bytes; after an abort one of the two may have
+  // issued a stage that the other has not, and the leader makes up for the
+  // missing part before it waits.
+  if (threadIdx.x == 0) {
+    const uint32_t a = in_cta(&sh.issued[rank], 0), qa = in_cta(&sh.q_issued[rank], 0);
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(issued) : "memory");
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(qa), "r"(q_issued) : "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  if (rank == 0 && threadIdx.x == 0) {
+    volatile int no_abort = 0;
+    const long long drain = p.wait_ns > kDrainNs ? p.wait_ns : kDrainNs;
+    auto settle = [&](uint64_t* bar, int i, int own, int peer, uint32_t bytes) {
+      if (i >= own) mbar_arrive_expect_tx(bar, bytes);  // only the peer's bytes come
+      else if (i >= peer)                               // only this CTA's do
+        asm volatile("mbarrier.complete_tx.relaxed.cluster.shared::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes)
+                     : "memory");
+    };
+    const int own = sh.issued[0], peer = sh.issued[1], top = max(own, peer);
+    for (int i = max(0, top - kStages); i < top; ++i) {
+      settle(&sh.full[i % kStages], i, own, peer, kStageBytes);
+      mbar_wait(&sh.full[i % kStages], (i / kStages) & 1, &no_abort, p.flags, drain);
+    }
+    const int qo = sh.q_issued[0], qp = sh.q_issued[1], qt = max(qo, qp);
+    if (qt > 0) {
+      settle(&sh.q_full, qt - 1, qo, qp, kQBytes);
+      mbar_wait(&sh.q_full, (qt - 1) & 1, &no_abort, p.flags, drain);
+    }
+  }
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  if (warp == 1) {
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kCols) : "memory");
+  }
+}
+
+}  // namespace
+
+int pair_chunks(int B, int S, int T_cap, int sms) {
+  const int np = (S + 1) / 2;
+  const long long tiles = (long long)B * pair_tiles(T_cap, S);
+  long long g = sms / 2 / np;
+  if (g < 1) g = 1;
+  return (int)(g < tiles ? g : tiles);
+}
+
+cudaError_t launch_attn_pair(const PairParams& p, cudaStream_t st) {
+  static std::atomic<unsigned long long> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (!(done.load() & bit)) {
+    e = cudaFuncSetAttribute(attn_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    if (e != cudaSuccess) return e;
+    done.fetch_or(bit);
+  }
+  return launch_pdl(attn_pair_kernel, dim3((unsigned)(2 * p.G * p.NP)), dim3(kThreads), kSmem, st, p);
+}
+
+}  // namespace mla

@@ -34,6 +34,7 @@
 #include <cmath>
 
 #include "attn_core.cuh"
+#include "attn_tree.h"
 #include "decode_tc.h"
 #include "gemm_tc.h"
 #include "sm100.cuh"
@@ -823,6 +824,8 @@ struct AbsorbParams {
   unsigned int* flags;
   PageTable pages;
   const int32_t* parent;  // tree attention: [B, S] parent indices, else null
+  int rope_x;             // blocks along x that form the rotary part (many rows); any more stage the tails
+  __nv_bfloat16* tail;    // pair attention: staged tail rows [B, kPairStage, 576], else null
 };
 
 // Rotary position of query row s of sequence b (length Tb): its row, or the
@@ -888,6 +891,45 @@ __device__ __forceinline__ void rope_rows(const AbsorbParams& p, int h, int tid,
         dst[kDr / 2 + j] = __float2bfloat16_rn(x.y * cs + x.x * sn);
       }
     }
+  }
+}
+
+// Tail rows of the pair attention: rows base16 .. T - 1 of every sequence, zeros
+// after them up to 80.  A row that holds a value that is not finite becomes zero
+// latents with a NaN rotary part (see attn_tree.cu).  One warp per row.
+__device__ __forceinline__ void stage_tail(const AbsorbParams& p, int warp0, int nwarps) {
+  const int lane = threadIdx.x & 31;
+  for (int e = warp0; e < p.B * 80; e += nwarps) {
+    const int b = e / 80, i = e % 80, Tb = p.T[b];
+    if (Tb < p.S || Tb > p.T_cap) continue;
+    const int t = pair_base16(Tb, p.S) + i;
+    uint4 v[3];
+#pragma unroll
+    for (int u = 0; u < 3; ++u) v[u] = make_uint4(0, 0, 0, 0);
+    bool bad = false;
+    const long long row = t < Tb ? cache_row(p.pages, b, p.T_cap, t, &bad) : 0;
+    if (bad && lane == 0) raise_flag(p.flags, MLA_DEV_BAD_INDEX);
+    bool odd = false;
+    if (t < Tb && !bad) {
+      const uint4* L = reinterpret_cast<const uint4*>(p.Lc + (size_t)row * kDl * 2);
+      v[0] = L[lane];
+      v[1] = L[32 + lane];
+      if (lane < 8) v[2] = reinterpret_cast<const uint4*>(p.Rc + (size_t)row * kDr)[lane];
+#pragma unroll
+      for (int u = 0; u < 3; ++u) {
+        const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) odd = odd || (w[k] & 0x7f80u) == 0x7f80u || (w[k] & 0x7f800000u) == 0x7f800000u;
+      }
+    }
+    if (__any_sync(0xffffffffu, odd)) {
+      v[0] = v[1] = make_uint4(0, 0, 0, 0);
+      v[2] = make_uint4(0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u);
+    }
+    uint4* dst = reinterpret_cast<uint4*>(p.tail + ((size_t)b * kPairStage + i) * kDc);
+    dst[lane] = v[0];
+    dst[32 + lane] = v[1];
+    if (lane < 8) dst[64 + lane] = v[2];
   }
 }
 
@@ -1004,7 +1046,7 @@ __global__ void __launch_bounds__(kAbsThreads, 2) absorb_kernel(const AbsorbPara
         }
         if (bad) raise_flag(p.flags, bad);
         p.bad[r] = bad;
-        tiles = bad ? 0 : (nk + kTile - 1) / kTile;
+        tiles = bad ? 0 : p.tail ? pair_tiles(nk, p.S) : (nk + kTile - 1) / kTile;
       }
       // block inclusive scan of `tiles`
       int x = tiles;
@@ -1028,7 +1070,10 @@ __global__ void __launch_bounds__(kAbsThreads, 2) absorb_kernel(const AbsorbPara
   }
 
   if constexpr (!kQabs) {  // rotary part only, every (row, pair) in parallel over the head's CTAs
-    rope_rows(p, h, cb * kAbsThreads + tid, gridDim.x * kAbsThreads);
+    if (cb < p.rope_x) rope_rows(p, h, cb * kAbsThreads + tid, p.rope_x * kAbsThreads);
+    else
+      stage_tail(p, (((cb - p.rope_x) * gridDim.y + h) * kAbsThreads + tid) >> 5,
+                 (gridDim.x - p.rope_x) * gridDim.y * (kAbsThreads / 32));
     return;
   }
   // R <= kAbsRows here (larger batches take the GEMM path)
@@ -1349,10 +1394,15 @@ struct MergeParams {
   float* inv_l;         // [R, 64]
   int B, S, G, sparse;
   const int32_t* parent;  // tree attention: [B, S] parent indices, else null
+  int pair;               // partials of the pair attention: tile_start counts its tiles
 };
 
 constexpr int kMergeBatch = 2;  // splits whose partials are loaded together
 
+// kSplit: clat rows are [R, 64, 1024], the bf16 value and then the bf16 of what
+// its rounding left, for a GEMM with K = 1024 that meets W_UV twice: rounding
+// the context once to bf16 would add 2^-9 to an output that is itself rounded.
+template <bool kSplit>
 __global__ void __launch_bounds__(256, 3) merge_kernel(const MergeParams p) {
   grid_dep_wait();
   grid_dep_launch();
@@ -1364,11 +1414,15 @@ __global__ void __launch_bounds__(256, 3) merge_kernel(const MergeParams p) {
   const int row = p.sparse ? r : b;
   const int NR = p.sparse ? R : p.B;
   const long long N = p.tile_start[NR];
-  __nv_bfloat16* dst = p.clat + ((size_t)r * kH + h) * kDl + 16 * lane;
+  __nv_bfloat16* dst = p.clat + ((size_t)r * kH + h) * (kSplit ? 2 * kDl : kDl) + 16 * lane;
   const int state = p.parent ? tree_node(p.parent + (size_t)b * p.S, s).state : kNodePresent;
   if (p.bad[row] || N <= 0 || state != kNodePresent) {
     *reinterpret_cast<uint4*>(dst) = make_uint4(0, 0, 0, 0);
     *reinterpret_cast<uint4*>(dst + 8) = make_uint4(0, 0, 0, 0);
+    if (kSplit) {
+      *reinterpret_cast<uint4*>(dst + kDl) = make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4*>(dst + kDl + 8) = make_uint4(0, 0, 0, 0);
+    }
     // an absent node's output is zero
     if (lane == 0) p.inv_l[(size_t)r * kH + h] = (p.bad[row] || N <= 0 || state == kNodeBad) ? qnan() : 1.f;
     return;
@@ -1381,7 +1435,7 @@ __global__ void __launch_bounds__(256, 3) merge_kernel(const MergeParams p) {
   float L = 0.f;
   auto slot_of = [&](int gg) -> int {  // the split of chunk gg, or -1 when the chunk has no tile of this row
     int lo, hi;
-    if (p.sparse) piece_range<true>(p.tile_start, p.T, p.S, s, row, gg, p.G, N, &lo, &hi);
+    if (p.sparse || p.pair) piece_range<true>(p.tile_start, p.T, p.S, s, row, gg, p.G, N, &lo, &hi);
     else piece_range<false>(p.tile_start, p.T, p.S, p.parent ? p.S - 1 : s, row, gg, p.G, N, &lo, &hi);
     if (lo >= hi) return -1;
     return p.sparse ? gg + row : (gg + row) * p.S + s;
@@ -1464,6 +1518,17 @@ __global__ void __launch_bounds__(256, 3) merge_kernel(const MergeParams p) {
   w1.w = pack2(acc[14] * il, acc[15] * il);
   *reinterpret_cast<uint4*>(dst) = w0;
   *reinterpret_cast<uint4*>(dst + 8) = w1;
+  if (kSplit) {
+    uint32_t lo[8];
+    const uint32_t hi[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&hi[i]));
+      lo[i] = pack2(acc[2 * i] * il - f.x, acc[2 * i + 1] * il - f.y);
+    }
+    *reinterpret_cast<uint4*>(dst + kDl) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    *reinterpret_cast<uint4*>(dst + kDl + 8) = make_uint4(lo[4], lo[5], lo[6], lo[7]);
+  }
   if (lane == 0) p.inv_l[(size_t)r * kH + h] = (L == L) ? 1.f : qnan();
 }
 
@@ -1550,7 +1615,8 @@ __global__ void __launch_bounds__(256) gather_kernel(const GatherParams p) {
 // ===========================================================================
 struct Plan {
   int G, NR, P, R, Kpad;
-  size_t off_q, off_ts, off_bad, off_o, off_ml, off_stage, off_clat, off_invl, off_q8, off_fh, total;
+  int Gp;  // tree attention with many rows: chunks of the pair kernel
+  size_t off_q, off_ts, off_bad, off_o, off_ml, off_stage, off_clat, off_invl, off_q8, off_fh, off_tail, total;
 };
 
 // Query rows above which the weight products run as tcgen05 GEMMs; below it
@@ -1581,7 +1647,7 @@ cudaError_t set_smem_once(Kern kern, int bytes, std::atomic<unsigned long long>*
 
 std::atomic<unsigned long long> g_abs_attr[9] = {}, g_attn_attr[14] = {}, g_cmb_attr{0};
 
-Plan make_plan(int B, int S, int T_cap, int sparse_topk) {
+Plan make_plan(int B, int S, int T_cap, int sparse_topk, bool tree = false) {
   Plan pl{};
   const int sms = sm_count();
   pl.R = B * S;
@@ -1603,6 +1669,11 @@ Plan make_plan(int B, int S, int T_cap, int sparse_topk) {
     pl.G = (int)G;
     pl.P = pl.G + pl.R - 1;
   }
+  const bool many_tree = tree && pl.R > kSmallRows;
+  if (many_tree) {
+    pl.Gp = pair_chunks(B, S, T_cap, sms);
+    pl.P = std::max(pl.P, (pl.Gp + B - 1) * S);
+  }
   size_t off = 0;
   pl.off_q = off;
   off = align256(off + (size_t)pl.R * kH * kDc * 2);
@@ -1618,22 +1689,109 @@ Plan make_plan(int B, int S, int T_cap, int sparse_topk) {
   pl.off_stage = off;  // two staging buffers: consecutive layers of one call alternate
   off = align256(off + 2 * (size_t)pl.R * pl.Kpad * kDc * 2);
   pl.off_clat = off;
-  off = align256(off + (pl.R > kSmallRows ? (size_t)pl.R * kH * kDl * 2 : 0));
+  off = align256(off + (pl.R > kSmallRows ? (size_t)pl.R * kH * kDl * (many_tree ? 4 : 2) : 0));
   pl.off_invl = off;
   off = align256(off + (pl.R > kSmallRows ? (size_t)pl.R * kH * 4 : 0));
   // FP8 cache (dense only): quantised query rows and their score factors
   pl.off_q8 = off;
-  off = align256(off + (sparse_topk ? 0 : (size_t)pl.R * kH * kQ8Row));
+  off = align256(off + (sparse_topk || tree ? 0 : (size_t)pl.R * kH * kQ8Row));
   pl.off_fh = off;
-  off = align256(off + (sparse_topk ? 0 : (size_t)pl.R * kH * 4));
+  off = align256(off + (sparse_topk || tree ? 0 : (size_t)pl.R * kH * 4));
+  pl.off_tail = off;
+  off = align256(off + (many_tree ? (size_t)B * kPairStage * kDc * 2 : 0));
   pl.total = off;
   return pl;
+}
+
+// Many rows: merge of the splits, then the W_UV lift as a GEMM.
+cudaError_t run_lift(const DecodeArgs& a, const Plan& pl, unsigned char* w, bool sparse, bool pair, cudaStream_t st) {
+  const Geometry& g = a.g;
+  MergeParams mp{};
+  mp.o_part = reinterpret_cast<float*>(w + pl.off_o);
+  mp.ml_part = reinterpret_cast<float*>(w + pl.off_ml);
+  mp.tile_start = reinterpret_cast<int32_t*>(w + pl.off_ts);
+  mp.T = a.T;
+  mp.bad = reinterpret_cast<int32_t*>(w + pl.off_bad);
+  mp.clat = reinterpret_cast<__nv_bfloat16*>(w + pl.off_clat);
+  mp.inv_l = reinterpret_cast<float*>(w + pl.off_invl);
+  mp.B = a.B;
+  mp.S = a.S;
+  mp.G = pair ? pl.Gp : pl.G;
+  mp.pair = pair ? 1 : 0;
+  mp.sparse = sparse ? 1 : 0;
+  mp.parent = a.parent;
+  kernel_mark(st, "merge");
+  const bool split = a.parent != nullptr;
+  cudaError_t e = launch_pdl(split ? merge_kernel<true> : merge_kernel<false>, dim3((pl.R * kH + 7) / 8), dim3(256), 0, st, mp);
+  if (e != cudaSuccess) return e;
+  GemmArgs gu{};
+  gu.a_base = mp.clat;
+  gu.a_ld_z = split ? 2 * kDl : kDl;
+  gu.a_ld_m = kH * gu.a_ld_z;
+  gu.b_base = a.kv_b;
+  gu.b_rows = (long long)kH * (g.Dn + g.Dv);
+  gu.b_cols = kDl;
+  gu.b_ld = kDl;
+  gu.b_mn_major = 0;
+  gu.b_row0 = g.Dn;
+  gu.b_rows_per_z = g.Dn + g.Dv;
+  gu.b_col0 = 0;
+  gu.c_base = a.out;
+  gu.c_ld_m = (long long)kH * g.Dv;
+  gu.c_ld_z = g.Dv;
+  gu.out_kind = a.out_bf16 ? kGemmOutBf16Scaled : kGemmOutF32Scaled;
+  gu.scale = mp.inv_l;
+  gu.M = pl.R;
+  gu.N = g.Dv;
+  gu.K = split ? 2 * kDl : kDl;
+  gu.b_k_wrap = split ? kDl : 0;
+  gu.Z = kH;
+  gu.flags = a.flags;
+  gu.wait_ns = a.wait_limit_ns;
+  kernel_mark(st, "up_gemm");
+  return launch_gemm_tc(gu, true, st);
+}
+
+// Whether the CTA-pair attention takes a many-row tree call.
+bool pair_pays(int B, int S, int T_cap) {
+  (void)B;
+  (void)T_cap;
+  return S >= 2;
+}
+
+cudaError_t run_pair(const DecodeArgs& a, const Plan& pl, unsigned char* w, long long pool_rows, cudaStream_t st) {
+  PairParams p{};
+  const void* qcat = w + pl.off_q;
+  const void* tail = w + pl.off_tail;
+  const uint64_t rows = (uint64_t)pool_rows, trows = (uint64_t)a.B * kPairStage;
+  if (!make_tmap_2d_bf16(&p.mQ, qcat, (uint64_t)pl.R * kH, kDc, kDc, kH, 64) ||
+      !make_tmap_2d_bf16(&p.mK, a.Lc, rows, kDl, kDl, 128, 64) ||
+      !make_tmap_2d_bf16(&p.mKr, a.Rc, rows, kDr, kDr, 128, 64) ||
+      !make_tmap_2d_bf16(&p.mV, a.Lc, rows, kDl, kDl, 64, 64) ||
+      !make_tmap_2d_bf16(&p.mT, tail, trows, kDc, kDc, 128, 64) || !make_tmap_2d_bf16(&p.mTv, tail, trows, kDc, kDc, 64, 64))
+    return cudaErrorInvalidValue;
+  p.T = a.T;
+  p.parent = a.parent;
+  p.tile_start = reinterpret_cast<const int32_t*>(w + pl.off_ts);
+  p.B = a.B;
+  p.S = a.S;
+  p.T_cap = a.T_cap;
+  p.G = pl.Gp;
+  p.NP = (a.S + 1) / 2;
+  p.c = a.g.scale * kLog2e;
+  p.o_part = reinterpret_cast<float*>(w + pl.off_o);
+  p.ml_part = reinterpret_cast<float*>(w + pl.off_ml);
+  p.flags = a.flags;
+  p.wait_ns = a.wait_limit_ns;
+  p.pages = a.pages;
+  kernel_mark(st, "attention");
+  return launch_attn_pair(p, st);
 }
 
 cudaError_t run(const DecodeArgs& a, void* ws, bool sparse, cudaStream_t st) {
   const Geometry& g = a.g;
   const int B = a.B, S = a.S;
-  const Plan pl = make_plan(B, S, a.T_cap, sparse ? a.topk : 0);
+  const Plan pl = make_plan(B, S, a.T_cap, sparse ? a.topk : 0, a.parent != nullptr);
   const bool paged = a.pages.table != nullptr;
   const long long pool_rows = paged ? (long long)a.pages.num_pages * a.pages.page_size : (long long)B * a.T_cap;
   if (pool_rows >= (1ll << 31) || (long long)B * a.T_cap >= (1ll << 31)) return cudaErrorInvalidValue;
@@ -1693,6 +1851,7 @@ cudaError_t run(const DecodeArgs& a, void* ws, bool sparse, cudaStream_t st) {
   ap.topk = a.topk;
   ap.sparse = sparse ? 1 : 0;
   const bool big = pl.R > kSmallRows;
+  const bool pair = a.parent && big && pair_pays(B, S, a.T_cap);
   ap.Lc = static_cast<const unsigned char*>(a.Lc);
   ap.Rc = static_cast<const __nv_bfloat16*>(a.Rc);
   ap.lat_row_bytes = a.lat_fp8 ? kDl : kDl * 2;
@@ -1714,10 +1873,12 @@ cudaError_t run(const DecodeArgs& a, void* ws, bool sparse, cudaStream_t st) {
   const AbsKern akern = big ? absorb_kernel<4, false> : abs_kerns[paged_abs ? 1 : 0][g.Dn / 64 - 1];
   // many rows: the rotary part of each head spread over up to four CTAs
   const int abs_gx = big ? std::min(4, (pl.R * (kDr / 2) + 2047) / 2048) : kDl / kAbsCols;
+  ap.rope_x = abs_gx;
+  if (pair) ap.tail = reinterpret_cast<__nv_bfloat16*>(w + pl.off_tail);
   e = set_smem_once(akern, (int)abs_smem, &g_abs_attr[big ? 8 : (paged_abs ? 4 : 0) + g.Dn / 64 - 1]);
   if (e != cudaSuccess) return e;
   kernel_mark(st, big ? "plan_rope" : "absorb");
-  e = launch_pdl(akern, dim3(abs_gx, kH), dim3(kAbsThreads), abs_smem, st, ap);
+  e = launch_pdl(akern, dim3(abs_gx + (pair ? 1 : 0), kH), dim3(kAbsThreads), abs_smem, st, ap);
   if (e != cudaSuccess) return e;
   if (big) {  // qabs for many rows: per-head GEMM [R x qk_nope] x W_UK[h] on the tensor cores
     GemmArgs ga{};
@@ -1764,6 +1925,11 @@ cudaError_t run(const DecodeArgs& a, void* ws, bool sparse, cudaStream_t st) {
   }
 
   // 2. attention
+  if (pair) {
+    e = run_pair(a, pl, w, pool_rows, st);
+    if (e != cudaSuccess) return e;
+    return run_lift(a, pl, w, sparse, true, st);
+  }
   AttnParams tp{};
   bool maps_ok = a.lat_fp8 ? make_tmap_2d_u8(&tp.mQ, q8, (uint64_t)pl.R * kH, kQ8Row, kQ8Row, kH, 128)
                            : make_tmap_2d_bf16(&tp.mQ, qcat, (uint64_t)pl.R * kH, kDc, kDc, kH, 64);
@@ -1830,49 +1996,7 @@ cudaError_t run(const DecodeArgs& a, void* ws, bool sparse, cudaStream_t st) {
   if (e != cudaSuccess) return e;
 
   // 3. merge of the splits and the W_UV lift
-  if (big) {
-    MergeParams mp{};
-    mp.o_part = o_part;
-    mp.ml_part = ml_part;
-    mp.tile_start = ts;
-    mp.T = a.T;
-    mp.bad = bad;
-    mp.clat = reinterpret_cast<__nv_bfloat16*>(w + pl.off_clat);
-    mp.inv_l = reinterpret_cast<float*>(w + pl.off_invl);
-    mp.B = B;
-    mp.S = S;
-    mp.G = pl.G;
-    mp.sparse = sparse ? 1 : 0;
-    mp.parent = a.parent;
-    kernel_mark(st, "merge");
-    e = launch_pdl(merge_kernel, dim3((pl.R * kH + 7) / 8), dim3(256), 0, st, mp);
-    if (e != cudaSuccess) return e;
-    GemmArgs gu{};
-    gu.a_base = mp.clat;
-    gu.a_ld_z = kDl;
-    gu.a_ld_m = (long long)kH * kDl;
-    gu.b_base = a.kv_b;
-    gu.b_rows = (long long)kH * (g.Dn + g.Dv);
-    gu.b_cols = kDl;
-    gu.b_ld = kDl;
-    gu.b_mn_major = 0;
-    gu.b_row0 = g.Dn;
-    gu.b_rows_per_z = g.Dn + g.Dv;
-    gu.b_col0 = 0;
-    gu.c_base = a.out;
-    gu.c_ld_m = (long long)kH * g.Dv;
-    gu.c_ld_z = g.Dv;
-    gu.out_kind = a.out_bf16 ? kGemmOutBf16Scaled : kGemmOutF32Scaled;
-    gu.scale = mp.inv_l;
-    gu.M = pl.R;
-    gu.N = g.Dv;
-    gu.K = kDl;
-    gu.Z = kH;
-    gu.flags = a.flags;
-    gu.wait_ns = a.wait_limit_ns;
-    kernel_mark(st, "up_gemm");
-    return launch_gemm_tc(gu, true, st);
-  }
+  if (big) return run_lift(a, pl, w, sparse, false, st);
   CombineParams cp{};
   cp.kv_b = static_cast<const __nv_bfloat16*>(a.kv_b);
   cp.o_part = o_part;
@@ -1910,8 +2034,8 @@ int tc_decode_launch_count(bool sparse, int B, int S) {
   return (sparse ? 1 : 0) + ((long long)B * S > kSmallRows ? 5 : 3);
 }
 
-size_t tc_decode_workspace_bytes(const Geometry&, int B, int S, int T_cap, int sparse_topk) {
-  return make_plan(B, S, T_cap, sparse_topk).total;
+size_t tc_decode_workspace_bytes(const Geometry&, int B, int S, int T_cap, int sparse_topk, bool tree) {
+  return make_plan(B, S, T_cap, sparse_topk, tree).total;
 }
 
 cudaError_t launch_decode_tc(const DecodeArgs& a, void* ws, size_t, cudaStream_t st) {

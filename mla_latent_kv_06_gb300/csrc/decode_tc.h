@@ -13,8 +13,9 @@ namespace mla {
 bool tc_decode_geometry_ok(const Geometry& g);
 
 // Workspace of the tensor-core path.  sparse_topk = 0 for dense decode (then
-// T_cap bounds the keys per sequence), else the selection width.
-size_t tc_decode_workspace_bytes(const Geometry& g, int B, int S, int T_cap, int sparse_topk);
+// T_cap bounds the keys per sequence), else the selection width.  tree: the
+// S new tokens form a drafted tree.
+size_t tc_decode_workspace_bytes(const Geometry& g, int B, int S, int T_cap, int sparse_topk, bool tree = false);
 
 // Kernels launched by one tensor-core decode call.
 int tc_decode_launch_count(bool sparse, int B, int S);
