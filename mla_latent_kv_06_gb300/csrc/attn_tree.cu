@@ -49,6 +49,7 @@ constexpr int kThreads = 320;  // warp 0: TMA, warp 1: MMA (leader CTA), warps 2
 constexpr int kSoft = 256, kSoftWarps = 8;
 constexpr int kRows = 64, kDl = 512, kDc = 576;
 constexpr int kStages = 7;
+constexpr int kFree = 4;  // barriers that free stages, two at a time (see issue)
 constexpr uint32_t kStageBytes = 16384, kQAtom = 8192;
 constexpr uint32_t kQBytes = 9 * kQAtom, kPBytes = 4 * 8192;
 constexpr uint32_t kRingOff = kQBytes + kPBytes;
@@ -58,7 +59,8 @@ constexpr float kTau = 8.f;  // lazy rescale threshold (log2 units)
 constexpr long long kDrainNs = 1000000000LL;
 
 struct Shared {
-  uint64_t full[kStages], empty[kStages];  // full: the leader's, for both CTAs' bytes
+  uint64_t full[kStages];  // the leader's, for both CTAs' bytes
+  uint64_t free2[kFree];   // stages 2m and 2m + 1 have been consumed: barrier m % kFree
   uint64_t q_full, q_empty, s_full[2], p_full, pv_done, mma_done;
   uint32_t tmem;
   int abort;
@@ -88,32 +90,66 @@ __device__ __forceinline__ uint32_t in_cta(const void* p, uint32_t rank) {
 __device__ __forceinline__ void arrive_leader(uint32_t bar) {
   __syncwarp();
   if ((threadIdx.x & 31) == 0)
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// Tile load into this CTA's shared memory, completing on a barrier of either CTA of the pair.
-__device__ __forceinline__ void load_2d(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+// One lane of a converged warp.
+__device__ __forceinline__ uint32_t elect_lane() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(r));
+  return r;
+}
+
+// Tile loads into this CTA's shared memory, completing on a barrier of either
+// CTA of the pair; issued by the lane with lead != 0 of a converged warp.
+__device__ __forceinline__ void load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar, uint32_t lead) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
-      "[%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+      "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %5, 0;\n\t"
+      "@e cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
+      "[%0], [%1, {%2, %3}], [%4];\n\t}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "r"(lead)
       : "memory");
 }
 
-__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar,
+                                        uint32_t lead) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %6, 0;\n\t"
+      "@e cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
+      "[%0], [%1, {%2, %3, %4}], [%5];\n\t}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar), "r"(lead)
+      : "memory");
+}
+
+__device__ __forceinline__ void expect_bytes(uint32_t bar, uint32_t bytes, uint32_t lead) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t.reg .b64 st;\n\tsetp.ne.b32 e, %2, 0;\n\t"
+      "@e mbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n\t}" ::"r"(bar),
+      "r"(bytes), "r"(lead)
+      : "memory");
+}
+
+// MMA and commit of the lane with lead != 0, called by the whole warp.  The
+// code around them stays free of divergence, so that the compiler keeps the
+// descriptors in uniform registers: the same loop run by one lane issues an
+// MMA every 84 cycles or slower (more instructions between MMAs, more idle
+// pipe), run by the warp every 64, the pipe's own rate.
+__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate,
+                                         uint32_t lead) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(lead)
       : "memory");
 }
 
 // Arrive on both CTAs' `bar` once the MMAs issued so far have retired.
-__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+__device__ __forceinline__ void commit_pair(uint64_t* bar, uint32_t lead) {
   asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+      "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %2, 0;\n\t"
+      "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(
           smem_u32(bar)),
-      "h"((uint16_t)3)
+      "h"((uint16_t)3), "r"(lead)
       : "memory");
 }
 
@@ -162,23 +198,29 @@ __device__ __forceinline__ Tile tile_at(int Tb, int S, int k) {
   return t;
 }
 
-// ------------------------------------------------------------ TMA producer (one thread of each CTA)
+// ------------------------------------------------------------ TMA producer (warp 0 of each CTA, converged)
 __device__ __forceinline__ void produce(const PairParams& p, Shared& sh, unsigned char* smem, uint32_t rank, int g, int pair,
                                         int* issued, int* q_issued) {
   volatile int* abort = &sh.abort;
-  int n = 0;
+  const uint32_t lead = elect_lane(), arm = rank == 0 ? lead : 0;  // the leader's lane arms the barriers
+  int n = 0, s = 0, freed = 0;  // stages issued, the next one's slot, freed pairs waited for
   bool ok = true;
-  // next ring stage: its address, or null when the wait for it gave up
-  auto stage = [&](uint32_t* bar) -> unsigned char* {
-    const int s = n % kStages, u = n / kStages;
-    if (!mbar_wait(&sh.empty[s], (u & 1) ^ 1, abort, p.flags, p.wait_ns)) {
-      ok = false;
-      return nullptr;
+  const uint32_t full0 = in_cta(&sh.full[0], 0), own0 = smem_u32(&sh.full[0]), ring0 = smem_u32(smem + kRingOff);
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, p.flags, p.wait_ns));
+  };
+  // Waits until the next stage is free: the one seven back, once its pair is.
+  auto acquire = [&]() -> bool {
+    if (n >= kStages && (n - kStages) / 2 >= freed) {
+      if (!wait(&sh.free2[freed % kFree], (freed / kFree) & 1)) return ok = false;
+      ++freed;
     }
-    if (rank == 0) mbar_arrive_expect_tx(&sh.full[s], 2 * kStageBytes);
-    *bar = in_cta(&sh.full[s], 0);
+    expect_bytes(own0 + 8 * s, 2 * kStageBytes, arm);
+    return true;
+  };
+  auto advance = [&]() {
     ++n;
-    return smem + kRingOff + s * kStageBytes;
+    s = s + 1 == kStages ? 0 : s + 1;
   };
   auto row_of = [&](int b, int t) -> int {
     bool bad = false;
@@ -194,27 +236,25 @@ __device__ __forceinline__ void produce(const PairParams& p, Shared& sh, unsigne
       if (t0 >= Tb) t0 = t.row0;  // no key of this half: any rows do
       y = row_of(b, t0);
     }
-    for (int d = 0; d < 9 && ok; ++d) {
-      uint32_t bar;
-      unsigned char* dst = stage(&bar);
-      if (!dst) break;
-      if (t.tail) load_2d(dst, &p.mT, 64 * d, y, bar);
-      else if (d < 8) load_2d(dst, &p.mK, 64 * d, y, bar);
-      else load_2d(dst, &p.mKr, 0, y, bar);
+    const CUtensorMap* lat = t.tail ? &p.mT : &p.mK;
+#pragma unroll 1
+    for (int d = 0; d < 9; ++d) {
+      if (!acquire()) return;
+      const bool rope = d == 8 && !t.tail;
+      load_2d(ring0 + s * kStageBytes, rope ? &p.mKr : lat, rope ? 0 : 64 * d, y, full0 + 8 * s, lead);
+      advance();
     }
   };
   auto load_v = [&](int b, int Tb, int k) {
     const Tile t = tile_at(Tb, p.S, k);
-    for (int kc = 0; kc < (t.keys + 63) / 64 && ok; ++kc) {
+    const CUtensorMap* map = t.tail ? &p.mTv : &p.mV;
+#pragma unroll 1
+    for (int kc = 0; kc < (t.keys + 63) / 64; ++kc) {
       const int y = t.tail ? b * kPairStage + 64 * kc : row_of(b, t.row0 + 64 * kc);
-      const CUtensorMap* map = t.tail ? &p.mTv : &p.mV;
-      for (int nb = 0; nb < 2 && ok; ++nb) {
-        uint32_t bar;
-        unsigned char* dst = stage(&bar);
-        if (!dst) break;
-        const int x = 256 * nb + 128 * (int)rank;
-        load_2d(dst, map, x, y, bar);
-        load_2d(dst + 8192, map, x + 64, y, bar);
+      for (int nb = 0; nb < 2; ++nb) {  // two 64-latent atoms of 64 keys each
+        if (!acquire()) return;
+        load_3d(ring0 + s * kStageBytes, map, 0, y, 4 * nb + 2 * (int)rank, full0 + 8 * s, lead);
+        advance();
       }
     }
   };
@@ -222,12 +262,12 @@ __device__ __forceinline__ void produce(const PairParams& p, Shared& sh, unsigne
   int np = 0;
   for (pc.start(p, g); ok && pc.next(); ++np) {
     const int Tb = p.T[pc.b];
-    ok = mbar_wait(&sh.q_empty, (np & 1) ^ 1, abort, p.flags, p.wait_ns);
+    ok = wait(&sh.q_empty, (np & 1) ^ 1);
     if (!ok) break;
-    if (rank == 0) mbar_arrive_expect_tx(&sh.q_full, 2 * kQBytes);
+    expect_bytes(smem_u32(&sh.q_full), 2 * kQBytes, arm);
     const uint32_t qbar = in_cta(&sh.q_full, 0);
     const int qrow = (pc.b * p.S + 2 * pair + (int)rank) * kRows;  // past the last node: another row or zeros
-    for (int d = 0; d < 9; ++d) load_2d(smem + d * kQAtom, &p.mQ, 64 * d, qrow, qbar);
+    for (int d = 0; d < 9; ++d) load_2d(smem_u32(smem + d * kQAtom), &p.mQ, 64 * d, qrow, qbar, lead);
     ++*q_issued;
     load_k(pc.b, Tb, pc.lo);
     for (int k = pc.lo; k < pc.hi && ok; ++k) {
@@ -236,80 +276,129 @@ __device__ __forceinline__ void produce(const PairParams& p, Shared& sh, unsigne
     }
   }
   *issued = n;
+  __syncwarp();
 }
 
-// ------------------------------------------------------------ MMA issuer (one thread of the leader CTA)
-__device__ __forceinline__ void issue(const PairParams& p, Shared& sh, unsigned char* smem, uint32_t tmem, int g) {
+// ------------------------------------------------------------ MMA issuer (warp 1 of the leader CTA, converged)
+__device__ __forceinline__ void issue(const PairParams& p, Shared& sh, unsigned char* smem, uint32_t tmem_any, int g) {
   volatile int* abort = &sh.abort;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_any, 0), lead = elect_lane();
   const uint32_t idS = idesc_bf16_f32(128, 256, 0, 0), idO = idesc_bf16_f32(128, 256, 0, 1);
   const uint64_t dQ = smem_desc_sw128(smem_u32(smem), 16, 1024);
   const uint64_t dP = smem_desc_sw128(smem_u32(smem + kQBytes), 16, 1024);
   const uint64_t dK = smem_desc_sw128(smem_u32(smem + kRingOff), 16, 1024);
   const uint64_t dV = smem_desc_sw128(smem_u32(smem + kRingOff), 8192, 1024);
-  int n = 0, it = 0;
-  bool ok = true;
+  int n = 0, it = 0, s = 0;
+  uint32_t par = 0;  // parity of the slot's phase
+  bool ok = true, ready = false;
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, p.flags, p.wait_ns));
+  };
+  // Waits for stage n.  The test of the stage after it is issued here, ahead
+  // of this stage's MMAs, and its answer used one stage later: a barrier test
+  // takes some 190 cycles, and four MMAs run for 258.
+  auto acquire = [&]() -> bool {
+    if (!__all_sync(0xffffffffu, ready) && !wait(&sh.full[s], par)) return ok = false;
+    const int s1 = s + 1 == kStages ? 0 : s + 1;
+    ready = mbar_test_wait(&sh.full[s1], s1 ? par : par ^ 1);
+    tc_fence_after();
+    return true;
+  };
+  // A commit after four MMAs costs the issuing warp 58 cycles that the pipe
+  // idles, after eight none: stages are freed in pairs.
+  auto release = [&]() {
+    if (n & 1) commit_pair(&sh.free2[(n >> 1) % kFree], lead);
+    ++n;
+    if (++s == kStages) {
+      s = 0;
+      par ^= 1;
+    }
+  };
   auto scores = [&](int j) {  // S of tile number j
     const uint32_t d = tmem + kColS + 128 * (j & 1);
-    for (int a = 0; a < 9; ++a, ++n) {
-      const int s = n % kStages;
-      if (!mbar_wait(&sh.full[s], (n / kStages) & 1, abort, p.flags, p.wait_ns)) {
-        ok = false;
-        return;
-      }
-      tc_fence_after();
+#pragma unroll
+    for (int a = 0; a < 9; ++a) {
+      if (!acquire()) return;
       const uint64_t db = dK + (uint64_t)(s * (kStageBytes >> 4)), da = dQ + (uint64_t)(a * (kQAtom >> 4));
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk) mma_pair(d, da + 2 * kk, db + 2 * kk, idS, (a | kk) != 0 ? 1u : 0u);
-      commit_pair(&sh.empty[s]);
+      for (int kk = 0; kk < 4; ++kk) mma_pair(d, da + 2 * kk, db + 2 * kk, idS, (a | kk) != 0 ? 1u : 0u, lead);
+      release();
     }
-    commit_pair(&sh.s_full[j & 1]);
+    commit_pair(&sh.s_full[j & 1], lead);
   };
   Pieces pc;
   int np = 0;
   for (pc.start(p, g); ok && pc.next(); ++np) {
     const int Tb = p.T[pc.b];
-    ok = mbar_wait(&sh.q_full, np & 1, abort, p.flags, p.wait_ns);
+    ok = wait(&sh.q_full, np & 1);
     if (!ok) break;
     tc_fence_after();
     scores(it);
-    if (ok && pc.lo + 1 == pc.hi) commit_pair(&sh.q_empty);
+    if (ok && pc.lo + 1 == pc.hi) commit_pair(&sh.q_empty, lead);
     for (int k = pc.lo; k < pc.hi && ok; ++k, ++it) {
       if (k + 1 < pc.hi) {
         scores(it + 1);
-        if (ok && k + 2 == pc.hi) commit_pair(&sh.q_empty);  // the piece's last score product
+        if (ok && k + 2 == pc.hi) commit_pair(&sh.q_empty, lead);  // the piece's last score product
       }
-      ok = ok && mbar_wait(&sh.p_full, it & 1, abort, p.flags, p.wait_ns);
+      ok = ok && wait(&sh.p_full, it & 1);
       if (!ok) break;
       tc_fence_after();
       const Tile t = tile_at(Tb, p.S, k);
-      for (int kc = 0; kc < (t.keys + 63) / 64 && ok; ++kc) {
-        const int steps = min(4, (t.keys - 64 * kc + 15) / 16);
-        for (int nb = 0; nb < 2; ++nb, ++n) {
-          const int s = n % kStages;
-          if (!mbar_wait(&sh.full[s], (n / kStages) & 1, abort, p.flags, p.wait_ns)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint64_t db = dV + (uint64_t)(s * (kStageBytes >> 4)), da = dP + (uint64_t)(kc * (8192 >> 4));
-          const uint32_t d = tmem + kColO + 128 * nb;
-          const uint32_t keep = (k > pc.lo || kc > 0) ? 1u : 0u;
-          if (steps == 4) {
+      uint32_t keep = k > pc.lo ? 1u : 0u;
+      if (t.keys == kPairTile) {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) mma_pair(d, da + 2 * kk, db + 128 * kk, idO, kk > 0 ? 1u : keep);
-          } else {
-            for (int kk = 0; kk < steps; ++kk) mma_pair(d, da + 2 * kk, db + 128 * kk, idO, kk > 0 ? 1u : keep);
+        for (int kc = 0; kc < 4; ++kc) {
+#pragma unroll
+          for (int nb = 0; nb < 2; ++nb) {
+            if (!ok || !acquire()) break;
+            const uint64_t db = dV + (uint64_t)(s * (kStageBytes >> 4)), da = dP + (uint64_t)(kc * (8192 >> 4));
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_pair(tmem + kColO + 128 * nb, da + 2 * kk, db + 128 * kk, idO, (kc | kk) != 0 ? 1u : keep, lead);
+            release();
           }
-          commit_pair(&sh.empty[s]);
+        }
+      } else {  // a piece's last tiles: whole 16-key steps
+        for (int kc = 0; kc < (t.keys + 63) / 64 && ok; ++kc) {
+          const int steps = min(4, (t.keys - 64 * kc + 15) / 16);
+          for (int nb = 0; nb < 2; ++nb) {
+            if (!acquire()) break;
+            const uint64_t db = dV + (uint64_t)(s * (kStageBytes >> 4)), da = dP + (uint64_t)(kc * (8192 >> 4));
+            for (int kk = 0; kk < steps; ++kk)
+              mma_pair(tmem + kColO + 128 * nb, da + 2 * kk, db + 128 * kk, idO, (kc | kk) != 0 ? 1u : keep, lead);
+            release();
+          }
         }
       }
-      if (ok) commit_pair(&sh.pv_done);
+      if (ok) commit_pair(&sh.pv_done, lead);
     }
   }
-  commit_pair(&sh.mma_done);
+  __syncwarp();
+  commit_pair(&sh.mma_done, lead);
 }
 
 // ------------------------------------------------------------ softmax warps
+// 32 lanes x 32 bits, 16 consecutive columns.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* v) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// The low n bits (none for n <= 0, all for n >= 64).
+__device__ __forceinline__ unsigned long long low_bits(int n) {
+  return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1;
+}
+
 __device__ __forceinline__ void soften(const PairParams& p, Shared& sh, unsigned char* smem, uint32_t tmem, uint32_t rank,
                                        int g, int pair) {
   volatile int* abort = &sh.abort;
@@ -332,6 +421,7 @@ __device__ __forceinline__ void soften(const PairParams& p, Shared& sh, unsigned
       mask = node.mask;
       if (node.state == kNodeBad && tsm == 0) raise_flag(p.flags, MLA_DEV_BAD_INDEX);
     }
+    const int rem = Tb - p.S - b16;  // prefix rows at the start of the tail
     float lsum = 0.f;
     for (int k = pc.lo; k < pc.hi; ++k, ++it) {
       const bool first = k == pc.lo;
@@ -339,38 +429,44 @@ __device__ __forceinline__ void soften(const PairParams& p, Shared& sh, unsigned
       bool fail = !mbar_wait(&sh.s_full[it & 1], (it >> 1) & 1, abort, p.flags, p.wait_ns);
       if (bar_red_or(1, kSoft, fail)) return;
       tc_fence_after();
-      float v[64];
-      tmem_ld64(t_lane + kColS + 128 * (it & 1) + 64 * ch, v);
-      tmem_wait_ld();
-      if (t.tail) {  // prefix remainder, then the tree's rows through the node's mask
-        const int rem = Tb - p.S - b16;
-#pragma unroll
-        for (int i = 0; i < 64; ++i) {
-          const int j = key0 + i;
-          const bool see = mask != 0 && j < t.keys && (j < rem || ((mask >> (j - rem)) & 1ull));
-          if (!see) v[i] = -INFINITY;
-          else if (fabsf(v[i]) == INFINITY) v[i] = __int_as_float(0x7fc00000);
+      // Scores are read from TMEM sixteen columns at a time, once for the maximum
+      // and once for the probabilities, in loops that are not unrolled: the
+      // eight warps' code then stays within the instruction cache next to the
+      // issuing warp's, whose fetches otherwise stall the tensor pipe.
+      const uint32_t sc = t_lane + kColS + 128 * (it & 1) + 64 * ch;
+      unsigned long long vis = ~0ull;  // bit i: key key0 + i is visible
+      const bool masked = t.tail || t.keys < kPairTile || mask == 0;
+      if (masked) {
+        vis = low_bits(t.keys - key0);
+        if (t.tail) {  // the prefix remainder, then the tree's rows through the node's mask
+          const int sh0 = rem - key0;  // the tree's first row
+          vis &= low_bits(sh0) | (sh0 >= 64 ? 0 : sh0 >= 0 ? mask << sh0 : sh0 > -64 ? mask >> -sh0 : 0);
         }
-      } else if (t.keys < kPairTile || mask == 0) {
+        if (mask == 0) vis = 0;
+      }
+      float mx = -INFINITY;
+#pragma unroll 1
+      for (int c0 = 0; c0 < 64; c0 += 16) {
+        float v[16];
+        tmem_ld16(sc + c0, v);
+        tmem_wait_ld();
+        const uint32_t bits = (uint32_t)(vis >> c0);
+        if (masked) {
 #pragma unroll
-        for (int i = 0; i < 64; ++i)
-          if (key0 + i >= t.keys || mask == 0) v[i] = -INFINITY;
+          for (int i = 0; i < 16; ++i) v[i] = (bits >> i) & 1u ? v[i] : -INFINITY;
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) mx = fmaxf(mx, v[i]);
       }
       // running maximum, moved only when a score exceeds it by more than kTau
       bool slow = first;
       float mrow = 0.f;
       if (!first) {
         mrow = sh.m[row];
-        float mx = v[0];
-#pragma unroll
-        for (int i = 1; i < 64; ++i) mx = fmaxf(mx, v[i]);
         slow = bar_red_or(2, kSoft, mx * c > mrow + kTau);
       }
       bool rescale = false;
       if (slow) {
-        float mx = v[0];
-#pragma unroll
-        for (int i = 1; i < 64; ++i) mx = fmaxf(mx, v[i]);
         sh.red[2 * (q >> 1) + ch][row] = mx;
         named_barrier(1, kSoft);
         bool need = false;
@@ -389,26 +485,43 @@ __device__ __forceinline__ void soften(const PairParams& p, Shared& sh, unsigned
         rescale = bar_red_or(2, kSoft, need);
         mrow = sh.m[row];
       }
-      // probabilities: bf16 is the value product's operand; the row sum adds the rounded values
-      uint32_t pk[32];
-      float add0 = 0.f, add1 = 0.f;
-#pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        pk[i] = pack2(exp2f(fmaf(v[2 * i], c, -mrow)), exp2f(fmaf(v[2 * i + 1], c, -mrow)));
-        const float2 f = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&pk[i]));
-        add0 += f.x;
-        add1 += f.y;
-      }
-      if (rescale) lsum *= sh.alpha[row];
-      lsum += add0 + add1;
       if (it > 0) {  // the previous value product has read P and written O
         fail = !mbar_wait(&sh.pv_done, (it - 1) & 1, abort, p.flags, p.wait_ns);
         if (bar_red_or(1, kSoft, fail)) return;
         tc_fence_after();
       }
+      // probabilities: bf16 is the value product's operand; the row sum adds the rounded values
+      if (rescale) lsum *= sh.alpha[row];
+#pragma unroll 1
+      for (int c0 = 0; c0 < 64; c0 += 16) {
+        float v[16];
+        tmem_ld16(sc + c0, v);
+        tmem_wait_ld();
+        const uint32_t bits = (uint32_t)(vis >> c0);
+        uint32_t pk[8];
+        float add0 = 0.f, add1 = 0.f;
+        if (masked) {  // (a branch around the loop: one inside it would cost more than the exponentials)
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        *reinterpret_cast<uint4*>(prow + ((i ^ (row & 7)) << 4)) = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+          for (int i = 0; i < 16; ++i) {
+            // only staged rows may hide values that are not finite
+            const float x = t.tail && fabsf(v[i]) == INFINITY ? qnan() : v[i];
+            v[i] = (bits >> i) & 1u ? x : -INFINITY;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = ex2(fmaf(v[i], c, -mrow));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          pk[i] = pack2(v[2 * i], v[2 * i + 1]);
+          const float2 f = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&pk[i]));
+          add0 += f.x;
+          add1 += f.y;
+        }
+        lsum += add0 + add1;
+        const int ck = c0 >> 3;  // 16-byte chunks ck and ck + 1 of the row, swizzled
+        *reinterpret_cast<uint4*>(prow + ((ck ^ (row & 7)) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+        *reinterpret_cast<uint4*>(prow + (((ck + 1) ^ (row & 7)) << 4)) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+      }
       if (rescale) {
         const float al = sh.alpha[row];
 #pragma unroll 1
@@ -459,14 +572,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_pa
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                          ~static_cast<uintptr_t>(1023));
   __shared__ Shared sh;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5;
   const uint32_t rank = cta_rank();
   const int cluster = blockIdx.x >> 1, pair = cluster % p.NP, g = cluster / p.NP;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kStages; ++i) {
-      mbar_init(&sh.full[i], 1);
-      mbar_init(&sh.empty[i], 1);
-    }
+    for (int i = 0; i < kStages; ++i) mbar_init(&sh.full[i], 1);
+    for (int i = 0; i < kFree; ++i) mbar_init(&sh.free2[i], 1);
     mbar_init(&sh.q_full, 1);
     mbar_init(&sh.q_empty, 1);
     mbar_init(&sh.s_full[0], 1);
@@ -491,15 +602,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_pa
 
   int issued = 0, q_issued = 0;
   if (warp == 0) {
-    if (lane == 0) produce(p, sh, smem, rank, g, pair, &issued, &q_issued);
-    __syncwarp();
+    produce(p, sh, smem, rank, g, pair, &issued, &q_issued);
   } else if (warp == 1) {
-    if (lane == 0) {
-      if (rank == 0) issue(p, sh, smem, tmem, g);
-      // both CTAs: every MMA and every arrival of its commits has happened
-      volatile int no_abort = 0;
-      mbar_wait(&sh.mma_done, 0, &no_abort, p.flags, p.wait_ns > kDrainNs ? p.wait_ns : kDrainNs);
-    }
+    if (rank == 0) issue(p, sh, smem, tmem, g);
+    // both CTAs: every MMA and every arrival of its commits has happened
+    volatile int no_abort = 0;
+    mbar_wait(&sh.mma_done, 0, &no_abort, p.flags, p.wait_ns > kDrainNs ? p.wait_ns : kDrainNs);
     __syncwarp();
   } else {
     soften(p, sh, smem, tmem, rank, g, pair);

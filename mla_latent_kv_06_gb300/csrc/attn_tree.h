@@ -25,9 +25,9 @@ struct PairParams {
   CUtensorMap mQ;   // qcat [R*64, 576], box 64 x 64
   CUtensorMap mK;   // latent rows, box 128 x 64
   CUtensorMap mKr;  // rotary key rows, box 128 x 64
-  CUtensorMap mV;   // latent rows, box 64 x 64
+  CUtensorMap mV;   // latents as (column in atom, row, 64-column atom), box 64 x 64 x 2
   CUtensorMap mT;   // staging [B*128, 576], box 128 x 64
-  CUtensorMap mTv;  // staging, box 64 x 64
+  CUtensorMap mTv;  // staged latents likewise
   const int32_t* T;
   const int32_t* parent;
   const int32_t* tile_start;  // [B + 1] prefix of pair_tiles

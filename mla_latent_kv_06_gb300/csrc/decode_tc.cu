@@ -1767,8 +1767,11 @@ cudaError_t run_pair(const DecodeArgs& a, const Plan& pl, unsigned char* w, long
   if (!make_tmap_2d_bf16(&p.mQ, qcat, (uint64_t)pl.R * kH, kDc, kDc, kH, 64) ||
       !make_tmap_2d_bf16(&p.mK, a.Lc, rows, kDl, kDl, 128, 64) ||
       !make_tmap_2d_bf16(&p.mKr, a.Rc, rows, kDr, kDr, 128, 64) ||
-      !make_tmap_2d_bf16(&p.mV, a.Lc, rows, kDl, kDl, 64, 64) ||
-      !make_tmap_2d_bf16(&p.mT, tail, trows, kDc, kDc, 128, 64) || !make_tmap_2d_bf16(&p.mTv, tail, trows, kDc, kDc, 64, 64))
+      !make_tmap_2d_bf16(&p.mT, tail, trows, kDc, kDc, 128, 64))
+    return cudaErrorInvalidValue;
+  const uint64_t vd[3] = {64, rows, kDl / 64}, vs[2] = {kDl * 2, 128}, td[3] = {64, trows, kDl / 64}, ts[2] = {kDc * 2, 128};
+  const uint32_t box[3] = {64, 64, 2};
+  if (!make_tmap_3d_bf16(&p.mV, a.Lc, vd, vs, box) || !make_tmap_3d_bf16(&p.mTv, tail, td, ts, box))
     return cudaErrorInvalidValue;
   p.T = a.T;
   p.parent = a.parent;
