@@ -100,6 +100,10 @@ __device__ __forceinline__ uint32_t elect_lane() {
   return r;
 }
 
+// A condition that is the same in every lane, as a vote: the compiler then
+// knows the branch on it does not diverge.
+__device__ __forceinline__ bool uni(bool c) { return __any_sync(0xffffffffu, c); }
+
 // Tile loads into this CTA's shared memory, completing on a barrier of either
 // CTA of the pair; issued by the lane with lead != 0 of a converged warp.
 __device__ __forceinline__ void load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar, uint32_t lead) {
@@ -198,6 +202,14 @@ __device__ __forceinline__ Tile tile_at(int Tb, int S, int k) {
   return t;
 }
 
+// mbar_wait out of line, for the MMA loop: its iterations then hold a test and
+// a call per barrier.  Inlined waits and unrolled stage loops lengthen the code
+// between MMAs and cost 20% of the kernel.
+__device__ __noinline__ bool slow_wait(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned int* flags,
+                                       long long limit_ns) {
+  return mbar_wait(bar, parity, abort, flags, limit_ns);
+}
+
 // ------------------------------------------------------------ TMA producer (warp 0 of each CTA, converged)
 __device__ __forceinline__ void produce(const PairParams& p, Shared& sh, unsigned char* smem, uint32_t rank, int g, int pair,
                                         int* issued, int* q_issued) {
@@ -249,7 +261,7 @@ __device__ __forceinline__ void produce(const PairParams& p, Shared& sh, unsigne
     const Tile t = tile_at(Tb, p.S, k);
     const CUtensorMap* map = t.tail ? &p.mTv : &p.mV;
 #pragma unroll 1
-    for (int kc = 0; kc < (t.keys + 63) / 64; ++kc) {
+    for (int kc = 0; uni(kc < (t.keys + 63) / 64); ++kc) {
       const int y = t.tail ? b * kPairStage + 64 * kc : row_of(b, t.row0 + 64 * kc);
       for (int nb = 0; nb < 2; ++nb) {  // two 64-latent atoms of 64 keys each
         if (!acquire()) return;
@@ -260,7 +272,7 @@ __device__ __forceinline__ void produce(const PairParams& p, Shared& sh, unsigne
   };
   Pieces pc;
   int np = 0;
-  for (pc.start(p, g); ok && pc.next(); ++np) {
+  for (pc.start(p, g); ok && uni(pc.next()); ++np) {
     const int Tb = p.T[pc.b];
     ok = wait(&sh.q_empty, (np & 1) ^ 1);
     if (!ok) break;
@@ -270,8 +282,8 @@ __device__ __forceinline__ void produce(const PairParams& p, Shared& sh, unsigne
     for (int d = 0; d < 9; ++d) load_2d(smem_u32(smem + d * kQAtom), &p.mQ, 64 * d, qrow, qbar, lead);
     ++*q_issued;
     load_k(pc.b, Tb, pc.lo);
-    for (int k = pc.lo; k < pc.hi && ok; ++k) {
-      if (k + 1 < pc.hi) load_k(pc.b, Tb, k + 1);
+    for (int k = pc.lo; uni(k < pc.hi) && ok; ++k) {
+      if (uni(k + 1 < pc.hi)) load_k(pc.b, Tb, k + 1);
       if (ok) load_v(pc.b, Tb, k);
     }
   }
@@ -292,7 +304,7 @@ __device__ __forceinline__ void issue(const PairParams& p, Shared& sh, unsigned 
   uint32_t par = 0;  // parity of the slot's phase
   bool ok = true, ready = false;
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, p.flags, p.wait_ns));
+    return __all_sync(0xffffffffu, slow_wait(bar, parity, abort, p.flags, p.wait_ns));
   };
   // Waits for stage n.  The test of the stage after it is issued here, ahead
   // of this stage's MMAs, and its answer used one stage later: a barrier test
@@ -301,7 +313,6 @@ __device__ __forceinline__ void issue(const PairParams& p, Shared& sh, unsigned 
     if (!__all_sync(0xffffffffu, ready) && !wait(&sh.full[s], par)) return ok = false;
     const int s1 = s + 1 == kStages ? 0 : s + 1;
     ready = mbar_test_wait(&sh.full[s1], s1 ? par : par ^ 1);
-    tc_fence_after();
     return true;
   };
   // A commit after four MMAs costs the issuing warp 58 cycles that the pipe
@@ -316,7 +327,7 @@ __device__ __forceinline__ void issue(const PairParams& p, Shared& sh, unsigned 
   };
   auto scores = [&](int j) {  // S of tile number j
     const uint32_t d = tmem + kColS + 128 * (j & 1);
-#pragma unroll
+#pragma unroll 1
     for (int a = 0; a < 9; ++a) {
       if (!acquire()) return;
       const uint64_t db = dK + (uint64_t)(s * (kStageBytes >> 4)), da = dQ + (uint64_t)(a * (kQAtom >> 4));
@@ -328,25 +339,25 @@ __device__ __forceinline__ void issue(const PairParams& p, Shared& sh, unsigned 
   };
   Pieces pc;
   int np = 0;
-  for (pc.start(p, g); ok && pc.next(); ++np) {
+  for (pc.start(p, g); ok && uni(pc.next()); ++np) {
     const int Tb = p.T[pc.b];
     ok = wait(&sh.q_full, np & 1);
     if (!ok) break;
     tc_fence_after();
     scores(it);
-    if (ok && pc.lo + 1 == pc.hi) commit_pair(&sh.q_empty, lead);
-    for (int k = pc.lo; k < pc.hi && ok; ++k, ++it) {
-      if (k + 1 < pc.hi) {
+    if (ok && uni(pc.lo + 1 == pc.hi)) commit_pair(&sh.q_empty, lead);
+    for (int k = pc.lo; uni(k < pc.hi) && ok; ++k, ++it) {
+      if (uni(k + 1 < pc.hi)) {
         scores(it + 1);
-        if (ok && k + 2 == pc.hi) commit_pair(&sh.q_empty, lead);  // the piece's last score product
+        if (ok && uni(k + 2 == pc.hi)) commit_pair(&sh.q_empty, lead);  // the piece's last score product
       }
       ok = ok && wait(&sh.p_full, it & 1);
       if (!ok) break;
       tc_fence_after();
       const Tile t = tile_at(Tb, p.S, k);
-      uint32_t keep = k > pc.lo ? 1u : 0u;
-      if (t.keys == kPairTile) {
-#pragma unroll
+      const uint32_t keep = uni(k > pc.lo) ? 1u : 0u;
+      if (uni(t.keys == kPairTile)) {
+#pragma unroll 1
         for (int kc = 0; kc < 4; ++kc) {
 #pragma unroll
           for (int nb = 0; nb < 2; ++nb) {
@@ -359,12 +370,12 @@ __device__ __forceinline__ void issue(const PairParams& p, Shared& sh, unsigned 
           }
         }
       } else {  // a piece's last tiles: whole 16-key steps
-        for (int kc = 0; kc < (t.keys + 63) / 64 && ok; ++kc) {
+        for (int kc = 0; uni(kc < (t.keys + 63) / 64) && ok; ++kc) {
           const int steps = min(4, (t.keys - 64 * kc + 15) / 16);
           for (int nb = 0; nb < 2; ++nb) {
             if (!acquire()) break;
             const uint64_t db = dV + (uint64_t)(s * (kStageBytes >> 4)), da = dP + (uint64_t)(kc * (8192 >> 4));
-            for (int kk = 0; kk < steps; ++kk)
+            for (int kk = 0; uni(kk < steps); ++kk)
               mma_pair(tmem + kColO + 128 * nb, da + 2 * kk, db + 128 * kk, idO, (kc | kk) != 0 ? 1u : keep, lead);
             release();
           }
@@ -656,12 +667,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_pa
 
 }  // namespace
 
+// Chunks of the tile list: G chunks times the node pairs are the items that the
+// clusters take in turn.  More chunks fill the last round of clusters better,
+// and cost a query load, a pipeline fill and a partial each (items about 2
+// tiles of 3.1 us, a node's partial 0.05 us to write and merge).
 int pair_chunks(int B, int S, int T_cap, int sms) {
-  const int np = (S + 1) / 2;
+  const int np = (S + 1) / 2, clusters = sms / 2;
   const long long tiles = (long long)B * pair_tiles(T_cap, S);
-  long long g = sms / 2 / np;
-  if (g < 1) g = 1;
-  return (int)(g < tiles ? g : tiles);
+  int best = 1;
+  double least = 1e30;
+  for (int g = 1; g <= 4 * clusters && g <= tiles; ++g) {
+    const long long rounds = ((long long)g * np + clusters - 1) / clusters;
+    if (g > 1 && rounds > 4) break;
+    const double us = rounds * 3.1 * ((double)tiles / g + 2.0) + 0.05 * (g + B - 1) * S;
+    if (us < least) {
+      least = us;
+      best = g;
+    }
+  }
+  return best;
 }
 
 cudaError_t launch_attn_pair(const PairParams& p, cudaStream_t st) {
