@@ -234,20 +234,25 @@ __device__ __forceinline__ void produce(const PairParams& p, Shared& sh, unsigne
     ++n;
     s = s + 1 == kStages ? 0 : s + 1;
   };
-  auto row_of = [&](int b, int t) -> int {
-    bool bad = false;
-    const int row = (int)cache_row(p.pages, b, p.T_cap, t, &bad);
-    if (bad) raise_flag(p.flags, MLA_DEV_BAD_INDEX);
-    return row;
+  // Source rows of the two 128-key halves of tile k (a half lies in one page).
+  // Looked up a tile ahead: a page table read in the way of the loads would
+  // hold up the ring.
+  struct Rows {
+    int y[2];
   };
-  auto load_k = [&](int b, int Tb, int k) {
+  auto rows_of = [&](int b, int Tb, int k) -> Rows {
     const Tile t = tile_at(Tb, p.S, k);
-    int y = b * kPairStage;
-    if (!t.tail) {
-      int t0 = t.row0 + 128 * (int)rank;
-      if (t0 >= Tb) t0 = t.row0;  // no key of this half: any rows do
-      y = row_of(b, t0);
-    }
+    if (t.tail) return Rows{{b * kPairStage, b * kPairStage}};
+    bool bad = false;
+    Rows r;
+    r.y[0] = (int)cache_row(p.pages, b, p.T_cap, t.row0, &bad);
+    // no key in the second half: its rows are not looked up (any do)
+    r.y[1] = t.row0 + 128 < Tb ? (int)cache_row(p.pages, b, p.T_cap, t.row0 + 128, &bad) : r.y[0];
+    if (bad) raise_flag(p.flags, MLA_DEV_BAD_INDEX);
+    return r;
+  };
+  auto load_k = [&](const Tile& t, const Rows& r) {
+    const int y = r.y[rank];
     const CUtensorMap* lat = t.tail ? &p.mT : &p.mK;
 #pragma unroll 1
     for (int d = 0; d < 9; ++d) {
@@ -257,12 +262,11 @@ __device__ __forceinline__ void produce(const PairParams& p, Shared& sh, unsigne
       advance();
     }
   };
-  auto load_v = [&](int b, int Tb, int k) {
-    const Tile t = tile_at(Tb, p.S, k);
+  auto load_v = [&](const Tile& t, const Rows& r) {
     const CUtensorMap* map = t.tail ? &p.mTv : &p.mV;
 #pragma unroll 1
     for (int kc = 0; uni(kc < (t.keys + 63) / 64); ++kc) {
-      const int y = t.tail ? b * kPairStage + 64 * kc : row_of(b, t.row0 + 64 * kc);
+      const int y = (t.tail || kc < 2 ? r.y[0] : r.y[1] - 128) + 64 * kc;
       for (int nb = 0; nb < 2; ++nb) {  // two 64-latent atoms of 64 keys each
         if (!acquire()) return;
         load_3d(ring0 + s * kStageBytes, map, 0, y, 4 * nb + 2 * (int)rank, full0 + 8 * s, lead);
@@ -281,10 +285,14 @@ __device__ __forceinline__ void produce(const PairParams& p, Shared& sh, unsigne
     const int qrow = (pc.b * p.S + 2 * pair + (int)rank) * kRows;  // past the last node: another row or zeros
     for (int d = 0; d < 9; ++d) load_2d(smem_u32(smem + d * kQAtom), &p.mQ, 64 * d, qrow, qbar, lead);
     ++*q_issued;
-    load_k(pc.b, Tb, pc.lo);
+    Rows r0 = rows_of(pc.b, Tb, pc.lo), r1 = pc.lo + 1 < pc.hi ? rows_of(pc.b, Tb, pc.lo + 1) : r0;
+    load_k(tile_at(Tb, p.S, pc.lo), r0);
     for (int k = pc.lo; uni(k < pc.hi) && ok; ++k) {
-      if (uni(k + 1 < pc.hi)) load_k(pc.b, Tb, k + 1);
-      if (ok) load_v(pc.b, Tb, k);
+      const Rows r2 = k + 2 < pc.hi ? rows_of(pc.b, Tb, k + 2) : r1;
+      if (uni(k + 1 < pc.hi)) load_k(tile_at(Tb, p.S, k + 1), r1);
+      if (ok) load_v(tile_at(Tb, p.S, k), r0);
+      r0 = r1;
+      r1 = r2;
     }
   }
   *issued = n;
