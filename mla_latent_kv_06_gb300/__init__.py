@@ -572,27 +572,36 @@ def cache_append_fp8_paged(comp, kv_a_ln, block_table, T, Lc8_pages, Rc_pages, d
 
 
 # ------------------------------------------------------------- drafted token trees
-def _on_device(device, stream, *named):
-    """The stream handle for a call on `device` (its current stream when none is
-    given) after checking that every (name, tensor, dtype) is a contiguous
-    tensor of that dtype there."""
-    torch = _torch()
-    for name, t, dtype in named:
+def _all_plain(device, dtype, *ts) -> bool:
+    """Every tensor contiguous, of `dtype`, on `device` (the calls below are short: the
+    check that passes is one expression per tensor, _explain finds words for one that fails)."""
+    for t in ts:
+        if t.dtype is not dtype or t.device != device or not t.is_contiguous():
+            return False
+    return True
+
+
+def _explain(device, **named):
+    for name, (t, dtype) in named.items():
         if t.dtype != dtype:
             raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
         if t.device != device:
             raise ValueError(f"{name} is on {t.device}, not on {device}")
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
+
+
+def _stream_on(torch, device, stream):
+    """Stream handle for a call on `device`, which has to be the current one."""
     if device.type != "cuda":
         raise ValueError("tensors must live on the GPU")
-    if device.index != torch.cuda.current_device():
+    if device.index != torch._C._cuda_getDevice():
         raise ValueError(f"tensors on {device}: make it the current device")
-    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _want(name, t, *shape):
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
 
 
@@ -605,44 +614,56 @@ def decode_tree_workspace_size(dims, dtype, B: int, S: int, T_cap: int) -> int:
     return lib().mla_decode_tree_workspace_size(ctypes.byref(d), code, B, S, T_cap)
 
 
-def _tree_args(q, caches, T, parent, kv_b, dims, out, out_dtype, stream, extra=()):
-    """Checks shared by the two tree attentions -> (dims struct, dtype code, out, stream handle)."""
-    torch = _torch()
+def _tree_args(torch, q, Lc, Rc, T, parent, kv_b, dims, out, out_dtype, workspace, T_cap):
+    """Checks shared by the two tree attentions ->
+    (dims struct, dtype code, out, its code, workspace, its bytes)."""
     B, S, H, qk = q.shape
+    dtype, device = q.dtype, q.device
     if H != dims.H or qk != dims.qk_nope + dims.qk_rope:
         raise ValueError(f"q has shape {tuple(q.shape)}, expected [B, S, {dims.H}, {dims.qk_nope + dims.qk_rope}]")
     code = _dtype_code(q)
     if out is None:
-        out = torch.empty(B, S, H, dims.v_head, dtype=out_dtype or torch.float32, device=q.device)
-    elif out_dtype is not None and out.dtype != out_dtype:
-        raise TypeError("out does not have out_dtype")
-    if caches[0].shape[2] != dims.kv_lora or caches[1].shape != caches[0].shape[:2] + (dims.qk_rope,):
+        out = torch.empty((B, S, H, dims.v_head), dtype=out_dtype or torch.float32, device=device)
+    else:
+        if out_dtype is not None and out.dtype != out_dtype:
+            raise TypeError("out does not have out_dtype")
+        _want("out", out, B, S, H, dims.v_head)
+    out_code = _dtype_code(out)
+    ls = Lc.shape
+    if ls[2] != dims.kv_lora or Rc.shape != (ls[0], ls[1], dims.qk_rope):
         raise ValueError("cache shapes do not match dims")
     _want("T", T, B)
     _want("parent", parent, B, S)
     _want("kv_b", kv_b, H, dims.qk_nope + dims.v_head, dims.kv_lora)
-    _want("out", out, B, S, H, dims.v_head)
-    _dtype_code(out)
-    st = _on_device(q.device, stream, ("q", q, q.dtype), ("Lc", caches[0], q.dtype), ("Rc", caches[1], q.dtype),
-                    ("kv_b", kv_b, q.dtype), ("T", T, torch.int32), ("parent", parent, torch.int32),
-                    ("out", out, out.dtype), *extra)
-    return make_dims(dims), code, out, st
+    i32 = torch.int32
+    if not (_all_plain(device, dtype, q, Lc, Rc, kv_b) and _all_plain(device, i32, T, parent)
+            and _all_plain(device, out.dtype, out)):
+        _explain(device, q=(q, dtype), Lc=(Lc, dtype), Rc=(Rc, dtype), kv_b=(kv_b, dtype), T=(T, i32), parent=(parent, i32),
+                 out=(out, out.dtype))
+    d = make_dims(dims)
+    if workspace is None:  # the library checks the size of one that is given
+        workspace, wsb = _workspace(lib().mla_decode_tree_workspace_size(ctypes.byref(d), code, B, S, T_cap), device, None)
+    else:
+        if workspace.device != device or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be contiguous and on {device}")
+        wsb = workspace.numel() * workspace.element_size()
+    return d, code, out, out_code, None if workspace is None else workspace.data_ptr(), wsb
 
 
 def decode_tree(q, Lc, Rc, T, parent, kv_b, dims, out=None, out_dtype=None, workspace=None, stream=None):
     """Absorbed decode of a drafted tree: q [B,S,H,qk] (node s at row T[b]-S+s), parent [B,S]
     int32 (-1 a child of the last committed token, -2 absent).  out [B,S,H,v_head] in
-    out_dtype (float32 unless given; bfloat16 is rounded once)."""
+    out_dtype (float32 unless given; bfloat16 is rounded once).  A workspace that is given
+    must have decode_tree_workspace_size() bytes."""
+    torch = _torch()
     B, S = q.shape[0], q.shape[1]
     T_cap = Lc.shape[1]
-    d, code, out, st = _tree_args(q, (Lc, Rc), T, parent, kv_b, dims, out, out_dtype, stream)
     if Lc.shape[0] != B:
         raise ValueError(f"cache of {Lc.shape[0]} sequences for {B} queries")
-    need = lib().mla_decode_tree_workspace_size(ctypes.byref(d), code, B, S, T_cap)
-    workspace, wsb = _workspace(need, q.device, workspace)
+    d, code, out, out_code, ws, wsb = _tree_args(torch, q, Lc, Rc, T, parent, kv_b, dims, out, out_dtype, workspace, T_cap)
+    st = _stream_on(torch, q.device, stream)
     _check(lib().mla_decode_tree(ctypes.byref(d), code, B, S, q.data_ptr(), Lc.data_ptr(), Rc.data_ptr(), T_cap,
-                                 T.data_ptr(), parent.data_ptr(), kv_b.data_ptr(), _dtype_code(out), out.data_ptr(),
-                                 _ptr(workspace), wsb, st))
+                                 T.data_ptr(), parent.data_ptr(), kv_b.data_ptr(), out_code, out.data_ptr(), ws, wsb, st))
     return out
 
 
@@ -654,39 +675,41 @@ def decode_tree_paged(q, Lc_pages, Rc_pages, block_table, T, parent, kv_b, dims,
     num_pages, page_size = Lc_pages.shape[0], Lc_pages.shape[1]
     max_pages = block_table.shape[1]
     _want("block_table", block_table, B, max_pages)
-    d, code, out, st = _tree_args(q, (Lc_pages, Rc_pages), T, parent, kv_b, dims, out, out_dtype, stream,
-                                  (("block_table", block_table, torch.int32),))
-    need = lib().mla_decode_tree_workspace_size(ctypes.byref(d), code, B, S, max_pages * page_size)
-    workspace, wsb = _workspace(need, q.device, workspace)
+    _explain(q.device, block_table=(block_table, torch.int32))
+    d, code, out, out_code, ws, wsb = _tree_args(torch, q, Lc_pages, Rc_pages, T, parent, kv_b, dims, out, out_dtype, workspace,
+                                       max_pages * page_size)
+    st = _stream_on(torch, q.device, stream)
     _check(lib().mla_decode_tree_paged(ctypes.byref(d), code, B, S, q.data_ptr(), Lc_pages.data_ptr(),
                                        Rc_pages.data_ptr(), num_pages, page_size, block_table.data_ptr(), max_pages,
-                                       T.data_ptr(), parent.data_ptr(), kv_b.data_ptr(), _dtype_code(out),
-                                       out.data_ptr(), _ptr(workspace), wsb, st))
+                                       T.data_ptr(), parent.data_ptr(), kv_b.data_ptr(), out_code, out.data_ptr(), ws,
+                                       wsb, st))
     return out
 
 
-def _append_tree_args(comp, kv_a_ln, T, parent, Lc, Rc, dims, stream, extra=()):
-    torch = _torch()
+def _append_tree_args(torch, comp, kv_a_ln, T, parent, Lc, Rc, dims):
     B, S = comp.shape[0], comp.shape[1]
+    dtype, device, i32 = comp.dtype, comp.device, torch.int32
     _want("comp", comp, B, S, dims.kv_lora + dims.qk_rope)
     _want("kv_a_ln", kv_a_ln, dims.kv_lora)
     _want("T", T, B)
     _want("parent", parent, B, S)
-    if Lc.shape[2] != dims.kv_lora or Rc.shape != Lc.shape[:2] + (dims.qk_rope,):
+    ls = Lc.shape
+    if ls[2] != dims.kv_lora or Rc.shape != (ls[0], ls[1], dims.qk_rope):
         raise ValueError("cache shapes do not match dims")
-    code = _dtype_code(comp)
-    st = _on_device(comp.device, stream, ("comp", comp, comp.dtype), ("kv_a_ln", kv_a_ln, comp.dtype),
-                    ("Lc", Lc, comp.dtype), ("Rc", Rc, comp.dtype), ("T", T, torch.int32),
-                    ("parent", parent, torch.int32), *extra)
-    return B, S, make_dims(dims), code, st
+    if not (_all_plain(device, dtype, comp, kv_a_ln, Lc, Rc) and _all_plain(device, i32, T, parent)):
+        _explain(device, comp=(comp, dtype), kv_a_ln=(kv_a_ln, dtype), Lc=(Lc, dtype), Rc=(Rc, dtype), T=(T, i32),
+                 parent=(parent, i32))
+    return B, S, make_dims(dims), _dtype_code(comp)
 
 
 def cache_append_tree(comp, kv_a_ln, T, parent, Lc, Rc, dims, rms_eps: float, stream=None):
     """cache_append of a drafted tree: node s goes to row T[b]-S+s with the rotary
     position of its depth; rows of absent nodes (parent -2) are left as they were."""
-    B, S, d, code, st = _append_tree_args(comp, kv_a_ln, T, parent, Lc, Rc, dims, stream)
+    torch = _torch()
+    B, S, d, code = _append_tree_args(torch, comp, kv_a_ln, T, parent, Lc, Rc, dims)
     if Lc.shape[0] != B:
         raise ValueError(f"cache of {Lc.shape[0]} sequences for {B} rows")
+    st = _stream_on(torch, comp.device, stream)
     _check(lib().mla_cache_append_tree(ctypes.byref(d), code, B, S, comp.data_ptr(), kv_a_ln.data_ptr(), rms_eps,
                                        Lc.shape[1], T.data_ptr(), parent.data_ptr(), Lc.data_ptr(), Rc.data_ptr(), st))
     return Lc, Rc
@@ -696,9 +719,10 @@ def cache_append_tree_paged(comp, kv_a_ln, block_table, T, parent, Lc_pages, Rc_
                             stream=None):
     """cache_append_tree into the page pools (in place)."""
     torch = _torch()
-    _want("block_table", block_table, comp.shape[0], block_table.shape[1])
-    B, S, d, code, st = _append_tree_args(comp, kv_a_ln, T, parent, Lc_pages, Rc_pages, dims, stream,
-                                          (("block_table", block_table, torch.int32),))
+    B, S, d, code = _append_tree_args(torch, comp, kv_a_ln, T, parent, Lc_pages, Rc_pages, dims)
+    _want("block_table", block_table, B, block_table.shape[1])
+    _explain(comp.device, block_table=(block_table, torch.int32))
+    st = _stream_on(torch, comp.device, stream)
     _check(lib().mla_cache_append_tree_paged(ctypes.byref(d), code, B, S, comp.data_ptr(), kv_a_ln.data_ptr(), rms_eps,
                                              Lc_pages.data_ptr(), Rc_pages.data_ptr(), Lc_pages.shape[0],
                                              Lc_pages.shape[1], block_table.data_ptr(), block_table.shape[1],
@@ -716,35 +740,37 @@ def tree_verify(p, q, tokens, parent, u, path=None, n_acc=None, token=None, stre
     n_acc [B], token [B]), all int32."""
     torch = _torch()
     B, S = tokens.shape
-    V = p.shape[2]
-    for name, x in (("p", p), ("q", q)):
-        if x is None:
-            continue
-        _want(name, x, B, S + 1, V)
-        if x.dtype != torch.float32:
+    V, device = p.shape[2], p.device
+    f32, i32 = torch.float32, torch.int32
+    for name, x in (("p", p),) if q is None else (("p", p), ("q", q)):
+        if x.shape != (B, S + 1, V):
+            raise ValueError(f"{name} has shape {tuple(x.shape)}, expected {(B, S + 1, V)}")
+        if x.dtype is not f32:
             raise TypeError(f"{name} must be torch.float32, got {x.dtype}")
         if x.stride(2) != 1 and V > 1:
             raise ValueError(f"the values of a row of {name} must be contiguous")
-        if x.device != p.device:
-            raise ValueError(f"{name} is on {x.device}, not on {p.device}")
+        if x.device != device:
+            raise ValueError(f"{name} is on {x.device}, not on {device}")
     _want("parent", parent, B, S)
     _want("u", u, B, S + 1)
+    if not (_all_plain(device, i32, tokens, parent) and _all_plain(device, f32, u)):
+        _explain(device, tokens=(tokens, i32), parent=(parent, i32), u=(u, f32))
     if path is None:
-        path = torch.empty(B, S, dtype=torch.int32, device=p.device)
+        path = torch.empty((B, S), dtype=i32, device=device)
     if n_acc is None:
-        n_acc = torch.empty(B, dtype=torch.int32, device=p.device)
+        n_acc = torch.empty(B, dtype=i32, device=device)
     if token is None:
-        token = torch.empty(B, dtype=torch.int32, device=p.device)
+        token = torch.empty(B, dtype=i32, device=device)
     _want("path", path, B, S)
     _want("n_acc", n_acc, B)
     _want("token", token, B)
-    i32 = torch.int32
-    st = _on_device(p.device, stream, ("tokens", tokens, i32), ("parent", parent, i32), ("u", u, torch.float32),
-                    ("path", path, i32), ("n_acc", n_acc, i32), ("token", token, i32))
-    _check(lib().mla_tree_verify(B, S, V, p.data_ptr(), p.stride(1), p.stride(0),
-                                 None if q is None else q.data_ptr(), 0 if q is None else q.stride(1),
-                                 0 if q is None else q.stride(0), tokens.data_ptr(), parent.data_ptr(), u.data_ptr(),
-                                 path.data_ptr(), n_acc.data_ptr(), token.data_ptr(), st))
+    if not _all_plain(device, i32, path, n_acc, token):
+        _explain(device, path=(path, i32), n_acc=(n_acc, i32), token=(token, i32))
+    st = _stream_on(torch, device, stream)
+    qp, qr, qb = (None, 0, 0) if q is None else (q.data_ptr(), q.stride(1), q.stride(0))
+    _check(lib().mla_tree_verify(B, S, V, p.data_ptr(), p.stride(1), p.stride(0), qp, qr, qb, tokens.data_ptr(),
+                                 parent.data_ptr(), u.data_ptr(), path.data_ptr(), n_acc.data_ptr(), token.data_ptr(),
+                                 st))
     return path, n_acc, token
 
 
@@ -770,7 +796,10 @@ class CacheRows:
         if block_table is not None:
             if block_table.dtype != torch.int32 or block_table.device != self.device or not block_table.is_contiguous():
                 raise ValueError("block_table must be a contiguous int32 tensor on the caches' GPU")
+            if block_table.dim() != 2:
+                raise ValueError("block_table must be [B, max_pages]")
         self.B = first.shape[0] if block_table is None else block_table.shape[0]
+        self.rows, self.cap = first.shape[0], first.shape[1]
         n = len(self.caches)
         self.n = n
         self.pointers = (ctypes.c_void_p * n)(*[c.data_ptr() for c in self.caches])
@@ -782,22 +811,24 @@ def tree_commit(rows: CacheRows, T, path, n_acc, T_out=None, stream=None):
     tree's rows in every cache of `rows`; returns T_out [B] int32 = T - S + n_acc."""
     torch = _torch()
     B, S = path.shape
+    device, i32 = rows.device, torch.int32
     if B != rows.B:
         raise ValueError(f"caches of {rows.B} sequences, path of {B}")
     if T_out is None:
-        T_out = torch.empty(B, dtype=torch.int32, device=path.device)
+        T_out = torch.empty(B, dtype=i32, device=device)
     _want("T", T, B)
     _want("n_acc", n_acc, B)
     _want("T_out", T_out, B)
-    i32 = torch.int32
-    st = _on_device(rows.device, stream, ("T", T, i32), ("path", path, i32), ("n_acc", n_acc, i32), ("T_out", T_out, i32))
-    first = rows.caches[0]
-    if rows.block_table is None:
-        rc = lib().mla_tree_commit(rows.n, rows.pointers, rows.row_bytes, B, S, first.shape[1], T.data_ptr(),
-                                   path.data_ptr(), n_acc.data_ptr(), T_out.data_ptr(), st)
+    if not _all_plain(device, i32, T, path, n_acc, T_out):
+        _explain(device, T=(T, i32), path=(path, i32), n_acc=(n_acc, i32), T_out=(T_out, i32))
+    st = _stream_on(torch, device, stream)
+    table = rows.block_table
+    if table is None:
+        rc = lib().mla_tree_commit(rows.n, rows.pointers, rows.row_bytes, B, S, rows.cap, T.data_ptr(), path.data_ptr(),
+                                   n_acc.data_ptr(), T_out.data_ptr(), st)
     else:
-        rc = lib().mla_tree_commit_paged(rows.n, rows.pointers, rows.row_bytes, B, S, first.shape[0], first.shape[1],
-                                         rows.block_table.data_ptr(), rows.block_table.shape[1], T.data_ptr(),
-                                         path.data_ptr(), n_acc.data_ptr(), T_out.data_ptr(), st)
+        rc = lib().mla_tree_commit_paged(rows.n, rows.pointers, rows.row_bytes, B, S, rows.rows, rows.cap,
+                                         table.data_ptr(), table.shape[1], T.data_ptr(), path.data_ptr(),
+                                         n_acc.data_ptr(), T_out.data_ptr(), st)
     _check(rc)
     return T_out
