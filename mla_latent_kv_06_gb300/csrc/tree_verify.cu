@@ -21,7 +21,6 @@
 
 #include "common.cuh"
 #include "internal.h"
-#include "tree.cuh"
 
 namespace mla {
 namespace {
@@ -31,7 +30,6 @@ namespace cg = cooperative_groups;
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kCluster = 8;
-constexpr int kStep = 128;  // elements of one warp step: 4 consecutive ones per lane
 
 struct Pair {
   float hi, lo;
@@ -71,117 +69,128 @@ __device__ __forceinline__ Pair left(float p, float q, float ch, float cl) {
   return Pair{pos ? s : (s + lo != s + lo ? s : 0.f), pos ? lo : 0.f};
 }
 
+// What the warps do next: sum W at context `at`, or draw from it.
+struct Command {
+  int at;
+  float ch, cl;                // c as a pair
+  int draft;                   // q enters (a rejection has happened)
+  unsigned long long removed;  // point drafts: rejected nodes of this context
+  int done;
+};
+
 struct Shared {
   // node data, filled by rank 0 and copied by the others
   int parent[kMaxTree], token[kMaxTree];
   float u[kMaxTree + 1], pt[kMaxTree], qt[kMaxTree];
-  double part[2][kCluster];  // slice totals of every CTA, alternating between passes
+  unsigned long long kids[kMaxTree + 1];  // children of every context
+  double part[2][kCluster];               // slice totals of every CTA, alternating between passes
   double warp_sum[kWarps];
-  int removed[kMaxTree];
+  Command cmd;
+  int bad[kMaxTree], up[kMaxTree];
+  int find_warp;
+  double find_t;
 };
 
-// Row segment of one warp: elements [lo, hi) of the vocabulary.
+// Segment of the vocabulary, in elements, and the weights there.
 struct Segment {
   const float* p;
   const float* q;  // null: point drafts, or no rejection yet
   int lo, hi;
   float ch, cl;
-  const int* removed;
-  int nremoved;  // removed tokens inside this segment are looked up when > 0
+  const int* token;            // of the nodes
+  unsigned long long removed;  // nodes whose token is removed and lies inside the segment
 };
 
 __device__ __forceinline__ Pair element(const Segment& g, int i, float p, float q) {
   if (g.q) return left(p, q, g.ch, g.cl);
   Pair v{p > 0.f || p != p ? p : 0.f, 0.f};
-  for (int k = 0; k < g.nremoved; ++k)
-    if (g.removed[k] == i) v.hi = 0.f;
+  for (unsigned long long m = g.removed; m; m &= m - 1)
+    if (g.token[__ffsll((long long)m) - 1] == i) v.hi = 0.f;
   return v;
 }
 
-// Lane's 4 elements of the step that starts at i0 (zeros past the end).
-__device__ __forceinline__ void load4(const Segment& g, int i0, int lane, float (&p)[4], float (&q)[4]) {
+// Nodes of `removed` whose token lies in [lo, hi) (the whole warp calls it).
+__device__ __forceinline__ unsigned long long removed_inside(const Shared& sh, unsigned long long removed, int lo, int hi) {
+  if (!removed) return 0;
+  const int lane = threadIdx.x & 31;
+  unsigned long long got = 0;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int i = i0 + 4 * lane + k;
-    p[k] = i < g.hi ? __ldg(g.p + i) : 0.f;
-    q[k] = g.q && i < g.hi ? __ldg(g.q + i) : 0.f;
+  for (int half = 0; half < 2; ++half) {
+    const int s = 32 * half + lane;
+    const bool in = ((removed >> s) & 1ull) && sh.token[s] >= lo && sh.token[s] < hi;
+    got |= (unsigned long long)__ballot_sync(0xffffffffu, in) << (32 * half);
   }
+  return got;
 }
 
+// Sum of W over the segment; the warp reads 32 consecutive elements at a time,
+// kAhead of them (of p and of q) in flight.
+constexpr int kAhead = 8;
 __device__ __forceinline__ Pair segment_sum(const Segment& g, int lane) {
   Pair acc{0.f, 0.f};
-#pragma unroll 2
-  for (int i0 = g.lo; i0 < g.hi; i0 += kStep) {
-    float p[4], q[4];
-    load4(g, i0, lane, p, q);
+  for (int i0 = g.lo; i0 < g.hi; i0 += 32 * kAhead) {
+    float p[kAhead], q[kAhead];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const Pair v = element(g, i0 + 4 * lane + k, p[k], q[k]);
+    for (int k = 0; k < kAhead; ++k) {
+      const int i = i0 + 32 * k + lane;
+      p[k] = i < g.hi ? __ldg(g.p + i) : 0.f;
+      q[k] = g.q && i < g.hi ? __ldg(g.q + i) : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const Pair v = element(g, i0 + 32 * k + lane, p[k], q[k]);
       add(acc, v.hi, v.lo);
     }
   }
   return warp_total(acc);
 }
 
-// First index whose cumulative weight inside the segment exceeds t, else the last one of positive weight.
+// First index of the segment (at most 32 elements a step) whose cumulative
+// weight exceeds t, else the last one of positive weight; -1: none.
 __device__ int segment_find(const Segment& g, double t, int lane) {
   double before = 0.0;
   int last = -1;
-  for (int i0 = g.lo; i0 < g.hi; i0 += kStep) {
-    float p[4], q[4];
-    load4(g, i0, lane, p, q);
-    double w[4], mine = 0.0;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      w[k] = value(element(g, i0 + 4 * lane + k, p[k], q[k]));
-      mine += w[k];
-    }
-    double incl = mine;
+  for (int i0 = g.lo; i0 < g.hi; i0 += 32) {
+    const int i = i0 + lane;
+    const float p = i < g.hi ? __ldg(g.p + i) : 0.f, q = g.q && i < g.hi ? __ldg(g.q + i) : 0.f;
+    const double w = value(element(g, i, p, q));
+    double incl = w;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const double up = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += up;
     }
-    const unsigned over = __ballot_sync(0xffffffffu, before + incl > t);
-    const unsigned some = __ballot_sync(0xffffffffu, mine > 0.0);
-    const int pick = over ? __ffs(over) - 1 : some ? 31 - __clz(some) : -1;
-    if (pick >= 0) {
-      int at = -1, lastpos = -1;
-      double c = before + incl - mine;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        c += w[k];
-        if (w[k] > 0.0) lastpos = i0 + 4 * lane + k;
-        if (at < 0 && c > t && w[k] > 0.0) at = i0 + 4 * lane + k;
-      }
-      // rounding may leave the lane's own sums at t: then its last positive one
-      if (at < 0) at = lastpos;
-      at = __shfl_sync(0xffffffffu, at, pick);
-      if (over && at >= 0) return at;
-      if (at >= 0) last = at;
-    }
+    const unsigned over = __ballot_sync(0xffffffffu, w > 0.0 && before + incl > t);
+    const unsigned some = __ballot_sync(0xffffffffu, w > 0.0);
+    if (over) return i0 + __ffs(over) - 1;
+    if (some) last = i0 + 31 - __clz(some);
     before += __shfl_sync(0xffffffffu, incl, 31);
   }
   return last;
 }
 
-// Index of the first of n totals at which the running sum exceeds *t (then *t
-// is reduced by the sum before it), else of the last positive one; -1: none.
-__device__ int pick_part(const double* part, int n, double* t) {
-  double c = 0.0, at = 0.0;
-  int last = -1;
-  for (int i = 0; i < n; ++i) {
-    if (part[i] > 0.0) {
-      last = i;
-      at = c;
-    }
-    c += part[i];
-    if (part[i] > 0.0 && c > *t) break;
+// Index of the first of n <= 32 totals (one per lane, 0 beyond n) at which the
+// running sum exceeds *t (then *t is reduced by the sum before it), else of
+// the last positive one; -1: none.  The whole warp calls it.
+__device__ __forceinline__ int pick_part(double mine, double* t) {
+  const int lane = threadIdx.x & 31;
+  double incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const double up = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += up;
   }
-  *t -= at;
-  return last;
+  const unsigned over = __ballot_sync(0xffffffffu, mine > 0.0 && incl > *t);
+  const unsigned some = __ballot_sync(0xffffffffu, mine > 0.0);
+  const int at = over ? __ffs(over) - 1 : some ? 31 - __clz(some) : -1;
+  if (at >= 0) *t -= __shfl_sync(0xffffffffu, incl - mine, at);
+  return at;
 }
 
+// The decisions (doubles: few, and made by one warp only, since all threads
+// together would queue at the fp64 pipe) sit in warp 0 of every CTA; the other
+// warps take its commands.  CTAs of a cluster reach the same decisions from
+// the same numbers: rank 0's copy of the node data and the exchanged totals.
 __global__ void __launch_bounds__(kThreads) tree_verify_kernel(const VerifyArgs a) {
   __shared__ Shared sh;
   cg::cluster_group cluster = cg::this_cluster();
@@ -191,23 +200,44 @@ __global__ void __launch_bounds__(kThreads) tree_verify_kernel(const VerifyArgs 
   const float* p0 = a.p + (long long)b * a.p_batch;
   const float* q0 = a.q ? a.q + (long long)b * a.q_batch : nullptr;
 
-  // Rank 0 reads the nodes; the cluster's CTAs take them from its shared
-  // memory, so that all of them walk the same tree whatever else happens.
-  if (rank == 0 && tid <= S) {
-    sh.u[tid] = a.u[(size_t)b * (S + 1) + tid];
+  if (rank == 0) {
+    if (tid <= S) sh.u[tid] = a.u[(size_t)b * (S + 1) + tid];
+    int up = -2, x = 0;
+    bool bad = false;
     if (tid < S) {
-      const TreeNode node = tree_node(a.parent + (size_t)b * S, tid);
-      int up = node.state == kNodePresent ? a.parent[(size_t)b * S + tid] : -2;
-      const int x = a.tokens[(size_t)b * S + tid];
-      const bool bad = node.state == kNodeBad || (up >= -1 && (x < 0 || x >= V));
-      if (bad) {
-        raise_flag(a.flags, MLA_DEV_BAD_INDEX);
-        up = -2;
-      }
-      sh.parent[tid] = up;
+      up = a.parent[(size_t)b * S + tid];
+      x = a.tokens[(size_t)b * S + tid];
+      bad = up < -2 || up >= tid || (up > -2 && (x < 0 || x >= V));
+      const bool read = up > -2 && !bad;
       sh.token[tid] = x;
-      sh.pt[tid] = up >= -1 ? p0[(long long)(up + 1) * a.p_row + x] : 0.f;
-      sh.qt[tid] = up >= -1 && q0 ? q0[(long long)(up + 1) * a.q_row + x] : 0.f;
+      sh.pt[tid] = read ? p0[(long long)(up + 1) * a.p_row + x] : 0.f;
+      sh.qt[tid] = read && q0 ? q0[(long long)(up + 1) * a.q_row + x] : 0.f;
+      sh.bad[tid] = bad;
+      sh.up[tid] = bad ? -2 : up;
+    }
+    __syncthreads();
+    // a node below an absent or bad one is bad: follow the parents by doubling
+    if (tid < kMaxTree) {
+      int far = tid < S && up >= 0 && !bad ? up : -1;
+      for (int r = 0; r < 6; ++r) {
+        const bool gone = far >= 0 && (sh.bad[far] || sh.up[far] == -2);
+        const int next = far >= 0 ? sh.up[far] : -1;
+        __syncwarp();
+        asm volatile("bar.sync 1, 64;" ::: "memory");
+        bad = bad || gone;
+        if (tid < S) {
+          sh.bad[tid] = bad;
+          // (an absent ancestor is found before it is followed)
+          sh.up[tid] = up == -2 || bad ? -2 : next;
+        }
+        far = next;
+        __syncwarp();
+        asm volatile("bar.sync 1, 64;" ::: "memory");
+      }
+      if (tid < S) {
+        if (bad) raise_flag(a.flags, MLA_DEV_BAD_INDEX);
+        sh.parent[tid] = bad ? -2 : up;
+      }
     }
   }
   cluster.sync();
@@ -223,102 +253,144 @@ __global__ void __launch_bounds__(kThreads) tree_verify_kernel(const VerifyArgs 
       }
     }
   }
+  if (tid <= kMaxTree) sh.kids[tid] = 0;
+  __syncthreads();
+  if (tid < S && sh.parent[tid] >= -1) atomicOr(&sh.kids[sh.parent[tid] + 1], 1ull << tid);
   __syncthreads();
 
-  // vocabulary slice of the CTA and segment of the warp, in whole warp steps
-  const int steps = (V + kStep - 1) / kStep;
-  const int per = (steps + kCluster * kWarps - 1) / (kCluster * kWarps);
+  // vocabulary segment of the warp, in whole groups of 32 elements
+  const int groups = (V + 31) / 32;
+  const int per = (groups + kCluster * kWarps - 1) / (kCluster * kWarps);
   Segment seg{};
-  seg.lo = min((rank * kWarps + warp) * per, steps) * kStep;
-  seg.hi = min(min((rank * kWarps + warp + 1) * per, steps) * kStep, V);
+  seg.token = sh.token;
+  seg.lo = min((rank * kWarps + warp) * per, groups) * 32;
+  seg.hi = min(min((rank * kWarps + warp + 1) * per, groups) * 32, V);
 
-  int pass = 0;
-  // Sum of W at context `at`; every thread of the cluster gets the same value.
-  // The warps' and CTAs' totals stay in sh for the draw.
-  auto total = [&](int at, double c, int nremoved) -> double {
-    seg.p = p0 + (long long)at * a.p_row;
-    seg.q = q0 && c != 0.0 ? q0 + (long long)at * a.q_row : nullptr;  // W = p before any rejection
-    seg.ch = (float)c;
-    seg.cl = (float)(c - (double)seg.ch);
-    seg.removed = sh.removed;
-    int inside = 0;
-    for (int k = 0; k < nremoved; ++k) inside |= sh.removed[k] >= seg.lo && sh.removed[k] < seg.hi;
-    seg.nremoved = inside ? nremoved : 0;
+  int at = 0, n = 0, pass = 0;
+  unsigned long long kids = sh.kids[0], removed = 0;
+  double c = 0.0, mass = 1.0, z = 0.0;
+  bool stale = false;  // mass not yet formed after a rejection
+  bool drawing = false, fallback = false;
+  for (;;) {
+    if (warp == 0) {
+      // walk until a sum is needed
+      while (!drawing) {
+        if (!kids) {
+          drawing = true;
+          break;
+        }
+        if (stale) break;  // another child of this context: its test needs the mass
+        const int s = __ffsll((long long)kids) - 1;
+        kids &= kids - 1;
+        double w = sh.pt[s], chance = sh.u[s];
+        if (q0) {
+          w = w - c * (double)sh.qt[s];
+          if (w < 0.0) w = 0.0;
+          chance = chance * (double)sh.qt[s] * mass;
+        } else {
+          for (unsigned long long m = removed; m; m &= m - 1)
+            if (sh.token[__ffsll((long long)m) - 1] == sh.token[s]) w = 0.0;
+          chance = chance * mass;
+        }
+        if (chance < w) {
+          if (rank == 0 && lane == 0) a.path[(size_t)b * S + n] = s;
+          ++n;
+          at = s + 1;
+          kids = sh.kids[at];
+          c = 0.0;
+          mass = 1.0;
+          removed = 0;
+        } else if (q0) {
+          c += mass;
+          stale = true;
+        } else {
+          mass = mass > w ? mass - w : 0.0;
+          removed |= 1ull << s;
+        }
+      }
+      if (lane == 0) {
+        const float ch = (float)c;
+        sh.cmd = Command{at, ch, (float)(c - (double)ch), q0 && c != 0.0 ? 1 : 0, removed, 0};
+      }
+    }
+    __syncthreads();
+    const Command cmd = sh.cmd;
+    if (cmd.done) break;
+    seg.p = p0 + (long long)cmd.at * a.p_row;
+    seg.q = cmd.draft ? q0 + (long long)cmd.at * a.q_row : nullptr;  // W = p before any rejection
+    seg.ch = cmd.ch;
+    seg.cl = cmd.cl;
+    seg.removed = removed_inside(sh, cmd.removed, seg.lo, seg.hi);
     const Pair s = segment_sum(seg, lane);
     if (lane == 0) sh.warp_sum[warp] = value(s);
     __syncthreads();
     if (warp == 0) {
-      double mine = 0.0;
-      for (int w = 0; w < kWarps; ++w) mine += sh.warp_sum[w];
+      double mine = lane < kWarps ? sh.warp_sum[lane] : 0.0;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
       if (lane < kCluster) cluster.map_shared_rank(&sh, lane)->part[pass & 1][rank] = mine;
     }
     cluster.sync();
-    double z = 0.0;
-    for (int r = 0; r < kCluster; ++r) z += sh.part[pass & 1][r];
-    ++pass;
-    return z;
-  };
-
-  int at = 0, n = 0, nremoved = 0;
-  double c = 0.0, mass = 1.0;
-  bool stale = false;  // mass not yet formed after a rejection
-  for (int s = 0; s < S; ++s) {
-    if (sh.parent[s] != at - 1) continue;
-    const int x = sh.token[s];
-    double w = sh.pt[s], chance = sh.u[s];
-    if (q0) {
-      if (stale) {
-        mass = total(at, c, 0);
+    if (warp == 0) {
+      z = lane < kCluster ? sh.part[pass & 1][lane] : 0.0;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+      if (!drawing) {
+        mass = z;
         stale = false;
+      } else if (!(z > 0.0) && z == z && !fallback && (c != 0.0 || removed)) {
+        fallback = true;  // nothing left: the target's own distribution
+        c = 0.0;
+        removed = 0;
+      } else {
+        if (lane == 0) sh.cmd.done = 1;
+        // which CTA, then which warp, the draw falls to
+        double t = (double)sh.u[S] * z;
+        int hit = -1;
+        if (z > 0.0 && z < 1e300) {
+          hit = pick_part(lane < kCluster ? sh.part[pass & 1][lane] : 0.0, &t);
+          hit = hit == rank ? pick_part(lane < kWarps ? sh.warp_sum[lane] : 0.0, &t) : -1;
+        } else if (rank == 0 && lane == 0) {  // an empty or non-finite distribution
+          raise_flag(a.flags, MLA_DEV_BAD_VALUE);
+          a.token[b] = -1;
+        }
+        if (lane == 0) {
+          sh.find_warp = hit;
+          sh.find_t = t;
+        }
+        drawing = true;
       }
-      w = w - c * (double)sh.qt[s];
-      if (w < 0.0) w = 0.0;
-      chance = chance * (double)sh.qt[s] * mass;
-    } else {
-      for (int k = 0; k < nremoved; ++k)
-        if (sh.removed[k] == x) w = 0.0;
-      chance = chance * mass;
     }
-    if (chance < w) {
-      if (rank == 0 && tid == 0) a.path[(size_t)b * S + n] = s;
-      ++n;
-      at = s + 1;
-      c = 0.0;
-      mass = 1.0;
-      stale = false;
-      nremoved = 0;
-    } else if (q0) {
-      c += mass;
-      stale = true;
-    } else {
-      mass = mass > w ? mass - w : 0.0;
-      __syncthreads();  // the list below is read by the passes and the tests above
-      if (tid == 0) sh.removed[nremoved] = x;
-      __syncthreads();
-      ++nremoved;
+    ++pass;
+    __syncthreads();
+    if (sh.cmd.done) break;
+  }
+  if (rank == 0 && warp == 0) {
+    for (int i = n + lane; i < S; i += 32) a.path[(size_t)b * S + i] = -1;
+    if (lane == 0) a.n_acc[b] = n;
+  }
+  // The warp's segment again, split over the CTA's warps.
+  const int hit = sh.find_warp;
+  if (hit < 0) return;
+  const int hlo = min((rank * kWarps + hit) * per, groups) * 32, hhi = min(min((rank * kWarps + hit + 1) * per, groups) * 32, V);
+  const int sub = (per + kWarps - 1) / kWarps;  // groups of 32 per warp
+  seg.lo = min(hlo + 32 * sub * warp, hhi);
+  seg.hi = min(hlo + 32 * sub * (warp + 1), hhi);
+  seg.removed = removed_inside(sh, sh.cmd.removed, seg.lo, seg.hi);
+  const Pair part = segment_sum(seg, lane);
+  if (lane == 0) sh.warp_sum[warp] = value(part);
+  __syncthreads();
+  if (warp == 0) {
+    double t = sh.find_t;
+    const int w = pick_part(lane < kWarps ? sh.warp_sum[lane] : 0.0, &t);
+    if (lane == 0) {
+      sh.find_warp = w;
+      sh.find_t = t;
     }
   }
-  if (rank == 0) {
-    for (int i = n + tid; i < S; i += kThreads) a.path[(size_t)b * S + i] = -1;
-    if (tid == 0) a.n_acc[b] = n;
-  }
-
-  double z = total(at, c, nremoved);
-  if (!(z > 0.0) && z == z) {  // nothing left: the target's own distribution
-    c = 0.0;
-    z = total(at, 0.0, 0);
-  }
-  if (!(z > 0.0) || !(z < 1e300)) {  // an empty or non-finite distribution
-    if (rank == 0 && tid == 0) {
-      raise_flag(a.flags, MLA_DEV_BAD_VALUE);
-      a.token[b] = -1;
-    }
-    return;
-  }
-  double t = (double)sh.u[S] * z;
-  if (pick_part(sh.part[(pass - 1) & 1], kCluster, &t) != rank) return;
-  if (pick_part(sh.warp_sum, kWarps, &t) != warp) return;
-  const int x = segment_find(seg, t, lane);
+  __syncthreads();
+  if (sh.find_warp != warp) return;
+  const int x = segment_find(seg, sh.find_t, lane);
   if (lane == 0) a.token[b] = x;
 }
 
