@@ -450,8 +450,7 @@ int dsa_index_key_append(int B, int S, int index_hd, int rope_dim, const float* 
  * pools); FP8 caches are not served.  The arithmetic is theirs as well; bf16
  * output is rounded once from the float result.
  *   workspace: mla_decode_tree_workspace_size() bytes, 256-byte aligned (the
- *              paged call takes T_cap = max_pages * page_size); 0 for the
- *              CUDA-core path
+ *              paged call takes T_cap = max_pages * page_size); may be 0
  * Errors: as mla_decode_absorbed; S > 64 returns MLA_ERR_UNSUPPORTED. */
 size_t mla_decode_tree_workspace_size(const mla_dims* d, int dtype, int B, int S, int T_cap);
 int mla_decode_tree(const mla_dims* d, int dtype, int B, int S, const void* q, const void* Lc, const void* Rc,

@@ -183,6 +183,13 @@ int run_decode(mla::DecodeArgs& a, int dtype, bool sparse, void* workspace, size
       return fail(MLA_ERR_INVALID, "workspace must be 256-byte aligned");
     e = sparse ? mla::launch_sparse_decode_tc(a, workspace, workspace_bytes, st)
                : mla::launch_decode_tc(a, workspace, workspace_bytes, st);
+  } else if (a.parent && mla::tree_simt_ok(a.g, a.B)) {
+    const size_t need = mla::tree_simt_workspace_bytes(a.g, a.B, a.S, a.T_cap);
+    if (need && (!workspace || workspace_bytes < need))
+      return fail(MLA_ERR_INVALID, "workspace of %zu bytes < %zu required", workspace_bytes, need);
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u)
+      return fail(MLA_ERR_INVALID, "workspace must be 256-byte aligned");
+    e = mla::launch_tree_simt(a, dtype, workspace, st);
   } else {
     mla::kernel_mark(st, sparse ? "sparse_decode_simt" : "decode_simt");
     e = mla::launch_decode_simt(a, dtype, sparse, st);
@@ -913,9 +920,12 @@ int run_commit(mla::CommitArgs& a, int n, void* const* cache, const int* row_byt
 MLA_EXPORT size_t mla_decode_tree_workspace_size(const mla_dims* d, int dtype, int B, int S, int T_cap) {
   mla::Geometry g;
   if (!resolve(d, &g) || B < 1 || S < 1 || S > mla::kMaxTree || T_cap < S) return 0;
+  size_t tc = 0;
   if (dtype == MLA_BF16 && mla::tc_decode_geometry_ok(g))
-    return round256(mla::tc_decode_workspace_bytes(g, B, S, T_cap, /*sparse_topk=*/0, /*tree=*/true));
-  return 0;
+    tc = round256(mla::tc_decode_workspace_bytes(g, B, S, T_cap, /*sparse_topk=*/0, /*tree=*/true));
+  // the CUDA-core path takes over for page sizes and addresses the tensor-core path does not serve
+  const size_t simt = mla::tree_simt_ok(g, B) ? round256(mla::tree_simt_workspace_bytes(g, B, S, T_cap)) : 0;
+  return tc > simt ? tc : simt;
 }
 
 MLA_EXPORT int mla_decode_tree(const mla_dims* d, int dtype, int B, int S, const void* q, const void* Lc,

@@ -161,6 +161,11 @@ struct KeyAppendArgs {
 };
 cudaError_t launch_index_key_append(const KeyAppendArgs& a, cudaStream_t st);
 
+// CUDA-core tree attention (kv_lora up to 512; other shapes take launch_decode_simt).
+bool tree_simt_ok(const Geometry& g, int B);
+size_t tree_simt_workspace_bytes(const Geometry& g, int B, int S, int T_cap);
+cudaError_t launch_tree_simt(const DecodeArgs& a, int dtype, void* ws, cudaStream_t st);
+
 // Largest drafted tree: its ancestor masks are 64-bit words.
 constexpr int kMaxTree = 64;
 

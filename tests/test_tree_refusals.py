@@ -35,7 +35,8 @@ def test_decode_tree(lib):
     assert lib.mla_decode_tree_workspace_size(ctypes.byref(GLM_D), 1, 1, 65, 100) == 0
     assert lib.mla_decode_tree_workspace_size(ctypes.byref(GLM_D), 1, 1, 8, 100) > 0
     tiny = mla.MlaDims(4, 16, 8, 32, 16, 0.0, 0.0)
-    assert lib.mla_decode_tree_workspace_size(ctypes.byref(tiny), 0, 1, 8, 100) == 0
+    assert lib.mla_decode_tree_workspace_size(ctypes.byref(tiny), 0, 1, 4, 64) == 0      # one split of the keys
+    assert lib.mla_decode_tree_workspace_size(ctypes.byref(tiny), 0, 1, 8, 100000) > 0   # several
 
 
 def test_append_tree(lib):
