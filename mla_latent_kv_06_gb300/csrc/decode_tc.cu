@@ -1393,16 +1393,10 @@ struct MergeParams {
   __nv_bfloat16* clat;  // [R, 64, 512]
   float* inv_l;         // [R, 64]
   int B, S, G, sparse;
-  const int32_t* parent;  // tree attention: [B, S] parent indices, else null
-  int pair;               // partials of the pair attention: tile_start counts its tiles
 };
 
 constexpr int kMergeBatch = 2;  // splits whose partials are loaded together
 
-// kSplit: clat rows are [R, 64, 1024], the bf16 value and then the bf16 of what
-// its rounding left, for a GEMM with K = 1024 that meets W_UV twice: rounding
-// the context once to bf16 would add 2^-9 to an output that is itself rounded.
-template <bool kSplit>
 __global__ void __launch_bounds__(256, 3) merge_kernel(const MergeParams p) {
   grid_dep_wait();
   grid_dep_launch();
@@ -1414,17 +1408,11 @@ __global__ void __launch_bounds__(256, 3) merge_kernel(const MergeParams p) {
   const int row = p.sparse ? r : b;
   const int NR = p.sparse ? R : p.B;
   const long long N = p.tile_start[NR];
-  __nv_bfloat16* dst = p.clat + ((size_t)r * kH + h) * (kSplit ? 2 * kDl : kDl) + 16 * lane;
-  const int state = p.parent ? tree_node(p.parent + (size_t)b * p.S, s).state : kNodePresent;
-  if (p.bad[row] || N <= 0 || state != kNodePresent) {
+  __nv_bfloat16* dst = p.clat + ((size_t)r * kH + h) * kDl + 16 * lane;
+  if (p.bad[row] || N <= 0) {
     *reinterpret_cast<uint4*>(dst) = make_uint4(0, 0, 0, 0);
     *reinterpret_cast<uint4*>(dst + 8) = make_uint4(0, 0, 0, 0);
-    if (kSplit) {
-      *reinterpret_cast<uint4*>(dst + kDl) = make_uint4(0, 0, 0, 0);
-      *reinterpret_cast<uint4*>(dst + kDl + 8) = make_uint4(0, 0, 0, 0);
-    }
-    // an absent node's output is zero
-    if (lane == 0) p.inv_l[(size_t)r * kH + h] = (p.bad[row] || N <= 0 || state == kNodeBad) ? qnan() : 1.f;
+    if (lane == 0) p.inv_l[(size_t)r * kH + h] = qnan();
     return;
   }
   const long long a = p.tile_start[row], e = p.tile_start[row + 1];
@@ -1435,8 +1423,8 @@ __global__ void __launch_bounds__(256, 3) merge_kernel(const MergeParams p) {
   float L = 0.f;
   auto slot_of = [&](int gg) -> int {  // the split of chunk gg, or -1 when the chunk has no tile of this row
     int lo, hi;
-    if (p.sparse || p.pair) piece_range<true>(p.tile_start, p.T, p.S, s, row, gg, p.G, N, &lo, &hi);
-    else piece_range<false>(p.tile_start, p.T, p.S, p.parent ? p.S - 1 : s, row, gg, p.G, N, &lo, &hi);
+    if (p.sparse) piece_range<true>(p.tile_start, p.T, p.S, s, row, gg, p.G, N, &lo, &hi);
+    else piece_range<false>(p.tile_start, p.T, p.S, s, row, gg, p.G, N, &lo, &hi);
     if (lo >= hi) return -1;
     return p.sparse ? gg + row : (gg + row) * p.S + s;
   };
@@ -1518,18 +1506,114 @@ __global__ void __launch_bounds__(256, 3) merge_kernel(const MergeParams p) {
   w1.w = pack2(acc[14] * il, acc[15] * il);
   *reinterpret_cast<uint4*>(dst) = w0;
   *reinterpret_cast<uint4*>(dst + 8) = w1;
-  if (kSplit) {
-    uint32_t lo[8];
-    const uint32_t hi[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&hi[i]));
-      lo[i] = pack2(acc[2 * i] * il - f.x, acc[2 * i + 1] * il - f.y);
-    }
-    *reinterpret_cast<uint4*>(dst + kDl) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-    *reinterpret_cast<uint4*>(dst + kDl + 8) = make_uint4(lo[4], lo[5], lo[6], lo[7]);
-  }
   if (lane == 0) p.inv_l[(size_t)r * kH + h] = (L == L) ? 1.f : qnan();
+}
+
+// ===========================================================================
+// Merge of the pair attention's partials.  kParts = 4: one warp per (row, head,
+// 128 of the 512 latents), eight splits in flight, so that few rows with many
+// splits still fill the GPU (2 nodes on 65536 keys, 76 splits: 20 us against 47).
+// kParts = 1: one warp per (row, head), two splits of four float4 in flight,
+// for many rows (512 rows, 14 splits: 47 us against 113).  clat rows are [R, 64, 1024], the bf16 value and
+// then the bf16 of what its rounding left, for a GEMM with K = 1024 that meets
+// W_UV twice: one rounding to bf16 (half a step, 2^-8) would add to an output
+// that may itself be rounded.  inv_l is 1, or NaN for a bad row; an absent
+// node's row is zero.
+// ===========================================================================
+struct PairMergeParams {
+  const float* o_part;
+  const float* ml_part;
+  const int32_t* tile_start;
+  const int32_t* bad;
+  const int32_t* parent;
+  __nv_bfloat16* clat;  // [R, 64, 1024]
+  float* inv_l;         // [R, 64]
+  int B, S, G;
+};
+
+template <int kParts>
+__global__ void __launch_bounds__(256) merge_pair_kernel(const PairMergeParams p) {
+  constexpr int kVec = 4 / kParts, kDeep = kParts == 4 ? 8 : 2;  // float4 per lane and split, splits in flight
+  grid_dep_wait();
+  grid_dep_launch();
+  const int lane = threadIdx.x & 31;
+  const long long gw = ((long long)blockIdx.x * 256 + threadIdx.x) >> 5;
+  const int part = (int)(gw % kParts);
+  const long long rh = gw / kParts;
+  const int r = (int)(rh / kH), h = (int)(rh % kH);
+  if (r >= p.B * p.S) return;
+  const int b = r / p.S, s = r % p.S;
+  const long long N = p.tile_start[p.B];
+  const int state = tree_node(p.parent + (size_t)b * p.S, s).state;
+  __nv_bfloat16* dst = p.clat + ((size_t)r * kH + h) * (2 * kDl) + 128 * part + 4 * lane;
+  const bool broken = p.bad[b] || state == kNodeBad;
+  float inv = 1.f;
+  float4 acc[kVec];
+#pragma unroll
+  for (int v = 0; v < kVec; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (!broken && state == kNodePresent) {
+    const long long a = p.tile_start[b], e = p.tile_start[b + 1];
+    const int glo = chunk_of(a, N, p.G), ghi = chunk_of(e - 1, N, p.G);
+    // split of chunk g: the piece (g, b), or none where the chunk has no tile of b
+    auto slot_of = [&](int g) -> long long {
+      const long long c0 = chunk_begin(N, g, p.G), c1 = chunk_begin(N, g + 1, p.G);
+      return g <= ghi && (a > c0 ? a : c0) < (e < c1 ? e : c1) ? (long long)(g + b) * p.S + s : -1;
+    };
+    float M = -INFINITY, L = 0.f;
+    for (int g0 = glo; g0 <= ghi; g0 += 32) {
+      const long long slot = slot_of(g0 + lane);
+      if (slot >= 0) M = fmaxf(M, p.ml_part[(slot * kH + h) * 2]);
+    }
+    M = warp_max(M);
+    for (int g0 = glo; g0 <= ghi; g0 += 32) {
+      const long long mine = slot_of(g0 + lane);
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (mine >= 0) ml = *reinterpret_cast<const float2*>(p.ml_part + (mine * kH + h) * 2);
+      const float w = mine >= 0 ? exp2f(ml.x - M) : 0.f;
+      L += warp_sum(w * ml.y);
+      const int cnt = min(32, ghi - g0 + 1);
+      for (int j0 = 0; j0 < cnt; j0 += kDeep) {
+        float4 o[kDeep][kVec];
+        float wg[kDeep];
+#pragma unroll
+        for (int u = 0; u < kDeep; ++u) {
+          const int j = min(j0 + u, 31);
+          const long long slot = __shfl_sync(0xffffffffu, mine, j);
+          const bool use = j0 + u < cnt && slot >= 0;
+          wg[u] = __shfl_sync(0xffffffffu, w, j);
+          if (!use) wg[u] = 0.f;
+          const float4* src = reinterpret_cast<const float4*>(p.o_part + ((use ? slot : 0) * kH + h) * kDl + 128 * part + 4 * lane);
+#pragma unroll
+          for (int v = 0; v < kVec; ++v) o[u][v] = use ? src[32 * v] : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int u = 0; u < kDeep; ++u)
+#pragma unroll
+          for (int v = 0; v < kVec; ++v) {
+            acc[v].x = fmaf(wg[u], o[u][v].x, acc[v].x);
+            acc[v].y = fmaf(wg[u], o[u][v].y, acc[v].y);
+            acc[v].z = fmaf(wg[u], o[u][v].z, acc[v].z);
+            acc[v].w = fmaf(wg[u], o[u][v].w, acc[v].w);
+          }
+      }
+    }
+    const float il = 1.f / L;
+#pragma unroll
+    for (int v = 0; v < kVec; ++v) acc[v] = make_float4(acc[v].x * il, acc[v].y * il, acc[v].z * il, acc[v].w * il);
+    if (L != L) inv = qnan();
+  } else if (broken) {
+    inv = qnan();
+  }
+#pragma unroll
+  for (int v = 0; v < kVec; ++v) {
+    const uint2 hi = make_uint2(pack2(acc[v].x, acc[v].y), pack2(acc[v].z, acc[v].w));
+    const float2 h0 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&hi.x));
+    const float2 h1 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&hi.y));
+    *reinterpret_cast<uint2*>(dst + 128 * v) = hi;
+    *reinterpret_cast<uint2*>(dst + kDl + 128 * v) =
+        make_uint2(pack2(acc[v].x - h0.x, acc[v].y - h0.y), pack2(acc[v].z - h1.x, acc[v].w - h1.y));
+  }
+  if (lane == 0 && part == 0) p.inv_l[(size_t)r * kH + h] = inv;
 }
 
 // ===========================================================================
@@ -1647,6 +1731,19 @@ cudaError_t set_smem_once(Kern kern, int bytes, std::atomic<unsigned long long>*
 
 std::atomic<unsigned long long> g_abs_attr[9] = {}, g_attn_attr[14] = {}, g_cmb_attr{0};
 
+// Whether a tree call takes the CTA-pair attention (and the GEMMs around it).
+// Up to 8 query rows can also take the GEMVs and one CTA per node, fewer and
+// shorter launches: measured us, that path against the pair's (nodes x keys)
+//   8 x 1024: 30.0, 37.4     8 x 4096: 38.7, 41.4     8 x 8192 (2 sequences): 64.1, 49.5
+//   8 x 16384: 62.3, 49.8    8 x 16384 (4 sequences): 94.7, 60.8
+// With more rows the pair is ahead from short contexts (11 x 9 nodes x 248
+// keys: 64.8, 59.9; 16 nodes x 2048: 49.6, 43.4) to long ones (16 x 2 nodes x
+// 16384: 289.8, 112.8), at worst 5% behind (32 x 64 nodes on 90 keys).
+bool pair_pays(int B, int S, int T_cap) {
+  if ((long long)B * S > kSmallRows) return true;
+  return S >= 2 && (long long)B * S * T_cap >= 65536;
+}
+
 Plan make_plan(int B, int S, int T_cap, int sparse_topk, bool tree = false) {
   Plan pl{};
   const int sms = sm_count();
@@ -1669,7 +1766,8 @@ Plan make_plan(int B, int S, int T_cap, int sparse_topk, bool tree = false) {
     pl.G = (int)G;
     pl.P = pl.G + pl.R - 1;
   }
-  const bool many_tree = tree && pl.R > kSmallRows;
+  const bool many_tree = tree && pair_pays(B, S, T_cap);
+  const bool many = pl.R > kSmallRows || many_tree;
   if (many_tree) {
     pl.Gp = pair_chunks(B, S, T_cap, sms);
     pl.P = std::max(pl.P, (pl.Gp + B - 1) * S);
@@ -1689,9 +1787,9 @@ Plan make_plan(int B, int S, int T_cap, int sparse_topk, bool tree = false) {
   pl.off_stage = off;  // two staging buffers: consecutive layers of one call alternate
   off = align256(off + 2 * (size_t)pl.R * pl.Kpad * kDc * 2);
   pl.off_clat = off;
-  off = align256(off + (pl.R > kSmallRows ? (size_t)pl.R * kH * kDl * (many_tree ? 4 : 2) : 0));
+  off = align256(off + (many ? (size_t)pl.R * kH * kDl * (many_tree ? 4 : 2) : 0));
   pl.off_invl = off;
-  off = align256(off + (pl.R > kSmallRows ? (size_t)pl.R * kH * 4 : 0));
+  off = align256(off + (many ? (size_t)pl.R * kH * 4 : 0));
   // FP8 cache (dense only): quantised query rows and their score factors
   pl.off_q8 = off;
   off = align256(off + (sparse_topk || tree ? 0 : (size_t)pl.R * kH * kQ8Row));
@@ -1706,27 +1804,39 @@ Plan make_plan(int B, int S, int T_cap, int sparse_topk, bool tree = false) {
 // Many rows: merge of the splits, then the W_UV lift as a GEMM.
 cudaError_t run_lift(const DecodeArgs& a, const Plan& pl, unsigned char* w, bool sparse, bool pair, cudaStream_t st) {
   const Geometry& g = a.g;
-  MergeParams mp{};
-  mp.o_part = reinterpret_cast<float*>(w + pl.off_o);
-  mp.ml_part = reinterpret_cast<float*>(w + pl.off_ml);
-  mp.tile_start = reinterpret_cast<int32_t*>(w + pl.off_ts);
-  mp.T = a.T;
-  mp.bad = reinterpret_cast<int32_t*>(w + pl.off_bad);
-  mp.clat = reinterpret_cast<__nv_bfloat16*>(w + pl.off_clat);
-  mp.inv_l = reinterpret_cast<float*>(w + pl.off_invl);
-  mp.B = a.B;
-  mp.S = a.S;
-  mp.G = pair ? pl.Gp : pl.G;
-  mp.pair = pair ? 1 : 0;
-  mp.sparse = sparse ? 1 : 0;
-  mp.parent = a.parent;
+  __nv_bfloat16* clat = reinterpret_cast<__nv_bfloat16*>(w + pl.off_clat);
+  float* inv_l = reinterpret_cast<float*>(w + pl.off_invl);
+  const float* o_part = reinterpret_cast<const float*>(w + pl.off_o);
+  const float* ml_part = reinterpret_cast<const float*>(w + pl.off_ml);
+  const int32_t* ts = reinterpret_cast<const int32_t*>(w + pl.off_ts);
+  const int32_t* bad = reinterpret_cast<const int32_t*>(w + pl.off_bad);
   kernel_mark(st, "merge");
-  const bool split = a.parent != nullptr;
-  cudaError_t e = launch_pdl(split ? merge_kernel<true> : merge_kernel<false>, dim3((pl.R * kH + 7) / 8), dim3(256), 0, st, mp);
+  cudaError_t e;
+  if (pair) {
+    const PairMergeParams mp{o_part, ml_part, ts, bad, a.parent, clat, inv_l, a.B, a.S, pl.Gp};
+    const bool few = pl.R <= 32;  // four warps per (row, head) while a warp each would not fill the GPU
+    const long long warps = (long long)pl.R * kH * (few ? 4 : 1);
+    e = launch_pdl(few ? merge_pair_kernel<4> : merge_pair_kernel<1>, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, st,
+                   mp);
+  } else {
+    MergeParams mp{};
+    mp.o_part = o_part;
+    mp.ml_part = ml_part;
+    mp.tile_start = ts;
+    mp.T = a.T;
+    mp.bad = bad;
+    mp.clat = clat;
+    mp.inv_l = inv_l;
+    mp.B = a.B;
+    mp.S = a.S;
+    mp.G = pl.G;
+    mp.sparse = sparse ? 1 : 0;
+    e = launch_pdl(merge_kernel, dim3((pl.R * kH + 7) / 8), dim3(256), 0, st, mp);
+  }
   if (e != cudaSuccess) return e;
   GemmArgs gu{};
-  gu.a_base = mp.clat;
-  gu.a_ld_z = split ? 2 * kDl : kDl;
+  gu.a_base = clat;
+  gu.a_ld_z = pair ? 2 * kDl : kDl;
   gu.a_ld_m = kH * gu.a_ld_z;
   gu.b_base = a.kv_b;
   gu.b_rows = (long long)kH * (g.Dn + g.Dv);
@@ -1740,23 +1850,16 @@ cudaError_t run_lift(const DecodeArgs& a, const Plan& pl, unsigned char* w, bool
   gu.c_ld_m = (long long)kH * g.Dv;
   gu.c_ld_z = g.Dv;
   gu.out_kind = a.out_bf16 ? kGemmOutBf16Scaled : kGemmOutF32Scaled;
-  gu.scale = mp.inv_l;
+  gu.scale = inv_l;
   gu.M = pl.R;
   gu.N = g.Dv;
-  gu.K = split ? 2 * kDl : kDl;
-  gu.b_k_wrap = split ? kDl : 0;
+  gu.K = pair ? 2 * kDl : kDl;
+  gu.b_k_wrap = pair ? kDl : 0;
   gu.Z = kH;
   gu.flags = a.flags;
   gu.wait_ns = a.wait_limit_ns;
   kernel_mark(st, "up_gemm");
   return launch_gemm_tc(gu, true, st);
-}
-
-// Whether the CTA-pair attention takes a many-row tree call.
-bool pair_pays(int B, int S, int T_cap) {
-  (void)B;
-  (void)T_cap;
-  return S >= 2;
 }
 
 cudaError_t run_pair(const DecodeArgs& a, const Plan& pl, unsigned char* w, long long pool_rows, cudaStream_t st) {
@@ -1853,8 +1956,8 @@ cudaError_t run(const DecodeArgs& a, void* ws, bool sparse, cudaStream_t st) {
   ap.Dv = g.Dv;
   ap.topk = a.topk;
   ap.sparse = sparse ? 1 : 0;
-  const bool big = pl.R > kSmallRows;
-  const bool pair = a.parent && big && pair_pays(B, S, a.T_cap);
+  const bool pair = a.parent && pair_pays(B, S, a.T_cap);
+  const bool big = pl.R > kSmallRows || pair;
   ap.Lc = static_cast<const unsigned char*>(a.Lc);
   ap.Rc = static_cast<const __nv_bfloat16*>(a.Rc);
   ap.lat_row_bytes = a.lat_fp8 ? kDl : kDl * 2;
