@@ -572,11 +572,11 @@ def cache_append_fp8_paged(comp, kv_a_ln, block_table, T, Lc8_pages, Rc_pages, d
 
 
 # ------------------------------------------------------------- drafted token trees
-def _all_plain(device, dtype, *ts) -> bool:
-    """Every tensor contiguous, of `dtype`, on `device` (the calls below are short: the
-    check that passes is one expression per tensor, _explain finds words for one that fails)."""
+def _all_plain(index, dtype, *ts) -> bool:
+    """Every tensor contiguous, of `dtype`, on GPU `index` (the calls below are short: the check
+    that passes is one expression per tensor, _explain finds words for one that fails)."""
     for t in ts:
-        if t.dtype is not dtype or t.device != device or not t.is_contiguous():
+        if t.dtype is not dtype or t.get_device() != index or not t.is_contiguous():
             return False
     return True
 
@@ -591,13 +591,13 @@ def _explain(device, **named):
             raise ValueError(f"{name} must be contiguous")
 
 
-def _stream_on(torch, device, stream):
-    """Stream handle for a call on `device`, which has to be the current one."""
-    if device.type != "cuda":
+def _stream_on(torch, index, stream):
+    """Stream handle for a call on GPU `index` (-1: the CPU), which has to be the current one."""
+    if index < 0:
         raise ValueError("tensors must live on the GPU")
-    if device.index != torch._C._cuda_getDevice():
-        raise ValueError(f"tensors on {device}: make it the current device")
-    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device.index)
+    if index != torch._C._cuda_getDevice():
+        raise ValueError(f"tensors on GPU {index}: make it the current device")
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(index)
 
 
 def _want(name, t, *shape):
@@ -618,12 +618,12 @@ def _tree_args(torch, q, Lc, Rc, T, parent, kv_b, dims, out, out_dtype, workspac
     """Checks shared by the two tree attentions ->
     (dims struct, dtype code, out, its code, workspace, its bytes)."""
     B, S, H, qk = q.shape
-    dtype, device = q.dtype, q.device
+    dtype, index = q.dtype, q.get_device()
     if H != dims.H or qk != dims.qk_nope + dims.qk_rope:
         raise ValueError(f"q has shape {tuple(q.shape)}, expected [B, S, {dims.H}, {dims.qk_nope + dims.qk_rope}]")
     code = _dtype_code(q)
     if out is None:
-        out = torch.empty((B, S, H, dims.v_head), dtype=out_dtype or torch.float32, device=device)
+        out = torch.empty((B, S, H, dims.v_head), dtype=out_dtype or torch.float32, device=q.device)
     else:
         if out_dtype is not None and out.dtype != out_dtype:
             raise TypeError("out does not have out_dtype")
@@ -636,16 +636,16 @@ def _tree_args(torch, q, Lc, Rc, T, parent, kv_b, dims, out, out_dtype, workspac
     _want("parent", parent, B, S)
     _want("kv_b", kv_b, H, dims.qk_nope + dims.v_head, dims.kv_lora)
     i32 = torch.int32
-    if not (_all_plain(device, dtype, q, Lc, Rc, kv_b) and _all_plain(device, i32, T, parent)
-            and _all_plain(device, out.dtype, out)):
-        _explain(device, q=(q, dtype), Lc=(Lc, dtype), Rc=(Rc, dtype), kv_b=(kv_b, dtype), T=(T, i32), parent=(parent, i32),
+    if not (_all_plain(index, dtype, q, Lc, Rc, kv_b) and _all_plain(index, i32, T, parent)
+            and _all_plain(index, out.dtype, out)):
+        _explain(q.device, q=(q, dtype), Lc=(Lc, dtype), Rc=(Rc, dtype), kv_b=(kv_b, dtype), T=(T, i32), parent=(parent, i32),
                  out=(out, out.dtype))
     d = make_dims(dims)
     if workspace is None:  # the library checks the size of one that is given
-        workspace, wsb = _workspace(lib().mla_decode_tree_workspace_size(ctypes.byref(d), code, B, S, T_cap), device, None)
+        workspace, wsb = _workspace(lib().mla_decode_tree_workspace_size(ctypes.byref(d), code, B, S, T_cap), q.device, None)
     else:
-        if workspace.device != device or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be contiguous and on {device}")
+        if workspace.get_device() != index or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be contiguous and on {q.device}")
         wsb = workspace.numel() * workspace.element_size()
     return d, code, out, out_code, None if workspace is None else workspace.data_ptr(), wsb
 
@@ -661,7 +661,7 @@ def decode_tree(q, Lc, Rc, T, parent, kv_b, dims, out=None, out_dtype=None, work
     if Lc.shape[0] != B:
         raise ValueError(f"cache of {Lc.shape[0]} sequences for {B} queries")
     d, code, out, out_code, ws, wsb = _tree_args(torch, q, Lc, Rc, T, parent, kv_b, dims, out, out_dtype, workspace, T_cap)
-    st = _stream_on(torch, q.device, stream)
+    st = _stream_on(torch, q.get_device(), stream)
     _check(lib().mla_decode_tree(ctypes.byref(d), code, B, S, q.data_ptr(), Lc.data_ptr(), Rc.data_ptr(), T_cap,
                                  T.data_ptr(), parent.data_ptr(), kv_b.data_ptr(), out_code, out.data_ptr(), ws, wsb, st))
     return out
@@ -678,7 +678,7 @@ def decode_tree_paged(q, Lc_pages, Rc_pages, block_table, T, parent, kv_b, dims,
     _explain(q.device, block_table=(block_table, torch.int32))
     d, code, out, out_code, ws, wsb = _tree_args(torch, q, Lc_pages, Rc_pages, T, parent, kv_b, dims, out, out_dtype, workspace,
                                        max_pages * page_size)
-    st = _stream_on(torch, q.device, stream)
+    st = _stream_on(torch, q.get_device(), stream)
     _check(lib().mla_decode_tree_paged(ctypes.byref(d), code, B, S, q.data_ptr(), Lc_pages.data_ptr(),
                                        Rc_pages.data_ptr(), num_pages, page_size, block_table.data_ptr(), max_pages,
                                        T.data_ptr(), parent.data_ptr(), kv_b.data_ptr(), out_code, out.data_ptr(), ws,
@@ -688,7 +688,7 @@ def decode_tree_paged(q, Lc_pages, Rc_pages, block_table, T, parent, kv_b, dims,
 
 def _append_tree_args(torch, comp, kv_a_ln, T, parent, Lc, Rc, dims):
     B, S = comp.shape[0], comp.shape[1]
-    dtype, device, i32 = comp.dtype, comp.device, torch.int32
+    dtype, index, i32 = comp.dtype, comp.get_device(), torch.int32
     _want("comp", comp, B, S, dims.kv_lora + dims.qk_rope)
     _want("kv_a_ln", kv_a_ln, dims.kv_lora)
     _want("T", T, B)
@@ -696,8 +696,8 @@ def _append_tree_args(torch, comp, kv_a_ln, T, parent, Lc, Rc, dims):
     ls = Lc.shape
     if ls[2] != dims.kv_lora or Rc.shape != (ls[0], ls[1], dims.qk_rope):
         raise ValueError("cache shapes do not match dims")
-    if not (_all_plain(device, dtype, comp, kv_a_ln, Lc, Rc) and _all_plain(device, i32, T, parent)):
-        _explain(device, comp=(comp, dtype), kv_a_ln=(kv_a_ln, dtype), Lc=(Lc, dtype), Rc=(Rc, dtype), T=(T, i32),
+    if not (_all_plain(index, dtype, comp, kv_a_ln, Lc, Rc) and _all_plain(index, i32, T, parent)):
+        _explain(comp.device, comp=(comp, dtype), kv_a_ln=(kv_a_ln, dtype), Lc=(Lc, dtype), Rc=(Rc, dtype), T=(T, i32),
                  parent=(parent, i32))
     return B, S, make_dims(dims), _dtype_code(comp)
 
@@ -709,7 +709,7 @@ def cache_append_tree(comp, kv_a_ln, T, parent, Lc, Rc, dims, rms_eps: float, st
     B, S, d, code = _append_tree_args(torch, comp, kv_a_ln, T, parent, Lc, Rc, dims)
     if Lc.shape[0] != B:
         raise ValueError(f"cache of {Lc.shape[0]} sequences for {B} rows")
-    st = _stream_on(torch, comp.device, stream)
+    st = _stream_on(torch, comp.get_device(), stream)
     _check(lib().mla_cache_append_tree(ctypes.byref(d), code, B, S, comp.data_ptr(), kv_a_ln.data_ptr(), rms_eps,
                                        Lc.shape[1], T.data_ptr(), parent.data_ptr(), Lc.data_ptr(), Rc.data_ptr(), st))
     return Lc, Rc
@@ -722,7 +722,7 @@ def cache_append_tree_paged(comp, kv_a_ln, block_table, T, parent, Lc_pages, Rc_
     B, S, d, code = _append_tree_args(torch, comp, kv_a_ln, T, parent, Lc_pages, Rc_pages, dims)
     _want("block_table", block_table, B, block_table.shape[1])
     _explain(comp.device, block_table=(block_table, torch.int32))
-    st = _stream_on(torch, comp.device, stream)
+    st = _stream_on(torch, comp.get_device(), stream)
     _check(lib().mla_cache_append_tree_paged(ctypes.byref(d), code, B, S, comp.data_ptr(), kv_a_ln.data_ptr(), rms_eps,
                                              Lc_pages.data_ptr(), Rc_pages.data_ptr(), Lc_pages.shape[0],
                                              Lc_pages.shape[1], block_table.data_ptr(), block_table.shape[1],
@@ -739,38 +739,42 @@ def tree_verify(p, q, tokens, parent, u, path=None, n_acc=None, token=None, stre
     [B,S] int32; u [B,S+1] float32 in [0,1).  Returns (path [B,S] accepted nodes then -1,
     n_acc [B], token [B]), all int32."""
     torch = _torch()
-    B, S = tokens.shape
-    V, device = p.shape[2], p.device
-    f32, i32 = torch.float32, torch.int32
-    for name, x in (("p", p),) if q is None else (("p", p), ("q", q)):
-        if x.shape != (B, S + 1, V):
-            raise ValueError(f"{name} has shape {tuple(x.shape)}, expected {(B, S + 1, V)}")
-        if x.dtype is not f32:
-            raise TypeError(f"{name} must be torch.float32, got {x.dtype}")
-        if x.stride(2) != 1 and V > 1:
-            raise ValueError(f"the values of a row of {name} must be contiguous")
-        if x.device != device:
-            raise ValueError(f"{name} is on {x.device}, not on {device}")
-    _want("parent", parent, B, S)
-    _want("u", u, B, S + 1)
-    if not (_all_plain(device, i32, tokens, parent) and _all_plain(device, f32, u)):
-        _explain(device, tokens=(tokens, i32), parent=(parent, i32), u=(u, f32))
+    B, S = shape = tokens.shape
+    index, f32, i32 = p.get_device(), torch.float32, torch.int32
+    want = (B, S + 1, p.shape[2])
+    if p.shape != want or p.dtype is not f32 or (q is not None and (q.shape != want or q.dtype is not f32 or q.get_device() != index)):
+        for name, x in (("p", p), ("q", p if q is None else q)):
+            _want(name, x, *want)
+            if x.dtype is not f32:
+                raise TypeError(f"{name} must be torch.float32, got {x.dtype}")
+        raise ValueError(f"q is on {q.device}, not on {p.device}")
+    pb, pr, pv = p.stride()
+    qp, qb, qr, qv = (None, 0, 0, 1) if q is None else (q.data_ptr(), *q.stride())
+    if (pv != 1 or qv != 1) and want[2] > 1:
+        raise ValueError("the values of a row of p and of q must be contiguous")
+    if parent.shape != shape or u.shape != want[:2]:
+        _want("parent", parent, B, S)
+        _want("u", u, B, S + 1)
+    if not (_all_plain(index, i32, tokens, parent) and _all_plain(index, f32, u)):
+        _explain(p.device, tokens=(tokens, i32), parent=(parent, i32), u=(u, f32))
+    st = _stream_on(torch, index, stream)
     if path is None:
-        path = torch.empty((B, S), dtype=i32, device=device)
+        path = torch.empty_like(tokens)
+    else:
+        _want("path", path, B, S)
+        _explain(p.device, path=(path, i32))
     if n_acc is None:
-        n_acc = torch.empty(B, dtype=i32, device=device)
+        n_acc = tokens.new_empty(B)
+    else:
+        _want("n_acc", n_acc, B)
+        _explain(p.device, n_acc=(n_acc, i32))
     if token is None:
-        token = torch.empty(B, dtype=i32, device=device)
-    _want("path", path, B, S)
-    _want("n_acc", n_acc, B)
-    _want("token", token, B)
-    if not _all_plain(device, i32, path, n_acc, token):
-        _explain(device, path=(path, i32), n_acc=(n_acc, i32), token=(token, i32))
-    st = _stream_on(torch, device, stream)
-    qp, qr, qb = (None, 0, 0) if q is None else (q.data_ptr(), q.stride(1), q.stride(0))
-    _check(lib().mla_tree_verify(B, S, V, p.data_ptr(), p.stride(1), p.stride(0), qp, qr, qb, tokens.data_ptr(),
-                                 parent.data_ptr(), u.data_ptr(), path.data_ptr(), n_acc.data_ptr(), token.data_ptr(),
-                                 st))
+        token = tokens.new_empty(B)
+    else:
+        _want("token", token, B)
+        _explain(p.device, token=(token, i32))
+    _check(lib().mla_tree_verify(B, S, want[2], p.data_ptr(), pr, pb, qp, qr, qb, tokens.data_ptr(), parent.data_ptr(),
+                                u.data_ptr(), path.data_ptr(), n_acc.data_ptr(), token.data_ptr(), st))
     return path, n_acc, token
 
 
@@ -800,6 +804,7 @@ class CacheRows:
                 raise ValueError("block_table must be [B, max_pages]")
         self.B = first.shape[0] if block_table is None else block_table.shape[0]
         self.rows, self.cap = first.shape[0], first.shape[1]
+        self.index = first.get_device()
         n = len(self.caches)
         self.n = n
         self.pointers = (ctypes.c_void_p * n)(*[c.data_ptr() for c in self.caches])
@@ -811,17 +816,20 @@ def tree_commit(rows: CacheRows, T, path, n_acc, T_out=None, stream=None):
     tree's rows in every cache of `rows`; returns T_out [B] int32 = T - S + n_acc."""
     torch = _torch()
     B, S = path.shape
-    device, i32 = rows.device, torch.int32
+    index, i32, shape = rows.index, torch.int32, (B,)
     if B != rows.B:
         raise ValueError(f"caches of {rows.B} sequences, path of {B}")
+    if T.shape != shape or n_acc.shape != shape:
+        _want("T", T, B)
+        _want("n_acc", n_acc, B)
+    if not _all_plain(index, i32, T, path, n_acc):
+        _explain(rows.device, T=(T, i32), path=(path, i32), n_acc=(n_acc, i32))
+    st = _stream_on(torch, index, stream)
     if T_out is None:
-        T_out = torch.empty(B, dtype=i32, device=device)
-    _want("T", T, B)
-    _want("n_acc", n_acc, B)
-    _want("T_out", T_out, B)
-    if not _all_plain(device, i32, T, path, n_acc, T_out):
-        _explain(device, T=(T, i32), path=(path, i32), n_acc=(n_acc, i32), T_out=(T_out, i32))
-    st = _stream_on(torch, device, stream)
+        T_out = torch.empty_like(T)
+    else:
+        _want("T_out", T_out, B)
+        _explain(rows.device, T_out=(T_out, i32))
     table = rows.block_table
     if table is None:
         rc = lib().mla_tree_commit(rows.n, rows.pointers, rows.row_bytes, B, S, rows.cap, T.data_ptr(), path.data_ptr(),

@@ -904,12 +904,8 @@ int run_commit(mla::CommitArgs& a, int n, void* const* cache, const int* row_byt
   for (int i0 = 0; i0 < n && e == cudaSuccess; i0 += mla::kCommitCaches) {
     a.n = n - i0 < mla::kCommitCaches ? n - i0 : mla::kCommitCaches;
     a.T_out = i0 == 0 ? T_out : nullptr;
-    for (int i = 0; i < a.n; ++i) {
-      a.cache[i] = cache[i0 + i];
-      a.row_bytes[i] = row_bytes[i0 + i];
-    }
     mla::kernel_mark(st, "tree_commit");
-    e = mla::launch_tree_commit(a, st);
+    e = mla::launch_tree_commit(a, cache + i0, row_bytes + i0, st);
   }
   mla::call_end(st);
   if (e != cudaSuccess) return cuda_fail(e, what);

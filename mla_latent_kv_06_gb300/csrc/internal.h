@@ -195,10 +195,9 @@ struct CommitArgs {
   int32_t* T_out;        // [B], or null: a later launch of the same call
   unsigned int* flags;
   PageTable pages;
-  void* cache[kCommitCaches];
-  int row_bytes[kCommitCaches];
 };
-cudaError_t launch_tree_commit(const CommitArgs& a, cudaStream_t st);
+// The n caches and their row sizes (host arrays, n <= kCommitCaches).
+cudaError_t launch_tree_commit(const CommitArgs& a, void* const* cache, const int* row_bytes, cudaStream_t st);
 
 // Sets the thread-local message returned by mla_last_error().
 void set_last_error(const char* msg);

@@ -47,7 +47,17 @@ __device__ __forceinline__ void move_rows(unsigned char* cache, int row_bytes, i
   }
 }
 
-__global__ void __launch_bounds__(kThreads) tree_commit_kernel(const __grid_constant__ CommitArgs a) {
+// Few caches take a launch with a short parameter block (1.6 KB of it costs the host time).
+template <int kCaches>
+struct CommitLaunch {
+  CommitArgs a;
+  void* cache[kCaches];
+  int row_bytes[kCaches];
+};
+
+template <int kCaches>
+__global__ void __launch_bounds__(kThreads) tree_commit_kernel(const __grid_constant__ CommitLaunch<kCaches> c) {
+  const CommitArgs& a = c.a;
   const int cache = blockIdx.x, b = blockIdx.y, lane = threadIdx.x & 31;
   const int S = a.S, Tb = __ldg(a.T + b), n = __ldg(a.n_acc + b);
   // lane holds path[lane] and path[32 + lane], and the pool rows of tree rows lane and 32 + lane
@@ -74,19 +84,30 @@ __global__ void __launch_bounds__(kThreads) tree_commit_kernel(const __grid_cons
     if (a.T_out) a.T_out[b] = bad_len ? Tb : bad ? base : base + n;
   }
   if (bad_len || bad) return;
-  unsigned char* c = static_cast<unsigned char*>(a.cache[cache]);
-  const int rb = a.row_bytes[cache];
-  const unsigned odd = (unsigned)(reinterpret_cast<uintptr_t>(c) | (unsigned)rb);
-  if ((odd & 15u) == 0) move_rows<uint4>(c, rb, n, p_lo, p_hi, row);
-  else if ((odd & 3u) == 0) move_rows<uint32_t>(c, rb, n, p_lo, p_hi, row);
-  else move_rows<unsigned char>(c, rb, n, p_lo, p_hi, row);
+  unsigned char* rows = static_cast<unsigned char*>(c.cache[cache]);
+  const int rb = c.row_bytes[cache];
+  const unsigned odd = (unsigned)(reinterpret_cast<uintptr_t>(rows) | (unsigned)rb);
+  if ((odd & 15u) == 0) move_rows<uint4>(rows, rb, n, p_lo, p_hi, row);
+  else if ((odd & 3u) == 0) move_rows<uint32_t>(rows, rb, n, p_lo, p_hi, row);
+  else move_rows<unsigned char>(rows, rb, n, p_lo, p_hi, row);
+}
+
+template <int kCaches>
+cudaError_t launch(const CommitArgs& a, void* const* cache, const int* row_bytes, cudaStream_t st) {
+  CommitLaunch<kCaches> c;
+  c.a = a;
+  for (int i = 0; i < a.n; ++i) {
+    c.cache[i] = cache[i];
+    c.row_bytes[i] = row_bytes[i];
+  }
+  tree_commit_kernel<kCaches><<<dim3(a.n, a.B), kThreads, 0, st>>>(c);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_tree_commit(const CommitArgs& a, cudaStream_t st) {
-  tree_commit_kernel<<<dim3(a.n, a.B), kThreads, 0, st>>>(a);
-  return cudaGetLastError();
+cudaError_t launch_tree_commit(const CommitArgs& a, void* const* cache, const int* row_bytes, cudaStream_t st) {
+  return a.n <= 8 ? launch<8>(a, cache, row_bytes, st) : launch<kCommitCaches>(a, cache, row_bytes, st);
 }
 
 }  // namespace mla

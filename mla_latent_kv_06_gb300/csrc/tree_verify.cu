@@ -191,7 +191,7 @@ __device__ __forceinline__ int pick_part(double mine, double* t) {
 // together would queue at the fp64 pipe) sit in warp 0 of every CTA; the other
 // warps take its commands.  CTAs of a cluster reach the same decisions from
 // the same numbers: rank 0's copy of the node data and the exchanged totals.
-__global__ void __launch_bounds__(kThreads) tree_verify_kernel(const VerifyArgs a) {
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) tree_verify_kernel(const VerifyArgs a) {
   __shared__ Shared sh;
   cg::cluster_group cluster = cg::this_cluster();
   const int b = blockIdx.x / kCluster, rank = (int)cluster.block_rank();
@@ -397,18 +397,8 @@ __global__ void __launch_bounds__(kThreads) tree_verify_kernel(const VerifyArgs 
 }  // namespace
 
 cudaError_t launch_tree_verify(const VerifyArgs& a, cudaStream_t st) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)a.B * kCluster);
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = kCluster;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tree_verify_kernel, a);
+  tree_verify_kernel<<<(unsigned)a.B * kCluster, kThreads, 0, st>>>(a);
+  return cudaGetLastError();
 }
 
 }  // namespace mla
