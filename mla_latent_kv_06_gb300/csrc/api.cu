@@ -771,7 +771,16 @@ int run_cache_append(const mla_dims* d, int dtype, int B, int S, const void* com
     a.lat_fp8 = 1;
     a.lat_inv_scale = 1.f / lat_scale;
   }
-  for (int j = 0; j < g.Dr / 2; ++j) a.turn[j] = mla::rope_turns(std::pow(g.rope_base, -2.0 * j / g.Dr));
+  // the frequencies depend on the base and the width alone; the powers cost the host 2 us a call
+  static thread_local double turn_base = 0.0;
+  static thread_local int turn_width = 0;
+  static thread_local uint64_t turn[mla::kMaxRopePairs];
+  if (turn_base != g.rope_base || turn_width != g.Dr) {
+    for (int j = 0; j < g.Dr / 2; ++j) turn[j] = mla::rope_turns(std::pow(g.rope_base, -2.0 * j / g.Dr));
+    turn_base = g.rope_base;
+    turn_width = g.Dr;
+  }
+  for (int j = 0; j < g.Dr / 2; ++j) a.turn[j] = turn[j];
   if (!a.flags) return fail(MLA_ERR_CUDA, "cannot resolve the device status word");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   mla::call_begin();

@@ -1965,7 +1965,14 @@ cudaError_t run(const DecodeArgs& a, void* ws, bool sparse, cudaStream_t st) {
   ap.prefetch =
       (!big && !sparse && (long long)B * a.T_cap * (ap.lat_row_bytes + kDr * 2) <= (48ll << 20)) ? 1 : 0;
   ap.pages = sparse ? PageTable{} : a.pages;
-  for (int j = 0; j < kDr / 2; ++j) ap.turn[j] = rope_turns(std::pow(g.rope_base, -2.0 * j / kDr));
+  // the frequencies depend on the base alone: 32 powers cost the host 2 us a call
+  static thread_local double turn_base = 0.0;
+  static thread_local uint64_t turn[kDr / 2];
+  if (turn_base != g.rope_base) {
+    for (int j = 0; j < kDr / 2; ++j) turn[j] = rope_turns(std::pow(g.rope_base, -2.0 * j / kDr));
+    turn_base = g.rope_base;
+  }
+  for (int j = 0; j < kDr / 2; ++j) ap.turn[j] = turn[j];
   ap.flags = a.flags;
   ap.parent = a.parent;
   const size_t abs_smem = (size_t)kAbsRows * g.Dn * 4 + (size_t)kAbsGroups * kAbsRows * kAbsCols * 4;
@@ -1978,7 +1985,7 @@ cudaError_t run(const DecodeArgs& a, void* ws, bool sparse, cudaStream_t st) {
   const bool paged_abs = ap.prefetch && ap.pages.table;
   const AbsKern akern = big ? absorb_kernel<4, false> : abs_kerns[paged_abs ? 1 : 0][g.Dn / 64 - 1];
   // many rows: the rotary part of each head spread over up to four CTAs
-  const int abs_gx = big ? std::min(4, (pl.R * (kDr / 2) + 2047) / 2048) : kDl / kAbsCols;
+  const int abs_gx = big ? std::min(pair ? 16 : 4, (pl.R * (kDr / 2) + 2047) / 2048) : kDl / kAbsCols;
   ap.rope_x = abs_gx;
   if (pair) ap.tail = reinterpret_cast<__nv_bfloat16*>(w + pl.off_tail);
   e = set_smem_once(akern, (int)abs_smem, &g_abs_attr[big ? 8 : (paged_abs ? 4 : 0) + g.Dn / 64 - 1]);

@@ -13,10 +13,12 @@
 // accepted when u a < W(x), and a rejection removes x and its mass.
 //
 // Rounding.  A decision sits on sums over the whole vocabulary, so they are
-// held to about 2^-48: c is a pair of floats, each W(x) = p - c q is formed
-// as an unevaluated pair hi + lo (the exact product by fma, the exact
-// difference by Knuth's two-sum) and added into a pair accumulator.  That runs on the fp32 pipe;
-// plain doubles would run at 1/64 of its rate here and bound the kernel.
+// held to about 2^-48 without the fp64 pipe, which has 1/64 of the fp32 rate
+// here and would bound the kernel: sum W = A - c B with A and B the sums of p and of q over
+// the x where p > c q (an x misjudged by rounding has W(x) next to zero), and
+// A and B are kept as unevaluated pairs hi + lo, added with Knuth's two-sum.
+// A pass over a vocabulary of 131072 costs 32 sequences some 20 instructions
+// an element, which is what bounds it; forming each W(x) as a pair cost 30.
 #include <cooperative_groups.h>
 
 #include "common.cuh"
@@ -78,13 +80,19 @@ struct Command {
   int done;
 };
 
+// The sums of p and of q over the x of a segment with p > c q (c = 0: of p).
+struct Sums {
+  Pair a, b;
+};
+
 struct Shared {
   // node data, filled by rank 0 and copied by the others
   int parent[kMaxTree], token[kMaxTree];
   float u[kMaxTree + 1], pt[kMaxTree], qt[kMaxTree];
   unsigned long long kids[kMaxTree + 1];  // children of every context
   double part[2][kCluster];               // slice totals of every CTA, alternating between passes
-  double warp_sum[kWarps];
+  Sums warp_sums[kWarps];                 // of the warps' segments ...
+  double warp_sum[kWarps];                // ... and their W
   Command cmd;
   int bad[kMaxTree], up[kMaxTree];
   int find_warp;
@@ -123,26 +131,44 @@ __device__ __forceinline__ unsigned long long removed_inside(const Shared& sh, u
   return got;
 }
 
-// Sum of W over the segment; the warp reads 32 consecutive elements at a time,
-// kAhead of them (of p and of q) in flight.
+// Sums over the segment, the same in every lane; the warp reads 32
+// consecutive elements at a time, kAhead of them (of p and of q) in flight.
 constexpr int kAhead = 8;
-__device__ __forceinline__ Pair segment_sum(const Segment& g, int lane) {
-  Pair acc{0.f, 0.f};
+template <bool kDraft>
+__device__ __forceinline__ Sums segment_sum(const Segment& g, int lane) {
+  Pair a{0.f, 0.f}, b{0.f, 0.f};
   for (int i0 = g.lo; i0 < g.hi; i0 += 32 * kAhead) {
     float p[kAhead], q[kAhead];
+    if (i0 + 32 * kAhead <= g.hi) {
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      const int i = i0 + 32 * k + lane;
-      p[k] = i < g.hi ? __ldg(g.p + i) : 0.f;
-      q[k] = g.q && i < g.hi ? __ldg(g.q + i) : 0.f;
+      for (int k = 0; k < kAhead; ++k) {
+        p[k] = __ldg(g.p + i0 + 32 * k + lane);
+        if (kDraft) q[k] = __ldg(g.q + i0 + 32 * k + lane);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int i = i0 + 32 * k + lane;
+        p[k] = i < g.hi ? __ldg(g.p + i) : 0.f;
+        q[k] = kDraft && i < g.hi ? __ldg(g.q + i) : 0.f;
+      }
     }
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
-      const Pair v = element(g, i0 + 32 * k + lane, p[k], q[k]);
-      add(acc, v.hi, v.lo);
+      if (kDraft) {
+        const float w = fmaf(-g.cl, q[k], fmaf(-g.ch, q[k], p[k]));
+        const bool in = !(w <= 0.f);  // (a NaN is in, so that the total shows it)
+        add(a, in ? p[k] : 0.f, 0.f);
+        add(b, in ? q[k] : 0.f, 0.f);
+      } else {
+        add(a, element(g, i0 + 32 * k + lane, p[k], 0.f).hi, 0.f);
+      }
     }
   }
-  return warp_total(acc);
+  return Sums{warp_total(a), kDraft ? warp_total(b) : b};
+}
+__device__ __forceinline__ Sums segment_sum(const Segment& g, int lane) {
+  return g.q ? segment_sum<true>(g, lane) : segment_sum<false>(g, lane);
 }
 
 // First index of the segment (at most 32 elements a step) whose cumulative
@@ -321,11 +347,16 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) tre
     seg.ch = cmd.ch;
     seg.cl = cmd.cl;
     seg.removed = removed_inside(sh, cmd.removed, seg.lo, seg.hi);
-    const Pair s = segment_sum(seg, lane);
-    if (lane == 0) sh.warp_sum[warp] = value(s);
+    const Sums s = segment_sum(seg, lane);
+    if (lane == 0) sh.warp_sums[warp] = s;
     __syncthreads();
-    if (warp == 0) {
-      double mine = lane < kWarps ? sh.warp_sum[lane] : 0.0;
+    if (warp == 0) {  // (one warp: every fp64 instruction of a warp takes 16 cycles)
+      double mine = 0.0;
+      if (lane < kWarps) {
+        const Sums x = sh.warp_sums[lane];
+        mine = value(x.a) - c * value(x.b);
+        sh.warp_sum[lane] = mine;
+      }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
       if (lane < kCluster) cluster.map_shared_rank(&sh, lane)->part[pass & 1][rank] = mine;
@@ -377,12 +408,16 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) tre
   seg.lo = min(hlo + 32 * sub * warp, hhi);
   seg.hi = min(hlo + 32 * sub * (warp + 1), hhi);
   seg.removed = removed_inside(sh, sh.cmd.removed, seg.lo, seg.hi);
-  const Pair part = segment_sum(seg, lane);
-  if (lane == 0) sh.warp_sum[warp] = value(part);
+  const Sums part = segment_sum(seg, lane);
+  if (lane == 0) sh.warp_sums[warp] = part;
   __syncthreads();
   if (warp == 0) {
-    double t = sh.find_t;
-    const int w = pick_part(lane < kWarps ? sh.warp_sum[lane] : 0.0, &t);
+    double t = sh.find_t, mine = 0.0;
+    if (lane < kWarps) {
+      const Sums x = sh.warp_sums[lane];
+      mine = value(x.a) - c * value(x.b);
+    }
+    const int w = pick_part(mine, &t);
     if (lane == 0) {
       sh.find_warp = w;
       sh.find_t = t;

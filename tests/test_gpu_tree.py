@@ -544,3 +544,24 @@ def test_two_streams_at_once(cuda_lib):
     for st, (out, verdict), want in zip(states, got, alone):
         assert torch.equal(out, want)
         _compare(verdict, *st["host"])
+
+
+def test_decode_tree_empty_trees(cuda_lib):
+    """Sequences without any node: zero rows, next to sequences that have some."""
+    for S, T in ((3, [20, 300]), (9, [700, 9, 33])):
+        B = len(T)
+        parent = random_parents(B, S, 4, absent=False)
+        parent[0] = -2
+        out, ref = _attend(cuda_lib, GLM, "bf16", T, S, parent, 900 + S)
+        _check(out, ref, parent, TOL["bf16"])
+
+
+@pytest.mark.parametrize("rem", [0, 1, 15])
+@pytest.mark.parametrize("page_size", [0, 128])
+def test_decode_tree_tail_boundaries(cuda_lib, rem, page_size):
+    """The tree's rows begin on, just after and just before a 16-key step, a key tile
+    and a page."""
+    S, T = 10, [256 + rem + 10, 512 + rem + 10, 16 + rem + 10, 128 + rem + 10]
+    parent = random_parents(4, S, 61 + rem)
+    out, ref = _attend(cuda_lib, GLM, "bf16", T, S, parent, 950 + rem, page_size=page_size)
+    _check(out, ref, parent, TOL["bf16"])
