@@ -823,23 +823,25 @@ struct AbsorbParams {
   uint64_t turn[kDr / 2];  // rope_turns(rope_base^(-2j/qk_rope)), from the host
   unsigned int* flags;
   PageTable pages;
-  const int32_t* parent;  // tree attention: [B, S] parent indices, else null
+  const int32_t* parent;  // tree attention: [B, S] parent indices
   int rope_x;             // blocks along x that form the rotary part (many rows); any more stage the tails
   __nv_bfloat16* tail;    // pair attention: staged tail rows [B, kPairStage, 576], else null
 };
 
 // Rotary position of query row s of sequence b (length Tb): its row, or the
 // prefix length plus its depth in a drafted tree.  Bad lengths give 0.
+template <bool kTree>
 __device__ __forceinline__ int query_pos(const AbsorbParams& p, int b, int s, int Tb) {
   if (Tb < p.S || Tb > p.T_cap) return 0;
-  return Tb - p.S + (p.parent ? tree_node(p.parent + (size_t)b * p.S, s).depth : s);
+  return Tb - p.S + (kTree ? tree_node(p.parent + (size_t)b * p.S, s).depth : s);
 }
 
 // Rotary part of query row r of head h, rotated to the row's own position.
+template <bool kTree>
 __device__ __forceinline__ void rope_row(const AbsorbParams& p, int r, int h, int j) {
   const int Dq = p.Dn + kDr;
   const int b = r / p.S, s = r % p.S;
-  const int pos = query_pos(p, b, s, p.T[b]);
+  const int pos = query_pos<kTree>(p, b, s, p.T[b]);
   float sn, cs;
   rope_cs_turns(pos, p.turn[j], &cs, &sn);
   const __nv_bfloat16* qr = p.q + ((size_t)r * kH + h) * Dq + p.Dn;
@@ -852,6 +854,7 @@ __device__ __forceinline__ void rope_row(const AbsorbParams& p, int r, int h, in
 // Rotary parts of rows x pairs e = tid, tid + nthr, ... (row e / 32, pair e % 32):
 // eight pairs per thread at a time, their loads (T[b] and the two bf16 values)
 // all in flight before the first rotation.
+template <bool kTree>
 __device__ __forceinline__ void rope_rows(const AbsorbParams& p, int h, int tid, int nthr) {
   const int R = p.B * p.S, Dq = p.Dn + kDr, n = R * (kDr / 2);
   for (int e0 = tid; e0 < n; e0 += 8 * nthr) {
@@ -860,7 +863,7 @@ __device__ __forceinline__ void rope_rows(const AbsorbParams& p, int h, int tid,
     // the 32 pairs of a row sit in one warp, so lane u walks up the tree for
     // the warp's u-th row
     int depth = 0;
-    if (p.parent) {
+    if (kTree) {
       const int lane = threadIdx.x & 31, e = e0 - lane + lane * nthr;
       if (lane < 8 && e < n) {
         const int r = e / (kDr / 2);
@@ -879,9 +882,9 @@ __device__ __forceinline__ void rope_rows(const AbsorbParams& p, int h, int tid,
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
       const int e = e0 + u * nthr;
-      const int up = p.parent ? __shfl_sync(0xffffffffu, depth, u) : 0;
+      const int up = kTree ? __shfl_sync(0xffffffffu, depth, u) : 0;
       if (e < n) {
-        const int r = e / (kDr / 2), j = e % (kDr / 2), s = p.parent ? up : r % p.S;
+        const int r = e / (kDr / 2), j = e % (kDr / 2), s = kTree ? up : r % p.S;
         const int pos = (Tb[u] < p.S || Tb[u] > p.T_cap) ? 0 : Tb[u] - p.S + s;
         float sn, cs;
         rope_cs_turns(pos, p.turn[j], &cs, &sn);
@@ -962,7 +965,7 @@ __device__ __forceinline__ void absorb_regs(const uint4 (&wv)[NV], const float* 
 // NV = qk_nope / 16: W_UK registers (16-byte vectors) per thread.  kQabs =
 // false: the plan and the rotary part only (the GEMM forms qabs); a separate
 // instantiation, so that the small-batch kernel carries only its own code.
-template <int NV, bool kQabs = true, bool kPaged = false>
+template <int NV, bool kQabs = true, bool kPaged = false, bool kTree = false>
 __global__ void __launch_bounds__(kAbsThreads, 2) absorb_kernel(const AbsorbParams p) {
   extern __shared__ __align__(128) unsigned char sm[];
   const int cb = blockIdx.x, h = blockIdx.y, tid = threadIdx.x;
@@ -1046,7 +1049,7 @@ __global__ void __launch_bounds__(kAbsThreads, 2) absorb_kernel(const AbsorbPara
         }
         if (bad) raise_flag(p.flags, bad);
         p.bad[r] = bad;
-        tiles = bad ? 0 : p.tail ? pair_tiles(nk, p.S) : (nk + kTile - 1) / kTile;
+        tiles = bad ? 0 : (kTree && p.tail) ? pair_tiles(nk, p.S) : (nk + kTile - 1) / kTile;
       }
       // block inclusive scan of `tiles`
       int x = tiles;
@@ -1070,7 +1073,8 @@ __global__ void __launch_bounds__(kAbsThreads, 2) absorb_kernel(const AbsorbPara
   }
 
   if constexpr (!kQabs) {  // rotary part only, every (row, pair) in parallel over the head's CTAs
-    if (cb < p.rope_x) rope_rows(p, h, cb * kAbsThreads + tid, p.rope_x * kAbsThreads);
+    const int nx = kTree ? p.rope_x : (int)gridDim.x;
+    if (!kTree || cb < nx) rope_rows<kTree>(p, h, cb * kAbsThreads + tid, nx * kAbsThreads);
     else
       stage_tail(p, (((cb - p.rope_x) * gridDim.y + h) * kAbsThreads + tid) >> 5,
                  (gridDim.x - p.rope_x) * gridDim.y * (kAbsThreads / 32));
@@ -1092,7 +1096,7 @@ __global__ void __launch_bounds__(kAbsThreads, 2) absorb_kernel(const AbsorbPara
     p.qcat[((size_t)r * kH + h) * kDc + cb * kAbsCols + col] = __float2bfloat16_rn(v);
   }
   if (cb == 0)
-    for (int e = tid; e < R * (kDr / 2); e += kAbsThreads) rope_row(p, e / (kDr / 2), h, e % (kDr / 2));
+    for (int e = tid; e < R * (kDr / 2); e += kAbsThreads) rope_row<kTree>(p, e / (kDr / 2), h, e % (kDr / 2));
 }
 
 // ===========================================================================
@@ -1118,11 +1122,12 @@ struct CombineParams {
   void* out;  // [R, 64, Dv] float or bf16, R <= kCmbRows
   int B, S, G, Dn, Dv, sparse, T_cap, topk;
   unsigned int* flags;
-  int out_bf16;
-  const int32_t* parent;  // tree attention: [B, S] parent indices, else null
+  int out_bf16;           // tree attention only
+  const int32_t* parent;  // tree attention: [B, S] parent indices
 };
 
 
+template <bool kTree>
 __global__ void __launch_bounds__(kCmbThreads) combine_kernel(const CombineParams p) {
   extern __shared__ __align__(128) unsigned char sm[];
   const __nv_bfloat16* Ws = reinterpret_cast<const __nv_bfloat16*>(sm);   // [64][512]
@@ -1177,8 +1182,8 @@ __global__ void __launch_bounds__(kCmbThreads) combine_kernel(const CombineParam
   if (warp < nr) {
     const int r = warp, b = r / p.S, s = r % p.S;
     const int row = p.sparse ? r : b;
-    const int sr = p.parent ? p.S - 1 : s;
-    const int state = p.parent ? tree_node(p.parent + (size_t)b * p.S, s).state : kNodePresent;
+    const int sr = kTree ? p.S - 1 : s;
+    const int state = kTree ? tree_node(p.parent + (size_t)b * p.S, s).state : kNodePresent;
     int cnt = 0;
     if (!cbad[row] && N > 0) {
       const long long a = cts[row], e = cts[row + 1];
@@ -1245,7 +1250,7 @@ __global__ void __launch_bounds__(kCmbThreads) combine_kernel(const CombineParam
       }
       L = warp_sum(L);
       // an absent tree node has no visible key: L is 0 and its output zero
-      const bool none = p.parent && L == 0.f;
+      const bool none = kTree && L == 0.f;
       for (int i = lane; i < cnt; i += 32) pm[warp * kMaxPieces + i] = none ? 0.f : pm[warp * kMaxPieces + i] / L;
     }
     __syncthreads();
@@ -1366,7 +1371,7 @@ __global__ void __launch_bounds__(kCmbThreads) combine_kernel(const CombineParam
         if ((lane & 3) == 0) {
           const int jj = 4 * ((lane >> 4) & 1) + 2 * ((lane >> 3) & 1) + ((lane >> 2) & 1);
           const size_t at = ((size_t)(r0 + w) * kH + h) * p.Dv + j0 + jw + jj;
-          if (p.out_bf16) static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(d[0] * inv_l[w]);
+          if (kTree && p.out_bf16) static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(d[0] * inv_l[w]);
           else static_cast<float*>(p.out)[at] = d[0] * inv_l[w];
         }
       }
@@ -1729,7 +1734,7 @@ cudaError_t set_smem_once(Kern kern, int bytes, std::atomic<unsigned long long>*
   return e;
 }
 
-std::atomic<unsigned long long> g_abs_attr[9] = {}, g_attn_attr[14] = {}, g_cmb_attr{0};
+std::atomic<unsigned long long> g_abs_attr[18] = {}, g_attn_attr[14] = {}, g_cmb_attr[2] = {};
 
 // Whether a tree call takes the CTA-pair attention (and the GEMMs around it).
 // Up to 8 query rows can also take the GEMVs and one CTA per node, fewer and
@@ -1978,17 +1983,24 @@ cudaError_t run(const DecodeArgs& a, void* ws, bool sparse, cudaStream_t st) {
   const size_t abs_smem = (size_t)kAbsRows * g.Dn * 4 + (size_t)kAbsGroups * kAbsRows * kAbsCols * 4;
   // one instantiation per case, so that each carries only its own code
   using AbsKern = void (*)(const AbsorbParams);
-  static const AbsKern abs_kerns[2][4] = {
+  static const AbsKern abs_kerns[4][4] = {
       {absorb_kernel<4>, absorb_kernel<8>, absorb_kernel<12>, absorb_kernel<16>},
       {absorb_kernel<4, true, true>, absorb_kernel<8, true, true>, absorb_kernel<12, true, true>,
-       absorb_kernel<16, true, true>}};
+       absorb_kernel<16, true, true>},
+      {absorb_kernel<4, true, false, true>, absorb_kernel<8, true, false, true>, absorb_kernel<12, true, false, true>,
+       absorb_kernel<16, true, false, true>},
+      {absorb_kernel<4, true, true, true>, absorb_kernel<8, true, true, true>, absorb_kernel<12, true, true, true>,
+       absorb_kernel<16, true, true, true>}};
   const bool paged_abs = ap.prefetch && ap.pages.table;
-  const AbsKern akern = big ? absorb_kernel<4, false> : abs_kerns[paged_abs ? 1 : 0][g.Dn / 64 - 1];
+  const int abs_kind = (a.parent ? 2 : 0) + (paged_abs ? 1 : 0);
+  const AbsKern akern = pair  ? absorb_kernel<4, false, false, true>
+                        : big ? absorb_kernel<4, false>
+                              : abs_kerns[abs_kind][g.Dn / 64 - 1];
   // many rows: the rotary part of each head spread over up to four CTAs
   const int abs_gx = big ? std::min(pair ? 16 : 4, (pl.R * (kDr / 2) + 2047) / 2048) : kDl / kAbsCols;
   ap.rope_x = abs_gx;
   if (pair) ap.tail = reinterpret_cast<__nv_bfloat16*>(w + pl.off_tail);
-  e = set_smem_once(akern, (int)abs_smem, &g_abs_attr[big ? 8 : (paged_abs ? 4 : 0) + g.Dn / 64 - 1]);
+  e = set_smem_once(akern, (int)abs_smem, &g_abs_attr[pair ? 17 : big ? 16 : 4 * abs_kind + g.Dn / 64 - 1]);
   if (e != cudaSuccess) return e;
   kernel_mark(st, big ? "plan_rope" : "absorb");
   e = launch_pdl(akern, dim3(abs_gx + (pair ? 1 : 0), kH), dim3(kAbsThreads), abs_smem, st, ap);
@@ -2130,10 +2142,11 @@ cudaError_t run(const DecodeArgs& a, void* ws, bool sparse, cudaStream_t st) {
   cp.flags = a.flags;
   const size_t cmb_smem = (size_t)kCmbWBytes + (size_t)kCmbRows * kCPitch * 4 + kCmbRows * 8 +
                           (size_t)kCmbRows * kMaxPieces * 12 + (size_t)(kCmbThreads / 32) * 128 * 16;
-  e = set_smem_once(combine_kernel, (int)cmb_smem, &g_cmb_attr);
+  const auto ckern = a.parent ? combine_kernel<true> : combine_kernel<false>;
+  e = set_smem_once(ckern, (int)cmb_smem, &g_cmb_attr[a.parent ? 1 : 0]);
   if (e != cudaSuccess) return e;
   kernel_mark(st, "combine");
-  return launch_pdl(combine_kernel, dim3(g.Dv / kCmbJ, kH), dim3(kCmbThreads), cmb_smem, st, cp);
+  return launch_pdl(ckern, dim3(g.Dv / kCmbJ, kH), dim3(kCmbThreads), cmb_smem, st, cp);
 }
 
 }  // namespace

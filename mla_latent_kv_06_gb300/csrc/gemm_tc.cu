@@ -35,7 +35,7 @@ struct GemmParams {
   CUtensorMap mA;  // 3D {k, z, m}, box {64, 1, 128}
   CUtensorMap mB;  // 2D; K-major box {64, BN}; MN-major box {64, 64}
   long long b_row0, b_rows_per_z, b_col0;
-  int b_slabs;  // K slabs of B: slab kb of A meets slab kb % b_slabs of B
+  int b_slabs;  // K slabs of B: slab kb >= b_slabs of A meets slab kb - b_slabs of B
   void* c_base;
   long long c_ld_m, c_ld_z;
   int out_kind;
@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(kGThreads, 1) gemm_kernel(const __grid_constan
         unsigned char* sB = smem + npre * Cfg::kStage + Cfg::kA;
         mbar_arrive_expect_tx(&full_bar[npre], Cfg::kStage);
         if (!kBMN) {
-          tma_load_2d(sB, &p.mB, (int)p.b_col0 + (kb % p.b_slabs) * 64, brow + n0, &full_bar[npre]);
+          tma_load_2d(sB, &p.mB, (int)p.b_col0 + (kb < p.b_slabs ? kb : kb - p.b_slabs) * 64, brow + n0, &full_bar[npre]);
         } else {
 #pragma unroll
           for (int j = 0; j < BN / 64; ++j)
@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kGThreads, 1) gemm_kernel(const __grid_constan
           mbar_arrive_expect_tx(&full_bar[st], Cfg::kStage);
           tma_load_3d(sA, &p.mA, kb * 64, z, m0, &full_bar[st]);
           if (!kBMN) {
-            tma_load_2d(sB, &p.mB, (int)p.b_col0 + (kb % p.b_slabs) * 64, brow + n0, &full_bar[st]);
+            tma_load_2d(sB, &p.mB, (int)p.b_col0 + (kb < p.b_slabs ? kb : kb - p.b_slabs) * 64, brow + n0, &full_bar[st]);
           } else {
 #pragma unroll
             for (int j = 0; j < BN / 64; ++j)
@@ -292,7 +292,7 @@ cudaError_t launch_gemm_tc(const GemmArgs& a, bool pdl, cudaStream_t st) {
   gp.b_row0 = a.b_row0;
   gp.b_rows_per_z = a.b_rows_per_z;
   gp.b_col0 = a.b_col0;
-  if (a.b_k_wrap && (a.b_mn_major || a.b_k_wrap % 64 != 0)) return cudaErrorInvalidValue;
+  if (a.b_k_wrap && (a.b_mn_major || a.b_k_wrap % 64 != 0 || a.K > 2 * a.b_k_wrap)) return cudaErrorInvalidValue;
   gp.b_slabs = a.b_k_wrap ? a.b_k_wrap / 64 : a.K / 64;
   gp.c_base = a.c_base;
   gp.c_ld_m = a.c_ld_m;

@@ -30,7 +30,7 @@ struct GemmArgs {
   int b_mn_major;      // 0: row n holds B_z[n, :] ; 1: row k holds B_z[:, n]
   long long b_row0, b_rows_per_z;
   long long b_col0;    // first column used (MN-major: column of n = 0)
-  int b_k_wrap;        // K-major B, > 0: column k reads column k % b_k_wrap (A rows of several parts times one B)
+  int b_k_wrap;        // K-major B, > 0: column k >= b_k_wrap reads column k - b_k_wrap (A rows of two parts times one B)
   // C: element (m, z, n) at c_base + m*c_ld_m + z*c_ld_z + n
   void* c_base;
   long long c_ld_m, c_ld_z;
