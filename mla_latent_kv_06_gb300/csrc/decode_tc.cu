@@ -1737,16 +1737,18 @@ cudaError_t set_smem_once(Kern kern, int bytes, std::atomic<unsigned long long>*
 std::atomic<unsigned long long> g_abs_attr[18] = {}, g_attn_attr[14] = {}, g_cmb_attr[2] = {};
 
 // Whether a tree call takes the CTA-pair attention (and the GEMMs around it).
-// Up to 8 query rows can also take the GEMVs and one CTA per node, fewer and
-// shorter launches: measured us, that path against the pair's (nodes x keys)
-//   8 x 1024: 30.0, 37.4     8 x 4096: 38.7, 41.4     8 x 8192 (2 sequences): 64.1, 49.5
-//   8 x 16384: 62.3, 49.8    8 x 16384 (4 sequences): 94.7, 60.8
+// Up to 8 query rows can also take the GEMVs and one CTA per node: three
+// launches, but every node reads the cache for itself and a CTA walks its tiles
+// one after the other.  Measured us, that path against the pair's:
+//   1 sequence:  8 nodes x 1024 keys 29.7, 36.5;  8 x 4096 38.7, 40.3;  3 x 20000 44.2, 46.6;
+//                8 x 16384 62.3, 47.2
+//   2 and 4:     2 nodes x 2048 26.0, 37.2;  4 x 4096 46.9, 39.4;  2 x 4096 48.1, 39.3
 // With more rows the pair is ahead from short contexts (11 x 9 nodes x 248
 // keys: 64.8, 59.9; 16 nodes x 2048: 49.6, 43.4) to long ones (16 x 2 nodes x
 // 16384: 289.8, 112.8), at worst 5% behind (32 x 64 nodes on 90 keys).
 bool pair_pays(int B, int S, int T_cap) {
   if ((long long)B * S > kSmallRows) return true;
-  return S >= 2 && (long long)B * S * T_cap >= 65536;
+  return S >= 2 && (long long)B * S * T_cap >= (B > 1 ? 32768 : 65536);
 }
 
 Plan make_plan(int B, int S, int T_cap, int sparse_topk, bool tree = false) {
