@@ -824,7 +824,7 @@ struct AbsorbParams {
   unsigned int* flags;
   PageTable pages;
   const int32_t* parent;  // tree attention: [B, S] parent indices
-  int rope_x;             // blocks along x that form the rotary part (many rows); any more stage the tails
+  int rope_x;             // tree: blocks along x that work on the head; any more stage the tails
   __nv_bfloat16* tail;    // pair attention: staged tail rows [B, kPairStage, 576], else null
 };
 
@@ -979,6 +979,13 @@ __global__ void __launch_bounds__(kAbsThreads, 2) absorb_kernel(const AbsorbPara
   // first; everything else waits for that kernel.
   const int c8 = tid % (kAbsCols / 8), grp = tid / (kAbsCols / 8);
   uint4 wv[NV];
+  const int nx = kTree ? p.rope_x : (int)gridDim.x;
+  if (kTree && cb >= nx) {  // the blocks past the head's own stage the tails
+    grid_dep_wait();
+    grid_dep_launch();
+    stage_tail(p, (((cb - nx) * gridDim.y + h) * kAbsThreads + tid) >> 5, (gridDim.x - nx) * gridDim.y * (kAbsThreads / 32));
+    return;
+  }
   if (kQabs) {
     const __nv_bfloat16* W = p.kv_b + (size_t)h * (Dn + p.Dv) * kDl + cb * kAbsCols + c8 * 8;
 #pragma unroll
@@ -994,7 +1001,7 @@ __global__ void __launch_bounds__(kAbsThreads, 2) absorb_kernel(const AbsorbPara
     // place it (lengths clamped to [0, T_cap], pages checked against the
     // pool), so values an earlier kernel is still writing can at worst
     // prefetch the wrong rows.
-    const int nblk = gridDim.x * gridDim.y, me = h * gridDim.x + cb;
+    const int nblk = nx * gridDim.y, me = h * nx + cb;
     // Paged caches: units of 16 KB, nine per key tile (eight 16-row blocks of
     // latent rows, then the tile's rope rows), dealt round-robin to the CTAs.
     for (int b = 0, base = 0; kPaged && b < p.B; ++b) {
@@ -1020,8 +1027,8 @@ __global__ void __launch_bounds__(kAbsThreads, 2) absorb_kernel(const AbsorbPara
       if (l1 > l0) l2_prefetch(lbase + l0, (uint32_t)(l1 - l0));
       if (r1 > r0) l2_prefetch(rbase + r0, (uint32_t)(r1 - r0));
     }
-    const __nv_bfloat16* wuv = p.kv_b + ((size_t)h * (p.Dn + p.Dv) + p.Dn + (size_t)cb * (p.Dv / gridDim.x)) * kDl;
-    l2_prefetch(wuv, (uint32_t)(p.Dv / gridDim.x) * kDl * 2);
+    const __nv_bfloat16* wuv = p.kv_b + ((size_t)h * (p.Dn + p.Dv) + p.Dn + (size_t)cb * (p.Dv / nx)) * kDl;
+    l2_prefetch(wuv, (uint32_t)(p.Dv / nx) * kDl * 2);
   }
   grid_dep_wait();
   grid_dep_launch();
@@ -1073,11 +1080,7 @@ __global__ void __launch_bounds__(kAbsThreads, 2) absorb_kernel(const AbsorbPara
   }
 
   if constexpr (!kQabs) {  // rotary part only, every (row, pair) in parallel over the head's CTAs
-    const int nx = kTree ? p.rope_x : (int)gridDim.x;
-    if (!kTree || cb < nx) rope_rows<kTree>(p, h, cb * kAbsThreads + tid, nx * kAbsThreads);
-    else
-      stage_tail(p, (((cb - p.rope_x) * gridDim.y + h) * kAbsThreads + tid) >> 5,
-                 (gridDim.x - p.rope_x) * gridDim.y * (kAbsThreads / 32));
+    rope_rows<kTree>(p, h, cb * kAbsThreads + tid, nx * kAbsThreads);
     return;
   }
   // R <= kAbsRows here (larger batches take the GEMM path)
@@ -1122,7 +1125,8 @@ struct CombineParams {
   void* out;  // [R, 64, Dv] float or bf16, R <= kCmbRows
   int B, S, G, Dn, Dv, sparse, T_cap, topk;
   unsigned int* flags;
-  int out_bf16;           // tree attention only
+  int out_bf16;           // tree attention only, like the next two
+  int pair;               // partials of the pair attention
   const int32_t* parent;  // tree attention: [B, S] parent indices
 };
 
@@ -1167,7 +1171,7 @@ __global__ void __launch_bounds__(kCmbThreads) combine_kernel(const CombineParam
       bad = (nk < 1 || nk > p.topk) ? 1 : 0;
     }
     cbad[tid] = bad;
-    cts[tid + 1] = bad ? 0 : (nk + kTile - 1) / kTile;
+    cts[tid + 1] = bad ? 0 : (kTree && p.pair) ? pair_tiles(nk, p.S) : (nk + kTile - 1) / kTile;
   }
   __syncthreads();
   if (tid == 0) {
@@ -1192,7 +1196,7 @@ __global__ void __launch_bounds__(kCmbThreads) combine_kernel(const CombineParam
         const int gg = g0 + lane;
         int lo = 0, hi = 0;
         if (gg <= ghi) {
-          if (p.sparse) piece_range<true>(cts, p.T, p.S, s, row, gg, p.G, N, &lo, &hi);
+          if (p.sparse || (kTree && p.pair)) piece_range<true>(cts, p.T, p.S, s, row, gg, p.G, N, &lo, &hi);
           else piece_range<false>(cts, p.T, p.S, sr, row, gg, p.G, N, &lo, &hi);
         }
         const bool has = lo < hi;
@@ -1704,7 +1708,7 @@ __global__ void __launch_bounds__(256) gather_kernel(const GatherParams p) {
 // ===========================================================================
 struct Plan {
   int G, NR, P, R, Kpad;
-  int Gp;  // tree attention with many rows: chunks of the pair kernel
+  int Gp;  // pair attention of a tree: its chunks
   size_t off_q, off_ts, off_bad, off_o, off_ml, off_stage, off_clat, off_invl, off_q8, off_fh, off_tail, total;
 };
 
@@ -1736,19 +1740,20 @@ cudaError_t set_smem_once(Kern kern, int bytes, std::atomic<unsigned long long>*
 
 std::atomic<unsigned long long> g_abs_attr[18] = {}, g_attn_attr[14] = {}, g_cmb_attr[2] = {};
 
-// Whether a tree call takes the CTA-pair attention (and the GEMMs around it).
-// Up to 8 query rows can also take the GEMVs and one CTA per node: three
-// launches, but every node reads the cache for itself and a CTA walks its tiles
-// one after the other.  Measured us, that path against the pair's:
-//   1 sequence:  8 nodes x 1024 keys 29.7, 36.5;  8 x 4096 38.7, 40.3;  3 x 20000 44.2, 46.6;
-//                8 x 16384 62.3, 47.2
-//   2 and 4:     2 nodes x 2048 26.0, 37.2;  4 x 4096 46.9, 39.4;  2 x 4096 48.1, 39.3
+// Whether a tree call takes the CTA-pair attention.  Up to 8 query rows can also
+// take one CTA per node, as plain decode does: it starts sooner, but every node
+// reads the cache for itself and a CTA walks its tiles one after the other.
+// Measured us of the whole call, one CTA per node against the pair:
+//   1 sequence: 8 nodes x 512 keys 28.3, 32.2;  8 x 2048 32.2, 34.1;  2 x 8192 27.0, 28.1;
+//               8 x 4096 38.6, 36.6;  4 x 8192 35.5, 32.8;  3 x 20000 44.6, 37.3;
+//               2 x 30000 45.6, 35.9
+//   2 and 4:    4 nodes x 1024 33.4, 34.0;  2 x 2048 37.0, 36.0;  2 x 4096 48.1, 38.6
 // With more rows the pair is ahead from short contexts (11 x 9 nodes x 248
 // keys: 64.8, 59.9; 16 nodes x 2048: 49.6, 43.4) to long ones (16 x 2 nodes x
 // 16384: 289.8, 112.8), at worst 5% behind (32 x 64 nodes on 90 keys).
 bool pair_pays(int B, int S, int T_cap) {
   if ((long long)B * S > kSmallRows) return true;
-  return S >= 2 && (long long)B * S * T_cap >= (B > 1 ? 32768 : 65536);
+  return S >= 2 && (long long)B * S * T_cap >= 24576;
 }
 
 Plan make_plan(int B, int S, int T_cap, int sparse_topk, bool tree = false) {
@@ -1773,10 +1778,9 @@ Plan make_plan(int B, int S, int T_cap, int sparse_topk, bool tree = false) {
     pl.G = (int)G;
     pl.P = pl.G + pl.R - 1;
   }
-  const bool many_tree = tree && pair_pays(B, S, T_cap);
-  const bool many = pl.R > kSmallRows || many_tree;
-  if (many_tree) {
-    pl.Gp = pair_chunks(B, S, T_cap, sms);
+  const bool pair = tree && pair_pays(B, S, T_cap);
+  if (pair) {
+    pl.Gp = std::min(pair_chunks(B, S, T_cap, sms), kMaxPieces);
     pl.P = std::max(pl.P, (pl.Gp + B - 1) * S);
   }
   size_t off = 0;
@@ -1794,16 +1798,16 @@ Plan make_plan(int B, int S, int T_cap, int sparse_topk, bool tree = false) {
   pl.off_stage = off;  // two staging buffers: consecutive layers of one call alternate
   off = align256(off + 2 * (size_t)pl.R * pl.Kpad * kDc * 2);
   pl.off_clat = off;
-  off = align256(off + (many ? (size_t)pl.R * kH * kDl * (many_tree ? 4 : 2) : 0));
+  off = align256(off + (pl.R > kSmallRows ? (size_t)pl.R * kH * kDl * (pair ? 4 : 2) : 0));
   pl.off_invl = off;
-  off = align256(off + (many ? (size_t)pl.R * kH * 4 : 0));
+  off = align256(off + (pl.R > kSmallRows ? (size_t)pl.R * kH * 4 : 0));
   // FP8 cache (dense only): quantised query rows and their score factors
   pl.off_q8 = off;
   off = align256(off + (sparse_topk || tree ? 0 : (size_t)pl.R * kH * kQ8Row));
   pl.off_fh = off;
   off = align256(off + (sparse_topk || tree ? 0 : (size_t)pl.R * kH * 4));
   pl.off_tail = off;
-  off = align256(off + (many_tree ? (size_t)B * kPairStage * kDc * 2 : 0));
+  off = align256(off + (pair ? (size_t)B * kPairStage * kDc * 2 : 0));
   pl.total = off;
   return pl;
 }
@@ -1964,7 +1968,7 @@ cudaError_t run(const DecodeArgs& a, void* ws, bool sparse, cudaStream_t st) {
   ap.topk = a.topk;
   ap.sparse = sparse ? 1 : 0;
   const bool pair = a.parent && pair_pays(B, S, a.T_cap);
-  const bool big = pl.R > kSmallRows || pair;
+  const bool big = pl.R > kSmallRows;
   ap.Lc = static_cast<const unsigned char*>(a.Lc);
   ap.Rc = static_cast<const __nv_bfloat16*>(a.Rc);
   ap.lat_row_bytes = a.lat_fp8 ? kDl : kDl * 2;
@@ -1995,14 +1999,13 @@ cudaError_t run(const DecodeArgs& a, void* ws, bool sparse, cudaStream_t st) {
        absorb_kernel<16, true, true, true>}};
   const bool paged_abs = ap.prefetch && ap.pages.table;
   const int abs_kind = (a.parent ? 2 : 0) + (paged_abs ? 1 : 0);
-  const AbsKern akern = pair  ? absorb_kernel<4, false, false, true>
-                        : big ? absorb_kernel<4, false>
-                              : abs_kerns[abs_kind][g.Dn / 64 - 1];
+  const AbsKern akern = big ? (a.parent ? absorb_kernel<4, false, false, true> : absorb_kernel<4, false>)
+                            : abs_kerns[abs_kind][g.Dn / 64 - 1];
   // many rows: the rotary part of each head spread over up to four CTAs
-  const int abs_gx = big ? std::min(pair ? 16 : 4, (pl.R * (kDr / 2) + 2047) / 2048) : kDl / kAbsCols;
+  const int abs_gx = big ? std::min(a.parent ? 16 : 4, (pl.R * (kDr / 2) + 2047) / 2048) : kDl / kAbsCols;
   ap.rope_x = abs_gx;
   if (pair) ap.tail = reinterpret_cast<__nv_bfloat16*>(w + pl.off_tail);
-  e = set_smem_once(akern, (int)abs_smem, &g_abs_attr[pair ? 17 : big ? 16 : 4 * abs_kind + g.Dn / 64 - 1]);
+  e = set_smem_once(akern, (int)abs_smem, &g_abs_attr[big ? (a.parent ? 17 : 16) : 4 * abs_kind + g.Dn / 64 - 1]);
   if (e != cudaSuccess) return e;
   kernel_mark(st, big ? "plan_rope" : "absorb");
   e = launch_pdl(akern, dim3(abs_gx + (pair ? 1 : 0), kH), dim3(kAbsThreads), abs_smem, st, ap);
@@ -2055,75 +2058,75 @@ cudaError_t run(const DecodeArgs& a, void* ws, bool sparse, cudaStream_t st) {
   if (pair) {
     e = run_pair(a, pl, w, pool_rows, st);
     if (e != cudaSuccess) return e;
-    return run_lift(a, pl, w, sparse, true, st);
-  }
-  AttnParams tp{};
-  bool maps_ok = a.lat_fp8 ? make_tmap_2d_u8(&tp.mQ, q8, (uint64_t)pl.R * kH, kQ8Row, kQ8Row, kH, 128)
-                           : make_tmap_2d_bf16(&tp.mQ, qcat, (uint64_t)pl.R * kH, kDc, kDc, kH, 64);
-  if (!sparse) {
-    const uint64_t rows = (uint64_t)pool_rows;
-    maps_ok = maps_ok &&
-              (a.lat_fp8 ? make_tmap_2d_u8(&tp.mL, a.Lc, rows, kDl, kDl, kTile, 128)
-                         : make_tmap_2d_bf16(&tp.mL, a.Lc, rows, kDl, kDl, kTile, 64)) &&
-              make_tmap_2d_bf16(&tp.mR, a.Rc, rows, kDr, kDr, kTile, 64);
-    tp.kv_rows = a.T_cap;
   } else {
-    const uint64_t rows = (uint64_t)pl.R * pl.Kpad;
-    maps_ok = maps_ok && make_tmap_2d_bf16(&tp.mL, stage, rows, kDl, kDc, kTile, 64) &&
-              make_tmap_2d_bf16(&tp.mR, stage + kDl, rows, kDr, kDc, kTile, 64);
-    tp.kv_rows = pl.Kpad;
+    AttnParams tp{};
+    bool maps_ok = a.lat_fp8 ? make_tmap_2d_u8(&tp.mQ, q8, (uint64_t)pl.R * kH, kQ8Row, kQ8Row, kH, 128)
+                             : make_tmap_2d_bf16(&tp.mQ, qcat, (uint64_t)pl.R * kH, kDc, kDc, kH, 64);
+    if (!sparse) {
+      const uint64_t rows = (uint64_t)pool_rows;
+      maps_ok = maps_ok &&
+                (a.lat_fp8 ? make_tmap_2d_u8(&tp.mL, a.Lc, rows, kDl, kDl, kTile, 128)
+                           : make_tmap_2d_bf16(&tp.mL, a.Lc, rows, kDl, kDl, kTile, 64)) &&
+                make_tmap_2d_bf16(&tp.mR, a.Rc, rows, kDr, kDr, kTile, 64);
+      tp.kv_rows = a.T_cap;
+    } else {
+      const uint64_t rows = (uint64_t)pl.R * pl.Kpad;
+      maps_ok = maps_ok && make_tmap_2d_bf16(&tp.mL, stage, rows, kDl, kDc, kTile, 64) &&
+                make_tmap_2d_bf16(&tp.mR, stage + kDl, rows, kDr, kDc, kTile, 64);
+      tp.kv_rows = pl.Kpad;
+    }
+    if (!maps_ok) return cudaErrorInvalidValue;
+    tp.T = a.T;
+    tp.sel = a.sel;
+    tp.nsel = a.nsel;
+    tp.tile_start = ts;
+    tp.B = B;
+    tp.S = S;
+    tp.T_cap = a.T_cap;
+    tp.G = pl.G;
+    tp.topk = a.topk;
+    // Few pieces leave SMs idle: then 2 or 4 CTAs share a piece, each repeating
+    // the score product (the tile comes from L2 after the first) and taking its
+    // share of the value product and of the partial's stores.
+    const int pieces = sparse ? pl.G : pl.G * S;
+    const int sms = sm_count();
+    tp.qsplit = pieces * 4 <= sms ? 4 : pieces * 2 <= sms ? 2 : 1;
+    tp.read_once = ((sparse || S == 1) && tp.qsplit == 1) ? 1 : 0;
+    tp.c = g.scale * kLog2e;
+    tp.lat_scale = a.lat_fp8 ? a.lat_scale : 1.f;
+    tp.fh = fh;
+    tp.qcat = qcat;
+    tp.o_part = o_part;
+    tp.ml_part = ml_part;
+    tp.flags = a.flags;
+    tp.wait_ns = a.wait_limit_ns;
+    tp.pages = sparse ? PageTable{} : a.pages;
+    tp.parent = a.parent;
+    // Streaming launches (one CTA per piece, at least two tiles a CTA by the
+    // T_cap bound) take the instantiation with the single-lane score loop.
+    const long long tiles_cap = (long long)B * ((a.T_cap + kTile - 1) / kTile);
+    const bool stream = !sparse && tp.qsplit == 1 && tiles_cap >= 2LL * pl.G;
+    auto kern = sparse     ? attn_kernel<true>
+                : a.parent ? (paged ? (stream ? attn_kernel<false, true, true, true> : attn_kernel<false, true, false, true>)
+                                    : (stream ? attn_kernel<false, false, true, true>
+                                              : attn_kernel<false, false, false, true>))
+                : a.lat_fp8 ? (big ? (stream ? attn8_kernel<false, true> : attn8_kernel<false>)
+                                   : (stream ? attn8_kernel<true, true> : attn8_kernel<true>))
+                : paged     ? (stream ? attn_kernel<false, true, true> : attn_kernel<false, true>)
+                            : (stream ? attn_kernel<false, false, true> : attn_kernel<false>);
+    const uint32_t attn_smem = a.lat_fp8 ? kAttn8DynSmem : kAttnDynSmem;
+    const int attr_slot = a.parent ? 10 + (paged ? 1 : 0) + (stream ? 2 : 0)
+                                   : (sparse ? 1 : a.lat_fp8 ? (big ? 2 : 4) : paged ? 3 : 0) + (stream ? 5 : 0);
+    e = set_smem_once(kern, (int)attn_smem, &g_attn_attr[attr_slot]);
+    if (e != cudaSuccess) return e;
+    const int nblk = pieces * tp.qsplit;
+    kernel_mark(st, "attention");
+    e = launch_pdl(kern, dim3(nblk), dim3(kAttnThreads), attn_smem, st, tp);
+    if (e != cudaSuccess) return e;
   }
-  if (!maps_ok) return cudaErrorInvalidValue;
-  tp.T = a.T;
-  tp.sel = a.sel;
-  tp.nsel = a.nsel;
-  tp.tile_start = ts;
-  tp.B = B;
-  tp.S = S;
-  tp.T_cap = a.T_cap;
-  tp.G = pl.G;
-  tp.topk = a.topk;
-  // Few pieces leave SMs idle: then 2 or 4 CTAs share a piece, each repeating
-  // the score product (the tile comes from L2 after the first) and taking its
-  // share of the value product and of the partial's stores.
-  const int pieces = sparse ? pl.G : pl.G * S;
-  const int sms = sm_count();
-  tp.qsplit = pieces * 4 <= sms ? 4 : pieces * 2 <= sms ? 2 : 1;
-  tp.read_once = ((sparse || S == 1) && tp.qsplit == 1) ? 1 : 0;
-  tp.c = g.scale * kLog2e;
-  tp.lat_scale = a.lat_fp8 ? a.lat_scale : 1.f;
-  tp.fh = fh;
-  tp.qcat = qcat;
-  tp.o_part = o_part;
-  tp.ml_part = ml_part;
-  tp.flags = a.flags;
-  tp.wait_ns = a.wait_limit_ns;
-  tp.pages = sparse ? PageTable{} : a.pages;
-  tp.parent = a.parent;
-  // Streaming launches (one CTA per piece, at least two tiles a CTA by the
-  // T_cap bound) take the instantiation with the single-lane score loop.
-  const long long tiles_cap = (long long)B * ((a.T_cap + kTile - 1) / kTile);
-  const bool stream = !sparse && tp.qsplit == 1 && tiles_cap >= 2LL * pl.G;
-  auto kern = sparse     ? attn_kernel<true>
-              : a.parent ? (paged ? (stream ? attn_kernel<false, true, true, true> : attn_kernel<false, true, false, true>)
-                                  : (stream ? attn_kernel<false, false, true, true>
-                                            : attn_kernel<false, false, false, true>))
-              : a.lat_fp8 ? (big ? (stream ? attn8_kernel<false, true> : attn8_kernel<false>)
-                                 : (stream ? attn8_kernel<true, true> : attn8_kernel<true>))
-              : paged     ? (stream ? attn_kernel<false, true, true> : attn_kernel<false, true>)
-                          : (stream ? attn_kernel<false, false, true> : attn_kernel<false>);
-  const uint32_t attn_smem = a.lat_fp8 ? kAttn8DynSmem : kAttnDynSmem;
-  const int attr_slot = a.parent ? 10 + (paged ? 1 : 0) + (stream ? 2 : 0)
-                                 : (sparse ? 1 : a.lat_fp8 ? (big ? 2 : 4) : paged ? 3 : 0) + (stream ? 5 : 0);
-  e = set_smem_once(kern, (int)attn_smem, &g_attn_attr[attr_slot]);
-  if (e != cudaSuccess) return e;
-  const int nblk = pieces * tp.qsplit;
-  kernel_mark(st, "attention");
-  e = launch_pdl(kern, dim3(nblk), dim3(kAttnThreads), attn_smem, st, tp);
-  if (e != cudaSuccess) return e;
 
   // 3. merge of the splits and the W_UV lift
-  if (big) return run_lift(a, pl, w, sparse, false, st);
+  if (big) return run_lift(a, pl, w, sparse, pair, st);
   CombineParams cp{};
   cp.kv_b = static_cast<const __nv_bfloat16*>(a.kv_b);
   cp.o_part = o_part;
@@ -2135,12 +2138,13 @@ cudaError_t run(const DecodeArgs& a, void* ws, bool sparse, cudaStream_t st) {
   cp.out = a.out;
   cp.B = B;
   cp.S = S;
-  cp.G = pl.G;
+  cp.G = pair ? pl.Gp : pl.G;
   cp.Dn = g.Dn;
   cp.Dv = g.Dv;
   cp.sparse = sparse ? 1 : 0;
   cp.parent = a.parent;
   cp.out_bf16 = a.out_bf16;
+  cp.pair = pair ? 1 : 0;
   cp.flags = a.flags;
   const size_t cmb_smem = (size_t)kCmbWBytes + (size_t)kCmbRows * kCPitch * 4 + kCmbRows * 8 +
                           (size_t)kCmbRows * kMaxPieces * 12 + (size_t)(kCmbThreads / 32) * 128 * 16;
