@@ -505,12 +505,14 @@ int mla_tree_verify(int B, int S, int V, const float* p, long long p_row, long l
 
 /* Commit of an accepted path: in each of n caches,
  *   row T[b] - S + i  <-  row T[b] - S + path[b, i],   i < n_acc[b]
- * and T_out[b] = T[b] - S + n_acc[b] (may be NULL; must not be T itself).
+ * and T_out[b] = T[b] - S + n_acc[b] (may be NULL; must not
+ * overlap T, path or n_acc).
  * path must increase within [0, S), as mla_tree_verify writes it.
  *   cache     HOST array of n device pointers, each [B, T_cap, row] (or a pool
  *             [num_pages, page_size, row]) with rows of row_bytes[i] bytes:
  *             every layer's Lc, Rc, Ic, FP8 codes, in any mix; all share T_cap
- *             (the pool's pages and table).  The array is read during the call only.
+ *             (the pool's pages and table).  No two may overlap, and in a
+ *             pool the tree's rows must lie in pages of one sequence only.  The array is read during the call only.
  *   row_bytes HOST array of n row sizes, >= 1 (multiples of 16 move fastest)
  * One launch serves 128 caches.  A bad length leaves the sequence and its
  * T_out = T as they were (MLA_DEV_BAD_LENGTH); a bad count, path or page

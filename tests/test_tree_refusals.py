@@ -60,7 +60,7 @@ def test_verify(lib):
 
 
 def test_commit(lib):
-    arr, hole = (ctypes.c_void_p * 2)(256, 512), (ctypes.c_void_p * 2)(256, None)
+    arr, hole = (ctypes.c_void_p * 2)(1 << 20, 2 << 20), (ctypes.c_void_p * 2)(1 << 20, None)
     size, zero = (ctypes.c_int * 2)(1024, 128), (ctypes.c_int * 2)(1024, 0)
 
     def call(n=2, cache=arr, rb=size, B=1, S=2, T_cap=16, T=P, path=P, n_acc=P, T_out=ctypes.c_void_p(1024)):
@@ -70,6 +70,30 @@ def test_commit(lib):
                 dict(S=17), dict(T=None), dict(path=None), dict(n_acc=None), dict(T_out=P)):
         assert call(**bad) == mla.MLA_ERR_INVALID, bad
     assert lib.mla_tree_commit_paged(2, arr, size, 1, 2, 4, 16, None, 2, P, P, P, None, None) == mla.MLA_ERR_INVALID
+
+
+@pytest.mark.parametrize("second,row_bytes,B,bad", [(1 << 20, 128, 1, True), ((1 << 20) + 16 * 1024 - 1, 128, 1, True),
+                                                    ((1 << 20) - 16 * 128 + 1, 128, 1, True),
+                                                    ((1 << 20) + 16 * 1024, 128, 2, True)])
+@pytest.mark.parametrize("paged", [False, True])
+def test_commit_refuses_caches_that_overlap(lib, second, row_bytes, B, bad, paged):
+    """The same cache twice, or caches of 16 rows per sequence that share bytes, would have rows moved twice."""
+    arr, size = (ctypes.c_void_p * 2)(1 << 20, second), (ctypes.c_int * 2)(1024, row_bytes)
+    x, y, z = (ctypes.c_void_p(i << 30) for i in (1, 2, 3))
+    if paged:
+        rc = lib.mla_tree_commit_paged(2, arr, size, B, 2, 4 * B, 4, ctypes.c_void_p(5 << 30), 4, x, y, z, None, None)
+    else:
+        rc = lib.mla_tree_commit(2, arr, size, B, 2, 16, x, y, z, None, None)
+    assert rc == mla.MLA_ERR_INVALID and b"overlaps" in lib.mla_last_error()
+
+
+def test_commit_refuses_lengths_over_its_arguments(lib):
+    arr, size = (ctypes.c_void_p * 1)(1 << 20), (ctypes.c_int * 1)(1024)
+    B, S, T, path, n = 3, 4, 1 << 30, 2 << 30, 3 << 30
+    for at in (T, T + 8, T - 8, path, path + 4 * B * S - 4, n, n - 4):
+        rc = lib.mla_tree_commit(1, arr, size, B, S, 16, ctypes.c_void_p(T), ctypes.c_void_p(path), ctypes.c_void_p(n),
+                                 ctypes.c_void_p(at), None)
+        assert rc == mla.MLA_ERR_INVALID and b"T_out" in lib.mla_last_error(), at
 
 
 def test_binding_refuses_on_the_host(lib):
