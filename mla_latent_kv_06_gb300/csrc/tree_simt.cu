@@ -232,7 +232,8 @@ __global__ void __launch_bounds__(kThreads) tree_attend_kernel(const __grid_cons
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const float x = seen[i] ? expf(sc[i] - mn) : 0.f;
+      // a visible key with a score of -inf holds values that are not finite: NaN, not weight 0
+      const float x = !seen[i] ? 0.f : sc[i] > -INFINITY ? expf(sc[i] - mn) : qnan();
       ps[rr * kKeys + tl + 16 * i] = x;
       sum += x;
     }
