@@ -591,13 +591,15 @@ def _explain(device, **named):
             raise ValueError(f"{name} must be contiguous")
 
 
-def _stream_on(torch, index, stream):
-    """Stream handle for a call on GPU `index` (-1: the CPU), which has to be the current one."""
+def _current_stream(torch, index):
+    """Handle of the current stream for a call on GPU `index` (-1: the CPU), which has to be the
+    current one.  A call with a stream= makes that stream current first, so that outputs and
+    scratch it allocates belong to the stream that uses them."""
     if index < 0:
         raise ValueError("tensors must live on the GPU")
     if index != torch._C._cuda_getDevice():
         raise ValueError(f"tensors on GPU {index}: make it the current device")
-    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(index)
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def _want(name, t, *shape):
@@ -656,12 +658,15 @@ def decode_tree(q, Lc, Rc, T, parent, kv_b, dims, out=None, out_dtype=None, work
     out_dtype (float32 unless given; bfloat16 is rounded once).  A workspace that is given
     must have decode_tree_workspace_size() bytes."""
     torch = _torch()
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return decode_tree(q, Lc, Rc, T, parent, kv_b, dims, out, out_dtype, workspace)
     B, S = q.shape[0], q.shape[1]
     T_cap = Lc.shape[1]
     if Lc.shape[0] != B:
         raise ValueError(f"cache of {Lc.shape[0]} sequences for {B} queries")
     d, code, out, out_code, ws, wsb = _tree_args(torch, q, Lc, Rc, T, parent, kv_b, dims, out, out_dtype, workspace, T_cap)
-    st = _stream_on(torch, q.get_device(), stream)
+    st = _current_stream(torch, q.get_device())
     _check(lib().mla_decode_tree(ctypes.byref(d), code, B, S, q.data_ptr(), Lc.data_ptr(), Rc.data_ptr(), T_cap,
                                  T.data_ptr(), parent.data_ptr(), kv_b.data_ptr(), out_code, out.data_ptr(), ws, wsb, st))
     return out
@@ -671,6 +676,9 @@ def decode_tree_paged(q, Lc_pages, Rc_pages, block_table, T, parent, kv_b, dims,
                       workspace=None, stream=None):
     """decode_tree over page pools (layouts as for decode_paged)."""
     torch = _torch()
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return decode_tree_paged(q, Lc_pages, Rc_pages, block_table, T, parent, kv_b, dims, out, out_dtype, workspace)
     B, S = q.shape[0], q.shape[1]
     num_pages, page_size = Lc_pages.shape[0], Lc_pages.shape[1]
     max_pages = block_table.shape[1]
@@ -678,7 +686,7 @@ def decode_tree_paged(q, Lc_pages, Rc_pages, block_table, T, parent, kv_b, dims,
     _explain(q.device, block_table=(block_table, torch.int32))
     d, code, out, out_code, ws, wsb = _tree_args(torch, q, Lc_pages, Rc_pages, T, parent, kv_b, dims, out, out_dtype, workspace,
                                        max_pages * page_size)
-    st = _stream_on(torch, q.get_device(), stream)
+    st = _current_stream(torch, q.get_device())
     _check(lib().mla_decode_tree_paged(ctypes.byref(d), code, B, S, q.data_ptr(), Lc_pages.data_ptr(),
                                        Rc_pages.data_ptr(), num_pages, page_size, block_table.data_ptr(), max_pages,
                                        T.data_ptr(), parent.data_ptr(), kv_b.data_ptr(), out_code, out.data_ptr(), ws,
@@ -706,10 +714,13 @@ def cache_append_tree(comp, kv_a_ln, T, parent, Lc, Rc, dims, rms_eps: float, st
     """cache_append of a drafted tree: node s goes to row T[b]-S+s with the rotary
     position of its depth; rows of absent nodes (parent -2) are left as they were."""
     torch = _torch()
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return cache_append_tree(comp, kv_a_ln, T, parent, Lc, Rc, dims, rms_eps)
     B, S, d, code = _append_tree_args(torch, comp, kv_a_ln, T, parent, Lc, Rc, dims)
     if Lc.shape[0] != B:
         raise ValueError(f"cache of {Lc.shape[0]} sequences for {B} rows")
-    st = _stream_on(torch, comp.get_device(), stream)
+    st = _current_stream(torch, comp.get_device())
     _check(lib().mla_cache_append_tree(ctypes.byref(d), code, B, S, comp.data_ptr(), kv_a_ln.data_ptr(), rms_eps,
                                        Lc.shape[1], T.data_ptr(), parent.data_ptr(), Lc.data_ptr(), Rc.data_ptr(), st))
     return Lc, Rc
@@ -719,10 +730,13 @@ def cache_append_tree_paged(comp, kv_a_ln, block_table, T, parent, Lc_pages, Rc_
                             stream=None):
     """cache_append_tree into the page pools (in place)."""
     torch = _torch()
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return cache_append_tree_paged(comp, kv_a_ln, block_table, T, parent, Lc_pages, Rc_pages, dims, rms_eps)
     B, S, d, code = _append_tree_args(torch, comp, kv_a_ln, T, parent, Lc_pages, Rc_pages, dims)
     _want("block_table", block_table, B, block_table.shape[1])
     _explain(comp.device, block_table=(block_table, torch.int32))
-    st = _stream_on(torch, comp.get_device(), stream)
+    st = _current_stream(torch, comp.get_device())
     _check(lib().mla_cache_append_tree_paged(ctypes.byref(d), code, B, S, comp.data_ptr(), kv_a_ln.data_ptr(), rms_eps,
                                              Lc_pages.data_ptr(), Rc_pages.data_ptr(), Lc_pages.shape[0],
                                              Lc_pages.shape[1], block_table.data_ptr(), block_table.shape[1],
@@ -739,6 +753,9 @@ def tree_verify(p, q, tokens, parent, u, path=None, n_acc=None, token=None, stre
     [B,S] int32; u [B,S+1] float32 in [0,1).  Returns (path [B,S] accepted nodes then -1,
     n_acc [B], token [B]), all int32."""
     torch = _torch()
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return tree_verify(p, q, tokens, parent, u, path, n_acc, token)
     B, S = shape = tokens.shape
     index, f32, i32 = p.get_device(), torch.float32, torch.int32
     want = (B, S + 1, p.shape[2])
@@ -757,7 +774,7 @@ def tree_verify(p, q, tokens, parent, u, path=None, n_acc=None, token=None, stre
         _want("u", u, B, S + 1)
     if not (_all_plain(index, i32, tokens, parent) and _all_plain(index, f32, u)):
         _explain(p.device, tokens=(tokens, i32), parent=(parent, i32), u=(u, f32))
-    st = _stream_on(torch, index, stream)
+    st = _current_stream(torch, index)
     if path is None:
         path = torch.empty_like(tokens)
     else:
@@ -815,6 +832,9 @@ def tree_commit(rows: CacheRows, T, path, n_acc, T_out=None, stream=None):
     """Moves the rows of the accepted nodes (path, n_acc of tree_verify) to the front of the
     tree's rows in every cache of `rows`; returns T_out [B] int32 = T - S + n_acc."""
     torch = _torch()
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return tree_commit(rows, T, path, n_acc, T_out)
     B, S = path.shape
     index, i32, shape = rows.index, torch.int32, (B,)
     if B != rows.B:
@@ -824,7 +844,7 @@ def tree_commit(rows: CacheRows, T, path, n_acc, T_out=None, stream=None):
         _want("n_acc", n_acc, B)
     if not _all_plain(index, i32, T, path, n_acc):
         _explain(rows.device, T=(T, i32), path=(path, i32), n_acc=(n_acc, i32))
-    st = _stream_on(torch, index, stream)
+    st = _current_stream(torch, index)
     if T_out is None:
         T_out = torch.empty_like(T)
     else:
