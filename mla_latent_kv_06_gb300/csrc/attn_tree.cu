@@ -702,6 +702,7 @@ int pair_chunks(int B, int S, int T_cap, int sms) {
     long long g = (long long)rounds * clusters / np;
     if (g < 1) g = 1;
     if (g > tiles) g = tiles;
+    if (g > kPairChunks) break;
     const long long turns = (g * np + clusters - 1) / clusters;
     const double us = turns * 3.1 * ((double)tiles / g + 2.0) + 0.05 * (double)(g + B - 1) * S;
     if (us < least) {

@@ -40,7 +40,8 @@ struct PairParams {
   PageTable pages;
 };
 
-// Clusters (CTA pairs) per chunk-and-pair grid: chunks of the tile list.
+// Chunks of the tile list, at most kPairChunks (the few-row combine lists a row's splits).
+constexpr int kPairChunks = 256;
 int pair_chunks(int B, int S, int T_cap, int sms);
 
 cudaError_t launch_attn_pair(const PairParams& p, cudaStream_t st);

@@ -1780,7 +1780,8 @@ Plan make_plan(int B, int S, int T_cap, int sparse_topk, bool tree = false) {
   }
   const bool pair = tree && pair_pays(B, S, T_cap);
   if (pair) {
-    pl.Gp = std::min(pair_chunks(B, S, T_cap, sms), kMaxPieces);
+    static_assert(kPairChunks <= kMaxPieces, "the combine lists up to kMaxPieces splits of a row");
+    pl.Gp = pair_chunks(B, S, T_cap, sms);
     pl.P = std::max(pl.P, (pl.Gp + B - 1) * S);
   }
   size_t off = 0;

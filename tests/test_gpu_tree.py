@@ -88,6 +88,105 @@ def test_decode_tree_longer_contexts(cuda_lib, T, S):
     _check(out, ref, parent, TOL["bf16"])
 
 
+# few query rows over a long cache take the pair attention between the GEMVs: by its
+# capacity, so that short and ragged contexts are cheap to check
+FEW = [([2], 2, 12300), ([130, 301], 3, 4100), ([700], 8, 3100), ([4099, 9, 2048, 513], 2, 4200), ([77, 1500], 4, 3080)]
+
+
+@pytest.mark.parametrize("T,S,cap", FEW)
+@pytest.mark.parametrize("paged", [False, True])
+def test_decode_tree_few_rows_on_a_long_cache(cuda_lib, T, S, cap, paged):
+    """Plain and paged, absent nodes and an empty tree among them, against the oracle; a
+    captured call replayed gives the same bits."""
+    B = len(T)
+    parent = random_parents(B, S, 13 * S)
+    if B > 1:
+        parent[-1] = -2
+    x = mla_inputs(GLM, B, S, T, max(T), "bf16", 800 + S, "cpu")
+    for b, s in zip(*np.nonzero(parent == -2)):
+        x["Lc"][b, T[b] - S + s] = float("nan")
+        x["Rc"][b, T[b] - S + s] = float("inf")
+    g = {k: v.to(DEV) for k, v in x.items()}
+    par = torch.from_numpy(parent).to(DEV)
+    if paged:
+        table, num_pages = paged_layout(T, 128, 5)
+        Lp, Rp = (to_pages(x[k], table, T, 128, num_pages).to(DEV) for k in ("Lc", "Rc"))
+        wide = torch.full((B, cap // 128 + 1), -1, dtype=torch.int32)
+        wide[:, :table.shape[1]] = table
+        wide = wide.to(DEV)
+
+        def call():
+            return cuda_lib.decode_tree_paged(g["q"], Lp, Rp, wide, g["T"], par, g["kv_b"], GLM)
+    else:
+        Lc, Rc = (torch.full((B, cap, w), float("nan"), dtype=torch.bfloat16, device=DEV) for w in (GLM.kv_lora, GLM.qk_rope))
+        Lc[:, :max(T)], Rc[:, :max(T)] = g["Lc"], g["Rc"]
+
+        def call():
+            return cuda_lib.decode_tree(g["q"], Lc, Rc, g["T"], par, g["kv_b"], GLM)
+    out = call()
+    assert cuda_lib.device_status() == 0
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        again = call()
+    graph.replay()
+    assert torch.equal(again, out) and cuda_lib.device_status() == 0
+    ref = oracle.decode_tree(to_np(x["q"]), to_np(x["Lc"]), to_np(x["Rc"]), T, parent, to_np(x["kv_b"]), GLM.qk_nope,
+                             GLM.softmax_scale)
+    _check(out, (ref, [(b, s) for b in range(B) for s in range(S)]), parent, TOL["bf16"])
+
+
+def test_decode_tree_few_rows_flags(cuda_lib):
+    """Bad nodes, lengths and pages, and a wait that runs out, on the few-row pair attention."""
+    S, cap = 4, 8192
+    T = [500, 40, 300]
+    x = mla_inputs(GLM, 2, S, T[:2], 500, "bf16", 45, "cpu")
+    Lc, Rc = (torch.zeros(2, cap, w, dtype=torch.bfloat16, device=DEV) for w in (GLM.kv_lora, GLM.qk_rope))
+    Lc[:, :500], Rc[:, :500] = x["Lc"].to(DEV), x["Rc"].to(DEV)
+    q, kv_b = x["q"].to(DEV), x["kv_b"].to(DEV)
+    parent = np.array([[-1, 0, 2, 1]] * 2, dtype=np.int32)  # node 2 is its own parent
+    good = np.array([[-1, 0, -1, 1]] * 2, dtype=np.int32)
+    par, lens = torch.from_numpy(parent).to(DEV), torch.tensor([500, cap + 1], dtype=torch.int32, device=DEV)
+    out = to_np(cuda_lib.decode_tree(q, Lc, Rc, lens, par, kv_b, GLM))
+    assert cuda_lib.device_status() == cuda_lib.MLA_DEV_BAD_INDEX | cuda_lib.MLA_DEV_BAD_LENGTH
+    assert np.all(np.isnan(out[1])) and np.all(np.isnan(out[0, 2]))
+    ref = oracle.decode_tree(to_np(x["q"]), to_np(x["Lc"]), to_np(x["Rc"]), T[:2], good, to_np(x["kv_b"]), GLM.qk_nope,
+                             GLM.softmax_scale)
+    check_close(out[0, [0, 1, 3]], ref[0, [0, 1, 3]], TOL["bf16"])
+    par, Tt = torch.from_numpy(good).to(DEV), x["T"].to(DEV)
+    table = torch.full((2, cap // 128), -1, dtype=torch.int32, device=DEV)
+    table[0, :4] = torch.arange(4)
+    table[1, 0] = 99  # outside the pool
+    out = cuda_lib.decode_tree_paged(q, Lc[0].view(-1, 128, 512), Rc[0].view(-1, 128, 64), table, Tt, par, kv_b, GLM)
+    assert cuda_lib.device_status() == cuda_lib.MLA_DEV_BAD_INDEX
+    check_close(to_np(out)[0], ref[0], TOL["bf16"])
+    cuda_lib.set_wait_limit_ns(1)
+    try:
+        cuda_lib.decode_tree(q, Lc, Rc, Tt, par, kv_b, GLM)
+        flags = cuda_lib.device_status()
+    finally:
+        cuda_lib.set_wait_limit_ns(2_000_000_000)
+    assert flags & cuda_lib.MLA_DEV_TIMEOUT
+    out = cuda_lib.decode_tree(q, Lc, Rc, Tt, par, kv_b, GLM)
+    assert cuda_lib.device_status() == 0
+    check_close(to_np(out), ref, TOL["bf16"])
+
+
+@pytest.mark.parametrize("dtype,dims,S,cap", [("f32", TINY, 3, 70), ("bf16", SMALL, 3, 300), ("bf16", GLM, 3, 300),
+                                              ("bf16", GLM, 3, 9000), ("bf16", GLM, 12, 300),
+                                              ("f32", Dims(2, 16, 8, 520, 16), 3, 70)])
+@pytest.mark.parametrize("value", [float("inf"), -float("inf")])
+def test_decode_tree_infinite_committed_row(cuda_lib, dtype, dims, S, cap, value):
+    """A committed row with an infinite latent turns every node into NaN or infinity, also where
+    its score is minus infinity and its weight would round to zero."""
+    T = [60]
+    x = mla_inputs(dims, 1, S, T, cap, dtype, 46, "cpu")
+    x["Lc"][0, 5, 1] = value
+    g = {k: v.to(DEV) for k, v in x.items()}
+    par = torch.full((1, S), -1, dtype=torch.int32, device=DEV)
+    out = cuda_lib.decode_tree(g["q"], g["Lc"], g["Rc"], g["T"], par, g["kv_b"], dims)
+    assert not torch.isfinite(out).any()
+
+
 @pytest.mark.parametrize("S", [8, 21])
 def test_decode_tree_large_scores_move_the_maximum(cuda_lib, S):
     """Scores that grow along the cache by far more than any fixed range: the running
@@ -542,6 +641,30 @@ def test_two_streams_at_once(cuda_lib):
     torch.cuda.synchronize()
     assert cuda_lib.device_status() == 0
     for st, (out, verdict), want in zip(states, got, alone):
+        assert torch.equal(out, want)
+        _compare(verdict, *st["host"])
+
+
+def test_stream_argument_owns_what_the_call_allocates(cuda_lib):
+    """Calls on a given stream, without workspace, while the current stream allocates and fills
+    memory: scratch and outputs belong to the given stream."""
+    T, S = [3000, 2500], 12
+    st = _step_state(cuda_lib, 58, T, S)
+    args = (st["q"][0], st["Lc"][0], st["Rc"][0], st["T"], st["parent"], st["kv_b"], GLM)
+    want = cuda_lib.decode_tree(*args)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    size = cuda_lib.decode_tree_workspace_size(GLM, torch.bfloat16, 2, S, st["Lc"].shape[2])
+    kept = []
+    for _ in range(20):
+        out = cuda_lib.decode_tree(*args, stream=side)
+        verdict = cuda_lib.tree_verify(st["p"], st["pq"], st["tokens"], st["parent"], st["u"], stream=side)
+        for n in (size, out.numel() * 4):
+            torch.empty(n, dtype=torch.uint8, device=DEV).fill_(255)
+        kept.append((out, verdict))
+    torch.cuda.synchronize()
+    assert cuda_lib.device_status() == 0
+    for out, verdict in kept:
         assert torch.equal(out, want)
         _compare(verdict, *st["host"])
 
