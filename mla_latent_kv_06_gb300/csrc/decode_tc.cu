@@ -1189,7 +1189,8 @@ __global__ void __launch_bounds__(kCmbThreads) combine_kernel(const CombineParam
     const int sr = kTree ? p.S - 1 : s;
     const int state = kTree ? tree_node(p.parent + (size_t)b * p.S, s).state : kNodePresent;
     int cnt = 0;
-    if (!cbad[row] && N > 0) {
+    // an absent tree node has no splits: zero times a context of NaN rows would not be zero
+    if (!cbad[row] && N > 0 && state != kNodeAbsent) {
       const long long a = cts[row], e = cts[row + 1];
       const int glo = chunk_of(a, N, p.G), ghi = chunk_of(e - 1, N, p.G);
       for (int g0 = glo; g0 <= ghi; g0 += 32) {
@@ -1253,9 +1254,7 @@ __global__ void __launch_bounds__(kCmbThreads) combine_kernel(const CombineParam
         L = fmaf(wg, pw[warp * kMaxPieces + i], L);
       }
       L = warp_sum(L);
-      // an absent tree node has no visible key: L is 0 and its output zero
-      const bool none = kTree && L == 0.f;
-      for (int i = lane; i < cnt; i += 32) pm[warp * kMaxPieces + i] = none ? 0.f : pm[warp * kMaxPieces + i] / L;
+      for (int i = lane; i < cnt; i += 32) pm[warp * kMaxPieces + i] = pm[warp * kMaxPieces + i] / L;
     }
     __syncthreads();
     // (b) clat[w][l] = sum_i weight_i * O_i[h][l] for every row at once:

@@ -177,14 +177,18 @@ def test_decode_tree_few_rows_flags(cuda_lib):
 @pytest.mark.parametrize("value", [float("inf"), -float("inf")])
 def test_decode_tree_infinite_committed_row(cuda_lib, dtype, dims, S, cap, value):
     """A committed row with an infinite latent turns every node into NaN or infinity, also where
-    its score is minus infinity and its weight would round to zero."""
+    its score is minus infinity and its weight would round to zero; an absent node stays zero,
+    also with a query of NaN."""
     T = [60]
     x = mla_inputs(dims, 1, S, T, cap, dtype, 46, "cpu")
     x["Lc"][0, 5, 1] = value
+    x["q"][0, 1] = float("nan")
     g = {k: v.to(DEV) for k, v in x.items()}
     par = torch.full((1, S), -1, dtype=torch.int32, device=DEV)
+    par[0, 1] = -2
     out = cuda_lib.decode_tree(g["q"], g["Lc"], g["Rc"], g["T"], par, g["kv_b"], dims)
-    assert not torch.isfinite(out).any()
+    assert not out[0, 1].any()
+    assert not torch.isfinite(out[0, [s for s in range(S) if s != 1]]).any()
 
 
 @pytest.mark.parametrize("S", [8, 21])
