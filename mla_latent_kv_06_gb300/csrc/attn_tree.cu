@@ -583,14 +583,26 @@ __device__ __forceinline__ void soften(const PairParams& p, Shared& sh, unsigned
         ml[0] = sh.m[tsm];
         ml[1] = sh.red[0][tsm] + sh.red[1][tsm] + sh.red[2][tsm] + sh.red[3][tsm];
       }
-      float* op = p.o_part + (slot * kRows + row) * kDl + 256 * ch + 128 * (q >> 1);
+      // Through the warp's 4 KB of the P buffer, so that eight lanes store 128 bytes of a
+      // row: with a row per lane every store was 32 partial sectors (8 nodes on 4096 keys,
+      // 19 MB of partials: the call 36.6 us against 33.8; 8 x 64 nodes 1122 against 1111).
+      float* op = p.o_part + (slot * kRows + 32 * (q & 1) + (lane >> 3)) * kDl + 256 * ch + 128 * (q >> 1) + 4 * (lane & 7);
+      float4* st = reinterpret_cast<float4*>(smem + kQBytes + (warp - 2) * 4096);
 #pragma unroll 1
       for (int c0 = 0; c0 < 128; c0 += 32) {
         float w[32];
         tmem_ld32(t_lane + kColO + 128 * ch + c0, w);
         tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 32; i += 4) *reinterpret_cast<float4*>(op + c0 + i) = make_float4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+        for (int i = 0; i < 8; ++i)
+          st[8 * lane + (i ^ (lane & 7))] = make_float4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = 4 * i + (lane >> 3);
+          *reinterpret_cast<float4*>(op + (size_t)(4 * i) * kDl + c0) = st[8 * r + ((lane & 7) ^ (r & 7))];
+        }
+        __syncwarp();
       }
     }
     tc_fence_before();
