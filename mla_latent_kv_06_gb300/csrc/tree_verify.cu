@@ -55,6 +55,36 @@ __device__ __forceinline__ void add(Pair& acc, float hi, float lo) {
   acc.hi = s;
 }
 
+// Two accumulators side by side: the packed instructions take one issue slot
+// for both, and issue is what a pass waits for when two CTAs share an SM.
+struct Pair2 {
+  unsigned long long hi, lo;
+};
+__device__ __forceinline__ unsigned long long pack(float x, float y) {
+  unsigned long long v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y));
+  return v;
+}
+__device__ __forceinline__ void unpack(unsigned long long v, float* x, float* y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(*x), "=f"(*y) : "l"(v));
+}
+__device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) {
+  unsigned long long v;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+  return v;
+}
+__device__ __forceinline__ unsigned long long sub2(unsigned long long a, unsigned long long b) {
+  unsigned long long v;
+  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+  return v;
+}
+__device__ __forceinline__ void add(Pair2& acc, float x, float y) {
+  const unsigned long long v = pack(x, y);
+  const unsigned long long s = add2(acc.hi, v), b = sub2(s, acc.hi);
+  acc.lo = add2(acc.lo, add2(sub2(acc.hi, sub2(s, b)), sub2(v, b)));
+  acc.hi = s;
+}
+
 // Total of the values of 2 * kFrom neighbouring lanes, the same in each of them.
 template <int kFrom = 16>
 __device__ __forceinline__ Pair warp_total(Pair v) {
@@ -156,7 +186,7 @@ __device__ __forceinline__ unsigned long long removed_inside(const Shared& sh, u
 constexpr int kAhead = 8;
 template <bool kDraft>
 __device__ __forceinline__ Sums segment_sum(const Segment& g, int lane) {
-  Pair a{0.f, 0.f}, b{0.f, 0.f};
+  Pair2 sum{0, 0};  // of p and of q; without q, of every other element of p
   for (int i0 = g.lo; i0 < g.hi; i0 += 32 * kAhead) {
     float p[kAhead], q[kAhead];
     if (i0 + 32 * kAhead <= g.hi) {
@@ -178,12 +208,18 @@ __device__ __forceinline__ Sums segment_sum(const Segment& g, int lane) {
       if (kDraft) {
         const float w = fmaf(-g.cl, q[k], fmaf(-g.ch, q[k], p[k]));
         const bool in = !(w <= 0.f);  // (a NaN is in, so that the total shows it)
-        add(a, in ? p[k] : 0.f, 0.f);
-        add(b, in ? q[k] : 0.f, 0.f);
-      } else {
-        add(a, element(g, i0 + 32 * k + lane, p[k], 0.f).hi, 0.f);
+        add(sum, in ? p[k] : 0.f, in ? q[k] : 0.f);
+      } else if (k % 2 == 0) {
+        add(sum, element(g, i0 + 32 * k + lane, p[k], 0.f).hi, element(g, i0 + 32 * k + 32 + lane, p[k + 1], 0.f).hi);
       }
     }
+  }
+  Pair a, b;
+  unpack(sum.hi, &a.hi, &b.hi);
+  unpack(sum.lo, &a.lo, &b.lo);
+  if (!kDraft) {
+    add(a, b.hi, b.lo);
+    b = Pair{0.f, 0.f};
   }
   return Sums{warp_total(a), kDraft ? warp_total(b) : b};
 }
