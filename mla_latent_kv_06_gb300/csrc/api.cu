@@ -912,16 +912,19 @@ int run_commit(mla::CommitArgs& a, int n, void* const* cache, const int* row_byt
       return fail(MLA_ERR_INVALID, "T_out must not overlap T, path or n_acc");
   }
   const uintptr_t rows = a.pages.table ? (uintptr_t)a.pages.num_pages * a.pages.page_size : (uintptr_t)a.B * a.T_cap;
+  uintptr_t least = UINTPTR_MAX, most = 0;  // of the caches so far
   for (int i = 0; i < n; ++i) {
     if (!cache[i] || row_bytes[i] < 1) return fail(MLA_ERR_INVALID, "cache %d: null pointer or row_bytes < 1", i);
-    // a cache given twice would have its rows moved twice (one pass without branches: 0.5 us for 96 caches)
+    // a cache given twice would have its rows moved twice; one outside the span of
+    // those before it, the usual case, is compared with none of them
     const uintptr_t c0 = reinterpret_cast<uintptr_t>(cache[i]), c1 = c0 + rows * row_bytes[i];
-    unsigned twice = 0;
-    for (int j = 0; j < i; ++j) {
-      const uintptr_t d0 = reinterpret_cast<uintptr_t>(cache[j]);
-      twice |= (unsigned)(d0 < c1) & (unsigned)(c0 < d0 + rows * row_bytes[j]);
-    }
-    if (twice) return fail(MLA_ERR_INVALID, "cache %d overlaps another one", i);
+    if (c0 < most && least < c1)
+      for (int j = 0; j < i; ++j) {
+        const uintptr_t d0 = reinterpret_cast<uintptr_t>(cache[j]);
+        if (d0 < c1 && c0 < d0 + rows * row_bytes[j]) return fail(MLA_ERR_INVALID, "cache %d overlaps another one", i);
+      }
+    least = c0 < least ? c0 : least;
+    most = c1 > most ? c1 : most;
   }
   a.flags = flags_ptr();
   if (!a.flags) return fail(MLA_ERR_CUDA, "cannot resolve the device status word");
