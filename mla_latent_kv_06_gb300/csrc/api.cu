@@ -913,16 +913,26 @@ int run_commit(mla::CommitArgs& a, int n, void* const* cache, const int* row_byt
   }
   const uintptr_t rows = a.pages.table ? (uintptr_t)a.pages.num_pages * a.pages.page_size : (uintptr_t)a.B * a.T_cap;
   uintptr_t least = UINTPTR_MAX, most = 0;  // of the caches so far
+  uintptr_t begin[mla::kCommitCaches], end[mla::kCommitCaches];  // the first ones'
   for (int i = 0; i < n; ++i) {
     if (!cache[i] || row_bytes[i] < 1) return fail(MLA_ERR_INVALID, "cache %d: null pointer or row_bytes < 1", i);
     // a cache given twice would have its rows moved twice; one outside the span of
     // those before it, the usual case, is compared with none of them
     const uintptr_t c0 = reinterpret_cast<uintptr_t>(cache[i]), c1 = c0 + rows * row_bytes[i];
-    if (c0 < most && least < c1)
-      for (int j = 0; j < i; ++j) {
+    if (c0 < most && least < c1) {
+      const int m = i < mla::kCommitCaches ? i : mla::kCommitCaches;
+      uintptr_t twice = 0;
+      for (int j = 0; j < m; ++j) twice |= (uintptr_t)(begin[j] < c1) & (uintptr_t)(c0 < end[j]);  // no branch: vector code
+      for (int j = m; j < i; ++j) {
         const uintptr_t d0 = reinterpret_cast<uintptr_t>(cache[j]);
-        if (d0 < c1 && c0 < d0 + rows * row_bytes[j]) return fail(MLA_ERR_INVALID, "cache %d overlaps another one", i);
+        twice |= (uintptr_t)(d0 < c1 && c0 < d0 + rows * row_bytes[j]);
       }
+      if (twice) return fail(MLA_ERR_INVALID, "cache %d overlaps another one", i);
+    }
+    if (i < mla::kCommitCaches) {
+      begin[i] = c0;
+      end[i] = c1;
+    }
     least = c0 < least ? c0 : least;
     most = c1 > most ? c1 : most;
   }

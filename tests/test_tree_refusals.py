@@ -87,6 +87,18 @@ def test_commit_refuses_caches_that_overlap(lib, second, row_bytes, B, bad, page
     assert rc == mla.MLA_ERR_INVALID and b"overlaps" in lib.mla_last_error()
 
 
+def test_commit_refuses_a_late_overlap(lib):
+    """Among many caches, out of order, only the last one overlaps: with an early or a late one."""
+    n = 300
+    x, y, z = (ctypes.c_void_p(i << 40) for i in (1, 2, 3))
+    for twin in (7, 200):
+        at = [(1 << 20) + 16 * 1024 * ((37 * i) % n) for i in range(n)]
+        at.append(at[twin])
+        rc = lib.mla_tree_commit(n + 1, (ctypes.c_void_p * (n + 1))(*at), (ctypes.c_int * (n + 1))(*[1024] * (n + 1)), 1, 2, 16,
+                                 x, y, z, None, None)
+        assert rc == mla.MLA_ERR_INVALID and b"cache 300 overlaps" in lib.mla_last_error()
+
+
 def test_commit_refuses_lengths_over_its_arguments(lib):
     arr, size = (ctypes.c_void_p * 1)(1 << 20), (ctypes.c_int * 1)(1024)
     B, S, T, path, n = 3, 4, 1 << 30, 2 << 30, 3 << 30
