@@ -38,9 +38,9 @@
 // cache is bf16; the row sums add the rounded probabilities, so that both
 // sides of the quotient use the same weights.  Scores, running maximum, sums and context are fp32.
 //
-// Measured: 8 trees of 64 nodes on 16k to 32k keys 1.01 ms, 1.73 PFLOP/s, the
-// sustained rate of the tensor pipe under the power limit (68% of its cycles
-// at full clock).  32 trees of 6 nodes on 1k to 32k keys 365 us, 1.25 PFLOP/s:
+// Measured: 8 trees of 64 nodes on 16k to 32k keys 1.01 ms, 1.74 PFLOP/s, the
+// sustained rate of the tensor pipe under the power limit (70% of its cycles
+// at full clock).  32 trees of 6 nodes on 1k to 32k keys 360 us, 1.26 PFLOP/s:
 // with 3 pairs on a tile, 3.7 us a tile against 3.1 with 32 pairs, although
 // DRAM runs at a quarter of its rate; fetching the tiles into L2 ahead of time
 // changed nothing (315 against 313 us on 32 x 6 x 16384).

@@ -1743,16 +1743,18 @@ std::atomic<unsigned long long> g_abs_attr[18] = {}, g_attn_attr[14] = {}, g_cmb
 // take one CTA per node, as plain decode does: it starts sooner, but every node
 // reads the cache for itself and a CTA walks its tiles one after the other.
 // Measured us of the whole call, one CTA per node against the pair:
-//   1 sequence: 8 nodes x 512 keys 28.3, 32.2;  8 x 2048 32.2, 34.1;  2 x 8192 27.0, 28.1;
-//               8 x 4096 38.6, 36.6;  4 x 8192 35.5, 32.8;  3 x 20000 44.6, 37.3;
-//               2 x 30000 45.6, 35.9
-//   2 and 4:    4 nodes x 1024 33.4, 34.0;  2 x 2048 37.0, 36.0;  2 x 4096 48.1, 38.6
+//   1 sequence:      8 nodes x 512 keys 28.3, 30.0;  8 x 1024 30.0, 30.6;  2 x 4096 23.8, 24.2;
+//                    8 x 2048 32.6, 31.7;  2 x 8192 26.9, 25.3;  8 x 4096 38.4, 34.1;
+//                    3 x 20000 45.4, 34.8;  2 x 30000 45.5, 34.0
+//   2 of 2 nodes:    256 keys 22.5, 26.2;  1024 24.8, 26.1;  4096 28.4, 28.0
+//   2 of 4, 4 of 2:  64 keys 28.4, 29.6 and 28.1, 30.3;  256 31.0, 30.5 and 31.7, 31.5;
+//                    1024 33.2, 31.3 and 34.2, 32.6;  2048 35.7, 32.4 and 36.6, 33.5
 // With more rows the pair is ahead from short contexts (11 x 9 nodes x 248
 // keys: 64.8, 59.9; 16 nodes x 2048: 49.6, 43.4) to long ones (16 x 2 nodes x
 // 16384: 289.8, 112.8), at worst 5% behind (32 x 64 nodes on 90 keys).
 bool pair_pays(int B, int S, int T_cap) {
   if ((long long)B * S > kSmallRows) return true;
-  return S >= 2 && (long long)B * S * T_cap >= 24576;
+  return S >= 2 && (long long)B * S * T_cap >= (B > 1 && B * S > 4 ? 2048 : 12288);
 }
 
 Plan make_plan(int B, int S, int T_cap, int sparse_topk, bool tree = false) {

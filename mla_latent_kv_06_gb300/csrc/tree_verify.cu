@@ -17,18 +17,19 @@
 // here and would bound the kernel: sum W = A - c B with A and B the sums of p and of q over
 // the x where p > c q (an x misjudged by rounding has W(x) next to zero), and
 // A and B are kept as unevaluated pairs hi + lo, added with Knuth's two-sum.
-// The sums cost some 20 instructions an element; forming each W(x) as a pair
-// cost 30.
+// The sums cost some 13 instructions an element (p and q added in packed
+// pairs; 20 one by one; 30 with each W(x) formed as a pair).
 //
 // A sequence is a cluster of 8 CTAs, each with an eighth of the vocabulary: a
 // row of p and of q of 131072 values, 1 MB, is 24 us of one SM's share of the
 // memory bandwidth.  Every context on the way that rejects a child, and the last draw, is a
 // pass over that context's rows that starts when the one before has decided,
 // so the bound is the latency of the passes: load, block sum, cluster sum.
-// Measured, vocabulary 131072, 32 trees of 24 nodes: 32 us, each byte of the
+// Measured, vocabulary 131072, 32 trees of 24 nodes: 30 us, each byte of the
 // rows that are looked at read from memory once (31.7 MB, 0.9 TB/s), barriers
-// the first stall; 5 drafts of one user over 32000: 10 us; 8 trees of 64 point
-// drafts over 100003: 15 us.
+// the first stall; a pass is about 6 us: loads and sums 3, totals and cluster
+// barrier 1.8, decision 1.2.  5 drafts of one user over 32000: 10 us; 8 trees of
+// 64 point drafts over 100003: 15 us.
 #include <cooperative_groups.h>
 
 #include "common.cuh"

@@ -89,7 +89,7 @@ def test_decode_tree_longer_contexts(cuda_lib, T, S):
 
 
 # few query rows over a long cache take the pair attention between the GEMVs: by its
-# capacity, so that short and ragged contexts are cheap to check
+# capacity, so that short and ragged contexts are cheap to check (and those of a few sequences)
 FEW = [([2], 2, 12300), ([130, 301], 3, 4100), ([700], 8, 3100), ([4099, 9, 2048, 513], 2, 4200), ([77, 1500], 4, 3080)]
 
 
@@ -133,6 +133,15 @@ def test_decode_tree_few_rows_on_a_long_cache(cuda_lib, T, S, cap, paged):
     ref = oracle.decode_tree(to_np(x["q"]), to_np(x["Lc"]), to_np(x["Rc"]), T, parent, to_np(x["kv_b"]), GLM.qk_nope,
                              GLM.softmax_scale)
     _check(out, (ref, [(b, s) for b in range(B) for s in range(S)]), parent, TOL["bf16"])
+
+
+@pytest.mark.parametrize("page_size", [0, 128])
+def test_decode_tree_single_nodes_on_long_contexts(cuda_lib, page_size):
+    """Trees of one node stream long caches through one CTA per chunk."""
+    T, parent = [5000, 4970, 4999, 5100, 5003, 77, 4900, 5096], np.full((8, 1), -1, dtype=np.int32)
+    parent[4] = -2
+    out, ref = _attend(cuda_lib, GLM, "bf16", T, 1, parent, 830, page_size=page_size)
+    _check(out, ref, parent, TOL["bf16"])
 
 
 def test_decode_tree_few_rows_flags(cuda_lib):
