@@ -184,13 +184,14 @@ def test_decode_tree_few_rows_flags(cuda_lib):
                                               ("bf16", GLM, 3, 9000), ("bf16", GLM, 12, 300),
                                               ("f32", Dims(2, 16, 8, 520, 16), 3, 70)])
 @pytest.mark.parametrize("value", [float("inf"), -float("inf")])
-def test_decode_tree_infinite_committed_row(cuda_lib, dtype, dims, S, cap, value):
-    """A committed row with an infinite latent turns every node into NaN or infinity, also where
+@pytest.mark.parametrize("last", [False, True])
+def test_decode_tree_infinite_committed_row(cuda_lib, dtype, dims, S, cap, value, last):
+    """A committed row (one far from the tree, or the one before it) with an infinite latent turns every node into NaN or infinity, also where
     its score is minus infinity and its weight would round to zero; an absent node stays zero,
     also with a query of NaN."""
-    T = [60]
+    T = [62]
     x = mla_inputs(dims, 1, S, T, cap, dtype, 46, "cpu")
-    x["Lc"][0, 5, 1] = value
+    x["Lc"][0, T[0] - S - 1 if last else 5, 1] = value
     x["q"][0, 1] = float("nan")
     g = {k: v.to(DEV) for k, v in x.items()}
     par = torch.full((1, S), -1, dtype=torch.int32, device=DEV)
