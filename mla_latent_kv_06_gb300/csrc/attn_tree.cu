@@ -12,7 +12,7 @@
 // products of cta_group::2: CTA r holds the query rows, probabilities, scores
 // and context of its own node (tree node 2i + r), and each supplies half of
 // the B operand, which the pair's tensor cores share:
-//   S[64 rows x 256 keys] = Q [K-major] . K^T    (K = 576; CTA r loads keys 128r ..)
+//   S[64 rows x 256 keys] = Q [K-major] . K^T    (K = 576 + 64; CTA r loads keys 128r ..)
 //   O[64 rows x 512]     += P [K-major] . V      (two N = 256 blocks; CTA r loads
 //                                                 latents 256n + 128r .. of all keys)
 // All products have N = 256: measured 64.6 cycles each, the full rate, against
@@ -33,14 +33,18 @@
 // NaN through their scores and the others, whose probability is zero, stay
 // untouched although the pair shares the value operand.
 //
-// Rounding.  The absorbed and rotated query and the probabilities are rounded
-// to bf16, because the products take both operands in one 16-bit type and the
-// cache is bf16; the row sums add the rounded probabilities, so that both
+// Rounding.  The absorbed query and the probabilities are rounded to bf16,
+// because the products take both operands in one 16-bit type and the cache is
+// bf16.  The rotated query is taken in two bf16 terms, 4 more products a tile:
+// its 64 values carry half of the scores' error, and the output's goes from 1.50
+// to 1.43 times that of its own rounding (emulated on 200 and 1000 keys) for 2%
+// of the time of a long context (a second term of the 512 latents would be 32 products more, one of the
+// probabilities 32).  The row sums add the rounded probabilities, so that both
 // sides of the quotient use the same weights.  Scores, running maximum, sums and context are fp32.
 //
-// Measured: 8 trees of 64 nodes on 16k to 32k keys 1.01 ms, 1.74 PFLOP/s, the
-// sustained rate of the tensor pipe under the power limit (70% of its cycles
-// at full clock).  32 trees of 6 nodes on 1k to 32k keys 360 us, 1.26 PFLOP/s:
+// Measured: 8 trees of 64 nodes on 16k to 32k keys 1.03 ms, 1.70 PFLOP/s of the
+// formula's (1.80 issued), the sustained rate of the tensor pipe under the
+// power limit.  32 trees of 6 nodes on 1k to 32k keys 368 us, 1.23 PFLOP/s:
 // with 3 pairs on a tile, 3.7 us a tile against 3.1 with 32 pairs, although
 // DRAM runs at a quarter of its rate; fetching the tiles into L2 ahead of time
 // changed nothing (315 against 313 us on 32 x 6 x 16384).
@@ -63,7 +67,7 @@ constexpr int kRows = 64, kDl = 512, kDc = 576;
 constexpr int kStages = 7;
 constexpr int kFree = 4;  // barriers that free stages, two at a time (see issue)
 constexpr uint32_t kStageBytes = 16384, kQAtom = 8192;
-constexpr uint32_t kQBytes = 9 * kQAtom, kPBytes = 4 * 8192;
+constexpr uint32_t kQBytes = 10 * kQAtom, kPBytes = 4 * 8192;
 constexpr uint32_t kRingOff = kQBytes + kPBytes;
 constexpr uint32_t kSmem = kRingOff + kStages * kStageBytes + 1024;
 constexpr uint32_t kColS = 0, kColO = 256, kCols = 512;
@@ -296,6 +300,7 @@ __device__ __forceinline__ void produce(const PairParams& p, Shared& sh, unsigne
     const uint32_t qbar = in_cta(&sh.q_full, 0);
     const int qrow = (pc.b * p.S + 2 * pair + (int)rank) * kRows;  // past the last node: another row or zeros
     for (int d = 0; d < 9; ++d) load_2d(smem_u32(smem + d * kQAtom), &p.mQ, 64 * d, qrow, qbar, lead);
+    load_2d(smem_u32(smem + 9 * kQAtom), &p.mQl, 0, qrow, qbar, lead);
     ++*q_issued;
     Rows r0 = rows_of(pc.b, Tb, pc.lo), r1 = pc.lo + 1 < pc.hi ? rows_of(pc.b, Tb, pc.lo + 1) : r0;
     load_k(tile_at(Tb, p.S, pc.lo), r0);
@@ -353,6 +358,10 @@ __device__ __forceinline__ void issue(const PairParams& p, Shared& sh, unsigned 
       const uint64_t db = dK + (uint64_t)(s * (kStageBytes >> 4)), da = dQ + (uint64_t)(a * (kQAtom >> 4));
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk) mma_pair(d, da + 2 * kk, db + 2 * kk, idS, (a | kk) != 0 ? 1u : 0u, lead);
+      if (a == 8) {  // the rotary keys again, with what rounding the rotated query left
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) mma_pair(d, da + (kQAtom >> 4) + 2 * kk, db + 2 * kk, idS, 1u, lead);
+      }
       release();
     }
     commit_pair(&sh.s_full[j & 1], lead);

@@ -23,6 +23,7 @@ __host__ __device__ __forceinline__ int pair_tiles(int T, int S) {
 
 struct PairParams {
   CUtensorMap mQ;   // qcat [R*64, 576], box 64 x 64
+  CUtensorMap mQl;  // remainders of the rotated queries [R*64, 64], box 64 x 64
   CUtensorMap mK;   // latent rows, box 128 x 64
   CUtensorMap mKr;  // rotary key rows, box 128 x 64
   CUtensorMap mV;   // latents as (column in atom, row, 64-column atom), box 64 x 64 x 2

@@ -826,6 +826,7 @@ struct AbsorbParams {
   const int32_t* parent;  // tree attention: [B, S] parent indices
   int rope_x;             // tree: blocks along x that work on the head; any more stage the tails
   __nv_bfloat16* tail;    // pair attention: staged tail rows [B, kPairStage, 576], else null
+  __nv_bfloat16* qlow;    // pair attention: the rotated queries' remainders [R, 64, 64]
 };
 
 // Rotary position of query row s of sequence b (length Tb): its row, or the
@@ -834,6 +835,15 @@ template <bool kTree>
 __device__ __forceinline__ int query_pos(const AbsorbParams& p, int b, int s, int Tb) {
   if (Tb < p.S || Tb > p.T_cap) return 0;
   return Tb - p.S + (kTree ? tree_node(p.parent + (size_t)b * p.S, s).depth : s);
+}
+
+// Element j of the rotated query of head row rh (row * 64 + head).  The pair
+// attention also takes what the rounding to bf16 left.
+template <bool kTree>
+__device__ __forceinline__ void put_rotated(const AbsorbParams& p, size_t rh, int j, float v) {
+  const __nv_bfloat16 hi = __float2bfloat16_rn(v);
+  p.qcat[rh * kDc + kDl + j] = hi;
+  if (kTree && p.tail) p.qlow[rh * kDr + j] = __float2bfloat16_rn(v - __bfloat162float(hi));
 }
 
 // Rotary part of query row r of head h, rotated to the row's own position.
@@ -846,9 +856,8 @@ __device__ __forceinline__ void rope_row(const AbsorbParams& p, int r, int h, in
   rope_cs_turns(pos, p.turn[j], &cs, &sn);
   const __nv_bfloat16* qr = p.q + ((size_t)r * kH + h) * Dq + p.Dn;
   const float x0 = __bfloat162float(qr[2 * j]), x1 = __bfloat162float(qr[2 * j + 1]);
-  __nv_bfloat16* dst = p.qcat + ((size_t)r * kH + h) * kDc + kDl;
-  dst[j] = __float2bfloat16_rn(x0 * cs - x1 * sn);
-  dst[kDr / 2 + j] = __float2bfloat16_rn(x1 * cs + x0 * sn);
+  put_rotated<kTree>(p, (size_t)r * kH + h, j, x0 * cs - x1 * sn);
+  put_rotated<kTree>(p, (size_t)r * kH + h, kDr / 2 + j, x1 * cs + x0 * sn);
 }
 
 // Rotary parts of rows x pairs e = tid, tid + nthr, ... (row e / 32, pair e % 32):
@@ -889,9 +898,8 @@ __device__ __forceinline__ void rope_rows(const AbsorbParams& p, int h, int tid,
         float sn, cs;
         rope_cs_turns(pos, p.turn[j], &cs, &sn);
         const float2 x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&raw[u]));
-        __nv_bfloat16* dst = p.qcat + ((size_t)r * kH + h) * kDc + kDl;
-        dst[j] = __float2bfloat16_rn(x.x * cs - x.y * sn);
-        dst[kDr / 2 + j] = __float2bfloat16_rn(x.y * cs + x.x * sn);
+        put_rotated<kTree>(p, (size_t)r * kH + h, j, x.x * cs - x.y * sn);
+        put_rotated<kTree>(p, (size_t)r * kH + h, kDr / 2 + j, x.y * cs + x.x * sn);
       }
     }
   }
@@ -1708,7 +1716,7 @@ __global__ void __launch_bounds__(256) gather_kernel(const GatherParams p) {
 struct Plan {
   int G, NR, P, R, Kpad;
   int Gp;  // pair attention of a tree: its chunks
-  size_t off_q, off_ts, off_bad, off_o, off_ml, off_stage, off_clat, off_invl, off_q8, off_fh, off_tail, total;
+  size_t off_q, off_ts, off_bad, off_o, off_ml, off_stage, off_clat, off_invl, off_q8, off_fh, off_tail, off_qlow, total;
 };
 
 // Query rows above which the weight products run as tcgen05 GEMMs; below it
@@ -1810,6 +1818,8 @@ Plan make_plan(int B, int S, int T_cap, int sparse_topk, bool tree = false) {
   off = align256(off + (sparse_topk || tree ? 0 : (size_t)pl.R * kH * 4));
   pl.off_tail = off;
   off = align256(off + (pair ? (size_t)B * kPairStage * kDc * 2 : 0));
+  pl.off_qlow = off;
+  off = align256(off + (pair ? (size_t)pl.R * kH * kDr * 2 : 0));
   pl.total = off;
   return pl;
 }
@@ -1879,8 +1889,10 @@ cudaError_t run_pair(const DecodeArgs& a, const Plan& pl, unsigned char* w, long
   PairParams p{};
   const void* qcat = w + pl.off_q;
   const void* tail = w + pl.off_tail;
+  const void* qlow = w + pl.off_qlow;
   const uint64_t rows = (uint64_t)pool_rows, trows = (uint64_t)a.B * kPairStage;
   if (!make_tmap_2d_bf16(&p.mQ, qcat, (uint64_t)pl.R * kH, kDc, kDc, kH, 64) ||
+      !make_tmap_2d_bf16(&p.mQl, qlow, (uint64_t)pl.R * kH, kDr, kDr, kH, 64) ||
       !make_tmap_2d_bf16(&p.mK, a.Lc, rows, kDl, kDl, 128, 64) ||
       !make_tmap_2d_bf16(&p.mKr, a.Rc, rows, kDr, kDr, 128, 64) ||
       !make_tmap_2d_bf16(&p.mT, tail, trows, kDc, kDc, 128, 64))
@@ -2006,7 +2018,10 @@ cudaError_t run(const DecodeArgs& a, void* ws, bool sparse, cudaStream_t st) {
   // many rows: the rotary part of each head spread over up to four CTAs
   const int abs_gx = big ? std::min(a.parent ? 16 : 4, (pl.R * (kDr / 2) + 2047) / 2048) : kDl / kAbsCols;
   ap.rope_x = abs_gx;
-  if (pair) ap.tail = reinterpret_cast<__nv_bfloat16*>(w + pl.off_tail);
+  if (pair) {
+    ap.tail = reinterpret_cast<__nv_bfloat16*>(w + pl.off_tail);
+    ap.qlow = reinterpret_cast<__nv_bfloat16*>(w + pl.off_qlow);
+  }
   e = set_smem_once(akern, (int)abs_smem, &g_abs_attr[big ? (a.parent ? 17 : 16) : 4 * abs_kind + g.Dn / 64 - 1]);
   if (e != cudaSuccess) return e;
   kernel_mark(st, big ? "plan_rope" : "absorb");
