@@ -424,7 +424,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) tre
       all.lo = __shfl_sync(0xffffffffu, all.lo, 0);
       z = value(all);
       if (!drawing) {
-        mass = z;
+        mass = z < 0.0 ? 0.0 : z;  // (less than the sums' rounding is left; a NaN stays)
         stale = false;
       } else if (!(z > 0.0) && z == z && !fallback && (c != 0.0 || removed)) {
         fallback = true;  // nothing left: the target's own distribution

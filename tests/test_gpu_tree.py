@@ -702,3 +702,41 @@ def test_decode_tree_tail_boundaries(cuda_lib, rem, page_size):
     parent = random_parents(4, S, 61 + rem)
     out, ref = _attend(cuda_lib, GLM, "bf16", T, S, parent, 950 + rem, page_size=page_size)
     _check(out, ref, parent, TOL["bf16"])
+
+
+# ------------------------------------------------------------------ verification at its edges
+RESIDUALS = [(V, B, ratio, spread) for V, B in ((511, 1024), (4099, 1024), (70001, 64)) for ratio in (1.5, 1.25)
+             for spread in (0, 30, 45)]
+
+
+def _vanishing(V, B, ratio, spread):
+    """Inputs of verification with p = ratio q on every other token, and drafts that the target never emits: a
+    rejection leaves 1 - 1 / ratio of what was left, so that after 30 (20) of them it is below the 2^-48 of the
+    sums, whose rounded value then has any sign.  The tree of sequence b is a star of `nodes[b]` drafts."""
+    S = 64
+    rng = np.random.default_rng(7)
+    # values over a range of `spread` powers of two, of 21 bits, so that ratio * q is exact in float32
+    q = np.ldexp(rng.integers(1 << 20, 1 << 21, (B, V)).astype(np.float64), -21)
+    q = np.ldexp(q, -np.where(rng.random((B, V)) < 0.5, 0, rng.integers(0, spread + 1, (B, V))))
+    q[:, 1::2], q[:, 0] = 0, 0
+    q *= 2.0 ** np.floor(np.log2(0.9 / ratio / q.sum(-1).max()))
+    q[:, 0] = np.round((1 / ratio - q.sum(-1)) * 2 ** 20) / 2 ** 20  # the target's sum is 1 up to 2^-20
+    p = ratio * q
+    q[:, 1::2] = ((1 - q.sum(-1)) / (V // 2))[:, None]
+    p, q = p.astype(np.float32), q.astype(np.float32)
+    assert np.array_equal(p[:, ::2].astype(np.float64), ratio * q[:, ::2].astype(np.float64))
+    nodes = 1 + np.arange(B) % (48 if ratio == 1.5 else 36)
+    parent = np.where(np.arange(S) < nodes[:, None], -1, -2).astype(np.int32)
+    tokens = (2 * rng.integers(0, V // 2, (B, S)) + 1).astype(np.int32)
+    u = rng.random((B, S + 1), dtype=np.float32)
+    P, Q = (torch.zeros(B, S + 1, V, device=DEV) for _ in range(2))
+    P[:, 0], Q[:, 0] = _to(p, q)
+    return (P, Q, *_to(tokens, parent, u)), (p, q, tokens, parent, u), nodes
+
+
+@pytest.mark.parametrize("V,B,ratio,spread", RESIDUALS)
+def test_verify_never_accepts_what_the_target_never_emits(cuda_lib, V, B, ratio, spread):
+    args, _, _ = _vanishing(V, B, ratio, spread)
+    path, n_acc, _ = cuda_lib.tree_verify(*args)
+    assert cuda_lib.device_status() == 0
+    assert not n_acc.any() and bool((path == -1).all())
