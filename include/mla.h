@@ -493,7 +493,9 @@ int mla_cache_append_tree_paged(const mla_dims* d, int dtype, int B, int S, cons
  * none).  Without q a child is accepted when u a < W(x) (W = p at first), and a
  * rejection subtracts W(x) from a and sets W(x) to 0.  If nothing is left of W
  * the draw is from p.  The emitted tokens are then distributed as the target's
- * own samples.  Sums over the vocabulary are held to about 2^-48.
+ * own samples.  Sums over the vocabulary are held to about 2^-48; where less than
+ * that is left of W after many rejections, W may count as empty.  token is an
+ * x with W(x) > 0 or, where W is empty, one with p(x) > 0.
  *
  * p (and q) are taken as distributions: values >= 0 whose sum is 1 up to
  * rounding; p_row and q_row >= V.  A context whose p has no finite positive

@@ -18,7 +18,11 @@
 // the x where p > c q (an x misjudged by rounding has W(x) next to zero), and
 // A and B are kept as unevaluated pairs hi + lo, added with Knuth's two-sum.
 // The sums cost some 13 instructions an element (p and q added in packed
-// pairs; 20 one by one; 30 with each W(x) formed as a pair).
+// pairs; 20 one by one; 30 with each W(x) formed as a pair).  Regrouped or
+// small, such a sum can be zero or negative although a W(x) is positive, and the
+// other way round.  So the draw takes CTA and warp by the rounded sums and,
+// inside the warp's segment, sums the W(x) one by one; where these are all zero
+// it looks through the whole vocabulary, so that a token is stored in any case.
 //
 // A sequence is a cluster of 8 CTAs, each with an eighth of the vocabulary: a
 // row of p and of q of 131072 values, 1 MB, is 24 us of one SM's share of the
@@ -111,15 +115,17 @@ __device__ __forceinline__ Pair minus_times(const Pair& a, const Pair& b, float 
   return Pair{s, ((a.hi - (s - t)) - (h + t)) + (a.lo - e)};
 }
 
-// max(p - (ch + cl) q, 0) as a pair.
+// max(p - (ch + cl) q, 0) as a pair whose high part is the rounded value, so
+// that sums of such pairs are positive where one of them is.
 __device__ __forceinline__ Pair left(float p, float q, float ch, float cl) {
   const float h = ch * q;
   const float e = fmaf(cl, q, fmaf(ch, q, -h));
   const float s = p - h, b = s - p;
   const float lo = ((p - (s - b)) - (h + b)) - e;
-  const bool pos = s + lo > 0.f;
+  const float w = s + lo, d = w - s;
+  const bool pos = w > 0.f;
   // a NaN stays one, so that the total shows it
-  return Pair{pos ? s : (s + lo != s + lo ? s : 0.f), pos ? lo : 0.f};
+  return Pair{pos || w != w ? w : 0.f, pos ? (s - (w - d)) + (lo - d) : 0.f};
 }
 
 // What the warps do next: sum W at context `at`, or draw from it.
@@ -146,9 +152,14 @@ struct Shared {
   Pair warp_sum[kWarps];                  // ... and their W
   Command cmd;
   int bad[kMaxTree], up[kMaxTree];
-  int find_warp;
+  int warp_last[kWarps];  // last x of positive weight in the warps' segments
+  int find_warp, find_last;
   double find_t;
 };
+
+// Shared::find_warp besides a warp's number: the draw is another CTA's, or no
+// warp's rounded sum is positive.
+constexpr int kNobody = -1, kSearch = -2;
 
 // Segment of the vocabulary, in elements, and the weights there.
 struct Segment {
@@ -228,6 +239,23 @@ __device__ __forceinline__ Sums segment_sum(const Segment& g, int lane) {
   return g.q ? segment_sum<true>(g, lane) : segment_sum<false>(g, lane);
 }
 
+// Sum of the weights one by one, not as A - c B: it is positive exactly where a
+// weight is.  *last: the last x of positive weight, or -1.
+__device__ Pair weight_sum(const Segment& g, int lane, int* last) {
+  Pair sum{0.f, 0.f};
+  int at = -1;
+#pragma unroll 2
+  for (int i0 = g.lo; i0 < g.hi; i0 += 32) {
+    const int i = i0 + lane;
+    const float p = i < g.hi ? __ldg(g.p + i) : 0.f, q = g.q && i < g.hi ? __ldg(g.q + i) : 0.f;
+    const Pair w = element(g, i, p, q);
+    add(sum, w.hi, w.lo);
+    if (w.hi > 0.f) at = i;
+  }
+  *last = __reduce_max_sync(0xffffffffu, at);
+  return warp_total(sum);
+}
+
 // First index of the segment (at most 32 elements a step) whose cumulative
 // weight exceeds t, else the last one of positive weight; -1: none.
 __device__ int segment_find(const Segment& g, double t, int lane) {
@@ -268,6 +296,40 @@ __device__ __forceinline__ int pick_part(double mine, double* t) {
   const int at = over ? __ffs(over) - 1 : some ? 31 - __clz(some) : -1;
   if (at >= 0) *t -= __shfl_sync(0xffffffffu, incl - mine, at);
   return at;
+}
+
+// The warp of the CTA to whose segment g a draw of t falls (u >= 0: of u times
+// the sum instead), sh.find_t then being what is left of t; -1: no weight is
+// positive.  *last: the last x of positive weight in any of the segments, or -1.
+// The whole CTA calls it.
+__device__ int find_share(Shared& sh, Segment& g, unsigned long long removed, double t, float u, int* last) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  g.removed = removed_inside(sh, removed, g.lo, g.hi);
+  const Pair mine = weight_sum(g, lane, last);
+  if (lane == 0) {
+    sh.warp_sum[warp] = mine;
+    sh.warp_last[warp] = *last;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    const double v = lane < kWarps ? value(sh.warp_sum[lane]) : 0.0;
+    if (u >= 0.f) {
+      t = v;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+      t *= (double)u;
+    }
+    const int w = pick_part(v, &t);
+    const int top = __reduce_max_sync(0xffffffffu, lane < kWarps ? sh.warp_last[lane] : -1);
+    if (lane == 0) {
+      sh.find_warp = w;
+      sh.find_t = t;
+      sh.find_last = top;
+    }
+  }
+  __syncthreads();
+  *last = sh.find_last;
+  return sh.find_warp;
 }
 
 // The decisions (doubles: few, and made by one warp only, since all threads
@@ -434,10 +496,11 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) tre
         if (lane == 0) sh.cmd.done = 1;
         // which CTA, then which warp, the draw falls to
         double t = (double)sh.u[S] * z;
-        int hit = -1;
+        int hit = kNobody;
         if (z > 0.0 && z < 1e300) {
-          hit = pick_part(lane < kCluster ? value(sh.part[pass & 1][lane]) : 0.0, &t);
-          hit = hit == rank ? pick_part(lane < kWarps ? value(sh.warp_sum[lane]) : 0.0, &t) : -1;
+          const int owner = pick_part(lane < kCluster ? value(sh.part[pass & 1][lane]) : 0.0, &t);
+          if (owner == rank) hit = pick_part(lane < kWarps ? value(sh.warp_sum[lane]) : 0.0, &t);
+          if ((owner == rank && hit < 0) || (owner < 0 && rank == 0)) hit = kSearch;
         } else if (rank == 0 && lane == 0) {  // an empty or non-finite distribution
           raise_flag(a.flags, MLA_DEV_BAD_VALUE);
           a.token[b] = -1;
@@ -457,33 +520,47 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) tre
     for (int i = n + lane; i < S; i += 32) a.path[(size_t)b * S + i] = -1;
     if (lane == 0) a.n_acc[b] = n;
   }
-  // The warp's segment again, split over the CTA's warps.
+  // The warp's segment again, split over the CTA's warps, weight by weight.
   const int hit = sh.find_warp;
-  if (hit < 0) return;
-  const int hlo = min((rank * kWarps + hit) * per, groups) * 32, hhi = min(min((rank * kWarps + hit + 1) * per, groups) * 32, V);
-  const int sub = (per + kWarps - 1) / kWarps;  // groups of 32 per warp
-  seg.lo = min(hlo + 32 * sub * warp, hhi);
-  seg.hi = min(hlo + 32 * sub * (warp + 1), hhi);
-  seg.removed = removed_inside(sh, sh.cmd.removed, seg.lo, seg.hi);
-  const Sums part = segment_sum(seg, lane);
-  if (lane == 0) sh.warp_sums[warp] = part;
-  __syncthreads();
-  if (warp == 0) {
-    double t = sh.find_t, mine = 0.0;
-    if (lane < kWarps) {
-      const Sums x = sh.warp_sums[lane];
-      mine = value(x.a) - c * value(x.b);
+  if (hit == kNobody) return;
+  const unsigned long long gone = sh.cmd.removed;
+  if (hit != kSearch) {
+    const int hlo = min((rank * kWarps + hit) * per, groups) * 32, hhi = min(min((rank * kWarps + hit + 1) * per, groups) * 32, V);
+    const int sub = (per + kWarps - 1) / kWarps;  // groups of 32 per warp
+    seg.lo = min(hlo + 32 * sub * warp, hhi);
+    seg.hi = min(hlo + 32 * sub * (warp + 1), hhi);
+    int last;
+    const int w = find_share(sh, seg, gone, sh.find_t, -1.f, &last);
+    if (w == warp) {
+      const int x = segment_find(seg, sh.find_t, lane);
+      if (lane == 0) a.token[b] = x;
     }
-    const int w = pick_part(mine, &t);
-    if (lane == 0) {
-      sh.find_warp = w;
-      sh.find_t = t;
-    }
+    if (w >= 0) return;
   }
-  __syncthreads();
-  if (sh.find_warp != warp) return;
-  const int x = segment_find(seg, sh.find_t, lane);
-  if (lane == 0) a.token[b] = x;
+  // The rounded sums pointed at weights that are all zero: what is left is at
+  // most their rounding.  The last x of positive weight, or, where there is
+  // none, a draw from p.  Never seen but on inputs made for it: 30 drafts
+  // rejected one after the other at one context.
+  const int stripe = (groups + kWarps - 1) / kWarps;
+  seg.lo = min(32 * min(stripe * warp, groups), V);
+  seg.hi = min(32 * min(stripe * (warp + 1), groups), V);
+  int last;
+  find_share(sh, seg, gone, 0.0, -1.f, &last);
+  if (last >= 0) {
+    if (tid == 0) a.token[b] = last;
+    return;
+  }
+  seg.q = nullptr;
+  const int w = find_share(sh, seg, 0, 0.0, sh.u[S], &last);
+  if (w < 0) {
+    if (tid == 0) {
+      raise_flag(a.flags, MLA_DEV_BAD_VALUE);
+      a.token[b] = -1;
+    }
+  } else if (w == warp) {
+    const int x = segment_find(seg, sh.find_t, lane);
+    if (lane == 0) a.token[b] = x;
+  }
 }
 
 }  // namespace

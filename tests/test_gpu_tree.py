@@ -740,3 +740,79 @@ def test_verify_never_accepts_what_the_target_never_emits(cuda_lib, V, B, ratio,
     path, n_acc, _ = cuda_lib.tree_verify(*args)
     assert cuda_lib.device_status() == 0
     assert not n_acc.any() and bool((path == -1).all())
+
+
+@pytest.mark.parametrize("V,B,ratio,spread", RESIDUALS)
+def test_verify_always_stores_a_token_that_the_target_emits(cuda_lib, V, B, ratio, spread):
+    """Wherever the rounded sums end; while 2^-19 is left the token is the exact one."""
+    args, (p, q, tokens, parent, u), nodes = _vanishing(V, B, ratio, spread)
+    token = torch.full((B,), -7, dtype=torch.int32, device=DEV)
+    cuda_lib.tree_verify(*args, token=token)
+    assert cuda_lib.device_status() == 0
+    token = token.cpu().numpy()
+    assert np.all((token >= 0) & (token < V) & (token % 2 == 0))
+    few = 12 if ratio == 1.5 else 8
+    for b in [b for b in range(B) if nodes[b] <= few][:20 if V < 1000 else 4 if V < 10000 else 0]:
+        rows = np.zeros((tokens.shape[1] + 1, V))
+        rows[0], draft = p[b], rows.copy()
+        draft[0] = q[b]
+        assert oracle.tree_verify(rows, draft, tokens[b], parent[b], u[b]) == ([], token[b])
+
+
+def _exact(row):
+    """Float32 values as whole numbers of 2^-149."""
+    m, e = np.frexp(row.astype(np.float64))
+    return [int(x) << int(k) if k >= 0 else int(x) >> -int(k) for x, k in zip((m * 2 ** 24).astype(np.int64), e + 125)]
+
+
+def _left_after_a_miss(p, q):
+    """What is left of p after a rejected draft of probability zero, exact: p itself without q, else max(p - q, 0)."""
+    return np.array(_exact(p) if q is None else [max(a - b, 0) for a, b in zip(_exact(p), _exact(q))], dtype=object)
+
+
+def _check_draws(lib, p, q, tokens, parent, u, left):
+    """The tokens drawn after one rejected draft per sequence; sequence 0 also against the oracle."""
+    outs = lib.tree_verify(*_to(p, q, tokens, parent, u))
+    assert lib.device_status() == 0
+    _compare([t[:1] for t in outs], p[:1], None if q is None else q[:1], tokens[:1], parent[:1], u[:1])
+    path, n_acc, token = (t.cpu().numpy() for t in outs)
+    assert not n_acc.any() and np.all(path == -1)
+    for b, w in enumerate(left):
+        grown = np.cumsum(w)
+        over = grown * (1 << 24) > int(float(u[b, -1]) * (1 << 24)) * grown[-1]  # u is a whole number of 2^-24
+        assert token[b] == int(np.argmax(over)), b
+
+
+@pytest.mark.parametrize("point", [False, True])
+@pytest.mark.parametrize("V,at", [(70001, (0, 31, 32, 63, 64, 95, 575, 576, 35000, 70000)), (131072, (33, 1023, 1056, 131071))])
+def test_verify_draws_deep_in_a_large_vocabulary(cuda_lib, V, at, point):
+    """Draws aimed at both sides of the borders of a warp's share and of its 32-element steps, against the
+    exact token."""
+    B, S = len(at), 1
+    p, q, tokens, parent, u = _verify_inputs(1, S, V, 15, point)
+    p[:, :, 1] = 0
+    left = _left_after_a_miss(p[0, 0], None if point else q[0, 0])
+    grown = np.cumsum(left)
+    some = np.nonzero(left > left.max() // 1000)[0]
+    u = np.full((B, 2), 0.5, dtype=np.float32)
+    for b, x in enumerate(at):
+        x = int(some[np.argmin(np.abs(some - x))])
+        u[b, 1] = ((2 * grown[x] - left[x]) * (1 << 23) // grown[-1]) / (1 << 24)  # the middle of its share
+    p, q = np.repeat(p, B, 0), None if point else np.repeat(q, B, 0)
+    _check_draws(cuda_lib, p, q, np.ones((B, S), dtype=np.int32), np.full((B, S), -1, dtype=np.int32), u, [left] * B)
+
+
+@pytest.mark.parametrize("V", [70001, 131072])
+def test_verify_draw_from_a_few_tokens_of_a_large_vocabulary(cuda_lib, V):
+    """What is left after a rejection lies in the first 32-element step of a warp's share, or in its last
+    token; random numbers next to 0 and 1."""
+    B, S = 4, 1
+    p, q = (np.full((B, S + 1, V), 1 / V, dtype=np.float32) for _ in range(2))
+    share = 32 * -(-(-(-V // 32)) // 128)
+    for b, few in enumerate(([7 * share + 3], [7 * share, 7 * share + 31], [9 * share - 1], [3 * share + 40, V - 1])):
+        p[b, 0, few] += np.float32(0.25)
+    p[:, 0, 2] = 0
+    left = [_left_after_a_miss(p[b, 0], q[b, 0]) for b in range(B)]
+    tokens, parent = np.full((B, S), 2, dtype=np.int32), np.full((B, S), -1, dtype=np.int32)
+    for last in (0.0, 0.5, np.nextafter(np.float32(1), np.float32(0))):
+        _check_draws(cuda_lib, p, q, tokens, parent, np.array([[0.5, last]] * B, dtype=np.float32), left)
