@@ -175,7 +175,7 @@ __device__ __forceinline__ Pair element(const Segment& g, int i, float p, float 
   if (g.q) return left(p, q, g.ch, g.cl);
   Pair v{p > 0.f || p != p ? p : 0.f, 0.f};
   for (unsigned long long m = g.removed; m; m &= m - 1)
-    if (g.token[__ffsll((long long)m) - 1] == i) v.hi = 0.f;
+    if (g.token[__ffsll((long long)m) - 1] == i) v.hi = p != p ? p : 0.f;  // (a removed NaN stays one)
   return v;
 }
 
@@ -449,7 +449,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) tre
           c += mass;
           stale = true;
         } else {
-          mass = mass > w ? mass - w : 0.0;
+          mass = mass <= w ? 0.0 : mass - w;  // (a NaN stays: no later child is accepted)
           removed |= 1ull << s;
         }
       }

@@ -816,3 +816,20 @@ def test_verify_draw_from_a_few_tokens_of_a_large_vocabulary(cuda_lib, V):
     tokens, parent = np.full((B, S), 2, dtype=np.int32), np.full((B, S), -1, dtype=np.int32)
     for last in (0.0, 0.5, np.nextafter(np.float32(1), np.float32(0))):
         _check_draws(cuda_lib, p, q, tokens, parent, np.array([[0.5, last]] * B, dtype=np.float32), left)
+
+
+@pytest.mark.parametrize("V", [9, 4099])
+def test_verify_point_drafts_flag_a_target_that_is_not_a_number(cuda_lib, V):
+    """The target's probability of a tried draft is NaN: with and without a second sibling and with the
+    draft repeated, nothing is accepted after it and the token is -1; the other sequence is untouched."""
+    B, S = 5, 3
+    p, _, tokens, parent, u = _verify_inputs(B, S, V, 8, point=True)
+    parent[:4] = [[-1, -2, -2], [-1, -1, 0], [-1, -1, -1], [-1, -1, -2]]
+    tokens[:4] = [[4, 0, 0], [4, 5, 1], [4, 4, 5], [5, 4, 0]]
+    p[:4, 0, 4] = np.nan
+    u[:4] = np.nextafter(np.float32(1), np.float32(0))
+    outs = cuda_lib.tree_verify(*_to(p, None, tokens, parent, u))
+    assert cuda_lib.device_status() == cuda_lib.MLA_DEV_BAD_VALUE
+    path, n_acc, token = (t.cpu().numpy() for t in outs)
+    assert not n_acc[:4].any() and np.all(path[:4] == -1) and np.all(token[:4] == -1)
+    _compare([t[4:] for t in outs], p[4:], None, tokens[4:], parent[4:], u[4:])
