@@ -442,7 +442,9 @@ int dsa_index_key_append(int B, int S, int index_hd, int rope_dim, const float* 
 /* Tree attention: mla_decode_absorbed with the query of node s attending to
  * the cached prefix t < T[b] - S and, among the tree's rows, to its own and
  * its ancestors'.  Rows of other branches, of absent nodes and past T[b] never
- * reach a result, whatever they hold.
+ * reach a result, whatever they hold.  A row that a node sees turns all of the node's
+ * heads into NaN if it holds a value that is not finite; a score beyond
+ * float's range counts as one.
  *   out [B, S, H, v_head] float (out_dtype MLA_F32) or bf16 (MLA_BF16),
  *       16-byte aligned
  * An absent node's output is zero, a bad node's NaN.  q, Lc, Rc, T, kv_b and

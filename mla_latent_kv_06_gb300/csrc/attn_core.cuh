@@ -617,6 +617,15 @@ __device__ __forceinline__ void attn_softmax(const AttnParams& p, AttnShared& sh
 #pragma unroll
       for (int i = 0; i < 32; ++i) v[i] = -INFINITY;
     }
+    if (kTree && valid) {  // a score of -inf gives NaN, not weight 0
+      float lo = v[0];
+#pragma unroll
+      for (int i = 1; i < 32; ++i) lo = fminf(lo, v[i]);
+      if (lo == -INFINITY) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = v[i] == -INFINITY ? __int_as_float(0x7fc00000) : v[i];
+      }
+    }
     // The running max of a head moves only when the tile's max exceeds it by
     // more than kTau (lazy rescale).  Past a piece's first tile that is rare,
     // and one OR over the threads tells whether any head's does: only then is

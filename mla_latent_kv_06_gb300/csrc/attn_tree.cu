@@ -31,7 +31,10 @@
 // a staging buffer (stage_tail): a row with a value that is not finite is staged as zero
 // latents with a NaN rotary part, so that it turns the nodes that see it into
 // NaN through their scores and the others, whose probability is zero, stay
-// untouched although the pair shares the value operand.
+// untouched although the pair shares the value operand.  A visible score of
+// -inf (an infinite rotary key under a finite latent) has weight zero and would
+// hide its row: the pass for the maximum takes the minimum along, and the row
+// sum becomes NaN (32 x 6 nodes 0.3% longer, other cases within the noise).
 //
 // Rounding.  The absorbed query and the probabilities are rounded to bf16,
 // because the products take both operands in one 16-bit type and the cache is
@@ -484,7 +487,7 @@ __device__ __forceinline__ void soften(const PairParams& p, Shared& sh, unsigned
         }
         if (mask == 0) vis = 0;
       }
-      float mx = -INFINITY;
+      float mx = -INFINITY, least = INFINITY;  // over the visible keys
 #pragma unroll 1
       for (int c0 = 0; c0 < 64; c0 += 16) {
         float v[16];
@@ -493,10 +496,16 @@ __device__ __forceinline__ void soften(const PairParams& p, Shared& sh, unsigned
         const uint32_t bits = (uint32_t)(vis >> c0);
         if (masked) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] = (bits >> i) & 1u ? v[i] : -INFINITY;
-        }
+          for (int i = 0; i < 16; ++i) {
+            least = (bits >> i) & 1u ? fminf(least, v[i]) : least;
+            mx = (bits >> i) & 1u ? fmaxf(mx, v[i]) : mx;
+          }
+        } else {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) mx = fmaxf(mx, v[i]);
+          for (int i = 0; i < 16; ++i) least = fminf(least, v[i]);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) mx = fmaxf(mx, v[i]);
+        }
       }
       // running maximum, moved only when a score exceeds it by more than kTau
       bool slow = first;
@@ -532,6 +541,8 @@ __device__ __forceinline__ void soften(const PairParams& p, Shared& sh, unsigned
       }
       // probabilities: bf16 is the value product's operand; the row sum adds the rounded values
       if (rescale) lsum *= sh.alpha[row];
+      // a score of -inf stands for values that are not finite: its weight of 0 would hide them
+      if (least == -INFINITY) lsum = qnan();
 #pragma unroll 1
       for (int c0 = 0; c0 < 64; c0 += 16) {
         float v[16];
@@ -542,11 +553,7 @@ __device__ __forceinline__ void soften(const PairParams& p, Shared& sh, unsigned
         float add0 = 0.f, add1 = 0.f;
         if (masked) {  // (a branch around the loop: one inside it would cost more than the exponentials)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            // only staged rows may hide values that are not finite
-            const float x = t.tail && fabsf(v[i]) == INFINITY ? qnan() : v[i];
-            v[i] = (bits >> i) & 1u ? x : -INFINITY;
-          }
+          for (int i = 0; i < 16; ++i) v[i] = (bits >> i) & 1u ? v[i] : -INFINITY;
         }
 #pragma unroll
         for (int i = 0; i < 16; ++i) v[i] = ex2(fmaf(v[i], c, -mrow));

@@ -115,6 +115,8 @@ __global__ void __launch_bounds__(kThreads) decode_simt_kernel(DecodeArgs a) {
       }
       if (lane == 0) {
         sc[j] = ok ? dot * g.scale : -INFINITY;
+        // (tree: a visible key with a score of -inf gives NaN, not weight 0)
+        if (kTree && ok && sc[j] == -INFINITY) sc[j] = qnan();
         // pool row (< 2^31, checked on the host); -1: a bad index or page, -2: outside the tree mask
         tok[j] = ok ? (int)row : seen ? -1 : -2;
       }

@@ -833,3 +833,30 @@ def test_verify_point_drafts_flag_a_target_that_is_not_a_number(cuda_lib, V):
     path, n_acc, token = (t.cpu().numpy() for t in outs)
     assert not n_acc[:4].any() and np.all(path[:4] == -1) and np.all(token[:4] == -1)
     _compare([t[4:] for t in outs], p[4:], None, tokens[4:], parent[4:], u[4:])
+
+
+# ------------------------------------------------------------------ attention over values at the end of their range
+WIDE = Dims(2, 16, 8, 520, 16)  # kv_lora beyond the tiled CUDA-core kernel's
+
+
+@pytest.mark.parametrize("dtype,dims,S,cap", [("f32", TINY, 3, 500), ("bf16", SMALL, 3, 500), ("f32", WIDE, 3, 500),
+                                              ("bf16", GLM, 1, 5000), ("bf16", GLM, 2, 500), ("bf16", GLM, 3, 9000),
+                                              ("bf16", GLM, 12, 500), ("bf16", GLM, 13, 3000)])
+@pytest.mark.parametrize("cache", ["Lc", "Rc"])
+@pytest.mark.parametrize("value", [float("inf"), -float("inf")])
+@pytest.mark.parametrize("row", [5, 300, -1])
+def test_decode_tree_infinite_rows_turn_every_head_into_nan(cuda_lib, dtype, dims, S, cap, cache, value, row):
+    """An infinite latent or rotary value in a committed row (in the first tiles, or the row before the tree)
+    gives scores of plus infinity to some heads and of minus infinity to others: all of them are NaN, and the
+    other sequence keeps its bits."""
+    T = [cap - 7 if S == 1 else 430, 77]
+    x = mla_inputs(dims, 2, S, T, cap, dtype, 47, "cpu")
+    par = torch.from_numpy(random_parents(2, S, 21, absent=False)).to(DEV)
+    g = {k: v.to(DEV) for k, v in x.items()}
+    clean = cuda_lib.decode_tree(g["q"], g["Lc"], g["Rc"], g["T"], par, g["kv_b"], dims)
+    assert torch.isfinite(clean).all()
+    g[cache][0, T[0] - S + row if row < 0 else row, 1] = value
+    out = cuda_lib.decode_tree(g["q"], g["Lc"], g["Rc"], g["T"], par, g["kv_b"], dims)
+    assert cuda_lib.device_status() == 0
+    assert torch.isnan(out[0]).all()
+    assert torch.equal(out[1], clean[1])
