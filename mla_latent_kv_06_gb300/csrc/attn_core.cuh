@@ -654,7 +654,7 @@ __device__ __forceinline__ void attn_softmax(const AttnParams& p, AttnShared& sh
         const float tmax =
             fmaxf(fmaxf(sh.red_max[0][tsm], sh.red_max[1][tsm]), fmaxf(sh.red_max[2][tsm], sh.red_max[3][tsm]));
         const float cand = tmax * c;
-        const float mo = first ? (kTree ? -1e30f : -INFINITY) : sh.m_sh[tsm];
+        const float mo = first ? (kTree ? kMaxFloor : -INFINITY) : sh.m_sh[tsm];
         float mn = mo, al = 1.f;
         if (cand > mo + kTau) {
           mn = cand;

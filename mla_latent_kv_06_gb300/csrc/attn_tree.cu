@@ -521,7 +521,7 @@ __device__ __forceinline__ void soften(const PairParams& p, Shared& sh, unsigned
         bool need = false;
         if (tsm < kRows) {
           const float tmax = fmaxf(fmaxf(sh.red[0][tsm], sh.red[1][tsm]), fmaxf(sh.red[2][tsm], sh.red[3][tsm])) * c;
-          const float mo = first ? -1e30f : sh.m[tsm];
+          const float mo = first ? kMaxFloor : sh.m[tsm];
           float mn = mo, al = 1.f;
           if (tmax > mo + kTau) {
             mn = tmax;

@@ -6,6 +6,7 @@
 // is the prefix length plus its depth (its number of ancestors).
 #pragma once
 
+#include <float.h>
 #include <stdint.h>
 
 #include "../../include/mla.h"
@@ -13,6 +14,10 @@
 namespace mla {
 
 enum TreeState { kNodePresent = 0, kNodeAbsent = 1, kNodeBad = 2 };
+
+// Where the running maximum of a node's scores starts.  Not at -inf: a tile may
+// show it no key, and its weights are then exp(-inf - maximum) = 0.
+constexpr float kMaxFloor = -FLT_MAX;
 
 struct TreeNode {
   unsigned long long mask;  // bit j: node j is visible (0 for an absent or bad node)

@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(kThreads) tree_attend_kernel(const __grid_cons
   float acc[kAcc];
 #pragma unroll
   for (int j = 0; j < kAcc; ++j) acc[j] = 0.f;
-  float m = -1e30f, l = 0.f;
+  float m = kMaxFloor, l = 0.f;
   const Tin* Lc = static_cast<const Tin*>(a.Lc);
   const Tin* Rc = static_cast<const Tin*>(a.Rc);
   for (int k0 = k_lo; k0 < k_hi; k0 += kKeys) {
@@ -297,7 +297,7 @@ __global__ void __launch_bounds__(128) tree_merge_kernel(const __grid_constant__
     if (lane == 0) fill[warp] = bad ? qnan() : node.state == kNodeAbsent ? 0.f : 1.f;
     const size_t step = (size_t)SH * (g.Dl + 2);
     const float* src = p.part + ((size_t)b * p.splits * SH + row0 + warp) * (g.Dl + 2);
-    float M = -1e30f;
+    float M = kMaxFloor;
     for (int i = lane; i < p.splits; i += 32) M = fmaxf(M, src[i * step + g.Dl]);
     M = warp_max(M);
     float L = 0.f, acc[kAcc / 2];

@@ -860,3 +860,25 @@ def test_decode_tree_infinite_rows_turn_every_head_into_nan(cuda_lib, dtype, dim
     assert cuda_lib.device_status() == 0
     assert torch.isnan(out[0]).all()
     assert torch.equal(out[1], clean[1])
+
+
+@pytest.mark.parametrize("dtype,dims,S,cap", [("f32", TINY, 3, 100), ("f32", TINY, 3, 9000), ("f32", WIDE, 3, 100),
+                                              ("bf16", GLM, 3, 300), ("bf16", GLM, 3, 9000), ("bf16", GLM, 12, 300)])
+def test_decode_tree_scores_far_below_zero(cuda_lib, dtype, dims, S, cap):
+    """All scores are the same number below -1e31 (W_UK copies the query's first element onto the first
+    latent, which W_UV drops): the output is W_UV times the mean of the visible rows."""
+    T = [90]
+    x = mla_inputs(dims, 1, S, T, cap, dtype, 48, "cpu")
+    x["q"].zero_()
+    x["q"][..., 0] = 2.0 ** 60
+    x["Lc"][0, :, 0] = -(2.0 ** 50)
+    x["kv_b"][:, :dims.qk_nope] = 0
+    x["kv_b"][:, 0, 0] = 1
+    x["kv_b"][:, dims.qk_nope:, 0] = 0
+    parent = random_parents(1, S, 4, absent=False)
+    g = {k: v.to(DEV) for k, v in x.items()}
+    out = cuda_lib.decode_tree(g["q"], g["Lc"], g["Rc"], g["T"], torch.from_numpy(parent).to(DEV), g["kv_b"], dims)
+    assert cuda_lib.device_status() == 0
+    ref = oracle.decode_tree(to_np(x["q"]), to_np(x["Lc"]), to_np(x["Rc"]), T, parent, to_np(x["kv_b"]), dims.qk_nope,
+                             dims.softmax_scale)
+    check_close(to_np(out), ref, TOL[dtype])
