@@ -453,7 +453,8 @@ int dsa_index_key_append(int B, int S, int index_hd, int rope_dim, const float* 
  * output is rounded once from the float result.
  *   workspace: mla_decode_tree_workspace_size() bytes, 256-byte aligned (the
  *              paged call takes T_cap = max_pages * page_size); may be 0
- * Errors: as mla_decode_absorbed; S > 64 returns MLA_ERR_UNSUPPORTED. */
+ * Errors: as mla_decode_absorbed; S > 64 and capacities above 2^31 - 1024 rows
+ * return MLA_ERR_UNSUPPORTED. */
 size_t mla_decode_tree_workspace_size(const mla_dims* d, int dtype, int B, int S, int T_cap);
 int mla_decode_tree(const mla_dims* d, int dtype, int B, int S, const void* q, const void* Lc, const void* Rc,
                     int T_cap, const int32_t* T, const int32_t* parent, const void* kv_b, int out_dtype, void* out,

@@ -877,6 +877,7 @@ int run_decode_tree(const mla_dims* d, int dtype, int B, int S, const void* q, c
   if (rc) return rc;
   if (out_dtype != MLA_F32 && out_dtype != MLA_BF16) return fail(MLA_ERR_INVALID, "unknown out_dtype %d", out_dtype);
   if (T_cap < S) return fail(MLA_ERR_INVALID, "T_cap=%d < S=%d", T_cap, S);
+  if (T_cap > mla::kMaxTreeCap) return fail(MLA_ERR_UNSUPPORTED, "capacity of %d rows above %d", T_cap, mla::kMaxTreeCap);
   if (!q || !Lc || !Rc || !T || !kv_b || !out) return fail(MLA_ERR_INVALID, "null tensor pointer");
   // the many-row path stores out 16 bytes at a time
   if (!aligned16(out)) return fail(MLA_ERR_INVALID, "out must be 16-byte aligned");
@@ -955,7 +956,7 @@ int run_commit(mla::CommitArgs& a, int n, void* const* cache, const int* row_byt
 
 MLA_EXPORT size_t mla_decode_tree_workspace_size(const mla_dims* d, int dtype, int B, int S, int T_cap) {
   mla::Geometry g;
-  if (!resolve(d, &g) || B < 1 || S < 1 || S > mla::kMaxTree || T_cap < S) return 0;
+  if (!resolve(d, &g) || B < 1 || S < 1 || S > mla::kMaxTree || T_cap < S || T_cap > mla::kMaxTreeCap) return 0;
   size_t tc = 0;
   if (dtype == MLA_BF16 && mla::tc_decode_geometry_ok(g))
     tc = round256(mla::tc_decode_workspace_bytes(g, B, S, T_cap, /*sparse_topk=*/0, /*tree=*/true));

@@ -169,6 +169,10 @@ cudaError_t launch_tree_simt(const DecodeArgs& a, int dtype, void* ws, cudaStrea
 // Largest drafted tree: its ancestor masks are 64-bit words.
 constexpr int kMaxTree = 64;
 
+// Largest capacity of a sequence in tree attention: the kernels' key indices step
+// past a length by up to a tile (256), and stay within int.
+constexpr int kMaxTreeCap = 0x7fffffff - 1023;
+
 struct VerifyArgs {
   int B, S, V;
   const float* p;  // row r of sequence b at p + b * p_batch + r * p_row, r = 0 .. S

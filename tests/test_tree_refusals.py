@@ -144,3 +144,16 @@ def test_binding_refuses_on_the_host(lib):
         mla.cache_append_tree(comp, ln, T, par, Lc, Rc, TINY, 1e-6)
     with pytest.raises(ValueError):
         mla.cache_append_tree(comp[:, :, 1:], ln, T, par, Lc, Rc, TINY, 1e-6)
+
+
+@pytest.mark.parametrize("dims,dtype", [(GLM_D, 1), (mla.MlaDims(1, 2, 2, 1, 1, 0.0, 0.0), 0)])
+def test_decode_tree_refuses_capacities_at_the_end_of_int32(lib, dims, dtype):
+    """Key indices step by up to 256 past a sequence's length in int32."""
+    top = (1 << 31) - 1
+    for cap in (top, top - 1022):
+        assert _decode(lib, d=dims, dtype=dtype, T_cap=cap) == mla.MLA_ERR_UNSUPPORTED, cap
+        assert lib.mla_decode_tree_workspace_size(ctypes.byref(dims), dtype, 1, 2, cap) == 0
+    assert lib.mla_decode_tree_workspace_size(ctypes.byref(dims), dtype, 1, 2, top - 1023) > 0
+    table_pages = (top - 127) // 128  # a capacity of 2^31 - 128 rows
+    assert lib.mla_decode_tree_paged(ctypes.byref(dims), dtype, 1, 2, P, P, P, 4, 128, P, table_pages, P, P, P, 0, P, None, 0,
+                                     None) == mla.MLA_ERR_UNSUPPORTED
