@@ -104,6 +104,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
     grid_dep_wait();
   }
   cx.N = cx.ts[cx.NR];
+  // No tile at all (only bad lengths): nobody loads a query, yet this grid must not end before
+  // the absorb kernel, whose late writes could then meet the next call's in the workspace.
+  if (cx.N == 0) grid_dep_wait();
   cx.g = kSparse ? brow : brow / S;
   cx.s = kSparse ? 0 : brow % S;
   cx.sr = kTree ? S - 1 : cx.s;
@@ -363,6 +366,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn8_kernel(const __grid_con
     grid_dep_wait();
   }
   const long long N = ts[NR];
+  if (N == 0) grid_dep_wait();  // as in attn_kernel
   const long long c0 = chunk_begin(N, g, p.G);
   const int row0 = first_row(ts, NR, c0);
 

@@ -882,3 +882,24 @@ def test_decode_tree_scores_far_below_zero(cuda_lib, dtype, dims, S, cap):
     ref = oracle.decode_tree(to_np(x["q"]), to_np(x["Lc"]), to_np(x["Rc"]), T, parent, to_np(x["kv_b"]), dims.qk_nope,
                              dims.softmax_scale)
     check_close(to_np(out), ref, TOL[dtype])
+
+
+@pytest.mark.parametrize("dtype,dims,S,cap", [("f32", TINY, 3, 500), ("bf16", GLM, 3, 300), ("bf16", GLM, 3, 9000),
+                                              ("bf16", GLM, 12, 300)])
+def test_decode_tree_of_bad_lengths_only(cuda_lib, dtype, dims, S, cap):
+    """No sequence has a tile: NaN and the flag; the calls after it, on the same workspace and at once, are as
+    usual."""
+    x = mla_inputs(dims, 2, S, [40, 90], cap, dtype, 49, "cpu")
+    par = torch.from_numpy(random_parents(2, S, 5, absent=False)).to(DEV)
+    g = {k: v.to(DEV) for k, v in x.items()}
+    bad = torch.tensor([S - 1, cap + 1], dtype=torch.int32, device=DEV)
+    size = cuda_lib.decode_tree_workspace_size(dims, g["q"].dtype, 2, S, cap)
+    ws = torch.empty(max(size, 256), dtype=torch.uint8, device=DEV)
+
+    def call(T):
+        return cuda_lib.decode_tree(g["q"], g["Lc"], g["Rc"], T, par, g["kv_b"], dims, workspace=ws)
+    want = call(g["T"])
+    assert cuda_lib.device_status() == 0 and torch.isfinite(want).all()
+    outs = [call(T) for _ in range(20) for T in (bad, g["T"])]
+    assert cuda_lib.device_status() == cuda_lib.MLA_DEV_BAD_LENGTH
+    assert all(torch.isnan(out).all() for out in outs[::2]) and all(torch.equal(out, want) for out in outs[1::2])
