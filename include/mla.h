@@ -503,8 +503,8 @@ int mla_cache_append_tree_paged(const mla_dims* d, int dtype, int B, int S, cons
  * p (and q) are taken as distributions: values >= 0 whose sum is 1 up to
  * rounding; p_row and q_row >= V.  A context whose p has no finite positive
  * mass raises MLA_DEV_BAD_VALUE and gives token -1, a NaN at a rejected draft
- * included; contexts at which a child is accepted at once are not summed, and so
- * not looked at.  A bad node or a token
+ * included; a context of which no sum is taken, because a child was accepted, is
+ * not checked.  A bad node or a token
  * outside [0, V) raises MLA_DEV_BAD_INDEX and is never accepted.  No workspace. */
 int mla_tree_verify(int B, int S, int V, const float* p, long long p_row, long long p_batch, const float* q,
                     long long q_row, long long q_batch, const int32_t* tokens, const int32_t* parent, const float* u,

@@ -528,7 +528,7 @@ __device__ __forceinline__ void attn_softmax(const AttnParams& p, AttnShared& sh
   int it = 0, slot = 0, pos = 0, nkeys = 0;
   const int32_t* srow = nullptr;
   unsigned long long tmask = 0;
-  int base = 0;  // tree: keys before the tree rows that the node sees (0 for an absent node)
+  int base = 0;  // tree: T - S, the keys before the tree's rows (an absent node's tmask is 0: it sees none)
   bool ok = true, bad_idx = false;
   float lp[32];
 #pragma unroll

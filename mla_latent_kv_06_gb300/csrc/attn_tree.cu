@@ -47,10 +47,11 @@
 //
 // Measured: 8 trees of 64 nodes on 16k to 32k keys 1.03 ms, 1.70 PFLOP/s of the
 // formula's (1.80 issued), the sustained rate of the tensor pipe under the
-// power limit.  32 trees of 6 nodes on 1k to 32k keys 368 us, 1.23 PFLOP/s:
+// power limit.  32 trees of 6 nodes on 1k to 32k keys 372 us, 1.22 PFLOP/s:
 // with 3 pairs on a tile, 3.7 us a tile against 3.1 with 32 pairs, although
-// DRAM runs at a quarter of its rate; fetching the tiles into L2 ahead of time
-// changed nothing (315 against 313 us on 32 x 6 x 16384).
+// DRAM runs at a quarter of its rate and L2 below a fifth of its sectors'
+// (4 x 6 x 4096); fetching the tiles into L2 ahead of time changed nothing (315
+// against 313 us on 32 x 6 x 16384).
 #include "attn_tree.h"
 
 #include <atomic>

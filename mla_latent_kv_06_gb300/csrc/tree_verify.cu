@@ -32,8 +32,8 @@
 // Measured, vocabulary 131072, 32 trees of 24 nodes: 30 us, each byte of the
 // rows that are looked at read from memory once (31.7 MB, 0.9 TB/s), barriers
 // the first stall; a pass is about 6 us: loads and sums 3, totals and cluster
-// barrier 1.8, decision 1.2.  5 drafts of one user over 32000: 10 us; 8 trees of
-// 64 point drafts over 100003: 15 us.
+// barrier 1.8, decision 1.2.  5 drafts of one user over 32000: 9.4 us; 8 trees of
+// 64 point drafts over 100003: 14 us, 4 of them the walk over the children.
 #include <cooperative_groups.h>
 
 #include "common.cuh"
