@@ -64,7 +64,8 @@ enum mla_device_flag {
   MLA_DEV_BAD_LENGTH = 1,   /* some T[b] outside [S, T_cap]: that sequence was skipped      */
   MLA_DEV_BAD_INDEX = 2,    /* a selected index < 0 or > pos, or nsel outside [1, topk]     */
   MLA_DEV_TIMEOUT = 4,      /* a bounded wait inside a kernel ran out; the kernel returned  */
-  MLA_DEV_BAD_VALUE = 8     /* a distribution with no finite positive mass (mla_tree_verify) */
+  MLA_DEV_BAD_VALUE = 8     /* a distribution with no finite positive mass (mla_tree_verify),
+                               logits or settings that give none (mla_sample)               */
 };
 
 /* Message of the last failing call on this thread ("" if none). */
@@ -529,6 +530,40 @@ int mla_tree_commit(int n, void* const* cache, const int* row_bytes, int B, int 
 int mla_tree_commit_paged(int n, void* const* cache, const int* row_bytes, int B, int S, int num_pages,
                           int page_size, const int32_t* block_table, int max_pages, const int32_t* T,
                           const int32_t* path, const int32_t* n_acc, int32_t* T_out, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Sampling: tokens, and the distributions that mla_tree_verify takes
+ *
+ * Row (b, n) of the logits, x[0 .. V), with its sequence's or its own settings.
+ * Its tokens are ordered by logit from the highest down, equal ones (-0 equals
+ * 0) by index from the lowest up, and w[i] = exp((x[i] - max) / temperature):
+ *   top_k   keeps the first top_k tokens of the order   (<= 0 or >= V: all)
+ *   min_p   keeps those with w[i] >= min_p, the largest in any case   (<= 0: all)
+ *   top_p   keeps, of what the two leave with mass W, the shortest start of
+ *           the order whose mass reaches top_p W, one token at least  (>= 1: all)
+ *   temperature 0 keeps the first token of the order alone, whatever the others
+ *   token   the least i whose cumulative w, over the kept tokens in index
+ *           order, exceeds u times their mass (u below 0 or NaN counts as 0, u
+ *           of 1 or more as just below 1)
+ *   probs   w[i] / mass for the kept tokens, 0 for the others
+ * A logit of -inf is never kept.  A row without a finite logit, with a NaN or
+ * +inf, or with a setting that is NaN or a temperature that is negative or
+ * infinite raises MLA_DEV_BAD_VALUE and gives token -1 and NaN probabilities.
+ * Comparisons of masses hold to 2^-33 of each weight, with exact sums of weights
+ * rounded to 2^-44 of the largest; results do not depend on the launch.
+ *
+ *   logits  float or bf16 (dtype), row (b, n) at element b * l_batch + n * l_row
+ *           (values of a row contiguous; l_row >= V)
+ *   temperature, top_p, min_p float and top_k int32: one entry per sequence [B],
+ *           or per row [B, N] where per_row != 0; NULL: off (temperature 1)
+ *   u, token  float and int32 [B, N], both or neither
+ *   probs   float, row (b, n) at b * p_batch + n * p_row, or NULL; rows must not overlap
+ * token and probs must not overlap each other or an input, compared from first to last element.
+ * Vocabularies above 327680 return MLA_ERR_UNSUPPORTED.  No workspace.
+ * ------------------------------------------------------------------------- */
+int mla_sample(int B, int N, int V, int dtype, const void* logits, long long l_row, long long l_batch,
+               const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p, int per_row,
+               const float* u, int32_t* token, float* probs, long long p_row, long long p_batch, void* stream);
 
 #ifdef __cplusplus
 }

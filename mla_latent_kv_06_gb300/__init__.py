@@ -36,6 +36,7 @@ EXPORTS = (
     "mla_cache_append_fp8_paged",
     "mla_decode_tree_workspace_size", "mla_decode_tree", "mla_decode_tree_paged", "mla_cache_append_tree",
     "mla_cache_append_tree_paged", "mla_tree_verify", "mla_tree_commit", "mla_tree_commit_paged",
+    "mla_sample",
 )
 
 
@@ -114,6 +115,7 @@ def _declare(lib: ctypes.CDLL) -> None:
                                              _P]),
         "mla_tree_verify": (_I, [_I, _I, _I, _P, _LL, _LL, _P, _LL, _LL, _P, _P, _P, _P, _P, _P, _P]),
         "mla_tree_commit": (_I, [_I, _PP, _IP, _I, _I, _I, _P, _P, _P, _P, _P]),
+        "mla_sample": (_I, [_I, _I, _I, _I, _P, _LL, _LL, _P, _P, _P, _P, _I, _P, _P, _P, _LL, _LL, _P]),
         "mla_tree_commit_paged": (_I, [_I, _PP, _IP, _I, _I, _I, _I, _P, _I, _P, _P, _P, _P, _P]),
     }
     for name, (res, args) in sig.items():
@@ -860,3 +862,85 @@ def tree_commit(rows: CacheRows, T, path, n_acc, T_out=None, stream=None):
                                          n_acc.data_ptr(), T_out.data_ptr(), st)
     _check(rc)
     return T_out
+
+
+def _sample(logits, u, temperature, top_k, top_p, min_p, token, probs):
+    torch = _torch()
+    if logits.dim() not in (2, 3):
+        raise ValueError("logits must be [B, V] or [B, N, V]")
+    lead, V, index = logits.shape[:-1], logits.shape[-1], logits.get_device()
+    code = _dtype_code(logits)
+    strides = logits.stride()
+    if strides[-1] != 1 and V > 1:
+        raise ValueError("the values of a row of logits must be contiguous")
+    f32, i32 = torch.float32, torch.int32
+    settings = (temperature, top_k, top_p, min_p)
+    per_row = 0
+    for name, x in zip(("temperature", "top_k", "top_p", "min_p"), settings):
+        if x is None:
+            continue
+        if x.shape == lead:
+            per_row = 1
+        elif x.shape != lead[:1]:
+            raise ValueError(f"{name}: shape {tuple(x.shape)}, not {tuple(lead)} or {tuple(lead[:1])}")
+        want = i32 if x is top_k else f32
+        if not _all_plain(index, want, x):
+            _explain(logits.device, **{name: (x, want)})
+    if len({x.shape for x in settings if x is not None}) > 1:
+        raise ValueError("the settings must be given all per sequence or all per row")
+    if u is not None:
+        _want("u", u, *lead)
+        if not _all_plain(index, f32, u):
+            _explain(logits.device, u=(u, f32))
+        if token is None:
+            token = u.new_empty(lead, dtype=i32)
+        else:
+            _want("token", token, *lead)
+            _explain(logits.device, token=(token, i32))
+    B, N = lead[0], lead[1] if len(lead) == 2 else 1
+    l_row = strides[1] if len(lead) == 2 else V
+    p_ptr, p_row, p_batch = None, 0, 0
+    if probs is True:
+        probs = logits.new_empty(logits.shape, dtype=f32)
+    elif probs is not None:
+        _want("probs", probs, *logits.shape)
+        if probs.dtype is not f32 or probs.get_device() != index or (probs.stride(-1) != 1 and V > 1):
+            raise ValueError("probs must be float32 on the logits' GPU, with contiguous rows")
+    st = _current_stream(torch, index)
+    if probs is not None:
+        p_ptr, p_batch, p_row = probs.data_ptr(), probs.stride(0), probs.stride(1) if len(lead) == 2 else V
+    temperature, top_k, top_p, min_p = (None if x is None else x.data_ptr() for x in settings)
+    _check(lib().mla_sample(B, N, V, code, logits.data_ptr(), l_row, strides[0], temperature, top_k, top_p, min_p, per_row,
+                            None if u is None else u.data_ptr(), None if u is None else token.data_ptr(), p_ptr, p_row,
+                            p_batch, st))
+    return token, probs
+
+
+def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, token=None, probs=None, return_probs=False,
+           stream=None):
+    """Draws a token of each row of logits [B,V] or [B,N,V] (float32 or bfloat16, rows may be
+    strided) with the numbers u in [0,1), float32, one per row.
+
+    temperature, top_p, min_p (float32) and top_k (int32) are tensors [B], or one entry per
+    row, or None for off; temperature 0 takes the highest logit.  The filters apply in the
+    order top_k, min_p, top_p; of equal logits the lower index counts as the higher.
+    Returns the tokens, int32; with return_probs (or a tensor probs to write to) also the
+    distributions that they were drawn from, float32, as tree_verify's q."""
+    if stream is not None:
+        with _torch().cuda.stream(stream):
+            return sample(logits, u, temperature, top_k, top_p, min_p, token, probs, return_probs)
+    if u is None:
+        raise ValueError("u is needed")
+    if probs is None and return_probs:
+        probs = True
+    token, probs = _sample(logits, u, temperature, top_k, top_p, min_p, token, probs)
+    return token if probs is None else (token, probs)
+
+
+def sample_probs(logits, temperature=None, top_k=None, top_p=None, min_p=None, probs=None, stream=None):
+    """The distributions that `sample` draws from, float32 of the logits' shape: with the
+    target's logits [B,S+1,V] of a drafted tree, tree_verify's p."""
+    if stream is not None:
+        with _torch().cuda.stream(stream):
+            return sample_probs(logits, temperature, top_k, top_p, min_p, probs)
+    return _sample(logits, None, temperature, top_k, top_p, min_p, None, True if probs is None else probs)[1]

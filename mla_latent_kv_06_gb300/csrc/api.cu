@@ -1053,3 +1053,52 @@ MLA_EXPORT int mla_tree_commit_paged(int n, void* const* cache, const int* row_b
   a.n_acc = n_acc;
   return run_commit(a, n, cache, row_bytes, T_out, stream, "mla_tree_commit_paged launch");
 }
+
+// ---------------------------------------------------------------- sampling
+MLA_EXPORT int mla_sample(int B, int N, int V, int dtype, const void* logits, long long l_row, long long l_batch,
+                          const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
+                          int per_row, const float* u, int32_t* token, float* probs, long long p_row, long long p_batch,
+                          void* stream) {
+  if (B < 1 || N < 1 || V < 1 || (long long)B * N > (1 << 24))
+    return fail(MLA_ERR_INVALID, "bad sizes B=%d N=%d V=%d (at most 2^24 rows)", B, N, V);
+  if (dtype != MLA_F32 && dtype != MLA_BF16) return fail(MLA_ERR_INVALID, "unknown dtype %d", dtype);
+  if (V > mla::kMaxSampleVocab)
+    return fail(MLA_ERR_UNSUPPORTED, "vocabulary of %d tokens above %d", V, mla::kMaxSampleVocab);
+  if (!logits || (!token && !probs)) return fail(MLA_ERR_INVALID, "null logits, or neither token nor probs");
+  if (!token != !u) return fail(MLA_ERR_INVALID, "u and token go together");
+  const int el = dtype == MLA_F32 ? 4 : 2;
+  if (reinterpret_cast<uintptr_t>(logits) % el || reinterpret_cast<uintptr_t>(probs) % 4)
+    return fail(MLA_ERR_INVALID, "logits and probs must be aligned to their elements");
+  constexpr long long kFar = 1ll << 40;  // strides whose offsets stay within 64 bits
+  if ((N > 1 && l_row < V) || l_row < 0 || l_batch < 0 || l_row > kFar || l_batch > kFar)
+    return fail(MLA_ERR_INVALID, "logits: rows of %d values need l_row >= V and l_batch >= 0", V);
+  if (probs && (p_row < 0 || p_batch < 0 || p_row > kFar || p_batch > kFar || (N > 1 && p_row < V) ||
+                (B > 1 && p_batch < (long long)(N - 1) * p_row + V)))
+    return fail(MLA_ERR_INVALID, "probs: rows of %d values overlap with p_row=%lld and p_batch=%lld", V, p_row, p_batch);
+  // what is written, against what other rows still read
+  const uintptr_t rows = (uintptr_t)B * N, sets = per_row ? rows : (uintptr_t)B;
+  const auto at = [](const void* x) { return reinterpret_cast<uintptr_t>(x); };
+  const uintptr_t l_end = at(logits) + ((uintptr_t)(B - 1) * l_batch + (uintptr_t)(N - 1) * l_row + V) * el;
+  const uintptr_t p_end = probs ? at(probs) + ((uintptr_t)(B - 1) * p_batch + (uintptr_t)(N - 1) * p_row + V) * 4 : 0;
+  const void* in[6] = {logits, u, temperature, top_k, top_p, min_p};
+  const uintptr_t in_end[6] = {l_end, at(u) + 4 * rows, at(temperature) + 4 * sets, at(top_k) + 4 * sets,
+                               at(top_p) + 4 * sets, at(min_p) + 4 * sets};
+  const auto meets = [&](uintptr_t lo, uintptr_t hi) {
+    for (int i = 0; i < 6; ++i)
+      if (in[i] && lo < in_end[i] && at(in[i]) < hi) return true;
+    return false;
+  };
+  if ((token && meets(at(token), at(token) + 4 * rows)) || (probs && meets(at(probs), p_end)) ||
+      (token && probs && at(token) < p_end && at(probs) < at(token) + 4 * rows))
+    return fail(MLA_ERR_INVALID, "token and probs must not overlap the inputs or each other");
+  mla::SampleArgs a{B, N, V, dtype, logits, l_row, l_batch, temperature, top_k, top_p, min_p, per_row != 0, u, token,
+                    probs, p_row, p_batch, flags_ptr()};
+  if (!a.flags) return fail(MLA_ERR_CUDA, "cannot resolve the device status word");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  mla::call_begin();
+  mla::kernel_mark(st, "sample");
+  cudaError_t e = mla::launch_sample(a, st);
+  mla::call_end(st);
+  if (e != cudaSuccess) return cuda_fail(e, "mla_sample launch");
+  return MLA_OK;
+}

@@ -188,6 +188,26 @@ struct VerifyArgs {
 };
 cudaError_t launch_tree_verify(const VerifyArgs& a, cudaStream_t st);
 
+// Largest vocabulary of mla_sample: a row lies in the shared memory of 8 CTAs.
+constexpr int kMaxSampleVocab = 8 * 40960;
+
+struct SampleArgs {
+  int B, N, V, dtype;
+  const void* logits;  // row n of sequence b at element b * l_batch + n * l_row
+  long long l_row, l_batch;
+  const float* temperature;  // settings of row b * N + n: entry b * N + n where per_row, else b; null: off
+  const int32_t* top_k;
+  const float* top_p;
+  const float* min_p;
+  int per_row;
+  const float* u;  // [B, N], with token
+  int32_t* token;  // [B, N], or null
+  float* probs;    // as logits, or null
+  long long p_row, p_batch;
+  unsigned int* flags;
+};
+cudaError_t launch_sample(const SampleArgs& a, cudaStream_t st);
+
 // Caches of one commit launch: pointers travel in the launch parameters.
 constexpr int kCommitCaches = 128;
 

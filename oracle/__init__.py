@@ -51,6 +51,9 @@ Parity status of each function (what pins it, see tests/test_oracle_pins.py):
 Drafted trees (tree.py, see tests/test_tree_oracle.py): a chain equals the
 causal decode and append; hand-worked trees, acceptances and moves; the emitted
 token's distribution, integrated exactly over u, is the target's.
+
+Sampling (sample.py, see tests/test_sample_oracle.py): hand-worked rows, filters
+and draws; limits in which a filter keeps everything or one token.
 """
 from .mla import (  # noqa: F401
     e4m3_decode,
@@ -77,6 +80,10 @@ from .mla import (  # noqa: F401
     topk_select,
     sparse_decode,
     query_positions,
+)
+from .sample import (  # noqa: F401
+    sample_filter,
+    sample_token,
 )
 from .tree import (  # noqa: F401
     ancestors,
