@@ -36,7 +36,7 @@ EXPORTS = (
     "mla_cache_append_fp8_paged",
     "mla_decode_tree_workspace_size", "mla_decode_tree", "mla_decode_tree_paged", "mla_cache_append_tree",
     "mla_cache_append_tree_paged", "mla_tree_verify", "mla_tree_commit", "mla_tree_commit_paged",
-    "mla_sample",
+    "mla_sample", "mla_decode_shared_workspace_size", "mla_decode_shared_paged",
 )
 
 
@@ -115,6 +115,8 @@ def _declare(lib: ctypes.CDLL) -> None:
                                              _P]),
         "mla_tree_verify": (_I, [_I, _I, _I, _P, _LL, _LL, _P, _LL, _LL, _P, _P, _P, _P, _P, _P, _P]),
         "mla_tree_commit": (_I, [_I, _PP, _IP, _I, _I, _I, _P, _P, _P, _P, _P]),
+        "mla_decode_shared_workspace_size": (_SZ, [_DP, _I, _I, _I, _I, _I]),
+        "mla_decode_shared_paged": (_I, [_DP, _I, _I, _I, _P, _P, _P, _I, _I, _P, _I, _P, _I, _P, _I, _P, _P, _SZ, _P]),
         "mla_sample": (_I, [_I, _I, _I, _I, _P, _LL, _LL, _P, _P, _P, _P, _I, _P, _P, _P, _LL, _LL, _P]),
         "mla_tree_commit_paged": (_I, [_I, _PP, _IP, _I, _I, _I, _I, _P, _I, _P, _P, _P, _P, _P]),
     }
@@ -862,6 +864,65 @@ def tree_commit(rows: CacheRows, T, path, n_acc, T_out=None, stream=None):
                                          n_acc.data_ptr(), T_out.data_ptr(), st)
     _check(rc)
     return T_out
+
+
+# ------------------------------------------------------------- one prompt, many continuations
+def decode_shared_workspace_size(dims, dtype, B: int, S: int, T_cap: int, shared: int) -> int:
+    """Workspace bytes of decode_shared_paged (dtype: torch.float32 or torch.bfloat16);
+    T_cap = max_pages * page_size."""
+    torch = _torch()
+    code = MLA_BF16 if dtype in (torch.bfloat16, MLA_BF16) else MLA_F32
+    d = make_dims(dims)
+    return lib().mla_decode_shared_workspace_size(ctypes.byref(d), code, B, S, T_cap, shared)
+
+
+def decode_shared_paged(q, Lc_pages, Rc_pages, block_table, T, shared: int, kv_b, dims, out=None, out_dtype=None,
+                        workspace=None, stream=None):
+    """decode_paged of sequences whose first `shared` tokens (a host number) are the same cache
+    rows: the attention over them is computed once for the whole batch.  T counts all tokens,
+    S + shared <= T[b].  out [B,S,H,v_head] in out_dtype (float32 unless given; bfloat16 is
+    rounded once).  A workspace that is given must have decode_shared_workspace_size() bytes."""
+    torch = _torch()
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return decode_shared_paged(q, Lc_pages, Rc_pages, block_table, T, shared, kv_b, dims, out, out_dtype, workspace)
+    B, S, H, qk = q.shape
+    dtype, index, i32 = q.dtype, q.get_device(), torch.int32
+    num_pages, page_size, _ = ls = Lc_pages.shape
+    max_pages = block_table.shape[1]
+    if H != dims.H or qk != dims.qk_nope + dims.qk_rope:
+        raise ValueError(f"q has shape {tuple(q.shape)}, expected [B, S, {dims.H}, {dims.qk_nope + dims.qk_rope}]")
+    if ls[2] != dims.kv_lora or Rc_pages.shape != (num_pages, page_size, dims.qk_rope):
+        raise ValueError("cache shapes do not match dims")
+    code = _dtype_code(q)
+    if out is None:
+        out = torch.empty((B, S, H, dims.v_head), dtype=out_dtype or torch.float32, device=q.device)
+    else:
+        if out_dtype is not None and out.dtype != out_dtype:
+            raise TypeError("out does not have out_dtype")
+        _want("out", out, B, S, H, dims.v_head)
+    out_code = _dtype_code(out)
+    _want("T", T, B)
+    _want("block_table", block_table, B, max_pages)
+    _want("kv_b", kv_b, H, dims.qk_nope + dims.v_head, dims.kv_lora)
+    if not (_all_plain(index, dtype, q, Lc_pages, Rc_pages, kv_b) and _all_plain(index, i32, T, block_table)
+            and _all_plain(index, out.dtype, out)):
+        _explain(q.device, q=(q, dtype), Lc_pages=(Lc_pages, dtype), Rc_pages=(Rc_pages, dtype), kv_b=(kv_b, dtype), T=(T, i32),
+                 block_table=(block_table, i32), out=(out, out.dtype))
+    st = _current_stream(torch, index)
+    d = make_dims(dims)
+    if workspace is None:  # the library checks the size of one that is given
+        workspace, wsb = _workspace(lib().mla_decode_shared_workspace_size(ctypes.byref(d), code, B, S, max_pages * page_size,
+                                                                           shared), q.device, None)
+    else:
+        if workspace.get_device() != index or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be contiguous and on {q.device}")
+        wsb = workspace.numel() * workspace.element_size()
+    _check(lib().mla_decode_shared_paged(ctypes.byref(d), code, B, S, q.data_ptr(), Lc_pages.data_ptr(), Rc_pages.data_ptr(),
+                                         num_pages, page_size, block_table.data_ptr(), max_pages, T.data_ptr(), shared,
+                                         kv_b.data_ptr(), out_code, out.data_ptr(),
+                                         None if workspace is None else workspace.data_ptr(), wsb, st))
+    return out
 
 
 def _sample(logits, u, temperature, top_k, top_p, min_p, token, probs):

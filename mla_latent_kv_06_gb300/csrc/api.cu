@@ -164,7 +164,7 @@ MLA_EXPORT size_t mla_decode_absorbed_workspace_size(const mla_dims* d, int dtyp
 namespace {
 // Enqueues one absorbed decode (dense or over selected keys) on either path.
 int run_decode(mla::DecodeArgs& a, int dtype, bool sparse, void* workspace, size_t workspace_bytes,
-               void* stream, const char* what, bool own_call = true) {
+               void* stream, const char* what, bool own_call = true, bool shared = false) {
   if (!a.pages.table && (long long)a.B * a.T_cap >= (1ll << 31))
     return fail(MLA_ERR_UNSUPPORTED, "B*T_cap of 2^31 rows or more");
   a.flags = flags_ptr();
@@ -175,15 +175,17 @@ int run_decode(mla::DecodeArgs& a, int dtype, bool sparse, void* workspace, size
   cudaError_t e;
   if (own_call) mla::call_begin();
   if (pages_ok && tc_decode_ok(a.g, dtype, a.q, a.Lc, a.Rc, a.kv_b)) {
-    size_t need = mla::tc_decode_workspace_bytes(a.g, a.B, a.S, sparse ? a.topk : a.T_cap, sparse ? a.topk : 0,
-                                                 a.parent != nullptr);
+    size_t need = shared ? mla::tc_shared_workspace_bytes(a.B, a.S, a.T_cap, a.lead)
+                         : mla::tc_decode_workspace_bytes(a.g, a.B, a.S, sparse ? a.topk : a.T_cap, sparse ? a.topk : 0,
+                                                          a.parent != nullptr);
     if (need && (!workspace || workspace_bytes < need))
       return fail(MLA_ERR_INVALID, "workspace of %zu bytes < %zu required", workspace_bytes, need);
     if (reinterpret_cast<uintptr_t>(workspace) & 255u)
       return fail(MLA_ERR_INVALID, "workspace must be 256-byte aligned");
-    e = sparse ? mla::launch_sparse_decode_tc(a, workspace, workspace_bytes, st)
-               : mla::launch_decode_tc(a, workspace, workspace_bytes, st);
-  } else if (a.parent && mla::tree_simt_ok(a.g, a.B)) {
+    e = shared   ? mla::launch_decode_shared_tc(a, workspace, st)
+        : sparse ? mla::launch_sparse_decode_tc(a, workspace, workspace_bytes, st)
+                 : mla::launch_decode_tc(a, workspace, workspace_bytes, st);
+  } else if ((a.parent || shared) && mla::tree_simt_ok(a.g, a.B)) {
     const size_t need = mla::tree_simt_workspace_bytes(a.g, a.B, a.S, a.T_cap);
     if (need && (!workspace || workspace_bytes < need))
       return fail(MLA_ERR_INVALID, "workspace of %zu bytes < %zu required", workspace_bytes, need);
@@ -1052,6 +1054,50 @@ MLA_EXPORT int mla_tree_commit_paged(int n, void* const* cache, const int* row_b
   a.path = path;
   a.n_acc = n_acc;
   return run_commit(a, n, cache, row_bytes, T_out, stream, "mla_tree_commit_paged launch");
+}
+
+// ---------------------------------------------------------------- shared prefix
+MLA_EXPORT size_t mla_decode_shared_workspace_size(const mla_dims* d, int dtype, int B, int S, int T_cap, int shared) {
+  mla::Geometry g;
+  if (!resolve(d, &g) || B < 1 || S < 1 || shared < 0 || T_cap > mla::kMaxTreeCap || T_cap < (long long)shared + S) return 0;
+  size_t tc = 0;
+  if (dtype == MLA_BF16 && mla::tc_decode_geometry_ok(g)) tc = round256(mla::tc_shared_workspace_bytes(B, S, T_cap, shared));
+  // the CUDA-core path takes over for page sizes and addresses the tensor-core path does not serve
+  const size_t simt = mla::tree_simt_ok(g, B) ? round256(mla::tree_simt_workspace_bytes(g, B, S, T_cap)) : 0;
+  return tc > simt ? tc : simt;
+}
+
+MLA_EXPORT int mla_decode_shared_paged(const mla_dims* d, int dtype, int B, int S, const void* q, const void* Lc_pages,
+                                       const void* Rc_pages, int num_pages, int page_size, const int32_t* block_table,
+                                       int max_pages, const int32_t* T, int shared, const void* kv_b, int out_dtype,
+                                       void* out, void* workspace, size_t workspace_bytes, void* stream) {
+  mla::DecodeArgs a{};
+  int rc = check_common(d, dtype, B, S, &a.g);
+  if (rc) return rc;
+  rc = check_pages(S, num_pages, page_size, block_table, max_pages, &a.pages);
+  if (rc) return rc;
+  a.T_cap = max_pages * page_size;
+  if (out_dtype != MLA_F32 && out_dtype != MLA_BF16) return fail(MLA_ERR_INVALID, "unknown out_dtype %d", out_dtype);
+  if (shared < 0 || (long long)shared + S > a.T_cap)
+    return fail(MLA_ERR_INVALID, "shared=%d tokens and S=%d new ones do not fit the capacity of %d", shared, S, a.T_cap);
+  if (a.T_cap > mla::kMaxTreeCap)
+    return fail(MLA_ERR_UNSUPPORTED, "capacity of %d rows above %d", a.T_cap, mla::kMaxTreeCap);
+  if ((long long)B * S > mla::kMaxSharedRows)
+    return fail(MLA_ERR_UNSUPPORTED, "%lld query rows above %d", (long long)B * S, mla::kMaxSharedRows);
+  if (!q || !Lc_pages || !Rc_pages || !T || !kv_b || !out) return fail(MLA_ERR_INVALID, "null tensor pointer");
+  if (!aligned16(out)) return fail(MLA_ERR_INVALID, "out must be 16-byte aligned");
+  a.B = B;
+  a.S = S;
+  a.q = q;
+  a.Lc = Lc_pages;
+  a.Rc = Rc_pages;
+  a.T = T;
+  a.kv_b = kv_b;
+  a.out = out;
+  a.out_bf16 = out_dtype == MLA_BF16;
+  a.lead = shared;
+  return run_decode(a, dtype, false, workspace, workspace_bytes, stream, "mla_decode_shared_paged launch", true,
+                    /*shared=*/true);
 }
 
 // ---------------------------------------------------------------- sampling

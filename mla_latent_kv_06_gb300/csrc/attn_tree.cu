@@ -45,6 +45,11 @@
 // probabilities 32).  The row sums add the rounded probabilities, so that both
 // sides of the quotient use the same weights.  Scores, running maximum, sums and context are fp32.
 //
+// kShared: a prefix that all sequences of a batch share.  Every query row sees all of its
+// whole tiles, so there is no tree, tail or mask; the two CTAs of a pair take rows 2i and
+// 2i + 1 of the batch, and the tiles of all pairs form one list that the clusters split
+// evenly.  The tail of the prefix and each sequence's own rows are attn_kernel's.
+//
 // Measured: 8 trees of 64 nodes on 16k to 32k keys 1.03 ms, 1.70 PFLOP/s of the
 // formula's (1.80 issued), the sustained rate of the tensor pipe under the
 // power limit.  32 trees of 6 nodes on 1k to 32k keys 372 us, 1.22 PFLOP/s:
@@ -177,17 +182,25 @@ __device__ __forceinline__ void commit_pair(uint64_t* bar, uint32_t lead) {
       : "memory");
 }
 
-// The pieces (sequence, tile range) of one chunk of the tile list.
+// The pieces of one chunk of the tile list: (sequence, tile range), or with a shared
+// prefix, whose rows are all alike, (pair of rows, tile range).
+template <bool kShared>
 struct Pieces {
   const int32_t* ts;
-  int B, b, lo, hi;
+  int B, b, lo, hi, tiles;
   long long c0, c1;
+  __device__ __forceinline__ long long first(int i) const { return kShared ? (long long)i * tiles : ts[i]; }
   __device__ __forceinline__ void start(const PairParams& p, int g) {
     ts = p.tile_start;
-    B = p.B;
-    const long long N = ts[B];
+    B = kShared ? p.NP : p.B;
+    tiles = p.tiles;
+    const long long N = first(B);
     c0 = N * g / p.G;
     c1 = N * (g + 1) / p.G;
+    if (kShared) {
+      b = (int)(c0 / tiles) - 1;
+      return;
+    }
     int l = 0, h = B;  // first sequence whose tiles reach past c0
     while (l < h) {
       const int mid = (l + h) >> 1;
@@ -198,7 +211,7 @@ struct Pieces {
   }
   __device__ __forceinline__ bool next() {
     for (++b; b < B; ++b) {
-      const long long a = ts[b], e = ts[b + 1];
+      const long long a = first(b), e = first(b + 1);
       if (a >= c1) return false;
       lo = (int)((a > c0 ? a : c0) - a);
       hi = (int)((e < c1 ? e : c1) - a);
@@ -213,7 +226,9 @@ struct Tile {
   int row0, keys;  // prefix: first key and number of keys (a multiple of 16); tail: staged rows
 };
 
+template <bool kShared>
 __device__ __forceinline__ Tile tile_at(int Tb, int S, int k) {
+  if (kShared) return Tile{false, k * kPairTile, kPairTile};
   const int b16 = pair_base16(Tb, S);
   Tile t;
   t.row0 = k * kPairTile;
@@ -230,7 +245,12 @@ __device__ __noinline__ bool slow_wait(uint64_t* bar, uint32_t parity, volatile 
   return mbar_wait(bar, parity, abort, flags, limit_ns);
 }
 
+// Bytes of one CTA's query block: with a shared prefix the rotated query is one term.
+template <bool kShared>
+constexpr uint32_t query_bytes() { return kShared ? 9 * kQAtom : kQBytes; }
+
 // ------------------------------------------------------------ TMA producer (warp 0 of each CTA, converged)
+template <bool kShared>
 __device__ __forceinline__ void produce(const PairParams& p, Shared& sh, unsigned char* smem, uint32_t rank, int g, int pair,
                                         int* issued, int* q_issued) {
   volatile int* abort = &sh.abort;
@@ -261,13 +281,14 @@ __device__ __forceinline__ void produce(const PairParams& p, Shared& sh, unsigne
     int y[2];
   };
   auto rows_of = [&](int b, int Tb, int k) -> Rows {
-    const Tile t = tile_at(Tb, p.S, k);
+    const Tile t = tile_at<kShared>(Tb, p.S, k);
+    if (kShared) b = 0;
     if (t.tail) return Rows{{b * kPairStage, b * kPairStage}};
     bool bad = false;
     Rows r;
     r.y[0] = (int)cache_row(p.pages, b, p.T_cap, t.row0, &bad);
     // no key in the second half: its rows are not looked up (any do)
-    r.y[1] = t.row0 + 128 < Tb ? (int)cache_row(p.pages, b, p.T_cap, t.row0 + 128, &bad) : r.y[0];
+    r.y[1] = kShared || t.row0 + 128 < Tb ? (int)cache_row(p.pages, b, p.T_cap, t.row0 + 128, &bad) : r.y[0];
     if (bad) raise_flag(p.flags, MLA_DEV_BAD_INDEX);
     return r;
   };
@@ -294,24 +315,25 @@ __device__ __forceinline__ void produce(const PairParams& p, Shared& sh, unsigne
       }
     }
   };
-  Pieces pc;
+  Pieces<kShared> pc;
   int np = 0;
   for (pc.start(p, g); ok && uni(pc.next()); ++np) {
-    const int Tb = p.T[pc.b];
+    const int Tb = kShared ? 0 : p.T[pc.b];
     ok = wait(&sh.q_empty, (np & 1) ^ 1);
     if (!ok) break;
-    expect_bytes(smem_u32(&sh.q_full), 2 * kQBytes, arm);
+    expect_bytes(smem_u32(&sh.q_full), 2 * query_bytes<kShared>(), arm);
     const uint32_t qbar = in_cta(&sh.q_full, 0);
-    const int qrow = (pc.b * p.S + 2 * pair + (int)rank) * kRows;  // past the last node: another row or zeros
+    // past the last node: another row or zeros
+    const int qrow = (kShared ? 2 * pc.b + (int)rank : pc.b * p.S + 2 * pair + (int)rank) * kRows;
     for (int d = 0; d < 9; ++d) load_2d(smem_u32(smem + d * kQAtom), &p.mQ, 64 * d, qrow, qbar, lead);
-    load_2d(smem_u32(smem + 9 * kQAtom), &p.mQl, 0, qrow, qbar, lead);
+    if (!kShared) load_2d(smem_u32(smem + 9 * kQAtom), &p.mQl, 0, qrow, qbar, lead);
     ++*q_issued;
     Rows r0 = rows_of(pc.b, Tb, pc.lo), r1 = pc.lo + 1 < pc.hi ? rows_of(pc.b, Tb, pc.lo + 1) : r0;
-    load_k(tile_at(Tb, p.S, pc.lo), r0);
+    load_k(tile_at<kShared>(Tb, p.S, pc.lo), r0);
     for (int k = pc.lo; uni(k < pc.hi) && ok; ++k) {
       const Rows r2 = k + 2 < pc.hi ? rows_of(pc.b, Tb, k + 2) : r1;
-      if (uni(k + 1 < pc.hi)) load_k(tile_at(Tb, p.S, k + 1), r1);
-      if (ok) load_v(tile_at(Tb, p.S, k), r0);
+      if (uni(k + 1 < pc.hi)) load_k(tile_at<kShared>(Tb, p.S, k + 1), r1);
+      if (ok) load_v(tile_at<kShared>(Tb, p.S, k), r0);
       r0 = r1;
       r1 = r2;
     }
@@ -321,6 +343,7 @@ __device__ __forceinline__ void produce(const PairParams& p, Shared& sh, unsigne
 }
 
 // ------------------------------------------------------------ MMA issuer (warp 1 of the leader CTA, converged)
+template <bool kShared>
 __device__ __forceinline__ void issue(const PairParams& p, Shared& sh, unsigned char* smem, uint32_t tmem_any, int g) {
   volatile int* abort = &sh.abort;
   const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_any, 0), lead = elect_lane();
@@ -362,7 +385,7 @@ __device__ __forceinline__ void issue(const PairParams& p, Shared& sh, unsigned 
       const uint64_t db = dK + (uint64_t)(s * (kStageBytes >> 4)), da = dQ + (uint64_t)(a * (kQAtom >> 4));
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk) mma_pair(d, da + 2 * kk, db + 2 * kk, idS, (a | kk) != 0 ? 1u : 0u, lead);
-      if (a == 8) {  // the rotary keys again, with what rounding the rotated query left
+      if (!kShared && a == 8) {  // the rotary keys again, with what rounding the rotated query left
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) mma_pair(d, da + (kQAtom >> 4) + 2 * kk, db + 2 * kk, idS, 1u, lead);
       }
@@ -370,10 +393,10 @@ __device__ __forceinline__ void issue(const PairParams& p, Shared& sh, unsigned 
     }
     commit_pair(&sh.s_full[j & 1], lead);
   };
-  Pieces pc;
+  Pieces<kShared> pc;
   int np = 0;
   for (pc.start(p, g); ok && uni(pc.next()); ++np) {
-    const int Tb = p.T[pc.b];
+    const int Tb = kShared ? 0 : p.T[pc.b];
     ok = wait(&sh.q_full, np & 1);
     if (!ok) break;
     tc_fence_after();
@@ -387,9 +410,9 @@ __device__ __forceinline__ void issue(const PairParams& p, Shared& sh, unsigned 
       ok = ok && wait(&sh.p_full, it & 1);
       if (!ok) break;
       tc_fence_after();
-      const Tile t = tile_at(Tb, p.S, k);
+      const Tile t = tile_at<kShared>(Tb, p.S, k);
       const uint32_t keep = uni(k > pc.lo) ? 1u : 0u;
-      if (uni(t.keys == kPairTile)) {
+      if (kShared || uni(t.keys == kPairTile)) {
 #pragma unroll 1
         for (int kc = 0; kc < 4; ++kc) {
 #pragma unroll
@@ -443,6 +466,7 @@ __device__ __forceinline__ unsigned long long low_bits(int n) {
   return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1;
 }
 
+template <bool kShared>
 __device__ __forceinline__ void soften(const PairParams& p, Shared& sh, unsigned char* smem, uint32_t tmem, uint32_t rank,
                                        int g, int pair) {
   volatile int* abort = &sh.abort;
@@ -453,14 +477,14 @@ __device__ __forceinline__ void soften(const PairParams& p, Shared& sh, unsigned
   const uint32_t t_lane = tmem + ((uint32_t)(32 * q) << 16);
   const uint32_t p_bar = in_cta(&sh.p_full, 0);
   unsigned char* prow = smem + kQBytes + (key0 >> 6) * 8192 + row * 128;
-  const int s = 2 * pair + (int)rank;
   const float c = p.c;
   int it = 0;
-  Pieces pc;
+  Pieces<kShared> pc;
   for (pc.start(p, g); pc.next();) {
-    const int b = pc.b, Tb = p.T[b], b16 = pair_base16(Tb, p.S);
+    const int b = pc.b, Tb = kShared ? 0 : p.T[b], b16 = kShared ? 0 : pair_base16(Tb, p.S);
+    const int s = 2 * (kShared ? b : pair) + (int)rank, rows = kShared ? p.R : p.S;
     unsigned long long mask = 0;
-    if (s < p.S) {
+    if (!kShared && s < p.S) {
       const TreeNode node = tree_node(p.parent + (size_t)b * p.S, s);
       mask = node.mask;
       if (node.state == kNodeBad && tsm == 0) raise_flag(p.flags, MLA_DEV_BAD_INDEX);
@@ -469,7 +493,7 @@ __device__ __forceinline__ void soften(const PairParams& p, Shared& sh, unsigned
     float lsum = 0.f;
     for (int k = pc.lo; k < pc.hi; ++k, ++it) {
       const bool first = k == pc.lo;
-      const Tile t = tile_at(Tb, p.S, k);
+      const Tile t = tile_at<kShared>(Tb, p.S, k);
       bool fail = !mbar_wait(&sh.s_full[it & 1], (it >> 1) & 1, abort, p.flags, p.wait_ns);
       if (bar_red_or(1, kSoft, fail)) return;
       tc_fence_after();
@@ -479,7 +503,7 @@ __device__ __forceinline__ void soften(const PairParams& p, Shared& sh, unsigned
       // issuing warp's, whose fetches otherwise stall the tensor pipe.
       const uint32_t sc = t_lane + kColS + 128 * (it & 1) + 64 * ch;
       unsigned long long vis = ~0ull;  // bit i: key key0 + i is visible
-      const bool masked = t.tail || t.keys < kPairTile || mask == 0;
+      const bool masked = kShared ? false : t.tail || t.keys < kPairTile || mask == 0;
       if (masked) {
         vis = low_bits(t.keys - key0);
         if (t.tail) {  // the prefix remainder, then the tree's rows through the node's mask
@@ -503,7 +527,7 @@ __device__ __forceinline__ void soften(const PairParams& p, Shared& sh, unsigned
           }
         } else {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) least = fminf(least, v[i]);
+          for (int i = 0; i < 16; ++i) least = kShared ? least : fminf(least, v[i]);
 #pragma unroll
           for (int i = 0; i < 16; ++i) mx = fmaxf(mx, v[i]);
         }
@@ -593,8 +617,8 @@ __device__ __forceinline__ void soften(const PairParams& p, Shared& sh, unsigned
     tc_fence_after();
     sh.red[2 * (q >> 1) + ch][row] = lsum;
     named_barrier(1, kSoft);
-    const size_t slot = (size_t)(g + b) * p.S + s;
-    if (s < p.S) {
+    const size_t slot = kShared ? (size_t)(g + b) * 2 + rank : (size_t)(g + b) * p.S + s;
+    if (s < rows) {
       if (tsm < kRows) {
         float* ml = p.ml_part + (slot * kRows + tsm) * 2;
         ml[0] = sh.m[tsm];
@@ -627,6 +651,7 @@ __device__ __forceinline__ void soften(const PairParams& p, Shared& sh, unsigned
   }
 }
 
+template <bool kShared>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_pair_kernel(const __grid_constant__ PairParams p) {
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -634,7 +659,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_pa
   __shared__ Shared sh;
   const int warp = threadIdx.x >> 5;
   const uint32_t rank = cta_rank();
-  const int cluster = blockIdx.x >> 1, pair = cluster % p.NP, g = cluster / p.NP;
+  const int cluster = blockIdx.x >> 1, pair = kShared ? 0 : cluster % p.NP, g = kShared ? cluster : cluster / p.NP;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) mbar_init(&sh.full[i], 1);
     for (int i = 0; i < kFree; ++i) mbar_init(&sh.free2[i], 1);
@@ -662,15 +687,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_pa
 
   int issued = 0, q_issued = 0;
   if (warp == 0) {
-    produce(p, sh, smem, rank, g, pair, &issued, &q_issued);
+    produce<kShared>(p, sh, smem, rank, g, pair, &issued, &q_issued);
   } else if (warp == 1) {
-    if (rank == 0) issue(p, sh, smem, tmem, g);
+    if (rank == 0) issue<kShared>(p, sh, smem, tmem, g);
     // both CTAs: every MMA and every arrival of its commits has happened
     volatile int no_abort = 0;
     mbar_wait(&sh.mma_done, 0, &no_abort, p.flags, p.wait_ns > kDrainNs ? p.wait_ns : kDrainNs);
     __syncwarp();
   } else {
-    soften(p, sh, smem, tmem, rank, g, pair);
+    soften<kShared>(p, sh, smem, tmem, rank, g, pair);
     __syncwarp();
   }
   // Never leave with copies in flight.  A stage's barrier expects the leader's
@@ -701,7 +726,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_pa
     }
     const int qo = sh.q_issued[0], qp = sh.q_issued[1], qt = max(qo, qp);
     if (qt > 0) {
-      settle(&sh.q_full, qt - 1, qo, qp, kQBytes);
+      settle(&sh.q_full, qt - 1, qo, qp, query_bytes<kShared>());
       mbar_wait(&sh.q_full, (qt - 1) & 1, &no_abort, p.flags, drain);
     }
   }
@@ -742,18 +767,27 @@ int pair_chunks(int B, int S, int T_cap, int sms) {
   return best;
 }
 
-cudaError_t launch_attn_pair(const PairParams& p, cudaStream_t st) {
+namespace {
+
+template <bool kShared>
+cudaError_t launch(const PairParams& p, int clusters, cudaStream_t st) {
   static std::atomic<unsigned long long> done{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const unsigned long long bit = 1ull << (dev & 63);
   if (!(done.load() & bit)) {
-    e = cudaFuncSetAttribute(attn_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    e = cudaFuncSetAttribute(attn_pair_kernel<kShared>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (e != cudaSuccess) return e;
     done.fetch_or(bit);
   }
-  return launch_pdl(attn_pair_kernel, dim3((unsigned)(2 * p.G * p.NP)), dim3(kThreads), kSmem, st, p);
+  return launch_pdl(attn_pair_kernel<kShared>, dim3((unsigned)(2 * clusters)), dim3(kThreads), kSmem, st, p);
 }
+
+}  // namespace
+
+cudaError_t launch_attn_pair(const PairParams& p, cudaStream_t st) { return launch<false>(p, p.G * p.NP, st); }
+
+cudaError_t launch_attn_prefix(const PairParams& p, cudaStream_t st) { return launch<true>(p, p.G, st); }
 
 }  // namespace mla

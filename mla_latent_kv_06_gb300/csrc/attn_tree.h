@@ -33,6 +33,7 @@ struct PairParams {
   const int32_t* parent;
   const int32_t* tile_start;  // [B + 1] prefix of pair_tiles
   int B, S, T_cap, G, NP;     // G chunks of the tile list, NP = ceil(S / 2) node pairs
+  int R, tiles;               // shared prefix: query rows (NP = ceil(R / 2) pairs), whole tiles of the prefix
   float c;                    // softmax scale * log2(e)
   float* o_part;              // [(g + b) * S + s][64][512]
   float* ml_part;             // [(g + b) * S + s][64][2]
@@ -46,5 +47,14 @@ constexpr int kPairChunks = 256;
 int pair_chunks(int B, int S, int T_cap, int sms);
 
 cudaError_t launch_attn_pair(const PairParams& p, cudaStream_t st);
+
+// The same pass of all R query rows over the first `tiles` tiles of sequence 0: the
+// list holds the tiles of every pair of rows, and chunk g's partials of pair i are
+// slots 2 (g + i) and 2 (g + i) + 1.
+inline int prefix_chunks(int NP, int tiles, int sms) {
+  const long long items = (long long)NP * tiles, clusters = sms / 2 > 0 ? sms / 2 : 1;
+  return (int)(items < clusters ? items : clusters);
+}
+cudaError_t launch_attn_prefix(const PairParams& p, cudaStream_t st);
 
 }  // namespace mla

@@ -44,7 +44,7 @@ __global__ void __launch_bounds__(kThreads) decode_simt_kernel(DecodeArgs a) {
   int* tok = reinterpret_cast<int*>(sc + kChunk);  // [kChunk] cache row of each slot, -1 if masked
 
   const int Tb = a.T[b];
-  const bool bad_len = (Tb < a.S || Tb > a.T_cap);
+  const bool bad_len = (Tb < a.S + a.lead || Tb > a.T_cap);
   TreeNode node{};
   if (kTree) node = tree_node(a.parent + (size_t)b * a.S, s);
   const int base = Tb - a.S;

@@ -828,6 +828,7 @@ struct AbsorbParams {
   unsigned int* flags;
   PageTable pages;
   const int32_t* parent;  // tree attention: [B, S] parent indices
+  int t0, lead;           // shared prefix: the plan's tiles start at key t0; lengths below S + lead are bad
   int rope_x;             // tree: blocks along x that work on the head; any more stage the tails
   __nv_bfloat16* tail;    // pair attention: staged tail rows [B, kPairStage, 576], else null
   __nv_bfloat16* qlow;    // pair attention: the rotated queries' remainders [R, 64, 64]
@@ -1060,8 +1061,8 @@ __global__ void __launch_bounds__(kAbsThreads, 2) absorb_kernel(const AbsorbPara
       if (r < NR) {
         const int b = p.sparse ? r / p.S : r;
         const int Tb = p.T[b];
-        int bad = (Tb < p.S || Tb > p.T_cap) ? MLA_DEV_BAD_LENGTH : 0;
-        int nk = Tb;
+        int bad = (Tb < p.S + p.lead || Tb > p.T_cap) ? MLA_DEV_BAD_LENGTH : 0;
+        int nk = Tb - p.t0;
         if (!bad && p.sparse) {
           nk = p.nsel[r];
           if (nk < 1 || nk > p.topk) bad = MLA_DEV_BAD_INDEX;
@@ -1637,6 +1638,113 @@ __global__ void __launch_bounds__(256) merge_pair_kernel(const PairMergeParams p
 }
 
 // ===========================================================================
+// Merge of a shared-prefix call: the partials of a row are those of its pair in
+// the prefix pass and those of its sequence's own keys.  Otherwise as
+// merge_pair_kernel.
+// ===========================================================================
+struct SharedMergeParams {
+  const float* o_part;   // the prefix's slots, then the own keys' from slot `own` on
+  const float* ml_part;
+  const int32_t* tile_start;  // of the own keys
+  const int32_t* T;
+  const int32_t* bad;
+  __nv_bfloat16* clat;  // [R, 64, 1024]
+  float* inv_l;         // [R, 64]
+  int B, S, G, t0;      // own keys: chunks, first key
+  int NP, tiles, Gp;    // prefix: pairs of rows, tiles, chunks
+  int own;
+};
+
+template <int kParts>
+__global__ void __launch_bounds__(256) merge_shared_kernel(const SharedMergeParams p) {
+  constexpr int kVec = 4 / kParts, kDeep = kParts == 4 ? 8 : 2;
+  grid_dep_wait();
+  grid_dep_launch();
+  const int lane = threadIdx.x & 31;
+  const long long gw = ((long long)blockIdx.x * 256 + threadIdx.x) >> 5;
+  const int part = (int)(gw % kParts);
+  const long long rh = gw / kParts;
+  const int r = (int)(rh / kH), h = (int)(rh % kH);
+  if (r >= p.B * p.S) return;
+  const int b = r / p.S, s = r % p.S;
+  __nv_bfloat16* dst = p.clat + ((size_t)r * kH + h) * (2 * kDl) + 128 * part + 4 * lane;
+  const bool broken = p.bad[b] != 0;
+  float inv = broken ? qnan() : 1.f;
+  float4 acc[kVec];
+#pragma unroll
+  for (int v = 0; v < kVec; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (!broken) {
+    const int pair = r >> 1;
+    const long long Np = (long long)p.NP * p.tiles, a = (long long)pair * p.tiles;
+    const int plo = p.tiles ? chunk_of(a, Np, p.Gp) : 0, n0 = p.tiles ? chunk_of(a + p.tiles - 1, Np, p.Gp) - plo + 1 : 0;
+    const long long N = p.tile_start[p.B];
+    const int glo = chunk_of(p.tile_start[b], N, p.G), n = n0 + chunk_of(p.tile_start[b + 1] - 1, N, p.G) - glo + 1;
+    // the row's i-th split: every chunk of the prefix holds tiles of the pair, one of the own
+    // keys may have none that the row sees
+    auto slot_of = [&](int i) -> long long {
+      if (i < n0) return (long long)(plo + i + pair) * 2 + (r & 1);
+      if (i >= n) return -1;
+      int lo, hi;
+      const int g = glo + i - n0;
+      piece_range<false>(p.tile_start, p.T, p.S, s, b, g, p.G, N, &lo, &hi, p.t0);
+      return lo < hi ? p.own + (long long)(g + b) * p.S + s : -1;
+    };
+    float M = -INFINITY, L = 0.f;
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      const long long slot = slot_of(i0 + lane);
+      if (slot >= 0) M = fmaxf(M, p.ml_part[(slot * kH + h) * 2]);
+    }
+    M = warp_max(M);
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      const long long mine = slot_of(i0 + lane);
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (mine >= 0) ml = *reinterpret_cast<const float2*>(p.ml_part + (mine * kH + h) * 2);
+      const float w = mine >= 0 ? exp2f(ml.x - M) : 0.f;
+      L += warp_sum(w * ml.y);
+      const int cnt = min(32, n - i0);
+      for (int j0 = 0; j0 < cnt; j0 += kDeep) {
+        float4 o[kDeep][kVec];
+        float wg[kDeep];
+#pragma unroll
+        for (int u = 0; u < kDeep; ++u) {
+          const int j = min(j0 + u, 31);
+          const long long slot = __shfl_sync(0xffffffffu, mine, j);
+          const bool use = j0 + u < cnt && slot >= 0;
+          wg[u] = __shfl_sync(0xffffffffu, w, j);
+          if (!use) wg[u] = 0.f;
+          const float4* src = reinterpret_cast<const float4*>(p.o_part + ((use ? slot : 0) * kH + h) * kDl + 128 * part + 4 * lane);
+#pragma unroll
+          for (int v = 0; v < kVec; ++v) o[u][v] = use ? src[32 * v] : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int u = 0; u < kDeep; ++u)
+#pragma unroll
+          for (int v = 0; v < kVec; ++v) {
+            acc[v].x = fmaf(wg[u], o[u][v].x, acc[v].x);
+            acc[v].y = fmaf(wg[u], o[u][v].y, acc[v].y);
+            acc[v].z = fmaf(wg[u], o[u][v].z, acc[v].z);
+            acc[v].w = fmaf(wg[u], o[u][v].w, acc[v].w);
+          }
+      }
+    }
+    const float il = 1.f / L;
+#pragma unroll
+    for (int v = 0; v < kVec; ++v) acc[v] = make_float4(acc[v].x * il, acc[v].y * il, acc[v].z * il, acc[v].w * il);
+    if (L != L) inv = qnan();
+  }
+#pragma unroll
+  for (int v = 0; v < kVec; ++v) {
+    const uint2 hi = make_uint2(pack2(acc[v].x, acc[v].y), pack2(acc[v].z, acc[v].w));
+    const float2 h0 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&hi.x));
+    const float2 h1 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&hi.y));
+    *reinterpret_cast<uint2*>(dst + 128 * v) = hi;
+    *reinterpret_cast<uint2*>(dst + kDl + 128 * v) =
+        make_uint2(pack2(acc[v].x - h0.x, acc[v].y - h0.y), pack2(acc[v].z - h1.x, acc[v].w - h1.y));
+  }
+  if (lane == 0 && part == 0) p.inv_l[(size_t)r * kH + h] = inv;
+}
+
+// ===========================================================================
 // Gather kernel (sparse only): staging[r, j, 0:512 | 512:576] = Lc | Rc of key
 // sel[r, j] for j < nsel[r]; zero rows past nsel or for an index outside
 // [0, pos] (flagged).  CTA = (32 keys, row r); one warp per key row.
@@ -1719,7 +1827,9 @@ __global__ void __launch_bounds__(256) gather_kernel(const GatherParams p) {
 // ===========================================================================
 struct Plan {
   int G, NR, P, R, Kpad;
-  int Gp;  // pair attention of a tree: its chunks
+  int Gp;  // pair attention of a tree, or of a shared prefix: its chunks
+  int NP, tiles, t0;  // shared prefix: pairs of rows, whole tiles, first key after them
+  int own;            // slots of the prefix's partials, before the own keys'
   size_t off_q, off_ts, off_bad, off_o, off_ml, off_stage, off_clat, off_invl, off_q8, off_fh, off_tail, off_qlow, total;
 };
 
@@ -1769,13 +1879,21 @@ bool pair_pays(int B, int S, int T_cap) {
   return S >= 2 && (long long)B * S * T_cap >= (B > 1 && B * S > 4 ? 2048 : 12288);
 }
 
-Plan make_plan(int B, int S, int T_cap, int sparse_topk, bool tree = false) {
+// lead >= 0: a shared prefix of that many tokens.
+Plan make_plan(int B, int S, int T_cap, int sparse_topk, bool tree = false, int lead = -1) {
   Plan pl{};
   const int sms = sm_count();
   pl.R = B * S;
   if (!sparse_topk) {
     pl.NR = B;
-    const long long tiles = (long long)B * ((T_cap + kTile - 1) / kTile);
+    if (lead >= 0) {
+      pl.NP = (pl.R + 1) / 2;
+      pl.tiles = lead / kPairTile;
+      pl.t0 = pl.tiles * kPairTile;
+      pl.Gp = prefix_chunks(pl.NP, pl.tiles, sms);
+      pl.own = pl.tiles ? 2 * (pl.Gp + pl.NP - 1) : 0;
+    }
+    const long long tiles = (long long)B * ((T_cap - pl.t0 + kTile - 1) / kTile);
     long long G = sms / S;
     if (G < 1) G = 1;
     if (G > tiles) G = tiles;
@@ -1792,6 +1910,7 @@ Plan make_plan(int B, int S, int T_cap, int sparse_topk, bool tree = false) {
     pl.P = pl.G + pl.R - 1;
   }
   const bool pair = tree && pair_pays(B, S, T_cap);
+  const bool lift = pl.R > kSmallRows || lead >= 0;  // by GEMM
   if (pair) {
     static_assert(kPairChunks <= kMaxPieces, "the combine lists up to kMaxPieces splits of a row");
     pl.Gp = pair_chunks(B, S, T_cap, sms);
@@ -1805,21 +1924,21 @@ Plan make_plan(int B, int S, int T_cap, int sparse_topk, bool tree = false) {
   pl.off_bad = off;
   off = align256(off + (size_t)pl.NR * 4);
   pl.off_o = off;
-  off = align256(off + (size_t)pl.P * kH * kDl * 4);
+  off = align256(off + (size_t)(pl.own + pl.P) * kH * kDl * 4);
   pl.off_ml = off;
-  off = align256(off + (size_t)pl.P * kH * 2 * 4);
+  off = align256(off + (size_t)(pl.own + pl.P) * kH * 2 * 4);
   pl.Kpad = sparse_topk ? (sparse_topk + kTile - 1) / kTile * kTile : 0;
   pl.off_stage = off;  // two staging buffers: consecutive layers of one call alternate
   off = align256(off + 2 * (size_t)pl.R * pl.Kpad * kDc * 2);
   pl.off_clat = off;
-  off = align256(off + (pl.R > kSmallRows ? (size_t)pl.R * kH * kDl * (pair ? 4 : 2) : 0));
+  off = align256(off + (lift ? (size_t)pl.R * kH * kDl * (pair || lead >= 0 ? 4 : 2) : 0));
   pl.off_invl = off;
-  off = align256(off + (pl.R > kSmallRows ? (size_t)pl.R * kH * 4 : 0));
+  off = align256(off + (lift ? (size_t)pl.R * kH * 4 : 0));
   // FP8 cache (dense only): quantised query rows and their score factors
   pl.off_q8 = off;
-  off = align256(off + (sparse_topk || tree ? 0 : (size_t)pl.R * kH * kQ8Row));
+  off = align256(off + (sparse_topk || tree || lead >= 0 ? 0 : (size_t)pl.R * kH * kQ8Row));
   pl.off_fh = off;
-  off = align256(off + (sparse_topk || tree ? 0 : (size_t)pl.R * kH * 4));
+  off = align256(off + (sparse_topk || tree || lead >= 0 ? 0 : (size_t)pl.R * kH * 4));
   pl.off_tail = off;
   off = align256(off + (pair ? (size_t)B * kPairStage * kDc * 2 : 0));
   pl.off_qlow = off;
@@ -1829,7 +1948,9 @@ Plan make_plan(int B, int S, int T_cap, int sparse_topk, bool tree = false) {
 }
 
 // Many rows: merge of the splits, then the W_UV lift as a GEMM.
-cudaError_t run_lift(const DecodeArgs& a, const Plan& pl, unsigned char* w, bool sparse, bool pair, cudaStream_t st) {
+// two: the merged context is two bf16 terms (the pair attention's partials, those of a shared prefix).
+cudaError_t run_lift(const DecodeArgs& a, const Plan& pl, unsigned char* w, bool sparse, bool pair, bool shared,
+                     cudaStream_t st) {
   const Geometry& g = a.g;
   __nv_bfloat16* clat = reinterpret_cast<__nv_bfloat16*>(w + pl.off_clat);
   float* inv_l = reinterpret_cast<float*>(w + pl.off_invl);
@@ -1837,9 +1958,17 @@ cudaError_t run_lift(const DecodeArgs& a, const Plan& pl, unsigned char* w, bool
   const float* ml_part = reinterpret_cast<const float*>(w + pl.off_ml);
   const int32_t* ts = reinterpret_cast<const int32_t*>(w + pl.off_ts);
   const int32_t* bad = reinterpret_cast<const int32_t*>(w + pl.off_bad);
+  const bool two = pair || shared;
   kernel_mark(st, "merge");
   cudaError_t e;
-  if (pair) {
+  if (shared) {
+    const SharedMergeParams mp{o_part, ml_part, ts,    a.T,  bad,   clat,     inv_l, a.B,
+                               a.S,    pl.G,    pl.t0, pl.NP, pl.tiles, pl.Gp, pl.own};
+    const bool few = pl.R <= 32;
+    const long long warps = (long long)pl.R * kH * (few ? 4 : 1);
+    e = launch_pdl(few ? merge_shared_kernel<4> : merge_shared_kernel<1>, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, st,
+                   mp);
+  } else if (pair) {
     const PairMergeParams mp{o_part, ml_part, ts, bad, a.parent, clat, inv_l, a.B, a.S, pl.Gp};
     const bool few = pl.R <= 32;  // four warps per (row, head) while a warp each would not fill the GPU
     const long long warps = (long long)pl.R * kH * (few ? 4 : 1);
@@ -1863,7 +1992,7 @@ cudaError_t run_lift(const DecodeArgs& a, const Plan& pl, unsigned char* w, bool
   if (e != cudaSuccess) return e;
   GemmArgs gu{};
   gu.a_base = clat;
-  gu.a_ld_z = pair ? 2 * kDl : kDl;
+  gu.a_ld_z = two ? 2 * kDl : kDl;
   gu.a_ld_m = kH * gu.a_ld_z;
   gu.b_base = a.kv_b;
   gu.b_rows = (long long)kH * (g.Dn + g.Dv);
@@ -1880,8 +2009,8 @@ cudaError_t run_lift(const DecodeArgs& a, const Plan& pl, unsigned char* w, bool
   gu.scale = inv_l;
   gu.M = pl.R;
   gu.N = g.Dv;
-  gu.K = pair ? 2 * kDl : kDl;
-  gu.b_k_wrap = pair ? kDl : 0;
+  gu.K = two ? 2 * kDl : kDl;
+  gu.b_k_wrap = two ? kDl : 0;
   gu.Z = kH;
   gu.flags = a.flags;
   gu.wait_ns = a.wait_limit_ns;
@@ -1923,13 +2052,41 @@ cudaError_t run_pair(const DecodeArgs& a, const Plan& pl, unsigned char* w, long
   return launch_attn_pair(p, st);
 }
 
-cudaError_t run(const DecodeArgs& a, void* ws, bool sparse, cudaStream_t st) {
+// All query rows over the whole tiles of the prefix, read through sequence 0's pages.
+cudaError_t run_prefix(const DecodeArgs& a, const Plan& pl, unsigned char* w, long long pool_rows, cudaStream_t st) {
+  PairParams p{};
+  const uint64_t rows = (uint64_t)pool_rows;
+  if (!make_tmap_2d_bf16(&p.mQ, w + pl.off_q, (uint64_t)pl.R * kH, kDc, kDc, kH, 64) ||
+      !make_tmap_2d_bf16(&p.mK, a.Lc, rows, kDl, kDl, 128, 64) ||
+      !make_tmap_2d_bf16(&p.mKr, a.Rc, rows, kDr, kDr, 128, 64))
+    return cudaErrorInvalidValue;
+  const uint64_t vd[3] = {64, rows, kDl / 64}, vs[2] = {kDl * 2, 128};
+  const uint32_t box[3] = {64, 64, 2};
+  if (!make_tmap_3d_bf16(&p.mV, a.Lc, vd, vs, box)) return cudaErrorInvalidValue;
+  p.B = a.B;
+  p.S = a.S;
+  p.T_cap = a.T_cap;
+  p.G = pl.Gp;
+  p.NP = pl.NP;
+  p.R = pl.R;
+  p.tiles = pl.tiles;
+  p.c = a.g.scale * kLog2e;
+  p.o_part = reinterpret_cast<float*>(w + pl.off_o);
+  p.ml_part = reinterpret_cast<float*>(w + pl.off_ml);
+  p.flags = a.flags;
+  p.wait_ns = a.wait_limit_ns;
+  p.pages = a.pages;
+  kernel_mark(st, "prefix");
+  return launch_attn_prefix(p, st);
+}
+
+cudaError_t run(const DecodeArgs& a, void* ws, bool sparse, cudaStream_t st, bool shared = false) {
   const Geometry& g = a.g;
   const int B = a.B, S = a.S;
-  const Plan pl = make_plan(B, S, a.T_cap, sparse ? a.topk : 0, a.parent != nullptr);
+  const Plan pl = make_plan(B, S, a.T_cap, sparse ? a.topk : 0, a.parent != nullptr, shared ? a.lead : -1);
   const bool paged = a.pages.table != nullptr;
   const long long pool_rows = paged ? (long long)a.pages.num_pages * a.pages.page_size : (long long)B * a.T_cap;
-  if (pool_rows >= (1ll << 31) || (long long)B * a.T_cap >= (1ll << 31)) return cudaErrorInvalidValue;
+  if (pool_rows >= (1ll << 31) || (!shared && (long long)B * a.T_cap >= (1ll << 31))) return cudaErrorInvalidValue;
   if (paged && a.pages.page_size % kTile != 0) return cudaErrorInvalidValue;
   unsigned char* w = static_cast<unsigned char*>(ws);
   __nv_bfloat16* qcat = reinterpret_cast<__nv_bfloat16*>(w + pl.off_q);
@@ -1985,6 +2142,8 @@ cudaError_t run(const DecodeArgs& a, void* ws, bool sparse, cudaStream_t st) {
   ap.Dv = g.Dv;
   ap.topk = a.topk;
   ap.sparse = sparse ? 1 : 0;
+  ap.t0 = pl.t0;
+  ap.lead = a.lead;
   const bool pair = a.parent && pair_pays(B, S, a.T_cap);
   const bool big = pl.R > kSmallRows;
   ap.Lc = static_cast<const unsigned char*>(a.Lc);
@@ -1992,7 +2151,7 @@ cudaError_t run(const DecodeArgs& a, void* ws, bool sparse, cudaStream_t st) {
   ap.lat_row_bytes = a.lat_fp8 ? kDl : kDl * 2;
   // L2 prefetch on the small-batch path while the cache stays well inside L2
   ap.prefetch =
-      (!big && !sparse && (long long)B * a.T_cap * (ap.lat_row_bytes + kDr * 2) <= (48ll << 20)) ? 1 : 0;
+      (!big && !sparse && !shared && (long long)B * a.T_cap * (ap.lat_row_bytes + kDr * 2) <= (48ll << 20)) ? 1 : 0;
   ap.pages = sparse ? PageTable{} : a.pages;
   // the frequencies depend on the base alone: 32 powers cost the host 2 us a call
   static thread_local double turn_base = 0.0;
@@ -2076,6 +2235,10 @@ cudaError_t run(const DecodeArgs& a, void* ws, bool sparse, cudaStream_t st) {
   }
 
   // 2. attention
+  if (shared && pl.tiles > 0) {
+    e = run_prefix(a, pl, w, pool_rows, st);
+    if (e != cudaSuccess) return e;
+  }
   if (pair) {
     e = run_pair(a, pl, w, pool_rows, st);
     if (e != cudaSuccess) return e;
@@ -2117,15 +2280,17 @@ cudaError_t run(const DecodeArgs& a, void* ws, bool sparse, cudaStream_t st) {
     tp.lat_scale = a.lat_fp8 ? a.lat_scale : 1.f;
     tp.fh = fh;
     tp.qcat = qcat;
-    tp.o_part = o_part;
-    tp.ml_part = ml_part;
+    tp.o_part = o_part + (size_t)pl.own * kH * kDl;
+    tp.ml_part = ml_part + (size_t)pl.own * kH * 2;
+    tp.t0 = pl.t0;
+    tp.lead = a.lead;
     tp.flags = a.flags;
     tp.wait_ns = a.wait_limit_ns;
     tp.pages = sparse ? PageTable{} : a.pages;
     tp.parent = a.parent;
     // Streaming launches (one CTA per piece, at least two tiles a CTA by the
     // T_cap bound) take the instantiation with the single-lane score loop.
-    const long long tiles_cap = (long long)B * ((a.T_cap + kTile - 1) / kTile);
+    const long long tiles_cap = (long long)B * ((a.T_cap - pl.t0 + kTile - 1) / kTile);
     const bool stream = !sparse && tp.qsplit == 1 && tiles_cap >= 2LL * pl.G;
     auto kern = sparse     ? attn_kernel<true>
                 : a.parent ? (paged ? (stream ? attn_kernel<false, true, true, true> : attn_kernel<false, true, false, true>)
@@ -2147,7 +2312,7 @@ cudaError_t run(const DecodeArgs& a, void* ws, bool sparse, cudaStream_t st) {
   }
 
   // 3. merge of the splits and the W_UV lift
-  if (big) return run_lift(a, pl, w, sparse, pair, st);
+  if (big || shared) return run_lift(a, pl, w, sparse, pair, shared, st);
   CombineParams cp{};
   cp.kv_b = static_cast<const __nv_bfloat16*>(a.kv_b);
   cp.o_part = o_part;
@@ -2189,6 +2354,14 @@ int tc_decode_launch_count(bool sparse, int B, int S) {
 
 size_t tc_decode_workspace_bytes(const Geometry&, int B, int S, int T_cap, int sparse_topk, bool tree) {
   return make_plan(B, S, T_cap, sparse_topk, tree).total;
+}
+
+size_t tc_shared_workspace_bytes(int B, int S, int T_cap, int lead) {
+  return make_plan(B, S, T_cap, 0, false, lead).total;
+}
+
+cudaError_t launch_decode_shared_tc(const DecodeArgs& a, void* ws, cudaStream_t st) {
+  return run(a, ws, false, st, /*shared=*/true);
 }
 
 cudaError_t launch_decode_tc(const DecodeArgs& a, void* ws, size_t, cudaStream_t st) {

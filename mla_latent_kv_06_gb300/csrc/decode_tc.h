@@ -17,6 +17,10 @@ bool tc_decode_geometry_ok(const Geometry& g);
 // S new tokens form a drafted tree.
 size_t tc_decode_workspace_bytes(const Geometry& g, int B, int S, int T_cap, int sparse_topk, bool tree = false);
 
+// Decode of a batch that shares its first a.lead tokens.
+size_t tc_shared_workspace_bytes(int B, int S, int T_cap, int lead);
+cudaError_t launch_decode_shared_tc(const DecodeArgs& a, void* ws, cudaStream_t st);
+
 // Kernels launched by one tensor-core decode call.
 int tc_decode_launch_count(bool sparse, int B, int S);
 

@@ -60,6 +60,9 @@ struct DecodeArgs {
   // Tree attention (dense only): parents of the S drafted nodes [B, S], else null
   const int32_t* parent;
   int out_bf16;
+  // Shared prefix: tokens below `lead` lie in the same rows for all sequences, and
+  // every length is at least S + lead
+  int lead;
 };
 
 cudaError_t launch_decode_simt(const DecodeArgs& a, int dtype, bool sparse, cudaStream_t st);
@@ -161,7 +164,8 @@ struct KeyAppendArgs {
 };
 cudaError_t launch_index_key_append(const KeyAppendArgs& a, cudaStream_t st);
 
-// CUDA-core tree attention (kv_lora up to 512; other shapes take launch_decode_simt).
+// CUDA-core attention of a tree, or causal where a.parent is null (kv_lora up to 512; other shapes take
+// launch_decode_simt).
 bool tree_simt_ok(const Geometry& g, int B);
 size_t tree_simt_workspace_bytes(const Geometry& g, int B, int S, int T_cap);
 cudaError_t launch_tree_simt(const DecodeArgs& a, int dtype, void* ws, cudaStream_t st);
@@ -169,9 +173,12 @@ cudaError_t launch_tree_simt(const DecodeArgs& a, int dtype, void* ws, cudaStrea
 // Largest drafted tree: its ancestor masks are 64-bit words.
 constexpr int kMaxTree = 64;
 
-// Largest capacity of a sequence in tree attention: the kernels' key indices step
-// past a length by up to a tile (256), and stay within int.
+// Largest capacity of a sequence in tree and shared-prefix attention: the kernels' key indices
+// step past a length by up to a tile (256), and stay within int.
 constexpr int kMaxTreeCap = 0x7fffffff - 1023;
+
+// Query rows B * S of a shared-prefix call.
+constexpr int kMaxSharedRows = 32768;
 
 struct VerifyArgs {
   int B, S, V;
