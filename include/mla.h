@@ -264,6 +264,8 @@ int mla_sparse_decode_paged(const mla_dims* d, int dtype, int B, int S, const vo
  *              the same pages there (which row they are read through is left open).
  *   T          S + shared <= T[b] <= max_pages * page_size (a shorter one is a
  *              bad length, its outputs NaN)
+ *   parent     [B, S] int32 or NULL: the S new tokens are the nodes of drafted trees, as
+ *              for mla_decode_tree (absent nodes give zero, bad ones NaN), else a chain
  *   out        [B, S, H, v_head] float (out_dtype MLA_F32) or bf16 (MLA_BF16),
  *              16-byte aligned
  *   workspace: mla_decode_shared_workspace_size() bytes, T_cap = max_pages *
@@ -271,18 +273,18 @@ int mla_sparse_decode_paged(const mla_dims* d, int dtype, int B, int S, const vo
  * `shared` is a host value: a captured graph keeps it.  It may be less than what the
  * sequences really share, and need not be a multiple of a page.  With the tensor-core
  * geometry (bf16, pages of a multiple of 128 rows) whole 256-token blocks of the
- * prefix run on CTA pairs, two query rows at a time; everything else runs the CUDA-core
- * kernels, each sequence reading the prefix through its own table.  bf16 output
- * is rounded once from the float result.  FP8 caches are not served.
+ * prefix run on CTA pairs, any two query rows of the batch at a time; everything else
+ * runs the CUDA-core kernels, each sequence reading the prefix through its own table.
+ * Arithmetic and bf16 output as mla_decode_tree.  FP8 caches are not served.
  * Errors: as mla_decode_paged; shared < 0 or shared + S above the capacity returns
- * MLA_ERR_INVALID, B * S above 32768 and capacities above 2^31 - 1024 rows
+ * MLA_ERR_INVALID, S above 64, B * S above 8192 and capacities above 2^31 - 1024 rows
  * MLA_ERR_UNSUPPORTED.
  * ------------------------------------------------------------------------- */
 size_t mla_decode_shared_workspace_size(const mla_dims* d, int dtype, int B, int S, int T_cap, int shared);
 int mla_decode_shared_paged(const mla_dims* d, int dtype, int B, int S, const void* q, const void* Lc_pages,
                             const void* Rc_pages, int num_pages, int page_size, const int32_t* block_table,
-                            int max_pages, const int32_t* T, int shared, const void* kv_b, int out_dtype, void* out,
-                            void* workspace, size_t workspace_bytes, void* stream);
+                            int max_pages, const int32_t* T, int shared, const int32_t* parent, const void* kv_b,
+                            int out_dtype, void* out, void* workspace, size_t workspace_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
  * FP8 latent cache (a cache format of this library: the pages name FP8 only

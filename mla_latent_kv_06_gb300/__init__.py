@@ -116,7 +116,7 @@ def _declare(lib: ctypes.CDLL) -> None:
         "mla_tree_verify": (_I, [_I, _I, _I, _P, _LL, _LL, _P, _LL, _LL, _P, _P, _P, _P, _P, _P, _P]),
         "mla_tree_commit": (_I, [_I, _PP, _IP, _I, _I, _I, _P, _P, _P, _P, _P]),
         "mla_decode_shared_workspace_size": (_SZ, [_DP, _I, _I, _I, _I, _I]),
-        "mla_decode_shared_paged": (_I, [_DP, _I, _I, _I, _P, _P, _P, _I, _I, _P, _I, _P, _I, _P, _I, _P, _P, _SZ, _P]),
+        "mla_decode_shared_paged": (_I, [_DP, _I, _I, _I, _P, _P, _P, _I, _I, _P, _I, _P, _I, _P, _P, _I, _P, _P, _SZ, _P]),
         "mla_sample": (_I, [_I, _I, _I, _I, _P, _LL, _LL, _P, _P, _P, _P, _I, _P, _P, _P, _LL, _LL, _P]),
         "mla_tree_commit_paged": (_I, [_I, _PP, _IP, _I, _I, _I, _I, _P, _I, _P, _P, _P, _P, _P]),
     }
@@ -877,15 +877,17 @@ def decode_shared_workspace_size(dims, dtype, B: int, S: int, T_cap: int, shared
 
 
 def decode_shared_paged(q, Lc_pages, Rc_pages, block_table, T, shared: int, kv_b, dims, out=None, out_dtype=None,
-                        workspace=None, stream=None):
+                        workspace=None, stream=None, parent=None):
     """decode_paged of sequences whose first `shared` tokens (a host number) are the same cache
     rows: the attention over them is computed once for the whole batch.  T counts all tokens,
-    S + shared <= T[b].  out [B,S,H,v_head] in out_dtype (float32 unless given; bfloat16 is
+    S + shared <= T[b].  With parent [B,S] int32 the new tokens are drafted trees, as for
+    decode_tree_paged.  out [B,S,H,v_head] in out_dtype (float32 unless given; bfloat16 is
     rounded once).  A workspace that is given must have decode_shared_workspace_size() bytes."""
     torch = _torch()
     if stream is not None:
         with torch.cuda.stream(stream):
-            return decode_shared_paged(q, Lc_pages, Rc_pages, block_table, T, shared, kv_b, dims, out, out_dtype, workspace)
+            return decode_shared_paged(q, Lc_pages, Rc_pages, block_table, T, shared, kv_b, dims, out, out_dtype, workspace,
+                                       parent=parent)
     B, S, H, qk = q.shape
     dtype, index, i32 = q.dtype, q.get_device(), torch.int32
     num_pages, page_size, _ = ls = Lc_pages.shape
@@ -909,6 +911,9 @@ def decode_shared_paged(q, Lc_pages, Rc_pages, block_table, T, shared: int, kv_b
             and _all_plain(index, out.dtype, out)):
         _explain(q.device, q=(q, dtype), Lc_pages=(Lc_pages, dtype), Rc_pages=(Rc_pages, dtype), kv_b=(kv_b, dtype), T=(T, i32),
                  block_table=(block_table, i32), out=(out, out.dtype))
+    if parent is not None:
+        _want("parent", parent, B, S)
+        _explain(q.device, parent=(parent, i32))
     st = _current_stream(torch, index)
     d = make_dims(dims)
     if workspace is None:  # the library checks the size of one that is given
@@ -920,7 +925,7 @@ def decode_shared_paged(q, Lc_pages, Rc_pages, block_table, T, shared: int, kv_b
         wsb = workspace.numel() * workspace.element_size()
     _check(lib().mla_decode_shared_paged(ctypes.byref(d), code, B, S, q.data_ptr(), Lc_pages.data_ptr(), Rc_pages.data_ptr(),
                                          num_pages, page_size, block_table.data_ptr(), max_pages, T.data_ptr(), shared,
-                                         kv_b.data_ptr(), out_code, out.data_ptr(),
+                                         None if parent is None else parent.data_ptr(), kv_b.data_ptr(), out_code, out.data_ptr(),
                                          None if workspace is None else workspace.data_ptr(), wsb, st))
     return out
 

@@ -1059,7 +1059,8 @@ MLA_EXPORT int mla_tree_commit_paged(int n, void* const* cache, const int* row_b
 // ---------------------------------------------------------------- shared prefix
 MLA_EXPORT size_t mla_decode_shared_workspace_size(const mla_dims* d, int dtype, int B, int S, int T_cap, int shared) {
   mla::Geometry g;
-  if (!resolve(d, &g) || B < 1 || S < 1 || shared < 0 || T_cap > mla::kMaxTreeCap || T_cap < (long long)shared + S) return 0;
+  if (!resolve(d, &g) || B < 1 || S < 1 || S > mla::kMaxTree || (long long)B * S > mla::kMaxSharedRows) return 0;
+  if (shared < 0 || T_cap > mla::kMaxTreeCap || T_cap < (long long)shared + S) return 0;
   size_t tc = 0;
   if (dtype == MLA_BF16 && mla::tc_decode_geometry_ok(g)) tc = round256(mla::tc_shared_workspace_bytes(B, S, T_cap, shared));
   // the CUDA-core path takes over for page sizes and addresses the tensor-core path does not serve
@@ -1069,11 +1070,13 @@ MLA_EXPORT size_t mla_decode_shared_workspace_size(const mla_dims* d, int dtype,
 
 MLA_EXPORT int mla_decode_shared_paged(const mla_dims* d, int dtype, int B, int S, const void* q, const void* Lc_pages,
                                        const void* Rc_pages, int num_pages, int page_size, const int32_t* block_table,
-                                       int max_pages, const int32_t* T, int shared, const void* kv_b, int out_dtype,
-                                       void* out, void* workspace, size_t workspace_bytes, void* stream) {
+                                       int max_pages, const int32_t* T, int shared, const int32_t* parent,
+                                       const void* kv_b, int out_dtype, void* out, void* workspace,
+                                       size_t workspace_bytes, void* stream) {
   mla::DecodeArgs a{};
   int rc = check_common(d, dtype, B, S, &a.g);
   if (rc) return rc;
+  if (S > mla::kMaxTree) return fail(MLA_ERR_UNSUPPORTED, "S=%d: at most %d new tokens", S, mla::kMaxTree);
   rc = check_pages(S, num_pages, page_size, block_table, max_pages, &a.pages);
   if (rc) return rc;
   a.T_cap = max_pages * page_size;
@@ -1096,6 +1099,7 @@ MLA_EXPORT int mla_decode_shared_paged(const mla_dims* d, int dtype, int B, int 
   a.out = out;
   a.out_bf16 = out_dtype == MLA_BF16;
   a.lead = shared;
+  a.parent = parent;
   return run_decode(a, dtype, false, workspace, workspace_bytes, stream, "mla_decode_shared_paged launch", true,
                     /*shared=*/true);
 }

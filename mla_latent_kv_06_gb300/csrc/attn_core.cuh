@@ -85,7 +85,6 @@ struct AttnParams {
   long long wait_ns;
   PageTable pages;  // dense path: key tiles come from pages (page_size a multiple of kTile)
   const int32_t* parent;  // tree attention: [B, S] parent indices
-  int t0, lead;  // dense: the pass starts at key t0 (a multiple of kTile); lengths below S + lead are bad
 };
 
 // One arrival per warp on a barrier initialised with the number of arriving
@@ -143,13 +142,13 @@ __device__ __forceinline__ int chunk_of(long long x, long long N, int G) {
 // Tiles of row `row` that chunk g processes for query position s: [lo, hi).
 template <bool kSparse>
 __device__ __forceinline__ void piece_range(const int32_t* ts, const int32_t* T, int S, int s, int row, int g,
-                                            int G, long long N, int* lo, int* hi, int t0 = 0) {
+                                            int G, long long N, int* lo, int* hi) {
   const long long a = ts[row], e = ts[row + 1];
   const long long c0 = chunk_begin(N, g, G), c1 = chunk_begin(N, g + 1, G);
   long long l = (a > c0 ? a : c0) - a, h = (e < c1 ? e : c1) - a;
   if (!kSparse && h > l) {
     const int pos = T[row] - S + s;
-    const long long vt = (pos - t0 + kTile) / kTile;  // tiles holding keys t0..pos
+    const long long vt = (pos + kTile) / kTile;  // tiles holding keys 0..pos
     if (h > vt) h = vt;
   }
   *lo = (int)l;
@@ -163,7 +162,7 @@ __device__ __forceinline__ bool next_piece(const AttnParams& p, const int32_t* t
   const long long c1 = chunk_begin(N, g + 1, p.G);
   for (; *row < NR; ++*row) {
     if (ts[*row] >= c1) return false;
-    piece_range<kSparse>(ts, p.T, p.S, s, *row, g, p.G, N, lo, hi, p.t0);
+    piece_range<kSparse>(ts, p.T, p.S, s, *row, g, p.G, N, lo, hi);
     if (*lo < *hi) return true;
   }
   return false;
@@ -174,8 +173,8 @@ template <bool kSparse>
 __device__ __forceinline__ int row_tiles(const AttnParams& p, int row) {
   const int b = kSparse ? row / p.S : row;
   const int Tb = p.T[b];
-  if (Tb < p.S + p.lead || Tb > p.T_cap) return 0;
-  int nk = Tb - p.t0;
+  if (Tb < p.S || Tb > p.T_cap) return 0;
+  int nk = Tb;
   if (kSparse) {
     nk = p.nsel[row];
     if (nk < 1 || nk > p.topk) return 0;
@@ -238,7 +237,7 @@ struct TileCursor {
 // tile inside a piece).
 template <bool kSparse>
 __device__ __forceinline__ int tile_keys(const AttnParams& p, int row, int s, int k) {
-  const int nk = kSparse ? p.nsel[row] : p.T[row] - p.S + s + 1 - p.t0;
+  const int nk = kSparse ? p.nsel[row] : p.T[row] - p.S + s + 1;
   const int n = nk - k * kTile;
   return n < kTile ? n : kTile;
 }
@@ -335,7 +334,7 @@ __device__ __forceinline__ void attn_producer(const AttnParams& p, AttnShared& s
     int y = c.row * p.kv_rows + c.k * kTile;  // tile-list row = block of key-source rows
     if (kPaged) {  // the tile's 128 rows lie in one page
       bool bad_page = false;
-      y = (int)cache_row(p.pages, c.row, p.T_cap, p.t0 + c.k * kTile, &bad_page);
+      y = (int)cache_row(p.pages, c.row, p.T_cap, c.k * kTile, &bad_page);
       if (bad_page) raise_flag(p.flags, MLA_DEV_BAD_INDEX);
     }
     const uint32_t par = (it & 1) ^ 1;
@@ -577,7 +576,7 @@ __device__ __forceinline__ void attn_softmax(const AttnParams& p, AttnShared& sh
       const int b = kSparse ? cur.row / S : cur.row;
       const int qs = kSparse ? cur.row % S : s;
       pos = p.T[b] - S + qs;
-      nkeys = kSparse ? p.nsel[cur.row] : pos + 1 - p.t0;
+      nkeys = kSparse ? p.nsel[cur.row] : pos + 1;
       if (kTree) {
         const TreeNode node = tree_node(p.parent + (size_t)cur.row * S, s);
         tmask = node.mask;

@@ -45,10 +45,11 @@
 // probabilities 32).  The row sums add the rounded probabilities, so that both
 // sides of the quotient use the same weights.  Scores, running maximum, sums and context are fp32.
 //
-// kShared: a prefix that all sequences of a batch share.  Every query row sees all of its
-// whole tiles, so there is no tree, tail or mask; the two CTAs of a pair take rows 2i and
-// 2i + 1 of the batch, and the tiles of all pairs form one list that the clusters split
-// evenly.  The tail of the prefix and each sequence's own rows are attn_kernel's.
+// kShared: a batch that shares a prefix.  Every query row sees all of the prefix's whole
+// tiles, so a pair is any two rows of the batch there; behind the prefix it is two nodes of
+// one sequence, as ever (one, with S = 1: half of the pair's M idles, and its tiles still
+// stream at the rate of the memory).  Both kinds of items lie in one tile list that the
+// clusters split evenly, so that the batch takes one launch and one round.
 //
 // Measured: 8 trees of 64 nodes on 16k to 32k keys 1.03 ms, 1.70 PFLOP/s of the
 // formula's (1.80 issued), the sustained rate of the tensor pipe under the
@@ -182,25 +183,23 @@ __device__ __forceinline__ void commit_pair(uint64_t* bar, uint32_t lead) {
       : "memory");
 }
 
-// The pieces of one chunk of the tile list: (sequence, tile range), or with a shared
-// prefix, whose rows are all alike, (pair of rows, tile range).
+// The pieces (item, tile range) of one chunk of the tile list.  Without a shared
+// prefix the items are the sequences, every cluster having its own node pair.
 template <bool kShared>
-struct Pieces {
+struct Pieces;
+
+template <>
+struct Pieces<false> {
   const int32_t* ts;
-  int B, b, lo, hi, tiles;
+  int B, b, lo, hi, pair;
   long long c0, c1;
-  __device__ __forceinline__ long long first(int i) const { return kShared ? (long long)i * tiles : ts[i]; }
-  __device__ __forceinline__ void start(const PairParams& p, int g) {
+  __device__ __forceinline__ void start(const PairParams& p, int g, int node_pair) {
     ts = p.tile_start;
-    B = kShared ? p.NP : p.B;
-    tiles = p.tiles;
-    const long long N = first(B);
+    B = p.B;
+    pair = node_pair;
+    const long long N = ts[B];
     c0 = N * g / p.G;
     c1 = N * (g + 1) / p.G;
-    if (kShared) {
-      b = (int)(c0 / tiles) - 1;
-      return;
-    }
     int l = 0, h = B;  // first sequence whose tiles reach past c0
     while (l < h) {
       const int mid = (l + h) >> 1;
@@ -211,13 +210,60 @@ struct Pieces {
   }
   __device__ __forceinline__ bool next() {
     for (++b; b < B; ++b) {
-      const long long a = first(b), e = first(b + 1);
+      const long long a = ts[b], e = ts[b + 1];
       if (a >= c1) return false;
       lo = (int)((a > c0 ? a : c0) - a);
       hi = (int)((e < c1 ? e : c1) - a);
       if (lo < hi) return true;
     }
     return false;
+  }
+  __device__ __forceinline__ bool prefix() const { return false; }
+  __device__ __forceinline__ long long slot(const PairParams& p, int g, int s, uint32_t) const {
+    return (long long)(g + b) * p.S + s;
+  }
+};
+
+template <>
+struct Pieces<true> {
+  SharedItems items;
+  int item, b, lo, hi, pair;  // a prefix item: b = 0, pair of the batch's rows
+  long long c0, c1;
+  __device__ __forceinline__ void start(const PairParams& p, int g, int) {
+    items = SharedItems{p.B, p.NP, p.shared, p.tiles, p.tile_start};
+    const long long N = items.total();
+    c0 = N * g / p.G;
+    c1 = N * (g + 1) / p.G;
+    if (c0 < items.prefix_units()) {  // the item in which the chunk begins
+      item = (int)(c0 / (kItemCost + items.tiles)) - 1;
+      return;
+    }
+    int l = 0, h = items.B;
+    while (l < h) {
+      const int mid = (l + h) >> 1;
+      if (items.own(mid + 1) > c0) h = mid;
+      else l = mid + 1;
+    }
+    item = items.shared + l * items.NP - 1;
+    if (l < items.B) item += (int)((c0 - items.own(l)) / items.each(l));
+  }
+  __device__ __forceinline__ bool next() {
+    const int n = items.count();
+    for (++item; item < n; ++item) {
+      const SharedItems::Item it = items.item(item);
+      if (it.at >= c1) return false;
+      it.range(c0, c1, &lo, &hi);
+      if (lo < hi) {
+        b = prefix() ? 0 : (item - items.shared) / items.NP;
+        pair = prefix() ? item : (item - items.shared) - b * items.NP;
+        return true;
+      }
+    }
+    return false;
+  }
+  __device__ __forceinline__ bool prefix() const { return item < items.shared; }
+  __device__ __forceinline__ long long slot(const PairParams&, int g, int, uint32_t rank) const {
+    return (long long)(g + item) * 2 + rank;
   }
 };
 
@@ -226,15 +272,25 @@ struct Tile {
   int row0, keys;  // prefix: first key and number of keys (a multiple of 16); tail: staged rows
 };
 
-template <bool kShared>
-__device__ __forceinline__ Tile tile_at(int Tb, int S, int k) {
-  if (kShared) return Tile{false, k * kPairTile, kPairTile};
-  const int b16 = pair_base16(Tb, S);
+// Tile k of a sequence of length Tb whose own tiles start at t0; base16 as by pair_base16.
+__device__ __forceinline__ Tile tile_at(int Tb, int b16, int t0, int k) {
   Tile t;
-  t.row0 = k * kPairTile;
+  t.row0 = t0 + k * kPairTile;
   t.tail = t.row0 >= b16;
   t.keys = t.tail ? Tb - b16 : min(kPairTile, b16 - t.row0);
   return t;
+}
+
+// What a piece's tiles are cut from: the sequence, or the prefix, of which every tile is whole.
+struct Span {
+  int Tb, b16, t0;
+  __device__ __forceinline__ Tile at(int k) const { return tile_at(Tb, b16, t0, k); }
+};
+template <bool kShared>
+__device__ __forceinline__ Span span_of(const PairParams& p, const Pieces<kShared>& pc) {
+  if (kShared && pc.prefix()) return Span{p.t0, p.t0, 0};
+  const int Tb = p.T[pc.b];
+  return Span{Tb, pair_base16(Tb, p.S), kShared ? p.t0 : 0};
 }
 
 // mbar_wait out of line, for the MMA loop: its iterations then hold a test and
@@ -244,10 +300,6 @@ __device__ __noinline__ bool slow_wait(uint64_t* bar, uint32_t parity, volatile 
                                        long long limit_ns) {
   return mbar_wait(bar, parity, abort, flags, limit_ns);
 }
-
-// Bytes of one CTA's query block: with a shared prefix the rotated query is one term.
-template <bool kShared>
-constexpr uint32_t query_bytes() { return kShared ? 9 * kQAtom : kQBytes; }
 
 // ------------------------------------------------------------ TMA producer (warp 0 of each CTA, converged)
 template <bool kShared>
@@ -280,15 +332,14 @@ __device__ __forceinline__ void produce(const PairParams& p, Shared& sh, unsigne
   struct Rows {
     int y[2];
   };
-  auto rows_of = [&](int b, int Tb, int k) -> Rows {
-    const Tile t = tile_at<kShared>(Tb, p.S, k);
-    if (kShared) b = 0;
+  auto rows_of = [&](int b, const Span& sp, int k) -> Rows {
+    const Tile t = sp.at(k);
     if (t.tail) return Rows{{b * kPairStage, b * kPairStage}};
     bool bad = false;
     Rows r;
     r.y[0] = (int)cache_row(p.pages, b, p.T_cap, t.row0, &bad);
     // no key in the second half: its rows are not looked up (any do)
-    r.y[1] = kShared || t.row0 + 128 < Tb ? (int)cache_row(p.pages, b, p.T_cap, t.row0 + 128, &bad) : r.y[0];
+    r.y[1] = t.row0 + 128 < sp.Tb ? (int)cache_row(p.pages, b, p.T_cap, t.row0 + 128, &bad) : r.y[0];
     if (bad) raise_flag(p.flags, MLA_DEV_BAD_INDEX);
     return r;
   };
@@ -317,23 +368,22 @@ __device__ __forceinline__ void produce(const PairParams& p, Shared& sh, unsigne
   };
   Pieces<kShared> pc;
   int np = 0;
-  for (pc.start(p, g); ok && uni(pc.next()); ++np) {
-    const int Tb = kShared ? 0 : p.T[pc.b];
+  for (pc.start(p, g, pair); ok && uni(pc.next()); ++np) {
+    const Span sp = span_of(p, pc);
     ok = wait(&sh.q_empty, (np & 1) ^ 1);
     if (!ok) break;
-    expect_bytes(smem_u32(&sh.q_full), 2 * query_bytes<kShared>(), arm);
+    expect_bytes(smem_u32(&sh.q_full), 2 * kQBytes, arm);
     const uint32_t qbar = in_cta(&sh.q_full, 0);
-    // past the last node: another row or zeros
-    const int qrow = (kShared ? 2 * pc.b + (int)rank : pc.b * p.S + 2 * pair + (int)rank) * kRows;
+    const int qrow = (pc.b * p.S + 2 * pc.pair + (int)rank) * kRows;  // past the last node: another row or zeros
     for (int d = 0; d < 9; ++d) load_2d(smem_u32(smem + d * kQAtom), &p.mQ, 64 * d, qrow, qbar, lead);
-    if (!kShared) load_2d(smem_u32(smem + 9 * kQAtom), &p.mQl, 0, qrow, qbar, lead);
+    load_2d(smem_u32(smem + 9 * kQAtom), &p.mQl, 0, qrow, qbar, lead);
     ++*q_issued;
-    Rows r0 = rows_of(pc.b, Tb, pc.lo), r1 = pc.lo + 1 < pc.hi ? rows_of(pc.b, Tb, pc.lo + 1) : r0;
-    load_k(tile_at<kShared>(Tb, p.S, pc.lo), r0);
+    Rows r0 = rows_of(pc.b, sp, pc.lo), r1 = pc.lo + 1 < pc.hi ? rows_of(pc.b, sp, pc.lo + 1) : r0;
+    load_k(sp.at(pc.lo), r0);
     for (int k = pc.lo; uni(k < pc.hi) && ok; ++k) {
-      const Rows r2 = k + 2 < pc.hi ? rows_of(pc.b, Tb, k + 2) : r1;
-      if (uni(k + 1 < pc.hi)) load_k(tile_at<kShared>(Tb, p.S, k + 1), r1);
-      if (ok) load_v(tile_at<kShared>(Tb, p.S, k), r0);
+      const Rows r2 = k + 2 < pc.hi ? rows_of(pc.b, sp, k + 2) : r1;
+      if (uni(k + 1 < pc.hi)) load_k(sp.at(k + 1), r1);
+      if (ok) load_v(sp.at(k), r0);
       r0 = r1;
       r1 = r2;
     }
@@ -344,7 +394,7 @@ __device__ __forceinline__ void produce(const PairParams& p, Shared& sh, unsigne
 
 // ------------------------------------------------------------ MMA issuer (warp 1 of the leader CTA, converged)
 template <bool kShared>
-__device__ __forceinline__ void issue(const PairParams& p, Shared& sh, unsigned char* smem, uint32_t tmem_any, int g) {
+__device__ __forceinline__ void issue(const PairParams& p, Shared& sh, unsigned char* smem, uint32_t tmem_any, int g, int pair) {
   volatile int* abort = &sh.abort;
   const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_any, 0), lead = elect_lane();
   const uint32_t idS = idesc_bf16_f32(128, 256, 0, 0), idO = idesc_bf16_f32(128, 256, 0, 1);
@@ -385,7 +435,7 @@ __device__ __forceinline__ void issue(const PairParams& p, Shared& sh, unsigned 
       const uint64_t db = dK + (uint64_t)(s * (kStageBytes >> 4)), da = dQ + (uint64_t)(a * (kQAtom >> 4));
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk) mma_pair(d, da + 2 * kk, db + 2 * kk, idS, (a | kk) != 0 ? 1u : 0u, lead);
-      if (!kShared && a == 8) {  // the rotary keys again, with what rounding the rotated query left
+      if (a == 8) {  // the rotary keys again, with what rounding the rotated query left
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) mma_pair(d, da + (kQAtom >> 4) + 2 * kk, db + 2 * kk, idS, 1u, lead);
       }
@@ -395,8 +445,8 @@ __device__ __forceinline__ void issue(const PairParams& p, Shared& sh, unsigned 
   };
   Pieces<kShared> pc;
   int np = 0;
-  for (pc.start(p, g); ok && uni(pc.next()); ++np) {
-    const int Tb = kShared ? 0 : p.T[pc.b];
+  for (pc.start(p, g, pair); ok && uni(pc.next()); ++np) {
+    const Span sp = span_of(p, pc);
     ok = wait(&sh.q_full, np & 1);
     if (!ok) break;
     tc_fence_after();
@@ -410,9 +460,9 @@ __device__ __forceinline__ void issue(const PairParams& p, Shared& sh, unsigned 
       ok = ok && wait(&sh.p_full, it & 1);
       if (!ok) break;
       tc_fence_after();
-      const Tile t = tile_at<kShared>(Tb, p.S, k);
+      const Tile t = sp.at(k);
       const uint32_t keep = uni(k > pc.lo) ? 1u : 0u;
-      if (kShared || uni(t.keys == kPairTile)) {
+      if (uni(t.keys == kPairTile)) {
 #pragma unroll 1
         for (int kc = 0; kc < 4; ++kc) {
 #pragma unroll
@@ -480,20 +530,24 @@ __device__ __forceinline__ void soften(const PairParams& p, Shared& sh, unsigned
   const float c = p.c;
   int it = 0;
   Pieces<kShared> pc;
-  for (pc.start(p, g); pc.next();) {
-    const int b = pc.b, Tb = kShared ? 0 : p.T[b], b16 = kShared ? 0 : pair_base16(Tb, p.S);
-    const int s = 2 * (kShared ? b : pair) + (int)rank, rows = kShared ? p.R : p.S;
+  for (pc.start(p, g, pair); pc.next();) {
+    const int b = pc.b, s = 2 * pc.pair + (int)rank;
+    const Span sp = span_of(p, pc);
+    const bool prefix = kShared && pc.prefix();
+    const int rows = prefix ? p.B * p.S : p.S;  // s is a row of the batch, or of its sequence
     unsigned long long mask = 0;
-    if (!kShared && s < p.S) {
-      const TreeNode node = tree_node(p.parent + (size_t)b * p.S, s);
+    if (prefix) {
+      mask = 1;  // (no tile of the prefix is masked)
+    } else if (s < p.S) {
+      const TreeNode node = node_at(p.parent, b, p.S, s);
       mask = node.mask;
       if (node.state == kNodeBad && tsm == 0) raise_flag(p.flags, MLA_DEV_BAD_INDEX);
     }
-    const int rem = Tb - p.S - b16;  // prefix rows at the start of the tail
+    const int rem = sp.Tb - p.S - sp.b16;  // prefix rows at the start of the tail
     float lsum = 0.f;
     for (int k = pc.lo; k < pc.hi; ++k, ++it) {
       const bool first = k == pc.lo;
-      const Tile t = tile_at<kShared>(Tb, p.S, k);
+      const Tile t = sp.at(k);
       bool fail = !mbar_wait(&sh.s_full[it & 1], (it >> 1) & 1, abort, p.flags, p.wait_ns);
       if (bar_red_or(1, kSoft, fail)) return;
       tc_fence_after();
@@ -503,7 +557,7 @@ __device__ __forceinline__ void soften(const PairParams& p, Shared& sh, unsigned
       // issuing warp's, whose fetches otherwise stall the tensor pipe.
       const uint32_t sc = t_lane + kColS + 128 * (it & 1) + 64 * ch;
       unsigned long long vis = ~0ull;  // bit i: key key0 + i is visible
-      const bool masked = kShared ? false : t.tail || t.keys < kPairTile || mask == 0;
+      const bool masked = t.tail || t.keys < kPairTile || mask == 0;
       if (masked) {
         vis = low_bits(t.keys - key0);
         if (t.tail) {  // the prefix remainder, then the tree's rows through the node's mask
@@ -527,7 +581,7 @@ __device__ __forceinline__ void soften(const PairParams& p, Shared& sh, unsigned
           }
         } else {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) least = kShared ? least : fminf(least, v[i]);
+          for (int i = 0; i < 16; ++i) least = fminf(least, v[i]);
 #pragma unroll
           for (int i = 0; i < 16; ++i) mx = fmaxf(mx, v[i]);
         }
@@ -617,7 +671,7 @@ __device__ __forceinline__ void soften(const PairParams& p, Shared& sh, unsigned
     tc_fence_after();
     sh.red[2 * (q >> 1) + ch][row] = lsum;
     named_barrier(1, kSoft);
-    const size_t slot = kShared ? (size_t)(g + b) * 2 + rank : (size_t)(g + b) * p.S + s;
+    const size_t slot = (size_t)pc.slot(p, g, s, rank);
     if (s < rows) {
       if (tsm < kRows) {
         float* ml = p.ml_part + (slot * kRows + tsm) * 2;
@@ -689,7 +743,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_pa
   if (warp == 0) {
     produce<kShared>(p, sh, smem, rank, g, pair, &issued, &q_issued);
   } else if (warp == 1) {
-    if (rank == 0) issue<kShared>(p, sh, smem, tmem, g);
+    if (rank == 0) issue<kShared>(p, sh, smem, tmem, g, pair);
     // both CTAs: every MMA and every arrival of its commits has happened
     volatile int no_abort = 0;
     mbar_wait(&sh.mma_done, 0, &no_abort, p.flags, p.wait_ns > kDrainNs ? p.wait_ns : kDrainNs);
@@ -726,7 +780,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_pa
     }
     const int qo = sh.q_issued[0], qp = sh.q_issued[1], qt = max(qo, qp);
     if (qt > 0) {
-      settle(&sh.q_full, qt - 1, qo, qp, query_bytes<kShared>());
+      settle(&sh.q_full, qt - 1, qo, qp, kQBytes);
       mbar_wait(&sh.q_full, (qt - 1) & 1, &no_abort, p.flags, drain);
     }
   }
@@ -788,6 +842,6 @@ cudaError_t launch(const PairParams& p, int clusters, cudaStream_t st) {
 
 cudaError_t launch_attn_pair(const PairParams& p, cudaStream_t st) { return launch<false>(p, p.G * p.NP, st); }
 
-cudaError_t launch_attn_prefix(const PairParams& p, cudaStream_t st) { return launch<true>(p, p.G, st); }
+cudaError_t launch_attn_shared(const PairParams& p, cudaStream_t st) { return launch<true>(p, p.G, st); }
 
 }  // namespace mla

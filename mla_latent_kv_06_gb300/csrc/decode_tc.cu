@@ -827,7 +827,7 @@ struct AbsorbParams {
   uint64_t turn[kDr / 2];  // rope_turns(rope_base^(-2j/qk_rope)), from the host
   unsigned int* flags;
   PageTable pages;
-  const int32_t* parent;  // tree attention: [B, S] parent indices
+  const int32_t* parent;  // tree attention: [B, S] parent indices (null: chains)
   int t0, lead;           // shared prefix: the plan's tiles start at key t0; lengths below S + lead are bad
   int rope_x;             // tree: blocks along x that work on the head; any more stage the tails
   __nv_bfloat16* tail;    // pair attention: staged tail rows [B, kPairStage, 576], else null
@@ -839,7 +839,7 @@ struct AbsorbParams {
 template <bool kTree>
 __device__ __forceinline__ int query_pos(const AbsorbParams& p, int b, int s, int Tb) {
   if (Tb < p.S || Tb > p.T_cap) return 0;
-  return Tb - p.S + (kTree ? tree_node(p.parent + (size_t)b * p.S, s).depth : s);
+  return Tb - p.S + (kTree ? node_at(p.parent, b, p.S, s).depth : s);
 }
 
 // Element j of the rotated query of head row rh (row * 64 + head).  The pair
@@ -881,7 +881,7 @@ __device__ __forceinline__ void rope_rows(const AbsorbParams& p, int h, int tid,
       const int lane = threadIdx.x & 31, e = e0 - lane + lane * nthr;
       if (lane < 8 && e < n) {
         const int r = e / (kDr / 2);
-        depth = tree_node(p.parent + (size_t)(r / p.S) * p.S, r % p.S).depth;
+        depth = node_at(p.parent, r / p.S, p.S, r % p.S).depth;
       }
     }
 #pragma unroll
@@ -911,14 +911,16 @@ __device__ __forceinline__ void rope_rows(const AbsorbParams& p, int h, int tid,
 }
 
 // Tail rows of the pair attention: rows base16 .. T - 1 of every sequence, zeros
-// after them up to 80.  A row that holds a value that is not finite becomes zero
+// after them up to a whole 16-key step (the value product reads no further, and the
+// scores of rows past T are masked).  A row that holds a value that is not finite becomes zero
 // latents with a NaN rotary part (see attn_tree.cu).  One warp per row.
 __device__ __forceinline__ void stage_tail(const AbsorbParams& p, int warp0, int nwarps) {
   const int lane = threadIdx.x & 31;
   for (int e = warp0; e < p.B * 80; e += nwarps) {
     const int b = e / 80, i = e % 80, Tb = p.T[b];
-    if (Tb < p.S || Tb > p.T_cap) continue;
+    if (Tb < p.S + p.lead || Tb > p.T_cap) continue;
     const int t = pair_base16(Tb, p.S) + i;
+    if (t >= ((Tb + 15) & ~15)) continue;
     uint4 v[3];
 #pragma unroll
     for (int u = 0; u < 3; ++u) v[u] = make_uint4(0, 0, 0, 0);
@@ -1062,14 +1064,14 @@ __global__ void __launch_bounds__(kAbsThreads, 2) absorb_kernel(const AbsorbPara
         const int b = p.sparse ? r / p.S : r;
         const int Tb = p.T[b];
         int bad = (Tb < p.S + p.lead || Tb > p.T_cap) ? MLA_DEV_BAD_LENGTH : 0;
-        int nk = Tb - p.t0;
+        int nk = Tb;
         if (!bad && p.sparse) {
           nk = p.nsel[r];
           if (nk < 1 || nk > p.topk) bad = MLA_DEV_BAD_INDEX;
         }
         if (bad) raise_flag(p.flags, bad);
         p.bad[r] = bad;
-        tiles = bad ? 0 : (kTree && p.tail) ? pair_tiles(nk, p.S) : (nk + kTile - 1) / kTile;
+        tiles = bad ? 0 : (kTree && p.tail) ? pair_tiles(nk, p.S, p.t0) : (nk + kTile - 1) / kTile;
       }
       // block inclusive scan of `tiles`
       int x = tiles;
@@ -1138,14 +1140,18 @@ struct CombineParams {
   void* out;  // [R, 64, Dv] float or bf16, R <= kCmbRows
   int B, S, G, Dn, Dv, sparse, T_cap, topk;
   unsigned int* flags;
-  int out_bf16;           // tree attention only, like the next two
+  int out_bf16;           // tree attention and shared prefixes only, like the next ones
   int pair;               // partials of the pair attention
-  const int32_t* parent;  // tree attention: [B, S] parent indices
+  const int32_t* parent;  // [B, S] parent indices (null: chains)
+  int t0, lead;           // shared prefix
+  SharedItems items;      // its list (the tile starts are the kernel's own)
 };
 
+enum CombineKind { kCmbPlain = 0, kCmbTree = 1, kCmbShared = 2 };
 
-template <bool kTree>
+template <int kKind>
 __global__ void __launch_bounds__(kCmbThreads) combine_kernel(const CombineParams p) {
+  constexpr bool kTree = kKind != kCmbPlain;  // rows are nodes
   extern __shared__ __align__(128) unsigned char sm[];
   const __nv_bfloat16* Ws = reinterpret_cast<const __nv_bfloat16*>(sm);   // [64][512]
   float* clat = reinterpret_cast<float*>(sm + kCmbWBytes);                 // [kCmbRows][kCPitch]
@@ -1178,13 +1184,14 @@ __global__ void __launch_bounds__(kCmbThreads) combine_kernel(const CombineParam
   if (tid < NR) {
     const int b = p.sparse ? tid / p.S : tid;
     const int Tb = p.T[b];
-    int bad = (Tb < p.S || Tb > p.T_cap) ? 1 : 0, nk = Tb;
+    int bad = (Tb < p.S + (kKind == kCmbShared ? p.lead : 0) || Tb > p.T_cap) ? 1 : 0, nk = Tb;
     if (!bad && p.sparse) {
       nk = p.nsel[tid];
       bad = (nk < 1 || nk > p.topk) ? 1 : 0;
     }
     cbad[tid] = bad;
-    cts[tid + 1] = bad ? 0 : (kTree && p.pair) ? pair_tiles(nk, p.S) : (nk + kTile - 1) / kTile;
+    cts[tid + 1] = bad ? 0 : kKind == kCmbShared ? pair_tiles(nk, p.S, p.t0)
+                   : (kTree && p.pair) ? pair_tiles(nk, p.S) : (nk + kTile - 1) / kTile;
   }
   __syncthreads();
   if (tid == 0) {
@@ -1200,10 +1207,22 @@ __global__ void __launch_bounds__(kCmbThreads) combine_kernel(const CombineParam
     const int r = warp, b = r / p.S, s = r % p.S;
     const int row = p.sparse ? r : b;
     const int sr = kTree ? p.S - 1 : s;
-    const int state = kTree ? tree_node(p.parent + (size_t)b * p.S, s).state : kNodePresent;
+    const int state = kTree ? node_at(p.parent, b, p.S, s).state : kNodePresent;
     int cnt = 0;
     // an absent tree node has no splits: zero times a context of NaN rows would not be zero
-    if (!cbad[row] && N > 0 && state != kNodeAbsent) {
+    if (kKind == kCmbShared && !cbad[row] && state != kNodeAbsent) {
+      SharedItems items = p.items;
+      items.ts = cts;
+      const long long units = items.total();
+      SharedSplits sp;
+      sp.start(items, units, p.G, r, b, s);
+      for (int i0 = 0; i0 < sp.n; i0 += 32) {
+        const long long slot = sp.slot(i0 + lane, units, p.G);
+        const unsigned m = __ballot_sync(0xffffffffu, slot >= 0);
+        if (slot >= 0) pslot[warp * kMaxPieces + cnt + __popc(m & ((1u << lane) - 1))] = (int)slot;
+        cnt += __popc(m);
+      }
+    } else if (!cbad[row] && N > 0 && state != kNodeAbsent) {
       const long long a = cts[row], e = cts[row + 1];
       const int glo = chunk_of(a, N, p.G), ghi = chunk_of(e - 1, N, p.G);
       for (int g0 = glo; g0 <= ghi; g0 += 32) {
@@ -1638,21 +1657,19 @@ __global__ void __launch_bounds__(256) merge_pair_kernel(const PairMergeParams p
 }
 
 // ===========================================================================
-// Merge of a shared-prefix call: the partials of a row are those of its pair in
-// the prefix pass and those of its sequence's own keys.  Otherwise as
-// merge_pair_kernel.
+// Merge of a shared-prefix call: the partials of a row are those of its two items
+// in the tile list, its pair of the batch's rows on the prefix and its pair of
+// nodes on the sequence's own keys.  Otherwise as merge_pair_kernel.
 // ===========================================================================
 struct SharedMergeParams {
-  const float* o_part;   // the prefix's slots, then the own keys' from slot `own` on
+  const float* o_part;
   const float* ml_part;
-  const int32_t* tile_start;  // of the own keys
-  const int32_t* T;
   const int32_t* bad;
-  __nv_bfloat16* clat;  // [R, 64, 1024]
-  float* inv_l;         // [R, 64]
-  int B, S, G, t0;      // own keys: chunks, first key
-  int NP, tiles, Gp;    // prefix: pairs of rows, tiles, chunks
-  int own;
+  const int32_t* parent;  // or null: chains
+  __nv_bfloat16* clat;    // [R, 64, 1024]
+  float* inv_l;           // [R, 64]
+  int S, G;
+  SharedItems items;
 };
 
 template <int kParts>
@@ -1665,30 +1682,21 @@ __global__ void __launch_bounds__(256) merge_shared_kernel(const SharedMergePara
   const int part = (int)(gw % kParts);
   const long long rh = gw / kParts;
   const int r = (int)(rh / kH), h = (int)(rh % kH);
-  if (r >= p.B * p.S) return;
+  if (r >= p.items.B * p.S) return;
   const int b = r / p.S, s = r % p.S;
   __nv_bfloat16* dst = p.clat + ((size_t)r * kH + h) * (2 * kDl) + 128 * part + 4 * lane;
-  const bool broken = p.bad[b] != 0;
+  const int state = node_at(p.parent, b, p.S, s).state;
+  const bool broken = p.bad[b] || state == kNodeBad;
   float inv = broken ? qnan() : 1.f;
   float4 acc[kVec];
 #pragma unroll
   for (int v = 0; v < kVec; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (!broken) {
-    const int pair = r >> 1;
-    const long long Np = (long long)p.NP * p.tiles, a = (long long)pair * p.tiles;
-    const int plo = p.tiles ? chunk_of(a, Np, p.Gp) : 0, n0 = p.tiles ? chunk_of(a + p.tiles - 1, Np, p.Gp) - plo + 1 : 0;
-    const long long N = p.tile_start[p.B];
-    const int glo = chunk_of(p.tile_start[b], N, p.G), n = n0 + chunk_of(p.tile_start[b + 1] - 1, N, p.G) - glo + 1;
-    // the row's i-th split: every chunk of the prefix holds tiles of the pair, one of the own
-    // keys may have none that the row sees
-    auto slot_of = [&](int i) -> long long {
-      if (i < n0) return (long long)(plo + i + pair) * 2 + (r & 1);
-      if (i >= n) return -1;
-      int lo, hi;
-      const int g = glo + i - n0;
-      piece_range<false>(p.tile_start, p.T, p.S, s, b, g, p.G, N, &lo, &hi, p.t0);
-      return lo < hi ? p.own + (long long)(g + b) * p.S + s : -1;
-    };
+  if (!broken && state == kNodePresent) {
+    const long long N = p.items.total();
+    SharedSplits sp;
+    sp.start(p.items, N, p.G, r, b, s);
+    const int n = sp.n;
+    auto slot_of = [&](int i) { return sp.slot(i, N, p.G); };
     float M = -INFINITY, L = 0.f;
     for (int i0 = 0; i0 < n; i0 += 32) {
       const long long slot = slot_of(i0 + lane);
@@ -1828,8 +1836,7 @@ __global__ void __launch_bounds__(256) gather_kernel(const GatherParams p) {
 struct Plan {
   int G, NR, P, R, Kpad;
   int Gp;  // pair attention of a tree, or of a shared prefix: its chunks
-  int NP, tiles, t0;  // shared prefix: pairs of rows, whole tiles, first key after them
-  int own;            // slots of the prefix's partials, before the own keys'
+  int shared, tiles;  // shared prefix: pairs of the batch's rows, whole tiles
   size_t off_q, off_ts, off_bad, off_o, off_ml, off_stage, off_clat, off_invl, off_q8, off_fh, off_tail, off_qlow, total;
 };
 
@@ -1859,7 +1866,7 @@ cudaError_t set_smem_once(Kern kern, int bytes, std::atomic<unsigned long long>*
   return e;
 }
 
-std::atomic<unsigned long long> g_abs_attr[18] = {}, g_attn_attr[14] = {}, g_cmb_attr[2] = {};
+std::atomic<unsigned long long> g_abs_attr[18] = {}, g_attn_attr[14] = {}, g_cmb_attr[3] = {};
 
 // Whether a tree call takes the CTA-pair attention.  Up to 8 query rows can also
 // take one CTA per node, as plain decode does: it starts sooner, but every node
@@ -1886,14 +1893,7 @@ Plan make_plan(int B, int S, int T_cap, int sparse_topk, bool tree = false, int 
   pl.R = B * S;
   if (!sparse_topk) {
     pl.NR = B;
-    if (lead >= 0) {
-      pl.NP = (pl.R + 1) / 2;
-      pl.tiles = lead / kPairTile;
-      pl.t0 = pl.tiles * kPairTile;
-      pl.Gp = prefix_chunks(pl.NP, pl.tiles, sms);
-      pl.own = pl.tiles ? 2 * (pl.Gp + pl.NP - 1) : 0;
-    }
-    const long long tiles = (long long)B * ((T_cap - pl.t0 + kTile - 1) / kTile);
+    const long long tiles = (long long)B * ((T_cap + kTile - 1) / kTile);
     long long G = sms / S;
     if (G < 1) G = 1;
     if (G > tiles) G = tiles;
@@ -1909,9 +1909,13 @@ Plan make_plan(int B, int S, int T_cap, int sparse_topk, bool tree = false, int 
     pl.G = (int)G;
     pl.P = pl.G + pl.R - 1;
   }
-  const bool pair = tree && pair_pays(B, S, T_cap);
-  const bool lift = pl.R > kSmallRows || lead >= 0;  // by GEMM
-  if (pair) {
+  const bool shared = lead >= 0, pair = shared || (tree && pair_pays(B, S, T_cap));
+  if (shared) {
+    pl.tiles = lead / kPairTile;
+    pl.shared = pl.tiles ? (pl.R + 1) / 2 : 0;
+    pl.Gp = std::max(sms / 2, 1);
+    pl.P = 2 * (pl.Gp + pl.shared + B * ((S + 1) / 2) - 1);
+  } else if (pair) {
     static_assert(kPairChunks <= kMaxPieces, "the combine lists up to kMaxPieces splits of a row");
     pl.Gp = pair_chunks(B, S, T_cap, sms);
     pl.P = std::max(pl.P, (pl.Gp + B - 1) * S);
@@ -1924,21 +1928,21 @@ Plan make_plan(int B, int S, int T_cap, int sparse_topk, bool tree = false, int 
   pl.off_bad = off;
   off = align256(off + (size_t)pl.NR * 4);
   pl.off_o = off;
-  off = align256(off + (size_t)(pl.own + pl.P) * kH * kDl * 4);
+  off = align256(off + (size_t)pl.P * kH * kDl * 4);
   pl.off_ml = off;
-  off = align256(off + (size_t)(pl.own + pl.P) * kH * 2 * 4);
+  off = align256(off + (size_t)pl.P * kH * 2 * 4);
   pl.Kpad = sparse_topk ? (sparse_topk + kTile - 1) / kTile * kTile : 0;
   pl.off_stage = off;  // two staging buffers: consecutive layers of one call alternate
   off = align256(off + 2 * (size_t)pl.R * pl.Kpad * kDc * 2);
   pl.off_clat = off;
-  off = align256(off + (lift ? (size_t)pl.R * kH * kDl * (pair || lead >= 0 ? 4 : 2) : 0));
+  off = align256(off + (pl.R > kSmallRows ? (size_t)pl.R * kH * kDl * (pair ? 4 : 2) : 0));
   pl.off_invl = off;
-  off = align256(off + (lift ? (size_t)pl.R * kH * 4 : 0));
+  off = align256(off + (pl.R > kSmallRows ? (size_t)pl.R * kH * 4 : 0));
   // FP8 cache (dense only): quantised query rows and their score factors
   pl.off_q8 = off;
-  off = align256(off + (sparse_topk || tree || lead >= 0 ? 0 : (size_t)pl.R * kH * kQ8Row));
+  off = align256(off + (sparse_topk || tree || shared ? 0 : (size_t)pl.R * kH * kQ8Row));
   pl.off_fh = off;
-  off = align256(off + (sparse_topk || tree || lead >= 0 ? 0 : (size_t)pl.R * kH * 4));
+  off = align256(off + (sparse_topk || tree || shared ? 0 : (size_t)pl.R * kH * 4));
   pl.off_tail = off;
   off = align256(off + (pair ? (size_t)B * kPairStage * kDc * 2 : 0));
   pl.off_qlow = off;
@@ -1948,7 +1952,11 @@ Plan make_plan(int B, int S, int T_cap, int sparse_topk, bool tree = false, int 
 }
 
 // Many rows: merge of the splits, then the W_UV lift as a GEMM.
-// two: the merged context is two bf16 terms (the pair attention's partials, those of a shared prefix).
+// The items of a shared-prefix call's tile list.
+SharedItems shared_items(const DecodeArgs& a, const Plan& pl, const unsigned char* w) {
+  return SharedItems{a.B, (a.S + 1) / 2, pl.shared, pl.tiles, reinterpret_cast<const int32_t*>(w + pl.off_ts)};
+}
+
 cudaError_t run_lift(const DecodeArgs& a, const Plan& pl, unsigned char* w, bool sparse, bool pair, bool shared,
                      cudaStream_t st) {
   const Geometry& g = a.g;
@@ -1958,12 +1966,10 @@ cudaError_t run_lift(const DecodeArgs& a, const Plan& pl, unsigned char* w, bool
   const float* ml_part = reinterpret_cast<const float*>(w + pl.off_ml);
   const int32_t* ts = reinterpret_cast<const int32_t*>(w + pl.off_ts);
   const int32_t* bad = reinterpret_cast<const int32_t*>(w + pl.off_bad);
-  const bool two = pair || shared;
   kernel_mark(st, "merge");
   cudaError_t e;
   if (shared) {
-    const SharedMergeParams mp{o_part, ml_part, ts,    a.T,  bad,   clat,     inv_l, a.B,
-                               a.S,    pl.G,    pl.t0, pl.NP, pl.tiles, pl.Gp, pl.own};
+    const SharedMergeParams mp{o_part, ml_part, bad, a.parent, clat, inv_l, a.S, pl.Gp, shared_items(a, pl, w)};
     const bool few = pl.R <= 32;
     const long long warps = (long long)pl.R * kH * (few ? 4 : 1);
     e = launch_pdl(few ? merge_shared_kernel<4> : merge_shared_kernel<1>, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, st,
@@ -1992,7 +1998,7 @@ cudaError_t run_lift(const DecodeArgs& a, const Plan& pl, unsigned char* w, bool
   if (e != cudaSuccess) return e;
   GemmArgs gu{};
   gu.a_base = clat;
-  gu.a_ld_z = two ? 2 * kDl : kDl;
+  gu.a_ld_z = pair ? 2 * kDl : kDl;
   gu.a_ld_m = kH * gu.a_ld_z;
   gu.b_base = a.kv_b;
   gu.b_rows = (long long)kH * (g.Dn + g.Dv);
@@ -2009,8 +2015,8 @@ cudaError_t run_lift(const DecodeArgs& a, const Plan& pl, unsigned char* w, bool
   gu.scale = inv_l;
   gu.M = pl.R;
   gu.N = g.Dv;
-  gu.K = two ? 2 * kDl : kDl;
-  gu.b_k_wrap = two ? kDl : 0;
+  gu.K = pair ? 2 * kDl : kDl;
+  gu.b_k_wrap = pair ? kDl : 0;
   gu.Z = kH;
   gu.flags = a.flags;
   gu.wait_ns = a.wait_limit_ns;
@@ -2018,7 +2024,8 @@ cudaError_t run_lift(const DecodeArgs& a, const Plan& pl, unsigned char* w, bool
   return launch_gemm_tc(gu, true, st);
 }
 
-cudaError_t run_pair(const DecodeArgs& a, const Plan& pl, unsigned char* w, long long pool_rows, cudaStream_t st) {
+cudaError_t run_pair(const DecodeArgs& a, const Plan& pl, unsigned char* w, long long pool_rows, bool shared,
+                     cudaStream_t st) {
   PairParams p{};
   const void* qcat = w + pl.off_q;
   const void* tail = w + pl.off_tail;
@@ -2042,6 +2049,9 @@ cudaError_t run_pair(const DecodeArgs& a, const Plan& pl, unsigned char* w, long
   p.T_cap = a.T_cap;
   p.G = pl.Gp;
   p.NP = (a.S + 1) / 2;
+  p.shared = pl.shared;
+  p.tiles = pl.tiles;
+  p.t0 = pl.tiles * kPairTile;
   p.c = a.g.scale * kLog2e;
   p.o_part = reinterpret_cast<float*>(w + pl.off_o);
   p.ml_part = reinterpret_cast<float*>(w + pl.off_ml);
@@ -2049,35 +2059,7 @@ cudaError_t run_pair(const DecodeArgs& a, const Plan& pl, unsigned char* w, long
   p.wait_ns = a.wait_limit_ns;
   p.pages = a.pages;
   kernel_mark(st, "attention");
-  return launch_attn_pair(p, st);
-}
-
-// All query rows over the whole tiles of the prefix, read through sequence 0's pages.
-cudaError_t run_prefix(const DecodeArgs& a, const Plan& pl, unsigned char* w, long long pool_rows, cudaStream_t st) {
-  PairParams p{};
-  const uint64_t rows = (uint64_t)pool_rows;
-  if (!make_tmap_2d_bf16(&p.mQ, w + pl.off_q, (uint64_t)pl.R * kH, kDc, kDc, kH, 64) ||
-      !make_tmap_2d_bf16(&p.mK, a.Lc, rows, kDl, kDl, 128, 64) ||
-      !make_tmap_2d_bf16(&p.mKr, a.Rc, rows, kDr, kDr, 128, 64))
-    return cudaErrorInvalidValue;
-  const uint64_t vd[3] = {64, rows, kDl / 64}, vs[2] = {kDl * 2, 128};
-  const uint32_t box[3] = {64, 64, 2};
-  if (!make_tmap_3d_bf16(&p.mV, a.Lc, vd, vs, box)) return cudaErrorInvalidValue;
-  p.B = a.B;
-  p.S = a.S;
-  p.T_cap = a.T_cap;
-  p.G = pl.Gp;
-  p.NP = pl.NP;
-  p.R = pl.R;
-  p.tiles = pl.tiles;
-  p.c = a.g.scale * kLog2e;
-  p.o_part = reinterpret_cast<float*>(w + pl.off_o);
-  p.ml_part = reinterpret_cast<float*>(w + pl.off_ml);
-  p.flags = a.flags;
-  p.wait_ns = a.wait_limit_ns;
-  p.pages = a.pages;
-  kernel_mark(st, "prefix");
-  return launch_attn_prefix(p, st);
+  return shared ? launch_attn_shared(p, st) : launch_attn_pair(p, st);
 }
 
 cudaError_t run(const DecodeArgs& a, void* ws, bool sparse, cudaStream_t st, bool shared = false) {
@@ -2142,9 +2124,10 @@ cudaError_t run(const DecodeArgs& a, void* ws, bool sparse, cudaStream_t st, boo
   ap.Dv = g.Dv;
   ap.topk = a.topk;
   ap.sparse = sparse ? 1 : 0;
-  ap.t0 = pl.t0;
+  ap.t0 = pl.tiles * kPairTile;
   ap.lead = a.lead;
-  const bool pair = a.parent && pair_pays(B, S, a.T_cap);
+  const bool tree = shared || a.parent;  // the kernels that look at nodes (chains without parents)
+  const bool pair = shared || (a.parent && pair_pays(B, S, a.T_cap));
   const bool big = pl.R > kSmallRows;
   ap.Lc = static_cast<const unsigned char*>(a.Lc);
   ap.Rc = static_cast<const __nv_bfloat16*>(a.Rc);
@@ -2175,20 +2158,22 @@ cudaError_t run(const DecodeArgs& a, void* ws, bool sparse, cudaStream_t st, boo
       {absorb_kernel<4, true, true, true>, absorb_kernel<8, true, true, true>, absorb_kernel<12, true, true, true>,
        absorb_kernel<16, true, true, true>}};
   const bool paged_abs = ap.prefetch && ap.pages.table;
-  const int abs_kind = (a.parent ? 2 : 0) + (paged_abs ? 1 : 0);
-  const AbsKern akern = big ? (a.parent ? absorb_kernel<4, false, false, true> : absorb_kernel<4, false>)
+  const int abs_kind = (tree ? 2 : 0) + (paged_abs ? 1 : 0);
+  const AbsKern akern = big ? (tree ? absorb_kernel<4, false, false, true> : absorb_kernel<4, false>)
                             : abs_kerns[abs_kind][g.Dn / 64 - 1];
   // many rows: the rotary part of each head spread over up to four CTAs
-  const int abs_gx = big ? std::min(a.parent ? 16 : 4, (pl.R * (kDr / 2) + 2047) / 2048) : kDl / kAbsCols;
+  const int abs_gx = big ? std::min(tree ? 16 : 4, (pl.R * (kDr / 2) + 2047) / 2048) : kDl / kAbsCols;
   ap.rope_x = abs_gx;
   if (pair) {
     ap.tail = reinterpret_cast<__nv_bfloat16*>(w + pl.off_tail);
     ap.qlow = reinterpret_cast<__nv_bfloat16*>(w + pl.off_qlow);
   }
-  e = set_smem_once(akern, (int)abs_smem, &g_abs_attr[big ? (a.parent ? 17 : 16) : 4 * abs_kind + g.Dn / 64 - 1]);
+  e = set_smem_once(akern, (int)abs_smem, &g_abs_attr[big ? (tree ? 17 : 16) : 4 * abs_kind + g.Dn / 64 - 1]);
   if (e != cudaSuccess) return e;
   kernel_mark(st, big ? "plan_rope" : "absorb");
-  e = launch_pdl(akern, dim3(abs_gx + (pair ? 1 : 0), kH), dim3(kAbsThreads), abs_smem, st, ap);
+  // a warp per staged row up to 8 blocks along x (32 sequences: plan_rope 12.5 us with one)
+  const int stage_gx = !pair ? 0 : std::min(8, (B * 80 + kH * (kAbsThreads / 32) - 1) / (kH * (kAbsThreads / 32)));
+  e = launch_pdl(akern, dim3(abs_gx + stage_gx, kH), dim3(kAbsThreads), abs_smem, st, ap);
   if (e != cudaSuccess) return e;
   if (big) {  // qabs for many rows: per-head GEMM [R x qk_nope] x W_UK[h] on the tensor cores
     GemmArgs ga{};
@@ -2235,12 +2220,8 @@ cudaError_t run(const DecodeArgs& a, void* ws, bool sparse, cudaStream_t st, boo
   }
 
   // 2. attention
-  if (shared && pl.tiles > 0) {
-    e = run_prefix(a, pl, w, pool_rows, st);
-    if (e != cudaSuccess) return e;
-  }
   if (pair) {
-    e = run_pair(a, pl, w, pool_rows, st);
+    e = run_pair(a, pl, w, pool_rows, shared, st);
     if (e != cudaSuccess) return e;
   } else {
     AttnParams tp{};
@@ -2280,17 +2261,15 @@ cudaError_t run(const DecodeArgs& a, void* ws, bool sparse, cudaStream_t st, boo
     tp.lat_scale = a.lat_fp8 ? a.lat_scale : 1.f;
     tp.fh = fh;
     tp.qcat = qcat;
-    tp.o_part = o_part + (size_t)pl.own * kH * kDl;
-    tp.ml_part = ml_part + (size_t)pl.own * kH * 2;
-    tp.t0 = pl.t0;
-    tp.lead = a.lead;
+    tp.o_part = o_part;
+    tp.ml_part = ml_part;
     tp.flags = a.flags;
     tp.wait_ns = a.wait_limit_ns;
     tp.pages = sparse ? PageTable{} : a.pages;
     tp.parent = a.parent;
     // Streaming launches (one CTA per piece, at least two tiles a CTA by the
     // T_cap bound) take the instantiation with the single-lane score loop.
-    const long long tiles_cap = (long long)B * ((a.T_cap - pl.t0 + kTile - 1) / kTile);
+    const long long tiles_cap = (long long)B * ((a.T_cap + kTile - 1) / kTile);
     const bool stream = !sparse && tp.qsplit == 1 && tiles_cap >= 2LL * pl.G;
     auto kern = sparse     ? attn_kernel<true>
                 : a.parent ? (paged ? (stream ? attn_kernel<false, true, true, true> : attn_kernel<false, true, false, true>)
@@ -2312,7 +2291,7 @@ cudaError_t run(const DecodeArgs& a, void* ws, bool sparse, cudaStream_t st, boo
   }
 
   // 3. merge of the splits and the W_UV lift
-  if (big || shared) return run_lift(a, pl, w, sparse, pair, shared, st);
+  if (big) return run_lift(a, pl, w, sparse, pair, shared, st);
   CombineParams cp{};
   cp.kv_b = static_cast<const __nv_bfloat16*>(a.kv_b);
   cp.o_part = o_part;
@@ -2331,11 +2310,17 @@ cudaError_t run(const DecodeArgs& a, void* ws, bool sparse, cudaStream_t st, boo
   cp.parent = a.parent;
   cp.out_bf16 = a.out_bf16;
   cp.pair = pair ? 1 : 0;
+  cp.t0 = pl.tiles * kPairTile;
+  cp.lead = a.lead;
+  if (shared) cp.items = shared_items(a, pl, w);
   cp.flags = a.flags;
   const size_t cmb_smem = (size_t)kCmbWBytes + (size_t)kCmbRows * kCPitch * 4 + kCmbRows * 8 +
                           (size_t)kCmbRows * kMaxPieces * 12 + (size_t)(kCmbThreads / 32) * 128 * 16;
-  const auto ckern = a.parent ? combine_kernel<true> : combine_kernel<false>;
-  e = set_smem_once(ckern, (int)cmb_smem, &g_cmb_attr[a.parent ? 1 : 0]);
+  const int kind = shared ? kCmbShared : a.parent ? kCmbTree : kCmbPlain;
+  const auto ckern = shared     ? combine_kernel<kCmbShared>
+                     : a.parent ? combine_kernel<kCmbTree>
+                                : combine_kernel<kCmbPlain>;
+  e = set_smem_once(ckern, (int)cmb_smem, &g_cmb_attr[kind]);
   if (e != cudaSuccess) return e;
   kernel_mark(st, "combine");
   return launch_pdl(ckern, dim3(g.Dv / kCmbJ, kH), dim3(kCmbThreads), cmb_smem, st, cp);

@@ -164,8 +164,7 @@ struct KeyAppendArgs {
 };
 cudaError_t launch_index_key_append(const KeyAppendArgs& a, cudaStream_t st);
 
-// CUDA-core attention of a tree, or causal where a.parent is null (kv_lora up to 512; other shapes take
-// launch_decode_simt).
+// CUDA-core tree attention, chains where a.parent is null (kv_lora up to 512; other shapes take launch_decode_simt).
 bool tree_simt_ok(const Geometry& g, int B);
 size_t tree_simt_workspace_bytes(const Geometry& g, int B, int S, int T_cap);
 cudaError_t launch_tree_simt(const DecodeArgs& a, int dtype, void* ws, cudaStream_t st);
@@ -178,7 +177,7 @@ constexpr int kMaxTree = 64;
 constexpr int kMaxTreeCap = 0x7fffffff - 1023;
 
 // Query rows B * S of a shared-prefix call.
-constexpr int kMaxSharedRows = 32768;
+constexpr int kMaxSharedRows = 8192;
 
 struct VerifyArgs {
   int B, S, V;

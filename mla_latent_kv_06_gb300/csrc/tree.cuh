@@ -42,4 +42,10 @@ __device__ __forceinline__ TreeNode tree_node(const int32_t* par, int s) {
   return n;
 }
 
+// Query s of sequence b: a node of the trees `parent` [B, S], or without them of a chain.
+__device__ __forceinline__ TreeNode node_at(const int32_t* parent, int b, int S, int s) {
+  if (parent) return tree_node(parent + (size_t)b * S, s);
+  return TreeNode{s >= 63 ? ~0ull : (2ull << s) - 1, s, kNodePresent};
+}
+
 }  // namespace mla

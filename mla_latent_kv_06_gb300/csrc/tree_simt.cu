@@ -10,10 +10,9 @@
 // on one sequence has one group of rows); a second kernel merges the splits
 // and lifts with W_UV.  With one split the same CTA does both.
 // Rows are ordered head-major, so that a CTA reads the W_UK of few heads.
-// Without a tree (kTree = false) query s sees the keys up to its own: the shared-prefix
-// calls take this form.  Each sequence reads the prefix through its own table there: a
-// key row in shared memory already serves 16 query rows, and grouping rows of several
-// sequences would help only models of fewer than 16 / S heads.
+// A shared-prefix call takes the same kernels, each sequence reading the prefix
+// through its own table: a key row in shared memory already serves 16 query rows, and
+// grouping rows of several sequences would help only models of fewer than 16 / S heads.
 // Bound: fp32 multiply-adds and shared-memory reads for long contexts, latency
 // for the toy model (4 heads, 4 nodes, 64 keys: 11.3 us, of which the launch
 // and the chain query - absorb - scores - softmax - lift is all).
@@ -121,14 +120,7 @@ __device__ __forceinline__ void lift(const DecodeArgs& a, int b, int row0, int n
 // Keys per tile: short rows take more, for fewer round trips.
 __host__ __device__ constexpr int keys_of(int acc) { return acc <= 2 ? 128 : acc <= 8 ? 64 : 32; }
 
-// State and visible keys of query s of sequence b.
-template <bool kTree>
-__device__ __forceinline__ TreeNode node_of(const DecodeArgs& a, int b, int s) {
-  if (kTree) return tree_node(a.parent + (size_t)b * a.S, s);
-  return TreeNode{1ull, s, kNodePresent};  // (the mask only says that it is there)
-}
-
-template <typename Tin, int kAcc, bool kTree>
+template <typename Tin, int kAcc>
 __global__ void __launch_bounds__(kThreads) tree_attend_kernel(const __grid_constant__ Params p) {
   const DecodeArgs& a = p.a;
   const Geometry& g = a.g;
@@ -149,7 +141,7 @@ __global__ void __launch_bounds__(kThreads) tree_attend_kernel(const __grid_cons
   const bool bad_len = Tb < a.S + a.lead || Tb > a.T_cap;
   if (tid < kRows) {
     TreeNode node{0ull, 0, kNodeAbsent};
-    if (tid < nrows) node = node_of<kTree>(a, b, (row0 + tid) % a.S);
+    if (tid < nrows) node = node_at(a.parent, b, a.S, (row0 + tid) % a.S);
     mask_sh[tid] = node.mask;
     depth_sh[tid] = node.depth;
     fill[tid] = bad_len || node.state == kNodeBad ? qnan() : node.state == kNodeAbsent ? 0.f : 1.f;
@@ -200,7 +192,6 @@ __global__ void __launch_bounds__(kThreads) tree_attend_kernel(const __grid_cons
   }
   __syncthreads();
   const unsigned long long mask = mask_sh[rr];
-  const int last = base + depth_sh[rr];  // without a tree: the query's own key
   float acc[kAcc];
 #pragma unroll
   for (int j = 0; j < kAcc; ++j) acc[j] = 0.f;
@@ -235,7 +226,7 @@ __global__ void __launch_bounds__(kThreads) tree_attend_kernel(const __grid_cons
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int k = tl + 16 * i, t = k0 + k;
-      seen[i] = mask && k < nk && (kTree ? t < base || ((mask >> (t - base)) & 1ull) : t <= last);
+      seen[i] = mask && k < nk && (t < base || ((mask >> (t - base)) & 1ull));
       sc[i] = seen[i] ? sc[i] : -INFINITY;
       top = fmaxf(top, sc[i]);
     }
@@ -293,7 +284,7 @@ __global__ void __launch_bounds__(kThreads) tree_attend_kernel(const __grid_cons
 // Merge of the splits of up to 4 rows, then the lift.
 constexpr int kMergeRows = 4;
 
-template <typename Tin, int kAcc, bool kTree>
+template <typename Tin, int kAcc>
 __global__ void __launch_bounds__(128) tree_merge_kernel(const __grid_constant__ Params p) {
   const DecodeArgs& a = p.a;
   const Geometry& g = a.g;
@@ -304,7 +295,7 @@ __global__ void __launch_bounds__(128) tree_merge_kernel(const __grid_constant__
   const int Tb = a.T[b];
   grid_dep_wait();
   if (warp < nrows) {
-    const TreeNode node = node_of<kTree>(a, b, (row0 + warp) % a.S);
+    const TreeNode node = node_at(a.parent, b, a.S, (row0 + warp) % a.S);
     const bool bad = Tb < a.S + a.lead || Tb > a.T_cap || node.state == kNodeBad;
     if (lane == 0) fill[warp] = bad ? qnan() : node.state == kNodeAbsent ? 0.f : 1.f;
     const size_t step = (size_t)SH * (g.Dl + 2);
@@ -355,7 +346,7 @@ int split_count(const Geometry& g, int B, int S, int T_cap) {
   return (int)(s < 1 ? 1 : s > 512 ? 512 : s);
 }
 
-template <typename Tin, int kAcc, bool kTree>
+template <typename Tin, int kAcc>
 cudaError_t launch(const Params& p, cudaStream_t st) {
   const DecodeArgs& a = p.a;
   const int smem = (int)smem_bytes(a.g);
@@ -365,22 +356,17 @@ cudaError_t launch(const Params& p, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const unsigned long long bit = 1ull << (dev & 63);
   if (!(done.load() & bit)) {
-    e = cudaFuncSetAttribute(tree_attend_kernel<Tin, kAcc, kTree>, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024);
+    e = cudaFuncSetAttribute(tree_attend_kernel<Tin, kAcc>, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024);
     if (e != cudaSuccess) return e;
     done.fetch_or(bit);
   }
   const int SH = a.S * a.g.H;
-  kernel_mark(st, kTree ? "tree_attend" : "attend");
-  tree_attend_kernel<Tin, kAcc, kTree><<<dim3((SH + kRows - 1) / kRows, p.splits, a.B), kThreads, smem, st>>>(p);
+  kernel_mark(st, "tree_attend");
+  tree_attend_kernel<Tin, kAcc><<<dim3((SH + kRows - 1) / kRows, p.splits, a.B), kThreads, smem, st>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess || p.splits == 1) return e;
-  kernel_mark(st, kTree ? "tree_merge" : "merge");
-  return launch_pdl(tree_merge_kernel<Tin, kAcc, kTree>, dim3((SH + kMergeRows - 1) / kMergeRows, a.B), dim3(128), 0, st, p);
-}
-
-template <int kAcc, bool kTree>
-cudaError_t launch_as(const Params& p, int dtype, cudaStream_t st) {
-  return dtype == MLA_F32 ? launch<float, kAcc, kTree>(p, st) : launch<__nv_bfloat16, kAcc, kTree>(p, st);
+  kernel_mark(st, "tree_merge");
+  return launch_pdl(tree_merge_kernel<Tin, kAcc>, dim3((SH + kMergeRows - 1) / kMergeRows, a.B), dim3(128), 0, st, p);
 }
 
 }  // namespace
@@ -397,11 +383,10 @@ size_t tree_simt_workspace_bytes(const Geometry& g, int B, int S, int T_cap) {
 cudaError_t launch_tree_simt(const DecodeArgs& a, int dtype, void* ws, cudaStream_t st) {
   Params p{a, split_count(a.g, a.B, a.S, a.T_cap), {}, static_cast<float*>(ws)};
   for (int j = 0; j < a.g.Dr / 2; ++j) p.turn[j] = rope_turns(std::pow(a.g.rope_base, -2.0 * j / a.g.Dr));
-  const int acc = acc_of(a.g);
-  if (a.parent) return acc == 2 ? launch_as<2, true>(p, dtype, st) : acc == 8 ? launch_as<8, true>(p, dtype, st)
-                                                                             : launch_as<32, true>(p, dtype, st);
-  return acc == 2 ? launch_as<2, false>(p, dtype, st) : acc == 8 ? launch_as<8, false>(p, dtype, st)
-                                                                 : launch_as<32, false>(p, dtype, st);
+  const bool f = dtype == MLA_F32;
+  if (acc_of(a.g) == 2) return f ? launch<float, 2>(p, st) : launch<__nv_bfloat16, 2>(p, st);
+  if (acc_of(a.g) == 8) return f ? launch<float, 8>(p, st) : launch<__nv_bfloat16, 8>(p, st);
+  return f ? launch<float, 32>(p, st) : launch<__nv_bfloat16, 32>(p, st);
 }
 
 }  // namespace mla

@@ -11,6 +11,7 @@ import torch
 
 import oracle
 from tests._np import check_close, to_np
+from tests._trees import random_parents
 from workload import GLM, TINY, Dims, append_inputs, mla_inputs
 
 pytestmark = pytest.mark.gpu
@@ -64,7 +65,7 @@ def _check(lib, out, x, T, dims, dtype):
 # (lengths, S, tokens really shared, shared as passed)
 CASES = [([1], 1, 0, 0), ([257], 1, 256, 256), ([300, 513], 1, 256, 256), ([700, 530, 900], 1, 512, 512),
          ([700, 530, 900], 2, 512, 511), ([650, 700], 3, 640, 640), ([400] * 9, 1, 256, 256), ([300, 290, 262], 6, 256, 255),
-         ([1100] * 5, 7, 1024, 1024), ([1030, 1500, 1024 + 5], 5, 1024, 1000), ([90, 100], 1, 0, 0), ([900, 901], 65, 768, 768)]
+         ([1100] * 5, 7, 1024, 1024), ([1030, 1500, 1024 + 5], 5, 1024, 1000), ([90, 100], 1, 0, 0), ([900, 901], 64, 768, 768)]
 
 
 @pytest.mark.parametrize("T,S,common,shared", CASES)
@@ -79,7 +80,7 @@ def test_glm(cuda_lib, T, S, common, shared, out_dtype, page):
 
 @pytest.mark.parametrize("dims,dtype,page", [(TINY, "f32", 16), (TINY, "f32", 128), (SMALL, "f32", 7), (SMALL, "bf16", 48),
                                              (WIDE, "f32", 32), (GLM, "f32", 128), (GLM, "bf16", 48)])
-@pytest.mark.parametrize("T,S,common", [([1], 1, 0), ([70, 66], 1, 48), ([300, 301, 400], 2, 256), ([130, 260], 70, 0), ([1500], 5, 1200)])
+@pytest.mark.parametrize("T,S,common", [([1], 1, 0), ([70, 66], 1, 48), ([300, 301, 400], 2, 256), ([130, 260], 64, 0), ([1500], 5, 1200)])
 def test_other_geometries(cuda_lib, dims, dtype, page, T, S, common):
     if S > 60 and dims.H == 64:
         S = 9
@@ -153,6 +154,44 @@ def test_bad_pages(cuda_lib, dims, dtype, page):
             _call(cuda_lib, x, shared, dims)
             assert cuda_lib.device_status() == cuda_lib.MLA_DEV_BAD_INDEX, (b, i, bad)
     assert cuda_lib.device_status() == 0
+
+
+@pytest.mark.parametrize("dims,dtype,page", [(GLM, "bf16", 128), (TINY, "f32", 16), (SMALL, "bf16", 32), (WIDE, "f32", 32)])
+@pytest.mark.parametrize("T,S,common", [([700, 530, 650], 5, 512), ([800, 770], 33, 704), ([300] * 4, 2, 256), ([40, 50], 8, 0)])
+def test_trees_behind_the_prefix(cuda_lib, dims, dtype, page, T, S, common):
+    """Drafted trees, absent nodes among them whose rows hold NaN, and one bad node."""
+    common = common // page * page
+    parent = random_parents(len(T), S, S)
+    x = _batch(dims, dtype, T, S, common, page, 71 + S)
+    rows = x["table"].long()
+    for b, s in zip(*np.nonzero(parent == -2)):
+        t = T[b] - S + s
+        x["Lp"][rows[b, t // page], t % page] = float("nan")
+        x["Rp"][rows[b, t // page], t % page] = float("inf")
+    par = torch.from_numpy(parent)
+    tbl = x["table"].tolist()
+    ref = oracle.decode_tree(to_np(x["q"]), oracle.unpage(to_np(x["Lp"]), tbl, T), oracle.unpage(to_np(x["Rp"]), tbl, T), T, parent,
+                             to_np(x["kv_b"]), dims.qk_nope, dims.softmax_scale)
+    for out_dtype in (None, torch.bfloat16):
+        out = _call(cuda_lib, x, common, dims, out_dtype=out_dtype, parent=par.to(DEV))
+        assert cuda_lib.device_status() == 0
+        got = to_np(out)
+        assert np.all(np.isfinite(got)) and np.all(got[parent == -2] == 0)
+        check_close(got[parent != -2], ref[parent != -2], TOL[dtype] + (2.0 ** -8 if out_dtype else 0))
+    par[0, 1] = 1  # its own parent
+    bad = [s for s in range(S) if s == 1 or _under(par[0].tolist(), s, 1)]
+    out = _call(cuda_lib, x, common, dims, parent=par.to(DEV))
+    assert cuda_lib.device_status() == cuda_lib.MLA_DEV_BAD_INDEX
+    assert bool(torch.isnan(out[0, bad]).all())
+    check_close(to_np(out[1:])[parent[1:] != -2], ref[1:][parent[1:] != -2], TOL[dtype])
+
+
+def _under(parent, s, top):
+    while parent[s] >= 0 and parent[s] != s:
+        s = parent[s]
+        if s == top:
+            return True
+    return False
 
 
 def test_graphs_that_share_a_workspace(cuda_lib):
