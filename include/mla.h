@@ -583,7 +583,7 @@ int mla_tree_commit_paged(int n, void* const* cache, const int* row_bytes, int B
  * A logit of -inf is never kept.  A row without a finite logit, with a NaN or
  * +inf, or with a setting that is NaN or a temperature that is negative or
  * infinite raises MLA_DEV_BAD_VALUE and gives token -1 and NaN probabilities.
- * Comparisons of masses hold to 2^-33 of each weight, with exact sums of weights
+ * Comparisons of masses hold to 2^-31 of each weight, with exact sums of weights
  * rounded to 2^-44 of the largest; results do not depend on the launch.
  *
  *   logits  float or bf16 (dtype), row (b, n) at element b * l_batch + n * l_row

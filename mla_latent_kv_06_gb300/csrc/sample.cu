@@ -8,24 +8,30 @@
 //   min-p : w(x) >= min_p, a threshold on x itself
 //   top-k : the code of the k-th token
 //   top-p : the code of the token at which the running mass reaches top_p W
-// The last two are found by select(): a histogram of counts or masses over
-// kBins intervals of the order, which narrows the threshold down to one
-// interval, until few enough candidates are left to rank them against each
-// other.  The draw is the least index whose cumulative kept mass exceeds u W.
+// The last two come from a histogram (of counts, or of masses) over kBins
+// intervals of x, which narrows the threshold down to one interval, and from its
+// tokens, ranked against each other; an interval of more than kList tokens is split
+// again, by x and then by codes.  A small k needs no histogram of the row: the
+// k-th of the threads' largest tokens bounds the k-th token from below, and
+// what reaches that bound, little more than k tokens, decides everything else.
+// The draw is the least index whose cumulative kept mass exceeds u W.
 //
 // Rounding.  A threshold and a draw compare sums over the vocabulary, so a
-// weight is a 64-bit integer, w 2^44 rounded once: sums are then exact, in any
-// order, and the kernel's atomics cannot change a result.  The exponential is
-// taken in fp32 pairs without the fp64 pipe (1/64 of the fp32 rate): x - max
-// by two-sum, times log2(e)/T as a pair, a table of 2^(-i/256) in 48 bits and
-// a cubic for the rest, error below 2^-33 of the weight.
+// weight is a 64-bit integer, w 2^45 cut to an odd number (an error of one unit
+// without a bias): sums are then exact, in any order, and the kernel's atomics
+// cannot change a result.  The exponential is taken without the fp64 pipe (1/64 of
+// the fp32 rate): 256 log2(e) x / T as an integer and a rest to 2^-25, from fused
+// multiply-adds whose products are exact; a table of 2^(-i/256) in 48 bits and a
+// cubic for the rest, error below 2^-31 of the weight (rms 2^-34).
 //
 // A row is a cluster of up to 8 CTAs, each with a contiguous part of the
-// vocabulary in shared memory as fp32, read once; a warp's part is contiguous
-// too, and no other warp reads it.
+// vocabulary in shared memory, read once, 16 bytes at a time from 16-byte
+// boundaries; a warp's part is contiguous too, and no other warp reads it.
 #include <cooperative_groups.h>
+#include <limits.h>
 
 #include <atomic>
+#include <utility>
 
 #include "common.cuh"
 #include "internal.h"
@@ -40,17 +46,19 @@ typedef unsigned long long u64;
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 1024;
-constexpr int kCluster = 8;    // most CTAs of a row
-constexpr int kList = 1024;    // candidates that are ranked against each other
-constexpr int kOne = 44;       // a weight of 1 is 2^kOne; kMaxSampleVocab of them stay below 2^63
+constexpr int kCluster = 8;  // most CTAs of a row
+constexpr int kList = 1024;  // tokens that are ranked against each other
+constexpr int kOwn = 768;    // most of them from one CTA
+constexpr int kSmallK = 512;  // top-k by the threads' largest tokens
+constexpr int kOne = 45;     // a weight of 1 is 2^kOne; kMaxSampleVocab of them stay below 2^64
 constexpr int kIndexBits = 20;
 constexpr u64 kIndexMask = (1ull << kIndexBits) - 1;
 constexpr float kNegligible = 256.f * (kOne + 2);  // 256 log2 of a weight that rounds to 0
-static_assert(kMaxSampleVocab <= (1 << 19), "sums of weights stay below 2^63, indices below 2^kIndexBits");
+static_assert(kMaxSampleVocab < (1 << 18) + (1 << 17), "sums of weights stay below 2^64, indices below 2^kIndexBits");
 
-// 2^(-i/256) as hi + lo, hi < 1 of 24 bits.
+// 2^(-i/256) as hi + lo, hi < 1 of 24 bits; lo times 2^40.
 struct ExpTable {
-  float hi[256], lo[256];
+  float v[256][2];
 };
 constexpr ExpTable make_table() {
   ExpTable t{};
@@ -63,31 +71,34 @@ constexpr ExpTable make_table() {
     }
     const long long scaled = (long long)(sum * 16777216.0);
     const long long top = scaled < 16777216 ? scaled : 16777215;
-    t.hi[i] = (float)((double)top / 16777216.0);
-    t.lo[i] = (float)(sum - (double)top / 16777216.0);
+    t.v[i][0] = (float)((double)top / 16777216.0);
+    t.v[i][1] = (float)((sum - (double)top / 16777216.0) * 1099511627776.0);
   }
   return t;
 }
-__constant__ ExpTable kTable = make_table();
-
-struct Bin {
-  unsigned cnt, lo, hi;  // tokens; mass as two words
-};
+__device__ const ExpTable kTable = make_table();
 
 struct Shared {
-  unsigned cnt[kBins], lo[kBins], hi[kBins];  // this CTA's histogram
-  unsigned tot_cnt[kBins];                    // the cluster's, written by all CTAs
-  u64 tot[kBins];
+  union {
+    struct {
+      unsigned cnt[kBins], lo[kBins], hi[kBins];  // this CTA's histogram: tokens, or mass as two words
+    };
+    struct {
+      u64 own_code[kOwn], own_w[kOwn];  // then its share of the list
+    };
+  };
+  u64 tot[kBins];                             // the cluster's, written by all CTAs
   u64 list_code[kList], list_w[kList];
   float2 table[256];
+  float2 heat;       // c as a pair
+  double least;      // T log(min_p)
   float max[kCluster], min[kCluster];
-  int bad[kCluster];
+  int first[kCluster];
   u64 mass[kCluster];
   u64 warp_mass[kWarps];
-  unsigned warp_cnt[kWarps];
   float warp_max[kWarps], warp_min[kWarps];
-  int listed;
-  int warp_bad;
+  int warp_first[kWarps];
+  int listed, listed_own, at[kCluster];
   int bin;
   u64 before;
   u64 code, upto;
@@ -107,41 +118,69 @@ __device__ __forceinline__ u64 warp_scan64(u64 v) {  // inclusive
   }
   return v;
 }
+// The larger one; NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 
-// log2(e) 256 / T as a pair.
+// With c = 256 log2(e) / T = hi + lo, 256 log2 of a weight is x c - top, top being max c
+// rounded up to an integer (the common factor cancels wherever weights are used).  Where
+// max c is too large for that (not fast), it is (x - max) c, with x - max by two-sum.
+// Logits below `least` have no weight.
 struct Heat {
-  float hi, lo;
+  float hi, lo, max, least;
+  int top;
+  bool fast;
 };
+__device__ __forceinline__ Heat make_heat(float max, float2 c) {
+  const float m = max * c.x;
+  Heat h{c.x, c.y, max, -INFINITY, 0, fabsf(m) < 2097152.f};
+  if (h.fast) {
+    h.top = (int)ceilf(m);
+    h.least = ((float)h.top - kNegligible) / c.x;
+  } else {
+    h.least = max - kNegligible / c.x;  // (rounding moves it by less than the spacing of such logits)
+  }
+  return h;
+}
 
-// w = exp((x - max) / T) as (mant_hi + mant_lo) 2^-n; false where w < 2^(-limit / 256).
+constexpr int kMagicBits = 0x4B400000;
+constexpr float kMagic = 12582912.f;  // 1.5 2^23: adding it rounds to an integer, in the low bits
+
+// A weight as (hi + lo 2^-40) 2^-n.  x from `least` up, or a little below: |x c| < 2^22.
 struct Parts {
   float hi, lo;
   int n;
 };
-__device__ __forceinline__ bool weight_parts(float x, float max, const Heat& h, const float2* table, float limit, Parts* p) {
-  const float d = max - x, b = d - max, dl = (max - (d - b)) + (-x - b);
-  const float y = d * h.hi;
-  if (!(y < limit)) return false;
-  const float e = fmaf(d, h.hi, -y) + fmaf(d, h.lo, dl * h.hi);
-  const float m = y + 12582912.f;  // 1.5 2^23: the integer part in the low bits
-  const int k = __float_as_int(m) - 0x4B400000;
-  const float r = (y - (m - 12582912.f)) + e;
-  const float z = r * -0.0027076061740622863f;  // ln(2) / 256
-  const float q = fmaf(z * z, fmaf(z, 1.f / 6.f, 0.5f), z);  // exp(z) - 1
+__device__ __forceinline__ Parts weight_parts(float x, const Heat& h, const float2* table) {
+  float r;
+  int k;
+  if (h.fast) {
+    const float z = fmaf(x, h.hi, kMagic);  // x c as an integer ...
+    r = fmaf(-x, h.lo, fmaf(-x, h.hi, z - kMagic));  // ... less x c: the products are exact
+    k = h.top + kMagicBits - __float_as_int(z);
+  } else {
+    const float d = h.max - x, b = d - h.max, dl = (h.max - (d - b)) + (-x - b);
+    const float z = fmaf(d, h.hi, kMagic);
+    r = fmaf(d, h.hi, -(z - kMagic)) + fmaf(d, h.lo, dl * h.hi);
+    k = __float_as_int(z) - kMagicBits;
+  }
   const float2 t = table[k & 255];
-  p->hi = t.x;
-  p->lo = fmaf(t.x, q, t.y);
-  p->n = k >> 8;
-  return true;
+  // (exp(-r ln(2) / 256) - 1) 2^40, |r| < 0.7: below 2^31
+  constexpr float kStep = -0.0027076061740622863f, kUnit = 1099511627776.f;
+  const float q = r * fmaf(r, fmaf(r, kStep * kStep * kStep / 6.f * kUnit, kStep * kStep / 2.f * kUnit), kStep * kUnit);
+  return Parts{t.x, fmaf(t.x, q, t.y), k >> 8};
 }
 
-__device__ __forceinline__ u64 weight(float x, float max, const Heat& h, const float2* table) {
-  Parts p;
-  if (!weight_parts(x, max, h, table, kNegligible, &p)) return 0;
-  // hi < 1 has exponent -1: 24 bits with the hidden one
+// For x >= least.
+__device__ __forceinline__ u64 weight(float x, const Heat& h, const float2* table) {
+  const Parts p = weight_parts(x, h, table);
+  // hi < 1 has exponent -1: 24 bits with the hidden one.  |lo| < 2^31.
   const u64 a = (u64)((__float_as_uint(p.hi) & 0x7fffffu) | 0x800000u) << (kOne - 24);
-  const long long c = (long long)__float2int_rn(p.lo * 1099511627776.f) << (kOne - 40);  // |lo| < 2^-9
-  return (((a + (u64)c) << 1 >> p.n) + 1) >> 1;
+  const long long c = (long long)__float2int_rn(p.lo) * (1ll << (kOne - 40));
+  return ((a + (u64)c) >> min((unsigned)p.n, 63u)) | 1;
 }
 
 __device__ __forceinline__ u64 code_of(float x, int index) {
@@ -163,282 +202,590 @@ __device__ __forceinline__ u64 fraction_of(float f, u64 m, bool* inexact) {
   return t >= 64 ? 0 : hi >> t;
 }
 
-// This CTA's part of a row, and what is known of the row.
-struct Row {
-  const float* x;  // shared memory
-  int base, lo, hi;  // index of x[0]; the warp's elements
-  float max;
-  Heat heat;
-  u64 floor;  // a token is kept when its code is at least this
+// Of a mass W, what the running mass has to reach: the least integer >= p W, and at least 1.
+__device__ __forceinline__ u64 wanted(float p, u64 whole) {
+  bool cut;
+  const u64 t = fraction_of(fmaxf(p, 0.f), whole, &cut);
+  return t + (cut || t == 0 ? 1 : 0);
+}
+
+// floor(u W), below W.
+__device__ __forceinline__ u64 drawn(float u, u64 whole) {
+  bool cut;
+  return u >= 1.f ? whole - 1 : u > 0.f ? fraction_of(u, whole, &cut) : 0;
+}
+
+template <typename Tin>
+struct Vec;
+template <>
+struct Vec<float> {
+  static constexpr int kN = 4;
+  static __device__ __forceinline__ void get(const uint4& v, float (&x)[4]) {
+    x[0] = __uint_as_float(v.x);
+    x[1] = __uint_as_float(v.y);
+    x[2] = __uint_as_float(v.z);
+    x[3] = __uint_as_float(v.w);
+  }
+  // running largest (NaN if one is) and smallest value
+  struct Extremes {
+    float mx = -INFINITY, mn = INFINITY;
+    __device__ __forceinline__ void add(const uint4& v) {
+      float x[4];
+      get(v, x);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        mx = max_nan(mx, x[j]);
+        mn = fminf(mn, x[j]);
+      }
+    }
+    __device__ __forceinline__ float max() const { return mx; }
+    __device__ __forceinline__ float min() const { return mn; }
+  };
+};
+template <>
+struct Vec<__nv_bfloat16> {
+  static constexpr int kN = 8;
+  static __device__ __forceinline__ void get(const uint4& v, float (&x)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+  struct Extremes {  // two values an instruction
+    uint32_t mx = 0xff80ff80u, mn = 0x7f807f80u;
+    __device__ __forceinline__ void add(const uint4& v) {
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(mx) : "r"(w[i]));
+        asm("min.bf16x2 %0, %0, %1;" : "+r"(mn) : "r"(w[i]));
+      }
+    }
+    __device__ __forceinline__ float max() const {
+      return max_nan(__uint_as_float(mx << 16), __uint_as_float(mx & 0xffff0000u));
+    }
+    __device__ __forceinline__ float min() const {
+      return fminf(__uint_as_float(mn << 16), __uint_as_float(mn & 0xffff0000u));
+    }
+  };
 };
 
-// The code at which the running count (kMass: mass) of the kept tokens, in
-// order, reaches a target: `target` for counts, the fraction `p` of the whole for masses.
-// range: tokens further than this below the maximum share the last interval.
-// Raises row.floor to that code (leaves it where the whole does not reach the
-// target); with kMass returns the mass kept.
+// This warp's part of a row, and what is kept of it.
+struct Row {
+  const unsigned char* part;  // the CTA's part in shared memory
+  int base;                   // index of its first element (below 0 where that is padding)
+  int lo, hi;                 // the warp's elements
+  Heat heat;
+  float thr;                  // kept: x above thr, or equal to it with an index up to `last`
+  int last;
+  __device__ __forceinline__ bool kept(float x, int i) const { return x > thr || (x == thr && base + i <= last); }
+  __device__ __forceinline__ void set(u64 code) {
+    const unsigned key = (unsigned)(code >> kIndexBits);
+    thr = __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
+    last = (int)(kIndexMask - (code & kIndexMask));
+  }
+  __device__ __forceinline__ float next() const {  // the float after thr
+    const int bits = __float_as_int(thr);
+    return thr == 0.f ? __int_as_float(1) : __int_as_float(bits + (bits < 0 ? -1 : 1));
+  }
+};
+
+// The kept ones of a vector's elements by one bound each (weighed: those with a weight).
+template <int kN>
+struct Bounds {
+  float thr, next, least;
+  int last;  // in the part; -1: none of the equal ones
+  __device__ __forceinline__ Bounds(const Row& row, bool weighed)
+      : thr(row.thr), next(row.next()), least(weighed ? row.heat.least : -INFINITY) {
+    const long long at = (long long)row.last - row.base;
+    last = (int)(at < -1 ? -1 : at < (1 << 30) ? at : 1 << 30);
+  }
+  __device__ __forceinline__ void test(const float (&x)[kN], int i, bool (&in)[kN]) const {
+    const float bound = fmaxf(i + kN - 1 <= last ? thr : next, least);
+#pragma unroll
+    for (int j = 0; j < kN; ++j) in[j] = x[j] >= bound;
+    if (i <= last && last < i + kN - 1) {  // `last` lies inside
+#pragma unroll
+      for (int j = 0; j < kN; ++j) in[j] = in[j] || (x[j] == thr && i + j <= last && x[j] >= least);
+    }
+  }
+};
+
+// Intervals of x below the maximum, the last one without an end: a monotonic map, whatever rounding does.
+struct Bins {
+  float step, off;
+  __device__ __forceinline__ Bins(float max, float range) : step(range > 0.f ? (float)kBins / range : 0.f), off(max * step) {}
+  __device__ __forceinline__ float at(float x) const {
+    return fminf(fmaxf(fmaf(-x, step, off), 0.f), (float)(kBins - 1));
+  }
+  static __device__ __forceinline__ int index(float f) { return (__float_as_int(f + kMagic) - kMagicBits) & (kBins - 1); }
+  // finer intervals inside interval b
+  static __device__ __forceinline__ float inside(float f, int b) {
+    return fminf(fmaxf((f - ((float)b - 0.5f)) * (float)kBins, 0.f), (float)(kBins - 1));
+  }
+};
+
+// f(x, i) for the warp's elements, a vector x at the elements i, i + 1, .. per lane and step.
+template <typename Tin, typename F>
+__device__ __forceinline__ void for_each(const Row& row, F&& f) {
+  constexpr int kN = Vec<Tin>::kN;
+  for (int i = row.lo + kN * (int)(threadIdx.x & 31); i < row.hi; i += 32 * kN) {
+    float x[kN];
+    Vec<Tin>::get(*reinterpret_cast<const uint4*>(row.part + (size_t)i * sizeof(Tin)), x);
+    f(x, i);
+  }
+}
+
+// Sums of the cluster's histograms, in every CTA's tot.  Two cluster barriers.
 template <bool kMass>
-__device__ u64 select(cg::cluster_group& cluster, Shared& sh, Row& row, float range, u64 target, float p) {
+__device__ __forceinline__ void sum_bins(cg::cluster_group& cluster, Shared& sh) {
+  const int C = (int)cluster.num_blocks(), share = kBins / C, first = (int)cluster.block_rank() * share;
+  cluster.sync();
+  for (int i = threadIdx.x; i < share; i += kThreads) {
+    const int bin = first + i;
+    u64 w = 0;
+    for (int q = 0; q < C; ++q) {
+      if (kMass) w += ((u64)*cluster.map_shared_rank(&sh.hi[bin], q) << 32) + *cluster.map_shared_rank(&sh.lo[bin], q);
+      else w += *cluster.map_shared_rank(&sh.cnt[bin], q);
+    }
+    for (int q = 0; q < C; ++q) *cluster.map_shared_rank(&sh.tot[bin], q) = w;
+  }
+  cluster.sync();
+}
+
+__device__ __forceinline__ void add_mass(Shared& sh, int bin, u64 w) {
+  const unsigned wl = (unsigned)w, old = atomicAdd(&sh.lo[bin], wl);
+  const unsigned wh = (unsigned)(w >> 32) + (old + wl < old ? 1u : 0u);
+  if (wh) atomicAdd(&sh.hi[bin], wh);
+}
+
+// The interval of tot in which the running sum, from `above` on, reaches the target, in
+// sh.bin with the sum before it in sh.before; the last one where it never does.
+// target(whole) gives the target for the sum of all.
+template <typename F>
+__device__ __forceinline__ u64 find_bin(Shared& sh, u64 above, F&& target) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
-  const float step = range > 0.f ? (float)kBins / range : 0.f;
-  u64 lo = 0, hi = ~0ull, above = 0;  // the threshold lies in [lo, hi]; what the codes above it hold
-  int b0 = -1, shift = 0;  // first level: intervals of x; later ones: of codes inside interval b0
-  auto first_bin = [&](float x) -> int {
-    const float f = (row.max - x) * step;
-    return f < (float)(kBins - 1) ? (int)f : kBins - 1;
+  constexpr int kPer = kBins / kThreads;
+  u64 mine[kPer], sum = 0;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) sum += mine[k] = sh.tot[tid * kPer + k];
+  const u64 incl = warp_scan64(sum);
+  if (lane == 31) sh.warp_mass[warp] = incl;
+  __syncthreads();
+  u64 run = above + incl - sum, whole = above;
+  for (int q = 0; q < kWarps; ++q) {
+    if (q < warp) run += sh.warp_mass[q];
+    whole += sh.warp_mass[q];
+  }
+  const u64 want = target(whole);
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    if ((run < want && want <= run + mine[k]) || (tid * kPer + k == kBins - 1 && want > whole)) {
+      sh.bin = tid * kPer + k;
+      sh.before = run;
+    }
+    run += mine[k];
+  }
+  __syncthreads();
+  return want;
+}
+
+// The kept tokens for which in(x, i) holds, with their codes and weights, in every CTA's list.
+// Their number, or one above kList where the list does not hold them all.  One cluster barrier.
+template <typename Tin, typename F>
+__device__ __forceinline__ int collect(cg::cluster_group& cluster, Shared& sh, const Row& row, F&& in) {
+  constexpr int kN = Vec<Tin>::kN;
+  const int C = (int)cluster.num_blocks(), tid = threadIdx.x;
+  const Bounds<kN> bounds(row, false);
+  for_each<Tin>(row, [&](const auto& x, int i) {
+    bool take[kN], any = false;
+    bounds.test(x, i, take);
+#pragma unroll
+    for (int j = 0; j < kN; ++j) {
+      take[j] = take[j] && in(x[j], i + j);
+      any = any || take[j];
+    }
+    if (!any) return;
+#pragma unroll
+    for (int j = 0; j < kN; ++j) {
+      if (!take[j]) continue;
+      const int at = atomicAdd(&sh.listed_own, 1);
+      if (at >= kOwn) continue;
+      sh.own_code[at] = code_of(x[j], row.base + i + j);
+      sh.own_w[at] = x[j] >= row.heat.least ? weight(x[j], row.heat, sh.table) : 0;
+    }
+  });
+  __syncthreads();
+  const int n = sh.listed_own;
+  if (tid < C) sh.at[tid] = atomicAdd(cluster.map_shared_rank(&sh.listed, tid), n > kOwn ? kList + 1 : n);
+  __syncthreads();
+  for (int q = 0; q < C; ++q) {
+    const int at = sh.at[q];
+    if (n > kOwn || at + n > kList) continue;
+    u64* code = cluster.map_shared_rank(&sh.list_code[0], q);
+    u64* w = cluster.map_shared_rank(&sh.list_w[0], q);
+    for (int i = tid; i < n; i += kThreads) {
+      code[at + i] = sh.own_code[i];
+      w[at + i] = sh.own_w[i];
+    }
+  }
+  cluster.sync();
+  return sh.listed;
+}
+
+__device__ __forceinline__ void clear_bins(Shared& sh) {
+  for (int i = threadIdx.x; i < kBins; i += kThreads) sh.cnt[i] = sh.lo[i] = sh.hi[i] = 0;
+  if (threadIdx.x == 0) sh.listed = sh.listed_own = 0;
+  __syncthreads();
+}
+
+// The code at which the running count (kMass: mass) of the kept tokens, in
+// order, reaches want(whole).  Makes it the row's threshold; where the whole
+// does not reach it, all stay.  range: about where the threshold lies, from the maximum.
+template <typename Tin, bool kMass, typename F>
+__device__ __forceinline__ u64 select(cg::cluster_group& cluster, Shared& sh, Row& row, float range, F&& want) {
+  constexpr int kN = Vec<Tin>::kN;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const Bins bins(row.heat.max, range);
+  const Bounds<kN> bounds(row, kMass);
+  u64 lo = 0, hi = (1ull << (32 + kIndexBits)) - 1, above = 0, target = 0;
+  int level = 0, b0 = 0, b1 = 0, shift = 0, n;
+  // the candidates of the present level, and their intervals at the next one
+  auto candidate = [&](float x, int i, int level) {
+    if (level == 0) return true;
+    const float f = bins.at(x);
+    if (Bins::index(f) != b0) return false;
+    if (level == 1) return true;
+    if (Bins::index(Bins::inside(f, b0)) != b1) return false;
+    const u64 code = code_of(x, row.base + i);
+    return level == 2 || (code >= lo && code <= hi);
   };
-  auto weigh = [&](float x) -> u64 { return kMass ? weight(x, row.max, row.heat, sh.table) : 1; };
+  auto place = [&](float x, int i) -> int {
+    const float f = bins.at(x);
+    return level == 0 ? Bins::index(f) : level == 1 ? Bins::index(Bins::inside(f, b0)) : (int)((hi - code_of(x, row.base + i)) >> shift);
+  };
   for (;;) {
-    for (int i = tid; i < kBins; i += kThreads) sh.cnt[i] = sh.lo[i] = sh.hi[i] = 0;
-    if (tid == 0) sh.listed = 0;
-    __syncthreads();
-    u64 last_w = 0;  // of the last interval, which may hold most tokens
-    unsigned last_n = 0;
-    for (int i = row.lo + lane; i < row.hi; i += 32) {
-      const float x = row.x[i];
-      const u64 code = code_of(x, row.base + i);
-      if (code < row.floor) continue;
-      int bin = first_bin(x);
-      if (b0 >= 0) {
-        if (bin != b0 || code < lo || code > hi) continue;
-        bin = (int)((hi - code) >> shift);
-      }
-      const u64 w = weigh(x);
-      if (bin == kBins - 1) {
-        last_w += w;
-        ++last_n;
-        continue;
-      }
-      atomicAdd(&sh.cnt[bin], 1u);
-      if (kMass) {
-        const unsigned wl = (unsigned)w, old = atomicAdd(&sh.lo[bin], wl);
-        const unsigned wh = (unsigned)(w >> 32) + (old + wl < old ? 1u : 0u);
-        if (wh) atomicAdd(&sh.hi[bin], wh);
-      }
-    }
-    last_w = warp_sum64(last_w);
-    last_n = __reduce_add_sync(0xffffffffu, last_n);
-    if (lane == 0 && last_n) {
-      atomicAdd(&sh.cnt[kBins - 1], last_n);
-      if (kMass) {
-        const unsigned wl = (unsigned)last_w, old = atomicAdd(&sh.lo[kBins - 1], wl);
-        atomicAdd(&sh.hi[kBins - 1], (unsigned)(last_w >> 32) + (old + wl < old ? 1u : 0u));
-      }
-    }
-    cluster.sync();
-    // each CTA sums its share of the intervals over the cluster and hands the sums to all
-    const int share = kBins / C;
-    for (int i = tid; i < share; i += kThreads) {
-      const int bin = rank * share + i;
-      unsigned n = 0;
-      u64 w = 0;
-      for (int q = 0; q < C; ++q) {
-        n += *cluster.map_shared_rank(&sh.cnt[bin], q);
-        if (kMass) w += ((u64)*cluster.map_shared_rank(&sh.hi[bin], q) << 32) + *cluster.map_shared_rank(&sh.lo[bin], q);
-      }
-      if (!kMass) w = n;
-      for (int q = 0; q < C; ++q) {
-        *cluster.map_shared_rank(&sh.tot_cnt[bin], q) = n;
-        *cluster.map_shared_rank(&sh.tot[bin], q) = w;
-      }
-    }
-    cluster.sync();
-    // the interval at which the running sum reaches the target
-    constexpr int kPer = kBins / kThreads;
-    u64 mine[kPer], sum = 0;
+    clear_bins(sh);
+    u64 last = 0;  // of the last interval, which may hold most tokens
+    for_each<Tin>(row, [&](const auto& x, int i) {
+      bool in[kN];
+      bounds.test(x, i, in);
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) sum += mine[k] = sh.tot[tid * kPer + k];
-    const u64 incl = warp_scan64(sum);
-    if (lane == 31) sh.warp_mass[warp] = incl;
-    __syncthreads();
-    u64 run = above + incl - sum, whole = above;
-    for (int q = 0; q < kWarps; ++q) {
-      if (q < warp) run += sh.warp_mass[q];
-      whole += sh.warp_mass[q];
-    }
-    if (b0 < 0) {
-      if (kMass) {
-        bool cut;
-        target = fraction_of(p, whole, &cut);
-        if (cut || target == 0) ++target;
-      } else if (whole <= target) {
-        return 0;
+      for (int j = 0; j < kN; ++j) {
+        if (!__any_sync(0xffffffffu, in[j])) continue;
+        const u64 w = kMass ? weight(x[j], row.heat, sh.table) : 1;
+        if (!in[j] || !candidate(x[j], i + j, level)) continue;
+        const int bin = place(x[j], i + j);
+        if (bin == kBins - 1) last += w;
+        else if (kMass) add_mass(sh, bin, w);
+        else atomicAdd(&sh.cnt[bin], 1u);
       }
+    });
+    last = warp_sum64(last);
+    if (lane == 0 && last) {
+      if (kMass) add_mass(sh, kBins - 1, last);
+      else atomicAdd(&sh.cnt[kBins - 1], (unsigned)last);
     }
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-      if (run < target && target <= run + mine[k]) {
-        sh.bin = tid * kPer + k;
-        sh.before = run;
-      }
-      run += mine[k];
-    }
-    __syncthreads();
+    sum_bins<kMass>(cluster, sh);
+    u64 whole_all = 0;
+    const u64 got = find_bin(sh, above, [&](u64 whole) {
+      whole_all = whole;
+      return level == 0 ? want(whole) : target;
+    });
+    target = got;
+    if (!kMass && level == 0 && whole_all <= target) return 0;
     const int bin = sh.bin;
-    const unsigned n = sh.tot_cnt[bin];
     above = sh.before;
-    if (b0 < 0) {
-      b0 = bin;
-    } else {
+    if (level == 0) b0 = bin;
+    else if (level == 1) b1 = bin;
+    else {
       hi -= (u64)bin << shift;
       const u64 width = (1ull << shift) - 1;
       if (hi - lo > width) lo = hi - width;
     }
+    n = collect<Tin>(cluster, sh, row, [&](float x, int i) { return candidate(x, i, level + 1); });
     if (n <= kList) break;
-    // too many to rank: split the interval by codes
-    if (b0 == bin && hi == ~0ull) {
-      lo = 0;
-      hi = (1ull << (32 + kIndexBits)) - 1;
+    ++level;
+    if (level >= 2) {  // by codes
+      shift = 64 - __clzll((long long)(hi - lo)) - 10;  // hi - lo < 2^(shift + 10), kBins intervals of 2^shift
+      if (shift < 0) shift = 0;
     }
-    shift = 64 - __clzll((long long)(hi - lo)) - 10;  // hi - lo < 2^(shift + 10), kBins intervals of 2^shift
-    if (shift < 0) shift = 0;
-    __syncthreads();
+    __syncthreads();  // (sh.listed has been read)
   }
-  // the candidates, in every CTA's list
-  for (int i = row.lo + lane; i < row.hi; i += 32) {
-    const float x = row.x[i];
-    const u64 code = code_of(x, row.base + i);
-    if (code < row.floor || first_bin(x) != b0 || code < lo || code > hi) continue;
-    const u64 w = weigh(x);
-    for (int q = 0; q < C; ++q) {
-      const int at = atomicAdd(cluster.map_shared_rank(&sh.listed, q), 1);
-      if (at < kList) {
-        *cluster.map_shared_rank(&sh.list_code[at], q) = code;
-        *cluster.map_shared_rank(&sh.list_w[at], q) = w;
-      }
-    }
-  }
-  cluster.sync();
-  const int n = min(sh.listed, kList);
   for (int i = tid; i < n; i += kThreads) {
-    const u64 code = sh.list_code[i], w = sh.list_w[i];
+    const u64 code = sh.list_code[i], w = kMass ? sh.list_w[i] : 1;
     u64 before = above;
-    for (int j = 0; j < n; ++j) before += sh.list_code[j] > code ? sh.list_w[j] : 0;
+    for (int j = 0; j < n; ++j) before += sh.list_code[j] > code ? (kMass ? sh.list_w[j] : 1) : 0;
     if (before < target && target <= before + w) {
       sh.code = code;
       sh.upto = before + w;
     }
   }
   __syncthreads();
-  row.floor = sh.code;
+  row.set(sh.code);
   const u64 kept = sh.upto;
   __syncthreads();
   return kept;
 }
 
-template <typename Tin>
-__device__ __forceinline__ void load_part(const Tin* src, float* dst, int lo, int hi, int valid, int lane, float* mx, float* mn,
-                                          bool* bad) {
-  constexpr int kAhead = 8;
-  for (int i0 = lo; i0 < hi; i0 += 32 * kAhead) {
-    float v[kAhead];
+// Sum over the CTA, in every thread.
+__device__ __forceinline__ u64 block_sum64(Shared& sh, u64 v) {
+  v = warp_sum64(v);
+  if ((threadIdx.x & 31) == 0) sh.warp_mass[threadIdx.x >> 5] = v;
+  __syncthreads();
+  u64 sum = 0;
+  for (int q = 0; q < kWarps; ++q) sum += sh.warp_mass[q];
+  __syncthreads();
+  return sum;
+}
+
+// All filters and the draw among the n tokens of the list, which hold the first k of the row.
+// Sets the row's threshold, returns the mass kept and the token drawn (by rank 0's CTA).
+__device__ __forceinline__ u64 small_row(Shared& sh, Row& row, int n, int k, float p, const float* u, int32_t* token) {
+  const int tid = threadIdx.x;
+  constexpr int kPer = kList / kThreads;
+  u64 code[kPer], w[kPer], before[kPer], sum = 0;
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      const int i = i0 + 32 * k + lane;
-      v[k] = i < valid && i < hi ? to_f32(src[i]) : -INFINITY;
+  for (int e = 0; e < kPer; ++e) {
+    const int i = tid + e * kThreads;
+    code[e] = w[e] = before[e] = 0;
+    if (i >= n) continue;
+    code[e] = sh.list_code[i];
+    w[e] = sh.list_w[i];
+    int rank = 0;
+    for (int j = 0; j < n; ++j)
+      if (sh.list_code[j] > code[e]) {
+        ++rank;
+        before[e] += sh.list_w[j];
+      }
+    if (rank >= k) code[e] = w[e] = 0;
+    sum += w[e];
+  }
+  u64 whole = block_sum64(sh, sum);
+  if (p < 1.f) {
+    const u64 target = wanted(p, whole);
+    sum = 0;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      if (before[e] >= target) code[e] = w[e] = 0;
+      sum += w[e];
     }
+    whole = block_sum64(sh, sum);
+  }
+  // the threshold: the least code kept
+  u64 least = ~0ull;
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      const int i = i0 + 32 * k + lane;
-      if (i < hi) dst[i] = v[k];
-      *mx = fmaxf(*mx, v[k]);
-      if (v[k] > -INFINITY) *mn = fminf(*mn, v[k]);
-      *bad = *bad || !(v[k] < INFINITY);
+  for (int e = 0; e < kPer; ++e)
+    if (code[e] && code[e] < least) least = code[e];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const u64 other = __shfl_xor_sync(0xffffffffu, least, o);
+    least = other < least ? other : least;
+  }
+  if ((tid & 31) == 0) sh.warp_mass[tid >> 5] = least;
+#pragma unroll
+  for (int e = 0; e < kPer; ++e)
+    if (tid + e * kThreads < n) sh.list_w[tid + e * kThreads] = w[e];
+  __syncthreads();
+  for (int q = 0; q < kWarps; ++q) least = sh.warp_mass[q] < least ? sh.warp_mass[q] : least;
+  row.set(least);
+  if (token) {
+    const u64 t = drawn(*u, whole);
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      if (!w[e]) continue;
+      const u64 place = kIndexMask - (code[e] & kIndexMask);
+      u64 run = 0;
+      for (int j = 0; j < n; ++j) run += kIndexMask - (sh.list_code[j] & kIndexMask) < place ? sh.list_w[j] : 0;
+      if (run <= t && t < run + w[e]) *token = (int32_t)place;
     }
   }
+  return whole;
+}
+
+// The part's elements into shared memory: whole 16-byte units by asynchronous copies, the
+// units at the row's ends element by element, -inf outside the row.  Elements
+// [head, head + V) of the padded row, whose element 0 lies at the 16-byte boundary `src`.
+template <typename Tin>
+__device__ __forceinline__ void load_part(const Tin* src, unsigned char* dst, long long start, int lo, int hi, int head, int V) {
+  constexpr int kN = Vec<Tin>::kN;
+  for (int i = lo + kN * (int)(threadIdx.x & 31); i < hi; i += 32 * kN) {
+    const long long at = start + i;
+    if (at >= head && at + kN <= (long long)head + V) {
+      const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst + (size_t)i * sizeof(Tin)));
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src + at) : "memory");
+    } else {
+      Tin* out = reinterpret_cast<Tin*>(dst) + i;
+#pragma unroll
+      for (int j = 0; j < kN; ++j)
+        out[j] = at + j >= head && at + j < (long long)head + V ? src[at + j] : static_cast<Tin>(-INFINITY);
+    }
+  }
+  asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
 }
 
 template <typename Tin>
-__global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a, int part) {
-  extern __shared__ __align__(16) float x_sh[];
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a, int part) {
+  constexpr int kN = Vec<Tin>::kN;
+  extern __shared__ __align__(16) unsigned char part_sh[];
   __shared__ Shared sh;
   cg::cluster_group cluster = cg::this_cluster();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int r = blockIdx.x / C, b = r / a.N, node = r % a.N;
   const int set = a.per_row ? r : b;  // the row's settings
+  auto started = cluster.barrier_arrive();  // (the others' shared memory may be written once they run)
+
+  Row row;
+  row.part = part_sh;
+  row.lo = warp * (part / kWarps);
+  row.hi = row.lo + part / kWarps;
+  const Tin* src = static_cast<const Tin*>(a.logits) + (long long)b * a.l_batch + (long long)node * a.l_row;
+  const int head = (int)((reinterpret_cast<uintptr_t>(src) & 15) / sizeof(Tin));
+  row.base = rank * part - head;
+  load_part<Tin>(src - head, part_sh, (long long)rank * part, row.lo, row.hi, head, a.V);
   float heat = a.temperature ? a.temperature[set] : 1.f;
   int k = a.top_k ? a.top_k[set] : 0;
   const float p = a.top_p ? a.top_p[set] : 1.f, least = a.min_p ? a.min_p[set] : 0.f;
-
-  Row row;
-  row.x = x_sh;
-  row.base = rank * part;
-  row.lo = warp * (part / kWarps);
-  row.hi = row.lo + part / kWarps;
-  if (tid < 256) sh.table[tid] = make_float2(kTable.hi[tid], kTable.lo[tid]);
-  if (tid == 0) sh.warp_bad = 0;
-  __syncthreads();
-  const Tin* src = static_cast<const Tin*>(a.logits) + (long long)b * a.l_batch + (long long)node * a.l_row + row.base;
-  float mx = -INFINITY, mn = INFINITY;
-  bool bad = false;
-  load_part(src, x_sh, row.lo, row.hi, min(a.V - row.base, part), lane, &mx, &mn, &bad);
-  mx = warp_max(mx);
-  mn = -warp_max(-mn);
-  if (__any_sync(0xffffffffu, bad) && lane == 0) sh.warp_bad = 1;
+  if (tid < 256) sh.table[tid] = *reinterpret_cast<const float2*>(kTable.v[tid]);
+  if (heat == 0.f) {
+    heat = 1.f;
+    k = 1;
+  }
+  // the row's constants in double, one thread each: all 512 at the rate of that pipe take 5 us
+  if (tid == 0) {
+    const double c = fmin(256.0 * 1.4426950408889634 / (double)heat, 1e36);  // (T below 4e-34 acts as that)
+    sh.heat = make_float2((float)c, (float)(c - (double)(float)c));
+  }
+  if (tid == 32 && least > 0.f) sh.least = (double)heat * log(fmin((double)least, 1.0));
+  // the thread's, the CTA's and the row's largest value (NaN if one is) and smallest
+  typename Vec<Tin>::Extremes extremes;
+  for (int i = row.lo + kN * lane; i < row.hi; i += 32 * kN)
+    extremes.add(*reinterpret_cast<const uint4*>(part_sh + (size_t)i * sizeof(Tin)));
+  float mx = extremes.max(), mn = extremes.min();
+  const float own = mx;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+  }
   if (lane == 0) {
     sh.warp_max[warp] = mx;
     sh.warp_min[warp] = mn;
   }
   __syncthreads();
+  cluster.barrier_wait(std::move(started));
   if (warp == 0) {
-    mx = warp_max(lane < kWarps ? sh.warp_max[lane] : -INFINITY);
-    mn = -warp_max(lane < kWarps ? -sh.warp_min[lane] : -INFINITY);
+    mx = lane < kWarps ? sh.warp_max[lane] : -INFINITY;
+    mn = lane < kWarps ? sh.warp_min[lane] : INFINITY;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+    }
     if (lane < C) {
       *cluster.map_shared_rank(&sh.max[rank], lane) = mx;
       *cluster.map_shared_rank(&sh.min[rank], lane) = mn;
-      *cluster.map_shared_rank(&sh.bad[rank], lane) = sh.warp_bad;
     }
   }
   cluster.sync();
-  row.max = sh.max[0];
+  mx = sh.max[0];
   mn = sh.min[0];
-  bad = sh.bad[0] != 0;
   for (int q = 1; q < C; ++q) {
-    row.max = fmaxf(row.max, sh.max[q]);
+    mx = max_nan(mx, sh.max[q]);
     mn = fminf(mn, sh.min[q]);
-    bad = bad || sh.bad[q] != 0;
   }
+  // elements [from, to) of the part are the row's
+  const int from = max(0, -row.base), to = (int)min((long long)part, (long long)a.V - row.base);
   float* out = a.probs ? a.probs + (long long)b * a.p_batch + (long long)node * a.p_row + row.base : nullptr;
-  const int valid = min(a.V - row.base, part);  // (below 1 for a CTA past the end)
   // no finite maximum, NaN or +inf among the logits, or settings that mean nothing
-  if (bad || !(row.max > -INFINITY) || !(heat >= 0.f && heat < INFINITY) || p != p || least != least) {
+  if (!(mx > -INFINITY && mx < INFINITY) || !(heat >= 0.f && heat < INFINITY) || p != p || least != least) {
     if (rank == 0 && tid == 0) {
       raise_flag(a.flags, MLA_DEV_BAD_VALUE);
       if (a.token) a.token[r] = -1;
     }
     if (out)
-      for (int i = row.lo + lane; i < min(row.hi, valid); i += 32) out[i] = qnan();
+      for (int i = max(row.lo, from) + lane; i < min(row.hi, to); i += 32) out[i] = qnan();
     return;
   }
-  if (heat == 0.f) {
-    heat = 1.f;
-    k = 1;
+  row.heat = make_heat(mx, sh.heat);
+  row.thr = -INFINITY;
+  row.last = INT_MIN;
+  if (least > 0.f) {  // w >= least, as a bound of x
+    row.thr = __double2float_ru((double)mx + sh.least);
+    row.last = INT_MAX;
   }
-  const double c = fmin(256.0 * 1.4426950408889634 / (double)heat, 1e36);  // (T below 4e-34 acts as that)
-  row.heat.hi = (float)c;
-  row.heat.lo = (float)(c - (double)row.heat.hi);
-  row.floor = (u64)0x00800000u << kIndexBits;  // above -inf
-  if (least > 0.f) {
-    const double t = (double)row.max + (double)heat * log(fmin((double)least, 1.0));
-    const u64 f = (u64)ordered_key(__double2float_ru(t)) << kIndexBits;
-    if (f > row.floor) row.floor = f;
-  }
-  const float spread = row.max - mn;
-  if (k > 0 && k < a.V) select<false>(cluster, sh, row, fminf(spread, 40.f * heat), (u64)k, 0.f);
+  const float spread = mx - mn;
   u64 total = 0;
-  if (p < 1.f) {
+  bool done = false;  // token and total are known
+  if (k == 1) {       // the first token of the order
+    int first = INT_MAX;
+    for_each<Tin>(row, [&](const auto& x, int i) {
+#pragma unroll
+      for (int j = kN - 1; j >= 0; --j)
+        if (x[j] == mx) first = min(first, row.base + i + j);
+    });
+    first = __reduce_min_sync(0xffffffffu, first);
+    if (lane == 0) sh.warp_first[warp] = first;
+    __syncthreads();
+    if (warp == 0) {
+      first = __reduce_min_sync(0xffffffffu, lane < kWarps ? sh.warp_first[lane] : INT_MAX);
+      if (lane < C) *cluster.map_shared_rank(&sh.first[rank], lane) = first;
+    }
+    cluster.sync();
+    first = sh.first[0];
+    for (int q = 1; q < C; ++q) first = min(first, sh.first[q]);
+    row.thr = mx;
+    row.last = first;
+    total = weight(mx, row.heat, sh.table);
+    if (a.token && rank == 0 && tid == 0) a.token[r] = first;
+    done = true;
+  } else if (k > 0 && k < a.V) {
+    const float range = fminf(spread, 64.f);
+    bool few = k <= kSmallK;
+    if (few) {
+      // the k-th of the threads' largest tokens lies in interval b0: no token of the first k lies behind it
+      const Bins bins(mx, range);
+      clear_bins(sh);
+      const int bin = Bins::index(bins.at(own));
+      const bool there = own > row.thr || (own == row.thr && row.last == INT_MAX);
+      const unsigned same = __ballot_sync(0xffffffffu, there && bin == kBins - 1);
+      if (there && bin < kBins - 1) atomicAdd(&sh.cnt[bin], 1u);
+      if (lane == 0 && same) atomicAdd(&sh.cnt[kBins - 1], (unsigned)__popc(same));
+      sum_bins<false>(cluster, sh);
+      find_bin(sh, 0, [&](u64) { return (u64)k; });
+      const int b0 = sh.bin;
+      const int n = collect<Tin>(cluster, sh, row, [&](float x, int) { return Bins::index(bins.at(x)) <= b0; });
+      few = n <= kList;
+      if (few) {
+        total = small_row(sh, row, n, k, p, a.token ? a.u + r : nullptr, a.token && rank == 0 ? a.token + r : nullptr);
+        done = true;
+      } else {
+        __syncthreads();  // (sh.listed has been read)
+      }
+    }
+    if (!few) select<Tin, false>(cluster, sh, row, range, [&](u64) { return (u64)k; });
+  }
+  if (!done && p < 1.f) {
     // tokens past this range hold less than 1 - p of the mass, whatever their number
     const float tail = logf((float)a.V) - logf(fmaxf(1.f - p, 1e-7f)) + 1.f;
-    total = select<true>(cluster, sh, row, fminf(spread, tail * heat), 0, fmaxf(p, 0.f));
+    total = select<Tin, true>(cluster, sh, row, fminf(spread, tail * heat), [&](u64 whole) { return wanted(p, whole); });
   }
-  if (a.token || p >= 1.f) {
+  if (!done && (a.token || p >= 1.f)) {
     u64 mine = 0;
-    for (int i = row.lo + lane; i < row.hi; i += 32) {
-      const float x = x_sh[i];
-      if (code_of(x, row.base + i) >= row.floor) mine += weight(x, row.max, row.heat, sh.table);
-    }
+    const Bounds<kN> bounds(row, true);
+    for_each<Tin>(row, [&](const auto& x, int i) {
+      bool in[kN];
+      bounds.test(x, i, in);
+#pragma unroll
+      for (int j = 0; j < kN; ++j) {
+        if (!__any_sync(0xffffffffu, in[j])) continue;
+        const u64 w = weight(x[j], row.heat, sh.table);
+        if (in[j]) mine += w;
+      }
+    });
     mine = warp_sum64(mine);
     if (lane == 0) sh.warp_mass[warp] = mine;
     __syncthreads();
@@ -449,40 +796,58 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a, in
     cluster.sync();
     total = 0;
     for (int q = 0; q < C; ++q) total += sh.mass[q];
-  }
-  if (a.token) {
-    // the CTA, the warp, the element at which the running mass exceeds t < total
-    bool cut;
-    const float u = a.u[r];
-    u64 t = u >= 1.f ? total - 1 : u > 0.f ? fraction_of(u, total, &cut) : 0;
-    for (int q = 0; q < rank; ++q) t -= sh.mass[q];  // (wraps where the draw is before this CTA)
-    if (t < sh.mass[rank]) {
-      int w = 0;
-      while (t >= sh.warp_mass[w]) t -= sh.warp_mass[w++];
-      if (w == warp) {
-        for (int i0 = row.lo; i0 < row.hi; i0 += 32) {
-          const float x = x_sh[i0 + lane];
-          const u64 v = code_of(x, row.base + i0 + lane) >= row.floor ? weight(x, row.max, row.heat, sh.table) : 0;
-          const u64 incl = warp_scan64(v);
-          const unsigned over = __ballot_sync(0xffffffffu, incl > t);
-          if (over) {
-            if (lane == 0) a.token[r] = row.base + i0 + __ffs(over) - 1;
-            break;
+    if (a.token) {
+      // the CTA, the warp, the element at which the running mass exceeds t < total
+      u64 t = drawn(a.u[r], total);
+      for (int q = 0; q < rank; ++q) t -= sh.mass[q];  // (wraps where the draw is before this CTA)
+      if (t < sh.mass[rank]) {
+        int w = 0;
+        while (t >= sh.warp_mass[w]) t -= sh.warp_mass[w++];
+        if (w == warp) {
+          for (int i0 = row.lo; i0 < row.hi; i0 += 32 * kN) {
+            const int i = i0 + kN * lane;
+            float x[kN];
+            Vec<Tin>::get(*reinterpret_cast<const uint4*>(part_sh + (size_t)i * sizeof(Tin)), x);
+            bool in[kN];
+            bounds.test(x, i, in);
+            u64 v[kN], sum = 0;
+#pragma unroll
+            for (int j = 0; j < kN; ++j) sum += v[j] = in[j] ? weight(x[j], row.heat, sh.table) : 0;
+            const u64 incl = warp_scan64(sum);
+            const unsigned over = __ballot_sync(0xffffffffu, incl > t);
+            if (over) {
+              if (lane == __ffs(over) - 1) {
+                u64 run = incl - sum;
+                int at = -1;
+#pragma unroll
+                for (int j = 0; j < kN; ++j) {
+                  run += v[j];
+                  if (at < 0 && run > t) at = j;
+                }
+                a.token[r] = row.base + i + at;
+              }
+              break;
+            }
+            t -= __shfl_sync(0xffffffffu, incl, 31);
           }
-          t -= __shfl_sync(0xffffffffu, incl, 31);
         }
       }
     }
   }
   if (out) {
-    const float inv = (float)((double)(1ull << kOne) / (double)total);
-    for (int i = row.lo + lane; i < min(row.hi, valid); i += 32) {
-      const float x = x_sh[i];
+    const float inv = (float)(1ull << kOne) / __ull2float_rn(total);
+    const Tin* x_sh = reinterpret_cast<const Tin*>(part_sh);
+    // down to 2^-160: smaller ones are 0 in fp32 (the loop's first bound on |x c| holds there too)
+    const float tiny = row.heat.least - (256.f * 160.f - kNegligible) / row.heat.hi;
+    for (int i = max(row.lo, from) + lane; i < min(row.hi, to); i += 32) {
+      const float x = to_f32(x_sh[i]);
       float v = 0.f;
-      Parts w;
-      if (code_of(x, row.base + i) >= row.floor && weight_parts(x, row.max, row.heat, sh.table, 256.f * 160.f, &w)) {
-        const int n0 = w.n >> 1;  // two factors of 2: n may pass the exponent's range
-        v = (w.hi + w.lo) * inv * __int_as_float((127 - n0) << 23) * __int_as_float((127 - (w.n - n0)) << 23);
+      if (row.kept(x, i) && x >= tiny) {
+        const Parts w = weight_parts(x, row.heat, sh.table);
+        const int n = min(w.n, 250), n0 = n >> 1;  // two factors of 2: n may pass the exponent's range
+        v = k == 1 ? 1.f
+                   : fmaf(w.lo, 9.094947017729282e-13f, w.hi) * inv * __int_as_float((127 - n0) << 23) *
+                         __int_as_float((127 - (n - n0)) << 23);
       }
       out[i] = v;
     }
@@ -503,15 +868,17 @@ cudaError_t launch(const SampleArgs& a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     done.fetch_or(bit);
   }
+  constexpr int kN = Vec<Tin>::kN, kUnit = kThreads * kN;
   const long long rows = (long long)a.B * a.N;
+  const int padded = a.V + kN - 1;
   int C = 1;
-  while (C < kCluster && (a.V + C - 1) / C > 16384) C *= 2;
-  while (C < kCluster && rows * C * 2 <= sms && a.V / C > 2048) C *= 2;
-  const int part = ((a.V + C - 1) / C + kThreads - 1) / kThreads * kThreads;
+  while (C < kCluster && (padded + C - 1) / C * (int)sizeof(Tin) > 73728) C *= 2;
+  while (C < kCluster && rows * C * 2 <= sms && padded / C > 2048) C *= 2;
+  const int part = ((padded + C - 1) / C + kUnit - 1) / kUnit * kUnit;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(rows * C));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = (size_t)part * sizeof(float);
+  cfg.dynamicSmemBytes = (size_t)part * sizeof(Tin);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;

@@ -1,9 +1,9 @@
 """GPU parity of the sampling calls against the long-double oracle.
 
-Tolerances.  A weight is off by at most 2^-33 of itself plus 2^-45 of the
-largest, so a compared sum by at most 2^-32 of the mass: a token, or the border
-of the kept set, may differ from the oracle's only where its comparison lies
-closer than that (the cases below are drawn, and none is known to).  A
+Tolerances.  A weight is off by 2^-31 of itself at most (four fp32 roundings of
+an exponent whose unit is ln(2)/256) plus 2^-45 of the largest, so that a token, or
+the border of the kept set, may differ from the oracle's only where its comparison
+lies closer than that: 2^-32 is allowed for sums, whose errors average.  A
 probability is a product of two factors each rounded once or twice to fp32 and
 a quotient's rounding: 4 * 2^-24 of itself, and it may be flushed below 2^-126.
 """
