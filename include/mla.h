@@ -579,7 +579,7 @@ int mla_tree_commit_paged(int n, void* const* cache, const int* row_bytes, int B
  *   token   the least i whose cumulative w, over the kept tokens in index
  *           order, exceeds u times their mass (u below 0 or NaN counts as 0, u
  *           of 1 or more as just below 1)
- *   probs   w[i] / mass for the kept tokens, 0 for the others
+ *   probs   w[i] / mass for the kept tokens, 0 for the others (and for a w below 2^-126)
  * A logit of -inf is never kept.  A row without a finite logit, with a NaN or
  * +inf, or with a setting that is NaN or a temperature that is negative or
  * infinite raises MLA_DEV_BAD_VALUE and gives token -1 and NaN probabilities.

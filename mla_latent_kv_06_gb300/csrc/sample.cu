@@ -17,12 +17,20 @@
 // The draw is the least index whose cumulative kept mass exceeds u W.
 //
 // Rounding.  A threshold and a draw compare sums over the vocabulary, so a
-// weight is a 64-bit integer, w 2^45 cut to an odd number (an error of one unit
-// without a bias): sums are then exact, in any order, and the kernel's atomics
-// cannot change a result.  The exponential is taken without the fp64 pipe (1/64 of
-// the fp32 rate): 256 log2(e) x / T as an integer and a rest to 2^-25, from fused
-// multiply-adds whose products are exact; a table of 2^(-i/256) in 48 bits and a
-// cubic for the rest, error below 2^-31 of the weight (rms 2^-34).
+// weight is an integer, w 2^44 rounded once: sums are then exact, in any order,
+// and the kernel's atomics cannot change a result.  The exponential is taken
+// without the fp64 pipe (1/64 of the fp32 rate) and without 64-bit shifts:
+//   z = x c rounded to an integer, c = 256 log2(e) / T, r = z - x c by two fused
+//   multiply-adds whose products are exact; k = top - z with top >= max c, so that
+//   w = 2^(-k/256) 2^(-r/256);
+//   a table of 2^(-i/256) as hi (1 + d) for the low 8 bits of k, the others moved into
+//   hi's exponent by one multiply-add (the table's entry holds i times that step, too);
+//   a cubic for 2^(-r/256) + d, whose product with hi is the weight's low part;
+//   the two parts added to 6 and to 1.5 2^-21, whose last places are 2^-21 and 2^-44:
+//   the integers are then in the sums' bits, and are added up as such.
+// The error is below 2^-31 of the weight (rms 2^-34) before the rounding.  Two
+// elements go through packed fp32 instructions; 71 instructions an element with
+// 64-bit integers, conversions and one element at a time.
 //
 // A row is a cluster of up to 8 CTAs, each with a contiguous part of the
 // vocabulary in shared memory, read once, 16 bytes at a time from 16-byte
@@ -50,15 +58,16 @@ constexpr int kCluster = 8;  // most CTAs of a row
 constexpr int kList = 1024;  // tokens that are ranked against each other
 constexpr int kOwn = 768;    // most of them from one CTA
 constexpr int kSmallK = 512;  // top-k by the threads' largest tokens
-constexpr int kOne = 45;     // a weight of 1 is 2^kOne; kMaxSampleVocab of them stay below 2^64
+constexpr int kOne = 44;     // a weight of 1 is 2^kOne; kMaxSampleVocab of them stay below 2^63
 constexpr int kIndexBits = 20;
 constexpr u64 kIndexMask = (1ull << kIndexBits) - 1;
 constexpr float kNegligible = 256.f * (kOne + 2);  // 256 log2 of a weight that rounds to 0
-static_assert(kMaxSampleVocab < (1 << 18) + (1 << 17), "sums of weights stay below 2^64, indices below 2^kIndexBits");
+static_assert(kMaxSampleVocab < (1 << 18) + (1 << 17), "sums of weights stay below 2^63, indices below 2^kIndexBits");
 
-// 2^(-i/256) as hi + lo, hi < 1 of 24 bits; lo times 2^40.
+// 2^(-i/256) = hi (1 + d), hi < 1 of 24 bits; hi's bits plus i 2^15 (the exponent's unit is 256 2^15).
 struct ExpTable {
-  float v[256][2];
+  int hi[256];
+  float d[256];
 };
 constexpr ExpTable make_table() {
   ExpTable t{};
@@ -69,10 +78,10 @@ constexpr ExpTable make_table() {
       term *= y / n;
       sum += term;
     }
-    const long long scaled = (long long)(sum * 16777216.0);
+    const long long scaled = (long long)(sum * 16777216.0);  // from 2^23 up
     const long long top = scaled < 16777216 ? scaled : 16777215;
-    t.v[i][0] = (float)((double)top / 16777216.0);
-    t.v[i][1] = (float)((sum - (double)top / 16777216.0) * 1099511627776.0);
+    t.hi[i] = 0x3f000000 + (int)(top - 8388608) + (i << 15);
+    t.d[i] = (float)(sum / ((double)top / 16777216.0) - 1.0);
   }
   return t;
 }
@@ -89,7 +98,7 @@ struct Shared {
   };
   u64 tot[kBins];                             // the cluster's, written by all CTAs
   u64 list_code[kList], list_w[kList];
-  float2 table[256];
+  int2 table[256];   // (hi, d's bits)
   float2 heat;       // c as a pair
   double least;      // T log(min_p)
   float max[kCluster], min[kCluster];
@@ -125,7 +134,7 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
-// With c = 256 log2(e) / T = hi + lo, 256 log2 of a weight is x c - top, top being max c
+// c = 256 log2(e) / T = hi + lo.  256 log2 of a weight is x c - top, top being max c
 // rounded up to an integer (the common factor cancels wherever weights are used).  Where
 // max c is too large for that (not fast), it is (x - max) c, with x - max by two-sum.
 // Logits below `least` have no weight.
@@ -146,41 +155,95 @@ __device__ __forceinline__ Heat make_heat(float max, float2 c) {
   return h;
 }
 
-constexpr int kMagicBits = 0x4B400000;
-constexpr float kMagic = 12582912.f;  // 1.5 2^23: adding it rounds to an integer, in the low bits
-
-// A weight as (hi + lo 2^-40) 2^-n.  x from `least` up, or a little below: |x c| < 2^22.
-struct Parts {
-  float hi, lo;
-  int n;
+// Two floats in packed instructions.
+struct Two {
+  u64 v;
+  __device__ __forceinline__ Two() {}
+  __device__ __forceinline__ Two(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
+  __device__ __forceinline__ void get(float* a, float* b) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(*a), "=f"(*b) : "l"(v)); }
 };
-__device__ __forceinline__ Parts weight_parts(float x, const Heat& h, const float2* table) {
-  float r;
-  int k;
-  if (h.fast) {
-    const float z = fmaf(x, h.hi, kMagic);  // x c as an integer ...
-    r = fmaf(-x, h.lo, fmaf(-x, h.hi, z - kMagic));  // ... less x c: the products are exact
-    k = h.top + kMagicBits - __float_as_int(z);
-  } else {
-    const float d = h.max - x, b = d - h.max, dl = (h.max - (d - b)) + (-x - b);
-    const float z = fmaf(d, h.hi, kMagic);
-    r = fmaf(d, h.hi, -(z - kMagic)) + fmaf(d, h.lo, dl * h.hi);
-    k = __float_as_int(z) - kMagicBits;
-  }
-  const float2 t = table[k & 255];
-  // (exp(-r ln(2) / 256) - 1) 2^40, |r| < 0.7: below 2^31
-  constexpr float kStep = -0.0027076061740622863f, kUnit = 1099511627776.f;
-  const float q = r * fmaf(r, fmaf(r, kStep * kStep * kStep / 6.f * kUnit, kStep * kStep / 2.f * kUnit), kStep * kUnit);
-  return Parts{t.x, fmaf(t.x, q, t.y), k >> 8};
+__device__ __forceinline__ Two both(float a) { return Two(a, a); }
+__device__ __forceinline__ Two operator+(Two a, Two b) {
+  Two r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ Two operator-(Two a, Two b) {
+  Two r;
+  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ Two operator*(Two a, Two b) {
+  Two r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ Two fma(Two a, Two b, Two c) {
+  Two r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
 }
 
-// For x >= least.
-__device__ __forceinline__ u64 weight(float x, const Heat& h, const float2* table) {
-  const Parts p = weight_parts(x, h, table);
-  // hi < 1 has exponent -1: 24 bits with the hidden one.  |lo| < 2^31.
-  const u64 a = (u64)((__float_as_uint(p.hi) & 0x7fffffu) | 0x800000u) << (kOne - 24);
-  const long long c = (long long)__float2int_rn(p.lo) * (1ll << (kOne - 40));
-  return ((a + (u64)c) >> min((unsigned)p.n, 63u)) | 1;
+constexpr int kMagicBits = 0x4B400000;
+constexpr float kMagic = 12582912.f;  // 1.5 2^23: adding it rounds to an integer, in the low bits
+// Adding these rounds to multiples of 2^-21 and 2^-44.
+constexpr float kHigh = 6.f, kLow = 1.5f / 2097152.f;
+constexpr int kHighBits = 0x40C00000, kLowBits = 0x35400000;
+constexpr int kHighShift = kOne - 21;
+
+// Weights of two logits as hi + lo, hi the rounded sum, below 2^-45 (which rounds to 0) where
+// not in.  x from 2^-kTiny up, |x c| < 2^22.
+constexpr int kTiny = 126;
+__device__ __forceinline__ void weights(float x0, float x1, bool in0, bool in1, const Heat& h, const int2* table, Two* hi, Two* lo) {
+  Two r;
+  int k0, k1;
+  if (h.fast) {  // `least` itself is 2^-46
+    x0 = in0 ? x0 : h.least;
+    x1 = in1 ? x1 : h.least;
+    const Two x(x0, x1), n(-x0, -x1);
+    const Two z = fma(x, both(h.hi), both(kMagic));
+    r = fma(n, both(h.lo), fma(n, both(h.hi), z - both(kMagic)));
+    float a, b;
+    z.get(&a, &b);
+    k0 = h.top + kMagicBits - __float_as_int(a);
+    k1 = h.top + kMagicBits - __float_as_int(b);
+  } else {
+    const Two x(in0 ? x0 : h.max, in1 ? x1 : h.max), d = both(h.max) - x, b = d - both(h.max), dl = (both(h.max) - (d - b)) - (x + b);
+    const Two z = fma(d, both(h.hi), both(kMagic));
+    r = (fma(d, both(h.hi), both(kMagic) - z)) + fma(d, both(h.lo), dl * both(h.hi));
+    float a, c;
+    z.get(&a, &c);
+    k0 = in0 ? min(__float_as_int(a) - kMagicBits, kTiny * 256) : kTiny * 256;
+    k1 = in1 ? min(__float_as_int(c) - kMagicBits, kTiny * 256) : kTiny * 256;
+  }
+  const int2 t0 = table[k0 & 255], t1 = table[k1 & 255];
+  constexpr float kStep = -0.0027076061740622863f;  // -ln(2) / 256
+  const Two q = fma(r, fma(r, fma(r, both(kStep * kStep * kStep / 6.f), both(kStep * kStep / 2.f)), both(kStep)),
+                    Two(__int_as_float(t0.y), __int_as_float(t1.y)));
+  const Two w(__int_as_float(t0.x - k0 * 32768), __int_as_float(t1.x - k1 * 32768));
+  const Two l = w * q, s = w + l;
+  *hi = s;
+  *lo = l - (s - w);
+}
+
+// The integers of two weights, w 2^44 = (a - kHighBits) 2^23 + (b - kLowBits).
+struct Units {
+  int a[2], b[2];
+};
+__device__ __forceinline__ Units units(float x0, float x1, bool in0, bool in1, const Heat& h, const int2* table) {
+  Two hi, lo;
+  weights(x0, x1, in0, in1, h, table, &hi, &lo);
+  const Two z = hi + both(kHigh), y = ((hi - (z - both(kHigh))) + lo) + both(kLow);
+  float a, b, c, d;
+  z.get(&a, &b);
+  y.get(&c, &d);
+  return Units{{__float_as_int(a), __float_as_int(b)}, {__float_as_int(c), __float_as_int(d)}};
+}
+__device__ __forceinline__ u64 weight_of(const Units& u, int j) {
+  return ((u64)(unsigned)(u.a[j] - kHighBits) << kHighShift) + (u64)(long long)(u.b[j] - kLowBits);
+}
+__device__ __forceinline__ u64 weight(float x, const Heat& h, const int2* table) {  // x >= least
+  return weight_of(units(x, x, true, true, h, table), 0);
 }
 
 __device__ __forceinline__ u64 code_of(float x, int index) {
@@ -473,14 +536,21 @@ __device__ __forceinline__ u64 select(cg::cluster_group& cluster, Shared& sh, Ro
       bool in[kN];
       bounds.test(x, i, in);
 #pragma unroll
-      for (int j = 0; j < kN; ++j) {
-        if (!__any_sync(0xffffffffu, in[j])) continue;
-        const u64 w = kMass ? weight(x[j], row.heat, sh.table) : 1;
-        if (!in[j] || !candidate(x[j], i + j, level)) continue;
-        const int bin = place(x[j], i + j);
-        if (bin == kBins - 1) last += w;
-        else if (kMass) add_mass(sh, bin, w);
-        else atomicAdd(&sh.cnt[bin], 1u);
+      for (int j = 0; j < kN; j += 2) {
+        in[j] = in[j] && candidate(x[j], i + j, level);
+        in[j + 1] = in[j + 1] && candidate(x[j + 1], i + j + 1, level);
+        if (!__any_sync(0xffffffffu, in[j] || in[j + 1])) continue;
+        Units w;
+        if (kMass) w = units(x[j], x[j + 1], in[j], in[j + 1], row.heat, sh.table);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          if (!in[j + e]) continue;
+          const u64 m = kMass ? weight_of(w, e) : 1;
+          const int bin = place(x[j + e], i + j + e);
+          if (bin == kBins - 1) last += m;
+          else if (kMass) add_mass(sh, bin, m);
+          else atomicAdd(&sh.cnt[bin], 1u);
+        }
       }
     });
     last = warp_sum64(last);
@@ -649,14 +719,15 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
   float heat = a.temperature ? a.temperature[set] : 1.f;
   int k = a.top_k ? a.top_k[set] : 0;
   const float p = a.top_p ? a.top_p[set] : 1.f, least = a.min_p ? a.min_p[set] : 0.f;
-  if (tid < 256) sh.table[tid] = *reinterpret_cast<const float2*>(kTable.v[tid]);
+  if (tid < 256) sh.table[tid] = make_int2(kTable.hi[tid], __float_as_int(kTable.d[tid]));
   if (heat == 0.f) {
     heat = 1.f;
     k = 1;
   }
   // the row's constants in double, one thread each: all 512 at the rate of that pipe take 5 us
   if (tid == 0) {
-    const double c = fmin(256.0 * 1.4426950408889634 / (double)heat, 1e36);  // (T below 4e-34 acts as that)
+    // (temperatures outside 4e-34 .. 3e35 act as these)
+    const double c = fmin(fmax(256.0 * 1.4426950408889634 / (double)heat, 1e-33), 1e36);
     sh.heat = make_float2((float)c, (float)(c - (double)(float)c));
   }
   if (tid == 32 && least > 0.f) sh.least = (double)heat * log(fmin((double)least, 1.0));
@@ -774,18 +845,21 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
     total = select<Tin, true>(cluster, sh, row, fminf(spread, tail * heat), [&](u64 whole) { return wanted(p, whole); });
   }
   if (!done && (a.token || p >= 1.f)) {
-    u64 mine = 0;
     const Bounds<kN> bounds(row, true);
+    const bool dense = row.thr == -INFINITY;
+    unsigned high = 0, low = 0;  // sums of the weights' integers: at most part / kThreads < 2^8 of them
     for_each<Tin>(row, [&](const auto& x, int i) {
       bool in[kN];
       bounds.test(x, i, in);
 #pragma unroll
-      for (int j = 0; j < kN; ++j) {
-        if (!__any_sync(0xffffffffu, in[j])) continue;
-        const u64 w = weight(x[j], row.heat, sh.table);
-        if (in[j]) mine += w;
+      for (int j = 0; j < kN; j += 2) {
+        if (!dense && !__any_sync(0xffffffffu, in[j] || in[j + 1])) continue;
+        const Units w = units(x[j], x[j + 1], in[j], in[j + 1], row.heat, sh.table);
+        high += (unsigned)(w.a[0] + w.a[1]) - 2u * kHighBits;
+        low += (unsigned)(w.b[0] + w.b[1]) - 2u * kLowBits;
       }
     });
+    u64 mine = ((u64)high << kHighShift) + (u64)(long long)(int)low;
     mine = warp_sum64(mine);
     if (lane == 0) sh.warp_mass[warp] = mine;
     __syncthreads();
@@ -837,19 +911,24 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
   if (out) {
     const float inv = (float)(1ull << kOne) / __ull2float_rn(total);
     const Tin* x_sh = reinterpret_cast<const Tin*>(part_sh);
-    // down to 2^-160: smaller ones are 0 in fp32 (the loop's first bound on |x c| holds there too)
-    const float tiny = row.heat.least - (256.f * 160.f - kNegligible) / row.heat.hi;
-    for (int i = max(row.lo, from) + lane; i < min(row.hi, to); i += 32) {
-      const float x = to_f32(x_sh[i]);
-      float v = 0.f;
-      if (row.kept(x, i) && x >= tiny) {
-        const Parts w = weight_parts(x, row.heat, sh.table);
-        const int n = min(w.n, 250), n0 = n >> 1;  // two factors of 2: n may pass the exponent's range
-        v = k == 1 ? 1.f
-                   : fmaf(w.lo, 9.094947017729282e-13f, w.hi) * inv * __int_as_float((127 - n0) << 23) *
-                         __int_as_float((127 - (n - n0)) << 23);
+    const float tiny = row.heat.least - (256.f * kTiny - kNegligible) / row.heat.hi;
+    const int end = min(row.hi, to);
+    for (int i = max(row.lo, from) + lane; i - lane < end; i += 64) {
+      float x[2], v[2] = {0.f, 0.f};
+      bool in[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        x[e] = i + 32 * e < end ? to_f32(x_sh[i + 32 * e]) : -INFINITY;
+        in[e] = x[e] >= tiny && row.kept(x[e], i + 32 * e);
       }
-      out[i] = v;
+      if (__any_sync(0xffffffffu, in[0] || in[1])) {
+        Two hi, lo;
+        weights(x[0], x[1], in[0], in[1], row.heat, sh.table, &hi, &lo);
+        ((hi + lo) * both(inv)).get(&v[0], &v[1]);
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (i + 32 * e < end) out[i + 32 * e] = !in[e] ? 0.f : k == 1 ? 1.f : v[e];
     }
   }
 }
