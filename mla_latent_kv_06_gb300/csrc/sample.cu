@@ -8,12 +8,16 @@
 //   min-p : w(x) >= min_p, a threshold on x itself
 //   top-k : the code of the k-th token
 //   top-p : the code of the token at which the running mass reaches top_p W
-// The last two come from a histogram (of counts, or of masses) over kBins
-// intervals of x, which narrows the threshold down to one interval, and from its
-// tokens, ranked against each other; an interval of more than kList tokens is split
-// again, by x and then by codes.  A small k needs no histogram of the row: the
-// k-th of the threads' largest tokens bounds the k-th token from below, and
-// what reaches that bound, little more than k tokens, decides everything else.
+// The last two come from a histogram over kBins intervals of x, which narrows the
+// threshold down to one interval, and from its tokens, ranked against each other;
+// an interval of more than kList tokens is split again, by x and then by codes.
+//   For top-p the histogram counts: a token's weight follows from its interval well
+// enough to name the threshold's (nucleus()), and one pass with exact weights then
+// gives W, the mass above that interval and its tokens, or says that it is
+// the next one.  Only ties that fill an interval go by a histogram of exact masses.
+//   A small k needs no histogram of the row: the k-th of the threads' largest tokens
+// bounds the k-th token from below, and what reaches that bound, little more than k
+// tokens, decides everything else.
 // The draw is the least index whose cumulative kept mass exceeds u W.
 //
 // Rounding.  A threshold and a draw compare sums over the vocabulary, so a
@@ -34,7 +38,9 @@
 //
 // A row is a cluster of up to 8 CTAs, each with a contiguous part of the
 // vocabulary in shared memory, read once, 16 bytes at a time from 16-byte
-// boundaries; a warp's part is contiguous too, and no other warp reads it.
+// boundaries; a warp's part is contiguous too, and no other warp reads it.  (A CTA
+// a row, streaming it from L2 in every pass, was slower up to 400 rows: 104 us
+// against 95 for 256 rows of 131072 at a temperature alone.)
 #include <cooperative_groups.h>
 #include <limits.h>
 
@@ -55,8 +61,7 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 1024;
 constexpr int kCluster = 8;  // most CTAs of a row
-constexpr int kList = 1024;  // tokens that are ranked against each other
-constexpr int kOwn = 768;    // most of them from one CTA
+constexpr int kList = 1024;  // tokens that are ranked against each other: two a thread
 constexpr int kSmallK = 512;  // top-k by the threads' largest tokens
 constexpr int kOne = 44;     // a weight of 1 is 2^kOne; kMaxSampleVocab of them stay below 2^63
 constexpr int kIndexBits = 20;
@@ -92,25 +97,23 @@ struct Shared {
     struct {
       unsigned cnt[kBins], lo[kBins], hi[kBins];  // this CTA's histogram: tokens, or mass as two words
     };
-    struct {
-      u64 own_code[kOwn], own_w[kOwn];  // then its share of the list
-    };
+    u64 own[kList];  // then its share of the list
   };
   u64 tot[kBins];                             // the cluster's, written by all CTAs
-  u64 list_code[kList], list_w[kList];
+  u64 list[kList], sum[kList];  // codes; running mass once ranked
   int2 table[256];   // (hi, d's bits)
   float2 heat;       // c as a pair
   double least;      // T log(min_p)
   float max[kCluster], min[kCluster];
   int first[kCluster];
-  u64 mass[kCluster];
-  u64 warp_mass[kWarps];
+  u64 mass[kCluster], over[kCluster];
+  u64 warp_mass[kWarps], warp_over[kWarps];
+  float warp_part[kWarps];
   float warp_max[kWarps], warp_min[kWarps];
   int warp_first[kWarps];
   int listed, listed_own, at[kCluster];
-  int bin;
+  int bin, pick;
   u64 before;
-  u64 code, upto;
 };
 
 __device__ __forceinline__ u64 warp_sum64(u64 v) {
@@ -340,6 +343,7 @@ struct Row {
   const unsigned char* part;  // the CTA's part in shared memory
   int base;                   // index of its first element (below 0 where that is padding)
   int lo, hi;                 // the warp's elements
+  int from, to;               // the part's elements that are the row's
   Heat heat;
   float thr;                  // kept: x above thr, or equal to it with an index up to `last`
   int last;
@@ -383,6 +387,7 @@ struct Bins {
   __device__ __forceinline__ float at(float x) const {
     return fminf(fmaxf(fmaf(-x, step, off), 0.f), (float)(kBins - 1));
   }
+  __device__ __forceinline__ float raw(float x) const { return fmaf(-x, step, off); }
   static __device__ __forceinline__ int index(float f) { return (__float_as_int(f + kMagic) - kMagicBits) & (kBins - 1); }
   // finer intervals inside interval b
   static __device__ __forceinline__ float inside(float f, int b) {
@@ -455,12 +460,86 @@ __device__ __forceinline__ u64 find_bin(Shared& sh, u64 above, F&& target) {
   return want;
 }
 
-// The kept tokens for which in(x, i) holds, with their codes and weights, in every CTA's list.
-// Their number, or one above kList where the list does not hold them all.  One cluster barrier.
+__device__ __forceinline__ void list_own(Shared& sh, u64 code) {
+  const int at = atomicAdd(&sh.listed_own, 1);
+  if (at < kList) sh.own[at] = code;
+}
+
+// This CTA's share of the list to every CTA's list.
+__device__ __forceinline__ void share_list(cg::cluster_group& cluster, Shared& sh) {
+  const int C = (int)cluster.num_blocks(), tid = threadIdx.x;
+  __syncthreads();
+  const int n = sh.listed_own;
+  if (tid < C) sh.at[tid] = atomicAdd(cluster.map_shared_rank(&sh.listed, tid), min(n, kList + 1));
+  __syncthreads();
+  for (int q = 0; q < C; ++q) {
+    const int at = sh.at[q];
+    if (at + n > kList) continue;
+    u64* list = cluster.map_shared_rank(&sh.list[0], q);
+    for (int i = tid; i < n; i += kThreads) list[at + i] = sh.own[i];
+  }
+}
+
+// The first n entries in descending order: a bitonic network, whose steps of up to 32 stay
+// inside a warp's 64 entries.  (Counting each one's rank took 8 us for 500.)
+__device__ __forceinline__ void sort_list(u64* v, int n) {
+  const int tid = threadIdx.x;
+  int m = 64;
+  while (m < n) m *= 2;
+  for (int i = n + tid; i < m; i += kThreads) v[i] = 0;
+  __syncthreads();
+  for (int size = 2; size <= m; size *= 2)
+    for (int stride = size / 2; stride > 0; stride /= 2) {
+      if (tid < m / 2) {
+        const int i = 2 * tid - (tid & (stride - 1)), j = i + stride;
+        const u64 a = v[i], b = v[j];
+        if ((a < b) == ((i & size) == 0)) {
+          v[i] = b;
+          v[j] = a;
+        }
+      }
+      if (stride > 32 || (stride == 1 && size > 32)) __syncthreads();
+      else __syncwarp();
+    }
+  __syncthreads();
+}
+
+__device__ __forceinline__ float logit_of(unsigned key) {
+  return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
+}
+
+// Running masses of the first n entries, whose logits are logit(i).
+template <typename F>
+__device__ __forceinline__ void sum_list(Shared& sh, const Heat& heat, int n, F&& logit) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, i = 2 * tid;
+  const float x0 = i < n ? logit(i) : -INFINITY, x1 = i + 1 < n ? logit(i + 1) : -INFINITY;
+  const Units w = units(x0, x1, x0 >= heat.least && i < n, x1 >= heat.least && i + 1 < n, heat, sh.table);
+  const u64 w0 = weight_of(w, 0), w1 = weight_of(w, 1), incl = warp_scan64(w0 + w1);
+  if (lane == 31) sh.warp_mass[warp] = incl;
+  __syncthreads();
+  u64 run = incl - w0 - w1;
+  for (int q = 0; q < warp; ++q) run += sh.warp_mass[q];
+  if (i < n) sh.sum[i] = run + w0;
+  if (i + 1 < n) sh.sum[i + 1] = run + w0 + w1;
+  __syncthreads();
+}
+__device__ __forceinline__ void rank_list(Shared& sh, const Heat& heat, int n) {
+  sort_list(sh.list, n);
+  sum_list(sh, heat, n, [&](int i) { return logit_of((unsigned)(sh.list[i] >> kIndexBits)); });
+}
+
+// The first entry whose running mass, from `above` on, reaches the target (there is one).
+__device__ __forceinline__ int pick_entry(Shared& sh, u64 above, u64 target, int n) {
+  for (int i = threadIdx.x; i < n; i += kThreads)
+    if (above + sh.sum[i] >= target && (i == 0 || above + sh.sum[i - 1] < target)) sh.pick = i;
+  __syncthreads();
+  return sh.pick;
+}
+
+// The codes of the kept tokens for which in(x, i) holds, in every CTA's list.  Their number, or one above kList where the list does not hold them all.  One cluster barrier.
 template <typename Tin, typename F>
 __device__ __forceinline__ int collect(cg::cluster_group& cluster, Shared& sh, const Row& row, F&& in) {
   constexpr int kN = Vec<Tin>::kN;
-  const int C = (int)cluster.num_blocks(), tid = threadIdx.x;
   const Bounds<kN> bounds(row, false);
   for_each<Tin>(row, [&](const auto& x, int i) {
     bool take[kN], any = false;
@@ -473,27 +552,10 @@ __device__ __forceinline__ int collect(cg::cluster_group& cluster, Shared& sh, c
     if (!any) return;
 #pragma unroll
     for (int j = 0; j < kN; ++j) {
-      if (!take[j]) continue;
-      const int at = atomicAdd(&sh.listed_own, 1);
-      if (at >= kOwn) continue;
-      sh.own_code[at] = code_of(x[j], row.base + i + j);
-      sh.own_w[at] = x[j] >= row.heat.least ? weight(x[j], row.heat, sh.table) : 0;
+      if (take[j]) list_own(sh, code_of(x[j], row.base + i + j));
     }
   });
-  __syncthreads();
-  const int n = sh.listed_own;
-  if (tid < C) sh.at[tid] = atomicAdd(cluster.map_shared_rank(&sh.listed, tid), n > kOwn ? kList + 1 : n);
-  __syncthreads();
-  for (int q = 0; q < C; ++q) {
-    const int at = sh.at[q];
-    if (n > kOwn || at + n > kList) continue;
-    u64* code = cluster.map_shared_rank(&sh.list_code[0], q);
-    u64* w = cluster.map_shared_rank(&sh.list_w[0], q);
-    for (int i = tid; i < n; i += kThreads) {
-      code[at + i] = sh.own_code[i];
-      w[at + i] = sh.own_w[i];
-    }
-  }
+  share_list(cluster, sh);
   cluster.sync();
   return sh.listed;
 }
@@ -584,93 +646,157 @@ __device__ __forceinline__ u64 select(cg::cluster_group& cluster, Shared& sh, Ro
     }
     __syncthreads();  // (sh.listed has been read)
   }
-  for (int i = tid; i < n; i += kThreads) {
-    const u64 code = sh.list_code[i], w = kMass ? sh.list_w[i] : 1;
-    u64 before = above;
-    for (int j = 0; j < n; ++j) before += sh.list_code[j] > code ? (kMass ? sh.list_w[j] : 1) : 0;
-    if (before < target && target <= before + w) {
-      sh.code = code;
-      sh.upto = before + w;
-    }
+  int i;
+  if (kMass) {
+    rank_list(sh, row.heat, n);
+    i = pick_entry(sh, above, target, n);
+  } else {
+    sort_list(sh.list, n);
+    i = (int)(target - above) - 1;
   }
-  __syncthreads();
-  row.set(sh.code);
-  const u64 kept = sh.upto;
+  row.set(sh.list[i]);
+  const u64 kept = kMass ? above + sh.sum[i] : 0;
   __syncthreads();
   return kept;
 }
 
-// Sum over the CTA, in every thread.
-__device__ __forceinline__ u64 block_sum64(Shared& sh, u64 v) {
-  v = warp_sum64(v);
-  if ((threadIdx.x & 31) == 0) sh.warp_mass[threadIdx.x >> 5] = v;
+// The same for the mass and top_p = p, by an estimate of the interval: false where that fails
+// (nothing has changed then).  *total: the mass kept; sh.over: the CTAs' masses above the
+// interval, sh.warp_over: the warps'; the rest of what is kept is the list up to sh.pick.
+template <typename Tin>
+__device__ __forceinline__ bool nucleus(cg::cluster_group& cluster, Shared& sh, Row& row, float range, float heat, float p,
+                                        u64* total) {
+  constexpr int kN = Vec<Tin>::kN, kPer = kBins / kThreads;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const Bins bins(row.heat.max, range);
+  const Bounds<kN> bounds(row, true);
+  clear_bins(sh);
+  unsigned last = 0;
+  for_each<Tin>(row, [&](const auto& x, int i) {
+    bool in[kN];
+    bounds.test(x, i, in);
+#pragma unroll
+    for (int j = 0; j < kN; ++j) {
+      const int bin = Bins::index(bins.at(x[j]));
+      if (in[j] && bin < kBins - 1) atomicAdd(&sh.cnt[bin], 1u);
+      last += in[j] && bin == kBins - 1 ? 1 : 0;
+    }
+  });
+  last = __reduce_add_sync(0xffffffffu, last);
+  if (lane == 0 && last) atomicAdd(&sh.cnt[kBins - 1], last);
+  sum_bins<false>(cluster, sh);
+  // the interval in which p of the mass is reached, a token taken to weigh what its interval's middle does
+  const float fall = range > 0.f ? -1.4426950f * range / ((float)kBins * heat) : 0.f;
+  float mine[kPer], sum = 0.f;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) sum += mine[k] = (float)sh.tot[tid * kPer + k] * exp2f(fall * (float)(tid * kPer + k));
+  float run = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const float up = __shfl_up_sync(0xffffffffu, run, o);
+    if (lane >= o) run += up;
+  }
+  if (lane == 31) sh.warp_part[warp] = run;
+  if (tid == 0) sh.bin = kBins - 1;
   __syncthreads();
-  u64 sum = 0;
-  for (int q = 0; q < kWarps; ++q) sum += sh.warp_mass[q];
+  float whole = 0.f;
+  run -= sum;
+  for (int q = 0; q < kWarps; ++q) {
+    if (q < warp) run += sh.warp_part[q];
+    whole += sh.warp_part[q];
+  }
+  const float goal = p * whole;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    run += mine[k];
+    if (run >= goal && mine[k] > 0.f) {
+      atomicMin(&sh.bin, tid * kPer + k);
+      break;
+    }
+  }
   __syncthreads();
-  return sum;
+  int bin = sh.bin;
+  for (int tries = 0; tries < 3; ++tries) {
+    // exact: the whole mass, the mass above the interval, its tokens
+    const float top = (float)bin - 0.5f, end = bin == kBins - 1 ? INFINITY : (float)bin + 0.5f;
+    unsigned high = 0, low = 0, high1 = 0, low1 = 0;
+    for_each<Tin>(row, [&](const auto& x, int i) {
+      bool in[kN];
+      bounds.test(x, i, in);
+#pragma unroll
+      for (int j = 0; j < kN; j += 2) {
+        if (!__any_sync(0xffffffffu, in[j] || in[j + 1])) continue;
+        const Units w = units(x[j], x[j + 1], in[j], in[j + 1], row.heat, sh.table);
+        high += (unsigned)(w.a[0] + w.a[1]) - 2u * kHighBits;
+        low += (unsigned)(w.b[0] + w.b[1]) - 2u * kLowBits;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float f = bins.raw(x[j + e]);
+          if (f < top) {  // (what is not in weighs nothing)
+            high1 += (unsigned)w.a[e] - kHighBits;
+            low1 += (unsigned)w.b[e] - kLowBits;
+          } else if (in[j + e] && f < end) {
+            list_own(sh, code_of(x[j + e], row.base + i + j + e));
+          }
+        }
+      }
+    });
+    const u64 all = warp_sum64(((u64)high << kHighShift) + (u64)(long long)(int)low);
+    const u64 over = warp_sum64(((u64)high1 << kHighShift) + (u64)(long long)(int)low1);
+    if (lane == 0) {
+      sh.warp_mass[warp] = all;
+      sh.warp_over[warp] = over;
+    }
+    share_list(cluster, sh);  // (begins with a barrier)
+    if (warp < 2) {
+      const u64 v = warp_sum64(lane < kWarps ? (warp ? sh.warp_over[lane] : sh.warp_mass[lane]) : 0);
+      if (lane < C) *cluster.map_shared_rank(warp ? &sh.over[rank] : &sh.mass[rank], lane) = v;
+    }
+    cluster.sync();
+    u64 mass = 0, above = 0;
+    for (int q = 0; q < C; ++q) {
+      mass += sh.mass[q];
+      above += sh.over[q];
+    }
+    const int n = sh.listed;
+    if (n > kList) return false;
+    const u64 target = wanted(p, mass);
+    if (n) rank_list(sh, row.heat, n);
+    const u64 here = n ? sh.sum[n - 1] : 0;
+    if (target > above && target <= above + here) {
+      const int i = pick_entry(sh, above, target, n);
+      row.set(sh.list[i]);
+      *total = above + sh.sum[i];
+      return true;
+    }
+    bin += target <= above ? -1 : 1;
+    if (bin < 0 || bin >= kBins) return false;
+    cluster.sync();  // (the lists and sums have been read)
+    if (tid == 0) sh.listed = sh.listed_own = 0;
+    cluster.sync();
+  }
+  return false;
 }
 
 // All filters and the draw among the n tokens of the list, which hold the first k of the row.
-// Sets the row's threshold, returns the mass kept and the token drawn (by rank 0's CTA).
+// Sets the row's threshold, returns the mass kept; *token, if wanted: the token drawn.
 __device__ __forceinline__ u64 small_row(Shared& sh, Row& row, int n, int k, float p, const float* u, int32_t* token) {
-  const int tid = threadIdx.x;
-  constexpr int kPer = kList / kThreads;
-  u64 code[kPer], w[kPer], before[kPer], sum = 0;
-#pragma unroll
-  for (int e = 0; e < kPer; ++e) {
-    const int i = tid + e * kThreads;
-    code[e] = w[e] = before[e] = 0;
-    if (i >= n) continue;
-    code[e] = sh.list_code[i];
-    w[e] = sh.list_w[i];
-    int rank = 0;
-    for (int j = 0; j < n; ++j)
-      if (sh.list_code[j] > code[e]) {
-        ++rank;
-        before[e] += sh.list_w[j];
-      }
-    if (rank >= k) code[e] = w[e] = 0;
-    sum += w[e];
-  }
-  u64 whole = block_sum64(sh, sum);
-  if (p < 1.f) {
-    const u64 target = wanted(p, whole);
-    sum = 0;
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) {
-      if (before[e] >= target) code[e] = w[e] = 0;
-      sum += w[e];
-    }
-    whole = block_sum64(sh, sum);
-  }
-  // the threshold: the least code kept
-  u64 least = ~0ull;
-#pragma unroll
-  for (int e = 0; e < kPer; ++e)
-    if (code[e] && code[e] < least) least = code[e];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const u64 other = __shfl_xor_sync(0xffffffffu, least, o);
-    least = other < least ? other : least;
-  }
-  if ((tid & 31) == 0) sh.warp_mass[tid >> 5] = least;
-#pragma unroll
-  for (int e = 0; e < kPer; ++e)
-    if (tid + e * kThreads < n) sh.list_w[tid + e * kThreads] = w[e];
+  rank_list(sh, row.heat, n);
+  int m = min(k, n);
+  if (p < 1.f) m = pick_entry(sh, 0, wanted(p, sh.sum[m - 1]), m) + 1;
+  const u64 whole = sh.sum[m - 1];
+  row.set(sh.list[m - 1]);
   __syncthreads();
-  for (int q = 0; q < kWarps; ++q) least = sh.warp_mass[q] < least ? sh.warp_mass[q] : least;
-  row.set(least);
-  if (token) {
-    const u64 t = drawn(*u, whole);
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) {
-      if (!w[e]) continue;
-      const u64 place = kIndexMask - (code[e] & kIndexMask);
-      u64 run = 0;
-      for (int j = 0; j < n; ++j) run += kIndexMask - (sh.list_code[j] & kIndexMask) < place ? sh.list_w[j] : 0;
-      if (run <= t && t < run + w[e]) *token = (int32_t)place;
+  if (token) {  // the kept ones by index
+    for (int i = threadIdx.x; i < m; i += kThreads) {
+      const u64 code = sh.list[i];
+      sh.list[i] = (code & kIndexMask) << 32 | code >> kIndexBits;
     }
+    sort_list(sh.list, m);
+    sum_list(sh, row.heat, m, [&](int i) { return logit_of((unsigned)sh.list[i]); });
+    const int i = pick_entry(sh, 0, drawn(*u, whole) + 1, m);
+    if (threadIdx.x == 0) *token = (int32_t)(kIndexMask - (sh.list[i] >> 32));
   }
   return whole;
 }
@@ -715,6 +841,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
   const Tin* src = static_cast<const Tin*>(a.logits) + (long long)b * a.l_batch + (long long)node * a.l_row;
   const int head = (int)((reinterpret_cast<uintptr_t>(src) & 15) / sizeof(Tin));
   row.base = rank * part - head;
+  row.from = max(0, -row.base);
+  row.to = (int)min((long long)part, (long long)a.V - row.base);
   load_part<Tin>(src - head, part_sh, (long long)rank * part, row.lo, row.hi, head, a.V);
   float heat = a.temperature ? a.temperature[set] : 1.f;
   int k = a.top_k ? a.top_k[set] : 0;
@@ -768,8 +896,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
     mx = max_nan(mx, sh.max[q]);
     mn = fminf(mn, sh.min[q]);
   }
-  // elements [from, to) of the part are the row's
-  const int from = max(0, -row.base), to = (int)min((long long)part, (long long)a.V - row.base);
   float* out = a.probs ? a.probs + (long long)b * a.p_batch + (long long)node * a.p_row + row.base : nullptr;
   // no finite maximum, NaN or +inf among the logits, or settings that mean nothing
   if (!(mx > -INFINITY && mx < INFINITY) || !(heat >= 0.f && heat < INFINITY) || p != p || least != least) {
@@ -778,7 +904,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
       if (a.token) a.token[r] = -1;
     }
     if (out)
-      for (int i = max(row.lo, from) + lane; i < min(row.hi, to); i += 32) out[i] = qnan();
+      for (int i = max(row.lo, row.from) + lane; i < min(row.hi, row.to); i += 32) out[i] = qnan();
     return;
   }
   row.heat = make_heat(mx, sh.heat);
@@ -839,12 +965,36 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
     }
     if (!few) select<Tin, false>(cluster, sh, row, range, [&](u64) { return (u64)k; });
   }
+  bool listed = false;  // the kept tokens: those above an interval, and some of the list
   if (!done && p < 1.f) {
-    // tokens past this range hold less than 1 - p of the mass, whatever their number
-    const float tail = logf((float)a.V) - logf(fmaxf(1.f - p, 1e-7f)) + 1.f;
-    total = select<Tin, true>(cluster, sh, row, fminf(spread, tail * heat), [&](u64 whole) { return wanted(p, whole); });
+    // tokens past the range hold less than (1 - p) / e^5 of the mass, whatever their number
+    const float tail = logf((float)a.V) - logf(fmaxf(1.f - p, 1e-7f)) + 5.f;
+    const float range = fminf(spread, tail * heat);
+    listed = nucleus<Tin>(cluster, sh, row, range, heat, p, &total);
+    if (!listed) {
+      __syncthreads();  // (sh.listed has been read)
+      total = select<Tin, true>(cluster, sh, row, range, [&](u64 whole) { return wanted(p, whole); });
+    }
   }
-  if (!done && (a.token || p >= 1.f)) {
+  if (listed && a.token) {
+    // the CTAs' and this CTA's warps' kept masses: above the interval, and from the list
+    const int each = part / kWarps;
+    u64 mine = 0, theirs = 0;
+    for (int i = lane; i <= sh.pick; i += 32) {
+      const int at = (int)(kIndexMask - (sh.list[i] & kIndexMask)) + head;
+      const u64 w = sh.sum[i] - (i ? sh.sum[i - 1] : 0);
+      if (at / part == warp) theirs += w;
+      if (at / part == rank && (at - rank * part) / each == warp) mine += w;
+    }
+    mine = warp_sum64(mine);
+    theirs = warp_sum64(theirs);
+    if (lane == 0) {
+      sh.warp_mass[warp] = sh.warp_over[warp] + mine;
+      if (warp < C) sh.mass[warp] = sh.over[warp] + theirs;
+    }
+    __syncthreads();
+  }
+  if (!done && !listed && (a.token || p >= 1.f)) {
     const Bounds<kN> bounds(row, true);
     const bool dense = row.thr == -INFINITY;
     unsigned high = 0, low = 0;  // sums of the weights' integers: at most part / kThreads < 2^8 of them
@@ -870,65 +1020,84 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
     cluster.sync();
     total = 0;
     for (int q = 0; q < C; ++q) total += sh.mass[q];
-    if (a.token) {
-      // the CTA, the warp, the element at which the running mass exceeds t < total
-      u64 t = drawn(a.u[r], total);
-      for (int q = 0; q < rank; ++q) t -= sh.mass[q];  // (wraps where the draw is before this CTA)
-      if (t < sh.mass[rank]) {
-        int w = 0;
-        while (t >= sh.warp_mass[w]) t -= sh.warp_mass[w++];
-        if (w == warp) {
-          for (int i0 = row.lo; i0 < row.hi; i0 += 32 * kN) {
-            const int i = i0 + kN * lane;
-            float x[kN];
-            Vec<Tin>::get(*reinterpret_cast<const uint4*>(part_sh + (size_t)i * sizeof(Tin)), x);
-            bool in[kN];
-            bounds.test(x, i, in);
-            u64 v[kN], sum = 0;
+  }
+  if (a.token && !done) {
+    // the CTA, the warp, the element at which the running mass exceeds t < total
+    const Bounds<kN> bounds(row, true);
+    u64 t = drawn(a.u[r], total);
+    for (int q = 0; q < rank; ++q) t -= sh.mass[q];  // (wraps where the draw is before this CTA)
+    if (t < sh.mass[rank]) {
+      int w = 0;
+      while (t >= sh.warp_mass[w]) t -= sh.warp_mass[w++];
+      if (w == warp) {
+        for (int i0 = row.lo; i0 < row.hi; i0 += 32 * kN) {
+          const int i = i0 + kN * lane;
+          float x[kN];
+          Vec<Tin>::get(*reinterpret_cast<const uint4*>(part_sh + (size_t)i * sizeof(Tin)), x);
+          bool in[kN];
+          bounds.test(x, i, in);
+          u64 v[kN], sum = 0;
 #pragma unroll
-            for (int j = 0; j < kN; ++j) sum += v[j] = in[j] ? weight(x[j], row.heat, sh.table) : 0;
-            const u64 incl = warp_scan64(sum);
-            const unsigned over = __ballot_sync(0xffffffffu, incl > t);
-            if (over) {
-              if (lane == __ffs(over) - 1) {
-                u64 run = incl - sum;
-                int at = -1;
+          for (int j = 0; j < kN; ++j) sum += v[j] = in[j] ? weight(x[j], row.heat, sh.table) : 0;
+          const u64 incl = warp_scan64(sum);
+          const unsigned over = __ballot_sync(0xffffffffu, incl > t);
+          if (over) {
+            if (lane == __ffs(over) - 1) {
+              u64 run = incl - sum;
+              int at = -1;
 #pragma unroll
-                for (int j = 0; j < kN; ++j) {
-                  run += v[j];
-                  if (at < 0 && run > t) at = j;
-                }
-                a.token[r] = row.base + i + at;
+              for (int j = 0; j < kN; ++j) {
+                run += v[j];
+                if (at < 0 && run > t) at = j;
               }
-              break;
+              a.token[r] = row.base + i + at;
             }
-            t -= __shfl_sync(0xffffffffu, incl, 31);
+            break;
           }
+          t -= __shfl_sync(0xffffffffu, incl, 31);
         }
       }
     }
   }
   if (out) {
     const float inv = (float)(1ull << kOne) / __ull2float_rn(total);
-    const Tin* x_sh = reinterpret_cast<const Tin*>(part_sh);
     const float tiny = row.heat.least - (256.f * kTiny - kNegligible) / row.heat.hi;
-    const int end = min(row.hi, to);
-    for (int i = max(row.lo, from) + lane; i - lane < end; i += 64) {
-      float x[2], v[2] = {0.f, 0.f};
-      bool in[2];
+    // v = probabilities of x0, x1 at elements i0, i1
+    auto probability = [&](float x0, float x1, int i0, int i1, float* v0, float* v1) {
+      const bool in0 = x0 >= tiny && row.kept(x0, i0), in1 = x1 >= tiny && row.kept(x1, i1);
+      *v0 = *v1 = 0.f;
+      if (!__any_sync(0xffffffffu, in0 || in1)) return;
+      Two hi, lo;
+      weights(x0, x1, in0, in1, row.heat, sh.table, &hi, &lo);
+      float a0, a1;
+      ((hi + lo) * both(inv)).get(&a0, &a1);
+      *v0 = !in0 ? 0.f : k == 1 ? 1.f : a0;
+      *v1 = !in1 ? 0.f : k == 1 ? 1.f : a1;
+    };
+    if ((reinterpret_cast<uintptr_t>(out) & 15) == 0) {  // the vectors' places are 16-byte units
+      for_each<Tin>(row, [&](const auto& x, int i) {
+        float v[kN];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        x[e] = i + 32 * e < end ? to_f32(x_sh[i + 32 * e]) : -INFINITY;
-        in[e] = x[e] >= tiny && row.kept(x[e], i + 32 * e);
-      }
-      if (__any_sync(0xffffffffu, in[0] || in[1])) {
-        Two hi, lo;
-        weights(x[0], x[1], in[0], in[1], row.heat, sh.table, &hi, &lo);
-        ((hi + lo) * both(inv)).get(&v[0], &v[1]);
-      }
+        for (int j = 0; j < kN; j += 2) probability(x[j], x[j + 1], i + j, i + j + 1, &v[j], &v[j + 1]);
+        if (i >= row.from && i + kN <= row.to) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
-        if (i + 32 * e < end) out[i + 32 * e] = !in[e] ? 0.f : k == 1 ? 1.f : v[e];
+          for (int j = 0; j < kN; j += 4) *reinterpret_cast<float4*>(out + i + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < kN; ++j)
+            if (i + j >= row.from && i + j < row.to) out[i + j] = v[j];
+        }
+      });
+    } else {  // an element per lane, so that a warp's stores are neighbours
+      const Tin* xs = reinterpret_cast<const Tin*>(part_sh);
+      const int end = min(row.hi, row.to);
+      for (int i = max(row.lo, row.from) + lane; i - lane < end; i += 64) {
+        const bool there0 = i < end, there1 = i + 32 < end;
+        float v0, v1;
+        probability(there0 ? to_f32(xs[i]) : -INFINITY, there1 ? to_f32(xs[i + 32]) : -INFINITY, i, i + 32, &v0, &v1);
+        if (there0) out[i] = v0;
+        if (there1) out[i + 32] = v1;
+      }
     }
   }
 }
@@ -947,11 +1116,12 @@ cudaError_t launch(const SampleArgs& a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     done.fetch_or(bit);
   }
-  constexpr int kN = Vec<Tin>::kN, kUnit = kThreads * kN;
+  // as few CTAs a row as leave room for two on an SM, more while the GPU is not full
+  constexpr int kN = Vec<Tin>::kN, kUnit = kThreads * kN, kHalf = 73728;
   const long long rows = (long long)a.B * a.N;
   const int padded = a.V + kN - 1;
   int C = 1;
-  while (C < kCluster && (padded + C - 1) / C * (int)sizeof(Tin) > 73728) C *= 2;
+  while (C < kCluster && (padded + C - 1) / C * (int)sizeof(Tin) > kHalf) C *= 2;
   while (C < kCluster && rows * C * 2 <= sms && padded / C > 2048) C *= 2;
   const int part = ((padded + C - 1) / C + kUnit - 1) / kUnit * kUnit;
   cudaLaunchConfig_t cfg{};
