@@ -12,8 +12,8 @@
 // threshold down to one interval, and from its tokens, ranked against each other;
 // an interval of more than kList tokens is split again, by x and then by codes.
 //   For top-p the histogram counts: a token's weight follows from its interval well
-// enough to name the threshold's (nucleus()), and one pass with exact weights then
-// gives W, the mass above that interval and its tokens, or says that it is
+// enough to name the threshold's (nucleus()).  One pass with exact weights then
+// gives W, the mass above that interval and the interval's tokens, or says that it is
 // the next one.  Only ties that fill an interval go by a histogram of exact masses.
 //   A small k needs no histogram of the row: the k-th of the threads' largest tokens
 // bounds the k-th token from below, and what reaches that bound, little more than k
@@ -62,6 +62,8 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 1024;
 constexpr int kCluster = 8;  // most CTAs of a row
 constexpr int kList = 1024;  // tokens that are ranked against each other: two a thread
+constexpr int kCount = 256;  // up to this many, by counting
+constexpr int kAround = 128; // tokens around an estimated threshold that are looked at in any case
 constexpr int kSmallK = 512;  // top-k by the threads' largest tokens
 constexpr int kOne = 44;     // a weight of 1 is 2^kOne; kMaxSampleVocab of them stay below 2^63
 constexpr int kIndexBits = 20;
@@ -95,7 +97,9 @@ __device__ const ExpTable kTable = make_table();
 struct Shared {
   union {
     struct {
-      unsigned cnt[kBins], lo[kBins], hi[kBins];  // this CTA's histogram: tokens, or mass as two words
+      unsigned cnt[kBins + 64];                // this CTA's histogram: tokens (and a place a lane for those
+                                               // of the last interval, and for no token) ...
+      unsigned lo[kBins], hi[kBins];           // ... or mass as two words
     };
     u64 own[kList];  // then its share of the list
   };
@@ -480,11 +484,28 @@ __device__ __forceinline__ void share_list(cg::cluster_group& cluster, Shared& s
   }
 }
 
-// The first n entries in descending order: a bitonic network, whose steps of up to 32 stay
-// inside a warp's 64 entries.  (Counting each one's rank took 8 us for 500.)
+// The first n entries, all different, in descending order.  Up to kCount of them by counting
+// each one's rank, more by a bitonic network, whose steps of up to 32 stay inside a
+// warp's 64 entries (28 barriers for 128, 45 for 512).
 __device__ __forceinline__ void sort_list(u64* v, int n) {
   const int tid = threadIdx.x;
-  int m = 64;
+  __syncthreads();  // (the entries are there)
+  if (n <= kCount) {
+    int group = 32;  // lanes an entry
+    while (group * n > kThreads) group /= 2;
+    const int e = tid / group;
+    const u64 mine = e < n ? v[e] : 0;
+    int rank = 0;
+    if (e < n)
+#pragma unroll 4
+      for (int j = tid % group; j < n; j += group) rank += v[j] > mine ? 1 : 0;
+    for (int o = group / 2; o > 0; o >>= 1) rank += __shfl_xor_sync(0xffffffffu, rank, o);
+    __syncthreads();
+    if (e < n && tid % group == 0) v[rank] = mine;
+    __syncthreads();
+    return;
+  }
+  int m = 512;
   while (m < n) m *= 2;
   for (int i = n + tid; i < m; i += kThreads) v[i] = 0;
   __syncthreads();
@@ -528,8 +549,10 @@ __device__ __forceinline__ void rank_list(Shared& sh, const Heat& heat, int n) {
   sum_list(sh, heat, n, [&](int i) { return logit_of((unsigned)(sh.list[i] >> kIndexBits)); });
 }
 
-// The first entry whose running mass, from `above` on, reaches the target (there is one).
+// The first of n entries whose running mass, from `above` on, reaches the target (there is one).
 __device__ __forceinline__ int pick_entry(Shared& sh, u64 above, u64 target, int n) {
+  if (threadIdx.x == 0) sh.pick = n - 1;
+  __syncthreads();
   for (int i = threadIdx.x; i < n; i += kThreads)
     if (above + sh.sum[i] >= target && (i == 0 || above + sh.sum[i - 1] < target)) sh.pick = i;
   __syncthreads();
@@ -562,6 +585,7 @@ __device__ __forceinline__ int collect(cg::cluster_group& cluster, Shared& sh, c
 
 __device__ __forceinline__ void clear_bins(Shared& sh) {
   for (int i = threadIdx.x; i < kBins; i += kThreads) sh.cnt[i] = sh.lo[i] = sh.hi[i] = 0;
+  if (threadIdx.x < 64) sh.cnt[kBins + threadIdx.x] = 0;
   if (threadIdx.x == 0) sh.listed = sh.listed_own = 0;
   __syncthreads();
 }
@@ -672,19 +696,20 @@ __device__ __forceinline__ bool nucleus(cg::cluster_group& cluster, Shared& sh, 
   const Bins bins(row.heat.max, range);
   const Bounds<kN> bounds(row, true);
   clear_bins(sh);
-  unsigned last = 0;
   for_each<Tin>(row, [&](const auto& x, int i) {
     bool in[kN];
     bounds.test(x, i, in);
 #pragma unroll
-    for (int j = 0; j < kN; ++j) {
+    for (int j = 0; j < kN; ++j) {  // (no branch: the last interval, and no token, at the lane's own place)
       const int bin = Bins::index(bins.at(x[j]));
-      if (in[j] && bin < kBins - 1) atomicAdd(&sh.cnt[bin], 1u);
-      last += in[j] && bin == kBins - 1 ? 1 : 0;
+      atomicAdd(&sh.cnt[!in[j] ? kBins + 32 + lane : bin == kBins - 1 ? kBins + lane : bin], 1u);
     }
   });
-  last = __reduce_add_sync(0xffffffffu, last);
-  if (lane == 0 && last) atomicAdd(&sh.cnt[kBins - 1], last);
+  __syncthreads();
+  if (warp == 0) {
+    const unsigned last = __reduce_add_sync(0xffffffffu, sh.cnt[kBins + lane]);
+    if (lane == 0) sh.cnt[kBins - 1] = last;
+  }
   sum_bins<false>(cluster, sh);
   // the interval in which p of the mass is reached, a token taken to weigh what its interval's middle does
   const float fall = range > 0.f ? -1.4426950f * range / ((float)kBins * heat) : 0.f;
@@ -700,13 +725,13 @@ __device__ __forceinline__ bool nucleus(cg::cluster_group& cluster, Shared& sh, 
   if (lane == 31) sh.warp_part[warp] = run;
   if (tid == 0) sh.bin = kBins - 1;
   __syncthreads();
-  float whole = 0.f;
   run -= sum;
+  float whole = 0.f;
   for (int q = 0; q < kWarps; ++q) {
     if (q < warp) run += sh.warp_part[q];
     whole += sh.warp_part[q];
   }
-  const float goal = p * whole;
+  const float goal = p * whole;  // (not of the exact mass: the first tokens' errors are in both sides)
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
     run += mine[k];
@@ -718,29 +743,44 @@ __device__ __forceinline__ bool nucleus(cg::cluster_group& cluster, Shared& sh, 
   __syncthreads();
   int bin = sh.bin;
   for (int tries = 0; tries < 3; ++tries) {
-    // exact: the whole mass, the mass above the interval, its tokens
-    const float top = (float)bin - 0.5f, end = bin == kBins - 1 ? INFINITY : (float)bin + 0.5f;
+    // its neighbours along with it while that is few tokens: where few tokens hold the mass
+    // the estimate is rough
+    int lo = bin, hi = bin;
+    for (u64 n = sh.tot[bin]; lo > 0 && hi < kBins - 1 && hi - bin < 8; --lo, ++hi)
+      if ((n += sh.tot[lo - 1] + sh.tot[hi + 1]) > kAround) break;
+    // exact: the whole mass, the mass above these intervals, their tokens
+    const float top = (float)lo - 0.5f, end = hi == kBins - 1 ? INFINITY : (float)hi + 0.5f;
     unsigned high = 0, low = 0, high1 = 0, low1 = 0;
     for_each<Tin>(row, [&](const auto& x, int i) {
-      bool in[kN];
+      bool in[kN], any = false;
       bounds.test(x, i, in);
 #pragma unroll
+      for (int j = 0; j < kN; ++j) any = any || in[j];
+      if (!__any_sync(0xffffffffu, any)) return;
+      any = false;
+#pragma unroll
       for (int j = 0; j < kN; j += 2) {
-        if (!__any_sync(0xffffffffu, in[j] || in[j + 1])) continue;
         const Units w = units(x[j], x[j + 1], in[j], in[j + 1], row.heat, sh.table);
-        high += (unsigned)(w.a[0] + w.a[1]) - 2u * kHighBits;
-        low += (unsigned)(w.b[0] + w.b[1]) - 2u * kLowBits;
+        high += (unsigned)(w.a[0] + w.a[1]);
+        low += (unsigned)(w.b[0] + w.b[1]);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const float f = bins.raw(x[j + e]);
-          if (f < top) {  // (what is not in weighs nothing)
-            high1 += (unsigned)w.a[e] - kHighBits;
-            low1 += (unsigned)w.b[e] - kLowBits;
-          } else if (in[j + e] && f < end) {
-            list_own(sh, code_of(x[j + e], row.base + i + j + e));
-          }
+          const bool over = f < top;  // (what is not in weighs nothing)
+          high1 += over ? (unsigned)w.a[e] : (unsigned)kHighBits;
+          low1 += over ? (unsigned)w.b[e] : (unsigned)kLowBits;
+          in[j + e] = in[j + e] && !over && f < end;
+          any = any || in[j + e];
         }
       }
+      high -= (unsigned)kN * kHighBits;
+      low -= (unsigned)kN * kLowBits;
+      high1 -= (unsigned)kN * kHighBits;
+      low1 -= (unsigned)kN * kLowBits;
+      if (any)
+#pragma unroll
+        for (int j = 0; j < kN; ++j)
+          if (in[j]) list_own(sh, code_of(x[j], row.base + i + j));
     });
     const u64 all = warp_sum64(((u64)high << kHighShift) + (u64)(long long)(int)low);
     const u64 over = warp_sum64(((u64)high1 << kHighShift) + (u64)(long long)(int)low1);
@@ -759,9 +799,9 @@ __device__ __forceinline__ bool nucleus(cg::cluster_group& cluster, Shared& sh, 
       mass += sh.mass[q];
       above += sh.over[q];
     }
+    const u64 target = wanted(p, mass);
     const int n = sh.listed;
     if (n > kList) return false;
-    const u64 target = wanted(p, mass);
     if (n) rank_list(sh, row.heat, n);
     const u64 here = n ? sh.sum[n - 1] : 0;
     if (target > above && target <= above + here) {
@@ -770,7 +810,7 @@ __device__ __forceinline__ bool nucleus(cg::cluster_group& cluster, Shared& sh, 
       *total = above + sh.sum[i];
       return true;
     }
-    bin += target <= above ? -1 : 1;
+    bin = target <= above ? lo - 1 : hi + 1;
     if (bin < 0 || bin >= kBins) return false;
     cluster.sync();  // (the lists and sums have been read)
     if (tid == 0) sh.listed = sh.listed_own = 0;
@@ -978,13 +1018,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
   }
   if (listed && a.token) {
     // the CTAs' and this CTA's warps' kept masses: above the interval, and from the list
-    const int each = part / kWarps;
     u64 mine = 0, theirs = 0;
     for (int i = lane; i <= sh.pick; i += 32) {
-      const int at = (int)(kIndexMask - (sh.list[i] & kIndexMask)) + head;
+      const int at = (int)(kIndexMask - (sh.list[i] & kIndexMask)) + head, own = at - rank * part;
       const u64 w = sh.sum[i] - (i ? sh.sum[i - 1] : 0);
-      if (at / part == warp) theirs += w;
-      if (at / part == rank && (at - rank * part) / each == warp) mine += w;
+      if (at >= warp * part && at < (warp + 1) * part) theirs += w;  // (of CTA `warp`)
+      if (own >= row.lo && own < row.hi) mine += w;
     }
     mine = warp_sum64(mine);
     theirs = warp_sum64(theirs);
@@ -1001,12 +1040,18 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
     for_each<Tin>(row, [&](const auto& x, int i) {
       bool in[kN];
       bounds.test(x, i, in);
-#pragma unroll
-      for (int j = 0; j < kN; j += 2) {
-        if (!dense && !__any_sync(0xffffffffu, in[j] || in[j + 1])) continue;
+      auto add = [&](int j) {
         const Units w = units(x[j], x[j + 1], in[j], in[j + 1], row.heat, sh.table);
         high += (unsigned)(w.a[0] + w.a[1]) - 2u * kHighBits;
         low += (unsigned)(w.b[0] + w.b[1]) - 2u * kLowBits;
+      };
+      if (dense) {  // straight through, so that the vector's chains overlap
+#pragma unroll
+        for (int j = 0; j < kN; j += 2) add(j);
+      } else {
+#pragma unroll
+        for (int j = 0; j < kN; j += 2)
+          if (__any_sync(0xffffffffu, in[j] || in[j + 1])) add(j);
       }
     });
     u64 mine = ((u64)high << kHighShift) + (u64)(long long)(int)low;
@@ -1028,7 +1073,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
     for (int q = 0; q < rank; ++q) t -= sh.mass[q];  // (wraps where the draw is before this CTA)
     if (t < sh.mass[rank]) {
       int w = 0;
-      while (t >= sh.warp_mass[w]) t -= sh.warp_mass[w++];
+      while (w < kWarps - 1 && t >= sh.warp_mass[w]) t -= sh.warp_mass[w++];
       if (w == warp) {
         for (int i0 = row.lo; i0 < row.hi; i0 += 32 * kN) {
           const int i = i0 + kN * lane;
