@@ -932,53 +932,55 @@ def decode_shared_paged(q, Lc_pages, Rc_pages, block_table, T, shared: int, kv_b
 
 def _sample(logits, u, temperature, top_k, top_p, min_p, token, probs):
     torch = _torch()
-    if logits.dim() not in (2, 3):
+    shape, strides, index = logits.shape, logits.stride(), logits.get_device()
+    if len(shape) == 2:
+        (B, V), N = shape, 1
+        lead, l_row = shape[:1], V
+    elif len(shape) == 3:
+        B, N, V = shape
+        lead, l_row = shape[:2], strides[1]
+    else:
         raise ValueError("logits must be [B, V] or [B, N, V]")
-    lead, V, index = logits.shape[:-1], logits.shape[-1], logits.get_device()
     code = _dtype_code(logits)
-    strides = logits.stride()
     if strides[-1] != 1 and V > 1:
         raise ValueError("the values of a row of logits must be contiguous")
     f32, i32 = torch.float32, torch.int32
-    settings = (temperature, top_k, top_p, min_p)
-    per_row = 0
-    for name, x in zip(("temperature", "top_k", "top_p", "min_p"), settings):
+    sets, where = None, []  # shape of the settings, their addresses
+    for x, want, name in ((temperature, f32, "temperature"), (top_k, i32, "top_k"), (top_p, f32, "top_p"), (min_p, f32, "min_p")):
         if x is None:
+            where.append(None)
             continue
-        if x.shape == lead:
-            per_row = 1
-        elif x.shape != lead[:1]:
-            raise ValueError(f"{name}: shape {tuple(x.shape)}, not {tuple(lead)} or {tuple(lead[:1])}")
-        want = i32 if x is top_k else f32
-        if not _all_plain(index, want, x):
+        if x.shape != lead and x.shape != shape[:1]:
+            raise ValueError(f"{name}: shape {tuple(x.shape)}, not {tuple(lead)} or {tuple(shape[:1])}")
+        if sets is not None and x.shape != sets:
+            raise ValueError("the settings must be given all per sequence or all per row")
+        sets = x.shape
+        if x.dtype is not want or x.get_device() != index or not x.is_contiguous():
             _explain(logits.device, **{name: (x, want)})
-    if len({x.shape for x in settings if x is not None}) > 1:
-        raise ValueError("the settings must be given all per sequence or all per row")
+        where.append(x.data_ptr())
+    u_ptr = token_ptr = None
     if u is not None:
         _want("u", u, *lead)
-        if not _all_plain(index, f32, u):
+        if u.dtype is not f32 or u.get_device() != index or not u.is_contiguous():
             _explain(logits.device, u=(u, f32))
         if token is None:
-            token = u.new_empty(lead, dtype=i32)
+            token = torch.empty_like(u, dtype=i32)
         else:
             _want("token", token, *lead)
             _explain(logits.device, token=(token, i32))
-    B, N = lead[0], lead[1] if len(lead) == 2 else 1
-    l_row = strides[1] if len(lead) == 2 else V
+        u_ptr, token_ptr = u.data_ptr(), token.data_ptr()
     p_ptr, p_row, p_batch = None, 0, 0
     if probs is True:
-        probs = logits.new_empty(logits.shape, dtype=f32)
+        probs = logits.new_empty(shape, dtype=f32)
     elif probs is not None:
-        _want("probs", probs, *logits.shape)
+        _want("probs", probs, *shape)
         if probs.dtype is not f32 or probs.get_device() != index or (probs.stride(-1) != 1 and V > 1):
             raise ValueError("probs must be float32 on the logits' GPU, with contiguous rows")
     st = _current_stream(torch, index)
     if probs is not None:
-        p_ptr, p_batch, p_row = probs.data_ptr(), probs.stride(0), probs.stride(1) if len(lead) == 2 else V
-    temperature, top_k, top_p, min_p = (None if x is None else x.data_ptr() for x in settings)
-    _check(lib().mla_sample(B, N, V, code, logits.data_ptr(), l_row, strides[0], temperature, top_k, top_p, min_p, per_row,
-                            None if u is None else u.data_ptr(), None if u is None else token.data_ptr(), p_ptr, p_row,
-                            p_batch, st))
+        p_ptr, p_batch, p_row = probs.data_ptr(), probs.stride(0), probs.stride(1) if N > 1 else V
+    _check(lib().mla_sample(B, N, V, code, logits.data_ptr(), l_row, strides[0], *where, 1 if sets == lead else 0, u_ptr,
+                            token_ptr, p_ptr, p_row, p_batch, st))
     return token, probs
 
 

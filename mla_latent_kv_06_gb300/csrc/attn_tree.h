@@ -86,7 +86,13 @@ struct SharedItems {
   }
 };
 
-// The partials of one query row: at most a few dozen chunks of its two items.
+// a / d for a >= 0, d > 0: in 32 bits wherever a fits.
+__device__ __forceinline__ long long over_chunks(long long a, int d) {
+  return ((unsigned long long)a >> 32) == 0 ? (long long)((unsigned)a / (unsigned)d) : a / d;
+}
+
+// The partials of one query row: at most kSharedSplits chunks of its two items.
+constexpr int kSharedChunks = 128, kSharedSplits = 2 * kSharedChunks;
 struct SharedSplits {
   SharedItems::Item item[2];
   int at[2], from[2], odd[2], n0, n;
@@ -112,14 +118,14 @@ struct SharedSplits {
     const bool own = i >= n0;
     const int g = own ? from[1] + i - n0 : from[0] + i;
     int lo, hi;
-    (own ? item[1] : item[0]).range(N * g / G, N * (g + 1) / G, &lo, &hi);
+    (own ? item[1] : item[0]).range(over_chunks(N * g, G), over_chunks(N * (g + 1), G), &lo, &hi);
     return lo < hi ? (long long)(g + (own ? at[1] : at[0])) * 2 + (own ? odd[1] : odd[0]) : -1;
   }
   // the chunk that holds unit x: the largest g with N g / G <= x
   static __device__ __forceinline__ int chunk(long long x, long long N, int G) {
-    int g = (int)(x * G / N);
+    int g = ((unsigned long long)(x * G) >> 32) == 0 ? (int)((unsigned)(x * G) / (unsigned)N) : (int)(x * G / N);
     if (g > G - 1) g = G - 1;
-    while (g + 1 < G && N * (g + 1) / G <= x) ++g;
+    while (g + 1 < G && over_chunks(N * (g + 1), G) <= x) ++g;
     return g;
   }
 };

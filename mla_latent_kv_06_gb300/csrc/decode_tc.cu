@@ -910,14 +910,14 @@ __device__ __forceinline__ void rope_rows(const AbsorbParams& p, int h, int tid,
   }
 }
 
-// Tail rows of the pair attention: rows base16 .. T - 1 of every sequence, zeros
+// Tail rows of the pair attention: rows base16 .. T - 1 of every sequence (up to 79), zeros
 // after them up to a whole 16-key step (the value product reads no further, and the
 // scores of rows past T are masked).  A row that holds a value that is not finite becomes zero
 // latents with a NaN rotary part (see attn_tree.cu).  One warp per row.
 __device__ __forceinline__ void stage_tail(const AbsorbParams& p, int warp0, int nwarps) {
-  const int lane = threadIdx.x & 31;
-  for (int e = warp0; e < p.B * 80; e += nwarps) {
-    const int b = e / 80, i = e % 80, Tb = p.T[b];
+  const int lane = threadIdx.x & 31, rows = (p.S + 30) & ~15;  // up to 15 + S, in whole steps
+  for (int e = warp0; e < p.B * rows; e += nwarps) {
+    const int b = e / rows, i = e % rows, Tb = p.T[b];
     if (Tb < p.S + p.lead || Tb > p.T_cap) continue;
     const int t = pair_base16(Tb, p.S) + i;
     if (t >= ((Tb + 15) & ~15)) continue;
@@ -1672,62 +1672,68 @@ struct SharedMergeParams {
   SharedItems items;
 };
 
-template <int kParts>
+// A CTA takes 8 heads of one row: one warp lists the row's splits for all (each warp for itself took
+// 28.6 us for 192 rows, and several warps per head, as merge_pair_kernel has for few rows, 39 and 74).
 __global__ void __launch_bounds__(256) merge_shared_kernel(const SharedMergeParams p) {
-  constexpr int kVec = 4 / kParts, kDeep = kParts == 4 ? 8 : 2;
+  constexpr int kDeep = 2;  // splits in flight
+  __shared__ int slots[kSharedSplits];
+  __shared__ int count_sh, state_sh;
   grid_dep_wait();
   grid_dep_launch();
-  const int lane = threadIdx.x & 31;
-  const long long gw = ((long long)blockIdx.x * 256 + threadIdx.x) >> 5;
-  const int part = (int)(gw % kParts);
-  const long long rh = gw / kParts;
-  const int r = (int)(rh / kH), h = (int)(rh % kH);
-  if (r >= p.items.B * p.S) return;
-  const int b = r / p.S, s = r % p.S;
-  __nv_bfloat16* dst = p.clat + ((size_t)r * kH + h) * (2 * kDl) + 128 * part + 4 * lane;
-  const int state = node_at(p.parent, b, p.S, s).state;
-  const bool broken = p.bad[b] || state == kNodeBad;
-  float inv = broken ? qnan() : 1.f;
-  float4 acc[kVec];
-#pragma unroll
-  for (int v = 0; v < kVec; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (!broken && state == kNodePresent) {
-    const long long N = p.items.total();
-    SharedSplits sp;
-    sp.start(p.items, N, p.G, r, b, s);
-    const int n = sp.n;
-    auto slot_of = [&](int i) { return sp.slot(i, N, p.G); };
-    float M = -INFINITY, L = 0.f;
-    for (int i0 = 0; i0 < n; i0 += 32) {
-      const long long slot = slot_of(i0 + lane);
-      if (slot >= 0) M = fmaxf(M, p.ml_part[(slot * kH + h) * 2]);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int r = blockIdx.x / (kH / 8), h = (blockIdx.x % (kH / 8)) * 8 + warp;
+  if (warp == 0) {
+    const int b = r / p.S, s = r % p.S;
+    const int state = p.bad[b] ? (int)kNodeBad : node_at(p.parent, b, p.S, s).state;
+    int cnt = 0;
+    if (state == kNodePresent) {
+      const long long N = p.items.total();
+      SharedSplits sp;
+      sp.start(p.items, N, p.G, r, b, s);
+      for (int i0 = 0; i0 < sp.n; i0 += 32) {
+        const long long slot = sp.slot(i0 + lane, N, p.G);
+        const unsigned m = __ballot_sync(0xffffffffu, slot >= 0);
+        if (slot >= 0) slots[cnt + __popc(m & ((1u << lane) - 1))] = (int)slot;
+        cnt += __popc(m);
+      }
     }
+    if (lane == 0) {
+      count_sh = cnt;
+      state_sh = state;
+    }
+  }
+  __syncthreads();
+  const int n = count_sh;
+  float4 acc[4];
+#pragma unroll
+  for (int v = 0; v < 4; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+  float inv = state_sh == kNodeBad ? qnan() : 1.f;
+  if (n > 0) {
+    float M = -INFINITY, L = 0.f;
+    for (int i = lane; i < n; i += 32) M = fmaxf(M, p.ml_part[((size_t)slots[i] * kH + h) * 2]);
     M = warp_max(M);
     for (int i0 = 0; i0 < n; i0 += 32) {
-      const long long mine = slot_of(i0 + lane);
       float2 ml = make_float2(-INFINITY, 0.f);
-      if (mine >= 0) ml = *reinterpret_cast<const float2*>(p.ml_part + (mine * kH + h) * 2);
-      const float w = mine >= 0 ? exp2f(ml.x - M) : 0.f;
+      if (i0 + lane < n) ml = *reinterpret_cast<const float2*>(p.ml_part + ((size_t)slots[i0 + lane] * kH + h) * 2);
+      const float w = i0 + lane < n ? exp2f(ml.x - M) : 0.f;
       L += warp_sum(w * ml.y);
       const int cnt = min(32, n - i0);
       for (int j0 = 0; j0 < cnt; j0 += kDeep) {
-        float4 o[kDeep][kVec];
+        float4 o[kDeep][4];
         float wg[kDeep];
 #pragma unroll
         for (int u = 0; u < kDeep; ++u) {
-          const int j = min(j0 + u, 31);
-          const long long slot = __shfl_sync(0xffffffffu, mine, j);
-          const bool use = j0 + u < cnt && slot >= 0;
-          wg[u] = __shfl_sync(0xffffffffu, w, j);
+          const bool use = j0 + u < cnt;
+          wg[u] = __shfl_sync(0xffffffffu, w, min(j0 + u, 31));
           if (!use) wg[u] = 0.f;
-          const float4* src = reinterpret_cast<const float4*>(p.o_part + ((use ? slot : 0) * kH + h) * kDl + 128 * part + 4 * lane);
+          const float4* src = reinterpret_cast<const float4*>(p.o_part + ((size_t)slots[use ? i0 + j0 + u : 0] * kH + h) * kDl) + lane;
 #pragma unroll
-          for (int v = 0; v < kVec; ++v) o[u][v] = use ? src[32 * v] : make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int v = 0; v < 4; ++v) o[u][v] = use ? src[32 * v] : make_float4(0.f, 0.f, 0.f, 0.f);
         }
 #pragma unroll
         for (int u = 0; u < kDeep; ++u)
 #pragma unroll
-          for (int v = 0; v < kVec; ++v) {
+          for (int v = 0; v < 4; ++v) {
             acc[v].x = fmaf(wg[u], o[u][v].x, acc[v].x);
             acc[v].y = fmaf(wg[u], o[u][v].y, acc[v].y);
             acc[v].z = fmaf(wg[u], o[u][v].z, acc[v].z);
@@ -1737,11 +1743,12 @@ __global__ void __launch_bounds__(256) merge_shared_kernel(const SharedMergePara
     }
     const float il = 1.f / L;
 #pragma unroll
-    for (int v = 0; v < kVec; ++v) acc[v] = make_float4(acc[v].x * il, acc[v].y * il, acc[v].z * il, acc[v].w * il);
+    for (int v = 0; v < 4; ++v) acc[v] = make_float4(acc[v].x * il, acc[v].y * il, acc[v].z * il, acc[v].w * il);
     if (L != L) inv = qnan();
   }
+  __nv_bfloat16* dst = p.clat + ((size_t)r * kH + h) * (2 * kDl) + 4 * lane;
 #pragma unroll
-  for (int v = 0; v < kVec; ++v) {
+  for (int v = 0; v < 4; ++v) {
     const uint2 hi = make_uint2(pack2(acc[v].x, acc[v].y), pack2(acc[v].z, acc[v].w));
     const float2 h0 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&hi.x));
     const float2 h1 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&hi.y));
@@ -1749,7 +1756,7 @@ __global__ void __launch_bounds__(256) merge_shared_kernel(const SharedMergePara
     *reinterpret_cast<uint2*>(dst + kDl + 128 * v) =
         make_uint2(pack2(acc[v].x - h0.x, acc[v].y - h0.y), pack2(acc[v].z - h1.x, acc[v].w - h1.y));
   }
-  if (lane == 0 && part == 0) p.inv_l[(size_t)r * kH + h] = inv;
+  if (lane == 0) p.inv_l[(size_t)r * kH + h] = inv;
 }
 
 // ===========================================================================
@@ -1913,10 +1920,10 @@ Plan make_plan(int B, int S, int T_cap, int sparse_topk, bool tree = false, int 
   if (shared) {
     pl.tiles = lead / kPairTile;
     pl.shared = pl.tiles ? (pl.R + 1) / 2 : 0;
-    pl.Gp = std::max(sms / 2, 1);
+    pl.Gp = std::min(std::max(sms / 2, 1), kSharedChunks);
     pl.P = 2 * (pl.Gp + pl.shared + B * ((S + 1) / 2) - 1);
   } else if (pair) {
-    static_assert(kPairChunks <= kMaxPieces, "the combine lists up to kMaxPieces splits of a row");
+    static_assert(kPairChunks <= kMaxPieces && kSharedSplits <= kMaxPieces, "the combine lists up to kMaxPieces splits of a row");
     pl.Gp = pair_chunks(B, S, T_cap, sms);
     pl.P = std::max(pl.P, (pl.Gp + B - 1) * S);
   }
@@ -1970,10 +1977,7 @@ cudaError_t run_lift(const DecodeArgs& a, const Plan& pl, unsigned char* w, bool
   cudaError_t e;
   if (shared) {
     const SharedMergeParams mp{o_part, ml_part, bad, a.parent, clat, inv_l, a.S, pl.Gp, shared_items(a, pl, w)};
-    const bool few = pl.R <= 32;
-    const long long warps = (long long)pl.R * kH * (few ? 4 : 1);
-    e = launch_pdl(few ? merge_shared_kernel<4> : merge_shared_kernel<1>, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, st,
-                   mp);
+    e = launch_pdl(merge_shared_kernel, dim3((unsigned)(pl.R * (kH / 8))), dim3(256), 0, st, mp);
   } else if (pair) {
     const PairMergeParams mp{o_part, ml_part, ts, bad, a.parent, clat, inv_l, a.B, a.S, pl.Gp};
     const bool few = pl.R <= 32;  // four warps per (row, head) while a warp each would not fill the GPU
@@ -2171,8 +2175,9 @@ cudaError_t run(const DecodeArgs& a, void* ws, bool sparse, cudaStream_t st, boo
   e = set_smem_once(akern, (int)abs_smem, &g_abs_attr[big ? (tree ? 17 : 16) : 4 * abs_kind + g.Dn / 64 - 1]);
   if (e != cudaSuccess) return e;
   kernel_mark(st, big ? "plan_rope" : "absorb");
-  // a warp per staged row up to 8 blocks along x (32 sequences: plan_rope 12.5 us with one)
-  const int stage_gx = !pair ? 0 : std::min(8, (B * 80 + kH * (kAbsThreads / 32) - 1) / (kH * (kAbsThreads / 32)));
+  // a warp per staged row up to 8 blocks along x
+  const int stage_rows = B * ((S + 30) & ~15), per_x = kH * (kAbsThreads / 32);
+  const int stage_gx = !pair ? 0 : std::min(8, (stage_rows + per_x - 1) / per_x);
   e = launch_pdl(akern, dim3(abs_gx + stage_gx, kH), dim3(kAbsThreads), abs_smem, st, ap);
   if (e != cudaSuccess) return e;
   if (big) {  // qabs for many rows: per-head GEMM [R x qk_nope] x W_UK[h] on the tensor cores
@@ -2196,6 +2201,7 @@ cudaError_t run(const DecodeArgs& a, void* ws, bool sparse, cudaStream_t st, boo
     ga.N = kDl;
     ga.K = g.Dn;
     ga.Z = kH;
+    ga.late_wait = shared ? 1 : 0;  // beside plan_rope: the call 2 us shorter, 9 to 192 rows
     ga.flags = a.flags;
     ga.wait_ns = a.wait_limit_ns;
     kernel_mark(st, "absorb_gemm");

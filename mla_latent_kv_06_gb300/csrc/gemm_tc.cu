@@ -41,6 +41,7 @@ struct GemmParams {
   int out_kind;
   const float* scale;
   int M, N, K, Z;
+  int late_wait;
   unsigned int* flags;
   long long wait_ns;
 };
@@ -115,7 +116,7 @@ __global__ void __launch_bounds__(kGThreads, 1) gemm_kernel(const __grid_constan
   tc_fence_after();
   const uint32_t tmem = tmem_base;
   volatile int* abort = &abort_flag;
-  grid_dep_wait();  // A (and the epilogue's scale) may come from the previous kernel
+  if (!p.late_wait) grid_dep_wait();  // A (and the epilogue's scale) may come from the previous kernel
   grid_dep_launch();
 
   if (warp == 0) {
@@ -244,6 +245,7 @@ __global__ void __launch_bounds__(kGThreads, 1) gemm_kernel(const __grid_constan
     tc_fence_after();
     tmem_dealloc(tmem, 2 * BN);
   }
+  if (p.late_wait) grid_dep_wait();  // the next kernel waits for this one alone
 }
 
 template <int BN, bool kBMN>
@@ -303,6 +305,7 @@ cudaError_t launch_gemm_tc(const GemmArgs& a, bool pdl, cudaStream_t st) {
   gp.N = a.N;
   gp.K = a.K;
   gp.Z = a.Z;
+  gp.late_wait = a.late_wait;
   gp.flags = a.flags;
   gp.wait_ns = a.wait_ns;
   if (BN == 256) return a.b_mn_major ? launch_one<256, true>(gp, pdl, st) : launch_one<256, false>(gp, pdl, st);

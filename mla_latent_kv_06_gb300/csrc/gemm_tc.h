@@ -37,6 +37,8 @@ struct GemmArgs {
   int out_kind;        // GemmOut
   const float* scale;  // kGemmOutF32Scaled, kGemmOutBf16Scaled: [M * Z]
   int M, N, K, Z;      // K % 64 == 0, N % 64 == 0
+  int late_wait;       // A comes from before the previous kernel, which has waited for it before it let this
+                       // one start: run beside that kernel, and end after it
   unsigned int* flags;
   long long wait_ns;
 };

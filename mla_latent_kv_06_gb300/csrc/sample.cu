@@ -1105,7 +1105,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
     }
   }
   if (out) {
-    const float inv = (float)(1ull << kOne) / __ull2float_rn(total);
+    // 2^kOne / total as a pair: the quotient's own error would be in every probability
+    const float t_hi = __ull2float_rn(total), t_lo = (float)(long long)(total - __float2ull_rn(t_hi));
+    const float inv = (float)(1ull << kOne) / t_hi;
+    const float inv_lo = fmaf(-t_lo, inv, fmaf(-t_hi, inv, (float)(1ull << kOne))) / t_hi;
     const float tiny = row.heat.least - (256.f * kTiny - kNegligible) / row.heat.hi;
     // v = probabilities of x0, x1 at elements i0, i1
     auto probability = [&](float x0, float x1, int i0, int i1, float* v0, float* v1) {
@@ -1115,7 +1118,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
       Two hi, lo;
       weights(x0, x1, in0, in1, row.heat, sh.table, &hi, &lo);
       float a0, a1;
-      ((hi + lo) * both(inv)).get(&a0, &a1);
+      fma(hi, both(inv), fma(hi, both(inv_lo), lo * both(inv))).get(&a0, &a1);
       *v0 = !in0 ? 0.f : k == 1 ? 1.f : a0;
       *v1 = !in1 ? 0.f : k == 1 ? 1.f : a1;
     };
