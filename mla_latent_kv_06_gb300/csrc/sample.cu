@@ -141,24 +141,22 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
-// c = 256 log2(e) / T = hi + lo.  256 log2 of a weight is x c - top, top being max c
-// rounded up to an integer (the common factor cancels wherever weights are used).  Where
-// max c is too large for that (not fast), it is (x - max) c, with x - max by two-sum.
-// Logits below `least` have no weight.
+// c = 256 log2(e) / T = hi + lo.  256 log2 of a weight is y c - top with y = x - shift: shift
+// 0 and top max c rounded up to an integer (the common factor cancels wherever weights are
+// used), or, where max c is 2^21 or more, shift max and top 0.  x - max is exact then for
+// every x that weighs something: it is within 2% of max.
 struct Heat {
-  float hi, lo, max, least;
+  float hi, lo, max, shift;
+  float least;  // x below it has no weight
+  float none;   // a y without weight
   int top;
-  bool fast;
 };
 __device__ __forceinline__ Heat make_heat(float max, float2 c) {
   const float m = max * c.x;
-  Heat h{c.x, c.y, max, -INFINITY, 0, fabsf(m) < 2097152.f};
-  if (h.fast) {
-    h.top = (int)ceilf(m);
-    h.least = ((float)h.top - kNegligible) / c.x;
-  } else {
-    h.least = max - kNegligible / c.x;  // (rounding moves it by less than the spacing of such logits)
-  }
+  const bool far = !(fabsf(m) < 2097152.f);
+  Heat h{c.x, c.y, max, far ? max : 0.f, 0.f, 0.f, far ? 0 : (int)ceilf(m)};
+  h.none = ((float)h.top - kNegligible) / c.x;
+  h.least = h.shift + h.none;
   return h;
 }
 
@@ -199,30 +197,18 @@ constexpr int kHighBits = 0x40C00000, kLowBits = 0x35400000;
 constexpr int kHighShift = kOne - 21;
 
 // Weights of two logits as hi + lo, hi the rounded sum, below 2^-45 (which rounds to 0) where
-// not in.  x from 2^-kTiny up, |x c| < 2^22.
+// not in.  x as y from 2^-kTiny up, |y c| < 2^22.
 constexpr int kTiny = 126;
 __device__ __forceinline__ void weights(float x0, float x1, bool in0, bool in1, const Heat& h, const int2* table, Two* hi, Two* lo) {
-  Two r;
-  int k0, k1;
-  if (h.fast) {  // `least` itself is 2^-46
-    x0 = in0 ? x0 : h.least;
-    x1 = in1 ? x1 : h.least;
-    const Two x(x0, x1), n(-x0, -x1);
-    const Two z = fma(x, both(h.hi), both(kMagic));
-    r = fma(n, both(h.lo), fma(n, both(h.hi), z - both(kMagic)));
-    float a, b;
-    z.get(&a, &b);
-    k0 = h.top + kMagicBits - __float_as_int(a);
-    k1 = h.top + kMagicBits - __float_as_int(b);
-  } else {
-    const Two x(in0 ? x0 : h.max, in1 ? x1 : h.max), d = both(h.max) - x, b = d - both(h.max), dl = (both(h.max) - (d - b)) - (x + b);
-    const Two z = fma(d, both(h.hi), both(kMagic));
-    r = (fma(d, both(h.hi), both(kMagic) - z)) + fma(d, both(h.lo), dl * both(h.hi));
-    float a, c;
-    z.get(&a, &c);
-    k0 = in0 ? min(__float_as_int(a) - kMagicBits, kTiny * 256) : kTiny * 256;
-    k1 = in1 ? min(__float_as_int(c) - kMagicBits, kTiny * 256) : kTiny * 256;
-  }
+  float y0, y1, z0, z1;
+  (Two(x0, x1) - both(h.shift)).get(&y0, &y1);
+  y0 = in0 ? y0 : h.none;  // 2^-46
+  y1 = in1 ? y1 : h.none;
+  const Two y(y0, y1), n(-y0, -y1);
+  const Two z = fma(y, both(h.hi), both(kMagic));
+  const Two r = fma(n, both(h.lo), fma(n, both(h.hi), z - both(kMagic)));
+  z.get(&z0, &z1);
+  const int k0 = h.top + kMagicBits - __float_as_int(z0), k1 = h.top + kMagicBits - __float_as_int(z1);
   const int2 t0 = table[k0 & 255], t1 = table[k1 & 255];
   constexpr float kStep = -0.0027076061740622863f;  // -ln(2) / 256
   const Two q = fma(r, fma(r, fma(r, both(kStep * kStep * kStep / 6.f), both(kStep * kStep / 2.f)), both(kStep)),
@@ -821,7 +807,7 @@ __device__ __forceinline__ bool nucleus(cg::cluster_group& cluster, Shared& sh, 
 
 // All filters and the draw among the n tokens of the list, which hold the first k of the row.
 // Sets the row's threshold, returns the mass kept; *token, if wanted: the token drawn.
-__device__ __forceinline__ u64 small_row(Shared& sh, Row& row, int n, int k, float p, const float* u, int32_t* token) {
+__device__ __forceinline__ u64 small_row(Shared& sh, Row& row, int n, int k, float p, float u, int32_t* token) {
   rank_list(sh, row.heat, n);
   int m = min(k, n);
   if (p < 1.f) m = pick_entry(sh, 0, wanted(p, sh.sum[m - 1]), m) + 1;
@@ -835,7 +821,7 @@ __device__ __forceinline__ u64 small_row(Shared& sh, Row& row, int n, int k, flo
     }
     sort_list(sh.list, m);
     sum_list(sh, row.heat, m, [&](int i) { return logit_of((unsigned)sh.list[i]); });
-    const int i = pick_entry(sh, 0, drawn(*u, whole) + 1, m);
+    const int i = pick_entry(sh, 0, drawn(u, whole) + 1, m);
     if (threadIdx.x == 0) *token = (int32_t)(kIndexMask - (sh.list[i] >> 32));
   }
   return whole;
@@ -886,7 +872,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
   load_part<Tin>(src - head, part_sh, (long long)rank * part, row.lo, row.hi, head, a.V);
   float heat = a.temperature ? a.temperature[set] : 1.f;
   int k = a.top_k ? a.top_k[set] : 0;
-  const float p = a.top_p ? a.top_p[set] : 1.f, least = a.min_p ? a.min_p[set] : 0.f;
+  const float p = a.top_p ? a.top_p[set] : 1.f, least = a.min_p ? a.min_p[set] : 0.f, u = a.u ? a.u[r] : 0.f;
   if (tid < 256) sh.table[tid] = make_int2(kTable.hi[tid], __float_as_int(kTable.d[tid]));
   if (heat == 0.f) {
     heat = 1.f;
@@ -997,7 +983,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
       const int n = collect<Tin>(cluster, sh, row, [&](float x, int) { return Bins::index(bins.at(x)) <= b0; });
       few = n <= kList;
       if (few) {
-        total = small_row(sh, row, n, k, p, a.token ? a.u + r : nullptr, a.token && rank == 0 ? a.token + r : nullptr);
+        total = small_row(sh, row, n, k, p, u, a.token && rank == 0 ? a.token + r : nullptr);
         done = true;
       } else {
         __syncthreads();  // (sh.listed has been read)
@@ -1069,7 +1055,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
   if (a.token && !done) {
     // the CTA, the warp, the element at which the running mass exceeds t < total
     const Bounds<kN> bounds(row, true);
-    u64 t = drawn(a.u[r], total);
+    u64 t = drawn(u, total);
     for (int q = 0; q < rank; ++q) t -= sh.mass[q];  // (wraps where the draw is before this CTA)
     if (t < sh.mass[rank]) {
       int w = 0;
@@ -1109,10 +1095,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
     const float t_hi = __ull2float_rn(total), t_lo = (float)(long long)(total - __float2ull_rn(t_hi));
     const float inv = (float)(1ull << kOne) / t_hi;
     const float inv_lo = fmaf(-t_lo, inv, fmaf(-t_hi, inv, (float)(1ull << kOne))) / t_hi;
-    const float tiny = row.heat.least - (256.f * kTiny - kNegligible) / row.heat.hi;
+    const float tiny = row.heat.none - (256.f * kTiny - kNegligible) / row.heat.hi;
     // v = probabilities of x0, x1 at elements i0, i1
     auto probability = [&](float x0, float x1, int i0, int i1, float* v0, float* v1) {
-      const bool in0 = x0 >= tiny && row.kept(x0, i0), in1 = x1 >= tiny && row.kept(x1, i1);
+      const bool in0 = x0 - row.heat.shift >= tiny && row.kept(x0, i0), in1 = x1 - row.heat.shift >= tiny && row.kept(x1, i1);
       *v0 = *v1 = 0.f;
       if (!__any_sync(0xffffffffu, in0 || in1)) return;
       Two hi, lo;
