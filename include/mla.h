@@ -277,8 +277,8 @@ int mla_sparse_decode_paged(const mla_dims* d, int dtype, int B, int S, const vo
  * runs the CUDA-core kernels, each sequence reading the prefix through its own table.
  * Arithmetic and bf16 output as mla_decode_tree.  FP8 caches are not served.
  * Errors: as mla_decode_paged; shared < 0 or shared + S above the capacity returns
- * MLA_ERR_INVALID, S above 64, B * S above 8192 and capacities above 2^31 - 1024 rows
- * MLA_ERR_UNSUPPORTED.
+ * MLA_ERR_INVALID, S above 64, B * S above 8192, capacities above 2^31 - 1024 rows and
+ * B * (capacity - shared) above 2^38 MLA_ERR_UNSUPPORTED.
  * ------------------------------------------------------------------------- */
 size_t mla_decode_shared_workspace_size(const mla_dims* d, int dtype, int B, int S, int T_cap, int shared);
 int mla_decode_shared_paged(const mla_dims* d, int dtype, int B, int S, const void* q, const void* Lc_pages,
@@ -576,6 +576,7 @@ int mla_tree_commit_paged(int n, void* const* cache, const int* row_bytes, int B
  *   top_p   keeps, of what the two leave with mass W, the shortest start of
  *           the order whose mass reaches top_p W, one token at least  (>= 1: all)
  *   temperature 0 keeps the first token of the order alone, whatever the others
+ *           (one above 0 but below 4e-34, or above 3e35, acts as these)
  *   token   the least i whose cumulative w, over the kept tokens in index
  *           order, exceeds u times their mass (u below 0 or NaN counts as 0, u
  *           of 1 or more as just below 1)

@@ -1087,6 +1087,9 @@ MLA_EXPORT int mla_decode_shared_paged(const mla_dims* d, int dtype, int B, int 
     return fail(MLA_ERR_UNSUPPORTED, "capacity of %d rows above %d", a.T_cap, mla::kMaxTreeCap);
   if ((long long)B * S > mla::kMaxSharedRows)
     return fail(MLA_ERR_UNSUPPORTED, "%lld query rows above %d", (long long)B * S, mla::kMaxSharedRows);
+  if ((long long)B * (a.T_cap - shared) > mla::kMaxSharedOwn)
+    return fail(MLA_ERR_UNSUPPORTED, "capacity of %lld tokens behind the prefix above %lld",
+                (long long)B * (a.T_cap - shared), mla::kMaxSharedOwn);
   if (!q || !Lc_pages || !Rc_pages || !T || !kv_b || !out) return fail(MLA_ERR_INVALID, "null tensor pointer");
   if (!aligned16(out)) return fail(MLA_ERR_INVALID, "out must be 16-byte aligned");
   a.B = B;
@@ -1117,9 +1120,10 @@ MLA_EXPORT int mla_sample(int B, int N, int V, int dtype, const void* logits, lo
   if (!logits || (!token && !probs)) return fail(MLA_ERR_INVALID, "null logits, or neither token nor probs");
   if (!token != !u) return fail(MLA_ERR_INVALID, "u and token go together");
   const int el = dtype == MLA_F32 ? 4 : 2;
-  if (reinterpret_cast<uintptr_t>(logits) % el || reinterpret_cast<uintptr_t>(probs) % 4)
-    return fail(MLA_ERR_INVALID, "logits and probs must be aligned to their elements");
-  constexpr long long kFar = 1ll << 40;  // strides whose offsets stay within 64 bits
+  const auto at = [](const void* x) { return reinterpret_cast<uintptr_t>(x); };
+  if (at(logits) % el || (at(probs) | at(u) | at(token) | at(temperature) | at(top_k) | at(top_p) | at(min_p)) % 4)
+    return fail(MLA_ERR_INVALID, "tensors must be aligned to their elements");
+  constexpr long long kFar = 1ll << 37;  // strides whose offsets in bytes stay below 2^63
   if ((N > 1 && l_row < V) || l_row < 0 || l_batch < 0 || l_row > kFar || l_batch > kFar)
     return fail(MLA_ERR_INVALID, "logits: rows of %d values need l_row >= V and l_batch >= 0", V);
   if (probs && (p_row < 0 || p_batch < 0 || p_row > kFar || p_batch > kFar || (N > 1 && p_row < V) ||
@@ -1127,7 +1131,6 @@ MLA_EXPORT int mla_sample(int B, int N, int V, int dtype, const void* logits, lo
     return fail(MLA_ERR_INVALID, "probs: rows of %d values overlap with p_row=%lld and p_batch=%lld", V, p_row, p_batch);
   // what is written, against what other rows still read
   const uintptr_t rows = (uintptr_t)B * N, sets = per_row ? rows : (uintptr_t)B;
-  const auto at = [](const void* x) { return reinterpret_cast<uintptr_t>(x); };
   const uintptr_t l_end = at(logits) + ((uintptr_t)(B - 1) * l_batch + (uintptr_t)(N - 1) * l_row + V) * el;
   const uintptr_t p_end = probs ? at(probs) + ((uintptr_t)(B - 1) * p_batch + (uintptr_t)(N - 1) * p_row + V) * 4 : 0;
   const void* in[6] = {logits, u, temperature, top_k, top_p, min_p};

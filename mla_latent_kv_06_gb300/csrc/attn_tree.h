@@ -123,7 +123,7 @@ struct SharedSplits {
   }
   // the chunk that holds unit x: the largest g with N g / G <= x
   static __device__ __forceinline__ int chunk(long long x, long long N, int G) {
-    int g = ((unsigned long long)(x * G) >> 32) == 0 ? (int)((unsigned)(x * G) / (unsigned)N) : (int)(x * G / N);
+    int g = ((unsigned long long)(N * G) >> 32) == 0 ? (int)((unsigned)(x * G) / (unsigned)N) : (int)(x * G / N);
     if (g > G - 1) g = G - 1;
     while (g + 1 < G && over_chunks(N * (g + 1), G) <= x) ++g;
     return g;

@@ -178,6 +178,8 @@ constexpr int kMaxTreeCap = 0x7fffffff - 1023;
 
 // Query rows B * S of a shared-prefix call.
 constexpr int kMaxSharedRows = 8192;
+// Its sequences' own capacities together: their tiles are counted in 32 bits.
+constexpr long long kMaxSharedOwn = 1ll << 38;
 
 struct VerifyArgs {
   int B, S, V;

@@ -874,14 +874,15 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
   int k = a.top_k ? a.top_k[set] : 0;
   const float p = a.top_p ? a.top_p[set] : 1.f, least = a.min_p ? a.min_p[set] : 0.f, u = a.u ? a.u[r] : 0.f;
   if (tid < 256) sh.table[tid] = make_int2(kTable.hi[tid], __float_as_int(kTable.d[tid]));
+  const bool valid = heat >= 0.f && heat < INFINITY && p == p && least == least;
   if (heat == 0.f) {
     heat = 1.f;
     k = 1;
   }
+  heat = fminf(fmaxf(heat, 4e-34f), 3e35f);  // (c and its low part stay normal numbers)
   // the row's constants in double, one thread each: all 512 at the rate of that pipe take 5 us
   if (tid == 0) {
-    // (temperatures outside 4e-34 .. 3e35 act as these)
-    const double c = fmin(fmax(256.0 * 1.4426950408889634 / (double)heat, 1e-33), 1e36);
+    const double c = 256.0 * 1.4426950408889634 / (double)heat;
     sh.heat = make_float2((float)c, (float)(c - (double)(float)c));
   }
   if (tid == 32 && least > 0.f) sh.least = (double)heat * log(fmin((double)least, 1.0));
@@ -924,7 +925,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
   }
   float* out = a.probs ? a.probs + (long long)b * a.p_batch + (long long)node * a.p_row + row.base : nullptr;
   // no finite maximum, NaN or +inf among the logits, or settings that mean nothing
-  if (!(mx > -INFINITY && mx < INFINITY) || !(heat >= 0.f && heat < INFINITY) || p != p || least != least) {
+  if (!(mx > -INFINITY && mx < INFINITY) || !valid) {
     if (rank == 0 && tid == 0) {
       raise_flag(a.flags, MLA_DEV_BAD_VALUE);
       if (a.token) a.token[r] = -1;

@@ -252,6 +252,90 @@ def test_repeats_streams_and_graphs(cuda_lib):
     assert cuda_lib.device_status() == 0
 
 
+def _many(lib, x, u, t, rows, every):
+    token = lib.sample(x, u, **t)
+    host = token.tolist()
+    for r in range(0, len(host), every):
+        _check_row(x[r].cpu().double().numpy(), host[r], None, u[r].item(), **rows[r])
+    for _ in range(20):
+        assert torch.equal(lib.sample(x, u, **t), token)
+    assert lib.device_status() == 0
+
+
+@pytest.mark.parametrize("V", [600, 20000, 131072])
+def test_many_rows_of_small_top_k(cuda_lib, V):
+    """Lists of every length that is ranked by counting or by sorting, one row beside another:
+    the same tokens each time."""
+    R = 256
+    x = _rows(V, R, 90 + V, torch.bfloat16).to(DEV)
+    u = torch.rand(R, generator=torch.Generator().manual_seed(V)).to(DEV)
+    k = [1 + (r * 37) % 512 for r in range(R)]
+    p = [1.0 if r % 3 else 0.9 for r in range(R)]
+    rows = [dict(top_k=a, top_p=float(np.float32(b))) for a, b in zip(k, p)]
+    t = dict(top_k=torch.tensor(k, dtype=torch.int32, device=DEV), top_p=torch.tensor(p, device=DEV))
+    _many(cuda_lib, x, u, t, rows, 5)
+
+
+@pytest.mark.parametrize("p", [0.3, 0.9, 0.999])
+def test_many_rows_of_top_p(cuda_lib, p):
+    R, V = 200, 50257
+    x = torch.cat([_rows(V, R // 2, 7, torch.float32, 0.05), _rows(V, R // 2, 8, torch.float32, 4.0)]).to(DEV)
+    u = torch.rand(R, generator=torch.Generator().manual_seed(9)).to(DEV)
+    t = dict(top_p=torch.full((R,), p, device=DEV))
+    _many(cuda_lib, x, u, t, [dict(top_p=t["top_p"][0].item())] * R, 9)
+
+
+def test_settings_at_the_ends(cuda_lib):
+    """The largest, smallest and meaningless values that each setting may have."""
+    V, top = 2000, 2 ** 31 - 1
+    tiny, huge, most = 2.0 ** -149, 3.0e35, 1 - 2.0 ** -24
+    f = np.float32
+    sets = [dict(top_p=tiny), dict(top_p=-1.0), dict(top_p=-INF), dict(top_p=INF), dict(top_p=most), dict(top_p=2.0 ** -126),
+            dict(min_p=tiny), dict(min_p=-INF), dict(min_p=INF), dict(min_p=most), dict(min_p=2.0), dict(top_k=-5), dict(top_k=-top - 1),
+            dict(top_k=top), dict(top_k=V - 1), dict(temperature=-0.0), dict(temperature=float(f(huge))),
+            dict(temperature=float(f(huge)), top_p=0.25), dict(temperature=float(f(huge)), min_p=0.5, top_k=9),
+            dict(temperature=float(f(4e-34)), top_p=0.75), dict(temperature=2.0 ** -149), dict(temperature=float(f(3.4e38)), top_p=0.5)]
+    R = len(sets)
+    x = _rows(V, R, 60, torch.float32)
+    for i, scale in ((16, 1e35), (17, 1e35), (18, 2e35)):
+        x[i] *= scale
+    u = torch.rand(R, generator=torch.Generator().manual_seed(61))
+    rows = [{**OFF, **s} for s in sets]
+    t = {k: torch.tensor([row[k] for row in rows], dtype=torch.int32 if k == "top_k" else torch.float32) for k in OFF}
+    token, probs = _run(cuda_lib, x, u, t)
+    for r in range(R):
+        _check_row(x[r].double().numpy(), token[r], probs[r], u[r].item(), **rows[r])
+
+
+def test_rows_far_apart(cuda_lib):
+    """Offsets past 32 bits: rows 3 GB apart in what is read and in what is written."""
+    V, step = 1001, (3 << 29) + 3
+    flat = torch.empty(2 * step + V, dtype=torch.bfloat16, device=DEV)
+    x = flat.as_strided((3, V), (step, 1))
+    small = _rows(V, 3, 15, torch.bfloat16).to(DEV)
+    x.copy_(small)
+    u = torch.rand(3, device=DEV)
+    token, probs = cuda_lib.sample(small, u, return_probs=True)
+    far = torch.empty(2 * step + V, dtype=torch.float32, device=DEV).as_strided((3, V), (step, 1))
+    got, there = cuda_lib.sample(x, u, probs=far)
+    assert cuda_lib.device_status() == 0
+    assert torch.equal(got, token) and torch.equal(there, probs)
+
+
+def test_calls_at_once(cuda_lib):
+    """Calls on two streams, each over and over, without a sign of the other."""
+    t = {k: v.to(DEV) for k, v in _settings(40)[1].items()}
+    inputs = [(_rows(V, 40, V, torch.float32).to(DEV), torch.rand(40, device=DEV)) for V in (9000, 70000)]
+    want = [cuda_lib.sample(x, u, return_probs=True, **t) for x, u in inputs]
+    streams = [torch.cuda.Stream() for _ in inputs]
+    torch.cuda.synchronize()
+    got = [[cuda_lib.sample(x, u, return_probs=True, stream=s, **t) for _ in range(10)] for (x, u), s in zip(inputs, streams)]
+    torch.cuda.synchronize()
+    for w, many in zip(want, got):
+        assert all(torch.equal(w[0], g[0]) and torch.equal(w[1], g[1]) for g in many)
+    assert cuda_lib.device_status() == 0
+
+
 def test_draws_follow_the_distribution(cuda_lib):
     """Evenly spaced numbers over one row: every token as often as its probability says, to within one."""
     V, R = 50, 4096

@@ -235,6 +235,64 @@ def test_graphs_that_share_a_workspace(cuda_lib):
     assert cuda_lib.device_status() == 0
 
 
+@pytest.mark.parametrize("dims,dtype,page,pages", [(GLM, "bf16", 128, 34000), (GLM, "f32", 128, 34000), (WIDE, "f32", 32, 130000)])
+def test_rows_far_inside_the_pool(cuda_lib, dims, dtype, page, pages):
+    """Element offsets past 32 bits: the bits of the same pages at the pool's start."""
+    T, S, shared = [700, 650, 530], 2, 512
+    assert pages * page * dims.kv_lora > 2 ** 31
+    x = _batch(dims, dtype, T, S, shared, page, 91)
+    want = _call(cuda_lib, x, shared, dims)
+    g = {k: v.to(DEV) for k, v in x.items()}
+    pools = []
+    for k in ("Lp", "Rp"):
+        pools.append(torch.empty((pages + len(x[k]),) + x[k].shape[1:], dtype=x[k].dtype, device=DEV))
+        pools[-1][pages:] = g[k]
+    out = cuda_lib.decode_shared_paged(g["q"], *pools, g["table"] + pages, g["T"], shared, g["kv_b"], dims)
+    assert torch.equal(out, want)
+    _check(cuda_lib, out, x, T, dims, dtype)
+
+
+def test_calls_at_once(cuda_lib):
+    """Calls of two batches on two streams, each over and over, without a sign of the other."""
+    cases = [(_batch(GLM, "bf16", [1500] * 20, 1, 1280, 128, 95), 1280, GLM), (_batch(GLM, "bf16", [900] * 3, 4, 512, 128, 96), 512, GLM),
+             (_batch(TINY, "f32", [400] * 6, 2, 256, 16, 97), 256, TINY)]
+    on = [({k: v.to(DEV) for k, v in x.items()}, shared, dims) for x, shared, dims in cases]
+    want = [_call(cuda_lib, *c) for c in on]
+    streams = [torch.cuda.Stream() for _ in on]
+    torch.cuda.synchronize()
+    got = [[] for _ in on]
+    for _ in range(8):
+        for c, s, outs in zip(on, streams, got):
+            outs.append(_call(cuda_lib, *c, stream=s))
+    torch.cuda.synchronize()
+    for w, outs in zip(want, got):
+        assert all(torch.equal(w, out) for out in outs)
+    assert cuda_lib.device_status() == 0
+
+
+@pytest.mark.parametrize("B,S", [(8192, 1), (128, 64)])
+def test_the_most_rows(cuda_lib, B, S):
+    """8192 query rows, three of them against the oracle; the sequences' last pages are a few
+    that many of them read."""
+    shared, page = 256, 128
+    T = [shared + S + b % 3 for b in range(B)]
+    g = torch.Generator(device=DEV).manual_seed(99)
+    q = torch.randn(B, S, GLM.H, GLM.qk_nope + GLM.qk_rope, generator=g, device=DEV).bfloat16()
+    Lp = torch.randn(9, page, GLM.kv_lora, generator=g, device=DEV).bfloat16()
+    Rp = torch.randn(9, page, GLM.qk_rope, generator=g, device=DEV).bfloat16()
+    kv_b = (torch.randn(GLM.H, GLM.qk_nope + GLM.v_head, GLM.kv_lora, generator=g, device=DEV) * GLM.kv_lora ** -0.5).bfloat16()
+    table = torch.tensor([[8, 3, [0, 1, 2, 4, 5, 6, 7][b % 7]] for b in range(B)], dtype=torch.int32)
+    length = torch.tensor(T, dtype=torch.int32, device=DEV)
+    out = cuda_lib.decode_shared_paged(q, Lp, Rp, table.to(DEV), length, shared, kv_b, GLM, out_dtype=torch.bfloat16)
+    assert cuda_lib.device_status() == 0 and bool(torch.isfinite(out).all())
+    for b, s in ((0, 0), (B // 2 + 1, S - 1), (B - 1, S // 2)):
+        rows = [oracle.page_row(table.tolist(), b, t, page) for t in range(T[b])]
+        L, R = (to_np(x.flatten(0, 1)[rows]) for x in (Lp, Rp))
+        pos = T[b] - S + s
+        ref = oracle.attend_absorbed(to_np(q[b, s]), L[:pos + 1], R[:pos + 1], to_np(kv_b), GLM.qk_nope, pos, GLM.softmax_scale)
+        check_close(to_np(out[b, s]), ref, TOL["bf16"] + 2.0 ** -8, (b, s))
+
+
 def test_continuations_of_one_prompt(cuda_lib):
     """A run as a server makes it: the prompt's rows appended once, then steps of every
     continuation -- append, shared attention, a stand-in for the rest of the model, sampling --

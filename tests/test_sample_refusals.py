@@ -32,7 +32,9 @@ def test_arguments(lib):
                 dict(token=None, u=None, probs=None), dict(u=None), dict(token=None), dict(l_row=99), dict(l_row=-1, N=1),
                 dict(l_batch=-1), dict(l_row=1 << 41), dict(l_batch=1 << 41), dict(p_row=99), dict(p_batch=299), dict(p_batch=-1),
                 dict(p_row=1 << 41, B=1), dict(logits=_at((1 << 30) + 2)), dict(logits=_at((1 << 30) + 1), dtype=1),
-                dict(probs=_at((5 << 30) + 2))):
+                dict(probs=_at((5 << 30) + 2)), dict(l_row=(1 << 37) + 1), dict(u=_at((3 << 30) + 1)), dict(token=_at((4 << 30) + 2)),
+                dict(temperature=_at((2 << 30) + 2)), dict(top_k=_at((2 << 30) + 1)), dict(top_p=_at((2 << 30) + 3)),
+                dict(min_p=_at((2 << 30) + 2))):
         assert _call(lib, **bad) == mla.MLA_ERR_INVALID, bad
     assert _call(lib, V=327681, l_row=327681, p_row=327681, p_batch=1 << 20) == mla.MLA_ERR_UNSUPPORTED
     assert b"327680" in lib.mla_last_error()

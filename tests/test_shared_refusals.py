@@ -36,6 +36,7 @@ def test_arguments(lib):
     assert _call(lib, S=65) == mla.MLA_ERR_UNSUPPORTED and b"64" in lib.mla_last_error()
     assert _call(lib, max_pages=((1 << 31) - 127) // 128) == mla.MLA_ERR_UNSUPPORTED
     assert _call(lib, num_pages=1 << 25) == mla.MLA_ERR_UNSUPPORTED
+    assert _call(lib, B=300, S=1, max_pages=(1 << 30) // 128) == mla.MLA_ERR_UNSUPPORTED and b"behind" in lib.mla_last_error()
 
 
 def test_workspace_size(lib):
