@@ -24,17 +24,18 @@
 // weight is an integer, w 2^44 rounded once: sums are then exact, in any order,
 // and the kernel's atomics cannot change a result.  The exponential is taken
 // without the fp64 pipe (1/64 of the fp32 rate) and without 64-bit shifts:
-//   z = x c rounded to an integer, c = 256 log2(e) / T, r = z - x c by two fused
-//   multiply-adds whose products are exact; k = top - z with top >= max c, so that
-//   w = 2^(-k/256) 2^(-r/256);
-//   a table of 2^(-i/256) as hi (1 + d) for the low 8 bits of k, the others moved into
-//   hi's exponent by one multiply-add (the table's entry holds i times that step, too);
-//   a cubic for 2^(-r/256) + d, whose product with hi is the weight's low part;
-//   the two parts added to 6 and to 1.5 2^-21, whose last places are 2^-21 and 2^-44:
-//   the integers are then in the sums' bits, and are added up as such.
-// The error is below 2^-31 of the weight (rms 2^-34) before the rounding.  Two
-// elements go through packed fp32 instructions; 71 instructions an element with
-// 64-bit integers, conversions and one element at a time.
+//   z = y c rounded to an integer, c = 256 log2(e) / T, t = y c - z by two fused
+//   multiply-adds whose products are exact; relative to an integer `top` above max c,
+//   w = 2^((z - top)/256) 2^(t/256);
+//   a table of 2^(-i/256) as hi (1 + d) for the low 8 bits of top - z, the others moved into
+//   hi's exponent by one addition (the table's entry holds i times that step, too);
+//   a cubic for 2^(t/256) - 1 + d, whose product with hi is the weight's low part;
+//   the two parts added to 3 and to 1.5 2^-21, whose last places are 2^-22 and 2^-44:
+//   the integers are then in the sums' bits, and are added up as such.  (What the second
+//   sum takes, up to 2^-23 and the low part's rounding, must stay inside its binade.)
+// The error is below 2^-31 of the weight before the rounding.  Two elements go through
+// packed fp32 instructions; 71 instructions an element with 64-bit integers, conversions
+// and one element at a time.
 //
 // A row is a cluster of up to 8 CTAs, each with a contiguous part of the
 // vocabulary in shared memory, read once, 16 bytes at a time from 16-byte
@@ -105,8 +106,7 @@ struct Shared {
   };
   u64 tot[kBins];                             // the cluster's, written by all CTAs
   u64 list[kList], sum[kList];  // codes; running mass once ranked
-  int2 table[256];   // (hi, d's bits)
-  float2 heat;       // c as a pair
+  int2 table[256];   // of i at -i mod 256: (hi, d's bits)
   double least;      // T log(min_p)
   float max[kCluster], min[kCluster];
   int first[kCluster];
@@ -142,20 +142,30 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 }
 
 // c = 256 log2(e) / T = hi + lo.  256 log2 of a weight is y c - top with y = x - shift: shift
-// 0 and top max c rounded up to an integer (the common factor cancels wherever weights are
+// 0 and top an integer above max c (the common factor cancels wherever weights are
 // used), or, where max c is 2^21 or more, shift max and top 0.  x - max is exact then for
 // every x that weighs something: it is within 2% of max.
+constexpr int kMagicBits = 0x4B400000;
+constexpr float kMagic = 12582912.f;  // 1.5 2^23: adding it rounds to an integer, in the low bits
 struct Heat {
   float hi, lo, max, shift;
+  float magic;  // kMagic - top
   float least;  // x below it has no weight
   float none;   // a y without weight
-  int top;
 };
-__device__ __forceinline__ Heat make_heat(float max, float2 c) {
-  const float m = max * c.x;
+__device__ __forceinline__ Heat make_heat(float max, float heat) {
+  constexpr double kC = 256.0 * 1.4426950408889634;
+  constexpr float kHi = (float)kC, kLo = (float)(kC - (double)kHi);
+  Heat h;
+  h.max = max;
+  h.hi = kHi / heat;
+  h.lo = (fmaf(-h.hi, heat, kHi) + kLo) / heat;
+  const float m = max * h.hi;
   const bool far = !(fabsf(m) < 2097152.f);
-  Heat h{c.x, c.y, max, far ? max : 0.f, 0.f, 0.f, far ? 0 : (int)ceilf(m)};
-  h.none = ((float)h.top - kNegligible) / c.x;
+  const float top = far ? 0.f : ceilf(m) + 1.f;
+  h.shift = far ? max : 0.f;
+  h.magic = kMagic - top;
+  h.none = (top - kNegligible) / h.hi;
   h.least = h.shift + h.none;
   return h;
 }
@@ -189,48 +199,50 @@ __device__ __forceinline__ Two fma(Two a, Two b, Two c) {
   return r;
 }
 
-constexpr int kMagicBits = 0x4B400000;
-constexpr float kMagic = 12582912.f;  // 1.5 2^23: adding it rounds to an integer, in the low bits
-// Adding these rounds to multiples of 2^-21 and 2^-44.
-constexpr float kHigh = 6.f, kLow = 1.5f / 2097152.f;
-constexpr int kHighBits = 0x40C00000, kLowBits = 0x35400000;
-constexpr int kHighShift = kOne - 21;
+// Adding these rounds to multiples of 2^-22 and 2^-44, whatever is added: up to 1, and up to 2^-22.
+constexpr float kHigh = 3.f, kLow = 1.5f / 2097152.f;
+constexpr int kHighBits = 0x40400000, kLowBits = 0x35400000;
+constexpr int kHighShift = kOne - 22;
 
-// Weights of two logits as hi + lo, hi the rounded sum, below 2^-45 (which rounds to 0) where
-// not in.  x as y from 2^-kTiny up, |y c| < 2^22.
+// Weights of two y as w + l, |l| below 2^-9 w.  y from 2^-kTiny up, |y c| < 2^22.
 constexpr int kTiny = 126;
-__device__ __forceinline__ void weights(float x0, float x1, bool in0, bool in1, const Heat& h, const int2* table, Two* hi, Two* lo) {
-  float y0, y1, z0, z1;
-  (Two(x0, x1) - both(h.shift)).get(&y0, &y1);
-  y0 = in0 ? y0 : h.none;  // 2^-46
-  y1 = in1 ? y1 : h.none;
-  const Two y(y0, y1), n(-y0, -y1);
-  const Two z = fma(y, both(h.hi), both(kMagic));
-  const Two r = fma(n, both(h.lo), fma(n, both(h.hi), z - both(kMagic)));
+__device__ __forceinline__ void weigh(Two y, const Heat& h, const int2* table, Two* w, Two* l) {
+  const Two z = fma(y, both(h.hi), both(h.magic));
+  const Two t = fma(y, both(h.lo), fma(y, both(h.hi), both(h.magic) - z));
+  float z0, z1;
   z.get(&z0, &z1);
-  const int k0 = h.top + kMagicBits - __float_as_int(z0), k1 = h.top + kMagicBits - __float_as_int(z1);
-  const int2 t0 = table[k0 & 255], t1 = table[k1 & 255];
-  constexpr float kStep = -0.0027076061740622863f;  // -ln(2) / 256
-  const Two q = fma(r, fma(r, fma(r, both(kStep * kStep * kStep / 6.f), both(kStep * kStep / 2.f)), both(kStep)),
+  const unsigned b0 = __float_as_uint(z0), b1 = __float_as_uint(z1);
+  const int2 t0 = table[b0 & 255], t1 = table[b1 & 255];
+  constexpr float kStep = 0.0027076061740622863f;  // ln(2) / 256
+  const Two q = fma(t, fma(t, fma(t, both(kStep * kStep * kStep / 6.f), both(kStep * kStep / 2.f)), both(kStep)),
                     Two(__int_as_float(t0.y), __int_as_float(t1.y)));
-  const Two w(__int_as_float(t0.x - k0 * 32768), __int_as_float(t1.x - k1 * 32768));
-  const Two l = w * q, s = w + l;
-  *hi = s;
-  *lo = l - (s - w);
+  *w = Two(__uint_as_float((unsigned)t0.x + (b0 << 15)), __uint_as_float((unsigned)t1.x + (b1 << 15)));
+  *l = *w * q;
 }
 
-// The integers of two weights, w 2^44 = (a - kHighBits) 2^23 + (b - kLowBits).
+// The integers of two weights, w 2^44 = (a - kHighBits) 2^22 + (b - kLowBits).
 struct Units {
   int a[2], b[2];
 };
-__device__ __forceinline__ Units units(float x0, float x1, bool in0, bool in1, const Heat& h, const int2* table) {
-  Two hi, lo;
-  weights(x0, x1, in0, in1, h, table, &hi, &lo);
-  const Two z = hi + both(kHigh), y = ((hi - (z - both(kHigh))) + lo) + both(kLow);
+__device__ __forceinline__ Units units(Two y, const Heat& h, const int2* table) {
+  Two w, l;
+  weigh(y, h, table, &w, &l);
+  const Two z = (w + l) + both(kHigh), x = ((w - (z - both(kHigh))) + l) + both(kLow);  // (w - z exact)
   float a, b, c, d;
   z.get(&a, &b);
-  y.get(&c, &d);
+  x.get(&c, &d);
   return Units{{__float_as_int(a), __float_as_int(b)}, {__float_as_int(c), __float_as_int(d)}};
+}
+// Of two logits: 0 where not in, or (units_all) below least.
+__device__ __forceinline__ Units units(float x0, float x1, bool in0, bool in1, const Heat& h, const int2* table) {
+  float y0, y1;
+  (Two(x0, x1) - both(h.shift)).get(&y0, &y1);
+  return units(Two(in0 ? y0 : h.none, in1 ? y1 : h.none), h, table);
+}
+__device__ __forceinline__ Units units_all(float x0, float x1, const Heat& h, const int2* table) {
+  float y0, y1;
+  (Two(x0, x1) - both(h.shift)).get(&y0, &y1);
+  return units(Two(fmaxf(y0, h.none), fmaxf(y1, h.none)), h, table);
 }
 __device__ __forceinline__ u64 weight_of(const Units& u, int j) {
   return ((u64)(unsigned)(u.a[j] - kHighBits) << kHighShift) + (u64)(long long)(u.b[j] - kLowBits);
@@ -831,25 +843,24 @@ __device__ __forceinline__ u64 small_row(Shared& sh, Row& row, int n, int k, flo
 // units at the row's ends element by element, -inf outside the row.  Elements
 // [head, head + V) of the padded row, whose element 0 lies at the 16-byte boundary `src`.
 template <typename Tin>
-__device__ __forceinline__ void load_part(const Tin* src, unsigned char* dst, long long start, int lo, int hi, int head, int V) {
+__device__ __forceinline__ void load_part(const Tin* src, unsigned char* dst, int start, int lo, int hi, int head, int V) {
   constexpr int kN = Vec<Tin>::kN;
   for (int i = lo + kN * (int)(threadIdx.x & 31); i < hi; i += 32 * kN) {
-    const long long at = start + i;
-    if (at >= head && at + kN <= (long long)head + V) {
+    const int at = start + i;
+    if (at >= head && at + kN <= head + V) {
       const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst + (size_t)i * sizeof(Tin)));
       asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src + at) : "memory");
     } else {
       Tin* out = reinterpret_cast<Tin*>(dst) + i;
 #pragma unroll
       for (int j = 0; j < kN; ++j)
-        out[j] = at + j >= head && at + j < (long long)head + V ? src[at + j] : static_cast<Tin>(-INFINITY);
+        out[j] = at + j >= head && at + j < head + V ? src[at + j] : static_cast<Tin>(-INFINITY);
     }
   }
-  asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
 }
 
 template <typename Tin>
-__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a, int part) {
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a) {
   constexpr int kN = Vec<Tin>::kN;
   extern __shared__ __align__(16) unsigned char part_sh[];
   __shared__ Shared sh;
@@ -862,30 +873,32 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
 
   Row row;
   row.part = part_sh;
-  row.lo = warp * (part / kWarps);
-  row.hi = row.lo + part / kWarps;
   const Tin* src = static_cast<const Tin*>(a.logits) + (long long)b * a.l_batch + (long long)node * a.l_row;
   const int head = (int)((reinterpret_cast<uintptr_t>(src) & 15) / sizeof(Tin));
-  row.base = rank * part - head;
+  // the padded row in units of a warp's vectors: CTA q has those from first(q) on
+  constexpr int kUnit = 32 * kN;
+  const int n_units = (head + a.V + kUnit - 1) / kUnit;
+  const auto first = [&](int q) { return n_units * q / C; };
+  const int u0 = first(rank), mine_units = first(rank + 1) - u0;
+  row.lo = mine_units * warp / kWarps * kUnit;
+  row.hi = mine_units * (warp + 1) / kWarps * kUnit;
+  row.base = u0 * kUnit - head;
   row.from = max(0, -row.base);
-  row.to = (int)min((long long)part, (long long)a.V - row.base);
-  load_part<Tin>(src - head, part_sh, (long long)rank * part, row.lo, row.hi, head, a.V);
+  row.to = min(mine_units * kUnit, a.V - row.base);
   float heat = a.temperature ? a.temperature[set] : 1.f;
   int k = a.top_k ? a.top_k[set] : 0;
   const float p = a.top_p ? a.top_p[set] : 1.f, least = a.min_p ? a.min_p[set] : 0.f, u = a.u ? a.u[r] : 0.f;
-  if (tid < 256) sh.table[tid] = make_int2(kTable.hi[tid], __float_as_int(kTable.d[tid]));
+  load_part<Tin>(src - head, part_sh, u0 * kUnit, row.lo, row.hi, head, a.V);
+  if (tid < 256) sh.table[-tid & 255] = make_int2(kTable.hi[tid], __float_as_int(kTable.d[tid]));
   const bool valid = heat >= 0.f && heat < INFINITY && p == p && least == least;
   if (heat == 0.f) {
     heat = 1.f;
     k = 1;
   }
   heat = fminf(fmaxf(heat, 4e-34f), 3e35f);  // (c and its low part stay normal numbers)
-  // the row's constants in double, one thread each: all 512 at the rate of that pipe take 5 us
-  if (tid == 0) {
-    const double c = 256.0 * 1.4426950408889634 / (double)heat;
-    sh.heat = make_float2((float)c, (float)(c - (double)(float)c));
-  }
+  // (in double by one thread: all 512 at the rate of that pipe take 5 us)
   if (tid == 32 && least > 0.f) sh.least = (double)heat * log(fmin((double)least, 1.0));
+  asm volatile("cp.async.wait_all;" ::: "memory");
   // the thread's, the CTA's and the row's largest value (NaN if one is) and smallest
   typename Vec<Tin>::Extremes extremes;
   for (int i = row.lo + kN * lane; i < row.hi; i += 32 * kN)
@@ -934,7 +947,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
       for (int i = max(row.lo, row.from) + lane; i < min(row.hi, row.to); i += 32) out[i] = qnan();
     return;
   }
-  row.heat = make_heat(mx, sh.heat);
+  row.heat = make_heat(mx, heat);
   row.thr = -INFINITY;
   row.last = INT_MIN;
   if (least > 0.f) {  // w >= least, as a bound of x
@@ -1007,9 +1020,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
     // the CTAs' and this CTA's warps' kept masses: above the interval, and from the list
     u64 mine = 0, theirs = 0;
     for (int i = lane; i <= sh.pick; i += 32) {
-      const int at = (int)(kIndexMask - (sh.list[i] & kIndexMask)) + head, own = at - rank * part;
+      const int at = (int)(kIndexMask - (sh.list[i] & kIndexMask)) + head, own = at - u0 * kUnit;
       const u64 w = sh.sum[i] - (i ? sh.sum[i - 1] : 0);
-      if (at >= warp * part && at < (warp + 1) * part) theirs += w;  // (of CTA `warp`)
+      if (at >= first(warp) * kUnit && at < first(warp + 1) * kUnit) theirs += w;  // (of CTA `warp`)
       if (own >= row.lo && own < row.hi) mine += w;
     }
     mine = warp_sum64(mine);
@@ -1023,22 +1036,21 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
   if (!done && !listed && (a.token || p >= 1.f)) {
     const Bounds<kN> bounds(row, true);
     const bool dense = row.thr == -INFINITY;
-    unsigned high = 0, low = 0;  // sums of the weights' integers: at most part / kThreads < 2^8 of them
+    unsigned high = 0, low = 0;  // sums of the weights' integers: less than 2^8 of them
     for_each<Tin>(row, [&](const auto& x, int i) {
-      bool in[kN];
-      bounds.test(x, i, in);
-      auto add = [&](int j) {
-        const Units w = units(x[j], x[j + 1], in[j], in[j + 1], row.heat, sh.table);
+      auto add = [&](const Units& w) {
         high += (unsigned)(w.a[0] + w.a[1]) - 2u * kHighBits;
         low += (unsigned)(w.b[0] + w.b[1]) - 2u * kLowBits;
       };
       if (dense) {  // straight through, so that the vector's chains overlap
 #pragma unroll
-        for (int j = 0; j < kN; j += 2) add(j);
+        for (int j = 0; j < kN; j += 2) add(units_all(x[j], x[j + 1], row.heat, sh.table));
       } else {
+        bool in[kN];
+        bounds.test(x, i, in);
 #pragma unroll
         for (int j = 0; j < kN; j += 2)
-          if (__any_sync(0xffffffffu, in[j] || in[j + 1])) add(j);
+          if (__any_sync(0xffffffffu, in[j] || in[j + 1])) add(units(x[j], x[j + 1], in[j], in[j + 1], row.heat, sh.table));
       }
     });
     u64 mine = ((u64)high << kHighShift) + (u64)(long long)(int)low;
@@ -1102,8 +1114,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
       const bool in0 = x0 - row.heat.shift >= tiny && row.kept(x0, i0), in1 = x1 - row.heat.shift >= tiny && row.kept(x1, i1);
       *v0 = *v1 = 0.f;
       if (!__any_sync(0xffffffffu, in0 || in1)) return;
-      Two hi, lo;
-      weights(x0, x1, in0, in1, row.heat, sh.table, &hi, &lo);
+      Two w, l;
+      weigh(Two(in0 ? x0 - row.heat.shift : row.heat.none, in1 ? x1 - row.heat.shift : row.heat.none), row.heat, sh.table, &w, &l);
+      const Two hi = w + l, lo = l - (hi - w);
       float a0, a1;
       fma(hi, both(inv), fma(hi, both(inv_lo), lo * both(inv))).get(&a0, &a1);
       *v0 = !in0 ? 0.f : k == 1 ? 1.f : a0;
@@ -1152,17 +1165,17 @@ cudaError_t launch(const SampleArgs& a, cudaStream_t st) {
     done.fetch_or(bit);
   }
   // as few CTAs a row as leave room for two on an SM, more while the GPU is not full
-  constexpr int kN = Vec<Tin>::kN, kUnit = kThreads * kN, kHalf = 73728;
+  constexpr int kN = Vec<Tin>::kN, kUnit = 32 * kN, kHalf = 73728;
   const long long rows = (long long)a.B * a.N;
-  const int padded = a.V + kN - 1;
+  const int units = (a.V + kN - 1 + kUnit - 1) / kUnit;  // (wherever the row begins in its first vector)
+  const auto part = [&](int C) { return (size_t)((units + C - 1) / C) * kUnit * sizeof(Tin); };
   int C = 1;
-  while (C < kCluster && (padded + C - 1) / C * (int)sizeof(Tin) > kHalf) C *= 2;
-  while (C < kCluster && rows * C * 2 <= sms && padded / C > 2048) C *= 2;
-  const int part = ((padded + C - 1) / C + kUnit - 1) / kUnit * kUnit;
+  while (C < kCluster && part(C) > kHalf) C *= 2;
+  while (C < kCluster && rows * C * 2 <= sms && a.V / C > 2048) C *= 2;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(rows * C));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = (size_t)part * sizeof(Tin);
+  cfg.dynamicSmemBytes = part(C);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1170,7 +1183,7 @@ cudaError_t launch(const SampleArgs& a, cudaStream_t st) {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, sample_kernel<Tin>, a, part);
+  return cudaLaunchKernelEx(&cfg, sample_kernel<Tin>, a);
 }
 
 }  // namespace

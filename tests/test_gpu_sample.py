@@ -336,6 +336,32 @@ def test_calls_at_once(cuda_lib):
     assert cuda_lib.device_status() == 0
 
 
+@pytest.mark.parametrize("offset,heat", [(0.0, 1.0), (0.0, 0.37), (-2000.0, 1.0), (2000.0, 1.0), (10000.0, 1.0), (-3e5, 7.0), (40.0, 3.0)])
+def test_weights_one_by_one(cuda_lib, offset, heat):
+    """A run of very light tokens between many of one weight and many of another: the token
+    drawn there tells the weights' errors, 2^-31 of each at most, to a few parts in 2^38."""
+    R, V, n = 64, 327680, 150000
+    g = np.random.default_rng(7)
+    ld, T = np.longdouble, np.longdouble(np.float32(heat))
+    top, low = np.float32(offset), np.float32(offset) - np.float32(14.0 * heat)
+    mid = top - (g.random(R) * 0.69 * heat + 1e-3).astype(np.float32)
+    x = torch.empty(R, V)
+    x[:, :n] = torch.from_numpy(mid)[:, None]
+    x[:, n:V - n] = float(low)
+    x[:, V - n:] = float(top)
+    wm, wl = np.exp((mid.astype(ld) - ld(top)) / T), np.exp((ld(low) - ld(top)) / T)
+    before, run = n * wm, (V - 2 * n) * wl
+    whole = before + run + n
+    u = ((before + run / 2) / whole).astype(np.float32)
+    want = n + np.floor((u.astype(ld) * whole - before) / wl).astype(np.int64)
+    there = (want > n + 100) & (want < V - n - 100)
+    assert there.sum() > R // 4
+    token = cuda_lib.sample(x.to(DEV), torch.from_numpy(u).to(DEV), temperature=torch.full((R,), heat, device=DEV)).cpu().numpy()
+    assert cuda_lib.device_status() == 0
+    off = np.abs(token - want)[there] * (wl / whole[there])  # of the mass
+    assert off.max() < 2.0 ** -31, np.log2(off.astype(float).max())
+
+
 def test_draws_follow_the_distribution(cuda_lib):
     """Evenly spaced numbers over one row: every token as often as its probability says, to within one."""
     V, R = 50, 4096
