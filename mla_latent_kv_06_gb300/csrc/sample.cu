@@ -294,6 +294,11 @@ struct Vec<float> {
     x[2] = __uint_as_float(v.z);
     x[3] = __uint_as_float(v.w);
   }
+  static __device__ __forceinline__ float max(const uint4& v) {
+    float x[4];
+    get(v, x);
+    return fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+  }
   // running largest (NaN if one is) and smallest value
   struct Extremes {
     float mx = -INFINITY, mn = INFINITY;
@@ -320,6 +325,13 @@ struct Vec<__nv_bfloat16> {
       x[2 * i] = __uint_as_float(w[i] << 16);
       x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
+  }
+  static __device__ __forceinline__ float max(const uint4& v) {
+    uint32_t m, n;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(v.x), "r"(v.y));
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(n) : "r"(v.z), "r"(v.w));
+    asm("max.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(n));
+    return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
   }
   struct Extremes {  // two values an instruction
     uint32_t mx = 0xff80ff80u, mn = 0x7f807f80u;
@@ -389,6 +401,8 @@ struct Bins {
   __device__ __forceinline__ float at(float x) const {
     return fminf(fmaxf(fmaf(-x, step, off), 0.f), (float)(kBins - 1));
   }
+  // a bound below every x of the intervals up to b, the last one aside
+  __device__ __forceinline__ float from(int b) const { return step > 0.f ? (off - (float)(b + 1) - fabsf(off) * 0x1p-22f) / step : -INFINITY; }
   __device__ __forceinline__ float raw(float x) const { return fmaf(-x, step, off); }
   static __device__ __forceinline__ int index(float f) { return (__float_as_int(f + kMagic) - kMagicBits) & (kBins - 1); }
   // finer intervals inside interval b
@@ -404,6 +418,19 @@ __device__ __forceinline__ void for_each(const Row& row, F&& f) {
   for (int i = row.lo + kN * (int)(threadIdx.x & 31); i < row.hi; i += 32 * kN) {
     float x[kN];
     Vec<Tin>::get(*reinterpret_cast<const uint4*>(row.part + (size_t)i * sizeof(Tin)), x);
+    f(x, i);
+  }
+}
+
+// The same without the steps in which no lane's vector has an x from `bound` up.
+template <typename Tin, typename F>
+__device__ __forceinline__ void for_each_from(const Row& row, float bound, F&& f) {
+  constexpr int kN = Vec<Tin>::kN;
+  for (int i = row.lo + kN * (int)(threadIdx.x & 31); i < row.hi; i += 32 * kN) {
+    const uint4 v = *reinterpret_cast<const uint4*>(row.part + (size_t)i * sizeof(Tin));
+    if (!__any_sync(0xffffffffu, Vec<Tin>::max(v) >= bound)) continue;
+    float x[kN];
+    Vec<Tin>::get(v, x);
     f(x, i);
   }
 }
@@ -557,12 +584,13 @@ __device__ __forceinline__ int pick_entry(Shared& sh, u64 above, u64 target, int
   return sh.pick;
 }
 
-// The codes of the kept tokens for which in(x, i) holds, in every CTA's list.  Their number, or one above kList where the list does not hold them all.  One cluster barrier.
+// The codes of the kept tokens for which in(x, i) holds (none of them below `from`), in every
+// CTA's list.  Their number, or one above kList where the list does not hold them all.  One cluster barrier.
 template <typename Tin, typename F>
-__device__ __forceinline__ int collect(cg::cluster_group& cluster, Shared& sh, const Row& row, F&& in) {
+__device__ __forceinline__ int collect(cg::cluster_group& cluster, Shared& sh, const Row& row, float from, F&& in) {
   constexpr int kN = Vec<Tin>::kN;
   const Bounds<kN> bounds(row, false);
-  for_each<Tin>(row, [&](const auto& x, int i) {
+  for_each_from<Tin>(row, fmaxf(from, row.thr), [&](const auto& x, int i) {
     bool take[kN], any = false;
     bounds.test(x, i, take);
 #pragma unroll
@@ -659,7 +687,7 @@ __device__ __forceinline__ u64 select(cg::cluster_group& cluster, Shared& sh, Ro
       const u64 width = (1ull << shift) - 1;
       if (hi - lo > width) lo = hi - width;
     }
-    n = collect<Tin>(cluster, sh, row, [&](float x, int i) { return candidate(x, i, level + 1); });
+    n = collect<Tin>(cluster, sh, row, b0 < kBins - 1 ? bins.from(b0) : -INFINITY, [&](float x, int i) { return candidate(x, i, level + 1); });
     if (n <= kList) break;
     ++level;
     if (level >= 2) {  // by codes
@@ -959,7 +987,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   bool done = false;  // token and total are known
   if (k == 1) {       // the first token of the order
     int first = INT_MAX;
-    for_each<Tin>(row, [&](const auto& x, int i) {
+    for_each_from<Tin>(row, mx, [&](const auto& x, int i) {
 #pragma unroll
       for (int j = kN - 1; j >= 0; --j)
         if (x[j] == mx) first = min(first, row.base + i + j);
@@ -994,7 +1022,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       sum_bins<false>(cluster, sh);
       find_bin(sh, 0, [&](u64) { return (u64)k; });
       const int b0 = sh.bin;
-      const int n = collect<Tin>(cluster, sh, row, [&](float x, int) { return Bins::index(bins.at(x)) <= b0; });
+      const int n = collect<Tin>(cluster, sh, row, b0 < kBins - 1 ? bins.from(b0) : -INFINITY, [&](float x, int) { return Bins::index(bins.at(x)) <= b0; });
       few = n <= kList;
       if (few) {
         total = small_row(sh, row, n, k, p, u, a.token && rank == 0 ? a.token + r : nullptr);
@@ -1035,24 +1063,25 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   }
   if (!done && !listed && (a.token || p >= 1.f)) {
     const Bounds<kN> bounds(row, true);
-    const bool dense = row.thr == -INFINITY;
     unsigned high = 0, low = 0;  // sums of the weights' integers: less than 2^8 of them
-    for_each<Tin>(row, [&](const auto& x, int i) {
-      auto add = [&](const Units& w) {
-        high += (unsigned)(w.a[0] + w.a[1]) - 2u * kHighBits;
-        low += (unsigned)(w.b[0] + w.b[1]) - 2u * kLowBits;
-      };
-      if (dense) {  // straight through, so that the vector's chains overlap
+    auto add = [&](const Units& w) {
+      high += (unsigned)(w.a[0] + w.a[1]) - 2u * kHighBits;
+      low += (unsigned)(w.b[0] + w.b[1]) - 2u * kLowBits;
+    };
+    if (row.thr == -INFINITY) {  // straight through, so that the vector's chains overlap
+      for_each<Tin>(row, [&](const auto& x, int) {
 #pragma unroll
         for (int j = 0; j < kN; j += 2) add(units_all(x[j], x[j + 1], row.heat, sh.table));
-      } else {
+      });
+    } else {
+      for_each_from<Tin>(row, bounds.thr, [&](const auto& x, int i) {
         bool in[kN];
         bounds.test(x, i, in);
 #pragma unroll
         for (int j = 0; j < kN; j += 2)
           if (__any_sync(0xffffffffu, in[j] || in[j + 1])) add(units(x[j], x[j + 1], in[j], in[j + 1], row.heat, sh.table));
-      }
-    });
+      });
+    }
     u64 mine = ((u64)high << kHighShift) + (u64)(long long)(int)low;
     mine = warp_sum64(mine);
     if (lane == 0) sh.warp_mass[warp] = mine;
@@ -1073,33 +1102,43 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     if (t < sh.mass[rank]) {
       int w = 0;
       while (w < kWarps - 1 && t >= sh.warp_mass[w]) t -= sh.warp_mass[w++];
-      if (w == warp) {
-        for (int i0 = row.lo; i0 < row.hi; i0 += 32 * kN) {
-          const int i = i0 + kN * lane;
+      // that warp's elements by all warps (by itself, step after step, 7500 cycles)
+      const int lo = mine_units * w / kWarps * kUnit, hi = mine_units * (w + 1) / kWarps * kUnit;
+      for (int i0 = lo; i0 < hi; i0 += kThreads * kN) {
+        const int i = i0 + kN * tid;
+        u64 v[kN], sum = 0;
+        if (i - kN * lane < hi) {
           float x[kN];
           Vec<Tin>::get(*reinterpret_cast<const uint4*>(part_sh + (size_t)i * sizeof(Tin)), x);
           bool in[kN];
           bounds.test(x, i, in);
-          u64 v[kN], sum = 0;
 #pragma unroll
-          for (int j = 0; j < kN; ++j) sum += v[j] = in[j] ? weight(x[j], row.heat, sh.table) : 0;
-          const u64 incl = warp_scan64(sum);
-          const unsigned over = __ballot_sync(0xffffffffu, incl > t);
-          if (over) {
-            if (lane == __ffs(over) - 1) {
-              u64 run = incl - sum;
-              int at = -1;
-#pragma unroll
-              for (int j = 0; j < kN; ++j) {
-                run += v[j];
-                if (at < 0 && run > t) at = j;
-              }
-              a.token[r] = row.base + i + at;
-            }
-            break;
+          for (int j = 0; j < kN; j += 2) {
+            const Units m = units(x[j], x[j + 1], in[j], in[j + 1], row.heat, sh.table);
+            sum += v[j] = weight_of(m, 0);
+            sum += v[j + 1] = weight_of(m, 1);
           }
-          t -= __shfl_sync(0xffffffffu, incl, 31);
         }
+        const u64 incl = warp_scan64(sum);
+        if (lane == 31) sh.warp_over[warp] = incl;
+        __syncthreads();
+        u64 run = incl - sum, all = 0;
+        for (int q = 0; q < kWarps; ++q) {
+          if (q < warp) run += sh.warp_over[q];
+          all += sh.warp_over[q];
+        }
+        if (run <= t && t < run + sum) {  // (one thread)
+          int at = -1;
+#pragma unroll
+          for (int j = 0; j < kN; ++j) {
+            run += v[j];
+            if (at < 0 && run > t) at = j;
+          }
+          a.token[r] = row.base + i + at;
+        }
+        if (t < all) break;
+        t -= all;
+        __syncthreads();
       }
     }
   }
