@@ -46,6 +46,7 @@
 #include <limits.h>
 
 #include <atomic>
+#include <type_traits>
 #include <utility>
 
 #include "common.cuh"
@@ -63,7 +64,6 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 1024;
 constexpr int kCluster = 8;  // most CTAs of a row
 constexpr int kList = 1024;  // tokens that are ranked against each other: two a thread
-constexpr int kCount = 256;  // up to this many, by counting
 constexpr int kAround = 128; // tokens around an estimated threshold that are looked at in any case
 constexpr int kSmallK = 512;  // top-k by the threads' largest tokens
 constexpr int kOne = 44;     // a weight of 1 is 2^kOne; kMaxSampleVocab of them stay below 2^63
@@ -96,13 +96,13 @@ constexpr ExpTable make_table() {
 __device__ const ExpTable kTable = make_table();
 
 struct Shared {
+  unsigned cnt[kBins + 64];  // this CTA's histogram: tokens (the last interval and, from kBins + 32 on,
+                             // what is no token have a place a lane) ...
   union {
     struct {
-      unsigned cnt[kBins + 64];                // this CTA's histogram: tokens (and a place a lane for those
-                                               // of the last interval, and for no token) ...
-      unsigned lo[kBins], hi[kBins];           // ... or mass as two words
+      unsigned lo[kBins], hi[kBins];  // ... or mass as two words
     };
-    u64 own[kList];  // then its share of the list
+    u64 own[kList];  // this CTA's share of the list
   };
   u64 tot[kBins];                             // the cluster's, written by all CTAs
   u64 list[kList], sum[kList];  // codes; running mass once ranked
@@ -403,7 +403,6 @@ struct Bins {
   }
   // a bound below every x of the intervals up to b, the last one aside
   __device__ __forceinline__ float from(int b) const { return step > 0.f ? (off - (float)(b + 1) - fabsf(off) * 0x1p-22f) / step : -INFINITY; }
-  __device__ __forceinline__ float raw(float x) const { return fmaf(-x, step, off); }
   static __device__ __forceinline__ int index(float f) { return (__float_as_int(f + kMagic) - kMagicBits) & (kBins - 1); }
   // finer intervals inside interval b
   static __device__ __forceinline__ float inside(float f, int b) {
@@ -435,18 +434,30 @@ __device__ __forceinline__ void for_each_from(const Row& row, float bound, F&& f
   }
 }
 
-// Sums of the cluster's histograms, in every CTA's tot.  Two cluster barriers.
+// Sums of the cluster's histograms, in every CTA's tot: thread t's are intervals kPer t up.
+// Tokens: one cluster barrier before, and one has to follow before cnt changes.  Mass: two.
+constexpr int kPer = kBins / kThreads;
 template <bool kMass>
 __device__ __forceinline__ void sum_bins(cg::cluster_group& cluster, Shared& sh) {
-  const int C = (int)cluster.num_blocks(), share = kBins / C, first = (int)cluster.block_rank() * share;
+  const int C = (int)cluster.num_blocks(), tid = threadIdx.x;
   cluster.sync();
-  for (int i = threadIdx.x; i < share; i += kThreads) {
+  if (!kMass) {
+    static_assert(kPer == 2, "two counters a load");
+    uint2 n = make_uint2(0, 0);
+    for (int q = 0; q < C; ++q) {
+      const uint2 m = *reinterpret_cast<const uint2*>(cluster.map_shared_rank(&sh.cnt[2 * tid], q));
+      n.x += m.x;
+      n.y += m.y;
+    }
+    sh.tot[2 * tid] = n.x;
+    sh.tot[2 * tid + 1] = n.y;
+    return;
+  }
+  const int share = kBins / C, first = (int)cluster.block_rank() * share;
+  for (int i = tid; i < share; i += kThreads) {
     const int bin = first + i;
     u64 w = 0;
-    for (int q = 0; q < C; ++q) {
-      if (kMass) w += ((u64)*cluster.map_shared_rank(&sh.hi[bin], q) << 32) + *cluster.map_shared_rank(&sh.lo[bin], q);
-      else w += *cluster.map_shared_rank(&sh.cnt[bin], q);
-    }
+    for (int q = 0; q < C; ++q) w += ((u64)*cluster.map_shared_rank(&sh.hi[bin], q) << 32) + *cluster.map_shared_rank(&sh.lo[bin], q);
     for (int q = 0; q < C; ++q) *cluster.map_shared_rank(&sh.tot[bin], q) = w;
   }
   cluster.sync();
@@ -464,7 +475,6 @@ __device__ __forceinline__ void add_mass(Shared& sh, int bin, u64 w) {
 template <typename F>
 __device__ __forceinline__ u64 find_bin(Shared& sh, u64 above, F&& target) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  constexpr int kPer = kBins / kThreads;
   u64 mine[kPer], sum = 0;
 #pragma unroll
   for (int k = 0; k < kPer; ++k) sum += mine[k] = sh.tot[tid * kPer + k];
@@ -509,44 +519,54 @@ __device__ __forceinline__ void share_list(cg::cluster_group& cluster, Shared& s
   }
 }
 
-// The first n entries, all different, in descending order.  Up to kCount of them by counting
-// each one's rank, more by a bitonic network, whose steps of up to 32 stay inside a
-// warp's 64 entries (28 barriers for 128, 45 for 512).
-__device__ __forceinline__ void sort_list(u64* v, int n) {
-  const int tid = threadIdx.x;
-  __syncthreads();  // (the entries are there)
-  if (n <= kCount) {
-    int group = 32;  // lanes an entry
-    while (group * n > kThreads) group /= 2;
-    const int e = tid / group;
-    const u64 mine = e < n ? v[e] : 0;
-    int rank = 0;
-    if (e < n)
-#pragma unroll 4
-      for (int j = tid % group; j < n; j += group) rank += v[j] > mine ? 1 : 0;
-    for (int o = group / 2; o > 0; o >>= 1) rank += __shfl_xor_sync(0xffffffffu, rank, o);
-    __syncthreads();
-    if (e < n && tid % group == 0) v[rank] = mine;
-    __syncthreads();
-    return;
-  }
-  int m = 512;
-  while (m < n) m *= 2;
-  for (int i = n + tid; i < m; i += kThreads) v[i] = 0;
-  __syncthreads();
-  for (int size = 2; size <= m; size *= 2)
+// A warp's 32 values in descending order.
+__device__ __forceinline__ u64 sort32(u64 x) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int size = 2; size <= 32; size *= 2)
+#pragma unroll
     for (int stride = size / 2; stride > 0; stride /= 2) {
-      if (tid < m / 2) {
-        const int i = 2 * tid - (tid & (stride - 1)), j = i + stride;
-        const u64 a = v[i], b = v[j];
-        if ((a < b) == ((i & size) == 0)) {
-          v[i] = b;
-          v[j] = a;
-        }
-      }
-      if (stride > 32 || (stride == 1 && size > 32)) __syncthreads();
-      else __syncwarp();
+      const u64 y = __shfl_xor_sync(0xffffffffu, x, stride);
+      const bool larger = ((lane & stride) == 0) == ((lane & size) == 0);  // keeps the larger one
+      x = (x > y) == larger ? x : y;
     }
+  return x;
+}
+
+// The first n entries, none 0 and all different, in descending order: 32 at a time in a warp's
+// registers, then every entry's rank in the other lists of 32 by bisection.  Three barriers;
+// (a bitonic network over all of them, 45 barriers for 512, took 14000 cycles, this 6000).
+__device__ __forceinline__ void sort_list(u64* v, int n) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, lists = (n + 31) / 32;
+  u64 e[kList / kThreads];
+  __syncthreads();  // (the entries are there)
+#pragma unroll
+  for (int q = 0; q < kList / kThreads; ++q) {
+    const int l = warp + q * kWarps;
+    if (l >= lists) break;
+    e[q] = v[l * 32 + lane] = sort32(l * 32 + lane < n ? v[l * 32 + lane] : 0);
+  }
+  __syncthreads();
+  int rank[kList / kThreads];
+#pragma unroll
+  for (int q = 0; q < kList / kThreads; ++q) {
+    const int own = warp + q * kWarps;
+    if (own >= lists) break;
+    rank[q] = lane;
+    for (int l = 0; l < lists; ++l) {
+      if (l == own) continue;
+      const u64* list = v + 32 * l;
+      int at = 0;  // entries above e
+#pragma unroll
+      for (int step = 16; step > 0; step /= 2)
+        if (list[at + step - 1] > e[q]) at += step;
+      rank[q] += at + (list[at] > e[q] ? 1 : 0);
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < kList / kThreads; ++q)
+    if (warp + q * kWarps < lists && e[q]) v[rank[q]] = e[q];
   __syncthreads();
 }
 
@@ -554,24 +574,38 @@ __device__ __forceinline__ float logit_of(unsigned key) {
   return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
 }
 
-// Running masses of the first n entries, whose logits are logit(i).
+// The first n entries of the list in descending order, and their running masses; the logits
+// are logit(entry).
 template <typename F>
-__device__ __forceinline__ void sum_list(Shared& sh, const Heat& heat, int n, F&& logit) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, i = 2 * tid;
-  const float x0 = i < n ? logit(i) : -INFINITY, x1 = i + 1 < n ? logit(i + 1) : -INFINITY;
-  const Units w = units(x0, x1, x0 >= heat.least && i < n, x1 >= heat.least && i + 1 < n, heat, sh.table);
-  const u64 w0 = weight_of(w, 0), w1 = weight_of(w, 1), incl = warp_scan64(w0 + w1);
+__device__ __forceinline__ void order_list(Shared& sh, const Heat& heat, int n, F&& logit) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (n <= 32) {  // by warp 0: the barriers of all cost more than its work
+    __syncthreads();
+    if (warp == 0) {
+      const u64 e = sort32(lane < n ? sh.list[lane] : 0);
+      const float x = lane < n ? logit(e) : -INFINITY;
+      sh.list[lane] = e;
+      sh.sum[lane] = warp_scan64(weight_of(units(x, x, x >= heat.least, false, heat, sh.table), 0));
+    }
+    __syncthreads();
+    return;
+  }
+  sort_list(sh.list, n);
+  const int i = 2 * tid;
+  const float x0 = i < n ? logit(sh.list[i]) : -INFINITY, x1 = i + 1 < n ? logit(sh.list[i + 1]) : -INFINITY;
+  const Units w = units(x0, x1, x0 >= heat.least, x1 >= heat.least, heat, sh.table);
+  const u64 w0 = weight_of(w, 0), w1 = weight_of(w, 1);
+  const u64 incl = warp_scan64(w0 + w1);
   if (lane == 31) sh.warp_mass[warp] = incl;
   __syncthreads();
   u64 run = incl - w0 - w1;
   for (int q = 0; q < warp; ++q) run += sh.warp_mass[q];
-  if (i < n) sh.sum[i] = run + w0;
-  if (i + 1 < n) sh.sum[i + 1] = run + w0 + w1;
+  sh.sum[i] = run + w0;
+  sh.sum[i + 1] = run + w0 + w1;
   __syncthreads();
 }
 __device__ __forceinline__ void rank_list(Shared& sh, const Heat& heat, int n) {
-  sort_list(sh.list, n);
-  sum_list(sh, heat, n, [&](int i) { return logit_of((unsigned)(sh.list[i] >> kIndexBits)); });
+  order_list(sh, heat, n, [](u64 code) { return logit_of((unsigned)(code >> kIndexBits)); });
 }
 
 // The first of n entries whose running mass, from `above` on, reaches the target (there is one).
@@ -609,8 +643,12 @@ __device__ __forceinline__ int collect(cg::cluster_group& cluster, Shared& sh, c
   return sh.listed;
 }
 
+template <bool kMass>
 __device__ __forceinline__ void clear_bins(Shared& sh) {
-  for (int i = threadIdx.x; i < kBins; i += kThreads) sh.cnt[i] = sh.lo[i] = sh.hi[i] = 0;
+  for (int i = threadIdx.x; i < kBins; i += kThreads) {
+    if (kMass) sh.lo[i] = sh.hi[i] = 0;
+    else sh.cnt[i] = 0;
+  }
   if (threadIdx.x < 64) sh.cnt[kBins + threadIdx.x] = 0;
   if (threadIdx.x == 0) sh.listed = sh.listed_own = 0;
   __syncthreads();
@@ -642,7 +680,7 @@ __device__ __forceinline__ u64 select(cg::cluster_group& cluster, Shared& sh, Ro
     return level == 0 ? Bins::index(f) : level == 1 ? Bins::index(Bins::inside(f, b0)) : (int)((hi - code_of(x, row.base + i)) >> shift);
   };
   for (;;) {
-    clear_bins(sh);
+    clear_bins<kMass>(sh);
     u64 last = 0;  // of the last interval, which may hold most tokens
     for_each<Tin>(row, [&](const auto& x, int i) {
       bool in[kN];
@@ -677,7 +715,10 @@ __device__ __forceinline__ u64 select(cg::cluster_group& cluster, Shared& sh, Ro
       return level == 0 ? want(whole) : target;
     });
     target = got;
-    if (!kMass && level == 0 && whole_all <= target) return 0;
+    if (!kMass && level == 0 && whole_all <= target) {
+      cluster.sync();  // (all have read cnt)
+      return 0;
+    }
     const int bin = sh.bin;
     above = sh.before;
     if (level == 0) b0 = bin;
@@ -716,24 +757,46 @@ __device__ __forceinline__ u64 select(cg::cluster_group& cluster, Shared& sh, Ro
 template <typename Tin>
 __device__ __forceinline__ bool nucleus(cg::cluster_group& cluster, Shared& sh, Row& row, float range, float heat, float p,
                                         u64* total) {
-  constexpr int kN = Vec<Tin>::kN, kPer = kBins / kThreads;
+  constexpr int kN = Vec<Tin>::kN;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
-  const Bins bins(row.heat.max, range);
   const Bounds<kN> bounds(row, true);
-  clear_bins(sh);
-  for_each<Tin>(row, [&](const auto& x, int i) {
-    bool in[kN];
-    bounds.test(x, i, in);
+  const bool dense = row.thr == -INFINITY;  // nothing filtered (what has no weight counts as of the last interval)
+  const float step = range > 0.f ? (float)kBins / range : 0.f;
+  clear_bins<false>(sh);
+  // places in cnt of two logits; one minimum gives those of the last interval 32 places
+  auto place = [&](float x0, float x1, int (&at)[2]) {
+    float f0, f1;
+    fma(both(row.heat.max) - Two(x0, x1), both(step), both(kMagic)).get(&f0, &f1);
+    at[0] = min(__float_as_int(f0) - kMagicBits, kBins - 1 + lane);
+    at[1] = min(__float_as_int(f1) - kMagicBits, kBins - 1 + lane);
+  };
+  if (dense) {
+    for_each<Tin>(row, [&](const auto& x, int) {
 #pragma unroll
-    for (int j = 0; j < kN; ++j) {  // (no branch: the last interval, and no token, at the lane's own place)
-      const int bin = Bins::index(bins.at(x[j]));
-      atomicAdd(&sh.cnt[!in[j] ? kBins + 32 + lane : bin == kBins - 1 ? kBins + lane : bin], 1u);
-    }
-  });
+      for (int j = 0; j < kN; j += 2) {
+        int at[2];
+        place(x[j], x[j + 1], at);
+        atomicAdd(&sh.cnt[at[0]], 1u);
+        atomicAdd(&sh.cnt[at[1]], 1u);
+      }
+    });
+  } else {
+    for_each_from<Tin>(row, bounds.thr, [&](const auto& x, int i) {
+      bool in[kN];
+      bounds.test(x, i, in);
+#pragma unroll
+      for (int j = 0; j < kN; j += 2) {
+        int at[2];
+        place(x[j], x[j + 1], at);
+        atomicAdd(&sh.cnt[in[j] ? at[0] : kBins + 32 + lane], 1u);  // (no branch)
+        atomicAdd(&sh.cnt[in[j + 1] ? at[1] : kBins + 32 + lane], 1u);
+      }
+    });
+  }
   __syncthreads();
   if (warp == 0) {
-    const unsigned last = __reduce_add_sync(0xffffffffu, sh.cnt[kBins + lane]);
+    const unsigned last = __reduce_add_sync(0xffffffffu, sh.cnt[kBins - 1 + lane]);
     if (lane == 0) sh.cnt[kBins - 1] = last;
   }
   sum_bins<false>(cluster, sh);
@@ -774,40 +837,41 @@ __device__ __forceinline__ bool nucleus(cg::cluster_group& cluster, Shared& sh, 
     int lo = bin, hi = bin;
     for (u64 n = sh.tot[bin]; lo > 0 && hi < kBins - 1 && hi - bin < 8; --lo, ++hi)
       if ((n += sh.tot[lo - 1] + sh.tot[hi + 1]) > kAround) break;
-    // exact: the whole mass, the mass above these intervals, their tokens
-    const float top = (float)lo - 0.5f, end = hi == kBins - 1 ? INFINITY : (float)hi + 0.5f;
+    // exact: the whole mass, the mass above these intervals, their tokens (from xe to xt)
+    const float width = range / (float)kBins;
+    const float xt = lo > 0 ? fmaf(0.5f - (float)lo, width, row.heat.max) : INFINITY;
+    const float xe = fmaxf(hi < kBins - 1 ? fmaf(-0.5f - (float)hi, width, row.heat.max) : -INFINITY, row.heat.least);
     unsigned high = 0, low = 0, high1 = 0, low1 = 0;
-    for_each<Tin>(row, [&](const auto& x, int i) {
+    auto step_of = [&](auto dense_t, const auto& x, int i) {
+      constexpr bool kDense = decltype(dense_t)::value;
       bool in[kN], any = false;
-      bounds.test(x, i, in);
-#pragma unroll
-      for (int j = 0; j < kN; ++j) any = any || in[j];
-      if (!__any_sync(0xffffffffu, any)) return;
-      any = false;
+      if (!kDense) bounds.test(x, i, in);
 #pragma unroll
       for (int j = 0; j < kN; j += 2) {
-        const Units w = units(x[j], x[j + 1], in[j], in[j + 1], row.heat, sh.table);
+        const Units w = kDense ? units_all(x[j], x[j + 1], row.heat, sh.table)
+                               : units(x[j], x[j + 1], in[j], in[j + 1], row.heat, sh.table);
         high += (unsigned)(w.a[0] + w.a[1]);
         low += (unsigned)(w.b[0] + w.b[1]);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float f = bins.raw(x[j + e]);
-          const bool over = f < top;  // (what is not in weighs nothing)
-          high1 += over ? (unsigned)w.a[e] : (unsigned)kHighBits;
-          low1 += over ? (unsigned)w.b[e] : (unsigned)kLowBits;
-          in[j + e] = in[j + e] && !over && f < end;
+          const bool over = x[j + e] > xt;  // (what is not in weighs nothing)
+          if (over) {
+            high1 += (unsigned)(w.a[e] - kHighBits);
+            low1 += (unsigned)(w.b[e] - kLowBits);
+          }
+          in[j + e] = (kDense || in[j + e]) && !over && x[j + e] >= xe;
           any = any || in[j + e];
         }
       }
       high -= (unsigned)kN * kHighBits;
       low -= (unsigned)kN * kLowBits;
-      high1 -= (unsigned)kN * kHighBits;
-      low1 -= (unsigned)kN * kLowBits;
       if (any)
 #pragma unroll
         for (int j = 0; j < kN; ++j)
           if (in[j]) list_own(sh, code_of(x[j], row.base + i + j));
-    });
+    };
+    if (dense) for_each<Tin>(row, [&](const auto& x, int i) { step_of(std::true_type{}, x, i); });
+    else for_each_from<Tin>(row, bounds.thr, [&](const auto& x, int i) { step_of(std::false_type{}, x, i); });
     const u64 all = warp_sum64(((u64)high << kHighShift) + (u64)(long long)(int)low);
     const u64 over = warp_sum64(((u64)high1 << kHighShift) + (u64)(long long)(int)low1);
     if (lane == 0) {
@@ -859,8 +923,7 @@ __device__ __forceinline__ u64 small_row(Shared& sh, Row& row, int n, int k, flo
       const u64 code = sh.list[i];
       sh.list[i] = (code & kIndexMask) << 32 | code >> kIndexBits;
     }
-    sort_list(sh.list, m);
-    sum_list(sh, row.heat, m, [&](int i) { return logit_of((unsigned)sh.list[i]); });
+    order_list(sh, row.heat, m, [](u64 entry) { return logit_of((unsigned)entry); });
     const int i = pick_entry(sh, 0, drawn(u, whole) + 1, m);
     if (threadIdx.x == 0) *token = (int32_t)(kIndexMask - (sh.list[i] >> 32));
   }
@@ -1013,7 +1076,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     if (few) {
       // the k-th of the threads' largest tokens lies in interval b0: no token of the first k lies behind it
       const Bins bins(mx, range);
-      clear_bins(sh);
+      clear_bins<false>(sh);
       const int bin = Bins::index(bins.at(own));
       const bool there = own > row.thr || (own == row.thr && row.last == INT_MAX);
       const unsigned same = __ballot_sync(0xffffffffu, there && bin == kBins - 1);
@@ -1025,6 +1088,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       const int n = collect<Tin>(cluster, sh, row, b0 < kBins - 1 ? bins.from(b0) : -INFINITY, [&](float x, int) { return Bins::index(bins.at(x)) <= b0; });
       few = n <= kList;
       if (few) {
+        if (rank != 0 && !out) return;  // (every CTA has the list: one is enough for the token)
         total = small_row(sh, row, n, k, p, u, a.token && rank == 0 ? a.token + r : nullptr);
         done = true;
       } else {
