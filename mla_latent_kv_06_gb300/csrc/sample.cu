@@ -1212,24 +1212,45 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     const float inv = (float)(1ull << kOne) / t_hi;
     const float inv_lo = fmaf(-t_lo, inv, fmaf(-t_hi, inv, (float)(1ull << kOne))) / t_hi;
     const float tiny = row.heat.none - (256.f * kTiny - kNegligible) / row.heat.hi;
-    // v = probabilities of x0, x1 at elements i0, i1
-    auto probability = [&](float x0, float x1, int i0, int i1, float* v0, float* v1) {
-      const bool in0 = x0 - row.heat.shift >= tiny && row.kept(x0, i0), in1 = x1 - row.heat.shift >= tiny && row.kept(x1, i1);
-      *v0 = *v1 = 0.f;
-      if (!__any_sync(0xffffffffu, in0 || in1)) return;
+    const bool dense = row.thr == -INFINITY;
+    // probabilities of two logits, in0 and in1: whether they are kept
+    auto probability = [&](float x0, float x1, bool in0, bool in1, float* v0, float* v1) {
+      float y0, y1, a0, a1;
+      (Two(x0, x1) - both(row.heat.shift)).get(&y0, &y1);
       Two w, l;
-      weigh(Two(in0 ? x0 - row.heat.shift : row.heat.none, in1 ? x1 - row.heat.shift : row.heat.none), row.heat, sh.table, &w, &l);
+      weigh(Two(fmaxf(y0, tiny), fmaxf(y1, tiny)), row.heat, sh.table, &w, &l);
       const Two hi = w + l, lo = l - (hi - w);
-      float a0, a1;
       fma(hi, both(inv), fma(hi, both(inv_lo), lo * both(inv))).get(&a0, &a1);
-      *v0 = !in0 ? 0.f : k == 1 ? 1.f : a0;
-      *v1 = !in1 ? 0.f : k == 1 ? 1.f : a1;
+      *v0 = in0 && y0 >= tiny ? a0 : 0.f;
+      *v1 = in1 && y1 >= tiny ? a1 : 0.f;
     };
     if ((reinterpret_cast<uintptr_t>(out) & 15) == 0) {  // the vectors' places are 16-byte units
-      for_each<Tin>(row, [&](const auto& x, int i) {
-        float v[kN];
+      const Bounds<kN> bounds(row, false);
+      for (int i = row.lo + kN * lane; i < row.hi; i += 32 * kN) {
+        const uint4 vec = *reinterpret_cast<const uint4*>(part_sh + (size_t)i * sizeof(Tin));
+        float x[kN], v[kN];
+        if (dense) {
+          Vec<Tin>::get(vec, x);
 #pragma unroll
-        for (int j = 0; j < kN; j += 2) probability(x[j], x[j + 1], i + j, i + j + 1, &v[j], &v[j + 1]);
+          for (int j = 0; j < kN; j += 2) probability(x[j], x[j + 1], true, true, &v[j], &v[j + 1]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < kN; ++j) v[j] = 0.f;
+          if (__any_sync(0xffffffffu, Vec<Tin>::max(vec) >= row.thr)) {
+            Vec<Tin>::get(vec, x);
+            bool in[kN];
+            bounds.test(x, i, in);
+#pragma unroll
+            for (int j = 0; j < kN; j += 2) {
+              if (k == 1) {
+                v[j] = in[j] ? 1.f : 0.f;
+                v[j + 1] = in[j + 1] ? 1.f : 0.f;
+              } else if (__any_sync(0xffffffffu, in[j] || in[j + 1])) {
+                probability(x[j], x[j + 1], in[j], in[j + 1], &v[j], &v[j + 1]);
+              }
+            }
+          }
+        }
         if (i >= row.from && i + kN <= row.to) {
 #pragma unroll
           for (int j = 0; j < kN; j += 4) *reinterpret_cast<float4*>(out + i + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
@@ -1238,14 +1259,16 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
           for (int j = 0; j < kN; ++j)
             if (i + j >= row.from && i + j < row.to) out[i + j] = v[j];
         }
-      });
+      }
     } else {  // an element per lane, so that a warp's stores are neighbours
       const Tin* xs = reinterpret_cast<const Tin*>(part_sh);
       const int end = min(row.hi, row.to);
       for (int i = max(row.lo, row.from) + lane; i - lane < end; i += 64) {
         const bool there0 = i < end, there1 = i + 32 < end;
-        float v0, v1;
-        probability(there0 ? to_f32(xs[i]) : -INFINITY, there1 ? to_f32(xs[i + 32]) : -INFINITY, i, i + 32, &v0, &v1);
+        const float x0 = there0 ? to_f32(xs[i]) : -INFINITY, x1 = there1 ? to_f32(xs[i + 32]) : -INFINITY;
+        const bool in0 = dense || row.kept(x0, i), in1 = dense || row.kept(x1, i + 32);
+        float v0 = in0 ? 1.f : 0.f, v1 = in1 ? 1.f : 0.f;
+        if (k != 1 && __any_sync(0xffffffffu, in0 || in1)) probability(x0, x1, in0, in1, &v0, &v1);
         if (there0) out[i] = v0;
         if (there1) out[i + 32] = v1;
       }
