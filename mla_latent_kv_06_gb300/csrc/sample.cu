@@ -3,22 +3,23 @@
 // Method.  The tokens of a row are ordered by (logit down, index up), and every
 // filter keeps a prefix of that order, so the kept set is one threshold: a
 // token's code, its ordered logit bits above its inverted index, is unique, and
-// a token is kept when its code reaches the threshold's.  Nothing is sorted.
+// a token is kept when its code reaches the threshold's.  No row is sorted.
 //   w(x)  = exp((x - max) / T)                      (T = 0: the first token alone)
 //   min-p : w(x) >= min_p, a threshold on x itself
 //   top-k : the code of the k-th token
 //   top-p : the code of the token at which the running mass reaches top_p W
-// The last two come from a histogram over kBins intervals of x, which narrows the
-// threshold down to one interval, and from its tokens, ranked against each other;
-// an interval of more than kList tokens is split again, by x and then by codes.
-//   For top-p the histogram counts: a token's weight follows from its interval well
-// enough to name the threshold's (nucleus()).  One pass with exact weights then
-// gives W, the mass above that interval and the interval's tokens, or says that it is
-// the next one.  Only ties that fill an interval go by a histogram of exact masses.
-//   A small k needs no histogram of the row: the k-th of the threads' largest tokens
-// bounds the k-th token from below, and what reaches that bound, little more than k
-// tokens, decides everything else.
-// The draw is the least index whose cumulative kept mass exceeds u W.
+// The last two come from a histogram that counts tokens in kBins intervals of x:
+//   top-k: it names the k-th token's interval, whose tokens are then sorted.  A small k needs
+// no histogram of the row: the k-th of the threads' largest tokens bounds the k-th token
+// from below, and what reaches that bound, little more than k tokens, decides
+// everything else, the other filters and the draw included.
+//   top-p: a token's weight follows from its interval well enough to name the threshold's
+// (nucleus()).  One pass with exact weights then gives W, the mass above that interval and
+// the interval's tokens, or says that it is the next one.
+//   An interval of more tokens than the list holds (ties) is split again, by x and then by
+// codes, on exact counts or masses (select()).
+// The draw is the least index whose cumulative kept mass exceeds u W: the CTA and the warp
+// by their sums, then that warp's elements by all threads.
 //
 // Rounding.  A threshold and a draw compare sums over the vocabulary, so a
 // weight is an integer, w 2^44 rounded once: sums are then exact, in any order,
@@ -39,9 +40,19 @@
 //
 // A row is a cluster of up to 8 CTAs, each with a contiguous part of the
 // vocabulary in shared memory, read once, 16 bytes at a time from 16-byte
-// boundaries; a warp's part is contiguous too, and no other warp reads it.  (A CTA
+// boundaries; a warp's part is contiguous too, and mostly no other warp reads it.  (A CTA
 // a row, streaming it from L2 in every pass, was slower up to 400 rows: 104 us
-// against 95 for 256 rows of 131072 at a temperature alone.)
+// against 95 for 256 rows of 131072 at a temperature alone, when that was measured.)
+//
+// Measured: 256 rows of 131072 bf16 logits 55 us at a temperature alone (1.2 TB/s), 111 with
+// top-p, 58 with top-k, 48 with min-p, 84 of all kinds; 400 rows with their probabilities 129
+// (2.4 TB/s) to 210.  Neither memory nor the arithmetic is at its rate (issue slots 51% used
+// while an SM is busy): a row goes through its passes with barriers of the CTA (500 cycles
+// each beside another CTA's work) and of the cluster (1500) between them, two CTAs fill an
+// SM's registers, and 76 rows at a time are 3.4 rounds for 256.  Fetching the next round's rows
+// into L2 ahead changed nothing.  CTAs of 1024 threads (one row of 131072 with top-p 29 us
+// against 23) and clusters of twice the CTAs (79 against 55) cost more in barriers than they give; CTAs of
+// twice the elements, one to an SM, 59.  One row of 32000 takes 7 us, with top-p 15.
 #include <cooperative_groups.h>
 #include <limits.h>
 
@@ -65,7 +76,10 @@ constexpr int kBins = 1024;
 constexpr int kCluster = 8;  // most CTAs of a row
 constexpr int kList = 1024;  // tokens that are ranked against each other: two a thread
 constexpr int kAround = 128; // tokens around an estimated threshold that are looked at in any case
-constexpr int kSmallK = 512;  // top-k by the threads' largest tokens
+// top-k by the threads' largest tokens, whose list then serves top-p and the draw too, or by
+// counts and a threshold.  64 rows of 131072 (8 of 32000), us: k = 200 20.6 and 24.0 (14.1, 13.0),
+// k = 500 32.7 and 27.0 (21.5, 13.5); with top-p after it, k = 500 31.7 and 45.7 (20.7, 23.2).
+constexpr int kSmallK = 256, kSmallKTopP = 512;
 constexpr int kOne = 44;     // a weight of 1 is 2^kOne; kMaxSampleVocab of them stay below 2^63
 constexpr int kIndexBits = 20;
 constexpr u64 kIndexMask = (1ull << kIndexBits) - 1;
@@ -401,8 +415,6 @@ struct Bins {
   __device__ __forceinline__ float at(float x) const {
     return fminf(fmaxf(fmaf(-x, step, off), 0.f), (float)(kBins - 1));
   }
-  // a bound below every x of the intervals up to b, the last one aside
-  __device__ __forceinline__ float from(int b) const { return step > 0.f ? (off - (float)(b + 1) - fabsf(off) * 0x1p-22f) / step : -INFINITY; }
   static __device__ __forceinline__ int index(float f) { return (__float_as_int(f + kMagic) - kMagicBits) & (kBins - 1); }
   // finer intervals inside interval b
   static __device__ __forceinline__ float inside(float f, int b) {
@@ -728,7 +740,7 @@ __device__ __forceinline__ u64 select(cg::cluster_group& cluster, Shared& sh, Ro
       const u64 width = (1ull << shift) - 1;
       if (hi - lo > width) lo = hi - width;
     }
-    n = collect<Tin>(cluster, sh, row, b0 < kBins - 1 ? bins.from(b0) : -INFINITY, [&](float x, int i) { return candidate(x, i, level + 1); });
+    n = collect<Tin>(cluster, sh, row, -INFINITY, [&](float x, int i) { return candidate(x, i, level + 1); });
     if (n <= kList) break;
     ++level;
     if (level >= 2) {  // by codes
@@ -751,6 +763,95 @@ __device__ __forceinline__ u64 select(cg::cluster_group& cluster, Shared& sh, Ro
   return kept;
 }
 
+// Intervals of x from its maximum on, in one packed multiply-add and, for the place in cnt, one
+// minimum, which gives what lies in the last interval or past it a place a lane.
+struct Places {
+  float max, step, width;
+  __device__ __forceinline__ Places(float max, float range)
+      : max(max), step(range > 0.f ? (float)kBins / range : 0.f), width(range / (float)kBins) {}
+  __device__ __forceinline__ void at(float x0, float x1, int (&place)[2]) const {
+    const int last = kBins - 1 + (int)(threadIdx.x & 31);
+    float f0, f1;
+    fma(both(max) - Two(x0, x1), both(step), both(kMagic)).get(&f0, &f1);
+    place[0] = min(__float_as_int(f0) - kMagicBits, last);
+    place[1] = min(__float_as_int(f1) - kMagicBits, last);
+  }
+  __device__ __forceinline__ int bin(float x) const {
+    return min(__float_as_int(__fmaf_rn(__fsub_rn(max, x), step, kMagic)) - kMagicBits, kBins - 1);
+  }
+  // a bound below every x of the intervals up to b
+  __device__ __forceinline__ float from(int b) const {
+    return b < kBins - 1 ? max - (float)(b + 1) * width - fabsf(max) * 0x1p-22f : -INFINITY;
+  }
+};
+
+// The cluster's histogram of the kept tokens in tot.  Of an unfiltered row, what has no weight
+// and what is outside the row counts as of the last interval.
+template <typename Tin>
+__device__ __forceinline__ void count_bins(cg::cluster_group& cluster, Shared& sh, const Row& row, const Places& places) {
+  constexpr int kN = Vec<Tin>::kN;
+  const int lane = threadIdx.x & 31;
+  clear_bins<false>(sh);
+  if (row.thr == -INFINITY) {
+    for_each<Tin>(row, [&](const auto& x, int) {
+#pragma unroll
+      for (int j = 0; j < kN; j += 2) {
+        int at[2];
+        places.at(x[j], x[j + 1], at);
+        atomicAdd(&sh.cnt[at[0]], 1u);
+        atomicAdd(&sh.cnt[at[1]], 1u);
+      }
+    });
+  } else {
+    const Bounds<kN> bounds(row, false);
+    for_each_from<Tin>(row, bounds.thr, [&](const auto& x, int i) {
+      bool in[kN];
+      bounds.test(x, i, in);
+#pragma unroll
+      for (int j = 0; j < kN; j += 2) {
+        int at[2];
+        places.at(x[j], x[j + 1], at);
+        atomicAdd(&sh.cnt[in[j] ? at[0] : kBins + 32 + lane], 1u);  // (no branch)
+        atomicAdd(&sh.cnt[in[j + 1] ? at[1] : kBins + 32 + lane], 1u);
+      }
+    });
+  }
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const unsigned last = __reduce_add_sync(0xffffffffu, sh.cnt[kBins - 1 + lane]);
+    if (lane == 0) sh.cnt[kBins - 1] = last;
+  }
+  sum_bins<false>(cluster, sh);
+}
+
+// top-k by counts: the row's threshold.  False where ties or the last interval are in the way.
+template <typename Tin>
+__device__ __forceinline__ bool top_count(cg::cluster_group& cluster, Shared& sh, Row& row, float range, int k) {
+  const Places places(row.heat.max, range);
+  count_bins<Tin>(cluster, sh, row, places);
+  u64 whole = 0;
+  find_bin(sh, 0, [&](u64 w) {
+    whole = w;
+    return (u64)k;
+  });
+  const int b = sh.bin;
+  const bool all = row.thr != -INFINITY && whole <= (u64)k;  // all stay
+  if (all || b == kBins - 1) {
+    cluster.sync();  // (all have read cnt)
+    return all;
+  }
+  const u64 above = sh.before;
+  const int n = collect<Tin>(cluster, sh, row, places.from(b), [&](float x, int) { return places.bin(x) == b; });
+  if (n > kList) {
+    __syncthreads();  // (sh.listed has been read)
+    return false;
+  }
+  sort_list(sh.list, n);
+  row.set(sh.list[k - 1 - (int)above]);
+  __syncthreads();
+  return true;
+}
+
 // The same for the mass and top_p = p, by an estimate of the interval: false where that fails
 // (nothing has changed then).  *total: the mass kept; sh.over: the CTAs' masses above the
 // interval, sh.warp_over: the warps'; the rest of what is kept is the list up to sh.pick.
@@ -761,45 +862,9 @@ __device__ __forceinline__ bool nucleus(cg::cluster_group& cluster, Shared& sh, 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const Bounds<kN> bounds(row, true);
-  const bool dense = row.thr == -INFINITY;  // nothing filtered (what has no weight counts as of the last interval)
-  const float step = range > 0.f ? (float)kBins / range : 0.f;
-  clear_bins<false>(sh);
-  // places in cnt of two logits; one minimum gives those of the last interval 32 places
-  auto place = [&](float x0, float x1, int (&at)[2]) {
-    float f0, f1;
-    fma(both(row.heat.max) - Two(x0, x1), both(step), both(kMagic)).get(&f0, &f1);
-    at[0] = min(__float_as_int(f0) - kMagicBits, kBins - 1 + lane);
-    at[1] = min(__float_as_int(f1) - kMagicBits, kBins - 1 + lane);
-  };
-  if (dense) {
-    for_each<Tin>(row, [&](const auto& x, int) {
-#pragma unroll
-      for (int j = 0; j < kN; j += 2) {
-        int at[2];
-        place(x[j], x[j + 1], at);
-        atomicAdd(&sh.cnt[at[0]], 1u);
-        atomicAdd(&sh.cnt[at[1]], 1u);
-      }
-    });
-  } else {
-    for_each_from<Tin>(row, bounds.thr, [&](const auto& x, int i) {
-      bool in[kN];
-      bounds.test(x, i, in);
-#pragma unroll
-      for (int j = 0; j < kN; j += 2) {
-        int at[2];
-        place(x[j], x[j + 1], at);
-        atomicAdd(&sh.cnt[in[j] ? at[0] : kBins + 32 + lane], 1u);  // (no branch)
-        atomicAdd(&sh.cnt[in[j + 1] ? at[1] : kBins + 32 + lane], 1u);
-      }
-    });
-  }
-  __syncthreads();
-  if (warp == 0) {
-    const unsigned last = __reduce_add_sync(0xffffffffu, sh.cnt[kBins - 1 + lane]);
-    if (lane == 0) sh.cnt[kBins - 1] = last;
-  }
-  sum_bins<false>(cluster, sh);
+  const bool dense = row.thr == -INFINITY;
+  const Places places(row.heat.max, range);
+  count_bins<Tin>(cluster, sh, row, places);
   // the interval in which p of the mass is reached, a token taken to weigh what its interval's middle does
   const float fall = range > 0.f ? -1.4426950f * range / ((float)kBins * heat) : 0.f;
   float mine[kPer], sum = 0.f;
@@ -838,9 +903,8 @@ __device__ __forceinline__ bool nucleus(cg::cluster_group& cluster, Shared& sh, 
     for (u64 n = sh.tot[bin]; lo > 0 && hi < kBins - 1 && hi - bin < 8; --lo, ++hi)
       if ((n += sh.tot[lo - 1] + sh.tot[hi + 1]) > kAround) break;
     // exact: the whole mass, the mass above these intervals, their tokens (from xe to xt)
-    const float width = range / (float)kBins;
-    const float xt = lo > 0 ? fmaf(0.5f - (float)lo, width, row.heat.max) : INFINITY;
-    const float xe = fmaxf(hi < kBins - 1 ? fmaf(-0.5f - (float)hi, width, row.heat.max) : -INFINITY, row.heat.least);
+    const float xt = lo > 0 ? fmaf(0.5f - (float)lo, places.width, row.heat.max) : INFINITY;
+    const float xe = fmaxf(hi < kBins - 1 ? fmaf(-0.5f - (float)hi, places.width, row.heat.max) : -INFINITY, row.heat.least);
     unsigned high = 0, low = 0, high1 = 0, low1 = 0;
     auto step_of = [&](auto dense_t, const auto& x, int i) {
       constexpr bool kDense = decltype(dense_t)::value;
@@ -1072,12 +1136,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     done = true;
   } else if (k > 0 && k < a.V) {
     const float range = fminf(spread, 64.f);
-    bool few = k <= kSmallK;
-    if (few) {
+    int n = 0;  // tokens listed
+    if (k <= (p < 1.f ? kSmallKTopP : kSmallK)) {
       // the k-th of the threads' largest tokens lies in interval b0: no token of the first k lies behind it
-      const Bins bins(mx, range);
+      const Places places(mx, range);
       clear_bins<false>(sh);
-      const int bin = Bins::index(bins.at(own));
+      const int bin = places.bin(own);
       const bool there = own > row.thr || (own == row.thr && row.last == INT_MAX);
       const unsigned same = __ballot_sync(0xffffffffu, there && bin == kBins - 1);
       if (there && bin < kBins - 1) atomicAdd(&sh.cnt[bin], 1u);
@@ -1085,17 +1149,19 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       sum_bins<false>(cluster, sh);
       find_bin(sh, 0, [&](u64) { return (u64)k; });
       const int b0 = sh.bin;
-      const int n = collect<Tin>(cluster, sh, row, b0 < kBins - 1 ? bins.from(b0) : -INFINITY, [&](float x, int) { return Bins::index(bins.at(x)) <= b0; });
-      few = n <= kList;
-      if (few) {
-        if (rank != 0 && !out) return;  // (every CTA has the list: one is enough for the token)
-        total = small_row(sh, row, n, k, p, u, a.token && rank == 0 ? a.token + r : nullptr);
-        done = true;
-      } else {
+      n = collect<Tin>(cluster, sh, row, places.from(b0), [&](float x, int) { return places.bin(x) <= b0; });
+      if (n > kList) {
+        n = 0;
         __syncthreads();  // (sh.listed has been read)
       }
     }
-    if (!few) select<Tin, false>(cluster, sh, row, range, [&](u64) { return (u64)k; });
+    if (n > 0) {
+      if (rank != 0 && !out) return;  // (every CTA has the list: one is enough for the token)
+      total = small_row(sh, row, n, k, p, u, a.token && rank == 0 ? a.token + r : nullptr);
+      done = true;
+    } else if (!top_count<Tin>(cluster, sh, row, range, k)) {
+      select<Tin, false>(cluster, sh, row, range, [&](u64) { return (u64)k; });
+    }
   }
   bool listed = false;  // the kept tokens: those above an interval, and some of the list
   if (!done && p < 1.f) {
