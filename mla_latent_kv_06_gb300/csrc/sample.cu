@@ -16,8 +16,8 @@
 //   top-p: a token's weight follows from its interval well enough to name the threshold's
 // (nucleus()).  One pass with exact weights then gives W, the mass above that interval and
 // the interval's tokens, or says that it is the next one.
-//   An interval of more tokens than the list holds (ties) is split again, by x and then by
-// codes, on exact counts or masses (select()).
+//   An interval of more tokens than the list holds is split by the bits of x, on exact counts
+// or masses, down to one value, and its tokens are counted out by index (refine()).
 // The draw is the least index whose cumulative kept mass exceeds u W: the CTA and the warp
 // by their sums, then that warp's elements by all threads.
 //
@@ -109,7 +109,15 @@ constexpr ExpTable make_table() {
 }
 __device__ const ExpTable kTable = make_table();
 
+// An interval of more tokens than the list holds, in which the threshold lies, from xe up to xt
+// or below.
+struct Crowd {
+  float xe, xt;
+  u64 above, target;  // masses
+};
+
 struct Shared {
+  Crowd crowd;
   unsigned cnt[kBins + 64];  // this CTA's histogram: tokens (the last interval and, from kBins + 32 on,
                              // what is no token have a place a lane) ...
   union {
@@ -130,6 +138,10 @@ struct Shared {
   float warp_max[kWarps], warp_min[kWarps];
   int warp_first[kWarps];
   int listed, listed_own, at[kCluster];
+  unsigned key_lo[kCluster], key_hi[kCluster], ties[kCluster];
+  unsigned warp_lo[kWarps], warp_hi[kWarps];
+  u64 span[kCluster];
+  int tie;
   int bin, pick;
   u64 before;
 };
@@ -297,6 +309,22 @@ __device__ __forceinline__ u64 drawn(float u, u64 whole) {
   return u >= 1.f ? whole - 1 : u > 0.f ? fraction_of(u, whole, &cut) : 0;
 }
 
+// Ordered integers of the type's values.
+template <typename Tin>
+struct Keys;
+template <>
+struct Keys<float> {
+  static __device__ __forceinline__ unsigned of(float x) { return ordered_key(x); }
+  static __device__ __forceinline__ float value(unsigned k) { return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k); }
+};
+template <>
+struct Keys<__nv_bfloat16> {
+  static __device__ __forceinline__ unsigned of(float x) { return ordered_key(x) >> 16; }
+  static __device__ __forceinline__ float value(unsigned k) {
+    return __uint_as_float((k & 0x8000u ? k & 0x7fffu : ~k & 0xffffu) << 16);
+  }
+};
+
 template <typename Tin>
 struct Vec;
 template <>
@@ -405,20 +433,6 @@ struct Bounds {
 #pragma unroll
       for (int j = 0; j < kN; ++j) in[j] = in[j] || (x[j] == thr && i + j <= last && x[j] >= least);
     }
-  }
-};
-
-// Intervals of x below the maximum, the last one without an end: a monotonic map, whatever rounding does.
-struct Bins {
-  float step, off;
-  __device__ __forceinline__ Bins(float max, float range) : step(range > 0.f ? (float)kBins / range : 0.f), off(max * step) {}
-  __device__ __forceinline__ float at(float x) const {
-    return fminf(fmaxf(fmaf(-x, step, off), 0.f), (float)(kBins - 1));
-  }
-  static __device__ __forceinline__ int index(float f) { return (__float_as_int(f + kMagic) - kMagicBits) & (kBins - 1); }
-  // finer intervals inside interval b
-  static __device__ __forceinline__ float inside(float f, int b) {
-    return fminf(fmaxf((f - ((float)b - 0.5f)) * (float)kBins, 0.f), (float)(kBins - 1));
   }
 };
 
@@ -655,112 +669,196 @@ __device__ __forceinline__ int collect(cg::cluster_group& cluster, Shared& sh, c
   return sh.listed;
 }
 
-template <bool kMass>
 __device__ __forceinline__ void clear_bins(Shared& sh) {
-  for (int i = threadIdx.x; i < kBins; i += kThreads) {
-    if (kMass) sh.lo[i] = sh.hi[i] = 0;
-    else sh.cnt[i] = 0;
-  }
+  for (int i = threadIdx.x; i < kBins; i += kThreads) sh.cnt[i] = sh.lo[i] = sh.hi[i] = 0;
   if (threadIdx.x < 64) sh.cnt[kBins + threadIdx.x] = 0;
   if (threadIdx.x == 0) sh.listed = sh.listed_own = 0;
   __syncthreads();
 }
 
-// The code at which the running count (kMass: mass) of the kept tokens, in
-// order, reaches want(whole).  Makes it the row's threshold; where the whole
-// does not reach it, all stay.  range: about where the threshold lies, from the maximum.
-template <typename Tin, bool kMass, typename F>
-__device__ __forceinline__ u64 select(cg::cluster_group& cluster, Shared& sh, Row& row, float range, F&& want) {
+// The least and the greatest key and the mass of the kept tokens for which in(x) holds (none of
+// them below `from`); lo > hi: there is none.  One cluster barrier.
+template <typename Tin, typename F>
+__device__ __forceinline__ void extent(cg::cluster_group& cluster, Shared& sh, const Row& row, float from, unsigned* lo, unsigned* hi,
+                                       u64* mass, F&& in) {
   constexpr int kN = Vec<Tin>::kN;
-  const int tid = threadIdx.x, lane = tid & 31;
-  const Bins bins(row.heat.max, range);
-  const Bounds<kN> bounds(row, kMass);
-  u64 lo = 0, hi = (1ull << (32 + kIndexBits)) - 1, above = 0, target = 0;
-  int level = 0, b0 = 0, b1 = 0, shift = 0, n;
-  // the candidates of the present level, and their intervals at the next one
-  auto candidate = [&](float x, int i, int level) {
-    if (level == 0) return true;
-    const float f = bins.at(x);
-    if (Bins::index(f) != b0) return false;
-    if (level == 1) return true;
-    if (Bins::index(Bins::inside(f, b0)) != b1) return false;
-    const u64 code = code_of(x, row.base + i);
-    return level == 2 || (code >= lo && code <= hi);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const Bounds<kN> bounds(row, false);
+  unsigned l = ~0u, h = 0;
+  u64 sum = 0;
+  for_each_from<Tin>(row, fmaxf(from, row.thr), [&](const auto& x, int i) {
+    bool take[kN];
+    bounds.test(x, i, take);
+#pragma unroll
+    for (int j = 0; j < kN; j += 2) {
+      take[j] = take[j] && in(x[j]);
+      take[j + 1] = take[j + 1] && in(x[j + 1]);
+      if (!__any_sync(0xffffffffu, take[j] || take[j + 1])) continue;
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (take[j + e]) {
+          l = min(l, Keys<Tin>::of(x[j + e]));
+          h = max(h, Keys<Tin>::of(x[j + e]));
+        }
+      const Units w = units(x[j], x[j + 1], take[j] && x[j] >= row.heat.least, take[j + 1] && x[j + 1] >= row.heat.least, row.heat, sh.table);
+      sum += weight_of(w, 0) + weight_of(w, 1);
+    }
+  });
+  l = __reduce_min_sync(0xffffffffu, l);
+  h = __reduce_max_sync(0xffffffffu, h);
+  sum = warp_sum64(sum);
+  if (lane == 0) {
+    sh.warp_lo[warp] = l;
+    sh.warp_hi[warp] = h;
+    sh.warp_mass[warp] = sum;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    l = __reduce_min_sync(0xffffffffu, lane < kWarps ? sh.warp_lo[lane] : ~0u);
+    h = __reduce_max_sync(0xffffffffu, lane < kWarps ? sh.warp_hi[lane] : 0u);
+    sum = warp_sum64(lane < kWarps ? sh.warp_mass[lane] : 0);
+    if (lane < C) {
+      *cluster.map_shared_rank(&sh.key_lo[rank], lane) = l;
+      *cluster.map_shared_rank(&sh.key_hi[rank], lane) = h;
+      *cluster.map_shared_rank(&sh.span[rank], lane) = sum;
+    }
+  }
+  cluster.sync();
+  *lo = ~0u;
+  *hi = 0;
+  *mass = 0;
+  for (int q = 0; q < C; ++q) {
+    *lo = min(*lo, sh.key_lo[q]);
+    *hi = max(*hi, sh.key_hi[q]);
+    *mass += sh.span[q];
+  }
+}
+
+// Of the kept tokens equal to v, those up to the m-th by index stay, and nothing below v.
+template <typename Tin>
+__device__ __forceinline__ void pick_tie(cg::cluster_group& cluster, Shared& sh, Row& row, float v, unsigned m) {
+  constexpr int kN = Vec<Tin>::kN;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const Bounds<kN> bounds(row, false);
+  auto equal = [&](const float (&x)[kN], int i, bool (&in)[kN]) {
+    unsigned n = 0;
+    bounds.test(x, i, in);
+#pragma unroll
+    for (int j = 0; j < kN; ++j) {
+      in[j] = in[j] && x[j] == v;
+      n += in[j] ? 1u : 0u;
+    }
+    return n;
   };
-  auto place = [&](float x, int i) -> int {
-    const float f = bins.at(x);
-    return level == 0 ? Bins::index(f) : level == 1 ? Bins::index(Bins::inside(f, b0)) : (int)((hi - code_of(x, row.base + i)) >> shift);
-  };
+  unsigned mine = 0;
+  for_each_from<Tin>(row, v, [&](const auto& x, int i) {
+    bool in[kN];
+    mine += equal(x, i, in);
+  });
+  mine = __reduce_add_sync(0xffffffffu, mine);
+  if (lane == 0) sh.warp_lo[warp] = mine;
+  if (tid == 0) sh.tie = INT_MAX;  // (all stay)
+  __syncthreads();
+  if (warp == 0) {
+    const unsigned sum = __reduce_add_sync(0xffffffffu, lane < kWarps ? sh.warp_lo[lane] : 0u);
+    if (lane < C) *cluster.map_shared_rank(&sh.ties[rank], lane) = sum;
+  }
+  cluster.sync();
+  unsigned left = m;
+  for (int q = 0; q < rank; ++q) left -= min(left, sh.ties[q]);
+  if (left > 0 && left <= sh.ties[rank]) {
+    int w = 0;
+    while (w < kWarps - 1 && left > sh.warp_lo[w]) left -= sh.warp_lo[w++];
+    if (w == warp) {
+      for (int i0 = row.lo; i0 < row.hi; i0 += 32 * kN) {
+        const int i = i0 + kN * lane;
+        float x[kN];
+        Vec<Tin>::get(*reinterpret_cast<const uint4*>(row.part + (size_t)i * sizeof(Tin)), x);
+        bool in[kN];
+        const unsigned n = equal(x, i, in), before = (unsigned)warp_scan64(n) - n;
+        if (before < left && left <= before + n) {  // (one lane)
+          unsigned run = before;
+          int at = 0;
+#pragma unroll
+          for (int j = 0; j < kN; ++j) {
+            run += in[j] ? 1u : 0u;
+            if (in[j] && run == left) at = j;
+          }
+          for (int q = 0; q < C; ++q) *cluster.map_shared_rank(&sh.tie, q) = row.base + i + at;
+        }
+        const unsigned all = __shfl_sync(0xffffffffu, before + n, 31);
+        if (left <= all) break;
+        left -= all;
+      }
+    }
+  }
+  cluster.sync();
+  row.thr = v;
+  row.last = sh.tie;
+}
+
+// The threshold of the kept tokens with keys lo .. hi at which the running count (kMass: mass)
+// from the greatest on, `above` at the start, reaches the target; where it does not, all
+// stay.  Returns it there.
+template <typename Tin, bool kMass>
+__device__ __forceinline__ u64 refine(cg::cluster_group& cluster, Shared& sh, Row& row, unsigned lo, unsigned hi, u64 above,
+                                      u64 target) {
+  constexpr int kN = Vec<Tin>::kN;
+  const int tid = threadIdx.x;
   for (;;) {
-    clear_bins<kMass>(sh);
-    u64 last = 0;  // of the last interval, which may hold most tokens
-    for_each<Tin>(row, [&](const auto& x, int i) {
+    if (lo > hi) return above;
+    if (lo == hi) {
+      const float v = Keys<Tin>::value(lo);
+      const u64 w = kMass ? weight(v, row.heat, sh.table) : 1;
+      const u64 m = (target - above + w - 1) / w;
+      pick_tie<Tin>(cluster, sh, row, v, (unsigned)min(m, (u64)INT_MAX));
+      return above + m * w;
+    }
+    const int shift = max(0, 32 - __clz((int)(hi - lo)) - 10);  // hi - lo < 2^(shift + 10), kBins intervals of 2^shift
+    const bool mass = kMass && shift > 0;  // (else an interval is a value: its mass follows from its count)
+    clear_bins(sh);
+    const Bounds<kN> bounds(row, kMass);
+    for_each_from<Tin>(row, fmaxf(Keys<Tin>::value(lo), row.thr), [&](const auto& x, int i) {
       bool in[kN];
       bounds.test(x, i, in);
 #pragma unroll
-      for (int j = 0; j < kN; j += 2) {
-        in[j] = in[j] && candidate(x[j], i + j, level);
-        in[j + 1] = in[j + 1] && candidate(x[j + 1], i + j + 1, level);
-        if (!__any_sync(0xffffffffu, in[j] || in[j + 1])) continue;
-        Units w;
-        if (kMass) w = units(x[j], x[j + 1], in[j], in[j + 1], row.heat, sh.table);
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          if (!in[j + e]) continue;
-          const u64 m = kMass ? weight_of(w, e) : 1;
-          const int bin = place(x[j + e], i + j + e);
-          if (bin == kBins - 1) last += m;
-          else if (kMass) add_mass(sh, bin, m);
-          else atomicAdd(&sh.cnt[bin], 1u);
-        }
+      for (int j = 0; j < kN; ++j) {
+        const unsigned key = Keys<Tin>::of(x[j]);
+        if (!in[j] || key < lo || key > hi) continue;
+        const int bin = (int)((hi - key) >> shift);
+        if (mass) add_mass(sh, bin, weight(x[j], row.heat, sh.table));
+        else atomicAdd(&sh.cnt[bin], 1u);
       }
     });
-    last = warp_sum64(last);
-    if (lane == 0 && last) {
-      if (kMass) add_mass(sh, kBins - 1, last);
-      else atomicAdd(&sh.cnt[kBins - 1], (unsigned)last);
+    if (mass) {
+      sum_bins<true>(cluster, sh);
+    } else {
+      sum_bins<false>(cluster, sh);
+      if (kMass)
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+          const unsigned off = (unsigned)(tid * kPer + k);
+          if (off <= hi - lo) sh.tot[off] *= weight(Keys<Tin>::value(hi - off), row.heat, sh.table);
+        }
     }
-    sum_bins<kMass>(cluster, sh);
-    u64 whole_all = 0;
-    const u64 got = find_bin(sh, above, [&](u64 whole) {
-      whole_all = whole;
-      return level == 0 ? want(whole) : target;
-    });
-    target = got;
-    if (!kMass && level == 0 && whole_all <= target) {
-      cluster.sync();  // (all have read cnt)
-      return 0;
-    }
-    const int bin = sh.bin;
+    find_bin(sh, above, [&](u64) { return target; });
+    const unsigned off = (unsigned)sh.bin << shift;
     above = sh.before;
-    if (level == 0) b0 = bin;
-    else if (level == 1) b1 = bin;
-    else {
-      hi -= (u64)bin << shift;
-      const u64 width = (1ull << shift) - 1;
-      if (hi - lo > width) lo = hi - width;
+    if (off > hi - lo) {  // not reached
+      cluster.sync();     // (all have read cnt)
+      return above;
     }
-    n = collect<Tin>(cluster, sh, row, -INFINITY, [&](float x, int i) { return candidate(x, i, level + 1); });
-    if (n <= kList) break;
-    ++level;
-    if (level >= 2) {  // by codes
-      shift = 64 - __clzll((long long)(hi - lo)) - 10;  // hi - lo < 2^(shift + 10), kBins intervals of 2^shift
-      if (shift < 0) shift = 0;
+    hi -= off;
+    if (hi - lo >= (1u << shift)) lo = hi - ((1u << shift) - 1);
+    if (shift > 0) {
+      const unsigned l = lo, h = hi;
+      u64 unused;
+      extent<Tin>(cluster, sh, row, Keys<Tin>::value(l), &lo, &hi, &unused, [&](float x) {
+        const unsigned key = Keys<Tin>::of(x);
+        return (!kMass || x >= row.heat.least) && key >= l && key <= h;
+      });
     }
-    __syncthreads();  // (sh.listed has been read)
   }
-  int i;
-  if (kMass) {
-    rank_list(sh, row.heat, n);
-    i = pick_entry(sh, above, target, n);
-  } else {
-    sort_list(sh.list, n);
-    i = (int)(target - above) - 1;
-  }
-  row.set(sh.list[i]);
-  const u64 kept = kMass ? above + sh.sum[i] : 0;
-  __syncthreads();
-  return kept;
 }
 
 // Intervals of x from its maximum on, in one packed multiply-add and, for the place in cnt, one
@@ -791,7 +889,7 @@ template <typename Tin>
 __device__ __forceinline__ void count_bins(cg::cluster_group& cluster, Shared& sh, const Row& row, const Places& places) {
   constexpr int kN = Vec<Tin>::kN;
   const int lane = threadIdx.x & 31;
-  clear_bins<false>(sh);
+  clear_bins(sh);
   if (row.thr == -INFINITY) {
     for_each<Tin>(row, [&](const auto& x, int) {
 #pragma unroll
@@ -824,9 +922,9 @@ __device__ __forceinline__ void count_bins(cg::cluster_group& cluster, Shared& s
   sum_bins<false>(cluster, sh);
 }
 
-// top-k by counts: the row's threshold.  False where ties or the last interval are in the way.
+// top-k by counts: the row's threshold.
 template <typename Tin>
-__device__ __forceinline__ bool top_count(cg::cluster_group& cluster, Shared& sh, Row& row, float range, int k) {
+__device__ __forceinline__ void top_count(cg::cluster_group& cluster, Shared& sh, Row& row, float range, int k) {
   const Places places(row.heat.max, range);
   count_bins<Tin>(cluster, sh, row, places);
   u64 whole = 0;
@@ -834,27 +932,27 @@ __device__ __forceinline__ bool top_count(cg::cluster_group& cluster, Shared& sh
     whole = w;
     return (u64)k;
   });
-  const int b = sh.bin;
-  const bool all = row.thr != -INFINITY && whole <= (u64)k;  // all stay
-  if (all || b == kBins - 1) {
+  if (row.thr != -INFINITY && whole <= (u64)k) {  // all stay
     cluster.sync();  // (all have read cnt)
-    return all;
+    return;
   }
-  const u64 above = sh.before;
+  const int b = sh.bin, left = k - (int)sh.before;
   const int n = collect<Tin>(cluster, sh, row, places.from(b), [&](float x, int) { return places.bin(x) == b; });
-  if (n > kList) {
-    __syncthreads();  // (sh.listed has been read)
-    return false;
+  if (n <= kList) {
+    sort_list(sh.list, n);
+    if (left <= n) row.set(sh.list[left - 1]);  // (more than there are, with the last interval: all stay)
+    __syncthreads();
+    return;
   }
-  sort_list(sh.list, n);
-  row.set(sh.list[k - 1 - (int)above]);
-  __syncthreads();
-  return true;
+  unsigned lo, hi;
+  u64 mass;
+  extent<Tin>(cluster, sh, row, places.from(b), &lo, &hi, &mass, [&](float x) { return places.bin(x) == b; });
+  refine<Tin, false>(cluster, sh, row, lo, hi, 0, (u64)left);
 }
 
-// The same for the mass and top_p = p, by an estimate of the interval: false where that fails
-// (nothing has changed then).  *total: the mass kept; sh.over: the CTAs' masses above the
-// interval, sh.warp_over: the warps'; the rest of what is kept is the list up to sh.pick.
+// The same for the mass and top_p = p, by an estimate of the interval.  *total: the mass kept.
+// True: sh.over holds the CTAs' masses above the interval, sh.warp_over the warps'; the rest of
+// what is kept is the list up to sh.pick.  False: the threshold is in sh.crowd.
 template <typename Tin>
 __device__ __forceinline__ bool nucleus(cg::cluster_group& cluster, Shared& sh, Row& row, float range, float heat, float p,
                                         u64* total) {
@@ -896,7 +994,7 @@ __device__ __forceinline__ bool nucleus(cg::cluster_group& cluster, Shared& sh, 
   }
   __syncthreads();
   int bin = sh.bin;
-  for (int tries = 0; tries < 3; ++tries) {
+  for (int tries = 0;; ++tries) {
     // its neighbours along with it while that is few tokens: where few tokens hold the mass
     // the estimate is rough
     int lo = bin, hi = bin;
@@ -955,22 +1053,44 @@ __device__ __forceinline__ bool nucleus(cg::cluster_group& cluster, Shared& sh, 
     }
     const u64 target = wanted(p, mass);
     const int n = sh.listed;
-    if (n > kList) return false;
-    if (n) rank_list(sh, row.heat, n);
-    const u64 here = n ? sh.sum[n - 1] : 0;
-    if (target > above && target <= above + here) {
-      const int i = pick_entry(sh, above, target, n);
-      row.set(sh.list[i]);
-      *total = above + sh.sum[i];
-      return true;
+    if (n <= kList) {
+      if (n) rank_list(sh, row.heat, n);
+      const u64 here = n ? sh.sum[n - 1] : 0;
+      if (target > above && target <= above + here) {
+        const int i = pick_entry(sh, above, target, n);
+        row.set(sh.list[i]);
+        *total = above + sh.sum[i];
+        return true;
+      }
     }
     bin = target <= above ? lo - 1 : hi + 1;
-    if (bin < 0 || bin >= kBins) return false;
+    const bool whole_row = tries == 2 || bin < 0 || bin >= kBins;  // (the estimate is of no use)
+    if (whole_row || (n > kList && target > above)) {
+      if (tid == 0) sh.crowd = whole_row ? Crowd{row.heat.least, INFINITY, 0, target} : Crowd{xe, xt, above, target};
+      __syncthreads();
+      return false;
+    }
     cluster.sync();  // (the lists and sums have been read)
     if (tid == 0) sh.listed = sh.listed_own = 0;
     cluster.sync();
   }
-  return false;
+}
+
+// The threshold in sh.crowd; returns the mass kept.
+template <typename Tin>
+__device__ __forceinline__ u64 settle(cg::cluster_group& cluster, Shared& sh, Row& row) {
+  unsigned lo, hi;
+  u64 here;
+  const float xe = sh.crowd.xe, xt = sh.crowd.xt;
+  extent<Tin>(cluster, sh, row, xe, &lo, &hi, &here, [&](float x) { return x >= xe && x <= xt; });
+  u64 above = sh.crowd.above;
+  if (sh.crowd.target > above + here) {  // below it
+    above += here;
+    lo = Keys<Tin>::of(row.heat.least);
+    hi = Keys<Tin>::of(xe);
+    if (Keys<Tin>::value(hi) >= xe) --hi;
+  }
+  return refine<Tin, true>(cluster, sh, row, lo, hi, above, sh.crowd.target);
 }
 
 // All filters and the draw among the n tokens of the list, which hold the first k of the row.
@@ -1140,7 +1260,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     if (k <= (p < 1.f ? kSmallKTopP : kSmallK)) {
       // the k-th of the threads' largest tokens lies in interval b0: no token of the first k lies behind it
       const Places places(mx, range);
-      clear_bins<false>(sh);
+      clear_bins(sh);
       const int bin = places.bin(own);
       const bool there = own > row.thr || (own == row.thr && row.last == INT_MAX);
       const unsigned same = __ballot_sync(0xffffffffu, there && bin == kBins - 1);
@@ -1159,8 +1279,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       if (rank != 0 && !out) return;  // (every CTA has the list: one is enough for the token)
       total = small_row(sh, row, n, k, p, u, a.token && rank == 0 ? a.token + r : nullptr);
       done = true;
-    } else if (!top_count<Tin>(cluster, sh, row, range, k)) {
-      select<Tin, false>(cluster, sh, row, range, [&](u64) { return (u64)k; });
+    } else {
+      top_count<Tin>(cluster, sh, row, range, k);
     }
   }
   bool listed = false;  // the kept tokens: those above an interval, and some of the list
@@ -1169,10 +1289,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     const float tail = logf((float)a.V) - logf(fmaxf(1.f - p, 1e-7f)) + 5.f;
     const float range = fminf(spread, tail * heat);
     listed = nucleus<Tin>(cluster, sh, row, range, heat, p, &total);
-    if (!listed) {
-      __syncthreads();  // (sh.listed has been read)
-      total = select<Tin, true>(cluster, sh, row, range, [&](u64 whole) { return wanted(p, whole); });
-    }
+    if (!listed) total = settle<Tin>(cluster, sh, row);
   }
   if (listed && a.token) {
     // the CTAs' and this CTA's warps' kept masses: above the interval, and from the list

@@ -121,6 +121,37 @@ def test_ties(cuda_lib, V):
             _check_row(xs[r].double().numpy(), token[r], probs[r], u[r].item(), **rows[r])
 
 
+def _crowds(V):
+    """Rows in which thousands of tokens fall into one narrow interval: as few values, as
+    many, as numbers around zero of every size and both signs."""
+    g = torch.Generator().manual_seed(V)
+    n = torch.randn(V, generator=g)
+    far = torch.arange(V) % 11 == 3
+    wide = 10.0 ** (torch.rand(V, generator=g) * 60 - 45) * (torch.randint(0, 2, (V,), generator=g) * 2 - 1)
+    return dict(quarters=(n * 12).round() / 4, integers=(n * 3).round(), two=torch.where(n > 0.1, 1.0, 0.996),
+                dense=torch.where(far, -9.0, 1 + (torch.arange(V) * 7919 % V) * 2.0 ** -23),
+                denser=torch.where(far, -12.0, 1 + (torch.arange(V) * 7919 % V // 40) * 2.0 ** -23),
+                around=torch.where(far, -11.0, wide.clamp(-1e-3, 1e-3)), lowest=torch.where(far, 0.01 * n, -30 + n * 1e-6),
+                most=torch.where(torch.arange(V) < 50, 3.0 + n, torch.tensor(-15.0)))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V", [30000, 131072])
+@pytest.mark.parametrize("kind", list(_crowds(1)))
+def test_crowded_intervals(cuda_lib, kind, V, dtype):
+    x = _crowds(V)[kind].to(dtype)
+    sets = [dict(top_p=0.3), dict(top_p=0.9), dict(top_p=0.9999), dict(top_k=100), dict(top_k=2000), dict(top_k=V // 2), dict(top_k=V - 2),
+            dict(top_k=V // 3, top_p=0.7), dict(top_k=3000, top_p=0.95, temperature=0.5), dict(min_p=0.4, top_p=0.6),
+            dict(min_p=0.01, top_k=V // 2, top_p=0.9), dict(top_p=0.8, temperature=30.0)]
+    rows = [{**OFF, **s} for s in sets]
+    t = {k: torch.tensor([row[k] for row in rows], dtype=torch.int32 if k == "top_k" else torch.float32) for k in OFF}
+    rows = [{k: t[k][r].item() for k in OFF} for r in range(len(sets))]
+    u = torch.rand(len(sets), generator=torch.Generator().manual_seed(V))
+    token, probs = _run(cuda_lib, x.expand(len(sets), V).contiguous(), u, t)
+    for r in range(len(sets)):
+        _check_row(x.double().numpy(), token[r], probs[r], u[r].item(), **rows[r])
+
+
 def test_uniform_counts(cuda_lib):
     """On equal logits the counts kept are exact: ceil(top_p V), top_k."""
     V = 3000
