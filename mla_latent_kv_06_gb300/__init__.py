@@ -971,7 +971,7 @@ def _sample(logits, u, temperature, top_k, top_p, min_p, token, probs):
         u_ptr, token_ptr = u.data_ptr(), token.data_ptr()
     p_ptr, p_row, p_batch = None, 0, 0
     if probs is True:
-        probs = logits.new_empty(shape, dtype=f32)
+        probs = torch.empty(shape, dtype=f32, device=logits.device)
     elif probs is not None:
         _want("probs", probs, *shape)
         if probs.dtype is not f32 or probs.get_device() != index or (probs.stride(-1) != 1 and V > 1):

@@ -49,7 +49,10 @@
 // tiles, so a pair is any two rows of the batch there; behind the prefix it is two nodes of
 // one sequence, as ever (one, with S = 1: half of the pair's M idles, and its tiles still
 // stream at the rate of the memory).  Both kinds of items lie in one tile list that the
-// clusters split evenly, so that the batch takes one launch and one round.
+// clusters split evenly, so that the batch takes one launch and one round.  64 rows on 16k
+// shared tokens and up to 2k of their own 125 us, 1.26 PFLOP/s (tensor pipe 66% busy: half of
+// an own tile's products idle); 32 x 6 rows on 32k and up to 1k 548 us, 1.63 PFLOP/s, the
+// rate that the power limit leaves; 8 rows on 4k and up to 512 20 us, one tile's chain.
 //
 // Measured: 8 trees of 64 nodes on 16k to 32k keys 1.03 ms, 1.70 PFLOP/s of the
 // formula's (1.80 issued), the sustained rate of the tensor pipe under the

@@ -45,8 +45,8 @@
 // against 95 for 256 rows of 131072 at a temperature alone, when that was measured.)
 //
 // Measured: 256 rows of 131072 bf16 logits 55 us at a temperature alone (1.2 TB/s), 111 with
-// top-p, 58 with top-k, 48 with min-p, 84 of all kinds; 400 rows with their probabilities 129
-// (2.4 TB/s) to 210.  Neither memory nor the arithmetic is at its rate (issue slots 51% used
+// top-p, 58 with top-k, 48 with min-p, 85 of all kinds; 400 rows with their probabilities 129
+// (2.4 TB/s) to 211.  Neither memory nor the arithmetic is at its rate (issue slots 51% used
 // while an SM is busy): a row goes through its passes with barriers of the CTA (500 cycles
 // each beside another CTA's work) and of the cluster (1500) between them, two CTAs fill an
 // SM's registers, and 76 rows at a time are 3.4 rounds for 256.  Fetching the next round's rows
