@@ -58,7 +58,6 @@
 
 #include <atomic>
 #include <type_traits>
-#include <utility>
 
 #include "common.cuh"
 #include "internal.h"
@@ -130,12 +129,11 @@ struct Shared {
   u64 list[kList], sum[kList];  // codes; running mass once ranked
   int2 table[256];   // of i at -i mod 256: (hi, d's bits)
   double least;      // T log(min_p)
-  float max[kCluster], min[kCluster];
+  float2 ends[kWarps];  // the warps' largest and smallest logits
   int first[kCluster];
   u64 mass[kCluster], over[kCluster];
   u64 warp_mass[kWarps], warp_over[kWarps];
   float warp_part[kWarps];
-  float warp_max[kWarps], warp_min[kWarps];
   int warp_first[kWarps];
   int listed, listed_own, at[kCluster];
   unsigned key_lo[kCluster], key_hi[kCluster], ties[kCluster];
@@ -1144,7 +1142,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int r = blockIdx.x / C, b = r / a.N, node = r % a.N;
   const int set = a.per_row ? r : b;  // the row's settings
-  auto started = cluster.barrier_arrive();  // (the others' shared memory may be written once they run)
 
   Row row;
   row.part = part_sh;
@@ -1185,31 +1182,21 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
     mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
   }
-  if (lane == 0) {
-    sh.warp_max[warp] = mx;
-    sh.warp_min[warp] = mn;
-  }
-  __syncthreads();
-  cluster.barrier_wait(std::move(started));
-  if (warp == 0) {
-    mx = lane < kWarps ? sh.warp_max[lane] : -INFINITY;
-    mn = lane < kWarps ? sh.warp_min[lane] : INFINITY;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-    }
-    if (lane < C) {
-      *cluster.map_shared_rank(&sh.max[rank], lane) = mx;
-      *cluster.map_shared_rank(&sh.min[rank], lane) = mn;
-    }
-  }
+  if (lane == 0) sh.ends[warp] = make_float2(mx, mn);
   cluster.sync();
-  mx = sh.max[0];
-  mn = sh.min[0];
-  for (int q = 1; q < C; ++q) {
-    mx = max_nan(mx, sh.max[q]);
-    mn = fminf(mn, sh.min[q]);
+  // (all warps' of all CTAs by every warp: a reduction in each CTA and an exchange take two barriers more)
+#pragma unroll
+  for (int e = 0; e < kCluster * kWarps; e += 32) {
+    if (e >= C * kWarps) break;
+    const int q = (e + lane) / kWarps;  // (with one CTA half of the lanes read it again)
+    const float2 ends = *cluster.map_shared_rank(&sh.ends[lane % kWarps], min(q, C - 1));
+    mx = max_nan(mx, ends.x);
+    mn = fminf(mn, ends.y);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
   }
   float* out = a.probs ? a.probs + (long long)b * a.p_batch + (long long)node * a.p_row + row.base : nullptr;
   // no finite maximum, NaN or +inf among the logits, or settings that mean nothing
@@ -1220,6 +1207,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     }
     if (out)
       for (int i = max(row.lo, row.from) + lane; i < min(row.hi, row.to); i += 32) out[i] = qnan();
+    cluster.sync();  // (all have read ends)
     return;
   }
   row.heat = make_heat(mx, heat);
