@@ -125,7 +125,7 @@ struct Shared {
     };
     u64 own[kList];  // this CTA's share of the list
   };
-  u64 tot[kBins];                             // the cluster's, written by all CTAs
+  u64 tot[kBins];               // the cluster's
   u64 list[kList], sum[kList];  // codes; running mass once ranked
   int2 table[256];   // of i at -i mod 256: (hi, d's bits)
   double least;      // T log(min_p)
@@ -558,8 +558,9 @@ __device__ __forceinline__ u64 sort32(u64 x) {
 }
 
 // The first n entries, none 0 and all different, in descending order: 32 at a time in a warp's
-// registers, then every entry's rank in the other lists of 32 by bisection.  Three barriers;
-// (a bitonic network over all of them, 45 barriers for 512, took 14000 cycles, this 6000).
+// registers, then every entry's rank in the other lists of 32 by bisection.  (480 entries with
+// their masses take 8000 to 13000 cycles beside another CTA's work; a bitonic network over all
+// of them, 45 barriers, 14000 to 15700.)
 __device__ __forceinline__ void sort_list(u64* v, int n) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, lists = (n + 31) / 32;
   u64 e[kList / kThreads];

@@ -101,6 +101,17 @@ def test_row_counts(cuda_lib, R, V):
         _check_row(x[r].double().numpy(), token[r], probs[r], u[r].item(), **rows[r])
 
 
+def test_very_many_rows(cuda_lib):
+    """More rows than a grid's second extent holds."""
+    R, V = 70001, 37
+    x = _rows(V, R, 77, torch.bfloat16)
+    u = torch.rand(R, generator=torch.Generator().manual_seed(78))
+    rows, t = _settings(R)
+    token, probs = _run(cuda_lib, x, u, t)
+    for r in list(range(0, R, 1999)) + [R - 1]:
+        _check_row(x[r].double().numpy(), token[r], probs[r], u[r].item(), **rows[r])
+
+
 @pytest.mark.parametrize("V", [40, 5000, 70000])
 def test_ties(cuda_lib, V):
     """Equal logits: the lower index counts as the higher, within candidates that fill
