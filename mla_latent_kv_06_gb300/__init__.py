@@ -930,6 +930,9 @@ def decode_shared_paged(q, Lc_pages, Rc_pages, block_table, T, shared: int, kv_b
     return out
 
 
+_SETTINGS = ("temperature", "top_k", "top_p", "min_p")
+
+
 def _sample(logits, u, temperature, top_k, top_p, min_p, token, probs):
     torch = _torch()
     shape, strides, index = logits.shape, logits.stride(), logits.get_device()
@@ -944,20 +947,22 @@ def _sample(logits, u, temperature, top_k, top_p, min_p, token, probs):
     code = _dtype_code(logits)
     if strides[-1] != 1 and V > 1:
         raise ValueError("the values of a row of logits must be contiguous")
-    f32, i32 = torch.float32, torch.int32
-    sets, where = None, []  # shape of the settings, their addresses
-    for x, want, name in ((temperature, f32, "temperature"), (top_k, i32, "top_k"), (top_p, f32, "top_p"), (min_p, f32, "min_p")):
+    f32, i32, first = torch.float32, torch.int32, shape[:1]
+    sets, where = None, [None] * 4  # shape of the settings, their addresses
+    for i, x in enumerate((temperature, top_k, top_p, min_p)):
         if x is None:
-            where.append(None)
             continue
-        if x.shape != lead and x.shape != shape[:1]:
-            raise ValueError(f"{name}: shape {tuple(x.shape)}, not {tuple(lead)} or {tuple(shape[:1])}")
-        if sets is not None and x.shape != sets:
-            raise ValueError("the settings must be given all per sequence or all per row")
-        sets = x.shape
+        given, want = x.shape, i32 if i == 1 else f32
+        if sets is None:
+            if given != first and given != lead:
+                raise ValueError(f"{_SETTINGS[i]}: shape {tuple(given)}, not {tuple(lead)} or {tuple(first)}")
+            sets = given
+        elif given != sets:
+            raise ValueError(f"{_SETTINGS[i]}: shape {tuple(given)}, the others {tuple(sets)} (the settings must be given all per "
+                             "sequence or all per row)")
         if x.dtype is not want or x.get_device() != index or not x.is_contiguous():
-            _explain(logits.device, **{name: (x, want)})
-        where.append(x.data_ptr())
+            _explain(logits.device, **{_SETTINGS[i]: (x, want)})
+        where[i] = x.data_ptr()
     u_ptr = token_ptr = None
     if u is not None:
         _want("u", u, *lead)
