@@ -129,13 +129,14 @@ struct Shared {
   u64 list[kList], sum[kList];  // codes; running mass once ranked
   int2 table[256];   // of i at -i mod 256: (hi, d's bits)
   double least;      // T log(min_p)
-  float2 ends[kWarps];  // the warps' largest and smallest logits
+  float2 ends[kWarps], end;  // the warps' and the CTA's largest and smallest logits
   int first[kCluster];
   u64 mass[kCluster], over[kCluster];
   u64 warp_mass[kWarps], warp_over[kWarps];
   float warp_part[kWarps];
   int warp_first[kWarps];
-  int listed, listed_own, at[kCluster];
+  int listed;  // entries of `own` (or what there would be)
+  u64 part[2];  // this CTA's mass, and what of it is above an interval
   unsigned key_lo[kCluster], key_hi[kCluster], ties[kCluster];
   unsigned warp_lo[kWarps], warp_hi[kWarps];
   u64 span[kCluster];
@@ -468,10 +469,16 @@ __device__ __forceinline__ void sum_bins(cg::cluster_group& cluster, Shared& sh)
   if (!kMass) {
     static_assert(kPer == 2, "two counters a load");
     uint2 n = make_uint2(0, 0);
-    for (int q = 0; q < C; ++q) {
-      const uint2 m = *reinterpret_cast<const uint2*>(cluster.map_shared_rank(&sh.cnt[2 * tid], q));
-      n.x += m.x;
-      n.y += m.y;
+    for (int q0 = 0; q0 < C; q0 += 4) {  // (four loads on their way before the first is used)
+      uint2 m[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        m[q] = q0 + q < C ? *reinterpret_cast<const uint2*>(cluster.map_shared_rank(&sh.cnt[2 * tid], q0 + q)) : make_uint2(0, 0);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        n.x += m[q].x;
+        n.y += m[q].y;
+      }
     }
     sh.tot[2 * tid] = n.x;
     sh.tot[2 * tid + 1] = n.y;
@@ -524,23 +531,42 @@ __device__ __forceinline__ u64 find_bin(Shared& sh, u64 above, F&& target) {
 }
 
 __device__ __forceinline__ void list_own(Shared& sh, u64 code) {
-  const int at = atomicAdd(&sh.listed_own, 1);
+  const int at = atomicAdd(&sh.listed, 1);
   if (at < kList) sh.own[at] = code;
 }
 
-// This CTA's share of the list to every CTA's list.
-__device__ __forceinline__ void share_list(cg::cluster_group& cluster, Shared& sh) {
-  const int C = (int)cluster.num_blocks(), tid = threadIdx.x;
-  __syncthreads();
-  const int n = sh.listed_own;
-  if (tid < C) sh.at[tid] = atomicAdd(cluster.map_shared_rank(&sh.listed, tid), min(n, kList + 1));
-  __syncthreads();
-  for (int q = 0; q < C; ++q) {
-    const int at = sh.at[q];
-    if (at + n > kList) continue;
-    u64* list = cluster.map_shared_rank(&sh.list[0], q);
-    for (int i = tid; i < n; i += kThreads) list[at + i] = sh.own[i];
+// A barrier of the cluster in two halves: no thread is past the second before all have reached
+// the first.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+
+// The CTAs' shares into this CTA's list, if it wants and they fit: how many there are.  A
+// cluster barrier has to be passed before, and cluster_wait() before `own` changes or the CTA
+// ends.  share: in lane q < C, CTA q's number.
+__device__ __forceinline__ int gather_list(cg::cluster_group& cluster, Shared& sh, int share, bool want) {
+  const int C = (int)cluster.num_blocks(), lane = threadIdx.x & 31;
+  int end = lane < C ? min(share, kList + 1) : 0;
+#pragma unroll
+  for (int o = 1; o < kCluster; o <<= 1) {
+    const int up = __shfl_up_sync(0xffffffffu, end, o);
+    if (lane >= o) end += up;
   }
+  const int n = __shfl_sync(0xffffffffu, end, C - 1);
+  if (want && n <= kList)
+    for (int i0 = 0; i0 < n; i0 += kThreads) {
+      const int i = i0 + (int)threadIdx.x;
+      int q = 0, base = 0;
+      for (int k = 0; k < C - 1; ++k) {
+        const int e = __shfl_sync(0xffffffffu, end, k);
+        if (i >= e) {
+          q = k + 1;
+          base = e;
+        }
+      }
+      if (i < n) sh.list[i] = *cluster.map_shared_rank(&sh.own[i - base], q);
+    }
+  cluster_arrive();
+  return n;
 }
 
 // A warp's 32 values in descending order.
@@ -643,10 +669,11 @@ __device__ __forceinline__ int pick_entry(Shared& sh, u64 above, u64 target, int
   return sh.pick;
 }
 
-// The codes of the kept tokens for which in(x, i) holds (none of them below `from`), in every
-// CTA's list.  Their number, or one above kList where the list does not hold them all.  One cluster barrier.
+// The codes of the kept tokens for which in(x, i) holds (none of them below `from`), in the list
+// of every CTA that wants it.  Their number, above kList where the list does not hold them all.
+// One cluster barrier, and cluster_wait() has to follow.
 template <typename Tin, typename F>
-__device__ __forceinline__ int collect(cg::cluster_group& cluster, Shared& sh, const Row& row, float from, F&& in) {
+__device__ __forceinline__ int collect(cg::cluster_group& cluster, Shared& sh, const Row& row, float from, bool want, F&& in) {
   constexpr int kN = Vec<Tin>::kN;
   const Bounds<kN> bounds(row, false);
   for_each_from<Tin>(row, fmaxf(from, row.thr), [&](const auto& x, int i) {
@@ -663,15 +690,15 @@ __device__ __forceinline__ int collect(cg::cluster_group& cluster, Shared& sh, c
       if (take[j]) list_own(sh, code_of(x[j], row.base + i + j));
     }
   });
-  share_list(cluster, sh);
   cluster.sync();
-  return sh.listed;
+  const int lane = threadIdx.x & 31;
+  return gather_list(cluster, sh, lane < (int)cluster.num_blocks() ? *cluster.map_shared_rank(&sh.listed, lane) : 0, want);
 }
 
 __device__ __forceinline__ void clear_bins(Shared& sh) {
   for (int i = threadIdx.x; i < kBins; i += kThreads) sh.cnt[i] = sh.lo[i] = sh.hi[i] = 0;
   if (threadIdx.x < 64) sh.cnt[kBins + threadIdx.x] = 0;
-  if (threadIdx.x == 0) sh.listed = sh.listed_own = 0;
+  if (threadIdx.x == 0) sh.listed = 0;
   __syncthreads();
 }
 
@@ -936,13 +963,15 @@ __device__ __forceinline__ void top_count(cg::cluster_group& cluster, Shared& sh
     return;
   }
   const int b = sh.bin, left = k - (int)sh.before;
-  const int n = collect<Tin>(cluster, sh, row, places.from(b), [&](float x, int) { return places.bin(x) == b; });
+  const int n = collect<Tin>(cluster, sh, row, places.from(b), true, [&](float x, int) { return places.bin(x) == b; });
   if (n <= kList) {
     sort_list(sh.list, n);
     if (left <= n) row.set(sh.list[left - 1]);  // (more than there are, with the last interval: all stay)
     __syncthreads();
+    cluster_wait();
     return;
   }
+  cluster_wait();
   unsigned lo, hi;
   u64 mass;
   extent<Tin>(cluster, sh, row, places.from(b), &lo, &hi, &mass, [&](float x) { return places.bin(x) == b; });
@@ -957,7 +986,7 @@ __device__ __forceinline__ bool nucleus(cg::cluster_group& cluster, Shared& sh, 
                                         u64* total) {
   constexpr int kN = Vec<Tin>::kN;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int C = (int)cluster.num_blocks();
   const Bounds<kN> bounds(row, true);
   const bool dense = row.thr == -INFINITY;
   const Places places(row.heat.max, range);
@@ -1039,19 +1068,25 @@ __device__ __forceinline__ bool nucleus(cg::cluster_group& cluster, Shared& sh, 
       sh.warp_mass[warp] = all;
       sh.warp_over[warp] = over;
     }
-    share_list(cluster, sh);  // (begins with a barrier)
+    __syncthreads();
     if (warp < 2) {
       const u64 v = warp_sum64(lane < kWarps ? (warp ? sh.warp_over[lane] : sh.warp_mass[lane]) : 0);
-      if (lane < C) *cluster.map_shared_rank(warp ? &sh.over[rank] : &sh.mass[rank], lane) = v;
+      if (lane == 0) sh.part[warp] = v;
     }
     cluster.sync();
     u64 mass = 0, above = 0;
-    for (int q = 0; q < C; ++q) {
-      mass += sh.mass[q];
-      above += sh.over[q];
+    int share = 0;
+    if (lane < C) {
+      share = *cluster.map_shared_rank(&sh.listed, lane);
+      const u64* part = cluster.map_shared_rank(&sh.part[0], lane);
+      mass = part[0];
+      above = part[1];
     }
+    const int n = gather_list(cluster, sh, share, true);
+    if (warp == 0 && lane < C) sh.over[lane] = above;
+    mass = warp_sum64(mass);
+    above = warp_sum64(above);
     const u64 target = wanted(p, mass);
-    const int n = sh.listed;
     if (n <= kList) {
       if (n) rank_list(sh, row.heat, n);
       const u64 here = n ? sh.sum[n - 1] : 0;
@@ -1059,9 +1094,11 @@ __device__ __forceinline__ bool nucleus(cg::cluster_group& cluster, Shared& sh, 
         const int i = pick_entry(sh, above, target, n);
         row.set(sh.list[i]);
         *total = above + sh.sum[i];
+        cluster_wait();
         return true;
       }
     }
+    cluster_wait();
     bin = target <= above ? lo - 1 : hi + 1;
     const bool whole_row = tries == 2 || bin < 0 || bin >= kBins;  // (the estimate is of no use)
     if (whole_row || (n > kList && target > above)) {
@@ -1069,9 +1106,9 @@ __device__ __forceinline__ bool nucleus(cg::cluster_group& cluster, Shared& sh, 
       __syncthreads();
       return false;
     }
-    cluster.sync();  // (the lists and sums have been read)
-    if (tid == 0) sh.listed = sh.listed_own = 0;
-    cluster.sync();
+    __syncthreads();  // (sh.sum and sh.bin have been read)
+    if (tid == 0) sh.listed = 0;
+    __syncthreads();
   }
 }
 
@@ -1151,7 +1188,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   // the padded row in units of a warp's vectors: CTA q has those from first(q) on
   constexpr int kUnit = 32 * kN;
   const int n_units = (head + a.V + kUnit - 1) / kUnit;
-  const auto first = [&](int q) { return n_units * q / C; };
+  const int log_c = 31 - __clz(C);  // (a power of two)
+  const auto first = [&](int q) { return n_units * q >> log_c; };
   const int u0 = first(rank), mine_units = first(rank + 1) - u0;
   row.lo = mine_units * warp / kWarps * kUnit;
   row.hi = mine_units * (warp + 1) / kWarps * kUnit;
@@ -1184,18 +1222,25 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
   }
   if (lane == 0) sh.ends[warp] = make_float2(mx, mn);
-  cluster.sync();
-  // (all warps' of all CTAs by every warp: a reduction in each CTA and an exchange take two barriers more)
+  __syncthreads();
+  if (warp == 0) {
+    mx = sh.ends[lane % kWarps].x;
+    mn = sh.ends[lane % kWarps].y;
 #pragma unroll
-  for (int e = 0; e < kCluster * kWarps; e += 32) {
-    if (e >= C * kWarps) break;
-    const int q = (e + lane) / kWarps;  // (with one CTA half of the lanes read it again)
-    const float2 ends = *cluster.map_shared_rank(&sh.ends[lane % kWarps], min(q, C - 1));
-    mx = max_nan(mx, ends.x);
-    mn = fminf(mn, ends.y);
+    for (int o = kWarps / 2; o > 0; o >>= 1) {
+      mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+    }
+    if (lane == 0) sh.end = make_float2(mx, mn);
+  }
+  cluster.sync();
+  {
+    const float2 end = *cluster.map_shared_rank(&sh.end, lane & (C - 1));
+    mx = end.x;
+    mn = end.y;
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
+  for (int o = kCluster / 2; o > 0; o >>= 1) {
     mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
     mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
   }
@@ -1258,15 +1303,19 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       sum_bins<false>(cluster, sh);
       find_bin(sh, 0, [&](u64) { return (u64)k; });
       const int b0 = sh.bin;
-      n = collect<Tin>(cluster, sh, row, places.from(b0), [&](float x, int) { return places.bin(x) <= b0; });
+      n = collect<Tin>(cluster, sh, row, places.from(b0), rank == 0 || out, [&](float x, int) { return places.bin(x) <= b0; });
       if (n > kList) {
         n = 0;
-        __syncthreads();  // (sh.listed has been read)
+        cluster_wait();
       }
     }
     if (n > 0) {
-      if (rank != 0 && !out) return;  // (every CTA has the list: one is enough for the token)
+      if (rank != 0 && !out) {  // (one CTA is enough for the token)
+        cluster_wait();
+        return;
+      }
       total = small_row(sh, row, n, k, p, u, a.token && rank == 0 ? a.token + r : nullptr);
+      cluster_wait();
       done = true;
     } else {
       top_count<Tin>(cluster, sh, row, range, k);
