@@ -44,15 +44,15 @@
 // a row, streaming it from L2 in every pass, was slower up to 400 rows: 104 us
 // against 95 for 256 rows of 131072 at a temperature alone, when that was measured.)
 //
-// Measured: 256 rows of 131072 bf16 logits 55 us at a temperature alone (1.2 TB/s), 111 with
-// top-p, 58 with top-k, 48 with min-p, 85 of all kinds; 400 rows with their probabilities 129
-// (2.4 TB/s) to 211.  Neither memory nor the arithmetic is at its rate (issue slots 51% used
+// Measured: 256 rows of 131072 bf16 logits 52 us at a temperature alone (1.3 TB/s), 110 with
+// top-p, 57 with top-k, 46 with min-p, 84 of all kinds; 400 rows with their probabilities 125
+// (2.5 TB/s) to 208.  Neither memory nor the arithmetic is at its rate (issue slots 51% used
 // while an SM is busy): a row goes through its passes with barriers of the CTA (500 cycles
 // each beside another CTA's work) and of the cluster (1500) between them, two CTAs fill an
 // SM's registers, and 76 rows at a time are 3.4 rounds for 256.  Fetching the next round's rows
 // into L2 ahead changed nothing.  CTAs of 1024 threads (one row of 131072 with top-p 29 us
 // against 23) and clusters of twice the CTAs (79 against 55) cost more in barriers than they give; CTAs of
-// twice the elements, one to an SM, 59.  One row of 32000 takes 7 us, with top-p 15.
+// twice the elements, one to an SM, 59.  One row of 32000 takes 6 us, with top-p 14.
 #include <cooperative_groups.h>
 #include <limits.h>
 
