@@ -260,10 +260,13 @@ int mla_sparse_decode_paged(const mla_dims* d, int dtype, int B, int S, const vo
  * system prompt, whose block tables name the same pages there.  The attention
  * over these rows is computed once for all B * S query rows.
  *   shared     tokens that all sequences have in common, from the first on, not
- *              counting any of the S new ones; 0: none.  All rows of block_table name
- *              the same pages there (which row they are read through is left open).
+ *              counting any of the S new ones; 0: none.  The block_table rows of all sequences
+ *              of a good length name the same pages there (which of these rows they are read
+ *              through is left open, so that an index outside the pool there may leave every
+ *              sequence's outputs undefined)
  *   T          S + shared <= T[b] <= max_pages * page_size (a shorter one is a
- *              bad length, its outputs NaN)
+ *              bad length, its outputs NaN, its row of block_table not read: a slot
+ *              of the batch without a sequence has T[b] = 0)
  *   parent     [B, S] int32 or NULL: the S new tokens are the nodes of drafted trees, as
  *              for mla_decode_tree (absent nodes give zero, bad ones NaN), else a chain
  *   out        [B, S, H, v_head] float (out_dtype MLA_F32) or bf16 (MLA_BF16),

@@ -880,7 +880,8 @@ def decode_shared_paged(q, Lc_pages, Rc_pages, block_table, T, shared: int, kv_b
                         workspace=None, stream=None, parent=None):
     """decode_paged of sequences whose first `shared` tokens (a host number) are the same cache
     rows: the attention over them is computed once for the whole batch.  T counts all tokens,
-    S + shared <= T[b].  With parent [B,S] int32 the new tokens are drafted trees, as for
+    S + shared <= T[b]; any other length, 0 for a slot without a sequence, gives NaN there and a
+    flag, and that row of block_table is not read.  With parent [B,S] int32 the new tokens are drafted trees, as for
     decode_tree_paged.  out [B,S,H,v_head] in out_dtype (float32 unless given; bfloat16 is
     rounded once).  A workspace that is given must have decode_shared_workspace_size() bytes."""
     torch = _torch()

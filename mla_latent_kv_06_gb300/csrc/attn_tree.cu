@@ -222,6 +222,7 @@ struct Pieces<false> {
     return false;
   }
   __device__ __forceinline__ bool prefix() const { return false; }
+  __device__ __forceinline__ int table() const { return b; }
   __device__ __forceinline__ long long slot(const PairParams& p, int g, int s, uint32_t) const {
     return (long long)(g + b) * p.S + s;
   }
@@ -231,10 +232,12 @@ template <>
 struct Pieces<true> {
   SharedItems items;
   int item, b, lo, hi, pair;  // a prefix item: b = 0, pair of the batch's rows
+  int reader;                 // the sequence through whose table the prefix is read
   long long c0, c1;
   __device__ __forceinline__ void start(const PairParams& p, int g, int) {
     items = SharedItems{p.B, p.NP, p.shared, p.tiles, p.tile_start};
-    const long long N = items.total();
+    reader = p.tile_start[p.B + 1];
+    const long long N = reader < 0 ? 0 : items.total();  // no sequence at all: no item either
     c0 = N * g / p.G;
     c1 = N * (g + 1) / p.G;
     if (c0 < items.prefix_units()) {  // the item in which the chunk begins
@@ -265,6 +268,7 @@ struct Pieces<true> {
     return false;
   }
   __device__ __forceinline__ bool prefix() const { return item < items.shared; }
+  __device__ __forceinline__ int table() const { return prefix() ? reader : b; }  // sequence that the tiles are read through
   __device__ __forceinline__ long long slot(const PairParams&, int g, int, uint32_t rank) const {
     return (long long)(g + item) * 2 + rank;
   }
@@ -381,10 +385,11 @@ __device__ __forceinline__ void produce(const PairParams& p, Shared& sh, unsigne
     for (int d = 0; d < 9; ++d) load_2d(smem_u32(smem + d * kQAtom), &p.mQ, 64 * d, qrow, qbar, lead);
     load_2d(smem_u32(smem + 9 * kQAtom), &p.mQl, 0, qrow, qbar, lead);
     ++*q_issued;
-    Rows r0 = rows_of(pc.b, sp, pc.lo), r1 = pc.lo + 1 < pc.hi ? rows_of(pc.b, sp, pc.lo + 1) : r0;
+    const int via = pc.table();
+    Rows r0 = rows_of(via, sp, pc.lo), r1 = pc.lo + 1 < pc.hi ? rows_of(via, sp, pc.lo + 1) : r0;
     load_k(sp.at(pc.lo), r0);
     for (int k = pc.lo; uni(k < pc.hi) && ok; ++k) {
-      const Rows r2 = k + 2 < pc.hi ? rows_of(pc.b, sp, k + 2) : r1;
+      const Rows r2 = k + 2 < pc.hi ? rows_of(via, sp, k + 2) : r1;
       if (uni(k + 1 < pc.hi)) load_k(sp.at(k + 1), r1);
       if (ok) load_v(sp.at(k), r0);
       r0 = r1;

@@ -32,7 +32,7 @@ struct PairParams {
   CUtensorMap mTv;  // staged latents likewise
   const int32_t* T;
   const int32_t* parent;
-  const int32_t* tile_start;  // [B + 1] prefix of pair_tiles
+  const int32_t* tile_start;  // [B + 1] prefix of pair_tiles, then the first sequence of a good length (-1: none)
   int B, S, T_cap, G, NP;     // G chunks of the tile list, NP = ceil(S / 2) node pairs
   int shared, tiles, t0;      // shared prefix: pairs of query rows (0 without tiles), whole tiles, tokens in them
   float c;                    // softmax scale * log2(e)
@@ -50,8 +50,10 @@ int pair_chunks(int B, int S, int T_cap, int sms);
 cudaError_t launch_attn_pair(const PairParams& p, cudaStream_t st);
 
 // The pass of a batch that shares a prefix.  Its list holds items: first, for every pair
-// of the batch's query rows, the prefix's tiles (read through sequence 0), then, for every
-// sequence and pair of its nodes, the sequence's own tiles.  An item is kItemCost units
+// of the batch's query rows, the prefix's tiles, then, for every
+// sequence and pair of its nodes, the sequence's own tiles.  The prefix is read through the first
+// sequence of a good length: what the table holds for one of a bad length, which is skipped,
+// may name any page or none.  An item is kItemCost units
 // for its query load, pipeline fill and partial, then one per tile; the clusters split the
 // units evenly.  Chunk g's partials of item i are slots 2 (g + i) and 2 (g + i) + 1.
 // kItemCost 1, 2 and 4, attention in us: 32 x 6 nodes on 32k shared tokens and none, 575,

@@ -29,6 +29,7 @@
 // quantises the query rows, and attn8_kernel, the attention on kind::f8f6f4
 // MMAs with two resident key tiles.
 #include <cuda_fp8.h>
+#include <limits.h>
 
 #include <atomic>
 #include <cmath>
@@ -815,7 +816,7 @@ struct AbsorbParams {
   const int32_t* T;
   const int32_t* nsel;
   __nv_bfloat16* qcat;  // [R, 64, 576]
-  int32_t* tile_start;  // [NR + 1]
+  int32_t* tile_start;  // [NR + 1]; pair attention: after them the first sequence of a good length, -1: none
   int32_t* bad;         // [NR]
   int B, S, T_cap, Dn, Dv, topk, sparse;
   // L2 prefetch (small batches): the latent cache rows [0, T[b]) of every
@@ -1055,7 +1056,11 @@ __global__ void __launch_bounds__(kAbsThreads, 2) absorb_kernel(const AbsorbPara
     const int NR = p.sparse ? R : p.B;
     __shared__ int carry;
     __shared__ int wsum[kAbsThreads / 32];
-    if (tid == 0) carry = 0;
+    __shared__ int first_good;
+    if (tid == 0) {
+      carry = 0;
+      first_good = INT_MAX;
+    }
     __syncthreads();
     for (int base = 0; base < NR; base += kAbsThreads) {
       const int r = base + tid;
@@ -1071,6 +1076,7 @@ __global__ void __launch_bounds__(kAbsThreads, 2) absorb_kernel(const AbsorbPara
         }
         if (bad) raise_flag(p.flags, bad);
         p.bad[r] = bad;
+        if (kTree && !bad) atomicMin(&first_good, r);
         tiles = bad ? 0 : (kTree && p.tail) ? pair_tiles(nk, p.S, p.t0) : (nk + kTile - 1) / kTile;
       }
       // block inclusive scan of `tiles`
@@ -1091,7 +1097,10 @@ __global__ void __launch_bounds__(kAbsThreads, 2) absorb_kernel(const AbsorbPara
       if (tid == kAbsThreads - 1) carry = incl;
       __syncthreads();
     }
-    if (tid == 0) p.tile_start[0] = 0;
+    if (tid == 0) {
+      p.tile_start[0] = 0;
+      if (kTree && p.tail) p.tile_start[NR + 1] = first_good == INT_MAX ? -1 : first_good;
+    }
   }
 
   if constexpr (!kQabs) {  // rotary part only, every (row, pair) in parallel over the head's CTAs
@@ -1931,7 +1940,7 @@ Plan make_plan(int B, int S, int T_cap, int sparse_topk, bool tree = false, int 
   pl.off_q = off;
   off = align256(off + (size_t)pl.R * kH * kDc * 2);
   pl.off_ts = off;
-  off = align256(off + (size_t)(pl.NR + 1) * 4);
+  off = align256(off + (size_t)(pl.NR + 2) * 4);
   pl.off_bad = off;
   off = align256(off + (size_t)pl.NR * 4);
   pl.off_o = off;

@@ -331,3 +331,44 @@ def test_continuations_of_one_prompt(cuda_lib):
         assert all(probs[b, int(token[b])] > 0 for b in range(B))
         seen |= set(token.tolist())
     assert cuda_lib.device_status() == 0 and len(seen) > 1
+
+
+def _part(x, keep):
+    return dict(x, q=x["q"][keep], T=x["T"][keep], table=x["table"][keep])
+
+
+@pytest.mark.parametrize("dims,dtype,page", [(GLM, "bf16", 128), (GLM, "bf16", 256), (TINY, "f32", 16), (WIDE, "f32", 32)])
+@pytest.mark.parametrize("T,S", [([700, 650, 520, 800], 2), ([530] * 5 + [900] * 6, 1), ([900, 700, 800], 9)])
+@pytest.mark.parametrize("trees", [False, True])
+def test_tables_of_bad_lengths_are_not_read(cuda_lib, dims, dtype, page, T, S, trees):
+    """Slots of a batch that hold no sequence: whatever stands in their rows of the block table,
+    the first rows among them, the other sequences do not notice and no index is flagged."""
+    shared, B = 512, len(T)
+    x = _batch(dims, dtype, T, S, shared, page, 45)
+    more = dict(parent=torch.arange(-1, S - 1, dtype=torch.int32).expand(B, S).contiguous().to(DEV)) if trees else {}
+    cap = x["table"].shape[1] * page
+    for bad, length in (([0], 0), ([0, 1], shared), ([0, B - 1], cap + 1), ([1], -1), (list(range(B - 1)), 0)):
+        keep = [b for b in range(B) if b not in bad]
+        y = dict(x, T=x["T"].clone(), table=x["table"].clone())
+        y["T"][bad] = length
+        for entries in (torch.full((y["table"].shape[1],), -1, dtype=torch.int32), x["table"][B - 1].flip(0)):  # none, another prompt's
+            y["table"][bad] = entries
+            out = _call(cuda_lib, y, shared, dims, **more)
+            assert cuda_lib.device_status() == cuda_lib.MLA_DEV_BAD_LENGTH, (bad, length)
+            assert bool(torch.isnan(out[bad]).all())
+            check_close(to_np(out[keep]), _reference(_part(x, keep), [T[b] for b in keep], dims), TOL[dtype], (bad, length))
+    y = dict(x, T=torch.zeros_like(x["T"]), table=torch.full_like(x["table"], -1))  # no sequence at all
+    assert bool(torch.isnan(_call(cuda_lib, y, shared, dims, **more)).all())
+    assert cuda_lib.device_status() == cuda_lib.MLA_DEV_BAD_LENGTH
+
+
+@pytest.mark.parametrize("dims,dtype,page", [(GLM, "bf16", 128), (TINY, "f32", 16), (WIDE, "f32", 32)])
+def test_bad_pages_behind_the_prefix_are_one_sequences(cuda_lib, dims, dtype, page):
+    T, S, shared = [700, 650, 800], 3, 512
+    x = _batch(dims, dtype, T, S, shared, page, 49)
+    ref = _reference(x, T, dims)
+    x["table"][1, 640 // page] = x["Lp"].shape[0]
+    out = to_np(_call(cuda_lib, x, shared, dims))
+    assert cuda_lib.device_status() == cuda_lib.MLA_DEV_BAD_INDEX
+    for b in (0, 2):
+        check_close(out[b], ref[b], TOL[dtype], b)
