@@ -164,7 +164,8 @@ MLA_EXPORT size_t mla_decode_absorbed_workspace_size(const mla_dims* d, int dtyp
 namespace {
 // Enqueues one absorbed decode (dense or over selected keys) on either path.
 int run_decode(mla::DecodeArgs& a, int dtype, bool sparse, void* workspace, size_t workspace_bytes,
-               void* stream, const char* what, bool own_call = true, bool shared = false) {
+               void* stream, const char* what, bool own_call = true) {
+  const bool shared = a.shared != 0;
   if (!a.pages.table && (long long)a.B * a.T_cap >= (1ll << 31))
     return fail(MLA_ERR_UNSUPPORTED, "B*T_cap of 2^31 rows or more");
   a.flags = flags_ptr();
@@ -1102,9 +1103,9 @@ MLA_EXPORT int mla_decode_shared_paged(const mla_dims* d, int dtype, int B, int 
   a.out = out;
   a.out_bf16 = out_dtype == MLA_BF16;
   a.lead = shared;
+  a.shared = 1;
   a.parent = parent;
-  return run_decode(a, dtype, false, workspace, workspace_bytes, stream, "mla_decode_shared_paged launch", true,
-                    /*shared=*/true);
+  return run_decode(a, dtype, false, workspace, workspace_bytes, stream, "mla_decode_shared_paged launch");
 }
 
 // ---------------------------------------------------------------- sampling

@@ -63,6 +63,7 @@ struct DecodeArgs {
   // Shared prefix: tokens below `lead` lie in the same rows for all sequences, and
   // every length is at least S + lead
   int lead;
+  int shared;  // a shared-prefix call (lead may be 0), whose arithmetic is the tree attention's
 };
 
 cudaError_t launch_decode_simt(const DecodeArgs& a, int dtype, bool sparse, cudaStream_t st);

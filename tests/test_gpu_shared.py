@@ -362,6 +362,31 @@ def test_tables_of_bad_lengths_are_not_read(cuda_lib, dims, dtype, page, T, S, t
     assert cuda_lib.device_status() == cuda_lib.MLA_DEV_BAD_LENGTH
 
 
+@pytest.mark.parametrize("dims,dtype,page", [(GLM, "bf16", 128), (TINY, "f32", 16), (SMALL, "bf16", 32), (WIDE, "f32", 32),
+                                             (WIDE, "bf16", 32)])
+@pytest.mark.parametrize("T,S", [([700, 530, 650], 2), ([640, 530, 650, 700], 5)])
+@pytest.mark.parametrize("kind,value", [("Lp", float("nan")), ("Lp", float("-inf")), ("Rp", float("inf")), ("Rp", float("-inf")),
+                                        ("Rp", float("nan"))])
+def test_visible_rows_that_are_not_finite(cuda_lib, dims, dtype, page, T, S, kind, value):
+    """A cached row with a value that is not finite makes the queries that see it NaN, by every
+    head, one whose score for it is -inf included, and no others."""
+    x = _batch(dims, dtype, T, S, 512, page, 47)
+    ref = _reference(x, T, dims)
+    seen = {100: lambda b, s: True, 400: lambda b, s: True,  # in the prefix, in a whole tile of it and behind them
+            T[1] - S - 1: lambda b, s: b == 1, T[1] - S: lambda b, s: b == 1, T[1] - 1: lambda b, s: b == 1 and s == S - 1}
+    for t, sees in seen.items():
+        y = dict(x, **{kind: x[kind].clone()})
+        y[kind][y["table"][1, t // page].item(), t % page, 1] = value
+        mask = np.array([[sees(b, s) for s in range(S)] for b in range(len(T))])
+        out = _call(cuda_lib, y, 500, dims)
+        assert cuda_lib.device_status() == 0
+        got = to_np(out)
+        assert np.all(np.isnan(got[mask])), (t, np.argwhere(~np.isnan(got[mask]).all(-1))[:4])
+        assert np.all(np.isfinite(got[~mask]))
+        if not mask.all():
+            check_close(got[~mask], ref[~mask], TOL[dtype], t)
+
+
 @pytest.mark.parametrize("dims,dtype,page", [(GLM, "bf16", 128), (TINY, "f32", 16), (WIDE, "f32", 32)])
 def test_bad_pages_behind_the_prefix_are_one_sequences(cuda_lib, dims, dtype, page):
     T, S, shared = [700, 650, 800], 3, 512
