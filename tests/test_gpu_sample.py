@@ -439,3 +439,66 @@ def test_drafts_sampled_and_verified(cuda_lib):
         assert target[b, n, int(token[b])] > 0
         for i in range(n):
             assert target[b, i, int(tokens[b, int(path[b, i])])] > 0
+
+
+def _check_border(x, token, probs, u, top_p=1.0, **filters):
+    """The kept set against the formula wherever the border lies, also on it: a start of the
+    order whose mass reaches top_p of the whole, and without its last token does not, to within the
+    errors of the sums -- 2^-31 of each weight and 2^-45 of the largest, on both sides of the
+    comparison; probabilities of the set that was kept, and a token out of it."""
+    w, _ = oracle.sample_filter(x, **filters)
+    order = np.lexsort((np.arange(len(x)), -x))
+    order = order[w[order] > 0]
+    grown = np.cumsum(w[order])
+    whole, kept = grown[-1], probs[order] > 0
+    slack = 2.0 ** -30 + len(x) * 2.0 ** -44 / whole
+    m = int(kept.sum())
+    assert m >= 1 and kept[:m].all() and int((probs > 0).sum()) == m, m
+    if top_p < 1:
+        assert grown[m - 1] / whole >= np.longdouble(top_p) - slack, m
+        assert m == 1 or grown[m - 2] / whole < np.longdouble(top_p) + slack, m
+    else:
+        assert m == len(order)
+    v = np.zeros_like(w)
+    v[order[:m]] = w[order[:m]]
+    ref = v / grown[m - 1]
+    assert np.all(np.abs(probs - ref) <= PROB * ref)
+    up = np.cumsum(ref)
+    assert ref[token] > 0 and up[token] - ref[token] <= u + slack and up[token] > u - slack
+
+
+@pytest.mark.parametrize("V", [40, 5000, 50257, 70000, 131072])
+def test_borders_on_a_token(cuda_lib, V):
+    """Equal weights: masses are whole numbers, so what is kept and drawn is exact."""
+    from fractions import Fraction
+    p = [0.5, 0.25, 0.75, 0.3, 0.9, 2.0 ** -20, 1 - 2.0 ** -24, 1.0]
+    sets = [dict(top_p=float(np.float32(q)), top_k=k, temperature=float(np.float32(t))) for q in p
+            for k, t in ((0, 1.0), (0, 0.3), (V - 1, 1.0), (V // 2, 4.0), (30, 1.0))]
+    t = {k: torch.tensor([s[k] for s in sets], dtype=torch.int32 if k == "top_k" else torch.float32) for k in ("top_p", "top_k", "temperature")}
+    for value, dtype in ((0.0, torch.float32), (-7.5, torch.float32), (3.0, torch.bfloat16)):
+        x = torch.full((len(sets), V), value).to(dtype)
+        u = torch.rand(len(sets), generator=torch.Generator().manual_seed(V))
+        u[::7] = 0.5
+        token, probs = _run(cuda_lib, x, u, t)
+        for r, s in enumerate(sets):
+            n = s["top_k"] if 0 < s["top_k"] < V else V
+            m = min(n, max(1, -(-Fraction(s["top_p"]) * n // 1)))
+            assert (probs[r] > 0).sum() == m and np.all(probs[r, :m] > 0), (r, s, m)
+            assert np.all(np.abs(probs[r, :m] * m - 1) <= PROB), (r, s)
+            assert token[r] == Fraction(u[r].item()) * m // 1, (r, s)
+
+
+@pytest.mark.parametrize("V", [40, 5000, 70000])
+def test_kept_sets_by_the_formula(cuda_lib, V):
+    """Rows of few values, whose borders often lie on a token, by the formula itself."""
+    at = torch.arange(V)
+    kinds = [_rows(V, 1, 3, torch.float32, 1.0, True)[0], torch.where(at % 3 == 0, 2.0, 2.0 - 1e-6), torch.where(at % 2 == 0, 0.0, -0.0),
+             (at // 7 % 2).float() * 0.25, torch.where(at % 2 == 0, 0.0, -INF), torch.where(at < V // 4, 1.0, -20.0)]
+    sets = [dict(top_p=p, top_k=k, min_p=low) for p in (0.25, 0.5, 0.75, 0.99, 1.0) for k in (0, 30, V // 2) for low in (0.0, 0.25)]
+    t = {k: torch.tensor([s[k] for s in sets], dtype=torch.int32 if k == "top_k" else torch.float32) for k in ("top_p", "top_k", "min_p")}
+    rows = [{k: t[k][r].item() for k in t} for r in range(len(sets))]
+    for x in kinds:
+        u = torch.rand(len(sets), generator=torch.Generator().manual_seed(V))
+        token, probs = _run(cuda_lib, x.repeat(len(sets), 1), u, t)
+        for r in range(len(sets)):
+            _check_border(x.double().numpy(), token[r], probs[r], u[r].item(), **rows[r])
