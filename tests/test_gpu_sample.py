@@ -502,3 +502,55 @@ def test_kept_sets_by_the_formula(cuda_lib, V):
         token, probs = _run(cuda_lib, x.repeat(len(sets), 1), u, t)
         for r in range(len(sets)):
             _check_border(x.double().numpy(), token[r], probs[r], u[r].item(), **rows[r])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V", [3000, 50257, 50432])
+@pytest.mark.parametrize("hide", [0, 1, 2, 50])
+def test_flat_rows_with_masked_tokens(cuda_lib, hide, V, dtype):
+    """Logits close to each other, down to equal ones and to differences that are denormal
+    numbers, of which some, half or nearly all are masked."""
+    g = torch.Generator().manual_seed(V + hide)
+    sets = [dict(top_p=p, top_k=k, min_p=low, temperature=heat) for p in (0.1, 0.9, 0.9999, 1.0) for k, low in ((0, 0.0), (40, 0.0), (900, 0.5))
+            for heat in (1.0, 0.01)]
+    t = {k: torch.tensor([s[k] for s in sets], dtype=torch.int32 if k == "top_k" else torch.float32) for k in sets[0]}
+    rows = [{k: t[k][r].item() for k in t} for r in range(len(sets))]
+    for scale, at in ((0.0, 0.0), (0.0, -4.0), (1e-40, 0.0), (1e-33, 0.0), (1e-3, 0.0), (0.05, 2.0)):
+        x = (at + scale * torch.randn(V, generator=g)).to(dtype)
+        order = torch.randperm(V, generator=g)
+        x[order[:hide if hide < 2 else V - V // hide]] = -INF
+        u = torch.rand(len(sets), generator=g)
+        token, probs = _run(cuda_lib, x.repeat(len(sets), 1), u, t)
+        for r in range(len(sets)):
+            _check_border(x.double().numpy(), token[r], probs[r], u[r].item(), **rows[r])
+
+
+def _time(call):
+    """Microseconds of a call among others, the least of several."""
+    graph = torch.cuda.CUDAGraph()
+    call()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        for _ in range(5):
+            call()
+    times = []
+    for _ in range(12):
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        a.record()
+        graph.replay()
+        b.record()
+        b.synchronize()
+        times.append(a.elapsed_time(b) * 200)
+    return min(times)
+
+
+def test_time_of_flat_rows_is_that_of_their_tokens(cuda_lib):
+    """A masked token, or a vocabulary that fills no whole vectors, costs a flat row next to nothing
+    (three times the row's time before such elements were left out of its smallest logit)."""
+    R, V = 256, 50432
+    x = torch.randn(R, V, device=DEV, generator=torch.Generator(device=DEV).manual_seed(1)) * 0.05
+    masked = x.clone()
+    masked[:, 7] = -INF
+    u, p = torch.rand(R, device=DEV), torch.full((R,), 0.9, device=DEV)
+    even, hidden, odd = (_time(lambda y=y: cuda_lib.sample(y, u, top_p=p)) for y in (x, masked, x[:, :50257].contiguous()))
+    assert hidden < 1.5 * even and odd < 1.5 * even, (even, hidden, odd)
