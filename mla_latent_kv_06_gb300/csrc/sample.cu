@@ -1209,7 +1209,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     heat = 1.f;
     k = 1;
   }
-  heat = fminf(fmaxf(heat, 4e-34f), 3e35f);  // (c and its low part stay normal numbers)
+  // c stays a normal number.  Its low part is a denormal one from about 1e32 on, off by up to
+  // 2^-150: times the |x - max| of a token that weighs something, at most 87 T, 2^-34 of its weight
+  // at 3e35 (what all tokens have in common cancels).
+  heat = fminf(fmaxf(heat, 4e-34f), 3e35f);
   // (in double by one thread: all 512 at the rate of that pipe take 5 us)
   if (tid == 32 && least > 0.f) sh.least = (double)heat * log(fmin((double)least, 1.0));
   asm volatile("cp.async.wait_all;" ::: "memory");

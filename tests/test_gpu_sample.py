@@ -554,3 +554,9 @@ def test_time_of_flat_rows_is_that_of_their_tokens(cuda_lib):
     u, p = torch.rand(R, device=DEV), torch.full((R,), 0.9, device=DEV)
     even, hidden, odd = (_time(lambda y=y: cuda_lib.sample(y, u, top_p=p)) for y in (x, masked, x[:, :50257].contiguous()))
     assert hidden < 1.5 * even and odd < 1.5 * even, (even, hidden, odd)
+
+
+@pytest.mark.parametrize("offset,heat", [(0.0, 3e35), (3.2e38, 3e35), (-3.2e38, 3e35), (3.2e38, 1e33), (-1e38, 1e34)])
+def test_weights_at_high_temperatures(cuda_lib, offset, heat):
+    """The same errors where the constants of a temperature are denormal numbers in part."""
+    test_weights_one_by_one(cuda_lib, offset, heat)
