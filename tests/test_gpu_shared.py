@@ -397,3 +397,24 @@ def test_bad_pages_behind_the_prefix_are_one_sequences(cuda_lib, dims, dtype, pa
     assert cuda_lib.device_status() == cuda_lib.MLA_DEV_BAD_INDEX
     for b in (0, 2):
         check_close(out[b], ref[b], TOL[dtype], b)
+
+
+@pytest.mark.parametrize("dims,dtype,page", [(GLM, "bf16", 128), (TINY, "f32", 16), (WIDE, "f32", 32)])
+@pytest.mark.parametrize("T,S", [([700, 650, 520], 1), ([700, 650, 520, 800, 530], 3)])
+def test_queries_that_are_not_finite(cuda_lib, dims, dtype, page, T, S):
+    """A query with such a value spoils its own output alone, although the prefix is read for the rows of
+    several sequences together; nor does an empty slot's, whatever it holds, spoil any."""
+    x = _batch(dims, dtype, T, S, 512, page, 53)
+    ref = _reference(x, T, dims)
+    for value in (float("nan"), float("inf"), float("-inf")):
+        for at in (0, dims.qk_nope + 1):
+            y = dict(x, q=x["q"].clone(), T=x["T"].clone())
+            y["q"][1, S - 1, :, at] = value
+            y["q"][2] = value
+            y["T"][2] = 0
+            out = to_np(_call(cuda_lib, y, 512, dims))
+            assert cuda_lib.device_status() == cuda_lib.MLA_DEV_BAD_LENGTH
+            spoilt = np.zeros(out.shape[:2], dtype=bool)
+            spoilt[1, S - 1] = spoilt[2] = True
+            assert np.all(np.isnan(out[spoilt])) and np.all(np.isfinite(out[~spoilt]))
+            check_close(out[~spoilt], ref[~spoilt], TOL[dtype], (value, at))
