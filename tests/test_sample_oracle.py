@@ -67,3 +67,29 @@ def test_min_p_of_one_keeps_the_largest_alone():
     """exp(z) < 1 for every z < 0, also where it rounds to 1."""
     w, _ = oracle.sample_filter([1e-45, 0.0, 1e-45], min_p=1.0)
     assert w.tolist() == [1, 0, 1]
+
+
+def test_filters_by_definition():
+    """Rows of weights that are powers of two, where every mass is a rational number: the filters one after
+    the other as the definition says, and evenly spaced numbers that give every token its share."""
+    from fractions import Fraction
+    rng = np.random.default_rng(5)
+    for _ in range(300):
+        n = int(rng.integers(1, 8))
+        e = rng.integers(-3, 1, n)
+        top_k, min_p, top_p = int(rng.integers(0, 9)), float(rng.choice([0, 0.25, 0.3, 1])), float(rng.choice([0, 0.25, 0.4, 0.6, 0.9, 1]))
+        w = [Fraction(2) ** int(a - e.max()) for a in e]
+        kept = sorted(range(n), key=lambda i: (-w[i], i))
+        kept = kept[:top_k] if top_k else kept
+        kept = [i for i in kept if w[i] >= Fraction(min_p)]
+        whole = sum(w[i] for i in kept)
+        m = next(m for m in range(1, len(kept) + 1) if sum(w[i] for i in kept[:m]) >= Fraction(top_p) * whole)
+        kept = set(kept[:m] if top_p < 1 else kept)
+        got, margin = oracle.sample_filter([float(a) * LN2 for a in e], top_k=top_k, min_p=min_p * (1 - 1e-12), top_p=top_p)
+        if margin < 1e-12:  # on the border: rounding of the weights decides
+            continue
+        want = np.array([float(w[i]) if i in kept else 0.0 for i in range(n)])
+        assert got.astype(float) == pytest.approx(want, abs=1e-12), (e, top_k, min_p, top_p)
+        R = 1000
+        drawn = np.bincount([oracle.sample_token(got, (r + 0.5) / R)[0] for r in range(R)], minlength=n)
+        assert np.all(np.abs(drawn - want / want.sum() * R) <= 1)
