@@ -883,7 +883,8 @@ def decode_shared_paged(q, Lc_pages, Rc_pages, block_table, T, shared: int, kv_b
     S + shared <= T[b]; any other length, 0 for a slot without a sequence, gives NaN there and a
     flag, and that row of block_table is not read.  With parent [B,S] int32 the new tokens are drafted trees, as for
     decode_tree_paged.  out [B,S,H,v_head] in out_dtype (float32 unless given; bfloat16 is
-    rounded once).  A workspace that is given must have decode_shared_workspace_size() bytes."""
+    rounded once).  A workspace that is given must have decode_shared_workspace_size() bytes.
+    One sequence, or a few with a short prefix, are faster through decode_paged."""
     torch = _torch()
     if stream is not None:
         with torch.cuda.stream(stream):
@@ -999,7 +1000,8 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, toke
     row, or None for off; temperature 0 takes the highest logit.  The filters apply in the
     order top_k, min_p, top_p; of equal logits the lower index counts as the higher.
     Returns the tokens, int32; with return_probs (or a tensor probs to write to) also the
-    distributions that they were drawn from, float32, as tree_verify's q."""
+    distributions that they were drawn from, float32, as tree_verify's q (a token that weighs less
+    than 2^-45 of the likeliest has its probability there, but is never drawn)."""
     if stream is not None:
         with _torch().cuda.stream(stream):
             return sample(logits, u, temperature, top_k, top_p, min_p, token, probs, return_probs)

@@ -1967,12 +1967,12 @@ Plan make_plan(int B, int S, int T_cap, int sparse_topk, bool tree = false, int 
   return pl;
 }
 
-// Many rows: merge of the splits, then the W_UV lift as a GEMM.
 // The items of a shared-prefix call's tile list.
 SharedItems shared_items(const DecodeArgs& a, const Plan& pl, const unsigned char* w) {
   return SharedItems{a.B, (a.S + 1) / 2, pl.shared, pl.tiles, reinterpret_cast<const int32_t*>(w + pl.off_ts)};
 }
 
+// Many rows: merge of the splits, then the W_UV lift as a GEMM.
 cudaError_t run_lift(const DecodeArgs& a, const Plan& pl, unsigned char* w, bool sparse, bool pair, bool shared,
                      cudaStream_t st) {
   const Geometry& g = a.g;

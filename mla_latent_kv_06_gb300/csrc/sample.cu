@@ -40,19 +40,22 @@
 //
 // A row is a cluster of up to 8 CTAs, each with a contiguous part of the
 // vocabulary in shared memory, read once, 16 bytes at a time from 16-byte
-// boundaries; a warp's part is contiguous too, and mostly no other warp reads it.  (A CTA
-// a row, streaming it from L2 in every pass, was slower up to 400 rows: 104 us
-// against 95 for 256 rows of 131072 at a temperature alone, when that was measured.)
+// boundaries; a warp's part is contiguous too, and mostly no other warp reads it.  (An early
+// form with a CTA a row, streaming it from L2 in every pass, took 104 us where clusters then took
+// 95: 256 rows of 131072 at a temperature alone.  It was not measured against the present passes.)
 //
-// Measured: 256 rows of 131072 bf16 logits 52 us at a temperature alone (1.3 TB/s), 110 with
-// top-p, 57 with top-k, 46 with min-p, 84 of all kinds; 400 rows with their probabilities 125
-// (2.5 TB/s) to 208.  Neither memory nor the arithmetic is at its rate (issue slots 51% used
-// while an SM is busy): a row goes through its passes with barriers of the CTA (500 cycles
-// each beside another CTA's work) and of the cluster (1500) between them, two CTAs fill an
+// Measured: 256 rows of 131072 bf16 logits of deviation 3 at a temperature of 0.8 53 us (1.3 TB/s),
+// with top-p 0.9 97, with top-k 50 52, with min-p 0.05 38, of all kinds 69; 400 rows with their
+// probabilities 128 (2.5 TB/s), with top-p 188.  No one unit is at its rate.  At a temperature alone
+// issue slots are 55% used while an SM is busy and the shared-memory pipe 57%: the exponentials'
+// table is read at random, 5.0 passes of the banks an instruction over all loads where 2 would do.  The
+// stalls are not_selected 2.4, math pipes 2.3, barriers 1.8 and short scoreboard 1.2 warps an issue; with
+// filters of all kinds barriers lead (3.0): a row goes through its passes with barriers of the CTA (500
+// cycles each beside another CTA's work) and of the cluster (1500) between them.  Two CTAs fill an
 // SM's registers, and 76 rows at a time are 3.4 rounds for 256.  Fetching the next round's rows
 // into L2 ahead changed nothing.  CTAs of 1024 threads (one row of 131072 with top-p 29 us
 // against 23) and clusters of twice the CTAs (79 against 55) cost more in barriers than they give; CTAs of
-// twice the elements, one to an SM, 59.  One row of 32000 takes 6 us, with top-p 14.
+// twice the elements, one to an SM, 59 against 52.  One row of 32000 fp32 takes 6.6 us, with top-p 12.5.
 #include <cooperative_groups.h>
 #include <limits.h>
 
@@ -76,8 +79,9 @@ constexpr int kCluster = 8;  // most CTAs of a row
 constexpr int kList = 1024;  // tokens that are ranked against each other: two a thread
 constexpr int kAround = 128; // tokens around an estimated threshold that are looked at in any case
 // top-k by the threads' largest tokens, whose list then serves top-p and the draw too, or by
-// counts and a threshold.  64 rows of 131072 (8 of 32000), us: k = 200 20.6 and 24.0 (14.1, 13.0),
-// k = 500 32.7 and 27.0 (21.5, 13.5); with top-p after it, k = 500 31.7 and 45.7 (20.7, 23.2).
+// counts and a threshold.  64 rows of 131072 bf16 (256 of these; 8 of 32000 fp32), us: k = 200 21.0 and
+// 23.9 (63.8 and 78.6; 13.7 and 12.3), k = 300 23.8 and 24.8 (72.0 and 82.4; 14.9 and 12.1), k = 500 33.3 and
+// 26.7 (95.0 and 87.4; 21.1 and 12.3); with top-p after it k = 500 32.3 and 45.8 (93.2 and 148.5; 20.3 and 20.3).
 constexpr int kSmallK = 256, kSmallKTopP = 512;
 constexpr int kOne = 44;     // a weight of 1 is 2^kOne; kMaxSampleVocab of them stay below 2^63
 constexpr int kIndexBits = 20;
@@ -309,13 +313,18 @@ __device__ __forceinline__ u64 drawn(float u, u64 whole) {
   return u >= 1.f ? whole - 1 : u > 0.f ? fraction_of(u, whole, &cut) : 0;
 }
 
+// The float whose ordered_key() this is.
+__device__ __forceinline__ float logit_of(unsigned key) {
+  return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
+}
+
 // Ordered integers of the type's values.
 template <typename Tin>
 struct Keys;
 template <>
 struct Keys<float> {
   static __device__ __forceinline__ unsigned of(float x) { return ordered_key(x); }
-  static __device__ __forceinline__ float value(unsigned k) { return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k); }
+  static __device__ __forceinline__ float value(unsigned k) { return logit_of(k); }
 };
 template <>
 struct Keys<__nv_bfloat16> {
@@ -405,8 +414,7 @@ struct Row {
   int last;
   __device__ __forceinline__ bool kept(float x, int i) const { return x > thr || (x == thr && base + i <= last); }
   __device__ __forceinline__ void set(u64 code) {
-    const unsigned key = (unsigned)(code >> kIndexBits);
-    thr = __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
+    thr = logit_of((unsigned)(code >> kIndexBits));
     last = (int)(kIndexMask - (code & kIndexMask));
   }
   __device__ __forceinline__ float next() const {  // the float after thr
@@ -620,10 +628,6 @@ __device__ __forceinline__ void sort_list(u64* v, int n) {
   for (int q = 0; q < kList / kThreads; ++q)
     if (warp + q * kWarps < lists && e[q]) v[rank[q]] = e[q];
   __syncthreads();
-}
-
-__device__ __forceinline__ float logit_of(unsigned key) {
-  return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
 }
 
 // The first n entries of the list in descending order, and their running masses; the logits
